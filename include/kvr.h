@@ -552,6 +552,151 @@ enum {
 kvr_status kvr_profile_enable(kvr_cache* c, int32_t enable);
 kvr_status kvr_profile_read(kvr_cache* c, double* ms, int64_t* launches, int32_t n);
 
+/* ---------------------------------------------------------------------------
+ * Paged cache: K/V rows in fixed-size pages, for what follows a repair:
+ * appending new tokens, answering with single-token queries over sequences of
+ * very different lengths, and blocks stored in four bits.
+ *
+ * One kvr_pages describes one layer's pages.  It is a plain host struct of
+ * device pointers; nothing is owned or kept by the library, so the calls can
+ * be captured into a CUDA graph and replayed with new device contents.
+ *
+ * Row of position g of sequence b, K/V head h:
+ *     page = page_table[b * max_pages + g / page_size],  slot = g % page_size
+ *     row  = page * page_stride + h * head_stride + slot * slot_stride
+ * (strides in rows), at k + row * row_bytes, and the same for v.  With
+ * page_stride = n_kv_heads * page_size, head_stride = page_size,
+ * slot_stride = 1 a page is [head][slot]; with slot_stride = n_kv_heads,
+ * head_stride = 1 it is [slot][head].  The rows of a kvr_cache's layer are
+ * pages too: slot_stride = 1, head_stride = capacity, page_stride =
+ * page_size, the base pointer at the layer, page id = p + the sequence's
+ * offset in pages (capacity a multiple of page_size).
+ *
+ * Formats:
+ *   KVR_F32   head_dim 64 or 128, rows of fp32; q, k, v and out rows are fp32.
+ *   KVR_BF16  head_dim 128, rows of bf16; q, k, v and out rows are bf16.
+ *   KVR_INT4  head_dim 128, 64-byte rows of codes; q, k, v and out rows are
+ *             bf16.  Each run of `group` dims (32, 64 or 128) has a scale s
+ *             and an offset o, fp16: value = s * code + o, code 0..15.  The
+ *             pairs (s, o) of a row are at k_scale + row * 4 * (128 / group)
+ *             bytes, group by group.  The row is 32 two-byte units of four
+ *             dims each, dim 4u + e in bits 4e..4e+3 of unit u; unit u is
+ *             stored at place 4 * (u % 8) + u / 8.  Values are held to the
+ *             range of fp16 (larger magnitudes saturate at 65504).
+ * page_size is 16, 32, 64, 128 or 256; n_q_heads / n_kv_heads is at most 16.
+ * k, v and the scale arrays are 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+#define KVR_INT4 2   /* page format only (see kvr_dtype for the others) */
+
+typedef struct {
+    int32_t format;        /* KVR_F32, KVR_BF16 or KVR_INT4 */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t group;         /* KVR_INT4: dims that share a scale; 0 otherwise */
+    int32_t n_pages;       /* pages in the pool: table entries are [0, n_pages) */
+    int32_t batch;
+    int32_t max_pages;     /* columns of the page table */
+    int64_t page_stride, head_stride, slot_stride;   /* rows */
+    void* k;
+    void* v;
+    void* k_scale;         /* KVR_INT4: fp16 pairs; NULL otherwise */
+    void* v_scale;
+    const int32_t* page_table;   /* device [batch][max_pages]; entries past a sequence's end are not read */
+    const int32_t* kv_len;       /* device [batch]: keys at or past it are never read by kvr_paged_attend */
+    int32_t* err;                /* device [4], zeroed once by the caller: device-side checks land here */
+} kvr_pages;
+
+/* How kvr_paged_attend turns products into logits and which keys a row sees.
+ * Zero-initialise and set what is wanted; a NULL kvr_score_opts is the plain
+ * causal softmax. */
+typedef struct {
+    float scale;           /* x = scale * <q, k>; 0 = 1/sqrt(head_dim) */
+    float softcap;         /* > 0: x <- softcap * tanh(x / softcap), before the biases */
+    float alpha, beta;     /* x += alpha of local keys, beta of S' keys (operator F, as kvr_create_cache) */
+    const uint32_t* local_bits;   /* device [batch][ceil(max_pages * page_size / 32)] or NULL */
+    const uint32_t* sink_bits;
+    const float* slopes;          /* device [n_q_heads] or NULL: x -= slopes[h] * |g - j| */
+    const int32_t* key_begin;     /* device [n_rows] or NULL (= 0): a row sees no key before it */
+    const int32_t* key_end;       /* device [n_rows] or NULL (= g + 1, causal): nor at or past it */
+} kvr_score_opts;
+
+/* ---------------------------------------------------------------------------
+ * Rows of every paged call: n_rows packed rows, sequence-major; sequence b
+ * owns rows [cu_rows[b], cu_rows[b+1]) (device int32 [batch+1], from 0,
+ * non-decreasing, at most n_rows); positions[r] (device int32 [n_rows]) is the
+ * row's global position g_r.  Rows at or past cu_rows[batch] belong to no
+ * sequence and are left alone, so a captured call can be replayed with fewer
+ * rows.  Row strides are in elements, heads of a row contiguous
+ * ([heads][head_dim]); row pointers and strides are 16-byte aligned.
+ *
+ * kvr_paged_append -- write the K/V of new rows into their pages, rotated on
+ * the way (rotate-half at g_r; "Budgeted KV-Cache Repair", Sec. 13.2, Eq. 21,
+ * for rows whose cache is paged), and rotate the rows' queries.
+ *   k_rows, v_rows  device [n_rows][n_kv_heads][head_dim].
+ *   rope        device float [rope_len][head_dim/2][2]: (cos, sin) of the
+ *               angles of each position, or NULL: nothing is rotated.
+ *   q_rows, q_out   device [n_rows][n_q_heads][head_dim] or both NULL;
+ *               q_out is packed (stride n_q_heads * head_dim) and may be
+ *               q_rows itself when that is packed too.
+ * The rotation is in fp32, each product and sum rounded on its own, and
+ * rounded once to the page format.  KVR_INT4, per group of fp32 values x (after the
+ * rotation): o = fp16(min x), s = fp16((max x - min x) * fp32(1/15)), code =
+ * clamp(rint((x - o) * (1/s)), 0, 15), 0 when s = 0.
+ * Positions of a sequence ascend; a row that does not lie above the row
+ * before it, or whose position is outside the table, the rope table or the
+ * pool, is not written (nor its query) and is reported by kvr_paged_status.
+ * kv_len is neither read nor changed.
+ * ------------------------------------------------------------------------- */
+kvr_status kvr_paged_append(const kvr_pages* p, int32_t n_rows, const int32_t* cu_rows, const int32_t* positions,
+                            const void* k_rows, int64_t k_stride, const void* v_rows, int64_t v_stride,
+                            const float* rope, int32_t rope_len, const void* q_rows, int64_t q_stride, void* q_out,
+                            int32_t n_q_heads, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kvr_paged_read -- K/V rows of the given positions out of the pages, as the
+ * values they stand for (KVR_INT4: s * code + o in fp32, rounded once to
+ * bf16); the inverse of the append's write.  k_out, v_out: device
+ * [n_rows][n_kv_heads][head_dim], row strides in elements; either may be NULL.
+ * Positions may come in any order and repeat.  kv_len is not read.
+ * ------------------------------------------------------------------------- */
+kvr_status kvr_paged_read(const kvr_pages* p, int32_t n_rows, const int32_t* cu_rows, const int32_t* positions,
+                          void* k_out, int64_t k_stride, void* v_out, int64_t v_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kvr_paged_attend -- attention of packed rows over the paged cache:
+ *   x_rj = scale * <q_r, k_j>; softcap, biases and slopes as kvr_score_opts;
+ *   o_r  = sum_j softmax_j(x_rj) v_j over the visible keys
+ *          j in [max(0, begin_r), min(end_r, kv_len_b)).
+ * A row that sees no key gets zeros.  Positions may come in any order and
+ * repeat; g_r sets the default end and the distance |g_r - j|, nothing else.
+ * Keys outside every row's interval, and past kv_len, are never used, whatever
+ * their slots hold; a non-finite K or V row inside one row's interval may
+ * reach the other rows of that sequence.
+ *   max_rows    upper bound of the rows of any sequence (1 for a decode
+ *               step); rows past it are not computed and reported.
+ *   q, out      device [n_rows][n_q_heads][head_dim], row strides in elements.
+ *   workspace   device, >= kvr_paged_workspace_bytes(p, n_q_heads, n_rows,
+ *               max_rows), 256-byte aligned; needs no initialisation.  Calls
+ *               whose GPU work overlaps need a workspace each.
+ * Long sequences are split over the GPU and merged in a fixed order: the same
+ * inputs give the same bits.  A sequence whose table holds an entry outside
+ * the pool is computed with page 0 in its place and reported.
+ * ------------------------------------------------------------------------- */
+size_t kvr_paged_workspace_bytes(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32_t max_rows);
+kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int32_t n_q_heads, int32_t n_rows,
+                            int32_t max_rows, const int32_t* cu_rows, const int32_t* positions, const void* q,
+                            int64_t q_stride, void* out, int64_t out_stride, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/* Synchronise `stream` and report device-side failures of the paged calls
+ * since the last report (EDEVICE: a position, a row offset, a length or a page
+ * out of range, or positions that do not ascend; ETIMEOUT), clearing them.
+ * All paged calls: EINVAL on NULL or misaligned arguments, bad shapes and a
+ * small workspace; EUNSUPPORTED on shapes above the stated limits; n_rows = 0
+ * enqueues nothing. */
+kvr_status kvr_paged_status(const kvr_pages* p, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,3 +15,4 @@ from .refresh import *  # noqa: F401,F403
 from .select import *   # noqa: F401,F403
 from . import policy  # noqa: F401  (CacheReforge layer-range policy: oracle.policy.*)
 from . import sur  # noqa: F401  (Semantic-Unit Refresh selection: oracle.sur.*)
+from . import paged  # noqa: F401  (paged cache: oracle.paged.*)

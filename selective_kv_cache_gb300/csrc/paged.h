@@ -1,0 +1,128 @@
+// paged.h -- the paged cache's device view, and how its attention shares work
+// over the GPU (paged_api.cu, paged_rows.cu, paged_plan.cu, paged_simt.cu).
+#pragma once
+#include "kvr_internal.h"
+
+namespace kvr {
+
+enum : int { DEV_ERR_ORDER = 8 };   // appended positions of a sequence do not ascend
+
+constexpr int kPagedMaxGroup = 16;   // query heads per K/V head
+
+struct PagedView {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* ks;
+    uint8_t* vs;
+    const int* table;
+    const int* kv_len;
+    int* err;
+    int64_t page_stride, head_stride, slot_stride;
+    int n_pages, batch, max_pages, page_shift, n_kv_heads, capacity;   // capacity = max_pages * page_size
+};
+
+// Packed rows of a call: sequence b owns rows [cu[b], cu[b+1]).
+struct PagedRows {
+    const int* cu;
+    const int* pos;
+    int n_rows;
+};
+
+struct PagedRowIo {   // append and read
+    PagedView p;
+    PagedRows r;
+    const uint8_t* k_in;
+    const uint8_t* v_in;
+    const uint8_t* q_in;
+    uint8_t* k_out;
+    uint8_t* v_out;
+    uint8_t* q_out;
+    int64_t k_stride, v_stride, q_stride;   // bytes
+    const float2* rope;
+    int rope_len, n_q_heads;
+};
+cudaError_t launch_paged_append(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s);
+cudaError_t launch_paged_read(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s);
+
+// One (sequence, run of `positions` packed rows) of an attention call, and its
+// K/V heads one after another: `units` runs of `unit_keys` keys starting at
+// the unit that holds key klo, for each head.
+struct PagedItem {
+    int klo, khi;     // keys any of its rows may see: [klo, khi)
+    int units;        // >= 1 when it has rows, else 0
+    int before;       // units of one head of all earlier items
+};
+// Where a CTA's equal share of the call's units begins.
+struct PagedShare {
+    int item, head, off;   // unit `off` of that item's head
+    int u0;                // in the call's units; share c ends where share c+1 begins
+};
+struct PagedAttn {
+    PagedView p;
+    PagedRows r;
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride;   // elements
+    int n_q_heads, G, max_rows;
+    int positions;                  // packed rows of an item
+    int tiles, n_items;             // items of a sequence, of the call (tiles * batch)
+    int unit_keys, n_cta, tile_rows;   // tile_rows >= positions * G: rows of a partial
+    float scale, softcap, alpha, beta;
+    const uint32_t* loc;
+    const uint32_t* snk;
+    const float* slopes;
+    const int* key_begin;
+    const int* key_end;
+    int words;
+    // workspace
+    PagedItem* items;               // [n_items]
+    PagedShare* shares;             // [n_cta + 1]; u0 of the last used + 1 is the end; item < 0: no work
+    float* part_o;                  // [n_cta][2][tile_rows][head_dim], unnormalised
+    float* part_ml;                 // [n_cta][2][tile_rows][2]: running max in base 2, sum
+};
+cudaError_t launch_paged_plan(const PagedAttn& a, cudaStream_t s);
+cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cudaStream_t s);
+cudaError_t launch_paged_simt(int format, int head_dim, int group, const PagedAttn& a, cudaStream_t s);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void paged_err(const PagedView& p, int bit, int detail) {
+    if (atomicOr(&p.err[0], bit) == 0) p.err[1] = detail;
+}
+
+// First page row of (page, head), in rows; a page outside the pool is
+// reported and page 0 taken in its place, so no access leaves the pool.
+__device__ __forceinline__ int paged_id(const PagedView& p, int id) {
+    if ((unsigned)id >= (unsigned)p.n_pages) {
+        paged_err(p, DEV_ERR_INDEX, id);
+        return 0;
+    }
+    return id;
+}
+__device__ __forceinline__ int64_t paged_row(const PagedView& p, int page, int slot, int head) {
+    return page * p.page_stride + slot * p.slot_stride + head * p.head_stride;
+}
+
+// Rows of sequence b that lie in [0, n_rows); a malformed cu_rows gives none
+// and is reported.
+__device__ __forceinline__ int paged_seq_rows(const PagedView& p, const PagedRows& r, int b, int* row0) {
+    const int a = r.cu[b], e = r.cu[b + 1];
+    *row0 = a;
+    if (a < 0 || e < a || e > r.n_rows) {
+        paged_err(p, DEV_ERR_INDEX, b);
+        return 0;
+    }
+    return e - a;
+}
+
+// Keys a row of sequence b may see: [lo, hi).
+__device__ __forceinline__ void paged_interval(const PagedAttn& a, int row, int kv_len, int* lo, int* hi) {
+    const int g = a.r.pos[row];
+    *lo = a.key_begin ? max(a.key_begin[row], 0) : 0;
+    *hi = min(a.key_end ? a.key_end[row] : (g < 0x7fffffff ? g + 1 : g), kv_len);
+}
+__device__ __forceinline__ int paged_kv_len(const PagedView& p, int b) {
+    return min(max(p.kv_len[b], 0), p.capacity);
+}
+#endif
+
+}  // namespace kvr

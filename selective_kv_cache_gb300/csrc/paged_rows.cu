@@ -1,0 +1,328 @@
+// paged_rows.cu -- rows into and out of the paged cache.
+//
+// Append: k'_r = R_{g_r} k_r (rotate-half pairs (i, i + dh/2)) and v_r go to
+// slot g_r of their sequence, queries are rotated beside them ("Budgeted
+// KV-Cache Repair for Evolving Contexts", Sec. 13.2, Eq. 21, for a cache in
+// pages).  Read is the inverse of the write.  Both move each byte once and do
+// a few flops on it: HBM-bound for prompts, launch-bound for decode steps.
+//
+// One CTA per packed row.  Sixteen or eight threads share a head's row and
+// own whole rotation pairs, so nothing is exchanged between threads but the
+// extrema of a 4-bit group, and a thread's (cos, sin) stay in registers over
+// the row's heads.  Rotation: fp32, products and sum rounded separately, so
+// that a plain elementwise evaluation gives the same bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "paged.h"
+
+namespace kvr {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// Sequence that owns row r: the number of ends cu[b+1] <= r.  Every lane of
+// the warp gets it; -1 when r lies past the last sequence or cu is malformed
+// around it.
+__device__ __forceinline__ int owner(const PagedView& p, const PagedRows& rr, int r) {
+    const int lane = threadIdx.x & 31;
+    int b = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const bool past = b0 + lane < p.batch && rr.cu[b0 + lane + 1] <= r;
+        b += __popc(__ballot_sync(0xffffffffu, past));
+    }
+    if (b >= p.batch) return -1;
+    if (r < rr.cu[b]) {
+        if (threadIdx.x == 0) paged_err(p, DEV_ERR_INDEX, r);
+        return -1;
+    }
+    return b;
+}
+
+__device__ __forceinline__ void unpack8(uint4 u, float* x) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The pair (x, y) turned by (cos, sin).
+__device__ __forceinline__ void turn(float& x, float& y, float2 cs) {
+    const float a = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, cs.y));
+    y = __fadd_rn(__fmul_rn(y, cs.x), __fmul_rn(x, cs.y));
+    x = a;
+}
+
+// A vector pair of one row: elements [v*E, v*E + E) and the same + dh/2.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ void rotate(uint4& lo, uint4& hi, const float2* cs) {
+        float x[8], y[8];
+        unpack8(lo, x);
+        unpack8(hi, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn(x[e], y[e], cs[e]);
+        lo = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+        hi = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+    }
+};
+template <>
+struct Pair<float> {
+    static constexpr int E = 4;
+    static __device__ __forceinline__ void rotate(uint4& lo, uint4& hi, const float2* cs) {
+        float* x = reinterpret_cast<float*>(&lo);
+        float* y = reinterpret_cast<float*>(&hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) turn(x[e], y[e], cs[e]);
+    }
+};
+
+// Where row r goes: its page row for head 0, or -1 (reported) when it may not
+// be written.
+__device__ __forceinline__ int64_t append_slot(const PagedRowIo& a, int r, int b, int g) {
+    if (g < 0 || g >= a.p.capacity || (a.rope && g >= a.rope_len)) {
+        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, g);
+        return -1;
+    }
+    if (r > a.r.cu[b] && a.r.pos[r - 1] >= g) {
+        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_ORDER, g);
+        return -1;
+    }
+    const int id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];
+    if ((unsigned)id >= (unsigned)a.p.n_pages) {
+        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, id);
+        return -1;
+    }
+    return paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kRowThreads) append_kernel(PagedRowIo a) {
+    constexpr int E = Pair<T>::E, VT = DH / 2 / E;   // elements per vector, threads per head's row
+    constexpr int kBytes = DH * (int)sizeof(T), kUnits = kRowThreads / VT;
+    const int r = blockIdx.x;
+    const int b = owner(a.p, a.r, r);
+    if (b < 0) return;
+    const int g = a.r.pos[r];
+    const int64_t row = append_slot(a, r, b, g);
+    if (row < 0) return;
+    const int v = threadIdx.x % VT, H = a.p.n_kv_heads;
+    float2 cs[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) cs[e] = a.rope ? a.rope[(int64_t)g * (DH / 2) + v * E + e] : make_float2(1.f, 0.f);
+    for (int u = threadIdx.x / VT; u < 2 * H + (a.q_in ? a.n_q_heads : 0); u += kUnits) {
+        const uint8_t* src;
+        uint8_t* dst;
+        if (u < H) {
+            src = a.k_in + r * a.k_stride + (int64_t)u * kBytes;
+            dst = a.p.k + (row + u * a.p.head_stride) * kBytes;
+        } else if (u < 2 * H) {
+            src = a.v_in + r * a.v_stride + (int64_t)(u - H) * kBytes;
+            dst = a.p.v + (row + (u - H) * a.p.head_stride) * kBytes;
+        } else {
+            src = a.q_in + r * a.q_stride + (int64_t)(u - 2 * H) * kBytes;
+            dst = a.q_out + ((int64_t)r * a.n_q_heads + u - 2 * H) * kBytes;
+        }
+        uint4 lo = reinterpret_cast<const uint4*>(src)[v], hi = reinterpret_cast<const uint4*>(src)[v + VT];
+        if (a.rope && (u < H || u >= 2 * H)) Pair<T>::rotate(lo, hi, cs);
+        reinterpret_cast<uint4*>(dst)[v] = lo;
+        reinterpret_cast<uint4*>(dst)[v + VT] = hi;
+    }
+}
+
+// 4-bit pages: thread v of a row's eight owns the unit quadruple u = v, 8 + v,
+// 16 + v, 24 + v (dims 32 i + 4 v .. + 3): whole rotation pairs, and the 8
+// bytes at place 4 v of the packed row.  The extrema of 32 dims are those of
+// the eight threads' i-th units; wider groups join their units.
+__device__ __forceinline__ void extremum8(float& lo, float& hi) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+}
+
+template <int NG>
+__global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) {
+    constexpr int kUnits = kRowThreads / 8, kJoin = 4 / NG;
+    const int r = blockIdx.x;
+    const int b = owner(a.p, a.r, r);
+    if (b < 0) return;
+    const int g = a.r.pos[r];
+    const int64_t row = append_slot(a, r, b, g);
+    if (row < 0) return;
+    const int v = threadIdx.x % 8, H = a.p.n_kv_heads;
+    float2 cs[8];   // dims 4v..4v+3 and 32 + 4v..
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        cs[e] = a.rope ? a.rope[(int64_t)g * 64 + (e >> 2) * 32 + 4 * v + (e & 3)] : make_float2(1.f, 0.f);
+    const int n_units = 2 * H + (a.q_in ? a.n_q_heads : 0);
+    // every thread of a warp runs the same rounds: the shuffles below need
+    // the whole warp
+    for (int u0 = 0; u0 < n_units; u0 += kUnits) {
+        const int u = u0 + threadIdx.x / 8;
+        const bool live = u < n_units, is_q = u >= 2 * H, is_v = !is_q && u >= H;
+        const uint8_t* src = a.k_in;
+        if (live)
+            src = is_q ? a.q_in + r * a.q_stride + (int64_t)(u - 2 * H) * 256
+                       : (is_v ? a.v_in + r * a.v_stride + (int64_t)(u - H) * 256
+                               : a.k_in + r * a.k_stride + (int64_t)u * 256);
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 w = live ? *reinterpret_cast<const uint2*>(src + 64 * i + 8 * v) : make_uint2(0u, 0u);
+            x[4 * i] = __uint_as_float(w.x << 16);
+            x[4 * i + 1] = __uint_as_float(w.x & 0xffff0000u);
+            x[4 * i + 2] = __uint_as_float(w.y << 16);
+            x[4 * i + 3] = __uint_as_float(w.y & 0xffff0000u);
+        }
+        if (a.rope && !is_v) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) turn(x[e], x[e + 8], cs[e]);
+        }
+        if (live && is_q) {
+            uint8_t* dst = a.q_out + ((int64_t)r * a.n_q_heads + u - 2 * H) * 256;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint2*>(dst + 64 * i + 8 * v) =
+                    make_uint2(pack2(x[4 * i], x[4 * i + 1]), pack2(x[4 * i + 2], x[4 * i + 3]));
+        }
+        float lo[NG], hi[NG];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -65504.f), 65504.f);   // fp16's range
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            lo[n] = hi[n] = x[4 * kJoin * n];
+#pragma unroll
+            for (int e = 1; e < 4 * kJoin; ++e) {
+                lo[n] = fminf(lo[n], x[4 * kJoin * n + e]);
+                hi[n] = fmaxf(hi[n], x[4 * kJoin * n + e]);
+            }
+            extremum8(lo[n], hi[n]);
+        }
+        if (!live || is_q) continue;
+        const int64_t at = row + (u - (is_v ? H : 0)) * a.p.head_stride;
+        __half2* meta = reinterpret_cast<__half2*>((is_v ? a.p.vs : a.p.ks) + at * (4 * NG));
+        uint32_t unit[4];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            // scale and offset are rounded to fp16 first and the codes chosen
+            // against the rounded ones, so their rounding costs range, not
+            // bias: a value is off by half a step plus at most the offset's
+            // rounding (2^-11 of it)
+            const __half sh = __float2half_rn(__fmul_rn(__fsub_rn(hi[n], lo[n]), 1.0f / 15.0f));
+            const __half oh = __float2half_rn(lo[n]);
+            const float s = __half2float(sh), o = __half2float(oh);
+            const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
+            if (v == n) meta[n] = __halves2half2(sh, oh);
+#pragma unroll
+            for (int i = n * kJoin; i < (n + 1) * kJoin; ++i) {
+                unit[i] = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[4 * i + e], o), inv)), 0.f), 15.f);
+                    unit[i] |= (uint32_t)c << (4 * e);
+                }
+            }
+        }
+        *reinterpret_cast<uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v) =
+            make_uint2(unit[0] | (unit[1] << 16), unit[2] | (unit[3] << 16));
+    }
+}
+
+// Page row of row r of a read, or -1 (reported).
+__device__ __forceinline__ int64_t read_slot(const PagedRowIo& a, int b, int g) {
+    if (g < 0 || g >= a.p.capacity) {
+        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, g);
+        return -1;
+    }
+    const int id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];
+    if ((unsigned)id >= (unsigned)a.p.n_pages) {
+        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, id);
+        return -1;
+    }
+    return paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
+}
+
+// NG = 0: rows copied as they are (VT 16-byte vectors); else 4-bit rows.
+template <int VT, int NG>
+__global__ void __launch_bounds__(kRowThreads) read_kernel(PagedRowIo a) {
+    constexpr int kThreadsPerRow = NG ? 8 : VT, kUnits = kRowThreads / kThreadsPerRow;
+    const int r = blockIdx.x;
+    const int b = owner(a.p, a.r, r);
+    if (b < 0) return;
+    const int64_t row = read_slot(a, b, a.r.pos[r]);
+    if (row < 0) return;
+    const int v = threadIdx.x % kThreadsPerRow, H = a.p.n_kv_heads;
+    for (int u = threadIdx.x / kThreadsPerRow; u < 2 * H; u += kUnits) {
+        const bool is_v = u >= H;
+        const int h = is_v ? u - H : u;
+        uint8_t* dst = is_v ? a.v_out : a.k_out;
+        if (!dst) continue;
+        dst += r * (is_v ? a.v_stride : a.k_stride);
+        const int64_t at = row + h * a.p.head_stride;
+        if (NG == 0) {
+            reinterpret_cast<uint4*>(dst + (int64_t)h * VT * 16)[v] =
+                reinterpret_cast<const uint4*>((is_v ? a.p.v : a.p.k) + at * VT * 16)[v];
+        } else {
+            constexpr int N = NG ? NG : 1;
+            const uint2 w = *reinterpret_cast<const uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v);
+            const __half2* meta = reinterpret_cast<const __half2*>((is_v ? a.p.vs : a.p.ks) + at * (4 * N));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 so = __half22float2(meta[i * N / 4]);
+                const uint32_t unit = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = fmaf((float)((unit >> (4 * e)) & 15u), so.x, so.y);
+                *reinterpret_cast<uint2*>(dst + (int64_t)h * 256 + 64 * i + 8 * v) =
+                    make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s) {
+    const dim3 grid((unsigned)a.r.n_rows);
+    if (format == KVR_BF16) {
+        KVR_LAUNCH(append_kernel<__nv_bfloat16, 128>, grid, dim3(kRowThreads), 0, s, a);
+    } else if (format == KVR_F32 && head_dim == 64) {
+        KVR_LAUNCH(append_kernel<float, 64>, grid, dim3(kRowThreads), 0, s, a);
+    } else if (format == KVR_F32) {
+        KVR_LAUNCH(append_kernel<float, 128>, grid, dim3(kRowThreads), 0, s, a);
+    } else if (group == 32) {
+        KVR_LAUNCH(append_int4_kernel<4>, grid, dim3(kRowThreads), 0, s, a);
+    } else if (group == 64) {
+        KVR_LAUNCH(append_int4_kernel<2>, grid, dim3(kRowThreads), 0, s, a);
+    } else {
+        KVR_LAUNCH(append_int4_kernel<1>, grid, dim3(kRowThreads), 0, s, a);
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_paged_read(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s) {
+    const dim3 grid((unsigned)a.r.n_rows);
+    if (format == KVR_INT4) {
+        if (group == 32) KVR_LAUNCH(read_kernel<16, 4>, grid, dim3(kRowThreads), 0, s, a);
+        else if (group == 64) KVR_LAUNCH(read_kernel<16, 2>, grid, dim3(kRowThreads), 0, s, a);
+        else KVR_LAUNCH(read_kernel<16, 1>, grid, dim3(kRowThreads), 0, s, a);
+    } else if (format == KVR_F32 && head_dim == 128) {
+        KVR_LAUNCH(read_kernel<32, 0>, grid, dim3(kRowThreads), 0, s, a);
+    } else {   // bf16 of 128 dims, fp32 of 64: 256-byte rows
+        KVR_LAUNCH(read_kernel<16, 0>, grid, dim3(kRowThreads), 0, s, a);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace kvr

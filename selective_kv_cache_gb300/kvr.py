@@ -22,7 +22,7 @@ lib = C.CDLL(LIB_PATH)
 
 KVR_OK, KVR_EINVAL, KVR_ERANGE, KVR_ENOMEM, KVR_ECUDA, KVR_ETIMEOUT, KVR_EDEVICE, KVR_ESTATE, KVR_EUNSUPPORTED = range(9)
 STATUS_NAMES = ["OK", "EINVAL", "ERANGE", "ENOMEM", "ECUDA", "ETIMEOUT", "EDEVICE", "ESTATE", "EUNSUPPORTED"]
-KVR_F32, KVR_BF16 = 0, 1
+KVR_F32, KVR_BF16, KVR_INT4 = 0, 1, 2   # KVR_INT4: page format only
 KVR_SINK_STATIC = 0x1
 KVR_COMMIT_META = 0x1
 KVR_SPLICE_LOCAL = 0x1
@@ -39,7 +39,8 @@ EXPORTS = ["kvr_create_cache", "kvr_destroy_cache", "kvr_select", "kvr_workspace
            "kvr_shift", "kvr_splice", "kvr_cache_info", "kvr_restart_layer", "kvr_policy_sensitivity",
            "kvr_policy_create", "kvr_policy_destroy", "kvr_policy_plan", "kvr_policy_commit", "kvr_policy_versions",
            "kvr_sur_workspace_bytes", "kvr_sur_select", "kvr_sur_status", "kvr_refresh_range",
-           "kvr_wait_check"]
+           "kvr_wait_check", "kvr_paged_append", "kvr_paged_read", "kvr_paged_workspace_bytes", "kvr_paged_attend",
+           "kvr_paged_status"]
 
 
 class kvr_model_desc(C.Structure):
@@ -52,6 +53,18 @@ class kvr_model_desc(C.Structure):
 class kvr_layer_weights(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("w_qkv", "b_qkv", "w_o", "w_gate_up", "w_down", "norm1", "norm2",
                                           "q_norm", "k_norm")]
+
+
+class kvr_pages(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("format", "n_kv_heads", "head_dim", "page_size", "group", "n_pages", "batch",
+                                         "max_pages")] + \
+               [(n, C.c_int64) for n in ("page_stride", "head_stride", "slot_stride")] + \
+               [(n, C.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table", "kv_len", "err")]
+
+
+class kvr_score_opts(C.Structure):
+    _fields_ = [(n, C.c_float) for n in ("scale", "softcap", "alpha", "beta")] + \
+               [(n, C.c_void_p) for n in ("local_bits", "sink_bits", "slopes", "key_begin", "key_end")]
 
 
 class KvrError(RuntimeError):
@@ -101,8 +114,16 @@ lib.kvr_read_selection.argtypes = [P, I32, P, I32, P, I32, P, P, P, P, I32, P, P
 lib.kvr_read_meta.argtypes = [P, P, P]
 lib.kvr_profile_enable.argtypes = [P, I32]
 lib.kvr_profile_read.argtypes = [P, P, P, I32]
+I64 = C.c_int64
+lib.kvr_paged_append.argtypes = [P, I32, P, P, P, I64, P, I64, P, I32, P, I64, P, I32, P]
+lib.kvr_paged_read.argtypes = [P, I32, P, P, P, I64, P, I64, P]
+lib.kvr_paged_workspace_bytes.argtypes = [P, I32, I32, I32]
+lib.kvr_paged_workspace_bytes.restype = C.c_size_t
+lib.kvr_paged_attend.argtypes = [P, P, I32, I32, I32, P, P, P, I64, P, I64, P, C.c_size_t, P]
+lib.kvr_paged_status.argtypes = [P, P]
 for _f in EXPORTS:
-    if _f not in ("kvr_workspace_bytes", "kvr_last_error", "kvr_restart_layer", "kvr_sur_workspace_bytes"):
+    if _f not in ("kvr_workspace_bytes", "kvr_last_error", "kvr_restart_layer", "kvr_sur_workspace_bytes",
+                  "kvr_paged_workspace_bytes"):
         getattr(lib, _f).restype = C.c_int
 
 
@@ -386,3 +407,180 @@ def kvr_sur_select(embed, suffix_ids, query_ids, unit_bounds, budget_percent: in
 
 def kvr_sur_status(workspace, stream=None):
     _check(lib.kvr_sur_status(_ptr(workspace), _stream(stream)), "kvr_sur_status")
+
+
+# ---------------------------------------------------------------- paged cache
+_PAGE_FORMATS = {"f32": KVR_F32, "bf16": KVR_BF16, "int4": KVR_INT4}
+_ROW_DTYPES = {KVR_F32: torch.float32, KVR_BF16: torch.bfloat16, KVR_INT4: torch.bfloat16}
+
+
+def _want(t, what: str, dtype, dims: int = 0, device=None):
+    """The binding's own check of a tensor argument: a wrong dtype, a host
+    tensor or one of another device would reach the kernels as a bare pointer."""
+    if t.dtype != dtype or not t.is_cuda or (dims and t.dim() != dims) or (device is not None and t.device != device):
+        raise ValueError(f"{what}: need a {dims or 'n'}-d {dtype} tensor on {device or 'the GPU'}, got a "
+                         f"{t.dim()}-d {t.dtype} tensor on {t.device}")
+    return t
+
+
+def _int_array(t, what: str, n: Optional[int] = None, device=None):
+    _want(t, what, torch.int32, device=device)
+    if not t.is_contiguous() or (n is not None and t.numel() < n):
+        raise ValueError(f"{what}: need a contiguous int32 tensor of at least {n} elements")
+    return t
+
+
+def pages(fmt: str, k, v, page_table, kv_len, err, n_kv_heads: int, page_size: int, layout: str = "hnd",
+          k_scale=None, v_scale=None, group: int = 0, strides=None, n_pages: Optional[int] = None) -> kvr_pages:
+    """kvr_pages of device tensors.  fmt: "f32", "bf16" or "int4".  k, v:
+    [n_pages, n_kv_heads, page_size, head_dim] ("hnd") or [n_pages, page_size,
+    n_kv_heads, head_dim] ("nhd"), contiguous; int4: uint8 of 64 bytes a row
+    and fp16 k_scale, v_scale [..., 128 / group, 2].  page_table: int32
+    [batch, max_pages]; kv_len: int32 [batch]; err: int32 [4], zeroed.
+    strides (page, head, slot, in rows) with n_pages describe another layout
+    of the same buffers, e.g. a kvr_cache's.  The tensors are kept alive by
+    the struct."""
+    f = _PAGE_FORMATS[fmt]
+    dt = torch.uint8 if f == KVR_INT4 else _ROW_DTYPES[f]
+    dev = _want(k, "k", dt).device
+    _want(v, "v", dt, device=dev)
+    if not k.is_contiguous() or not v.is_contiguous() or k.shape != v.shape:
+        raise ValueError("k and v: need contiguous tensors of one shape")
+    head_dim = 128 if f == KVR_INT4 else k.shape[-1]
+    if f == KVR_INT4 and k.shape[-1] != 64:
+        raise ValueError("k and v: 4-bit rows are 64 bytes")
+    if strides is None:
+        want = (n_kv_heads, page_size) if layout == "hnd" else (page_size, n_kv_heads)
+        if layout not in ("hnd", "nhd") or k.dim() != 4 or tuple(k.shape[1:3]) != want:
+            raise ValueError(f"k and v: shape {tuple(k.shape)} is not the {layout} layout of {n_kv_heads} heads and "
+                             f"{page_size} slots")
+        strides = (n_kv_heads * page_size, page_size, 1) if layout == "hnd" else (n_kv_heads * page_size, 1, n_kv_heads)
+        n_pages = k.shape[0]
+    elif n_pages is None or n_pages < 1 or (n_pages - 1) * strides[0] + (n_kv_heads - 1) * strides[1] + (
+            page_size - 1) * strides[2] >= k.numel() // k.shape[-1]:
+        raise ValueError("strides: the last page's rows lie outside k and v")
+    if f == KVR_INT4:
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not _want(t, what, torch.float16, device=dev).is_contiguous() or group not in (32, 64, 128) or \
+                    t.numel() * group != k.numel() * 4:
+                raise ValueError(f"{what}: need contiguous (scale, offset) pairs of every {group} dims of k and v")
+    if page_table.dim() != 2:
+        raise ValueError("page_table: need [batch, max_pages]")
+    batch, max_pages = page_table.shape
+    _int_array(page_table, "page_table", device=dev)
+    _int_array(kv_len, "kv_len", batch, device=dev)
+    _int_array(err, "err", 4, device=dev)
+    p = kvr_pages(f, n_kv_heads, head_dim, page_size, group, n_pages, batch, max_pages, *strides, _ptr(k), _ptr(v),
+                  _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(kv_len), _ptr(err))
+    p.tensors = (k, v, k_scale, v_scale, page_table, kv_len, err)
+    p.device = dev
+    p.row_dtype = _ROW_DTYPES[f]
+    return p
+
+
+def score_opts(scale: float = 0.0, softcap: float = 0.0, alpha: float = 0.0, beta: float = 0.0, local_bits=None,
+               sink_bits=None, slopes=None, key_begin=None, key_end=None) -> kvr_score_opts:
+    """kvr_score_opts of device tensors (kept alive by the struct).  The bit
+    masks are int32 tensors of the same words."""
+    for t, what in ((local_bits, "local_bits"), (sink_bits, "sink_bits"), (key_begin, "key_begin"),
+                    (key_end, "key_end")):
+        if t is not None:
+            _int_array(t, what)
+    if slopes is not None and not _want(slopes, "slopes", torch.float32).is_contiguous():
+        raise ValueError("slopes: need a contiguous tensor")
+    o = kvr_score_opts(scale, softcap, alpha, beta, _ptr(local_bits), _ptr(sink_bits), _ptr(slopes), _ptr(key_begin),
+                       _ptr(key_end))
+    o.tensors = (local_bits, sink_bits, slopes, key_begin, key_end)
+    return o
+
+
+def _packed_rows(p: kvr_pages, t, what: str, n: int):
+    """(pointer, row stride in elements) of a [rows, heads, head_dim] operand."""
+    if t.dtype != p.row_dtype or t.device != p.device or t.dim() != 3 or t.shape[0] < n or t.shape[2] != p.head_dim or \
+            t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != p.head_dim) or \
+            (t.shape[0] > 1 and t.stride(0) < t.shape[1] * p.head_dim):
+        raise ValueError(f"{what}: need [{n}, heads, {p.head_dim}] of {p.row_dtype} on {p.device}, a row's heads "
+                         f"contiguous; got {tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
+    # the stride of a single row is whatever torch says; the library wants a full one
+    return t.data_ptr(), max(t.stride(0), t.shape[1] * p.head_dim)
+
+
+def _rows(p: kvr_pages, cu_rows, positions):
+    if torch.cuda.current_device() != p.device.index:
+        raise ValueError(f"the pages are on {p.device}, the current device is cuda:{torch.cuda.current_device()}")
+    _int_array(cu_rows, "cu_rows", p.batch + 1, p.device)
+    _int_array(positions, "positions", None, p.device)
+    return positions.numel()
+
+
+def _paged_stream(p: kvr_pages, stream) -> int:
+    return torch.cuda.current_stream(p.device).cuda_stream if stream is None else _stream(stream)
+
+
+def kvr_paged_append(p: kvr_pages, cu_rows, positions, k_rows, v_rows, rope=None, q_rows=None, q_out=None,
+                     stream=None):
+    """k_rows, v_rows: [n_rows, n_kv_heads, head_dim]; rope: fp32 [rope_len,
+    head_dim / 2, 2] (cos, sin) or None; q_rows, q_out: [n_rows, n_q_heads,
+    head_dim] (q_out packed) or None."""
+    n = _rows(p, cu_rows, positions)
+    kp, ks = _packed_rows(p, k_rows, "k_rows", n)
+    vp, vs = _packed_rows(p, v_rows, "v_rows", n)
+    if k_rows.shape[1] != p.n_kv_heads or v_rows.shape[1] != p.n_kv_heads:
+        raise ValueError(f"k_rows, v_rows: need {p.n_kv_heads} heads")
+    qp = qs = qo = None
+    hq = 0
+    if q_rows is not None and q_out is not None:
+        qp, qs = _packed_rows(p, q_rows, "q_rows", n)
+        qo, _ = _packed_rows(p, q_out, "q_out", n)
+        hq = q_rows.shape[1]
+        if q_out.shape[1] != hq or not q_out.is_contiguous():
+            raise ValueError("q_out: need a packed tensor of q_rows' heads")
+    elif q_rows is not None or q_out is not None:
+        raise ValueError("q_rows and q_out go together")
+    if rope is not None and (not _want(rope, "rope", torch.float32, 3, p.device).is_contiguous() or
+                             rope.shape[1:] != (p.head_dim // 2, 2)):
+        raise ValueError(f"rope: need a contiguous [rope_len, {p.head_dim // 2}, 2]")
+    _check(lib.kvr_paged_append(C.byref(p), n, cu_rows.data_ptr(), positions.data_ptr(), kp, ks, vp, vs, _ptr(rope),
+                                0 if rope is None else rope.shape[0], qp, qs or 0, qo, hq, _paged_stream(p, stream)),
+           "kvr_paged_append")
+
+
+def kvr_paged_read(p: kvr_pages, cu_rows, positions, k_out=None, v_out=None, stream=None):
+    """k_out, v_out: [n_rows, n_kv_heads, head_dim] in the row type, or None."""
+    n = _rows(p, cu_rows, positions)
+    ptrs = []
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and t.shape[1:2] != (p.n_kv_heads,):
+            raise ValueError(f"{what}: need {p.n_kv_heads} heads")
+        ptrs += (None, 0) if t is None else _packed_rows(p, t, what, n)
+    _check(lib.kvr_paged_read(C.byref(p), n, cu_rows.data_ptr(), positions.data_ptr(), *ptrs,
+                              _paged_stream(p, stream)), "kvr_paged_read")
+
+
+def kvr_paged_workspace_bytes(p: kvr_pages, n_q_heads: int, n_rows: int, max_rows: int) -> int:
+    return int(lib.kvr_paged_workspace_bytes(C.byref(p), n_q_heads, n_rows, max_rows))
+
+
+def kvr_paged_attend(p: kvr_pages, opts: Optional[kvr_score_opts], max_rows: int, cu_rows, positions, q, out,
+                     workspace, stream=None):
+    """q, out: [n_rows, n_q_heads, head_dim]; workspace: uint8 of
+    kvr_paged_workspace_bytes; opts: score_opts(...) or None."""
+    n = _rows(p, cu_rows, positions)
+    qp, qs = _packed_rows(p, q, "q", n)
+    op, os_ = _packed_rows(p, out, "out", n)
+    if out.shape[1] != q.shape[1]:
+        raise ValueError("out: need q's heads")
+    if opts is not None:
+        words = -(-p.max_pages * p.page_size // 32) * p.batch
+        for t, what, need in zip(opts.tensors, ("local_bits", "sink_bits", "slopes", "key_begin", "key_end"),
+                                 (words, words, q.shape[1], n, n)):
+            if t is not None and (t.numel() < need or t.device != p.device):
+                raise ValueError(f"{what}: need {need} elements on {p.device}")
+    _want(workspace, "workspace", torch.uint8, 1, p.device)
+    _check(lib.kvr_paged_attend(C.byref(p), None if opts is None else C.byref(opts), q.shape[1], n, max_rows,
+                                cu_rows.data_ptr(), positions.data_ptr(), qp, qs, op, os_, workspace.data_ptr(),
+                                workspace.numel(), _paged_stream(p, stream)), "kvr_paged_attend")
+
+
+def kvr_paged_status(p: kvr_pages, stream=None):
+    _check(lib.kvr_paged_status(C.byref(p), _paged_stream(p, stream)), "kvr_paged_status")
