@@ -51,11 +51,14 @@ struct PagedItem {
     int klo, khi;     // keys any of its rows may see: [klo, khi)
     int units;        // >= 1 when it has rows, else 0
     int before;       // units of one head of all earlier items
+    int seq, kv;      // its sequence and that one's length
+    int row0, rows;   // its packed rows
 };
 // Where a CTA's equal share of the call's units begins.
 struct PagedShare {
     int item, head, off;   // unit `off` of that item's head
     int u0;                // in the call's units; share c ends where share c+1 begins
+    PagedItem first;       // that item, so that a CTA's first loads wait for one record only
 };
 struct PagedAttn {
     PagedView p;
@@ -83,6 +86,14 @@ struct PagedAttn {
 cudaError_t launch_paged_plan(const PagedAttn& a, cudaStream_t s);
 cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cudaStream_t s);
 cudaError_t launch_paged_simt(int format, int head_dim, int group, const PagedAttn& a, cudaStream_t s);
+
+// Up to 16 rows (positions * G) an item, bf16 or 4-bit pages.
+cudaError_t launch_paged_decode(int format, int group, const PagedAttn& a, cudaStream_t s);
+int paged_decode_unit(int format);
+// its CTAs resident per SM (registers: the blocks in flight and the output)
+constexpr int paged_decode_ctas(bool int4, int row_tiles) {
+    return row_tiles == 1 ? 3 : 2;
+}
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void paged_err(const PagedView& p, int bit, int detail) {

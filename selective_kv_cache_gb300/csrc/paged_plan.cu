@@ -24,7 +24,7 @@ constexpr int kCoarse = 4096;
 // Keys that the rows of item i can see, its units, and the checks of its
 // sequence's row range.
 __device__ __forceinline__ PagedItem make_item(const PagedAttn& a, int i) {
-    PagedItem it{0, 0, 0, 0};
+    PagedItem it{};
     const int b = i / a.tiles, t = i - b * a.tiles;
     int row0;
     const int n = paged_seq_rows(a.p, a.r, b, &row0);
@@ -49,6 +49,10 @@ __device__ __forceinline__ PagedItem make_item(const PagedAttn& a, int i) {
     if (lo >= hi) lo = hi = 0;   // nothing visible: one unit without keys, which writes the zeros
     it.klo = lo;
     it.khi = hi;
+    it.seq = b;
+    it.kv = kv;
+    it.row0 = row0 + r0;
+    it.rows = r1 - r0;
     it.units = max(1, (hi + a.unit_keys - 1) / a.unit_keys - lo / a.unit_keys);
     return it;
 }
@@ -63,7 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
     int carry = 0;
     for (int base = 0; base < a.n_items; base += kPlanThreads) {
         const int i = base + threadIdx.x;
-        PagedItem it{0, 0, 0, 0};
+        PagedItem it{};
         if (i < a.n_items) it = make_item(a, i);
         int incl = it.units;
 #pragma unroll
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
     const long long T = (long long)s_total * H;
     const int n = (int)min((long long)a.n_cta, T);
     for (int c = threadIdx.x; c <= a.n_cta; c += kPlanThreads) {
-        PagedShare sh{-1, 0, 0, (int)T};
+        PagedShare sh{-1, 0, 0, (int)T, {}};
         if (c < n) {
             sh.u0 = (int)(T * c / n);
             const int x = sh.u0 / H;   // before_i <= u0 / H exactly when H before_i <= u0
@@ -109,7 +113,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
             }
             int i = l * step;
             while (i + 1 < a.n_items && a.items[i + 1].before <= x) ++i;
-            const int rem = sh.u0 - H * a.items[i].before, units = a.items[i].units;
+            sh.first = a.items[i];
+            const int rem = sh.u0 - H * sh.first.before, units = sh.first.units;
             sh.item = i;
             sh.head = rem / units;
             sh.off = rem - sh.head * units;
@@ -139,11 +144,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) merge_kernel(PagedAttn a) {
     if (sh.item < 0 || sh.off == 0) return;
     const int start = sh.u0 - sh.off, prev = a.shares[c - 1].u0;
     if (prev > start) return;
-    const PagedItem it = a.items[sh.item];
-    const int end = start + it.units;
-    const int b = sh.item / a.tiles, t = sh.item - b * a.tiles;
-    const int row0 = a.r.cu[b] + t * a.positions;
-    const int n = min(min(a.r.cu[b + 1] - a.r.cu[b], a.max_rows) - t * a.positions, a.positions);
+    const PagedItem it = sh.first;
+    const int end = start + it.units, row0 = it.row0, n = it.rows;
     const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= n * a.G) return;
     const size_t stride = (size_t)2 * a.tile_rows;   // rows from one share's first slot to the next's

@@ -40,10 +40,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttn a) {
     while (u < u1) {
         const PagedItem it = a.items[i];
         const int n = min(it.units - off, u1 - u);
-        const int b = i / a.tiles, t = i - b * a.tiles;
-        const int row0 = a.r.cu[b] + t * a.positions;
-        const int np = min(min(a.r.cu[b + 1] - a.r.cu[b], a.max_rows) - t * a.positions, a.positions);
-        const int kv = paged_kv_len(a.p, b);
+        const int b = it.seq, row0 = it.row0, np = it.rows, kv = it.kv;
         __syncthreads();
         for (int e = threadIdx.x; e < kRows * DH; e += kThreads) {
             const int m = e / DH, d = e % DH;
