@@ -583,7 +583,8 @@ kvr_status kvr_profile_read(kvr_cache* c, double* ms, int64_t* launches, int32_t
  *             dims each, dim 4u + e in bits 4e..4e+3 of unit u; unit u is
  *             stored at place 4 * (u % 8) + u / 8.  Values are held to the
  *             range of fp16 (larger magnitudes saturate at 65504).
- * page_size is 16, 32, 64, 128 or 256; n_q_heads / n_kv_heads is at most 16.
+ * page_size is 16, 32, 64, 128 or 256; n_q_heads / n_kv_heads is at most 16;
+ * page and slot strides are at most 2^21 rows.
  * k, v and the scale arrays are 16-byte aligned.
  * ------------------------------------------------------------------------- */
 #define KVR_INT4 2   /* page format only (see kvr_dtype for the others) */

@@ -1,6 +1,8 @@
 // paged.h -- the paged cache's device view, and how its attention shares work
 // over the GPU (paged_api.cu, paged_rows.cu, paged_plan.cu, paged_simt.cu).
 #pragma once
+#include <atomic>
+
 #include "kvr_internal.h"
 
 namespace kvr {
@@ -92,11 +94,24 @@ cudaError_t launch_paged_decode(int format, int group, const PagedAttn& a, cudaS
 int paged_decode_unit(int format);
 // its CTAs resident per SM (registers: the blocks in flight and the output)
 constexpr int paged_decode_ctas(bool int4, int row_tiles) {
-    return row_tiles == 1 ? 3 : 2;
+    return int4 && row_tiles == 1 ? 3 : 2;
 }
 
 #ifdef __CUDACC__
-__device__ __forceinline__ void paged_err(const PagedView& p, int bit, int detail) {
+// Dynamic shared memory above 48 KB for a kernel: set once per device.
+template <typename... A>
+cudaError_t allow_smem(void (*kernel)(A...), int bytes, std::atomic<uint64_t>* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+static __device__ __noinline__ void paged_err(const PagedView& p, int bit, int detail) {
     if (atomicOr(&p.err[0], bit) == 0) p.err[1] = detail;
 }
 
