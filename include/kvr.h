@@ -635,7 +635,7 @@ typedef struct {
  * the way (rotate-half at g_r; "Budgeted KV-Cache Repair", Sec. 13.2, Eq. 21,
  * for rows whose cache is paged), and rotate the rows' queries.
  *   k_rows, v_rows  device [n_rows][n_kv_heads][head_dim].
- *   rope        device float [rope_len][head_dim/2][2]: (cos, sin) of the
+ *   rope        device float [rope_len][head_dim/2][2], 16-byte aligned: (cos, sin) of the
  *               angles of each position, or NULL: nothing is rotated.
  *   q_rows, q_out   device [n_rows][n_q_heads][head_dim] or both NULL;
  *               q_out is packed (stride n_q_heads * head_dim) and may be

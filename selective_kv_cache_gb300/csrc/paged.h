@@ -42,6 +42,7 @@ struct PagedRowIo {   // append and read
     int64_t k_stride, v_stride, q_stride;   // bytes
     const float2* rope;
     int rope_len, n_q_heads;
+    int units, rows_per_block;              // (row, head) units of a row; set by the launcher
 };
 cudaError_t launch_paged_append(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s);
 cudaError_t launch_paged_read(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s);
@@ -79,8 +80,9 @@ struct PagedAttn {
     const int* key_begin;
     const int* key_end;
     int words;
+    int planned;                    // items and shares come from launch_paged_plan (else the kernel derives them)
     // workspace
-    PagedItem* items;               // [n_items]
+    PagedItem* items;               // [n_items], when planned
     PagedShare* shares;             // [n_cta + 1]; u0 of the last used + 1 is the end; item < 0: no work
     float* part_o;                  // [n_cta][2][tile_rows][head_dim], unnormalised
     float* part_ml;                 // [n_cta][2][tile_rows][2]: running max in base 2, sum
@@ -92,6 +94,7 @@ cudaError_t launch_paged_simt(int format, int head_dim, int group, const PagedAt
 // Up to 16 rows (positions * G) an item, bf16 or 4-bit pages.
 cudaError_t launch_paged_decode(int format, int group, const PagedAttn& a, cudaStream_t s);
 int paged_decode_unit(int format);
+int paged_decode_inline_items();   // calls of up to this many items need no plan launch
 // its CTAs resident per SM (registers: the blocks in flight and the output)
 constexpr int paged_decode_ctas(bool int4, int row_tiles) {
     return int4 && row_tiles == 1 ? 3 : 2;
@@ -148,6 +151,42 @@ __device__ __forceinline__ void paged_interval(const PagedAttn& a, int row, int 
 }
 __device__ __forceinline__ int paged_kv_len(const PagedView& p, int b) {
     return min(max(p.kv_len[b], 0), p.capacity);
+}
+
+// Keys that the rows of item i can see, its units, and the checks of its
+// sequence's row range.
+__device__ __forceinline__ PagedItem paged_item(const PagedAttn& a, int i) {
+    PagedItem it{};
+    const int b = i / a.tiles, t = i - b * a.tiles;
+    int row0;
+    const int n = paged_seq_rows(a.p, a.r, b, &row0);
+    if (t == 0) {
+        if (n > a.max_rows) paged_err(a.p, DEV_ERR_INDEX, n);
+        const int kv = a.p.kv_len[b];
+        if (kv < 0 || kv > a.p.capacity) paged_err(a.p, DEV_ERR_INDEX, kv);
+    }
+    const int r0 = t * a.positions, r1 = min(min(n, a.max_rows), r0 + a.positions);
+    if (r0 >= r1) return it;
+    const int kv = paged_kv_len(a.p, b);
+    int lo = 0x7fffffff, hi = 0;
+    for (int r = row0 + r0; r < row0 + r1; ++r) {
+        if (a.r.pos[r] < 0) paged_err(a.p, DEV_ERR_INDEX, a.r.pos[r]);
+        int l, h;
+        paged_interval(a, r, kv, &l, &h);
+        if (l < h) {
+            lo = min(lo, l);
+            hi = max(hi, h);
+        }
+    }
+    if (lo >= hi) lo = hi = 0;   // nothing visible: one unit without keys, which writes the zeros
+    it.klo = lo;
+    it.khi = hi;
+    it.seq = b;
+    it.kv = kv;
+    it.row0 = row0 + r0;
+    it.rows = r1 - r0;
+    it.units = max(1, (hi + a.unit_keys - 1) / a.unit_keys - lo / a.unit_keys);
+    return it;
 }
 #endif
 

@@ -154,8 +154,8 @@ kvr_status kvr_paged_append(const kvr_pages* p, int32_t n_rows, const int32_t* c
     if (n_rows == 0) return KVR_OK;
     if (!row_operand(p, k_rows, k_stride, p->n_kv_heads) || !row_operand(p, v_rows, v_stride, p->n_kv_heads))
         return fail(KVR_EINVAL, "append: K/V rows must be non-NULL, 16-byte aligned and at least a row apart");
-    if (rope && (rope_len < 1 || (reinterpret_cast<uintptr_t>(rope) & 7u)))
-        return fail(KVR_EINVAL, "append: the rope table needs rope_len >= 1 and 8-byte alignment");
+    if (rope && (rope_len < 1 || !aligned16(rope)))
+        return fail(KVR_EINVAL, "append: the rope table needs rope_len >= 1 and 16-byte alignment");
     if ((q_rows == nullptr) != (q_out == nullptr)) return fail(KVR_EINVAL, "append: q_rows and q_out go together");
     if (q_rows) {
         if (n_q_heads < 1 || n_q_heads > 65535) return fail(KVR_EINVAL, "append: n_q_heads out of range");
@@ -270,7 +270,8 @@ kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int3
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    KVR_CHECK_LAUNCH(launch_paged_plan(a, s), "paged plan");
+    a.planned = !g.decode || g.n_items > paged_decode_inline_items();
+    if (a.planned) KVR_CHECK_LAUNCH(launch_paged_plan(a, s), "paged plan");
     if (g.decode) KVR_CHECK_LAUNCH(launch_paged_decode(p->format, p->group, a, s), "paged attention");
     else KVR_CHECK_LAUNCH(launch_paged_simt(p->format, p->head_dim, p->group, a, s), "paged attention");
     KVR_CHECK_LAUNCH(launch_paged_merge(p->format == KVR_F32 ? KVR_F32 : KVR_BF16, p->head_dim, a, s), "paged merge");

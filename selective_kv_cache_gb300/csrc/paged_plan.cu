@@ -21,42 +21,6 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kCoarse = 4096;
 
-// Keys that the rows of item i can see, its units, and the checks of its
-// sequence's row range.
-__device__ __forceinline__ PagedItem make_item(const PagedAttn& a, int i) {
-    PagedItem it{};
-    const int b = i / a.tiles, t = i - b * a.tiles;
-    int row0;
-    const int n = paged_seq_rows(a.p, a.r, b, &row0);
-    if (t == 0) {
-        if (n > a.max_rows) paged_err(a.p, DEV_ERR_INDEX, n);
-        const int kv = a.p.kv_len[b];
-        if (kv < 0 || kv > a.p.capacity) paged_err(a.p, DEV_ERR_INDEX, kv);
-    }
-    const int r0 = t * a.positions, r1 = min(min(n, a.max_rows), r0 + a.positions);
-    if (r0 >= r1) return it;
-    const int kv = paged_kv_len(a.p, b);
-    int lo = 0x7fffffff, hi = 0;
-    for (int r = row0 + r0; r < row0 + r1; ++r) {
-        if (a.r.pos[r] < 0) paged_err(a.p, DEV_ERR_INDEX, a.r.pos[r]);
-        int l, h;
-        paged_interval(a, r, kv, &l, &h);
-        if (l < h) {
-            lo = min(lo, l);
-            hi = max(hi, h);
-        }
-    }
-    if (lo >= hi) lo = hi = 0;   // nothing visible: one unit without keys, which writes the zeros
-    it.klo = lo;
-    it.khi = hi;
-    it.seq = b;
-    it.kv = kv;
-    it.row0 = row0 + r0;
-    it.rows = r1 - r0;
-    it.units = max(1, (hi + a.unit_keys - 1) / a.unit_keys - lo / a.unit_keys);
-    return it;
-}
-
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
     __shared__ int coarse[kCoarse];
     __shared__ int warp_sum[32];
@@ -68,7 +32,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
     for (int base = 0; base < a.n_items; base += kPlanThreads) {
         const int i = base + threadIdx.x;
         PagedItem it{};
-        if (i < a.n_items) it = make_item(a, i);
+        if (i < a.n_items) it = paged_item(a, i);
         int incl = it.units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -130,66 +94,108 @@ __device__ __forceinline__ void store4(__nv_bfloat16* o, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-constexpr int kMergeRows = 8;   // rows of a merge block, one per warp
+constexpr int kMergeWarps = 16, kMergeRows = 16, kMergeBatch = 8;
 
-// Block (c - 1, rows): the (item, head) that share c enters in its middle, if
-// share c is the first to do so.  One warp per row, four dims per lane (dims
-// past head_dim idle): the maxima and weights of up to 32 partials at a time
-// in the lanes, then each partial's row scaled and added in share order.
+// Block (c - 1, y): rows 16 y .. of the (item, head) that share c enters in
+// its middle, if share c is the first to do so.  The 16 warps are dealt to the
+// rows (one each, or several to a row when there are few), a row's warps take
+// its partials in turn, eight loads in flight a lane, four dims a lane (lanes
+// past head_dim idle); a row's warps are joined through shared memory, in
+// order.  A long sequence has a partial per CTA, so it is the loads in flight that
+// count here: 57 partials of 4 rows 12 -> 4 us against a warp per row.
 template <typename T, int DH>
-__global__ void __launch_bounds__(32 * kMergeRows) merge_kernel(PagedAttn a) {
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(PagedAttn a) {
+    __shared__ float sO[kMergeWarps][DH];
+    __shared__ float2 sML[kMergeWarps];
     pdl_wait();
     const int c = blockIdx.x + 1;
     const PagedShare sh = a.shares[c];
+    const int prev = a.shares[c - 1].u0;
     if (sh.item < 0 || sh.off == 0) return;
-    const int start = sh.u0 - sh.off, prev = a.shares[c - 1].u0;
+    const int start = sh.u0 - sh.off;
     if (prev > start) return;
     const PagedItem it = sh.first;
-    const int end = start + it.units, row0 = it.row0, n = it.rows;
-    const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= n * a.G) return;
+    const int end = start + it.units;
+    const int rows = min(it.rows * a.G - (int)blockIdx.y * kMergeRows, kMergeRows);
+    if (rows <= 0) return;
+    // partials: shares c - 1, c, ... that begin before the end
+    int parts = 1;
+    for (int k0 = c;; k0 += 32 * kMergeWarps) {
+        const int k = k0 + threadIdx.x;
+        const int n = __syncthreads_count(k < a.n_cta && a.shares[k].item >= 0 && a.shares[k].u0 < end);
+        parts += n;
+        if (n < 32 * kMergeWarps) break;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wpr = kMergeWarps >> (32 - __clz(rows - 1));   // warps of a row: 16 / (rows rounded up to a power of two)
+    const int m = warp / wpr, sub = warp % wpr, row = blockIdx.y * kMergeRows + m;
     const size_t stride = (size_t)2 * a.tile_rows;   // rows from one share's first slot to the next's
     const size_t first = (size_t)(c - 1) * stride + (prev == start ? 0 : a.tile_rows) + row;
-    float M = -INFINITY;
-    for (int k0 = 0;; k0 += 32) {
-        const int k = k0 + lane;   // partial k belongs to share c - 1 + k
-        const bool live = c - 1 + k < a.n_cta && (k == 0 || (a.shares[c - 1 + k].item >= 0 && a.shares[c - 1 + k].u0 < end));
-        if (live) M = fmaxf(M, a.part_ml[2 * (k == 0 ? first : (size_t)(c - 1 + k) * stride + row)]);
-        if (!__all_sync(0xffffffffu, live)) break;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
+    float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0;; k0 += 32) {
-        const int k = k0 + lane;
-        const bool live = c - 1 + k < a.n_cta && (k == 0 || (a.shares[c - 1 + k].item >= 0 && a.shares[c - 1 + k].u0 < end));
-        const size_t at = k == 0 ? first : (size_t)(c - 1 + k) * stride + row;
-        float w = 0.f, l = 0.f;
-        if (live) {
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
-            w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);   // a share that saw no key of the row takes no part
-            l = w * ml.y;
-        }
-        const int parts = __popc(__ballot_sync(0xffffffffu, live));
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            L += __shfl_sync(0xffffffffu, l, i);
-            if (wi != 0.f && lane < DH / 4) {
-                const size_t ai = k0 + i == 0 ? first : (size_t)(c - 1 + k0 + i) * stride + row;
-                const float4 o = *reinterpret_cast<const float4*>(a.part_o + ai * DH + 4 * lane);
-                acc.x += wi * o.x;
-                acc.y += wi * o.y;
-                acc.z += wi * o.z;
-                acc.w += wi * o.w;
+    for (int k0 = sub; m < rows && k0 < parts; k0 += wpr * kMergeBatch) {
+        float2 ml[kMergeBatch];
+        float4 o[kMergeBatch];
+#pragma unroll
+        for (int x = 0; x < kMergeBatch; ++x) {
+            const int k = k0 + x * wpr;
+            ml[x] = make_float2(-INFINITY, 0.f);
+            o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < parts) {
+                const size_t at = k == 0 ? first : (size_t)(c - 1 + k) * stride + row;
+                ml[x] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+                if (lane < DH / 4) o[x] = *reinterpret_cast<const float4*>(a.part_o + at * DH + 4 * lane);
             }
         }
-        if (parts < 32) break;
+        float top = M;
+#pragma unroll
+        for (int x = 0; x < kMergeBatch; ++x) top = fmaxf(top, ml[x].x);
+        const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+        M = top;
+        L *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int x = 0; x < kMergeBatch; ++x) {
+            // a share that saw no key of the row takes no part
+            const float w = ml[x].x == -INFINITY ? 0.f : exp2f(ml[x].x - M);
+            if (w != 0.f) {
+                L = fmaf(w, ml[x].y, L);
+                acc.x = fmaf(w, o[x].x, acc.x);
+                acc.y = fmaf(w, o[x].y, acc.y);
+                acc.z = fmaf(w, o[x].z, acc.z);
+                acc.w = fmaf(w, o[x].w, acc.w);
+            }
+        }
+    }
+    if (wpr > 1) {   // block-uniform
+        if (lane == 0) sML[warp] = make_float2(M, L);
+        if (lane < DH / 4) *reinterpret_cast<float4*>(&sO[warp][4 * lane]) = acc;
+        __syncthreads();
+        if (sub || m >= rows) return;
+        float top = M;
+        for (int w = 1; w < wpr; ++w) top = fmaxf(top, sML[warp + w].x);
+        const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+        L *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        for (int w = 1; w < wpr; ++w) {
+            const float2 ml = sML[warp + w];
+            const float g = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+            if (g == 0.f) continue;
+            L = fmaf(g, ml.y, L);
+            if (lane < DH / 4) {
+                const float4 o = *reinterpret_cast<const float4*>(&sO[warp + w][4 * lane]);
+                acc.x = fmaf(g, o.x, acc.x);
+                acc.y = fmaf(g, o.y, acc.y);
+                acc.z = fmaf(g, o.z, acc.z);
+                acc.w = fmaf(g, o.w, acc.w);
+            }
+        }
+    } else if (m >= rows) {
+        return;
     }
     const float inv = L > 0.f ? 1.0f / L : 0.f;
     if (lane < DH / 4)
-        store4(reinterpret_cast<T*>(a.out) + (int64_t)(row0 + row / a.G) * a.out_stride +
+        store4(reinterpret_cast<T*>(a.out) + (int64_t)(it.row0 + row / a.G) * a.out_stride +
                    (int64_t)(sh.head * a.G + row % a.G) * DH + 4 * lane,
                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
 }
@@ -204,9 +210,9 @@ cudaError_t launch_paged_plan(const PagedAttn& a, cudaStream_t s) {
 cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cudaStream_t s) {
     if (a.n_cta < 2) return cudaSuccess;
     const dim3 grid((unsigned)a.n_cta - 1, (unsigned)((a.positions * a.G + kMergeRows - 1) / kMergeRows));
-    if (dtype == KVR_BF16) KVR_LAUNCH(merge_kernel<__nv_bfloat16, 128>, grid, dim3(32 * kMergeRows), 0, s, a);
-    else if (head_dim == 64) KVR_LAUNCH(merge_kernel<float, 64>, grid, dim3(32 * kMergeRows), 0, s, a);
-    else KVR_LAUNCH(merge_kernel<float, 128>, grid, dim3(32 * kMergeRows), 0, s, a);
+    if (dtype == KVR_BF16) KVR_LAUNCH(merge_kernel<__nv_bfloat16, 128>, grid, dim3(32 * kMergeWarps), 0, s, a);
+    else if (head_dim == 64) KVR_LAUNCH(merge_kernel<float, 64>, grid, dim3(32 * kMergeWarps), 0, s, a);
+    else KVR_LAUNCH(merge_kernel<float, 128>, grid, dim3(32 * kMergeWarps), 0, s, a);
     return cudaSuccess;
 }
 

@@ -6,10 +6,11 @@
 // pages).  Read is the inverse of the write.  Both move each byte once and do
 // a few flops on it: HBM-bound for prompts, launch-bound for decode steps.
 //
-// One CTA per packed row.  Sixteen or eight threads share a head's row and
-// own whole rotation pairs, so nothing is exchanged between threads but the
-// extrema of a 4-bit group, and a thread's (cos, sin) stay in registers over
-// the row's heads.  Rotation: fp32, products and sum rounded separately, so
+// A CTA takes a few packed rows (up to 8, so that models of few heads fill its
+// threads too): a warp per row finds the row's sequence and slot, then all
+// threads walk the rows' (row, head) units.  Sixteen or eight threads share a
+// unit and own whole rotation pairs, so nothing is exchanged between threads
+// but the extrema of a 4-bit group.  Rotation: fp32, products and sum rounded separately, so
 // that a plain elementwise evaluation gives the same bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -19,7 +20,7 @@
 namespace kvr {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kMaxRows = 8;
 
 // Sequence that owns row r: the number of ends cu[b+1] <= r.  Every lane of
 // the warp gets it; -1 when r lies past the last sequence or cu is malformed
@@ -86,54 +87,77 @@ struct Pair<float> {
     }
 };
 
-// Where row r goes: its page row for head 0, or -1 (reported) when it may not
-// be written.
-__device__ __forceinline__ int64_t append_slot(const PagedRowIo& a, int r, int b, int g) {
-    if (g < 0 || g >= a.p.capacity || (a.rope && g >= a.rope_len)) {
-        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, g);
-        return -1;
+// Slots of the CTA's rows in shared memory: the page row of head 0 and the
+// position, page row -1 for a row that is not to be touched.  kAppend checks
+// what a write needs besides.
+struct RowSlot {
+    int64_t at;
+    int g;
+};
+template <bool kAppend>
+__device__ __forceinline__ void find_slots(const PagedRowIo& a, RowSlot* slots, int rows) {
+    for (int i = threadIdx.x >> 5; i < rows; i += kRowThreads / 32) {   // a warp per row
+        const int r = blockIdx.x * a.rows_per_block + i, lane = threadIdx.x & 31;
+        const int b = r < a.r.n_rows ? owner(a.p, a.r, r) : -1;
+        int64_t at = -1;
+        int g = 0;
+        if (b >= 0) {
+            g = a.r.pos[r];
+            int bad = 0;
+            if (g < 0 || g >= a.p.capacity || (kAppend && a.rope && g >= a.rope_len)) bad = DEV_ERR_INDEX;
+            else if (kAppend && r > a.r.cu[b] && a.r.pos[r - 1] >= g) bad = DEV_ERR_ORDER;
+            int id = 0;
+            if (!bad) {
+                id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];
+                if ((unsigned)id >= (unsigned)a.p.n_pages) bad = DEV_ERR_INDEX;
+            }
+            if (!bad) at = paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
+            else if (lane == 0) paged_err(a.p, bad, g);
+        }
+        if (lane == 0) slots[i] = RowSlot{at, g};
     }
-    if (r > a.r.cu[b] && a.r.pos[r - 1] >= g) {
-        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_ORDER, g);
-        return -1;
-    }
-    const int id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];
-    if ((unsigned)id >= (unsigned)a.p.n_pages) {
-        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, id);
-        return -1;
-    }
-    return paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
+    __syncthreads();
 }
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(PagedRowIo a) {
-    constexpr int E = Pair<T>::E, VT = DH / 2 / E;   // elements per vector, threads per head's row
-    constexpr int kBytes = DH * (int)sizeof(T), kUnits = kRowThreads / VT;
-    const int r = blockIdx.x;
-    const int b = owner(a.p, a.r, r);
-    if (b < 0) return;
-    const int g = a.r.pos[r];
-    const int64_t row = append_slot(a, r, b, g);
-    if (row < 0) return;
+    constexpr int E = Pair<T>::E, VT = DH / 2 / E;   // elements per vector, threads per unit
+    constexpr int kBytes = DH * (int)sizeof(T);
+    __shared__ RowSlot slots[kMaxRows];
+    find_slots<true>(a, slots, a.rows_per_block);
     const int v = threadIdx.x % VT, H = a.p.n_kv_heads;
-    float2 cs[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) cs[e] = a.rope ? a.rope[(int64_t)g * (DH / 2) + v * E + e] : make_float2(1.f, 0.f);
-    for (int u = threadIdx.x / VT; u < 2 * H + (a.q_in ? a.n_q_heads : 0); u += kUnits) {
+    float2 cs[E];   // of the row in hand
+    int in_hand = -1;
+    for (int x = threadIdx.x / VT; x < a.rows_per_block * a.units; x += kRowThreads / VT) {
+        const int i = x / a.units, u = x - i * a.units;
+        const RowSlot slot = slots[i];
+        if (slot.at < 0) continue;
+        const int64_t r = (int64_t)blockIdx.x * a.rows_per_block + i;
         const uint8_t* src;
         uint8_t* dst;
         if (u < H) {
             src = a.k_in + r * a.k_stride + (int64_t)u * kBytes;
-            dst = a.p.k + (row + u * a.p.head_stride) * kBytes;
+            dst = a.p.k + (slot.at + u * a.p.head_stride) * kBytes;
         } else if (u < 2 * H) {
             src = a.v_in + r * a.v_stride + (int64_t)(u - H) * kBytes;
-            dst = a.p.v + (row + (u - H) * a.p.head_stride) * kBytes;
+            dst = a.p.v + (slot.at + (u - H) * a.p.head_stride) * kBytes;
         } else {
             src = a.q_in + r * a.q_stride + (int64_t)(u - 2 * H) * kBytes;
-            dst = a.q_out + ((int64_t)r * a.n_q_heads + u - 2 * H) * kBytes;
+            dst = a.q_out + (r * a.n_q_heads + u - 2 * H) * kBytes;
         }
         uint4 lo = reinterpret_cast<const uint4*>(src)[v], hi = reinterpret_cast<const uint4*>(src)[v + VT];
-        if (a.rope && (u < H || u >= 2 * H)) Pair<T>::rotate(lo, hi, cs);
+        if (a.rope && (u < H || u >= 2 * H)) {
+            if (i != in_hand) {
+                in_hand = i;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float4 w = *reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * (DH / 2) + v * E + e);
+                    cs[e] = make_float2(w.x, w.y);
+                    cs[e + 1] = make_float2(w.z, w.w);
+                }
+            }
+            Pair<T>::rotate(lo, hi, cs);
+        }
         reinterpret_cast<uint4*>(dst)[v] = lo;
         reinterpret_cast<uint4*>(dst)[v + VT] = hi;
     }
@@ -153,24 +177,18 @@ __device__ __forceinline__ void extremum8(float& lo, float& hi) {
 
 template <int NG>
 __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) {
-    constexpr int kUnits = kRowThreads / 8, kJoin = 4 / NG;
-    const int r = blockIdx.x;
-    const int b = owner(a.p, a.r, r);
-    if (b < 0) return;
-    const int g = a.r.pos[r];
-    const int64_t row = append_slot(a, r, b, g);
-    if (row < 0) return;
+    constexpr int kJoin = 4 / NG;
+    __shared__ RowSlot slots[kMaxRows];
+    find_slots<true>(a, slots, a.rows_per_block);
     const int v = threadIdx.x % 8, H = a.p.n_kv_heads;
-    float2 cs[8];   // dims 4v..4v+3 and 32 + 4v..
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        cs[e] = a.rope ? a.rope[(int64_t)g * 64 + (e >> 2) * 32 + 4 * v + (e & 3)] : make_float2(1.f, 0.f);
-    const int n_units = 2 * H + (a.q_in ? a.n_q_heads : 0);
+    const int total = a.rows_per_block * a.units;
     // every thread of a warp runs the same rounds: the shuffles below need
     // the whole warp
-    for (int u0 = 0; u0 < n_units; u0 += kUnits) {
-        const int u = u0 + threadIdx.x / 8;
-        const bool live = u < n_units, is_q = u >= 2 * H, is_v = !is_q && u >= H;
+    for (int x0 = 0; x0 < total; x0 += kRowThreads / 8) {
+        const int n = x0 + threadIdx.x / 8, ri = min(n, total - 1) / a.units, u = n - ri * a.units;
+        const RowSlot slot = slots[ri];
+        const int64_t r = (int64_t)blockIdx.x * a.rows_per_block + ri, row = slot.at;
+        const bool live = n < total && row >= 0, is_q = u >= 2 * H, is_v = !is_q && u >= H;
         const uint8_t* src = a.k_in;
         if (live)
             src = is_q ? a.q_in + r * a.q_stride + (int64_t)(u - 2 * H) * 256
@@ -185,17 +203,25 @@ __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) 
             x[4 * i + 2] = __uint_as_float(w.y << 16);
             x[4 * i + 3] = __uint_as_float(w.y & 0xffff0000u);
         }
-        if (a.rope && !is_v) {
+        if (a.rope && live && !is_v) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) turn(x[e], x[e + 8], cs[e]);
+            for (int i = 0; i < 2; ++i) {   // dims 4v.. and 32 + 4v.. with their pairs 64 further
+                const float4* cs = reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * 64 + 32 * i + 4 * v);
+                const float4 c0 = cs[0], c1 = cs[1];
+                turn(x[4 * i], x[4 * i + 8], make_float2(c0.x, c0.y));
+                turn(x[4 * i + 1], x[4 * i + 9], make_float2(c0.z, c0.w));
+                turn(x[4 * i + 2], x[4 * i + 10], make_float2(c1.x, c1.y));
+                turn(x[4 * i + 3], x[4 * i + 11], make_float2(c1.z, c1.w));
+            }
         }
         if (live && is_q) {
-            uint8_t* dst = a.q_out + ((int64_t)r * a.n_q_heads + u - 2 * H) * 256;
+            uint8_t* dst = a.q_out + (r * a.n_q_heads + u - 2 * H) * 256;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<uint2*>(dst + 64 * i + 8 * v) =
                     make_uint2(pack2(x[4 * i], x[4 * i + 1]), pack2(x[4 * i + 2], x[4 * i + 3]));
         }
+        if (__all_sync(0xffffffffu, !live || is_q)) continue;   // nothing to quantise in this warp
         float lo[NG], hi[NG];
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -65504.f), 65504.f);   // fp16's range
@@ -223,7 +249,7 @@ __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) 
             const __half oh = __float2half_rn(lo[n]);
             const float s = __half2float(sh), o = __half2float(oh);
             const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
-            if (v == n) meta[n] = __halves2half2(sh, oh);
+            if (v == n) meta[n] = __halves2half2(sh, oh);   // NG <= 4 of the eight threads
 #pragma unroll
             for (int i = n * kJoin; i < (n + 1) * kJoin; ++i) {
                 unit[i] = 0u;
@@ -239,88 +265,82 @@ __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) 
     }
 }
 
-// Page row of row r of a read, or -1 (reported).
-__device__ __forceinline__ int64_t read_slot(const PagedRowIo& a, int b, int g) {
-    if (g < 0 || g >= a.p.capacity) {
-        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, g);
-        return -1;
-    }
-    const int id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];
-    if ((unsigned)id >= (unsigned)a.p.n_pages) {
-        if (threadIdx.x == 0) paged_err(a.p, DEV_ERR_INDEX, id);
-        return -1;
-    }
-    return paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
-}
-
-// NG = 0: rows copied as they are (VT 16-byte vectors); else 4-bit rows.
+// NG = 0: rows copied as they are (VT 16-byte vectors); else 4-bit rows.  K heads first, then V heads;
+// when only one of the two is wanted, its heads alone.
 template <int VT, int NG>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(PagedRowIo a) {
-    constexpr int kThreadsPerRow = NG ? 8 : VT, kUnits = kRowThreads / kThreadsPerRow;
-    const int r = blockIdx.x;
-    const int b = owner(a.p, a.r, r);
-    if (b < 0) return;
-    const int64_t row = read_slot(a, b, a.r.pos[r]);
-    if (row < 0) return;
-    const int v = threadIdx.x % kThreadsPerRow, H = a.p.n_kv_heads;
-    for (int u = threadIdx.x / kThreadsPerRow; u < 2 * H; u += kUnits) {
-        const bool is_v = u >= H;
-        const int h = is_v ? u - H : u;
-        uint8_t* dst = is_v ? a.v_out : a.k_out;
-        if (!dst) continue;
-        dst += r * (is_v ? a.v_stride : a.k_stride);
+    constexpr int kPerUnit = NG ? 8 : VT;
+    __shared__ RowSlot slots[kMaxRows];
+    find_slots<false>(a, slots, a.rows_per_block);
+    const int v = threadIdx.x % kPerUnit, H = a.p.n_kv_heads;
+    for (int x = threadIdx.x / kPerUnit; x < a.rows_per_block * a.units; x += kRowThreads / kPerUnit) {
+        const int i = x / a.units, u = x - i * a.units;
+        const int64_t row = slots[i].at;
+        if (row < 0) continue;
+        const int64_t r = (int64_t)blockIdx.x * a.rows_per_block + i;
+        const bool is_v = u >= H || !a.k_out;
+        const int h = u >= H ? u - H : u;
+        uint8_t* dst = is_v ? a.v_out + r * a.v_stride : a.k_out + r * a.k_stride;
         const int64_t at = row + h * a.p.head_stride;
-        if (NG == 0) {
+        if constexpr (NG == 0) {
             reinterpret_cast<uint4*>(dst + (int64_t)h * VT * 16)[v] =
                 reinterpret_cast<const uint4*>((is_v ? a.p.v : a.p.k) + at * VT * 16)[v];
         } else {
-            constexpr int N = NG ? NG : 1;
             const uint2 w = *reinterpret_cast<const uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v);
-            const __half2* meta = reinterpret_cast<const __half2*>((is_v ? a.p.vs : a.p.ks) + at * (4 * N));
+            const __half2* meta = reinterpret_cast<const __half2*>((is_v ? a.p.vs : a.p.ks) + at * (4 * NG));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 so = __half22float2(meta[i * N / 4]);
-                const uint32_t unit = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
-                float x[4];
+            for (int g = 0; g < 4; ++g) {
+                const float2 so = __half22float2(meta[g * NG / 4]);
+                const uint32_t unit = (g < 2 ? w.x : w.y) >> (16 * (g & 1));
+                float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = fmaf((float)((unit >> (4 * e)) & 15u), so.x, so.y);
-                *reinterpret_cast<uint2*>(dst + (int64_t)h * 256 + 64 * i + 8 * v) =
-                    make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+                for (int e = 0; e < 4; ++e) y[e] = fmaf((float)((unit >> (4 * e)) & 15u), so.x, so.y);
+                *reinterpret_cast<uint2*>(dst + (int64_t)h * 256 + 64 * g + 8 * v) =
+                    make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
             }
         }
     }
 }
 
+// Rows of a CTA: as many as keep its threads busy for about one round each,
+// while there are CTAs for every SM.
+int rows_per_block(int n_rows, int units, int threads_per_unit) {
+    int n = 1;
+    while (n < kMaxRows && 2 * n * units * threads_per_unit <= 2 * kRowThreads && n_rows / (2 * n) >= 2 * kNumSMs) n *= 2;
+    return n;
+}
+
 }  // namespace
 
-cudaError_t launch_paged_append(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s) {
-    const dim3 grid((unsigned)a.r.n_rows);
-    if (format == KVR_BF16) {
-        KVR_LAUNCH(append_kernel<__nv_bfloat16, 128>, grid, dim3(kRowThreads), 0, s, a);
-    } else if (format == KVR_F32 && head_dim == 64) {
-        KVR_LAUNCH(append_kernel<float, 64>, grid, dim3(kRowThreads), 0, s, a);
-    } else if (format == KVR_F32) {
-        KVR_LAUNCH(append_kernel<float, 128>, grid, dim3(kRowThreads), 0, s, a);
-    } else if (group == 32) {
-        KVR_LAUNCH(append_int4_kernel<4>, grid, dim3(kRowThreads), 0, s, a);
-    } else if (group == 64) {
-        KVR_LAUNCH(append_int4_kernel<2>, grid, dim3(kRowThreads), 0, s, a);
-    } else {
-        KVR_LAUNCH(append_int4_kernel<1>, grid, dim3(kRowThreads), 0, s, a);
-    }
+cudaError_t launch_paged_append(int format, int head_dim, int group, const PagedRowIo& a_in, cudaStream_t s) {
+    PagedRowIo a = a_in;
+    const int per_unit = format == KVR_F32 && head_dim == 128 ? 16 : 8;
+    a.units = 2 * a.p.n_kv_heads + (a.q_in ? a.n_q_heads : 0);
+    a.rows_per_block = rows_per_block(a.r.n_rows, a.units, per_unit);
+    const dim3 grid((unsigned)((a.r.n_rows + a.rows_per_block - 1) / a.rows_per_block)), block(kRowThreads);
+    if (format == KVR_BF16) KVR_LAUNCH(append_kernel<__nv_bfloat16, 128>, grid, block, 0, s, a);
+    else if (format == KVR_F32 && head_dim == 64) KVR_LAUNCH(append_kernel<float, 64>, grid, block, 0, s, a);
+    else if (format == KVR_F32) KVR_LAUNCH(append_kernel<float, 128>, grid, block, 0, s, a);
+    else if (group == 32) KVR_LAUNCH(append_int4_kernel<4>, grid, block, 0, s, a);
+    else if (group == 64) KVR_LAUNCH(append_int4_kernel<2>, grid, block, 0, s, a);
+    else KVR_LAUNCH(append_int4_kernel<1>, grid, block, 0, s, a);
     return cudaSuccess;
 }
 
-cudaError_t launch_paged_read(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s) {
-    const dim3 grid((unsigned)a.r.n_rows);
+cudaError_t launch_paged_read(int format, int head_dim, int group, const PagedRowIo& a_in, cudaStream_t s) {
+    PagedRowIo a = a_in;
+    const int per_unit = format == KVR_INT4 ? 8 : (format == KVR_F32 && head_dim == 128 ? 32 : 16);
+    a.units = (a.k_out && a.v_out ? 2 : 1) * a.p.n_kv_heads;
+    a.rows_per_block = rows_per_block(a.r.n_rows, a.units, per_unit);
+    const dim3 grid((unsigned)((a.r.n_rows + a.rows_per_block - 1) / a.rows_per_block)), block(kRowThreads);
     if (format == KVR_INT4) {
-        if (group == 32) KVR_LAUNCH(read_kernel<16, 4>, grid, dim3(kRowThreads), 0, s, a);
-        else if (group == 64) KVR_LAUNCH(read_kernel<16, 2>, grid, dim3(kRowThreads), 0, s, a);
-        else KVR_LAUNCH(read_kernel<16, 1>, grid, dim3(kRowThreads), 0, s, a);
+        if (group == 32) KVR_LAUNCH(read_kernel<16, 4>, grid, block, 0, s, a);
+        else if (group == 64) KVR_LAUNCH(read_kernel<16, 2>, grid, block, 0, s, a);
+        else KVR_LAUNCH(read_kernel<16, 1>, grid, block, 0, s, a);
     } else if (format == KVR_F32 && head_dim == 128) {
-        KVR_LAUNCH(read_kernel<32, 0>, grid, dim3(kRowThreads), 0, s, a);
+        KVR_LAUNCH(read_kernel<32, 0>, grid, block, 0, s, a);
     } else {   // bf16 of 128 dims, fp32 of 64: 256-byte rows
-        KVR_LAUNCH(read_kernel<16, 0>, grid, dim3(kRowThreads), 0, s, a);
+        KVR_LAUNCH(read_kernel<16, 0>, grid, block, 0, s, a);
     }
     return cudaSuccess;
 }

@@ -475,6 +475,7 @@ def pages(fmt: str, k, v, page_table, kv_len, err, n_kv_heads: int, page_size: i
     p.tensors = (k, v, k_scale, v_scale, page_table, kv_len, err)
     p.device = dev
     p.row_dtype = _ROW_DTYPES[f]
+    p.addr = C.addressof(p)
     return p
 
 
@@ -491,30 +492,41 @@ def score_opts(scale: float = 0.0, softcap: float = 0.0, alpha: float = 0.0, bet
     o = kvr_score_opts(scale, softcap, alpha, beta, _ptr(local_bits), _ptr(sink_bits), _ptr(slopes), _ptr(key_begin),
                        _ptr(key_end))
     o.tensors = (local_bits, sink_bits, slopes, key_begin, key_end)
+    o.given = [(what, None, None) if t is None else (what, t.numel(), t.device) for t, what in
+               zip(o.tensors, ("local_bits", "sink_bits", "slopes", "key_begin", "key_end"))]
+    o.addr = C.addressof(o)
     return o
 
 
 def _packed_rows(p: kvr_pages, t, what: str, n: int):
-    """(pointer, row stride in elements) of a [rows, heads, head_dim] operand."""
-    if t.dtype != p.row_dtype or t.device != p.device or t.dim() != 3 or t.shape[0] < n or t.shape[2] != p.head_dim or \
-            t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != p.head_dim) or \
-            (t.shape[0] > 1 and t.stride(0) < t.shape[1] * p.head_dim):
-        raise ValueError(f"{what}: need [{n}, heads, {p.head_dim}] of {p.row_dtype} on {p.device}, a row's heads "
-                         f"contiguous; got {tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
+    """(pointer, row stride in elements, heads) of a [rows, heads, head_dim] operand."""
+    dh = p.head_dim
+    try:
+        rows, heads, d = t.shape
+        s0, s1, s2 = t.stride()
+    except ValueError:
+        rows = -1
+    if rows < n or d != dh or s2 != 1 or (s1 != dh and heads > 1) or (s0 < heads * dh and rows > 1) or \
+            t.dtype is not p.row_dtype or t.device != p.device:
+        raise ValueError(f"{what}: need [{n}, heads, {dh}] of {p.row_dtype} on {p.device}, a row's heads contiguous; "
+                         f"got {tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
     # the stride of a single row is whatever torch says; the library wants a full one
-    return t.data_ptr(), max(t.stride(0), t.shape[1] * p.head_dim)
+    return t.data_ptr(), s0 if s0 > heads * dh else heads * dh, heads
 
 
 def _rows(p: kvr_pages, cu_rows, positions):
-    if torch.cuda.current_device() != p.device.index:
-        raise ValueError(f"the pages are on {p.device}, the current device is cuda:{torch.cuda.current_device()}")
-    _int_array(cu_rows, "cu_rows", p.batch + 1, p.device)
-    _int_array(positions, "positions", None, p.device)
-    return positions.numel()
+    """(n_rows, the two pointers).  A call on pages of another device than the
+    current one fails in the launch: its stream is of the pages' device."""
+    if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.device != p.device:
+        _int_array(positions, "positions", None, p.device)
+    if cu_rows.dtype is not torch.int32 or not cu_rows.is_contiguous() or cu_rows.device != p.device or \
+            cu_rows.numel() <= p.batch:
+        _int_array(cu_rows, "cu_rows", p.batch + 1, p.device)
+    return positions.numel(), cu_rows.data_ptr(), positions.data_ptr()
 
 
 def _paged_stream(p: kvr_pages, stream) -> int:
-    return torch.cuda.current_stream(p.device).cuda_stream if stream is None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(p.device.index) if stream is None else _stream(stream)
 
 
 def kvr_paged_append(p: kvr_pages, cu_rows, positions, k_rows, v_rows, rope=None, q_rows=None, q_out=None,
@@ -522,39 +534,39 @@ def kvr_paged_append(p: kvr_pages, cu_rows, positions, k_rows, v_rows, rope=None
     """k_rows, v_rows: [n_rows, n_kv_heads, head_dim]; rope: fp32 [rope_len,
     head_dim / 2, 2] (cos, sin) or None; q_rows, q_out: [n_rows, n_q_heads,
     head_dim] (q_out packed) or None."""
-    n = _rows(p, cu_rows, positions)
-    kp, ks = _packed_rows(p, k_rows, "k_rows", n)
-    vp, vs = _packed_rows(p, v_rows, "v_rows", n)
-    if k_rows.shape[1] != p.n_kv_heads or v_rows.shape[1] != p.n_kv_heads:
+    n, cu, pos = _rows(p, cu_rows, positions)
+    kp, ks, kh = _packed_rows(p, k_rows, "k_rows", n)
+    vp, vs, vh = _packed_rows(p, v_rows, "v_rows", n)
+    if kh != p.n_kv_heads or vh != p.n_kv_heads:
         raise ValueError(f"k_rows, v_rows: need {p.n_kv_heads} heads")
-    qp = qs = qo = None
-    hq = 0
+    qp, qs, qo, hq = None, 0, None, 0
     if q_rows is not None and q_out is not None:
-        qp, qs = _packed_rows(p, q_rows, "q_rows", n)
-        qo, _ = _packed_rows(p, q_out, "q_out", n)
-        hq = q_rows.shape[1]
-        if q_out.shape[1] != hq or not q_out.is_contiguous():
+        qp, qs, hq = _packed_rows(p, q_rows, "q_rows", n)
+        qo, _, ho = _packed_rows(p, q_out, "q_out", n)
+        if ho != hq or not q_out.is_contiguous():
             raise ValueError("q_out: need a packed tensor of q_rows' heads")
     elif q_rows is not None or q_out is not None:
         raise ValueError("q_rows and q_out go together")
-    if rope is not None and (not _want(rope, "rope", torch.float32, 3, p.device).is_contiguous() or
-                             rope.shape[1:] != (p.head_dim // 2, 2)):
-        raise ValueError(f"rope: need a contiguous [rope_len, {p.head_dim // 2}, 2]")
-    _check(lib.kvr_paged_append(C.byref(p), n, cu_rows.data_ptr(), positions.data_ptr(), kp, ks, vp, vs, _ptr(rope),
-                                0 if rope is None else rope.shape[0], qp, qs or 0, qo, hq, _paged_stream(p, stream)),
-           "kvr_paged_append")
+    table, rope_len = None, 0
+    if rope is not None:
+        if rope.dtype is not torch.float32 or not rope.is_contiguous() or rope.device != p.device or \
+                rope.shape[1:] != (p.head_dim // 2, 2):
+            raise ValueError(f"rope: need a contiguous fp32 [rope_len, {p.head_dim // 2}, 2] on {p.device}")
+        table, rope_len = rope.data_ptr(), rope.shape[0]
+    _check(lib.kvr_paged_append(p.addr, n, cu, pos, kp, ks, vp, vs, table, rope_len, qp, qs, qo, hq,
+                                _paged_stream(p, stream)), "kvr_paged_append")
 
 
 def kvr_paged_read(p: kvr_pages, cu_rows, positions, k_out=None, v_out=None, stream=None):
     """k_out, v_out: [n_rows, n_kv_heads, head_dim] in the row type, or None."""
-    n = _rows(p, cu_rows, positions)
-    ptrs = []
+    n, cu, pos = _rows(p, cu_rows, positions)
+    args = []
     for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and t.shape[1:2] != (p.n_kv_heads,):
+        ptr, stride, heads = (None, 0, p.n_kv_heads) if t is None else _packed_rows(p, t, what, n)
+        if heads != p.n_kv_heads:
             raise ValueError(f"{what}: need {p.n_kv_heads} heads")
-        ptrs += (None, 0) if t is None else _packed_rows(p, t, what, n)
-    _check(lib.kvr_paged_read(C.byref(p), n, cu_rows.data_ptr(), positions.data_ptr(), *ptrs,
-                              _paged_stream(p, stream)), "kvr_paged_read")
+        args += (ptr, stride)
+    _check(lib.kvr_paged_read(p.addr, n, cu, pos, *args, _paged_stream(p, stream)), "kvr_paged_read")
 
 
 def kvr_paged_workspace_bytes(p: kvr_pages, n_q_heads: int, n_rows: int, max_rows: int) -> int:
@@ -565,21 +577,21 @@ def kvr_paged_attend(p: kvr_pages, opts: Optional[kvr_score_opts], max_rows: int
                      workspace, stream=None):
     """q, out: [n_rows, n_q_heads, head_dim]; workspace: uint8 of
     kvr_paged_workspace_bytes; opts: score_opts(...) or None."""
-    n = _rows(p, cu_rows, positions)
-    qp, qs = _packed_rows(p, q, "q", n)
-    op, os_ = _packed_rows(p, out, "out", n)
-    if out.shape[1] != q.shape[1]:
+    n, cu, pos = _rows(p, cu_rows, positions)
+    qp, qs, hq = _packed_rows(p, q, "q", n)
+    op, os_, ho = _packed_rows(p, out, "out", n)
+    if ho != hq:
         raise ValueError("out: need q's heads")
     if opts is not None:
         words = -(-p.max_pages * p.page_size // 32) * p.batch
-        for t, what, need in zip(opts.tensors, ("local_bits", "sink_bits", "slopes", "key_begin", "key_end"),
-                                 (words, words, q.shape[1], n, n)):
-            if t is not None and (t.numel() < need or t.device != p.device):
+        for (what, numel, device), need in zip(opts.given, (words, words, hq, n, n)):
+            if numel is not None and (numel < need or device != p.device):
                 raise ValueError(f"{what}: need {need} elements on {p.device}")
-    _want(workspace, "workspace", torch.uint8, 1, p.device)
-    _check(lib.kvr_paged_attend(C.byref(p), None if opts is None else C.byref(opts), q.shape[1], n, max_rows,
-                                cu_rows.data_ptr(), positions.data_ptr(), qp, qs, op, os_, workspace.data_ptr(),
-                                workspace.numel(), _paged_stream(p, stream)), "kvr_paged_attend")
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != p.device:
+        _want(workspace, "workspace", torch.uint8, 1, p.device)
+    _check(lib.kvr_paged_attend(p.addr, None if opts is None else opts.addr, hq, n, max_rows, cu, pos, qp, qs, op, os_,
+                                workspace.data_ptr(), workspace.numel(), _paged_stream(p, stream)),
+           "kvr_paged_attend")
 
 
 def kvr_paged_status(p: kvr_pages, stream=None):
