@@ -91,6 +91,8 @@ cudaError_t launch_paged_plan(const PagedAttn& a, cudaStream_t s);
 cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cudaStream_t s);
 cudaError_t launch_paged_simt(int format, int head_dim, int group, const PagedAttn& a, cudaStream_t s);
 
+// Items of two tiles of 128 / G positions each, bf16 or 4-bit pages, units of 128 keys.
+cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStream_t s, std::string* why);
 // Up to 16 rows (positions * G) an item, bf16 or 4-bit pages.
 cudaError_t launch_paged_decode(int format, int group, const PagedAttn& a, cudaStream_t s);
 int paged_decode_unit(int format);
@@ -114,15 +116,15 @@ cudaError_t allow_smem(void (*kernel)(A...), int bytes, std::atomic<uint64_t>* d
     return e;
 }
 
-static __device__ __noinline__ void paged_err(const PagedView& p, int bit, int detail) {
-    if (atomicOr(&p.err[0], bit) == 0) p.err[1] = detail;
+__device__ __forceinline__ void paged_err(int* err, int bit, int detail) {
+    if (atomicOr(&err[0], bit) == 0) err[1] = detail;
 }
 
 // First page row of (page, head), in rows; a page outside the pool is
 // reported and page 0 taken in its place, so no access leaves the pool.
 __device__ __forceinline__ int paged_id(const PagedView& p, int id) {
     if ((unsigned)id >= (unsigned)p.n_pages) {
-        paged_err(p, DEV_ERR_INDEX, id);
+        paged_err(p.err, DEV_ERR_INDEX, id);
         return 0;
     }
     return id;
@@ -137,7 +139,7 @@ __device__ __forceinline__ int paged_seq_rows(const PagedView& p, const PagedRow
     const int a = r.cu[b], e = r.cu[b + 1];
     *row0 = a;
     if (a < 0 || e < a || e > r.n_rows) {
-        paged_err(p, DEV_ERR_INDEX, b);
+        paged_err(p.err, DEV_ERR_INDEX, b);
         return 0;
     }
     return e - a;
@@ -161,16 +163,16 @@ __device__ __forceinline__ PagedItem paged_item(const PagedAttn& a, int i) {
     int row0;
     const int n = paged_seq_rows(a.p, a.r, b, &row0);
     if (t == 0) {
-        if (n > a.max_rows) paged_err(a.p, DEV_ERR_INDEX, n);
+        if (n > a.max_rows) paged_err(a.p.err, DEV_ERR_INDEX, n);
         const int kv = a.p.kv_len[b];
-        if (kv < 0 || kv > a.p.capacity) paged_err(a.p, DEV_ERR_INDEX, kv);
+        if (kv < 0 || kv > a.p.capacity) paged_err(a.p.err, DEV_ERR_INDEX, kv);
     }
     const int r0 = t * a.positions, r1 = min(min(n, a.max_rows), r0 + a.positions);
     if (r0 >= r1) return it;
     const int kv = paged_kv_len(a.p, b);
     int lo = 0x7fffffff, hi = 0;
     for (int r = row0 + r0; r < row0 + r1; ++r) {
-        if (a.r.pos[r] < 0) paged_err(a.p, DEV_ERR_INDEX, a.r.pos[r]);
+        if (a.r.pos[r] < 0) paged_err(a.p.err, DEV_ERR_INDEX, a.r.pos[r]);
         int l, h;
         paged_interval(a, r, kv, &l, &h);
         if (l < h) {

@@ -90,7 +90,7 @@ PagedView view(const kvr_pages* p) {
 // Geometry of an attention call: which kernel, its item and share sizes.
 struct Geometry {
     int G, positions, tiles, n_items, unit_keys, n_cta, tile_rows;
-    bool decode;
+    bool decode, tc;
 };
 constexpr int kSimtRows = 16, kSimtKeys = 32;
 
@@ -101,16 +101,21 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     if (max_rows < 1) return fail(KVR_EINVAL, "max_rows must be positive");
     max_rows = std::min(max_rows, n_rows);
     g->decode = p->format != KVR_F32 && (int64_t)max_rows * g->G <= 16;
+    g->tc = p->format != KVR_F32 && !g->decode;
     if (g->decode) {
         g->tile_rows = max_rows * g->G <= 8 ? 8 : 16;
         g->unit_keys = paged_decode_unit(p->format);
         g->n_cta = paged_decode_ctas(p->format == KVR_INT4, g->tile_rows / 8) * kNumSMs;
+    } else if (g->tc) {
+        g->tile_rows = 256;
+        g->unit_keys = 128;
+        g->n_cta = kNumSMs;
     } else {
         g->tile_rows = kSimtRows;
         g->unit_keys = kSimtKeys;
         g->n_cta = 4 * kNumSMs;
     }
-    g->positions = g->tile_rows / g->G;
+    g->positions = g->tc ? 2 * (128 / g->G) : g->tile_rows / g->G;
     g->tiles = (max_rows + g->positions - 1) / g->positions;
     // shares and items are counted in 32 bits
     const int64_t items = (int64_t)g->tiles * p->batch;
@@ -270,9 +275,11 @@ kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int3
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    std::string why;
     a.planned = !g.decode || g.n_items > paged_decode_inline_items();
     if (a.planned) KVR_CHECK_LAUNCH(launch_paged_plan(a, s), "paged plan");
     if (g.decode) KVR_CHECK_LAUNCH(launch_paged_decode(p->format, p->group, a, s), "paged attention");
+    else if (g.tc) KVR_CHECK_LAUNCH(launch_paged_tc(p->format, p->group, a, s, &why), ("paged attention " + why).c_str());
     else KVR_CHECK_LAUNCH(launch_paged_simt(p->format, p->head_dim, p->group, a, s), "paged attention");
     KVR_CHECK_LAUNCH(launch_paged_merge(p->format == KVR_F32 ? KVR_F32 : KVR_BF16, p->head_dim, a, s), "paged merge");
     return KVR_OK;

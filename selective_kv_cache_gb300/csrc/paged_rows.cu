@@ -34,7 +34,7 @@ __device__ __forceinline__ int owner(const PagedView& p, const PagedRows& rr, in
     }
     if (b >= p.batch) return -1;
     if (r < rr.cu[b]) {
-        if (threadIdx.x == 0) paged_err(p, DEV_ERR_INDEX, r);
+        if (threadIdx.x == 0) paged_err(p.err, DEV_ERR_INDEX, r);
         return -1;
     }
     return b;
@@ -112,7 +112,7 @@ __device__ __forceinline__ void find_slots(const PagedRowIo& a, RowSlot* slots, 
                 if ((unsigned)id >= (unsigned)a.p.n_pages) bad = DEV_ERR_INDEX;
             }
             if (!bad) at = paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
-            else if (lane == 0) paged_err(a.p, bad, g);
+            else if (lane == 0) paged_err(a.p.err, bad, g);
         }
         if (lane == 0) slots[i] = RowSlot{at, g};
     }

@@ -1,0 +1,623 @@
+// paged_tc.cu -- attention of many rows over the paged cache on the sm_103a
+// tensor cores (bf16 and 4-bit pages): prompts, refreshed rows, drafted tokens
+// beyond 16 rows per K/V head.
+//
+//   x_rj = cap(scale <q_r, k_j>) + alpha loc_j + beta snk_j - slope |g_r - j|
+//   o_r  = sum_j softmax_j(x_rj) v_j,   j in [lo_r, hi_r)
+//
+// A CTA walks its share of units: 128 keys of one (item, K/V head), an item
+// being up to two tiles of 128 MMA rows (positions x the head's G query
+// heads) that share every K and V tile.  The two tiles alternate on the tensor
+// pipe: while one's softmax runs, the other's products do, and a tile's next
+// scores go over its P as soon as the product with V has read it, so that two
+// score buffers and two outputs fill tensor memory exactly.
+//   warp 0      bf16: K and V pages by TMA into a ring of five 32 KB tiles, a
+//               copy per page and 64-column half (one lane each), K_0 V_0 K_1 V_1 ...
+//   warp 1      tcgen05.mma: S_t = Q_t K^T, O_t += P_t V.  One thread issues all
+//               products; they complete in order, so "S_t of tile j is done" also
+//               says that tile j - 1's product with V is.
+//   warps 4-11  softmax, four warps a row tile, one thread a row: no exchange
+//               between threads.  Base 2; the running maximum is raised, and O
+//               rescaled in tensor memory, only when it grows by more than
+//               2^8.  P goes to tensor memory in 16 bits (bf16; fp16 for 4-bit
+//               pages) as the A operand: 2^-8 (2^-11) of a weight at most.
+//   warps 12-15 4 bits only, in the copies' place: codes to their values in
+//               fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
+//               ring in the operand's swizzle.  A word's nibbles come out in
+//               pairs (e, e + 4), so the 8 dims of a chunk lie in the order 0 4 1
+//               5 2 6 3 7; Q is stored in that order and O read back from it.
+// Bound by the exponentials and the tensor pipe alike: 2 x 128 x 128 of the
+// first and four 128^3 products a unit.
+// Every wait is bounded; on a timeout the CTA records it, drains its copies and
+// products, frees tensor memory and returns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <string>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace kvr {
+namespace {
+
+constexpr uint32_t kHalf = 16384;               // 128 rows x 128 B
+constexpr uint32_t kTile = 2 * kHalf;           // 128 x 128 16-bit values
+constexpr int kRing = 5;
+constexpr uint32_t kOffQ = 0;                   // two row tiles
+constexpr uint32_t kOffRing = 2 * kTile;
+constexpr uint32_t kOffBar = kOffRing + kRing * kTile;
+constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+constexpr uint32_t kColS = 0, kColO = 256;      // TMEM columns of tile t: S (P over its first 64) at 128 t, O at 256 + 128 t
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.0f;
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                              *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t with_1024(uint32_t x, uint32_t mask) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(0x64006400u));
+    return y;
+}
+// code - 8 of the even and of the odd nibble of each half, exact
+__device__ __forceinline__ uint32_t even8(uint32_t x) { return hfma2(with_1024(x, 0x000f000fu), 0x3c003c00u, 0xe408e408u); }
+__device__ __forceinline__ uint32_t odd8(uint32_t x) { return hfma2(with_1024(x, 0x00f000f0u), 0x2c002c00u, 0xd480d480u); }
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+// one lane polls, the whole warp follows (keeps tcgen05 .sync.aligned ops converged)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    int ok = 0;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn_major, int b_mn_major) {   // kind::f16 with fp16 A/B, fp32 D
+    return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// The runs of units (one item and head each) of a CTA's share, in order; every
+// role of the CTA walks them for itself.
+struct Walk {
+    PagedItem it;
+    int i, h, off, u, u1, n;
+    __device__ __forceinline__ Walk(const PagedShare& sh, int end) : it(sh.first), i(sh.item), h(sh.head), off(sh.off), u(sh.u0), u1(end) {
+        n = min(it.units - off, u1 - u);
+    }
+    __device__ __forceinline__ bool live() const { return u < u1; }
+    __device__ __forceinline__ int key0(int s) const { return ((it.klo >> 7) + off + s) << 7; }
+    __device__ __forceinline__ int tiles(int per_tile) const { return it.rows > per_tile ? 2 : 1; }
+    __device__ __forceinline__ void next(const PagedAttn& a) {
+        u += n;
+        off = 0;
+        if (++h == a.p.n_kv_heads) {
+            h = 0;
+            if (u < u1) {
+                do it = a.items[++i];
+                while (it.units == 0);
+            }
+        }
+        n = min(it.units, u1 - u);
+    }
+};
+
+template <bool kInt4, bool kExtra>
+__global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PagedAttn a,
+                    int n_groups) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);   // [kRing] a K or V tile has landed
+    uint64_t* empty = full + kRing;                                 // [kRing] its products are done
+    uint64_t* q_full = empty + kRing;                               // [2] Q_t is in place
+    uint64_t* s_full = q_full + 2;                                  // [2] S_t is done
+    uint64_t* p_full = s_full + 2;                                  // [2] P_t is in tensor memory
+    uint64_t* o_done = p_full + 2;                                  // [2] a run's last product with V is done
+    uint64_t* drained = o_done + 2;                                 // every product issued is done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.G, per_tile = 128 / G;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&full[i], kInt4 ? 4 : 1);
+        for (int i = 0; i < kRing; ++i) mbar_init(&empty[i], 1);
+        mbar_init(drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 4);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0 && !kInt4) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    const PagedShare sh = a.shares[blockIdx.x];
+    const int u1 = sh.item < 0 ? sh.u0 : a.shares[blockIdx.x + 1].u0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+    bool ok = true;
+
+    // registers to the softmax, which holds a row of scores a thread: 72 + 2 x
+    // 216 of 3 x 168 a thread, 64 + 2 x 176 + 96 of 4 x 128
+    if (warp < 4) {
+        reg_dec<kInt4 ? 64 : 72>();
+    if (warp == 0) {
+        if constexpr (!kInt4) {
+            // ---------------------------------------------------------- K and V copies
+            // a lane per (operand half, page): tiles of 16-slot pages take 16 copies each
+            const int shift = min(a.p.page_shift, 7), pages = 128 >> shift;   // pages of a tile
+            const int half = lane & 1, pg = lane >> 1;
+            const uint32_t dst_off = (uint32_t)half * kHalf + ((uint32_t)pg << (shift + 7));
+            int x = 0;   // ring index of the next tile
+            for (Walk w(sh, u1); w.live() && ok; w.next(a)) {
+                const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
+                for (int s = 0; s < w.n && ok; ++s) {
+                    const int k0 = w.key0(s) + (pg << shift);
+                    // pages none of whose keys is visible are not touched
+                    const bool mine = pg < pages && k0 < w.it.khi && k0 + (1 << shift) > w.it.klo;
+                    const int id = mine ? paged_id(a.p, table[k0 >> a.p.page_shift]) : 0;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) << (shift + 7);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++x) {
+                        const int slot = x % kRing;
+                        // a full barrier is armed again only after every poller of its last phase has passed it:
+                        // the products that free the slot waited for it
+                        if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_4d(smem + kOffRing + slot * kTile + dst_off, kv ? &tmV : &tmK, &full[slot], 64 * half,
+                                        k0 & ((1 << a.p.page_shift) - 1), w.h, id);
+                    }
+                }
+            }
+            // let every copy still in flight land before the CTA exits
+            if (!ok)
+                for (int y = max(x - kRing, 0); y < x; ++y) warp_wait(&full[y % kRing], (uint32_t)(y / kRing) & 1u);
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- products
+        if (lane == 0) {
+            const uint32_t id_s = kInt4 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+            const uint32_t id_o = kInt4 ? idesc_f16(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);   // V is MN-major
+            int g = 0, runs[2] = {0, 0}, ps[2] = {0, 0};   // tiles, runs and P tiles so far
+            auto landed = [&](int x) { return mbar_wait(&full[x % kRing], (uint32_t)(x / kRing) & 1u); };
+            auto scores = [&](int t, int x) {
+                const uint32_t qa = sbase + kOffQ + (uint32_t)t * kTile, ka = sbase + kOffRing + (uint32_t)(x % kRing) * kTile;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t o = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
+                    mma_bf16(tmem + kColS + 128u * t, sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(ka + o, 16, 1024), id_s, kk > 0);
+                }
+                mma_commit(&s_full[t]);
+            };
+            for (Walk w(sh, u1); w.live() && ok; w.next(a)) {
+                const int nt = w.tiles(per_tile);
+                for (int t = 0; t < nt && ok; ++t) {
+                    ok = mbar_wait(&q_full[t], (uint32_t)(runs[t]++) & 1u) && (t || landed(2 * g));
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(t, 2 * g);
+                    if (t == nt - 1) mma_commit(&empty[(2 * g) % kRing]);
+                }
+                for (int s = 0; s < w.n && ok; ++s, ++g) {
+                    const int v = 2 * g + 1;
+                    const uint32_t va = sbase + kOffRing + (uint32_t)(v % kRing) * kTile;
+                    for (int t = 0; t < nt; ++t) {
+                        ok = mbar_wait(&p_full[t], (uint32_t)(ps[t]++) & 1u) && (t || landed(v));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t pt = tmem + kColS + 128u * t;
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
+                                        sdesc_sw128(va + (uint32_t)kk * 2048u, kHalf, 1024), id_o, (s > 0 || kk > 0));
+                        if (s == w.n - 1) mma_commit(&o_done[t]);
+                        if (t == nt - 1) mma_commit(&empty[v % kRing]);
+                        if (s + 1 < w.n) {
+                            if (t == 0 && !landed(v + 1)) {
+                                ok = false;
+                                break;
+                            }
+                            scores(t, v + 1);
+                            if (t == nt - 1) mma_commit(&empty[(v + 1) % kRing]);
+                        }
+                    }
+                }
+            }
+            mma_commit(drained);
+            if (!mbar_wait(drained, 0)) ok = false;
+        }
+    }
+    } else if (warp < 12) {
+        reg_inc<kInt4 ? 176 : 216>();
+        // -------------------------------------------------------------- softmax
+        const int t = warp >= 8 ? 1 : 0, m = 32 * (warp & 3) + lane;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + kColS + 128u * t + lane_base, to = tmem + kColO + 128u * t + lane_base;
+        const float sl2 = a.scale * kLog2e;
+        int g = 0, tile = 0, runs = 0;   // tiles of the CTA, tiles and runs of this row tile
+        bool first = true;
+        for (Walk w(sh, u1); w.live() && ok; w.next(a)) {
+            const bool whole = w.n == w.it.units;
+            const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * a.tile_rows;
+            first = false;
+            if (t >= w.tiles(per_tile)) {
+                g += w.n;
+                continue;
+            }
+            const int p = t * per_tile + m / G, gi = m % G;
+            const bool valid = m < per_tile * G && p < w.it.rows;
+            const int64_t row = w.it.row0 + p;
+            const int head = w.h * G + gi;
+            // ---- Q: this thread's row into the operand's swizzle.  The last
+            // run's scores are done with the tile (this thread has seen them).
+            float lsr = sl2;
+            {
+                uint4 q[16];
+                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                                  row * a.q_stride + (int64_t)head * 128);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) q[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (kInt4) {
+                    // to fp16, scaled by a power of two to [128, 256) at the row's largest
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7f80u, (ws[e] >> 16) & 0x7f80u));
+                    }
+                    const int ex = min(max((int)(top >> 7), 8), 253);
+                    const float f = __uint_as_float((uint32_t)(261 - ex) << 23);      // 2^(134 - ex)
+                    lsr = sl2 * __uint_as_float((uint32_t)(ex - 7) << 23);            // 2^(ex - 134)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[2 * e] = __uint_as_float(ws[e] << 16) * f;
+                            x[2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u) * f;
+                        }
+                        q[c] = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
+                    }
+                }
+                const uint32_t dst = sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)m * 128u;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    sts16(dst + (uint32_t)(c >> 3) * kHalf + (uint32_t)(((c & 7) ^ (m & 7)) << 4), q[c]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[t]);
+            // ---- what the row sees
+            int lo = w.it.klo, hi = w.it.khi, gpos = 0;
+            float slope = 0.f;
+            if (valid) {
+                paged_interval(a, (int)row, w.it.kv, &lo, &hi);
+                if (kExtra && a.slopes) {
+                    gpos = a.r.pos[row];
+                    slope = a.slopes[head] * kLog2e;
+                }
+            }
+            const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+            float m_run = -INFINITY, m_neg = 0.f, l_run = 0.f;
+            for (int s = 0; s < w.n; ++s, ++g, ++tile) {
+                const int key0 = w.key0(s);
+                if (!warp_wait(&s_full[t], (uint32_t)tile & 1u)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float x[128];
+                tmem_ld32x2(ts, x);
+                tmem_ld32x2(ts + 64u, x + 64);
+                float ls = lsr;
+                if constexpr (kExtra) {
+                    ls = 1.f;
+                    const float cap_in = a.softcap > 0.f ? 2.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+                    if (a.softcap > 0.f) {
+                        const float c_in = lsr * cap_in;
+#pragma unroll
+                        for (int k = 0; k < 128; ++k)   // cap tanh(u) = cap (1 - 2 / (1 + exp(2u)))
+                            x[k] = fmaf(-2.f * cap_out, __fdividef(1.f, 1.f + ex2(x[k] * c_in)), cap_out);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) x[k] *= lsr;
+                    }
+                    if (a.loc || a.snk) {
+                        const int64_t word = (int64_t)w.it.seq * a.words + (key0 >> 5);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const bool in = (key0 >> 5) + q < a.words;
+                            const uint32_t lw = a.loc && in ? a.loc[word + q] : 0u, sw = a.snk && in ? a.snk[word + q] : 0u;
+                            if ((lw | sw) == 0u) continue;   // warp-uniform
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                float b = ((lw >> k) & 1u) ? a.alpha * kLog2e : 0.f;
+                                b += ((sw >> k) & 1u) ? a.beta * kLog2e : 0.f;
+                                x[32 * q + k] += b;
+                            }
+                        }
+                    }
+                    if (a.slopes) {
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) x[k] = fmaf(-slope, (float)abs(gpos - key0 - k), x[k]);
+                    }
+                }
+                if (key0 < all_lo || key0 + 128 > all_hi) {   // warp-uniform
+                    const int l = lo - key0, h = hi - key0;
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        if (k < l || k >= h) x[k] = -INFINITY;
+                }
+                float mx[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    mx[i] = fmaxf(x[i], x[i + 8]);
+#pragma unroll
+                    for (int q = 1; q < 8; ++q) mx[i] = max3f(mx[i], x[i + 16 * q], x[i + 16 * q + 8]);
+                }
+                const float top = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ls;
+                const bool raise = top > m_run + kLazy;
+                if (__any_sync(0xffffffffu, raise)) {
+                    // the scores of this tile being done, so is the product of the one before: O stands still
+                    const float f = raise ? ex2(m_run - top) : 1.f;
+                    if (s > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            float o[16];
+                            tmem_ld16(to + 16u * c, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tmem_st16(to + 16u * c, o);
+                        }
+                    }
+                    if (raise) {
+                        l_run *= f;
+                        m_run = top;
+                        m_neg = -top;
+                    }
+                }
+                const float2 sc = make_float2(ls, ls), nm = make_float2(m_neg, m_neg);
+                float2 acc[4] = {};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int k = 32 * c + 2 * e;
+                        const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), sc, nm);
+                        const float2 z = make_float2(ex2(y.x), ex2(y.y));
+                        pk[e] = kInt4 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
+                        acc[e & 3] = __fadd2_rn(acc[e & 3], z);
+                    }
+                    tmem_st16_async(ts + 16u * c, pk);
+                }
+                const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+                const float2 a03 = __fadd2_rn(a01, a23);
+                l_run += a03.x + a03.y;
+                if (!kInt4 && (key0 < w.it.klo || key0 + 128 > w.it.khi)) {
+                    // keys nobody sees: whatever their slots held is not used.  Both row
+                    // tiles write the same zeros, each before its own product.
+                    const int vx = 2 * g + 1;
+                    if (!warp_wait(&full[vx % kRing], (uint32_t)(vx / kRing) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const int key = key0 + m;
+                    if (key < w.it.klo || key >= w.it.khi) {
+                        const uint32_t d = sbase + kOffRing + (uint32_t)(vx % kRing) * kTile + (uint32_t)m * 128u;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            sts16(d + 16u * c, make_uint4(0u, 0u, 0u, 0u));
+                            sts16(d + kHalf + 16u * c, make_uint4(0u, 0u, 0u, 0u));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            // ---- the run's rows
+            if (!warp_wait(&o_done[t], (uint32_t)(runs++) & 1u)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.out_stride + (int64_t)head * 128;
+            const size_t at = slot + (size_t)(p * G + gi);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                float y[16], o[16];
+                tmem_ld16(to + 16u * c, y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)   // 4 bits: column 2 k + b of a chunk of 8 is dim k + 4 b
+                    o[e] = kInt4 ? y[(e & 8) + 2 * (e & 3) + ((e >> 2) & 1)] : y[e];
+                if (!valid) continue;
+                if (whole) {
+                    uint32_t k[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) k[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+                    reinterpret_cast<uint4*>(out + 16 * c)[0] = make_uint4(k[0], k[1], k[2], k[3]);
+                    reinterpret_cast<uint4*>(out + 16 * c)[1] = make_uint4(k[4], k[5], k[6], k[7]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<float4*>(a.part_o + at * 128 + 16 * c + 4 * e) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+            if (valid && !whole) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m_run, l_run);
+            tc_fence_before();
+        }
+    } else if constexpr (kInt4) {
+        reg_dec<96>();
+        // -------------------------------------------------------------- 4-bit tiles to fp16
+        // thread (key, q): keys ct / 4 + 32 i, the 16 bytes that hold dims 8 q..
+        // of each 32-dim block; the next tile's words are on their way meanwhile
+        const int ct = threadIdx.x - 384, q = ct & 3, kr = ct >> 2;
+        const int in_page = (1 << a.p.page_shift) - 1, mb = 4 * n_groups;
+        uint4 cw[4];
+        uint32_t cm[4][4];
+        int64_t rows[4];         // page rows of the tile being loaded; -1: not seen
+        int x = 0;               // ring index of the tile in hand
+        auto locate = [&](const Walk& w, int s) {
+            const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = w.key0(s) + kr + 32 * i;
+                rows[i] = -1;
+                if (key >= w.it.klo && key < w.it.khi)
+                    rows[i] = paged_row(a.p, paged_id(a.p, table[key >> a.p.page_shift]), key & in_page, w.h);
+            }
+        };
+        auto load = [&](int kv) {
+            const uint8_t* base = kv ? a.p.v : a.p.k;
+            const uint8_t* meta = kv ? a.p.vs : a.p.ks;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cw[i] = make_uint4(0u, 0u, 0u, 0u);
+                cm[i][0] = cm[i][1] = cm[i][2] = cm[i][3] = 0u;
+                if (rows[i] < 0) continue;
+                cw[i] = *reinterpret_cast<const uint4*>(base + rows[i] * 64 + 16 * q);
+                const uint8_t* mp = meta + rows[i] * mb;
+                if (n_groups == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(mp);
+                    cm[i][0] = v.x, cm[i][1] = v.y, cm[i][2] = v.z, cm[i][3] = v.w;
+                } else if (n_groups == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(mp);
+                    cm[i][0] = cm[i][1] = v.x, cm[i][2] = cm[i][3] = v.y;
+                } else {
+                    cm[i][0] = cm[i][1] = cm[i][2] = cm[i][3] = *reinterpret_cast<const uint32_t*>(mp);
+                }
+            }
+        };
+        auto convert = [&]() -> bool {
+            const int slot = x % kRing;
+            if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) return false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = kr + 32 * i;
+                const uint32_t d = sbase + kOffRing + (uint32_t)slot * kTile + (uint32_t)key * 128u;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {   // 32-dim block: units of the chunk's two 8-byte halves
+                    const uint32_t w = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w,
+                                                   (b & 1) ? 0x7632 : 0x5410);
+                    const uint32_t sc = __byte_perm(cm[i][b], 0u, 0x1010);
+                    const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[i][b], 0u, 0x3232));
+                    sts16(d + (uint32_t)(b >> 1) * kHalf + (uint32_t)(((4 * (b & 1) + q) ^ (key & 7)) << 4),
+                          make_uint4(hfma2(even8(w), sc, o8), hfma2(odd8(w), sc, o8), hfma2(even8(w >> 8), sc, o8),
+                                     hfma2(odd8(w >> 8), sc, o8)));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[slot]);
+            ++x;
+            return true;
+        };
+        Walk w(sh, u1);
+        int s = 0;
+        if (w.live()) {
+            locate(w, 0);
+            load(0);
+        }
+        while (w.live()) {
+            if (!(ok = convert())) break;      // K
+            load(1);
+            // where the next tile's rows are
+            Walk nw = w;
+            int ns = s + 1;
+            if (ns == w.n) {
+                nw.next(a);
+                ns = 0;
+            }
+            if (nw.live()) locate(nw, ns);
+            if (!(ok = convert())) break;      // V
+            if (nw.live()) load(0);
+            w = nw;
+            s = ns;
+        }
+    }
+    if (!ok && lane == 0) paged_err(a.p.err, DEV_ERR_TIMEOUT, warp);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <bool kInt4, bool kExtra>
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const PagedAttn& a, int n_groups, cudaStream_t s) {
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(paged_tc_kernel<kInt4, kExtra>, (int)kSmem, &allowed);
+    if (e != cudaSuccess) return e;
+    KVR_LAUNCH(paged_tc_kernel<kInt4, kExtra>, dim3((unsigned)a.n_cta), dim3(kInt4 ? 512 : 384), kSmem, s, k, v, a, n_groups);
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStream_t s, std::string* why) {
+    const bool extra = a.softcap > 0.f || a.loc || a.snk || a.slopes;
+    CUtensorMap k{}, v{};
+    if (format == KVR_INT4)
+        return extra ? launch<true, true>(k, v, a, 128 / group, s) : launch<true, false>(k, v, a, 128 / group, s);
+    // pages as (dim, slot, head, page); a box is one page's share of a 128-key tile, half a row wide
+    const uint64_t dims[4] = {128, 1ull << a.p.page_shift, (uint64_t)a.p.n_kv_heads, (uint64_t)a.p.n_pages};
+    const uint64_t strides[3] = {(uint64_t)a.p.slot_stride * 256, (uint64_t)a.p.head_stride * 256,
+                                 (uint64_t)a.p.page_stride * 256};
+    const uint32_t box[4] = {64, 1u << (a.p.page_shift < 7 ? a.p.page_shift : 7), 1, 1};
+    if (!make_tmap_4d_bf16(&k, a.p.k, dims, strides, box, why) || !make_tmap_4d_bf16(&v, a.p.v, dims, strides, box, why))
+        return cudaErrorInvalidValue;
+    return extra ? launch<false, true>(k, v, a, 0, s) : launch<false, false>(k, v, a, 0, s);
+}
+
+}  // namespace kvr
