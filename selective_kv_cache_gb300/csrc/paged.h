@@ -47,20 +47,22 @@ struct PagedRowIo {   // append and read
 cudaError_t launch_paged_append(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s);
 cudaError_t launch_paged_read(int format, int head_dim, int group, const PagedRowIo& a, cudaStream_t s);
 
-// One (sequence, run of `positions` packed rows) of an attention call, and its
-// K/V heads one after another: `units` runs of `unit_keys` keys starting at
-// the unit that holds key klo, for each head.
+// Up to `positions` packed rows of one sequence, for each K/V head: `units`
+// times unit_keys keys, from the unit that holds key klo.
 struct PagedItem {
     int klo, khi;     // keys any of its rows may see: [klo, khi)
     int units;        // >= 1 when it has rows, else 0
-    int before;       // units of one head of all earlier items
+    int before;       // cost of one head of all earlier items
     int seq, kv;      // its sequence and that one's length
     int row0, rows;   // its packed rows
 };
-// Where a CTA's equal share of the call's units begins.
+// The call's work is a line of runs, (item, head) by (item, head), each as long
+// as its units plus run_cost for starting it; CTA c's equal share of the line
+// is [u0(c), u0(c + 1)).  A share that begins or ends in a run's start does not
+// split the run.
 struct PagedShare {
-    int item, head, off;   // unit `off` of that item's head
-    int u0;                // in the call's units; share c ends where share c+1 begins
+    int item, head, off;   // the run it begins in and its first unit there
+    int u0, run;           // its place on the line, and that run's
     PagedItem first;       // that item, so that a CTA's first loads wait for one record only
 };
 struct PagedAttn {
@@ -72,7 +74,7 @@ struct PagedAttn {
     int n_q_heads, G, max_rows;
     int positions;                  // packed rows of an item
     int tiles, n_items;             // items of a sequence, of the call (tiles * batch)
-    int unit_keys, n_cta, tile_rows;   // tile_rows >= positions * G: rows of a partial
+    int unit_keys, run_cost, n_cta, tile_rows;   // tile_rows >= positions * G: rows of a partial
     float scale, softcap, alpha, beta;
     const uint32_t* loc;
     const uint32_t* snk;
@@ -156,13 +158,15 @@ __device__ __forceinline__ int paged_kv_len(const PagedView& p, int b) {
 }
 
 // Keys that the rows of item i can see, its units, and the checks of its
-// sequence's row range.
-__device__ __forceinline__ PagedItem paged_item(const PagedAttn& a, int i) {
+// sequence's row range.  Lanes lane, lane + step, ... of a step-wide group share
+// the rows and all get the answer (step 1: a thread for itself).
+template <int kStep>
+__device__ __forceinline__ PagedItem paged_item(const PagedAttn& a, int i, int lane) {
     PagedItem it{};
     const int b = i / a.tiles, t = i - b * a.tiles;
     int row0;
     const int n = paged_seq_rows(a.p, a.r, b, &row0);
-    if (t == 0) {
+    if (t == 0 && lane == 0) {
         if (n > a.max_rows) paged_err(a.p.err, DEV_ERR_INDEX, n);
         const int kv = a.p.kv_len[b];
         if (kv < 0 || kv > a.p.capacity) paged_err(a.p.err, DEV_ERR_INDEX, kv);
@@ -170,15 +174,20 @@ __device__ __forceinline__ PagedItem paged_item(const PagedAttn& a, int i) {
     const int r0 = t * a.positions, r1 = min(min(n, a.max_rows), r0 + a.positions);
     if (r0 >= r1) return it;
     const int kv = paged_kv_len(a.p, b);
-    int lo = 0x7fffffff, hi = 0;
-    for (int r = row0 + r0; r < row0 + r1; ++r) {
-        if (a.r.pos[r] < 0) paged_err(a.p.err, DEV_ERR_INDEX, a.r.pos[r]);
+    int lo = 0x7fffffff, hi = 0, least = 0;
+    for (int r = row0 + r0 + lane; r < row0 + r1; r += kStep) {
+        least = min(least, a.r.pos[r]);
         int l, h;
         paged_interval(a, r, kv, &l, &h);
         if (l < h) {
             lo = min(lo, l);
             hi = max(hi, h);
         }
+    }
+    if (least < 0) paged_err(a.p.err, DEV_ERR_INDEX, least);
+    if (kStep == 32) {
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
     }
     if (lo >= hi) lo = hi = 0;   // nothing visible: one unit without keys, which writes the zeros
     it.klo = lo;
@@ -190,6 +199,43 @@ __device__ __forceinline__ PagedItem paged_item(const PagedAttn& a, int i) {
     it.units = max(1, (hi + a.unit_keys - 1) / a.unit_keys - lo / a.unit_keys);
     return it;
 }
+
+// Shares in use of a line of length T: each longer than a run's start, so none is without units.
+__device__ __forceinline__ int paged_shares(const PagedAttn& a, long long T) {
+    return (int)min((long long)a.n_cta, T > 0 ? max(T / (a.run_cost + 1), 1ll) : 0ll);
+}
+// Share c of n, given the item its place falls into.
+__device__ __forceinline__ PagedShare paged_share(const PagedAttn& a, int u0, int i, const PagedItem& it) {
+    const int H = a.p.n_kv_heads, len = it.units + a.run_cost, rem = u0 - H * it.before, head = rem / len;
+    const int run = H * it.before + head * len;
+    return PagedShare{i, head, max(u0 - run - a.run_cost, 0), u0, run, it};
+}
+
+// The runs of a CTA's share in order: n units of head h of item i from unit off.
+struct PagedWalk {
+    PagedItem it;
+    int i, h, off, run, u1, n;
+    bool first;   // the share's first run: its partial goes to slot 0, another's to slot 1
+    __device__ __forceinline__ PagedWalk(const PagedAttn& a, const PagedShare& sh, int end)
+        : it(sh.first), i(sh.item), h(sh.head), off(sh.off), run(sh.run), u1(end), first(true) {
+        n = sh.item < 0 ? 0 : min(it.units, u1 - run - a.run_cost) - off;
+    }
+    __device__ __forceinline__ bool live() const { return n > 0; }
+    __device__ __forceinline__ bool whole() const { return n == it.units; }
+    __device__ __forceinline__ void next(const PagedAttn& a, const PagedItem* items) {
+        run += it.units + a.run_cost;
+        off = 0;
+        first = false;
+        if (++h == a.p.n_kv_heads) {
+            h = 0;
+            if (run < u1) {
+                do it = items[++i];
+                while (it.units == 0);
+            }
+        }
+        n = min(it.units, u1 - run - a.run_cost);
+    }
+};
 #endif
 
 }  // namespace kvr

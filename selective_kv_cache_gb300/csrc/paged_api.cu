@@ -89,7 +89,7 @@ PagedView view(const kvr_pages* p) {
 
 // Geometry of an attention call: which kernel, its item and share sizes.
 struct Geometry {
-    int G, positions, tiles, n_items, unit_keys, n_cta, tile_rows;
+    int G, positions, tiles, n_items, unit_keys, run_cost, n_cta, tile_rows;
     bool decode, tc;
 };
 constexpr int kSimtRows = 16, kSimtKeys = 32;
@@ -101,6 +101,7 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     if (max_rows < 1) return fail(KVR_EINVAL, "max_rows must be positive");
     max_rows = std::min(max_rows, n_rows);
     g->decode = p->format != KVR_F32 && (int64_t)max_rows * g->G <= 16;
+    g->run_cost = 0;
     g->tc = p->format != KVR_F32 && !g->decode;
     if (g->decode) {
         g->tile_rows = max_rows * g->G <= 8 ? 8 : 16;
@@ -109,6 +110,7 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     } else if (g->tc) {
         g->tile_rows = 256;
         g->unit_keys = 128;
+        g->run_cost = 2;
         g->n_cta = kNumSMs;
     } else {
         g->tile_rows = kSimtRows;
@@ -119,7 +121,7 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     g->tiles = (max_rows + g->positions - 1) / g->positions;
     // shares and items are counted in 32 bits
     const int64_t items = (int64_t)g->tiles * p->batch;
-    const int64_t units = ((int64_t)p->max_pages * p->page_size + g->unit_keys - 1) / g->unit_keys;
+    const int64_t units = ((int64_t)p->max_pages * p->page_size + g->unit_keys - 1) / g->unit_keys + g->run_cost;
     if (items > (int64_t(1) << 28) || items * units * p->n_kv_heads >= (int64_t(1) << 31))
         return fail(KVR_EUNSUPPORTED, "batch * rows * keys is too large for one call");
     g->n_items = (int)items;
@@ -257,6 +259,7 @@ kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int3
     a.tiles = g.tiles;
     a.n_items = g.n_items;
     a.unit_keys = g.unit_keys;
+    a.run_cost = g.run_cost;
     a.n_cta = g.n_cta;
     a.tile_rows = g.tile_rows;
     a.scale = o.scale > 0.f ? o.scale : (float)(1.0 / std::sqrt((double)p->head_dim));

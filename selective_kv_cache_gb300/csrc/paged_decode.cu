@@ -158,13 +158,14 @@ struct Decode {
 // scan, instead of a launch before this one.  Thread i takes items 2 i, 2 i + 1.
 __device__ __forceinline__ PagedShare inline_share(const PagedAttn& a, PagedItem* items, int* u1) {
     __shared__ int sums[kWarps];
-    __shared__ PagedShare out[2];   // this share, and where the next begins
+    __shared__ PagedShare out;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PagedItem it[2] = {};
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-        if (2 * (int)threadIdx.x + e < a.n_items) it[e] = paged_item(a, 2 * threadIdx.x + e);
-    int incl = it[0].units + it[1].units;
+        if (2 * (int)threadIdx.x + e < a.n_items) it[e] = paged_item<1>(a, 2 * threadIdx.x + e, 0);
+    const int cost[2] = {it[0].units ? it[0].units + a.run_cost : 0, it[1].units ? it[1].units + a.run_cost : 0};
+    int incl = cost[0] + cost[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -172,7 +173,7 @@ __device__ __forceinline__ PagedShare inline_share(const PagedAttn& a, PagedItem
     }
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int total = 0, before = incl - it[0].units - it[1].units;
+    int total = 0, before = incl - cost[0] - cost[1];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += sums[w];
@@ -180,28 +181,24 @@ __device__ __forceinline__ PagedShare inline_share(const PagedAttn& a, PagedItem
     }
     const int H = a.p.n_kv_heads;
     const long long T = (long long)total * H;
-    const int n = (int)min((long long)a.n_cta, T), c = blockIdx.x;
+    const int n = paged_shares(a, T), c = blockIdx.x;
     const int u0 = c < n ? (int)(T * c / n) : (int)T;
-    if (threadIdx.x == 0) out[0].item = -1;
+    if (threadIdx.x == 0) out = PagedShare{-1, 0, 0, u0, u0, {}};
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        it[e].before = before + (e ? it[0].units : 0);
+        it[e].before = before + (e ? cost[0] : 0);
         const int i = 2 * threadIdx.x + e;
         if (i < a.n_items) items[i] = it[e];
         const long long rem = (long long)u0 - (long long)H * it[e].before;
-        if (c < n && rem >= 0 && rem < (long long)H * it[e].units) {
-            const int head = (int)rem / it[e].units;
-            out[0] = PagedShare{i, head, (int)rem - head * it[e].units, u0, it[e]};
-        }
+        if (c < n && rem >= 0 && rem < (long long)H * cost[e]) out = paged_share(a, u0, i, it[e]);
     }
     __syncthreads();
-    PagedShare sh = out[0];
-    sh.u0 = u0;
+    const PagedShare sh = out;
     *u1 = c + 1 < n ? (int)(T * (c + 1) / n) : (int)T;
     if (threadIdx.x == 0) {   // for the merge
         a.shares[c] = sh;
-        if (c == (int)gridDim.x - 1) a.shares[c + 1] = PagedShare{-1, 0, 0, (int)T, {}};
+        if (c == (int)gridDim.x - 1) a.shares[c + 1] = PagedShare{-1, 0, 0, (int)T, (int)T, {}};
     }
     return sh;
 }
@@ -225,13 +222,10 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
     } else {
         sh = inline_share(a, items, &u1);
     }
-    if (sh.item < 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-    const int H = a.p.n_kv_heads, G = a.G, shift = a.p.page_shift, in_page = (1 << shift) - 1;
+    const int G = a.G, shift = a.p.page_shift, in_page = (1 << shift) - 1;
     const float sl2 = a.scale * kLog2e;
-    PagedItem it = sh.first;
-    int i = sh.item, h = sh.head, off = sh.off, u = sh.u0;
-    bool first = true;
+    const PagedItem* all_items = a.planned ? a.items : items;
     const int slot_b = (int)a.p.slot_stride * RB, page_b = (int)a.p.page_stride * RB;   // below 2^31 (checked)
     const int slot_m = (int)a.p.slot_stride * MB, page_m = (int)a.p.page_stride * MB;
     const uint32_t ring = smem_u32(smem) + warp * D::kRing;
@@ -250,8 +244,9 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
     const uint32_t v_get = D::kV + (NG ? (4 * (t >> 1) + (t & 1)) * 64 + 16 * ((r >> 1) ^ (2 * (t >> 1))) + 8 * (r & 1)
                                        : 512 * t + 16 * (2 * (r ^ t) + (r & 1)));
 
-    while (u < u1) {
-        const int n = min(it.units - off, u1 - u);
+    for (PagedWalk run(a, sh, u1); run.live(); run.next(a, all_items)) {
+        const PagedItem it = run.it;
+        const int n = run.n, off = run.off, h = run.h;
         const int rows = it.rows * G;
         const int* table = a.p.table + (int64_t)it.seq * a.p.max_pages;
         // 16-key blocks [kb0, kb_end) hold the item's keys; this warp's steps
@@ -673,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
         __syncthreads();   // the join's outputs lie over every warp's ring
 
         // ---- join the warps: rows 2t, 2t + 1 of each tile
-        const bool whole = n == it.units;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * a.tile_rows;
+        const bool whole = run.whole();
+        const size_t slot = ((size_t)blockIdx.x * 2 + (run.first ? 0 : 1)) * a.tile_rows;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -738,16 +733,6 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
                 }
             }
             __syncthreads();
-        }
-        first = false;
-        u += n;
-        off = 0;
-        if (++h == H) {
-            h = 0;
-            if (u < u1) {
-                do it = a.planned ? a.items[++i] : items[++i];
-                while (it.units == 0);
-            }
         }
     }
 }

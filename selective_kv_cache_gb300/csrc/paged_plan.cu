@@ -1,16 +1,15 @@
 // paged_plan.cu -- sharing one paged attention call over the GPU, and merging
 // what was split.
 //
-// The call's work is a line of units: for each item (a run of packed rows of
-// one sequence), for each K/V head, the runs of unit_keys keys its rows can
-// see.  CTA c takes units [c T / n, (c + 1) T / n): equal shares whatever the
-// sequences' lengths, which only the device knows.  An (item, head) that one
+// The call's work is a line (paged.h: PagedShare) cut into equal shares,
+// whatever the sequences' lengths, which only the device knows.  A run that one
 // CTA holds whole is written by it; the others leave unnormalised partial rows
-// (at most two per CTA: its first and its last), merged afterwards in key
+// (at most two per CTA: its first and its last run), merged afterwards in key
 // order, so the bits depend on nothing but the inputs.
 //
-// Both kernels here are latency, not bandwidth: the plan is one block reading
-// a few words per row; the merge reads each partial once, from L2.
+// All kernels here are latency, not bandwidth: a warp per item reads a few
+// words per row, one block scans the items, the merge reads each partial once,
+// from L2.
 #include <cuda_bf16.h>
 
 #include "paged.h"
@@ -21,19 +20,27 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kCoarse = 4096;
 
+__global__ void __launch_bounds__(256) items_kernel(PagedAttn a) {
+    pdl_trigger();
+    const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (i >= a.n_items) return;
+    const PagedItem it = paged_item<32>(a, i, lane);
+    if (lane == 0) a.items[i] = it;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
     __shared__ int coarse[kCoarse];
     __shared__ int warp_sum[32];
-    __shared__ int s_total;
     pdl_trigger();
+    pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int step = (a.n_items + kCoarse - 1) / kCoarse;   // items per coarse entry
     int carry = 0;
     for (int base = 0; base < a.n_items; base += kPlanThreads) {
         const int i = base + threadIdx.x;
-        PagedItem it{};
-        if (i < a.n_items) it = paged_item(a, i);
-        int incl = it.units;
+        const int units = i < a.n_items ? a.items[i].units : 0;
+        const int cost = units ? units + a.run_cost : 0;
+        int incl = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -51,24 +58,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
             warp_sum[lane] = v;
         }
         __syncthreads();
-        it.before = carry + (w ? warp_sum[w - 1] : 0) + incl - it.units;
+        const int before = carry + (w ? warp_sum[w - 1] : 0) + incl - cost;
         carry += warp_sum[31];
         if (i < a.n_items) {
-            a.items[i] = it;
-            if (i % step == 0) coarse[i / step] = it.before;
+            a.items[i].before = before;
+            if (i % step == 0) coarse[i / step] = before;
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) s_total = carry;
-    __syncthreads();
     const int H = a.p.n_kv_heads;
-    const long long T = (long long)s_total * H;
-    const int n = (int)min((long long)a.n_cta, T);
+    const long long T = (long long)carry * H;
+    const int n = paged_shares(a, T);
     for (int c = threadIdx.x; c <= a.n_cta; c += kPlanThreads) {
-        PagedShare sh{-1, 0, 0, (int)T, {}};
+        PagedShare sh{-1, 0, 0, (int)T, (int)T, {}};
         if (c < n) {
-            sh.u0 = (int)(T * c / n);
-            const int x = sh.u0 / H;   // before_i <= u0 / H exactly when H before_i <= u0
+            const int u0 = (int)(T * c / n);
+            const int x = u0 / H;   // before_i <= u0 / H exactly when H before_i <= u0
             int l = 0, r = (a.n_items + step - 1) / step - 1;
             while (l < r) {   // last coarse entry at or below x
                 const int m = (l + r + 1) >> 1;
@@ -77,11 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PagedAttn a) {
             }
             int i = l * step;
             while (i + 1 < a.n_items && a.items[i + 1].before <= x) ++i;
-            sh.first = a.items[i];
-            const int rem = sh.u0 - H * sh.first.before, units = sh.first.units;
-            sh.item = i;
-            sh.head = rem / units;
-            sh.off = rem - sh.head * units;
+            sh = paged_share(a, u0, i, a.items[i]);
         }
         a.shares[c] = sh;
     }
@@ -94,43 +95,47 @@ __device__ __forceinline__ void store4(__nv_bfloat16* o, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-constexpr int kMergeWarps = 16, kMergeRows = 16, kMergeBatch = 8;
+constexpr int kMergeRows = 16, kMergeBatch = 8;
 
-// Block (c - 1, y): rows 16 y .. of the (item, head) that share c enters in
-// its middle, if share c is the first to do so.  The 16 warps are dealt to the
-// rows (one each, or several to a row when there are few), a row's warps take
-// its partials in turn, eight loads in flight a lane, four dims a lane (lanes
-// past head_dim idle); a row's warps are joined through shared memory, in
-// order.  A long sequence has a partial per CTA, so it is the loads in flight that
-// count here: 57 partials of 4 rows 12 -> 4 us against a warp per row.
-template <typename T, int DH>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(PagedAttn a) {
-    __shared__ float sO[kMergeWarps][DH];
-    __shared__ float2 sML[kMergeWarps];
+// Block (c - 1, y): rows 16 y .. of the run that share c enters in its middle,
+// if share c is the first to do so.  Items of up to 16 rows (kWarps = 16): the
+// warps are dealt to the rows (one each, or several to a row when there are
+// few), a row's warps take its partials in turn, eight loads in flight a lane,
+// four dims a lane (lanes past head_dim idle), and are joined through shared
+// memory, in order.  A long sequence has a partial per CTA, so it is the loads
+// in flight that count: 57 partials of 4 rows 12 -> 5 us against a warp per
+// row.  Larger items (kWarps = 4) have many rows and few partials: a warp takes
+// rows in turn, and the blocks are small, since most find nothing to do.
+template <typename T, int DH, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) merge_kernel(PagedAttn a) {
+    __shared__ float sO[kWarps][DH];
+    __shared__ float2 sML[kWarps];
     pdl_wait();
     const int c = blockIdx.x + 1;
     const PagedShare sh = a.shares[c];
     const int prev = a.shares[c - 1].u0;
     if (sh.item < 0 || sh.off == 0) return;
-    const int start = sh.u0 - sh.off;
-    if (prev > start) return;
+    if (prev > sh.run + a.run_cost) return;   // an earlier share began past its first unit
     const PagedItem it = sh.first;
-    const int end = start + it.units;
+    const int end = sh.run + a.run_cost + it.units;
     const int rows = min(it.rows * a.G - (int)blockIdx.y * kMergeRows, kMergeRows);
     if (rows <= 0) return;
     // partials: shares c - 1, c, ... that begin before the end
     int parts = 1;
-    for (int k0 = c;; k0 += 32 * kMergeWarps) {
+    for (int k0 = c;; k0 += 32 * kWarps) {
         const int k = k0 + threadIdx.x;
         const int n = __syncthreads_count(k < a.n_cta && a.shares[k].item >= 0 && a.shares[k].u0 < end);
         parts += n;
-        if (n < 32 * kMergeWarps) break;
+        if (n < 32 * kWarps) break;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wpr = kMergeWarps >> (32 - __clz(rows - 1));   // warps of a row: 16 / (rows rounded up to a power of two)
-    const int m = warp / wpr, sub = warp % wpr, row = blockIdx.y * kMergeRows + m;
+    // warps of a row: 16 / (rows rounded up to a power of two)
+    const int wpr = kWarps == 16 ? 16 >> (32 - __clz(rows - 1)) : 1;
     const size_t stride = (size_t)2 * a.tile_rows;   // rows from one share's first slot to the next's
-    const size_t first = (size_t)(c - 1) * stride + (prev == start ? 0 : a.tile_rows) + row;
+    for (int m = warp / wpr; m < kMergeRows; m += kWarps) {   // one round when kWarps = 16
+    const int sub = warp % wpr, row = blockIdx.y * kMergeRows + m;
+    if (kWarps < 16 && m >= rows) break;
+    const size_t first = (size_t)(c - 1) * stride + (prev >= sh.run ? 0 : a.tile_rows) + row;
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = sub; m < rows && k0 < parts; k0 += wpr * kMergeBatch) {
@@ -198,22 +203,29 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(PagedAttn a) {
         store4(reinterpret_cast<T*>(a.out) + (int64_t)(it.row0 + row / a.G) * a.out_stride +
                    (int64_t)(sh.head * a.G + row % a.G) * DH + 4 * lane,
                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+}
+
+template <typename T, int DH>
+cudaError_t merge(const PagedAttn& a, cudaStream_t s) {
+    const dim3 grid((unsigned)a.n_cta - 1, (unsigned)((a.positions * a.G + kMergeRows - 1) / kMergeRows));
+    if (a.tile_rows <= kMergeRows) KVR_LAUNCH(merge_kernel<T, DH, 16>, grid, dim3(32 * 16), 0, s, a);
+    else if constexpr (sizeof(T) == 2) KVR_LAUNCH(merge_kernel<T, DH, 4>, grid, dim3(32 * 4), 0, s, a);
+    return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedAttn& a, cudaStream_t s) {
+    KVR_LAUNCH(items_kernel, dim3((unsigned)((a.n_items + 7) / 8)), dim3(256), 0, s, a);
     KVR_LAUNCH(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
     return cudaSuccess;
 }
 
 cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cudaStream_t s) {
     if (a.n_cta < 2) return cudaSuccess;
-    const dim3 grid((unsigned)a.n_cta - 1, (unsigned)((a.positions * a.G + kMergeRows - 1) / kMergeRows));
-    if (dtype == KVR_BF16) KVR_LAUNCH(merge_kernel<__nv_bfloat16, 128>, grid, dim3(32 * kMergeWarps), 0, s, a);
-    else if (head_dim == 64) KVR_LAUNCH(merge_kernel<float, 64>, grid, dim3(32 * kMergeWarps), 0, s, a);
-    else KVR_LAUNCH(merge_kernel<float, 128>, grid, dim3(32 * kMergeWarps), 0, s, a);
-    return cudaSuccess;
+    if (dtype == KVR_BF16) return merge<__nv_bfloat16, 128>(a, s);
+    return head_dim == 64 ? merge<float, 64>(a, s) : merge<float, 128>(a, s);
 }
 
 }  // namespace kvr

@@ -29,17 +29,12 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttn a) {
     __shared__ float sP[4][kKeys][4];
     pdl_wait();
     pdl_trigger();
-    const PagedShare sh = a.shares[blockIdx.x];
-    if (sh.item < 0) return;
-    const int u1 = a.shares[blockIdx.x + 1].u0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int H = a.p.n_kv_heads, G = a.G;
+    const int G = a.G;
     constexpr float kLog2e = 1.4426950408889634f;
-    int i = sh.item, h = sh.head, off = sh.off, u = sh.u0;
-    bool first = true;
-    while (u < u1) {
-        const PagedItem it = a.items[i];
-        const int n = min(it.units - off, u1 - u);
+    for (PagedWalk w(a, a.shares[blockIdx.x], a.shares[blockIdx.x + 1].u0); w.live(); w.next(a, a.items)) {
+        const PagedItem& it = w.it;
+        const int n = w.n, h = w.h, off = w.off;
         const int b = it.seq, row0 = it.row0, np = it.rows, kv = it.kv;
         __syncthreads();
         for (int e = threadIdx.x; e < kRows * DH; e += kThreads) {
@@ -151,14 +146,14 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttn a) {
                 y = key >= lo[j] && key < hi[j] ? y * kLog2e : -INFINITY;
                 float mx = y;
 #pragma unroll
-                for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                for (int z = 16; z > 0; z >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
                 const float m_new = fmaxf(m_run[j], mx);
                 const float base = m_new == -INFINITY ? 0.f : m_new;
                 const float p = exp2f(y - base);
                 const float f = exp2f(m_run[j] - base);
                 float sum = p;
 #pragma unroll
-                for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                for (int z = 16; z > 0; z >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
                 m_run[j] = m_new;
                 l_run[j] = l_run[j] * f + sum;
 #pragma unroll
@@ -181,8 +176,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttn a) {
                 }
             }
         }
-        const bool whole = n == it.units;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * a.tile_rows;
+        const bool whole = w.whole();
+        const size_t slot = ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.tile_rows;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int m = 4 * warp + j;
@@ -204,14 +199,6 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedAttn a) {
                     a.part_ml[2 * (slot + m) + 1] = l_run[j];
                 }
             }
-        }
-        first = false;
-        u += n;
-        off = 0;
-        if (++h == H) {
-            h = 0;
-            do ++i;
-            while (u < u1 && i < a.n_items && a.items[i].units == 0);
         }
     }
 }

@@ -83,6 +83,33 @@ __device__ __forceinline__ uint32_t with_1024(uint32_t x, uint32_t mask) {
 // code - 8 of the even and of the odd nibble of each half, exact
 __device__ __forceinline__ uint32_t even8(uint32_t x) { return hfma2(with_1024(x, 0x000f000fu), 0x3c003c00u, 0xe408e408u); }
 __device__ __forceinline__ uint32_t odd8(uint32_t x) { return hfma2(with_1024(x, 0x00f000f0u), 0x2c002c00u, 0xd480d480u); }
+// 128 consecutive columns of this thread's lane: four loads, one wait
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+#define KVR_LD32(OFF)                                                                                              \
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"    \
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"                        \
+                 : "=r"(r[OFF]), "=r"(r[OFF + 1]), "=r"(r[OFF + 2]), "=r"(r[OFF + 3]), "=r"(r[OFF + 4]),            \
+                   "=r"(r[OFF + 5]), "=r"(r[OFF + 6]), "=r"(r[OFF + 7]), "=r"(r[OFF + 8]), "=r"(r[OFF + 9]),        \
+                   "=r"(r[OFF + 10]), "=r"(r[OFF + 11]), "=r"(r[OFF + 12]), "=r"(r[OFF + 13]), "=r"(r[OFF + 14]),   \
+                   "=r"(r[OFF + 15]), "=r"(r[OFF + 16]), "=r"(r[OFF + 17]), "=r"(r[OFF + 18]), "=r"(r[OFF + 19]),   \
+                   "=r"(r[OFF + 20]), "=r"(r[OFF + 21]), "=r"(r[OFF + 22]), "=r"(r[OFF + 23]), "=r"(r[OFF + 24]),   \
+                   "=r"(r[OFF + 25]), "=r"(r[OFF + 26]), "=r"(r[OFF + 27]), "=r"(r[OFF + 28]), "=r"(r[OFF + 29]),   \
+                   "=r"(r[OFF + 30]), "=r"(r[OFF + 31])                                                             \
+                 : "r"(taddr + (OFF)) : "memory")
+    KVR_LD32(0);
+    KVR_LD32(32);
+    KVR_LD32(64);
+    KVR_LD32(96);
+#undef KVR_LD32
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // no use of a destination moves above the wait
+#pragma unroll
+    for (int i = 0; i < 128; i += 16)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                     "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])::"memory");
+}
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
@@ -103,30 +130,8 @@ __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.al
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// The runs of units (one item and head each) of a CTA's share, in order; every
-// role of the CTA walks them for itself.
-struct Walk {
-    PagedItem it;
-    int i, h, off, u, u1, n;
-    __device__ __forceinline__ Walk(const PagedShare& sh, int end) : it(sh.first), i(sh.item), h(sh.head), off(sh.off), u(sh.u0), u1(end) {
-        n = min(it.units - off, u1 - u);
-    }
-    __device__ __forceinline__ bool live() const { return u < u1; }
-    __device__ __forceinline__ int key0(int s) const { return ((it.klo >> 7) + off + s) << 7; }
-    __device__ __forceinline__ int tiles(int per_tile) const { return it.rows > per_tile ? 2 : 1; }
-    __device__ __forceinline__ void next(const PagedAttn& a) {
-        u += n;
-        off = 0;
-        if (++h == a.p.n_kv_heads) {
-            h = 0;
-            if (u < u1) {
-                do it = a.items[++i];
-                while (it.units == 0);
-            }
-        }
-        n = min(it.units, u1 - u);
-    }
-};
+__device__ __forceinline__ int first_key(const PagedWalk& w, int s) { return ((w.it.klo >> 7) + w.off + s) << 7; }
+__device__ __forceinline__ int row_tiles(const PagedWalk& w, int per_tile) { return w.it.rows > per_tile ? 2 : 1; }
 
 template <bool kInt4, bool kExtra>
 __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
@@ -139,8 +144,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     uint64_t* empty = full + kRing;                                 // [kRing] its products are done
     uint64_t* q_full = empty + kRing;                               // [2] Q_t is in place
     uint64_t* s_full = q_full + 2;                                  // [2] S_t is done
-    uint64_t* p_full = s_full + 2;                                  // [2] P_t is in tensor memory
-    uint64_t* o_done = p_full + 2;                                  // [2] a run's last product with V is done
+    uint64_t* p_full = s_full + 2;                                  // [2][2] half of P_t is in tensor memory
+    uint64_t* o_done = p_full + 4;                                  // [2] a run's last product with V is done
     uint64_t* drained = o_done + 2;                                 // every product issued is done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,7 +158,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_done[i], 1);
         }
         fence_mbar_init();
@@ -188,10 +194,10 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             const int half = lane & 1, pg = lane >> 1;
             const uint32_t dst_off = (uint32_t)half * kHalf + ((uint32_t)pg << (shift + 7));
             int x = 0;   // ring index of the next tile
-            for (Walk w(sh, u1); w.live() && ok; w.next(a)) {
+            for (PagedWalk w(a, sh, u1); w.live() && ok; w.next(a, a.items)) {
                 const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
                 for (int s = 0; s < w.n && ok; ++s) {
-                    const int k0 = w.key0(s) + (pg << shift);
+                    const int k0 = first_key(w, s) + (pg << shift);
                     // pages none of whose keys is visible are not touched
                     const bool mine = pg < pages && k0 < w.it.khi && k0 + (1 << shift) > w.it.klo;
                     const int id = mine ? paged_id(a.p, table[k0 >> a.p.page_shift]) : 0;
@@ -233,8 +239,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 }
                 mma_commit(&s_full[t]);
             };
-            for (Walk w(sh, u1); w.live() && ok; w.next(a)) {
-                const int nt = w.tiles(per_tile);
+            for (PagedWalk w(a, sh, u1); w.live() && ok; w.next(a, a.items)) {
+                const int nt = row_tiles(w, per_tile);
                 for (int t = 0; t < nt && ok; ++t) {
                     ok = mbar_wait(&q_full[t], (uint32_t)(runs[t]++) & 1u) && (t || landed(2 * g));
                     if (!ok) break;
@@ -246,14 +252,20 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     const int v = 2 * g + 1;
                     const uint32_t va = sbase + kOffRing + (uint32_t)(v % kRing) * kTile;
                     for (int t = 0; t < nt; ++t) {
-                        ok = mbar_wait(&p_full[t], (uint32_t)(ps[t]++) & 1u) && (t || landed(v));
-                        if (!ok) break;
-                        tc_fence_after();
                         const uint32_t pt = tmem + kColS + 128u * t;
+                        // the first half's product runs while the softmax is on the second
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
-                                        sdesc_sw128(va + (uint32_t)kk * 2048u, kHalf, 1024), id_o, (s > 0 || kk > 0));
+                        for (int hf = 0; hf < 2; ++hf) {
+                            ok = mbar_wait(&p_full[2 * t + hf], (uint32_t)ps[t] & 1u) && (t || hf || landed(v));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
+                                mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
+                                            sdesc_sw128(va + (uint32_t)kk * 2048u, kHalf, 1024), id_o, (s > 0 || kk > 0));
+                        }
+                        if (!ok) break;
+                        ++ps[t];
                         if (s == w.n - 1) mma_commit(&o_done[t]);
                         if (t == nt - 1) mma_commit(&empty[v % kRing]);
                         if (s + 1 < w.n) {
@@ -279,60 +291,69 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         const uint32_t ts = tmem + kColS + 128u * t + lane_base, to = tmem + kColO + 128u * t + lane_base;
         const float sl2 = a.scale * kLog2e;
         int g = 0, tile = 0, runs = 0;   // tiles of the CTA, tiles and runs of this row tile
-        bool first = true;
-        for (Walk w(sh, u1); w.live() && ok; w.next(a)) {
-            const bool whole = w.n == w.it.units;
-            const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * a.tile_rows;
-            first = false;
-            if (t >= w.tiles(per_tile)) {
-                g += w.n;
-                continue;
-            }
-            const int p = t * per_tile + m / G, gi = m % G;
-            const bool valid = m < per_tile * G && p < w.it.rows;
-            const int64_t row = w.it.row0 + p;
-            const int head = w.h * G + gi;
-            // ---- Q: this thread's row into the operand's swizzle.  The last
-            // run's scores are done with the tile (this thread has seen them).
-            float lsr = sl2;
-            {
-                uint4 q[16];
-                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                                  row * a.q_stride + (int64_t)head * 128);
+        float lsr_next = sl2;            // what turns the row's products into base-2 logits
+        auto active = [&](const PagedWalk& w) { return t < row_tiles(w, per_tile); };
+        auto position = [&](const PagedWalk& w) { return t * per_tile + m / G; };
+        auto valid_in = [&](const PagedWalk& w) { return m < per_tile * G && position(w) < w.it.rows; };
+        // this thread's row of a run's Q into the operand's swizzle; the scores
+        // of the run before are done with the tile (this thread has seen them)
+        auto load_q = [&](const PagedWalk& w) {
+            uint4 q[16];
+            const bool valid = valid_in(w);
+            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                              (int64_t)(w.it.row0 + position(w)) * a.q_stride +
+                                                              (int64_t)(w.h * G + m % G) * 128);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) q[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                if constexpr (kInt4) {
-                    // to fp16, scaled by a power of two to [128, 256) at the row's largest
-                    uint32_t top = 0u;
+            for (int c = 0; c < 16; ++c) q[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (kInt4) {
+                // to fp16, scaled by a power of two to [128, 256) at the row's largest
+                uint32_t top = 0u;
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+                for (int c = 0; c < 16; ++c) {
+                    const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7f80u, (ws[e] >> 16) & 0x7f80u));
-                    }
-                    const int ex = min(max((int)(top >> 7), 8), 253);
-                    const float f = __uint_as_float((uint32_t)(261 - ex) << 23);      // 2^(134 - ex)
-                    lsr = sl2 * __uint_as_float((uint32_t)(ex - 7) << 23);            // 2^(ex - 134)
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
-                        float x[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[2 * e] = __uint_as_float(ws[e] << 16) * f;
-                            x[2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u) * f;
-                        }
-                        q[c] = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
-                    }
+                    for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7f80u, (ws[e] >> 16) & 0x7f80u));
                 }
-                const uint32_t dst = sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)m * 128u;
+                const int ex = min(max((int)(top >> 7), 8), 253);
+                const float f = __uint_as_float((uint32_t)(261 - ex) << 23);      // 2^(134 - ex)
+                lsr_next = sl2 * __uint_as_float((uint32_t)(ex - 7) << 23);       // 2^(ex - 134)
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    sts16(dst + (uint32_t)(c >> 3) * kHalf + (uint32_t)(((c & 7) ^ (m & 7)) << 4), q[c]);
+                for (int c = 0; c < 16; ++c) {
+                    const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] = __uint_as_float(ws[e] << 16) * f;
+                        x[2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u) * f;
+                    }
+                    q[c] = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
+                }
             }
+            const uint32_t dst = sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)m * 128u;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                sts16(dst + (uint32_t)(c >> 3) * kHalf + (uint32_t)(((c & 7) ^ (m & 7)) << 4), q[c]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[t]);
+        };
+        PagedWalk w(a, sh, u1);
+        auto skip = [&](PagedWalk& x) {   // to the next run this row tile has rows in; its units are counted
+            while (x.live() && !active(x)) {
+                g += x.n;
+                x.next(a, a.items);
+            }
+        };
+        skip(w);
+        if (w.live()) load_q(w);
+        while (w.live() && ok) {
+            const bool whole = w.whole();
+            const size_t slot = ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.tile_rows;
+            const int p = position(w), gi = m % G;
+            const bool valid = valid_in(w);
+            const int64_t row = w.it.row0 + p;
+            const int head = w.h * G + gi;
+            const float lsr = lsr_next;
             // ---- what the row sees
             int lo = w.it.klo, hi = w.it.khi, gpos = 0;
             float slope = 0.f;
@@ -346,15 +367,14 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
             float m_run = -INFINITY, m_neg = 0.f, l_run = 0.f;
             for (int s = 0; s < w.n; ++s, ++g, ++tile) {
-                const int key0 = w.key0(s);
+                const int key0 = first_key(w, s);
                 if (!warp_wait(&s_full[t], (uint32_t)tile & 1u)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 float x[128];
-                tmem_ld32x2(ts, x);
-                tmem_ld32x2(ts + 64u, x + 64);
+                tmem_ld128(ts, x);
                 float ls = lsr;
                 if constexpr (kExtra) {
                     ls = 1.f;
@@ -422,24 +442,6 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         m_neg = -top;
                     }
                 }
-                const float2 sc = make_float2(ls, ls), nm = make_float2(m_neg, m_neg);
-                float2 acc[4] = {};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int k = 32 * c + 2 * e;
-                        const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), sc, nm);
-                        const float2 z = make_float2(ex2(y.x), ex2(y.y));
-                        pk[e] = kInt4 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
-                        acc[e & 3] = __fadd2_rn(acc[e & 3], z);
-                    }
-                    tmem_st16_async(ts + 16u * c, pk);
-                }
-                const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-                const float2 a03 = __fadd2_rn(a01, a23);
-                l_run += a03.x + a03.y;
                 if (!kInt4 && (key0 < w.it.klo || key0 + 128 > w.it.khi)) {
                     // keys nobody sees: whatever their slots held is not used.  Both row
                     // tiles write the same zeros, each before its own product.
@@ -459,12 +461,37 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
+                const float2 sc = make_float2(ls, ls), nm = make_float2(m_neg, m_neg);
+                float2 acc[4] = {};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int k = 32 * c + 2 * e;
+                        const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), sc, nm);
+                        const float2 z = make_float2(ex2(y.x), ex2(y.y));
+                        pk[e] = kInt4 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
+                        acc[e & 3] = __fadd2_rn(acc[e & 3], z);
+                    }
+                    tmem_st16_async(ts + 16u * c, pk);
+                    if (c & 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * t + (c >> 1)]);
+                    }
+                }
+                const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+                const float2 a03 = __fadd2_rn(a01, a23);
+                l_run += a03.x + a03.y;
             }
             if (!ok) break;
+            // ---- the next run's Q, so that its first scores are on their way meanwhile
+            PagedWalk nw = w;
+            nw.next(a, a.items);
+            skip(nw);
+            if (nw.live()) load_q(nw);
             // ---- the run's rows
             if (!warp_wait(&o_done[t], (uint32_t)(runs++) & 1u)) {
                 ok = false;
@@ -497,6 +524,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             }
             if (valid && !whole) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m_run, l_run);
             tc_fence_before();
+            w = nw;
         }
     } else if constexpr (kInt4) {
         reg_dec<96>();
@@ -509,11 +537,11 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         uint32_t cm[4][4];
         int64_t rows[4];         // page rows of the tile being loaded; -1: not seen
         int x = 0;               // ring index of the tile in hand
-        auto locate = [&](const Walk& w, int s) {
+        auto locate = [&](const PagedWalk& w, int s) {
             const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int key = w.key0(s) + kr + 32 * i;
+                const int key = first_key(w, s) + kr + 32 * i;
                 rows[i] = -1;
                 if (key >= w.it.klo && key < w.it.khi)
                     rows[i] = paged_row(a.p, paged_id(a.p, table[key >> a.p.page_shift]), key & in_page, w.h);
@@ -564,7 +592,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             ++x;
             return true;
         };
-        Walk w(sh, u1);
+        PagedWalk w(a, sh, u1);
         int s = 0;
         if (w.live()) {
             locate(w, 0);
@@ -574,10 +602,10 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             if (!(ok = convert())) break;      // K
             load(1);
             // where the next tile's rows are
-            Walk nw = w;
+            PagedWalk nw = w;
             int ns = s + 1;
             if (ns == w.n) {
-                nw.next(a);
+                nw.next(a, a.items);
                 ns = 0;
             }
             if (nw.live()) locate(nw, ns);
