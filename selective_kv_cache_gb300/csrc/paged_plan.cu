@@ -97,17 +97,27 @@ __device__ __forceinline__ void store4(__nv_bfloat16* o, float4 v) {
 
 constexpr int kMergeRows = 16, kMergeBatch = 8;
 
-// Block (c - 1, y): rows 16 y .. of the run that share c enters in its middle,
-// if share c is the first to do so.  Items of up to 16 rows (kWarps = 16): the
-// warps are dealt to the rows (one each, or several to a row when there are
+// Partials of the run that ends at `end` and that share c - 1 begins: its own
+// and those of shares c, c + 1, ... that begin before the end.
+__device__ __forceinline__ int count_parts(const PagedAttn& a, int c, int end) {
+    int parts = 1;
+    for (int k0 = c;; k0 += blockDim.x) {
+        const int k = k0 + threadIdx.x;
+        const int n = __syncthreads_count(k < a.n_cta && a.shares[k].item >= 0 && a.shares[k].u0 < end);
+        parts += n;
+        if (n < (int)blockDim.x) return parts;
+    }
+}
+
+// Block c - 1: the rows of the run that share c enters in its middle,
+// if share c is the first to do so.  Items of up to 16 rows: the warps are dealt to the rows (one each, or several to a row when there are
 // few), a row's warps take its partials in turn, eight loads in flight a lane,
 // four dims a lane (lanes past head_dim idle), and are joined through shared
 // memory, in order.  A long sequence has a partial per CTA, so it is the loads
-// in flight that count: 57 partials of 4 rows 12 -> 5 us against a warp per
-// row.  Larger items (kWarps = 4) have many rows and few partials: a warp takes
-// rows in turn, and the blocks are small, since most find nothing to do.
-template <typename T, int DH, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) merge_kernel(PagedAttn a) {
+// in flight that count: 57 partials of 4 rows 12 -> 5 us against a warp per row.
+template <typename T, int DH>
+__global__ void __launch_bounds__(32 * 16) merge_kernel(PagedAttn a) {
+    constexpr int kWarps = 16;
     __shared__ float sO[kWarps][DH];
     __shared__ float2 sML[kWarps];
     pdl_wait();
@@ -118,23 +128,13 @@ __global__ void __launch_bounds__(32 * kWarps) merge_kernel(PagedAttn a) {
     if (prev > sh.run + a.run_cost) return;   // an earlier share began past its first unit
     const PagedItem it = sh.first;
     const int end = sh.run + a.run_cost + it.units;
-    const int rows = min(it.rows * a.G - (int)blockIdx.y * kMergeRows, kMergeRows);
-    if (rows <= 0) return;
-    // partials: shares c - 1, c, ... that begin before the end
-    int parts = 1;
-    for (int k0 = c;; k0 += 32 * kWarps) {
-        const int k = k0 + threadIdx.x;
-        const int n = __syncthreads_count(k < a.n_cta && a.shares[k].item >= 0 && a.shares[k].u0 < end);
-        parts += n;
-        if (n < 32 * kWarps) break;
-    }
+    const int rows = it.rows * a.G;   // at most 16
+    const int parts = count_parts(a, c, end);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // warps of a row: 16 / (rows rounded up to a power of two)
-    const int wpr = kWarps == 16 ? 16 >> (32 - __clz(rows - 1)) : 1;
+    const int wpr = kWarps >> (32 - __clz(rows - 1));
     const size_t stride = (size_t)2 * a.tile_rows;   // rows from one share's first slot to the next's
-    for (int m = warp / wpr; m < kMergeRows; m += kWarps) {   // one round when kWarps = 16
-    const int sub = warp % wpr, row = blockIdx.y * kMergeRows + m;
-    if (kWarps < 16 && m >= rows) break;
+    const int m = warp / wpr, sub = warp % wpr, row = m;
     const size_t first = (size_t)(c - 1) * stride + (prev >= sh.run ? 0 : a.tile_rows) + row;
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -203,15 +203,60 @@ __global__ void __launch_bounds__(32 * kWarps) merge_kernel(PagedAttn a) {
         store4(reinterpret_cast<T*>(a.out) + (int64_t)(it.row0 + row / a.G) * a.out_stride +
                    (int64_t)(sh.head * a.G + row % a.G) * DH + 4 * lane,
                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    }
 }
 
-template <typename T, int DH>
-cudaError_t merge(const PagedAttn& a, cudaStream_t s) {
-    const dim3 grid((unsigned)a.n_cta - 1, (unsigned)((a.positions * a.G + kMergeRows - 1) / kMergeRows));
-    if (a.tile_rows <= kMergeRows) KVR_LAUNCH(merge_kernel<T, DH, 16>, grid, dim3(32 * 16), 0, s, a);
-    else if constexpr (sizeof(T) == 2) KVR_LAUNCH(merge_kernel<T, DH, 4>, grid, dim3(32 * 4), 0, s, a);
-    return cudaSuccess;
+// The same for items of two 128-row tiles, whose partials lie chunk by chunk
+// of four dims, [32][tile_rows] (the attention's lanes are rows): block (c - 1,
+// y) takes rows 32 y .., a lane a row and a warp eight of the chunks, so that
+// loads are whole lines, and turns them through shared memory into rows.  Few
+// partials each; most blocks find nothing to do, so they are small.
+__global__ void __launch_bounds__(128) merge_tiles_kernel(PagedAttn a) {
+    __shared__ float sO[32][132];
+    pdl_wait();
+    const int c = blockIdx.x + 1;
+    const PagedShare sh = a.shares[c];
+    const int prev = a.shares[c - 1].u0;
+    if (sh.item < 0 || sh.off == 0 || prev > sh.run + a.run_cost) return;
+    const PagedItem it = sh.first;
+    const int per_tile = 128 / a.G, t = blockIdx.y >> 2;            // row tile
+    const int rows = min(it.rows - t * per_tile, per_tile) * a.G;   // its rows
+    const int m0 = 32 * (blockIdx.y & 3);
+    if (m0 >= rows) return;
+    const int parts = count_parts(a, c, sh.run + a.run_cost + it.units);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, m = t * 128 + m0 + lane;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool live = m0 + lane < rows;
+    for (int k = 0; k < parts && live; ++k) {
+        const size_t slot = ((size_t)2 * (c - 1 + k) + (k == 0 && prev < sh.run ? 1 : 0)) * a.tile_rows;
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot + m));
+        float4 o[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            o[x] = *reinterpret_cast<const float4*>(a.part_o + slot * 128 + 4 * ((size_t)(8 * warp + x) * a.tile_rows + m));
+        if (ml.x == -INFINITY) continue;   // saw no key of the row
+        const float top = fmaxf(M, ml.x), f = M == -INFINITY ? 0.f : exp2f(M - top), g = exp2f(ml.x - top);
+        M = top;
+        L = L * f + g * ml.y;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            acc[x] = make_float4(fmaf(g, o[x].x, acc[x].x * f), fmaf(g, o[x].y, acc[x].y * f),
+                                 fmaf(g, o[x].z, acc[x].z * f), fmaf(g, o[x].w, acc[x].w * f));
+    }
+    const float inv = L > 0.f ? 1.0f / L : 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        *reinterpret_cast<float4*>(&sO[lane][4 * (8 * warp + x)]) =
+            make_float4(acc[x].x * inv, acc[x].y * inv, acc[x].z * inv, acc[x].w * inv);
+    __syncthreads();
+    for (int i = warp; i < 32 && m0 + i < rows; i += 4) {
+        const int r = m0 + i;
+        store4(reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(it.row0 + t * per_tile + r / a.G) * a.out_stride +
+                   (int64_t)(sh.head * a.G + r % a.G) * 128 + 4 * lane,
+               *reinterpret_cast<const float4*>(&sO[i][4 * lane]));
+    }
 }
 
 }  // namespace
@@ -224,8 +269,12 @@ cudaError_t launch_paged_plan(const PagedAttn& a, cudaStream_t s) {
 
 cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cudaStream_t s) {
     if (a.n_cta < 2) return cudaSuccess;
-    if (dtype == KVR_BF16) return merge<__nv_bfloat16, 128>(a, s);
-    return head_dim == 64 ? merge<float, 64>(a, s) : merge<float, 128>(a, s);
+    const dim3 grid((unsigned)a.n_cta - 1), block(32 * 16);
+    if (a.tile_rows > kMergeRows) KVR_LAUNCH(merge_tiles_kernel, dim3(grid.x, 8), dim3(128), 0, s, a);
+    else if (dtype == KVR_BF16) KVR_LAUNCH(merge_kernel<__nv_bfloat16, 128>, grid, block, 0, s, a);
+    else if (head_dim == 64) KVR_LAUNCH(merge_kernel<float, 64>, grid, block, 0, s, a);
+    else KVR_LAUNCH(merge_kernel<float, 128>, grid, block, 0, s, a);
+    return cudaSuccess;
 }
 
 }  // namespace kvr

@@ -16,18 +16,24 @@
 //   warp 1      tcgen05.mma: S_t = Q_t K^T, O_t += P_t V.  One thread issues all
 //               products; they complete in order, so "S_t of tile j is done" also
 //               says that tile j - 1's product with V is.
+//   warp 2      bf16: Q of the next run by TMA, as soon as the last scores
+//               are done with its tile (4 bits: the softmax warps, scaled to fp16).
 //   warps 4-11  softmax, four warps a row tile, one thread a row: no exchange
 //               between threads.  Base 2; the running maximum is raised, and O
 //               rescaled in tensor memory, only when it grows by more than
-//               2^8.  P goes to tensor memory in 16 bits (bf16; fp16 for 4-bit
+//               2^8, so the weights are taken against the old maximum while the
+//               tile's own is still being found, and taken again in the rare
+//               tile that raises it.  P goes to tensor memory in 16 bits (bf16; fp16 for 4-bit
 //               pages) as the A operand: 2^-8 (2^-11) of a weight at most.
-//   warps 12-15 4 bits only, in the copies' place: codes to their values in
-//               fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
+//   warps 12-15 4 bits only, in the copies' place: packed rows come in
+//               asynchronously three tiles ahead; codes to their values in fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
 //               ring in the operand's swizzle.  A word's nibbles come out in
 //               pairs (e, e + 4), so the 8 dims of a chunk lie in the order 0 4 1
 //               5 2 6 3 7; Q is stored in that order and O read back from it.
 // Bound by the exponentials and the tensor pipe alike: 2 x 128 x 128 of the
 // first and four 128^3 products a unit.
+// The runs' bookkeeping lives in shared memory, a copy per warp: a spilled register
+// costs an L2 round trip here, where shared memory takes all but a few KB of L1.
 // Every wait is bounded; on a timeout the CTA records it, drains its copies and
 // products, frees tensor memory and returns.
 #include <cuda_bf16.h>
@@ -43,11 +49,18 @@ namespace {
 
 constexpr uint32_t kHalf = 16384;               // 128 rows x 128 B
 constexpr uint32_t kTile = 2 * kHalf;           // 128 x 128 16-bit values
-constexpr int kRing = 5;
 constexpr uint32_t kOffQ = 0;                   // two row tiles
 constexpr uint32_t kOffRing = 2 * kTile;
-constexpr uint32_t kOffBar = kOffRing + kRing * kTile;
-constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+// bf16: five tiles of ring.  4 bits: four, and in the fifth's place three
+// packed tiles (128 rows of codes, then their scale pairs) on their way in.
+constexpr int kStaged = 3;
+constexpr uint32_t kStageCodes = 128 * 64, kStage = kStageCodes + 128 * 16;
+constexpr uint32_t kOffStage = kOffRing + 4 * kTile;
+constexpr uint32_t kOffBar = kOffRing + 5 * kTile;
+constexpr uint32_t kOffWalk = kOffBar + 256;    // a PagedWalk per warp
+constexpr uint32_t kWalkBytes = 80;
+constexpr uint32_t kSmem = kOffWalk + 16 * kWalkBytes + 1024;
+static_assert(sizeof(PagedWalk) <= kWalkBytes && kStaged * kStage <= kTile, "shared memory layout");
 constexpr uint32_t kColS = 0, kColO = 256;      // TMEM columns of tile t: S (P over its first 64) at 128 t, O at 256 + 128 t
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
@@ -110,6 +123,26 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
                      "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
                      "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])::"memory");
 }
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src) {
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
@@ -135,28 +168,37 @@ __device__ __forceinline__ int row_tiles(const PagedWalk& w, int per_tile) { ret
 
 template <bool kInt4, bool kExtra>
 __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
-    paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PagedAttn a,
-                    int n_groups) {
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmQ, PagedAttn a, int n_groups) {
+    constexpr int kRing = kInt4 ? 4 : 5;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);   // [kRing] a K or V tile has landed
     uint64_t* empty = full + kRing;                                 // [kRing] its products are done
     uint64_t* q_full = empty + kRing;                               // [2] Q_t is in place
-    uint64_t* s_full = q_full + 2;                                  // [2] S_t is done
+    uint64_t* q_empty = q_full + 2;                                 // [2] a run's last scores are done with Q_t
+    uint64_t* s_full = q_empty + 2;                                 // [2] S_t is done
     uint64_t* p_full = s_full + 2;                                  // [2][2] half of P_t is in tensor memory
     uint64_t* o_done = p_full + 4;                                  // [2] a run's last product with V is done
     uint64_t* drained = o_done + 2;                                 // every product issued is done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.G, per_tile = 128 / G;
+    PagedWalk& w = *reinterpret_cast<PagedWalk*>(smem + kOffWalk + warp * kWalkBytes);
+    auto advance = [&]() {
+        __syncwarp();
+        if (lane == 0) w.next(a, a.items);
+        __syncwarp();
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) mbar_init(&full[i], kInt4 ? 4 : 1);
         for (int i = 0; i < kRing; ++i) mbar_init(&empty[i], 1);
         mbar_init(drained, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 4);
+            mbar_init(&q_full[i], kInt4 ? 4 : 1);
+            mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[2 * i], 4);
             mbar_init(&p_full[2 * i + 1], 4);
@@ -167,14 +209,22 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     if (warp == 0 && lane == 0 && !kInt4) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
+        prefetch_tmap(&tmQ);
     }
+    if (warp == 2 && !kInt4)   // rows of a tile that no position fills (128 % G): zeros for good
+        for (int i = lane; i < 2 * (128 - per_tile * G) * 16; i += 32) {
+            const int t = i / ((128 - per_tile * G) * 16), j = i % ((128 - per_tile * G) * 16);
+            sts16(sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)(j & 1) * kHalf +
+                      (uint32_t)(per_tile * G + (j >> 4)) * 128u + (uint32_t)((j >> 1) & 7) * 16u,
+                  make_uint4(0u, 0u, 0u, 0u));
+            fence_proxy_async_smem();
+        }
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     pdl_wait();
-    const PagedShare sh = a.shares[blockIdx.x];
-    const int u1 = sh.item < 0 ? sh.u0 : a.shares[blockIdx.x + 1].u0;
+    if (lane == 0) w = PagedWalk(a, a.shares[blockIdx.x], a.shares[blockIdx.x + 1].u0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -183,9 +233,9 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     bool ok = true;
 
     // registers to the softmax, which holds a row of scores a thread: 72 + 2 x
-    // 216 of 3 x 168 a thread, 64 + 2 x 176 + 96 of 4 x 128
+    // 216 of 3 x 168 a thread, 56 + 2 x 184 + 88 of 4 x 128
     if (warp < 4) {
-        reg_dec<kInt4 ? 64 : 72>();
+        reg_dec<kInt4 ? 56 : 72>();
     if (warp == 0) {
         if constexpr (!kInt4) {
             // ---------------------------------------------------------- K and V copies
@@ -194,12 +244,13 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             const int half = lane & 1, pg = lane >> 1;
             const uint32_t dst_off = (uint32_t)half * kHalf + ((uint32_t)pg << (shift + 7));
             int x = 0;   // ring index of the next tile
-            for (PagedWalk w(a, sh, u1); w.live() && ok; w.next(a, a.items)) {
+            for (; w.live() && ok; advance()) {
                 const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
-                for (int s = 0; s < w.n && ok; ++s) {
-                    const int k0 = first_key(w, s) + (pg << shift);
+                const int n = w.n, klo = w.it.klo, khi = w.it.khi, head = w.h, key_base = first_key(w, 0) + (pg << shift);
+                for (int s = 0; s < n && ok; ++s) {
+                    const int k0 = key_base + 128 * s;
                     // pages none of whose keys is visible are not touched
-                    const bool mine = pg < pages && k0 < w.it.khi && k0 + (1 << shift) > w.it.klo;
+                    const bool mine = pg < pages && k0 < khi && k0 + (1 << shift) > klo;
                     const int id = mine ? paged_id(a.p, table[k0 >> a.p.page_shift]) : 0;
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) << (shift + 7);
 #pragma unroll
@@ -215,7 +266,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         __syncwarp();
                         if (mine)
                             tma_load_4d(smem + kOffRing + slot * kTile + dst_off, kv ? &tmV : &tmK, &full[slot], 64 * half,
-                                        k0 & ((1 << a.p.page_shift) - 1), w.h, id);
+                                        k0 & ((1 << a.p.page_shift) - 1), head, id);
                     }
                 }
             }
@@ -239,16 +290,17 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 }
                 mma_commit(&s_full[t]);
             };
-            for (PagedWalk w(a, sh, u1); w.live() && ok; w.next(a, a.items)) {
-                const int nt = row_tiles(w, per_tile);
+            for (; w.live() && ok; w.next(a, a.items)) {
+                const int nt = row_tiles(w, per_tile), n = w.n;
                 for (int t = 0; t < nt && ok; ++t) {
                     ok = mbar_wait(&q_full[t], (uint32_t)(runs[t]++) & 1u) && (t || landed(2 * g));
                     if (!ok) break;
                     tc_fence_after();
                     scores(t, 2 * g);
+                    if (n == 1) mma_commit(&q_empty[t]);
                     if (t == nt - 1) mma_commit(&empty[(2 * g) % kRing]);
                 }
-                for (int s = 0; s < w.n && ok; ++s, ++g) {
+                for (int s = 0; s < n && ok; ++s, ++g) {
                     const int v = 2 * g + 1;
                     const uint32_t va = sbase + kOffRing + (uint32_t)(v % kRing) * kTile;
                     for (int t = 0; t < nt; ++t) {
@@ -266,14 +318,15 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         }
                         if (!ok) break;
                         ++ps[t];
-                        if (s == w.n - 1) mma_commit(&o_done[t]);
+                        if (s == n - 1) mma_commit(&o_done[t]);
                         if (t == nt - 1) mma_commit(&empty[v % kRing]);
-                        if (s + 1 < w.n) {
+                        if (s + 1 < n) {
                             if (t == 0 && !landed(v + 1)) {
                                 ok = false;
                                 break;
                             }
                             scores(t, v + 1);
+                            if (s + 2 == n) mma_commit(&q_empty[t]);
                             if (t == nt - 1) mma_commit(&empty[(v + 1) % kRing]);
                         }
                     }
@@ -282,31 +335,54 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             mma_commit(drained);
             if (!mbar_wait(drained, 0)) ok = false;
         }
+    } else if (!kInt4 && warp == 2) {
+        // ------------------------------------------------------------- Q by TMA
+        if (lane == 0) {
+            int runs[2] = {0, 0};
+            for (; w.live() && ok; w.next(a, a.items))
+                for (int t = 0; t < row_tiles(w, per_tile) && ok; ++t) {
+                    const int r = runs[t]++;
+                    if (r > 0 && !mbar_wait(&q_empty[t], (uint32_t)(r - 1) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = smem + kOffQ + (uint32_t)t * kTile;
+                    mbar_arrive_expect_tx(&q_full[t], 2u * 128u * (uint32_t)(per_tile * G));
+                    tma_load_3d(dst, &tmQ, &q_full[t], 0, w.h * G, w.it.row0 + t * per_tile);
+                    tma_load_3d(dst + kHalf, &tmQ, &q_full[t], 64, w.h * G, w.it.row0 + t * per_tile);
+                }
+            for (int t = 0; t < 2; ++t)   // the last copies land before the CTA exits
+                if (runs[t] > 0 && !mbar_wait(&q_full[t], (uint32_t)(runs[t] - 1) & 1u)) ok = false;
+        }
     }
     } else if (warp < 12) {
-        reg_inc<kInt4 ? 176 : 216>();
+        reg_inc<kInt4 ? 184 : 216>();
         // -------------------------------------------------------------- softmax
         const int t = warp >= 8 ? 1 : 0, m = 32 * (warp & 3) + lane;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + kColS + 128u * t + lane_base, to = tmem + kColO + 128u * t + lane_base;
         const float sl2 = a.scale * kLog2e;
         int g = 0, tile = 0, runs = 0;   // tiles of the CTA, tiles and runs of this row tile
-        float lsr_next = sl2;            // what turns the row's products into base-2 logits
-        auto active = [&](const PagedWalk& w) { return t < row_tiles(w, per_tile); };
-        auto position = [&](const PagedWalk& w) { return t * per_tile + m / G; };
-        auto valid_in = [&](const PagedWalk& w) { return m < per_tile * G && position(w) < w.it.rows; };
-        // this thread's row of a run's Q into the operand's swizzle; the scores
-        // of the run before are done with the tile (this thread has seen them)
-        auto load_q = [&](const PagedWalk& w) {
-            uint4 q[16];
-            const bool valid = valid_in(w);
-            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                              (int64_t)(w.it.row0 + position(w)) * a.q_stride +
-                                                              (int64_t)(w.h * G + m % G) * 128);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) q[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        auto skip = [&]() {   // to the next run this row tile has rows in; the units passed are counted
+            while (w.live() && t >= row_tiles(w, per_tile)) {
+                g += w.n;
+                advance();
+            }
+        };
+        float lsr_next = sl2;   // what turns the row's products into base-2 logits
+        // 4 bits: this thread's row of Q to fp16, scaled by a power of two to [128,
+        // 256) at its largest, into the operand's swizzle; the scores of the run
+        // before are done with the tile (this thread has seen them)
+        auto load_q = [&]() {
             if constexpr (kInt4) {
-                // to fp16, scaled by a power of two to [128, 256) at the row's largest
+                uint4 q[16];
+                const int p = t * per_tile + m / G;
+                const bool valid = m < per_tile * G && p < w.it.rows;
+                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                                  (int64_t)(w.it.row0 + p) * a.q_stride +
+                                                                  (int64_t)(w.h * G + m % G) * 128);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) q[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
                 uint32_t top = 0u;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
@@ -317,6 +393,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 const int ex = min(max((int)(top >> 7), 8), 253);
                 const float f = __uint_as_float((uint32_t)(261 - ex) << 23);      // 2^(134 - ex)
                 lsr_next = sl2 * __uint_as_float((uint32_t)(ex - 7) << 23);       // 2^(ex - 134)
+                const uint32_t dst = sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)m * 128u;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
@@ -326,34 +403,24 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         x[2 * e] = __uint_as_float(ws[e] << 16) * f;
                         x[2 * e + 1] = __uint_as_float(ws[e] & 0xffff0000u) * f;
                     }
-                    q[c] = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
+                    sts16(dst + (uint32_t)(c >> 3) * kHalf + (uint32_t)(((c & 7) ^ (m & 7)) << 4),
+                          make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]),
+                                     pack_f16(x[3], x[7])));
                 }
-            }
-            const uint32_t dst = sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)m * 128u;
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-                sts16(dst + (uint32_t)(c >> 3) * kHalf + (uint32_t)(((c & 7) ^ (m & 7)) << 4), q[c]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[t]);
-        };
-        PagedWalk w(a, sh, u1);
-        auto skip = [&](PagedWalk& x) {   // to the next run this row tile has rows in; its units are counted
-            while (x.live() && !active(x)) {
-                g += x.n;
-                x.next(a, a.items);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[t]);
             }
         };
-        skip(w);
-        if (w.live()) load_q(w);
+        skip();
+        if (w.live()) load_q();
         while (w.live() && ok) {
             const bool whole = w.whole();
             const size_t slot = ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.tile_rows;
-            const int p = position(w), gi = m % G;
-            const bool valid = valid_in(w);
+            const int p = t * per_tile + m / G, gi = m % G;
+            const bool valid = m < per_tile * G && p < w.it.rows;
             const int64_t row = w.it.row0 + p;
             const int head = w.h * G + gi;
-            const float lsr = lsr_next;
             // ---- what the row sees
             int lo = w.it.klo, hi = w.it.khi, gpos = 0;
             float slope = 0.f;
@@ -365,9 +432,11 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 }
             }
             const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+            const int n = w.n, klo = w.it.klo, khi = w.it.khi, key_base = first_key(w, 0), seq = w.it.seq;
+            const float lsr = lsr_next;
             float m_run = -INFINITY, m_neg = 0.f, l_run = 0.f;
-            for (int s = 0; s < w.n; ++s, ++g, ++tile) {
-                const int key0 = first_key(w, s);
+            for (int s = 0; s < n; ++s, ++g, ++tile) {
+                const int key0 = key_base + 128 * s;
                 if (!warp_wait(&s_full[t], (uint32_t)tile & 1u)) {
                     ok = false;
                     break;
@@ -389,7 +458,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         for (int k = 0; k < 128; ++k) x[k] *= lsr;
                     }
                     if (a.loc || a.snk) {
-                        const int64_t word = (int64_t)w.it.seq * a.words + (key0 >> 5);
+                        const int64_t word = (int64_t)seq * a.words + (key0 >> 5);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const bool in = (key0 >> 5) + q < a.words;
@@ -414,35 +483,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     for (int k = 0; k < 128; ++k)
                         if (k < l || k >= h) x[k] = -INFINITY;
                 }
-                float mx[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    mx[i] = fmaxf(x[i], x[i + 8]);
-#pragma unroll
-                    for (int q = 1; q < 8; ++q) mx[i] = max3f(mx[i], x[i + 16 * q], x[i + 16 * q + 8]);
-                }
-                const float top = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ls;
-                const bool raise = top > m_run + kLazy;
-                if (__any_sync(0xffffffffu, raise)) {
-                    // the scores of this tile being done, so is the product of the one before: O stands still
-                    const float f = raise ? ex2(m_run - top) : 1.f;
-                    if (s > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            float o[16];
-                            tmem_ld16(to + 16u * c, o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
-                            tmem_st16(to + 16u * c, o);
-                        }
-                    }
-                    if (raise) {
-                        l_run *= f;
-                        m_run = top;
-                        m_neg = -top;
-                    }
-                }
-                if (!kInt4 && (key0 < w.it.klo || key0 + 128 > w.it.khi)) {
+                if (!kInt4 && (key0 < klo || key0 + 128 > khi)) {
                     // keys nobody sees: whatever their slots held is not used.  Both row
                     // tiles write the same zeros, each before its own product.
                     const int vx = 2 * g + 1;
@@ -451,7 +492,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         break;
                     }
                     const int key = key0 + m;
-                    if (key < w.it.klo || key >= w.it.khi) {
+                    if (key < klo || key >= khi) {
                         const uint32_t d = sbase + kOffRing + (uint32_t)(vx % kRing) * kTile + (uint32_t)m * 128u;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
@@ -461,37 +502,84 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                const float2 sc = make_float2(ls, ls), nm = make_float2(m_neg, m_neg);
-                float2 acc[4] = {};
+                auto maximum = [&]() {
+                    float mx[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                    for (int i = 0; i < 8; ++i) {
+                        mx[i] = fmaxf(x[i], x[i + 8]);
+#pragma unroll
+                        for (int q = 1; q < 8; ++q) mx[i] = max3f(mx[i], x[i + 16 * q], x[i + 16 * q + 8]);
+                    }
+                    return max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ls;
+                };
+                // weights of 32 keys against the running maximum, in 16 bits, and their sum
+                auto weights = [&](int c, uint32_t* pk, float2& sum) {
+                    const float2 sc = make_float2(ls, ls), nm = make_float2(m_neg, m_neg);
+                    float2 acc[2] = {};
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int k = 32 * c + 2 * e;
                         const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), sc, nm);
                         const float2 z = make_float2(ex2(y.x), ex2(y.y));
                         pk[e] = kInt4 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
-                        acc[e & 3] = __fadd2_rn(acc[e & 3], z);
+                        acc[e & 1] = __fadd2_rn(acc[e & 1], z);
                     }
-                    tmem_st16_async(ts + 16u * c, pk);
-                    if (c & 1) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[2 * t + (c >> 1)]);
+                    sum = __fadd2_rn(acc[0], acc[1]);
+                };
+                float top;
+                if (s == 0) {
+                    top = maximum();
+                    if (top > -INFINITY) m_run = top, m_neg = -top;
+                }
+                uint32_t pk[2][16];
+                float2 sum[4];
+                weights(0, pk[0], sum[0]);
+                weights(1, pk[1], sum[1]);
+                if (s > 0) {
+                    top = maximum();
+                    const bool raise = top > m_run + kLazy;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        // the scores of this tile being done, so is the product of the one before: O stands still
+                        const float f = raise ? ex2(m_run - top) : 1.f;
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            float o[16];
+                            tmem_ld16(to + 16u * c, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tmem_st16(to + 16u * c, o);
+                        }
+                        if (raise) {
+                            l_run *= f;
+                            m_run = top;
+                            m_neg = -top;
+                        }
+                        weights(0, pk[0], sum[0]);
+                        weights(1, pk[1], sum[1]);
                     }
                 }
-                const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-                const float2 a03 = __fadd2_rn(a01, a23);
-                l_run += a03.x + a03.y;
+                tmem_st16_async(ts, pk[0]);
+                tmem_st16_async(ts + 16u, pk[1]);
+                weights(2, pk[0], sum[2]);   // while the stores land
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * t]);
+                tmem_st16_async(ts + 32u, pk[0]);
+                weights(3, pk[1], sum[3]);
+                tmem_st16_async(ts + 48u, pk[1]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * t + 1]);
+                const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                l_run += all.x + all.y;
             }
             if (!ok) break;
             // ---- the next run's Q, so that its first scores are on their way meanwhile
-            PagedWalk nw = w;
-            nw.next(a, a.items);
-            skip(nw);
-            if (nw.live()) load_q(nw);
+            advance();
+            skip();
+            if (w.live()) load_q();
             // ---- the run's rows
             if (!warp_wait(&o_done[t], (uint32_t)(runs++) & 1u)) {
                 ok = false;
@@ -500,7 +588,13 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
             __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.out_stride + (int64_t)head * 128;
-            const size_t at = slot + (size_t)(p * G + gi);
+            __nv_bfloat16* out_pair = reinterpret_cast<__nv_bfloat16*>(
+                __shfl_xor_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), 1));
+            const bool valid_pair = __shfl_xor_sync(0xffffffffu, (int)valid, 1) != 0;
+            // partials lie chunk by chunk of four dims, [32][tile_rows], so that the
+            // lanes' rows are neighbours; whole rows leave as 32-byte sectors, two lanes
+            // exchanging 16 bytes each
+            float* po = a.part_o + slot * 128 + 4 * (size_t)(t * 128 + m);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 float y[16], o[16];
@@ -508,112 +602,130 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)   // 4 bits: column 2 k + b of a chunk of 8 is dim k + 4 b
                     o[e] = kInt4 ? y[(e & 8) + 2 * (e & 3) + ((e >> 2) & 1)] : y[e];
-                if (!valid) continue;
                 if (whole) {
                     uint32_t k[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) k[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-                    reinterpret_cast<uint4*>(out + 16 * c)[0] = make_uint4(k[0], k[1], k[2], k[3]);
-                    reinterpret_cast<uint4*>(out + 16 * c)[1] = make_uint4(k[4], k[5], k[6], k[7]);
-                } else {
+                    // even lane: first 16 bytes of its own row and of its neighbour's; odd lane: the second
+                    const bool odd = lane & 1;
+                    uint4 own = odd ? make_uint4(k[4], k[5], k[6], k[7]) : make_uint4(k[0], k[1], k[2], k[3]);
+                    uint4 other = odd ? make_uint4(k[0], k[1], k[2], k[3]) : make_uint4(k[4], k[5], k[6], k[7]);
+                    other.x = __shfl_xor_sync(0xffffffffu, other.x, 1);
+                    other.y = __shfl_xor_sync(0xffffffffu, other.y, 1);
+                    other.z = __shfl_xor_sync(0xffffffffu, other.z, 1);
+                    other.w = __shfl_xor_sync(0xffffffffu, other.w, 1);
+                    // first the even lane's row, then the odd lane's
+                    if (odd ? valid_pair : valid) *reinterpret_cast<uint4*>((odd ? out_pair : out) + 16 * c + 8 * odd) = odd ? other : own;
+                    if (odd ? valid : valid_pair) *reinterpret_cast<uint4*>((odd ? out : out_pair) + 16 * c + 8 * odd) = odd ? own : other;
+                } else if (valid) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<float4*>(a.part_o + at * 128 + 16 * c + 4 * e) =
+                        *reinterpret_cast<float4*>(po + (size_t)(4 * c + e) * 4 * a.tile_rows) =
                             make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
-            if (valid && !whole) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m_run, l_run);
+            if (valid && !whole)
+                *reinterpret_cast<float2*>(a.part_ml + 2 * (slot + t * 128 + m)) = make_float2(m_run, l_run);
             tc_fence_before();
-            w = nw;
         }
     } else if constexpr (kInt4) {
-        reg_dec<96>();
+        reg_dec<88>();
         // -------------------------------------------------------------- 4-bit tiles to fp16
         // thread (key, q): keys ct / 4 + 32 i, the 16 bytes that hold dims 8 q..
-        // of each 32-dim block; the next tile's words are on their way meanwhile
+        // of each 32-dim block; the quad's first copies the key's scale pairs
         const int ct = threadIdx.x - 384, q = ct & 3, kr = ct >> 2;
         const int in_page = (1 << a.p.page_shift) - 1, mb = 4 * n_groups;
-        uint4 cw[4];
-        uint32_t cm[4][4];
-        int64_t rows[4];         // page rows of the tile being loaded; -1: not seen
-        int x = 0;               // ring index of the tile in hand
-        auto locate = [&](const PagedWalk& w, int s) {
+        const uint32_t stage0 = sbase + kOffStage;
+        int x = 0, y = 0;        // tiles converted, tiles asked for
+        int s = 0;               // unit being asked for, of run w
+        int id[4];               // its pages; -1: the key is not seen
+        auto locate = [&]() {
+            if (!w.live()) return;
             const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = first_key(w, s) + kr + 32 * i;
-                rows[i] = -1;
-                if (key >= w.it.klo && key < w.it.khi)
-                    rows[i] = paged_row(a.p, paged_id(a.p, table[key >> a.p.page_shift]), key & in_page, w.h);
+                id[i] = -1;
+                if (key >= w.it.klo && key < w.it.khi) id[i] = paged_id(a.p, table[key >> a.p.page_shift]);
             }
         };
-        auto load = [&](int kv) {
-            const uint8_t* base = kv ? a.p.v : a.p.k;
-            const uint8_t* meta = kv ? a.p.vs : a.p.ks;
+        // ask for the next tile (K then V of a unit); a key nobody sees gets zeros:
+        // 0 * (c - 8) + 0
+        auto ask = [&]() {
+            if (w.live()) {
+                const bool is_v = y & 1;
+                const uint32_t d = stage0 + (uint32_t)(y % kStaged) * kStage;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                cw[i] = make_uint4(0u, 0u, 0u, 0u);
-                cm[i][0] = cm[i][1] = cm[i][2] = cm[i][3] = 0u;
-                if (rows[i] < 0) continue;
-                cw[i] = *reinterpret_cast<const uint4*>(base + rows[i] * 64 + 16 * q);
-                const uint8_t* mp = meta + rows[i] * mb;
-                if (n_groups == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(mp);
-                    cm[i][0] = v.x, cm[i][1] = v.y, cm[i][2] = v.z, cm[i][3] = v.w;
-                } else if (n_groups == 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(mp);
-                    cm[i][0] = cm[i][1] = v.x, cm[i][2] = cm[i][3] = v.y;
-                } else {
-                    cm[i][0] = cm[i][1] = cm[i][2] = cm[i][3] = *reinterpret_cast<const uint32_t*>(mp);
+                for (int i = 0; i < 4; ++i) {
+                    const int k = kr + 32 * i;
+                    const uint32_t dc = d + 64u * k + 16u * q, dm = d + kStageCodes + (uint32_t)(mb * k);
+                    if (id[i] < 0) {
+                        sts16(dc, make_uint4(0u, 0u, 0u, 0u));
+                        if (q < n_groups) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dm + 4u * q), "r"(0u) : "memory");
+                        continue;
+                    }
+                    const int64_t row = paged_row(a.p, id[i], (first_key(w, s) + k) & in_page, w.h);
+                    copy_async<16>(dc, (is_v ? a.p.v : a.p.k) + row * 64 + 16 * q);
+                    if (q == 0) {
+                        const uint8_t* mp = (is_v ? a.p.vs : a.p.ks) + row * mb;
+                        if (n_groups == 4) copy_async<16>(dm, mp);
+                        else if (n_groups == 2) copy_async<8>(dm, mp);
+                        else copy_async<4>(dm, mp);
+                    }
+                }
+                ++y;
+                if (is_v) {
+                    if (++s == w.n) {
+                        s = 0;
+                        advance();
+                    }
+                    locate();
                 }
             }
+            copy_commit();
         };
-        auto convert = [&]() -> bool {
+        locate();
+        for (int i = 0; i < kStaged; ++i) ask();
+        while (x < y) {
             const int slot = x % kRing;
-            if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) return false;
+            copy_wait<kStaged - 1>();
+            __syncwarp();
+            if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) {
+                ok = false;
+                break;
+            }
+            const uint32_t d = stage0 + (uint32_t)(x % kStaged) * kStage;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int key = kr + 32 * i;
-                const uint32_t d = sbase + kOffRing + (uint32_t)slot * kTile + (uint32_t)key * 128u;
+                const int k = kr + 32 * i;
+                const uint4 cw = lds16(d + 64u * k + 16u * q);
+                const uint32_t dm = d + kStageCodes + (uint32_t)(mb * k);
+                uint32_t cm[4];
+                if (n_groups == 4) {
+                    const uint4 v = lds16(dm);
+                    cm[0] = v.x, cm[1] = v.y, cm[2] = v.z, cm[3] = v.w;
+                } else {
+                    cm[0] = cm[1] = lds4(dm);
+                    cm[2] = cm[3] = n_groups == 2 ? lds4(dm + 4u) : cm[0];
+                }
+                const uint32_t dst = sbase + kOffRing + (uint32_t)slot * kTile + (uint32_t)k * 128u;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {   // 32-dim block: units of the chunk's two 8-byte halves
-                    const uint32_t w = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w,
-                                                   (b & 1) ? 0x7632 : 0x5410);
-                    const uint32_t sc = __byte_perm(cm[i][b], 0u, 0x1010);
-                    const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[i][b], 0u, 0x3232));
-                    sts16(d + (uint32_t)(b >> 1) * kHalf + (uint32_t)(((4 * (b & 1) + q) ^ (key & 7)) << 4),
-                          make_uint4(hfma2(even8(w), sc, o8), hfma2(odd8(w), sc, o8), hfma2(even8(w >> 8), sc, o8),
-                                     hfma2(odd8(w >> 8), sc, o8)));
+                    const uint32_t z = __byte_perm(b < 2 ? cw.x : cw.y, b < 2 ? cw.z : cw.w, (b & 1) ? 0x7632 : 0x5410);
+                    const uint32_t sc = __byte_perm(cm[b], 0u, 0x1010);
+                    const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[b], 0u, 0x3232));
+                    sts16(dst + (uint32_t)(b >> 1) * kHalf + (uint32_t)(((4 * (b & 1) + q) ^ (k & 7)) << 4),
+                          make_uint4(hfma2(even8(z), sc, o8), hfma2(odd8(z), sc, o8), hfma2(even8(z >> 8), sc, o8),
+                                     hfma2(odd8(z >> 8), sc, o8)));
                 }
             }
             fence_proxy_async_smem();
-            __syncwarp();
+            __syncwarp();   // the packed tile has been read, too
             if (lane == 0) mbar_arrive(&full[slot]);
             ++x;
-            return true;
-        };
-        PagedWalk w(a, sh, u1);
-        int s = 0;
-        if (w.live()) {
-            locate(w, 0);
-            load(0);
+            ask();
         }
-        while (w.live()) {
-            if (!(ok = convert())) break;      // K
-            load(1);
-            // where the next tile's rows are
-            PagedWalk nw = w;
-            int ns = s + 1;
-            if (ns == w.n) {
-                nw.next(a, a.items);
-                ns = 0;
-            }
-            if (nw.live()) locate(nw, ns);
-            if (!(ok = convert())) break;      // V
-            if (nw.live()) load(0);
-            w = nw;
-            s = ns;
-        }
+        copy_wait<0>();
     }
     if (!ok && lane == 0) paged_err(a.p.err, DEV_ERR_TIMEOUT, warp);
     tc_fence_before();
@@ -623,11 +735,12 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
 }
 
 template <bool kInt4, bool kExtra>
-cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const PagedAttn& a, int n_groups, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const PagedAttn& a, int n_groups,
+                   cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(paged_tc_kernel<kInt4, kExtra>, (int)kSmem, &allowed);
     if (e != cudaSuccess) return e;
-    KVR_LAUNCH(paged_tc_kernel<kInt4, kExtra>, dim3((unsigned)a.n_cta), dim3(kInt4 ? 512 : 384), kSmem, s, k, v, a, n_groups);
+    KVR_LAUNCH(paged_tc_kernel<kInt4, kExtra>, dim3((unsigned)a.n_cta), dim3(kInt4 ? 512 : 384), kSmem, s, k, v, q, a, n_groups);
     return cudaSuccess;
 }
 
@@ -635,9 +748,9 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const PagedAttn& 
 
 cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStream_t s, std::string* why) {
     const bool extra = a.softcap > 0.f || a.loc || a.snk || a.slopes;
-    CUtensorMap k{}, v{};
+    CUtensorMap k{}, v{}, q{};
     if (format == KVR_INT4)
-        return extra ? launch<true, true>(k, v, a, 128 / group, s) : launch<true, false>(k, v, a, 128 / group, s);
+        return extra ? launch<true, true>(k, v, q, a, 128 / group, s) : launch<true, false>(k, v, q, a, 128 / group, s);
     // pages as (dim, slot, head, page); a box is one page's share of a 128-key tile, half a row wide
     const uint64_t dims[4] = {128, 1ull << a.p.page_shift, (uint64_t)a.p.n_kv_heads, (uint64_t)a.p.n_pages};
     const uint64_t strides[3] = {(uint64_t)a.p.slot_stride * 256, (uint64_t)a.p.head_stride * 256,
@@ -645,7 +758,11 @@ cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStrea
     const uint32_t box[4] = {64, 1u << (a.p.page_shift < 7 ? a.p.page_shift : 7), 1, 1};
     if (!make_tmap_4d_bf16(&k, a.p.k, dims, strides, box, why) || !make_tmap_4d_bf16(&v, a.p.v, dims, strides, box, why))
         return cudaErrorInvalidValue;
-    return extra ? launch<false, true>(k, v, a, 0, s) : launch<false, false>(k, v, a, 0, s);
+    // Q as (dim, head, row): a box is a row tile of one K/V head, positions x query heads
+    if (!make_tmap_3d_bf16(&q, a.q, 128, (uint64_t)a.n_q_heads, (uint64_t)a.r.n_rows, 256, (uint64_t)a.q_stride * 2, 64,
+                           (uint32_t)a.G, (uint32_t)(128 / a.G), why))
+        return cudaErrorInvalidValue;
+    return extra ? launch<false, true>(k, v, q, a, 0, s) : launch<false, false>(k, v, q, a, 0, s);
 }
 
 }  // namespace kvr
