@@ -16,8 +16,8 @@
 //   warp 1      tcgen05.mma: S_t = Q_t K^T, O_t += P_t V.  One thread issues all
 //               products; they complete in order, so "S_t of tile j is done" also
 //               says that tile j - 1's product with V is.
-//   warp 2      bf16: Q of the next run by TMA, as soon as the last scores
-//               are done with its tile (4 bits: the softmax warps, scaled to fp16).
+//   warp 2      Q of the next run by TMA, as soon as the last scores are done
+//               with its tile (4 bits: the softmax warps then scale it to fp16 in place).
 //   warps 4-11  softmax, four warps a row tile, one thread a row: no exchange
 //               between threads.  Base 2; the running maximum is raised, and O
 //               rescaled in tensor memory, only when it grows by more than
@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     uint64_t* s_full = q_empty + 2;                                 // [2] S_t is done
     uint64_t* p_full = s_full + 2;                                  // [2][2] half of P_t is in tensor memory
     uint64_t* o_done = p_full + 4;                                  // [2] a run's last product with V is done
-    uint64_t* drained = o_done + 2;                                 // every product issued is done
+    uint64_t* q_raw = o_done + 2;                                   // [2] 4 bits: Q_t has landed in bf16
+    uint64_t* drained = q_raw + 2;                                  // every product issued is done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.G, per_tile = 128 / G;
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         mbar_init(drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], kInt4 ? 4 : 1);
+            mbar_init(&q_raw[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[2 * i], 4);
@@ -206,12 +208,14 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         }
         fence_mbar_init();
     }
-    if (warp == 0 && lane == 0 && !kInt4) {
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
+    if (warp == 0 && lane == 0) {
+        if (!kInt4) {
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+        }
         prefetch_tmap(&tmQ);
     }
-    if (warp == 2 && !kInt4)   // rows of a tile that no position fills (128 % G): zeros for good
+    if (warp == 2)   // rows of a tile that no position fills (128 % G): zeros for good
         for (int i = lane; i < 2 * (128 - per_tile * G) * 16; i += 32) {
             const int t = i / ((128 - per_tile * G) * 16), j = i % ((128 - per_tile * G) * 16);
             sts16(sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)(j & 1) * kHalf +
@@ -335,24 +339,26 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             mma_commit(drained);
             if (!mbar_wait(drained, 0)) ok = false;
         }
-    } else if (!kInt4 && warp == 2) {
+    } else if (warp == 2) {
         // ------------------------------------------------------------- Q by TMA
         if (lane == 0) {
+            uint64_t* landed = kInt4 ? q_raw : q_full;
             int runs[2] = {0, 0};
             for (; w.live() && ok; w.next(a, a.items))
                 for (int t = 0; t < row_tiles(w, per_tile) && ok; ++t) {
                     const int r = runs[t]++;
                     if (r > 0 && !mbar_wait(&q_empty[t], (uint32_t)(r - 1) & 1u)) {
                         ok = false;
+                        --runs[t];
                         break;
                     }
                     uint8_t* dst = smem + kOffQ + (uint32_t)t * kTile;
-                    mbar_arrive_expect_tx(&q_full[t], 2u * 128u * (uint32_t)(per_tile * G));
-                    tma_load_3d(dst, &tmQ, &q_full[t], 0, w.h * G, w.it.row0 + t * per_tile);
-                    tma_load_3d(dst + kHalf, &tmQ, &q_full[t], 64, w.h * G, w.it.row0 + t * per_tile);
+                    mbar_arrive_expect_tx(&landed[t], 2u * 128u * (uint32_t)(per_tile * G));
+                    tma_load_3d(dst, &tmQ, &landed[t], 0, w.h * G, w.it.row0 + t * per_tile);
+                    tma_load_3d(dst + kHalf, &tmQ, &landed[t], 64, w.h * G, w.it.row0 + t * per_tile);
                 }
             for (int t = 0; t < 2; ++t)   // the last copies land before the CTA exits
-                if (runs[t] > 0 && !mbar_wait(&q_full[t], (uint32_t)(runs[t] - 1) & 1u)) ok = false;
+                if (runs[t] > 0 && !mbar_wait(&landed[t], (uint32_t)(runs[t] - 1) & 1u)) ok = false;
         }
     }
     } else if (warp < 12) {
@@ -371,18 +377,15 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         };
         float lsr_next = sl2;   // what turns the row's products into base-2 logits
         // 4 bits: this thread's row of Q to fp16, scaled by a power of two to [128,
-        // 256) at its largest, into the operand's swizzle; the scores of the run
-        // before are done with the tile (this thread has seen them)
+        // 256) at its largest, in place (the permuted order stays within a chunk)
         auto load_q = [&]() {
             if constexpr (kInt4) {
+                if (!(ok = warp_wait(&q_raw[t], (uint32_t)runs & 1u))) return;
+                const uint32_t dst = sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)m * 128u;
                 uint4 q[16];
-                const int p = t * per_tile + m / G;
-                const bool valid = m < per_tile * G && p < w.it.rows;
-                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                                  (int64_t)(w.it.row0 + p) * a.q_stride +
-                                                                  (int64_t)(w.h * G + m % G) * 128);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) q[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < 16; ++c)
+                    q[c] = lds16(dst + (uint32_t)(c >> 3) * kHalf + (uint32_t)(((c & 7) ^ (m & 7)) << 4));
                 uint32_t top = 0u;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
@@ -393,7 +396,6 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 const int ex = min(max((int)(top >> 7), 8), 253);
                 const float f = __uint_as_float((uint32_t)(261 - ex) << 23);      // 2^(134 - ex)
                 lsr_next = sl2 * __uint_as_float((uint32_t)(ex - 7) << 23);       // 2^(ex - 134)
-                const uint32_t dst = sbase + kOffQ + (uint32_t)t * kTile + (uint32_t)m * 128u;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
@@ -477,30 +479,17 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         for (int k = 0; k < 128; ++k) x[k] = fmaf(-slope, (float)abs(gpos - key0 - k), x[k]);
                     }
                 }
-                if (key0 < all_lo || key0 + 128 > all_hi) {   // warp-uniform
-                    const int l = lo - key0, h = hi - key0;
+                if (key0 + 128 > all_hi) {   // warp-uniform, as the next
+                    const int h = hi - key0;
 #pragma unroll
                     for (int k = 0; k < 128; ++k)
-                        if (k < l || k >= h) x[k] = -INFINITY;
+                        if (k >= h) x[k] = -INFINITY;
                 }
-                if (!kInt4 && (key0 < klo || key0 + 128 > khi)) {
-                    // keys nobody sees: whatever their slots held is not used.  Both row
-                    // tiles write the same zeros, each before its own product.
-                    const int vx = 2 * g + 1;
-                    if (!warp_wait(&full[vx % kRing], (uint32_t)(vx / kRing) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    const int key = key0 + m;
-                    if (key < klo || key >= khi) {
-                        const uint32_t d = sbase + kOffRing + (uint32_t)(vx % kRing) * kTile + (uint32_t)m * 128u;
+                if (key0 < all_lo) {
+                    const int l = lo - key0;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            sts16(d + 16u * c, make_uint4(0u, 0u, 0u, 0u));
-                            sts16(d + kHalf + 16u * c, make_uint4(0u, 0u, 0u, 0u));
-                        }
-                    }
-                    fence_proxy_async_smem();
+                    for (int k = 0; k < 128; ++k)
+                        if (k < l) x[k] = -INFINITY;
                 }
                 auto maximum = [&]() {
                     float mx[8];
@@ -558,6 +547,25 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         weights(1, pk[1], sum[1]);
                     }
                 }
+                // keys nobody sees: whatever their slots held is not used.  Both row
+                // tiles write the same zeros, each before its own product.
+                if (!kInt4 && (key0 < klo || key0 + 128 > khi)) {
+                    const int vx = 2 * g + 1;
+                    if (!warp_wait(&full[vx % kRing], (uint32_t)(vx / kRing) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const int key = key0 + m;
+                    if (key < klo || key >= khi) {
+                        const uint32_t d = sbase + kOffRing + (uint32_t)(vx % kRing) * kTile + (uint32_t)m * 128u;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            sts16(d + 16u * c, make_uint4(0u, 0u, 0u, 0u));
+                            sts16(d + kHalf + 16u * c, make_uint4(0u, 0u, 0u, 0u));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
                 tmem_st16_async(ts, pk[0]);
                 tmem_st16_async(ts + 16u, pk[1]);
                 weights(2, pk[0], sum[2]);   // while the stores land
@@ -579,9 +587,10 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             // ---- the next run's Q, so that its first scores are on their way meanwhile
             advance();
             skip();
+            ++runs;
             if (w.live()) load_q();
             // ---- the run's rows
-            if (!warp_wait(&o_done[t], (uint32_t)(runs++) & 1u)) {
+            if (!ok || !warp_wait(&o_done[t], (uint32_t)(runs - 1) & 1u)) {
                 ok = false;
                 break;
             }
@@ -596,32 +605,39 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             // exchanging 16 bytes each
             float* po = a.part_o + slot * 128 + 4 * (size_t)(t * 128 + m);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                float y[16], o[16];
-                tmem_ld16(to + 16u * c, y);
+            for (int hf = 0; hf < 2; ++hf) {
+                float y[64];
+                tmem_ld32x2(to + 64u * hf, y);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)   // 4 bits: column 2 k + b of a chunk of 8 is dim k + 4 b
-                    o[e] = kInt4 ? y[(e & 8) + 2 * (e & 3) + ((e >> 2) & 1)] : y[e];
-                if (whole) {
-                    uint32_t k[8];
+                for (int c = 0; c < 4; ++c) {
+                    float o[16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) k[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-                    // even lane: first 16 bytes of its own row and of its neighbour's; odd lane: the second
-                    const bool odd = lane & 1;
-                    uint4 own = odd ? make_uint4(k[4], k[5], k[6], k[7]) : make_uint4(k[0], k[1], k[2], k[3]);
-                    uint4 other = odd ? make_uint4(k[0], k[1], k[2], k[3]) : make_uint4(k[4], k[5], k[6], k[7]);
-                    other.x = __shfl_xor_sync(0xffffffffu, other.x, 1);
-                    other.y = __shfl_xor_sync(0xffffffffu, other.y, 1);
-                    other.z = __shfl_xor_sync(0xffffffffu, other.z, 1);
-                    other.w = __shfl_xor_sync(0xffffffffu, other.w, 1);
-                    // first the even lane's row, then the odd lane's
-                    if (odd ? valid_pair : valid) *reinterpret_cast<uint4*>((odd ? out_pair : out) + 16 * c + 8 * odd) = odd ? other : own;
-                    if (odd ? valid : valid_pair) *reinterpret_cast<uint4*>((odd ? out : out_pair) + 16 * c + 8 * odd) = odd ? own : other;
-                } else if (valid) {
+                    for (int e = 0; e < 16; ++e)   // 4 bits: column 2 k + b of a chunk of 8 is dim k + 4 b
+                        o[e] = kInt4 ? y[16 * c + (e & 8) + 2 * (e & 3) + ((e >> 2) & 1)] : y[16 * c + e];
+                    const int d = 64 * hf + 16 * c;
+                    if (whole) {
+                        uint32_t k[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<float4*>(po + (size_t)(4 * c + e) * 4 * a.tile_rows) =
-                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e) k[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+                        // even lane: first 16 bytes of its own row and of its neighbour's; odd lane: the second
+                        const bool odd = lane & 1;
+                        const uint4 own = odd ? make_uint4(k[4], k[5], k[6], k[7]) : make_uint4(k[0], k[1], k[2], k[3]);
+                        uint4 other = odd ? make_uint4(k[0], k[1], k[2], k[3]) : make_uint4(k[4], k[5], k[6], k[7]);
+                        other.x = __shfl_xor_sync(0xffffffffu, other.x, 1);
+                        other.y = __shfl_xor_sync(0xffffffffu, other.y, 1);
+                        other.z = __shfl_xor_sync(0xffffffffu, other.z, 1);
+                        other.w = __shfl_xor_sync(0xffffffffu, other.w, 1);
+                        // first the even lane's row, then the odd lane's
+                        if (odd ? valid_pair : valid)
+                            *reinterpret_cast<uint4*>((odd ? out_pair : out) + d + 8 * odd) = odd ? other : own;
+                        if (odd ? valid : valid_pair)
+                            *reinterpret_cast<uint4*>((odd ? out : out_pair) + d + 8 * odd) = odd ? own : other;
+                    } else if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float4*>(po + (size_t)(d / 4 + e) * 4 * a.tile_rows) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
                 }
             }
             if (valid && !whole)
@@ -646,7 +662,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             for (int i = 0; i < 4; ++i) {
                 const int key = first_key(w, s) + kr + 32 * i;
                 id[i] = -1;
-                if (key >= w.it.klo && key < w.it.khi) id[i] = paged_id(a.p, table[key >> a.p.page_shift]);
+                if (key >= w.it.klo && key < w.it.khi) id[i] = table[key >> a.p.page_shift] & 0x7fffffff;   // checked when used
             }
         };
         // ask for the next tile (K then V of a unit); a key nobody sees gets zeros:
@@ -654,6 +670,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         auto ask = [&]() {
             if (w.live()) {
                 const bool is_v = y & 1;
+                const int key0 = first_key(w, s), head = w.h;
                 const uint32_t d = stage0 + (uint32_t)(y % kStaged) * kStage;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -664,7 +681,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         if (q < n_groups) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dm + 4u * q), "r"(0u) : "memory");
                         continue;
                     }
-                    const int64_t row = paged_row(a.p, id[i], (first_key(w, s) + k) & in_page, w.h);
+                    const int64_t row = paged_row(a.p, paged_id(a.p, id[i]), (key0 + k) & in_page, head);
                     copy_async<16>(dc, (is_v ? a.p.v : a.p.k) + row * 64 + 16 * q);
                     if (q == 0) {
                         const uint8_t* mp = (is_v ? a.p.vs : a.p.ks) + row * mb;
@@ -695,29 +712,37 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 break;
             }
             const uint32_t d = stage0 + (uint32_t)(x % kStaged) * kStage;
+            uint4 cw[4];
+            uint32_t cm[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int k = kr + 32 * i;
-                const uint4 cw = lds16(d + 64u * k + 16u * q);
+                cw[i] = lds16(d + 64u * k + 16u * q);
                 const uint32_t dm = d + kStageCodes + (uint32_t)(mb * k);
-                uint32_t cm[4];
                 if (n_groups == 4) {
                     const uint4 v = lds16(dm);
-                    cm[0] = v.x, cm[1] = v.y, cm[2] = v.z, cm[3] = v.w;
+                    cm[i][0] = v.x, cm[i][1] = v.y, cm[i][2] = v.z, cm[i][3] = v.w;
                 } else {
-                    cm[0] = cm[1] = lds4(dm);
-                    cm[2] = cm[3] = n_groups == 2 ? lds4(dm + 4u) : cm[0];
+                    cm[i][0] = cm[i][1] = lds4(dm);
+                    cm[i][2] = cm[i][3] = n_groups == 2 ? lds4(dm + 4u) : cm[i][0];
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = kr + 32 * i;
                 const uint32_t dst = sbase + kOffRing + (uint32_t)slot * kTile + (uint32_t)k * 128u;
+                uint4 v[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {   // 32-dim block: units of the chunk's two 8-byte halves
-                    const uint32_t z = __byte_perm(b < 2 ? cw.x : cw.y, b < 2 ? cw.z : cw.w, (b & 1) ? 0x7632 : 0x5410);
-                    const uint32_t sc = __byte_perm(cm[b], 0u, 0x1010);
-                    const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[b], 0u, 0x3232));
-                    sts16(dst + (uint32_t)(b >> 1) * kHalf + (uint32_t)(((4 * (b & 1) + q) ^ (k & 7)) << 4),
-                          make_uint4(hfma2(even8(z), sc, o8), hfma2(odd8(z), sc, o8), hfma2(even8(z >> 8), sc, o8),
-                                     hfma2(odd8(z >> 8), sc, o8)));
+                    const uint32_t z = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w, (b & 1) ? 0x7632 : 0x5410);
+                    const uint32_t sc = __byte_perm(cm[i][b], 0u, 0x1010);
+                    const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[i][b], 0u, 0x3232));
+                    v[b] = make_uint4(hfma2(even8(z), sc, o8), hfma2(odd8(z), sc, o8), hfma2(even8(z >> 8), sc, o8),
+                                      hfma2(odd8(z >> 8), sc, o8));
                 }
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    sts16(dst + (uint32_t)(b >> 1) * kHalf + (uint32_t)(((4 * (b & 1) + q) ^ (k & 7)) << 4), v[b]);
             }
             fence_proxy_async_smem();
             __syncwarp();   // the packed tile has been read, too
@@ -749,6 +774,10 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap
 cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStream_t s, std::string* why) {
     const bool extra = a.softcap > 0.f || a.loc || a.snk || a.slopes;
     CUtensorMap k{}, v{}, q{};
+    // Q as (dim, head, row): a box is a row tile of one K/V head, positions x query heads
+    if (!make_tmap_3d_bf16(&q, a.q, 128, (uint64_t)a.n_q_heads, (uint64_t)a.r.n_rows, 256, (uint64_t)a.q_stride * 2, 64,
+                           (uint32_t)a.G, (uint32_t)(128 / a.G), why))
+        return cudaErrorInvalidValue;
     if (format == KVR_INT4)
         return extra ? launch<true, true>(k, v, q, a, 128 / group, s) : launch<true, false>(k, v, q, a, 128 / group, s);
     // pages as (dim, slot, head, page); a box is one page's share of a 128-key tile, half a row wide
@@ -757,10 +786,6 @@ cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStrea
                                  (uint64_t)a.p.page_stride * 256};
     const uint32_t box[4] = {64, 1u << (a.p.page_shift < 7 ? a.p.page_shift : 7), 1, 1};
     if (!make_tmap_4d_bf16(&k, a.p.k, dims, strides, box, why) || !make_tmap_4d_bf16(&v, a.p.v, dims, strides, box, why))
-        return cudaErrorInvalidValue;
-    // Q as (dim, head, row): a box is a row tile of one K/V head, positions x query heads
-    if (!make_tmap_3d_bf16(&q, a.q, 128, (uint64_t)a.n_q_heads, (uint64_t)a.r.n_rows, 256, (uint64_t)a.q_stride * 2, 64,
-                           (uint32_t)a.G, (uint32_t)(128 / a.G), why))
         return cudaErrorInvalidValue;
     return extra ? launch<false, true>(k, v, q, a, 0, s) : launch<false, false>(k, v, q, a, 0, s);
 }
