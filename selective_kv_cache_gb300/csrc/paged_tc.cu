@@ -237,9 +237,9 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     bool ok = true;
 
     // registers to the softmax, which holds a row of scores a thread: 72 + 2 x
-    // 216 of 3 x 168 a thread, 56 + 2 x 184 + 88 of 4 x 128
+    // 216 of 3 x 168 a thread, 72 + 2 x 176 + 88 of 4 x 128
     if (warp < 4) {
-        reg_dec<kInt4 ? 56 : 72>();
+        reg_dec<72>();
     if (warp == 0) {
         if constexpr (!kInt4) {
             // ---------------------------------------------------------- K and V copies
@@ -283,22 +283,27 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         if (lane == 0) {
             const uint32_t id_s = kInt4 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
             const uint32_t id_o = kInt4 ? idesc_f16(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);   // V is MN-major
-            int g = 0, runs[2] = {0, 0}, ps[2] = {0, 0};   // tiles, runs and P tiles so far
+            int g = 0;                      // tiles so far
+            uint32_t runs = 0, ps = 0;      // bit t: parity of the runs and of the P tiles of row tile t
             auto landed = [&](int x) { return mbar_wait(&full[x % kRing], (uint32_t)(x / kRing) & 1u); };
             auto scores = [&](int t, int x) {
-                const uint32_t qa = sbase + kOffQ + (uint32_t)t * kTile, ka = sbase + kOffRing + (uint32_t)(x % kRing) * kTile;
+                // descriptors advance by addresses / 16 in their low bits: two
+                // registers each, where building every one anew spilled
+                const uint64_t qd = sdesc_sw128(sbase + kOffQ + (uint32_t)t * kTile, 16, 1024);
+                const uint64_t kd = sdesc_sw128(sbase + kOffRing + (uint32_t)(x % kRing) * kTile, 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t o = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
-                    mma_bf16(tmem + kColS + 128u * t, sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(ka + o, 16, 1024), id_s, kk > 0);
+                    const uint32_t o = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
+                    mma_bf16(tmem + kColS + 128u * t, qd + o, kd + o, id_s, kk > 0);
                 }
                 mma_commit(&s_full[t]);
             };
             for (; w.live() && ok; w.next(a, a.items)) {
                 const int nt = row_tiles(w, per_tile), n = w.n;
                 for (int t = 0; t < nt && ok; ++t) {
-                    ok = mbar_wait(&q_full[t], (uint32_t)(runs[t]++) & 1u) && (t || landed(2 * g));
+                    ok = mbar_wait(&q_full[t], (runs >> t) & 1u) && (t || landed(2 * g));
                     if (!ok) break;
+                    runs ^= 1u << t;
                     tc_fence_after();
                     scores(t, 2 * g);
                     if (n == 1) mma_commit(&q_empty[t]);
@@ -306,22 +311,22 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 }
                 for (int s = 0; s < n && ok; ++s, ++g) {
                     const int v = 2 * g + 1;
-                    const uint32_t va = sbase + kOffRing + (uint32_t)(v % kRing) * kTile;
+                    const uint64_t vd = sdesc_sw128(sbase + kOffRing + (uint32_t)(v % kRing) * kTile, kHalf, 1024);
                     for (int t = 0; t < nt; ++t) {
                         const uint32_t pt = tmem + kColS + 128u * t;
                         // the first half's product runs while the softmax is on the second
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            ok = mbar_wait(&p_full[2 * t + hf], (uint32_t)ps[t] & 1u) && (t || hf || landed(v));
+                            ok = mbar_wait(&p_full[2 * t + hf], (ps >> t) & 1u) && (t || hf || landed(v));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
                             for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
                                 mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
-                                            sdesc_sw128(va + (uint32_t)kk * 2048u, kHalf, 1024), id_o, (s > 0 || kk > 0));
+                                            vd + (uint32_t)kk * 128u, id_o, (s > 0 || kk > 0));
                         }
                         if (!ok) break;
-                        ++ps[t];
+                        ps ^= 1u << t;
                         if (s == n - 1) mma_commit(&o_done[t]);
                         if (t == nt - 1) mma_commit(&empty[v % kRing]);
                         if (s + 1 < n) {
@@ -343,26 +348,27 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         // ------------------------------------------------------------- Q by TMA
         if (lane == 0) {
             uint64_t* landed = kInt4 ? q_raw : q_full;
-            int runs[2] = {0, 0};
+            uint32_t begun = 0, runs = 0;   // bit t: row tile t has begun a run; parity of its runs
             for (; w.live() && ok; w.next(a, a.items))
-                for (int t = 0; t < row_tiles(w, per_tile) && ok; ++t) {
-                    const int r = runs[t]++;
-                    if (r > 0 && !mbar_wait(&q_empty[t], (uint32_t)(r - 1) & 1u)) {
+                for (int t = 0; t < row_tiles(w, per_tile); ++t) {
+                    // the run before this one; its own parity is the other
+                    if (((begun >> t) & 1u) && !mbar_wait(&q_empty[t], ((runs >> t) & 1u) ^ 1u)) {
                         ok = false;
-                        --runs[t];
                         break;
                     }
                     uint8_t* dst = smem + kOffQ + (uint32_t)t * kTile;
                     mbar_arrive_expect_tx(&landed[t], 2u * 128u * (uint32_t)(per_tile * G));
                     tma_load_3d(dst, &tmQ, &landed[t], 0, w.h * G, w.it.row0 + t * per_tile);
                     tma_load_3d(dst + kHalf, &tmQ, &landed[t], 64, w.h * G, w.it.row0 + t * per_tile);
+                    begun |= 1u << t;
+                    runs ^= 1u << t;
                 }
             for (int t = 0; t < 2; ++t)   // the last copies land before the CTA exits
-                if (runs[t] > 0 && !mbar_wait(&landed[t], (uint32_t)(runs[t] - 1) & 1u)) ok = false;
+                if (((begun >> t) & 1u) && !mbar_wait(&landed[t], ((runs >> t) & 1u) ^ 1u)) ok = false;
         }
     }
     } else if (warp < 12) {
-        reg_inc<kInt4 ? 184 : 216>();
+        reg_inc<kInt4 ? 176 : 216>();
         // -------------------------------------------------------------- softmax
         const int t = warp >= 8 ? 1 : 0, m = 32 * (warp & 3) + lane;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
@@ -515,36 +521,47 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     }
                     sum = __fadd2_rn(acc[0], acc[1]);
                 };
-                float top;
-                if (s == 0) {
-                    top = maximum();
-                    if (top > -INFINITY) m_run = top, m_neg = -top;
-                }
+                // the scores of this tile being done, so is the product of the one before: O stands still
+                auto rescale = [&](float f) {
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        float o[16];
+                        tmem_ld16(to + 16u * c, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        tmem_st16(to + 16u * c, o);
+                    }
+                };
                 uint32_t pk[2][16];
                 float2 sum[4];
-                weights(0, pk[0], sum[0]);
-                weights(1, pk[1], sum[1]);
-                if (s > 0) {
-                    top = maximum();
+                if constexpr (kInt4) {   // no registers to spare for weights that may be taken twice
+                    const float top = maximum();
                     const bool raise = top > m_run + kLazy;
                     if (__any_sync(0xffffffffu, raise)) {
-                        // the scores of this tile being done, so is the product of the one before: O stands still
                         const float f = raise ? ex2(m_run - top) : 1.f;
-#pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            float o[16];
-                            tmem_ld16(to + 16u * c, o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
-                            tmem_st16(to + 16u * c, o);
+                        if (s > 0) rescale(f);
+                        if (raise) l_run *= f, m_run = top, m_neg = -top;
+                    }
+                    weights(0, pk[0], sum[0]);
+                    tmem_st16_async(ts, pk[0]);
+                    weights(1, pk[1], sum[1]);
+                } else {
+                    if (s == 0) {
+                        const float top = maximum();
+                        if (top > -INFINITY) m_run = top, m_neg = -top;
+                    }
+                    weights(0, pk[0], sum[0]);
+                    weights(1, pk[1], sum[1]);
+                    if (s > 0) {
+                        const float top = maximum();
+                        const bool raise = top > m_run + kLazy;
+                        if (__any_sync(0xffffffffu, raise)) {
+                            const float f = raise ? ex2(m_run - top) : 1.f;
+                            rescale(f);
+                            if (raise) l_run *= f, m_run = top, m_neg = -top;
+                            weights(0, pk[0], sum[0]);
+                            weights(1, pk[1], sum[1]);
                         }
-                        if (raise) {
-                            l_run *= f;
-                            m_run = top;
-                            m_neg = -top;
-                        }
-                        weights(0, pk[0], sum[0]);
-                        weights(1, pk[1], sum[1]);
                     }
                 }
                 // keys nobody sees: whatever their slots held is not used.  Both row
@@ -566,7 +583,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                tmem_st16_async(ts, pk[0]);
+                if (!kInt4) tmem_st16_async(ts, pk[0]);
                 tmem_st16_async(ts + 16u, pk[1]);
                 weights(2, pk[0], sum[2]);   // while the stores land
                 tmem_wait_st();
