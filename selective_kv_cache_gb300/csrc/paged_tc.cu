@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     uint64_t* q_full = empty + kRing;                               // [2] Q_t is in place
     uint64_t* q_empty = q_full + 2;                                 // [2] a run's last scores are done with Q_t
     uint64_t* s_full = q_empty + 2;                                 // [2] S_t is done
-    uint64_t* p_full = s_full + 2;                                  // [2][2] half of P_t is in tensor memory
-    uint64_t* o_done = p_full + 4;                                  // [2] a run's last product with V is done
+    uint64_t* p_full = s_full + 2;                                  // [2] P_t is in tensor memory
+    uint64_t* o_done = p_full + 2;                                  // [2] a run's last product with V is done
     uint64_t* q_raw = o_done + 2;                                   // [2] 4 bits: Q_t has landed in bf16
     uint64_t* drained = q_raw + 2;                                  // every product issued is done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             mbar_init(&q_raw[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[2 * i], 4);
-            mbar_init(&p_full[2 * i + 1], 4);
+            mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
         fence_mbar_init();
@@ -314,18 +313,13 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     const uint64_t vd = sdesc_sw128(sbase + kOffRing + (uint32_t)(v % kRing) * kTile, kHalf, 1024);
                     for (int t = 0; t < nt; ++t) {
                         const uint32_t pt = tmem + kColS + 128u * t;
-                        // the first half's product runs while the softmax is on the second
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            ok = mbar_wait(&p_full[2 * t + hf], (ps >> t) & 1u) && (t || hf || landed(v));
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
-                                mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
-                                            vd + (uint32_t)kk * 128u, id_o, (s > 0 || kk > 0));
-                        }
+                        ok = mbar_wait(&p_full[t], (ps >> t) & 1u) && (t || landed(v));
                         if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u, vd + (uint32_t)kk * 128u, id_o,
+                                        (s > 0 || kk > 0));
                         ps ^= 1u << t;
                         if (s == n - 1) mma_commit(&o_done[t]);
                         if (t == nt - 1) mma_commit(&empty[v % kRing]);
@@ -583,20 +577,18 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     }
                     fence_proxy_async_smem();
                 }
+                // (P handed over in halves was slower: the issuing thread held the pipe
+                // for the second half while the other row tile had products to run)
                 if (!kInt4) tmem_st16_async(ts, pk[0]);
                 tmem_st16_async(ts + 16u, pk[1]);
-                weights(2, pk[0], sum[2]);   // while the stores land
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * t]);
+                weights(2, pk[0], sum[2]);
                 tmem_st16_async(ts + 32u, pk[0]);
                 weights(3, pk[1], sum[3]);
                 tmem_st16_async(ts + 48u, pk[1]);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * t + 1]);
+                if (lane == 0) mbar_arrive(&p_full[t]);
                 const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 l_run += all.x + all.y;
             }
