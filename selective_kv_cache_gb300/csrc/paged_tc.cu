@@ -21,17 +21,19 @@
 //   warps 4-11  softmax, four warps a row tile, one thread a row: no exchange
 //               between threads.  Base 2; the running maximum is raised, and O
 //               rescaled in tensor memory, only when it grows by more than
-//               2^8, so the weights are taken against the old maximum while the
-//               tile's own is still being found, and taken again in the rare
-//               tile that raises it.  P goes to tensor memory in 16 bits (bf16; fp16 for 4-bit
+//               2^8.  P goes to tensor memory in 16 bits (bf16; fp16 for 4-bit
 //               pages) as the A operand: 2^-8 (2^-11) of a weight at most.
-//   warps 12-15 4 bits only, in the copies' place: packed rows come in
+//   warps 12-15 4 bits only, in warp 0's place: packed rows come in
 //               asynchronously three tiles ahead; codes to their values in fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
 //               ring in the operand's swizzle.  A word's nibbles come out in
 //               pairs (e, e + 4), so the 8 dims of a chunk lie in the order 0 4 1
 //               5 2 6 3 7; Q is stored in that order and O read back from it.
-// Bound by the exponentials and the tensor pipe alike: 2 x 128 x 128 of the
-// first and four 128^3 products a unit.
+// A unit is four 128^3 products (2048 cycles of the pipe) and 2 x 128 x 128
+// exponentials (1024).  Measured: about 3900 cycles, 1.09 PFLOP/s at 4096 rows
+// over 8192 keys of a 32/8-head model.  What bounds it is the chain of a row tile
+// (scores, softmax 1750, product with V) together with the issuing thread, which
+// shares its scheduler with the softmax: the waits and commits around a
+// tile's 16 products take as long as the products.
 // The runs' bookkeeping lives in shared memory, a copy per warp: a spilled register
 // costs an L2 round trip here, where shared memory takes all but a few KB of L1.
 // Every wait is bounded; on a timeout the CTA records it, drains its copies and
@@ -58,9 +60,9 @@ constexpr uint32_t kStageCodes = 128 * 64, kStage = kStageCodes + 128 * 16;
 constexpr uint32_t kOffStage = kOffRing + 4 * kTile;
 constexpr uint32_t kOffBar = kOffRing + 5 * kTile;
 constexpr uint32_t kOffWalk = kOffBar + 256;    // a PagedWalk per warp
-constexpr uint32_t kWalkBytes = 80;
-constexpr uint32_t kSmem = kOffWalk + 16 * kWalkBytes + 1024;
-static_assert(sizeof(PagedWalk) <= kWalkBytes && kStaged * kStage <= kTile, "shared memory layout");
+constexpr uint32_t kWalkBytes = 72;
+constexpr uint32_t kSmem = kOffWalk + 16 * kWalkBytes;
+static_assert(sizeof(PagedWalk) <= kWalkBytes && kStaged * kStage <= kTile && kSmem <= 232448, "shared memory layout");
 constexpr uint32_t kColS = 0, kColO = 256;      // TMEM columns of tile t: S (P over its first 64) at 128 t, O at 256 + 128 t
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
@@ -171,9 +173,12 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ CUtensorMap tmQ, PagedAttn a, int n_groups) {
     constexpr int kRing = kInt4 ? 4 : 5;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
+    if (sbase & 1023u) {   // the swizzle's atoms need it; the declaration asks for it
+        if (threadIdx.x == 0) paged_err(a.p.err, DEV_ERR_INDEX, (int)sbase);
+        return;
+    }
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);   // [kRing] a K or V tile has landed
     uint64_t* empty = full + kRing;                                 // [kRing] its products are done
     uint64_t* q_full = empty + kRing;                               // [2] Q_t is in place
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     bool ok = true;
 
     // registers to the softmax, which holds a row of scores a thread: 72 + 2 x
-    // 216 of 3 x 168 a thread, 72 + 2 x 176 + 88 of 4 x 128
+    // 216 of 3 x 168 a thread (bf16), 72 + 2 x 176 + 88 of 4 x 128 (4 bits)
     if (warp < 4) {
         reg_dec<72>();
     if (warp == 0) {
@@ -286,8 +291,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             uint32_t runs = 0, ps = 0;      // bit t: parity of the runs and of the P tiles of row tile t
             auto landed = [&](int x) { return mbar_wait(&full[x % kRing], (uint32_t)(x / kRing) & 1u); };
             auto scores = [&](int t, int x) {
-                // descriptors advance by addresses / 16 in their low bits: two
-                // registers each, where building every one anew spilled
+                // descriptors advance by addresses / 16 in their low bits
                 const uint64_t qd = sdesc_sw128(sbase + kOffQ + (uint32_t)t * kTile, 16, 1024);
                 const uint64_t kd = sdesc_sw128(sbase + kOffRing + (uint32_t)(x % kRing) * kTile, 16, 1024);
 #pragma unroll
@@ -313,24 +317,22 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     const uint64_t vd = sdesc_sw128(sbase + kOffRing + (uint32_t)(v % kRing) * kTile, kHalf, 1024);
                     for (int t = 0; t < nt; ++t) {
                         const uint32_t pt = tmem + kColS + 128u * t;
-                        ok = mbar_wait(&p_full[t], (ps >> t) & 1u) && (t || landed(v));
+                        // everything the tile's two products need is waited for before the
+                        // first, so that nothing comes between them on the pipe
+                        ok = (t || (landed(v) && (s + 1 == n || landed(v + 1)))) && mbar_wait(&p_full[t], (ps >> t) & 1u);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u, vd + (uint32_t)kk * 128u, id_o,
-                                        (s > 0 || kk > 0));
+                            mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
+                                        vd + (uint32_t)kk * 128u, id_o, (s > 0 || kk > 0));
                         ps ^= 1u << t;
-                        if (s == n - 1) mma_commit(&o_done[t]);
-                        if (t == nt - 1) mma_commit(&empty[v % kRing]);
-                        if (s + 1 < n) {
-                            if (t == 0 && !landed(v + 1)) {
-                                ok = false;
-                                break;
-                            }
-                            scores(t, v + 1);
-                            if (s + 2 == n) mma_commit(&q_empty[t]);
-                            if (t == nt - 1) mma_commit(&empty[(v + 1) % kRing]);
+                        if (s + 1 < n) scores(t, v + 1);
+                        if (s + 2 == n) mma_commit(&q_empty[t]);
+                        if (s + 1 == n) mma_commit(&o_done[t]);
+                        if (t == nt - 1) {
+                            mma_commit(&empty[v % kRing]);
+                            if (s + 1 < n) mma_commit(&empty[(v + 1) % kRing]);
                         }
                     }
                 }
@@ -444,9 +446,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     break;
                 }
                 tc_fence_after();
-                float x[128];
+                float x[128], ls = lsr;
                 tmem_ld128(ts, x);
-                float ls = lsr;
                 if constexpr (kExtra) {
                     ls = 1.f;
                     const float cap_in = a.softcap > 0.f ? 2.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
@@ -460,11 +461,12 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         for (int k = 0; k < 128; ++k) x[k] *= lsr;
                     }
                     if (a.loc || a.snk) {
-                        const int64_t word = (int64_t)seq * a.words + (key0 >> 5);
+                        const int word = key0 >> 5;
+                        const int64_t at = (int64_t)seq * a.words + word;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const bool in = (key0 >> 5) + q < a.words;
-                            const uint32_t lw = a.loc && in ? a.loc[word + q] : 0u, sw = a.snk && in ? a.snk[word + q] : 0u;
+                            const bool in = word + q < a.words;
+                            const uint32_t lw = a.loc && in ? a.loc[at + q] : 0u, sw = a.snk && in ? a.snk[at + q] : 0u;
                             if ((lw | sw) == 0u) continue;   // warp-uniform
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
@@ -491,20 +493,36 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     for (int k = 0; k < 128; ++k)
                         if (k < l) x[k] = -INFINITY;
                 }
-                auto maximum = [&]() {
-                    float mx[8];
+                float mx[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        mx[i] = fmaxf(x[i], x[i + 8]);
+                for (int i = 0; i < 8; ++i) {
+                    mx[i] = fmaxf(x[i], x[i + 8]);
 #pragma unroll
-                        for (int q = 1; q < 8; ++q) mx[i] = max3f(mx[i], x[i + 16 * q], x[i + 16 * q + 8]);
+                    for (int q = 1; q < 8; ++q) mx[i] = max3f(mx[i], x[i + 16 * q], x[i + 16 * q + 8]);
+                }
+                const float top = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ls;
+                const bool raise = top > m_run + kLazy;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? ex2(m_run - top) : 1.f;
+                    if (s > 0) {
+                        // the scores of this tile being done, so is the product of the one before: O stands still
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            float o[16];
+                            tmem_ld16(to + 16u * c, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tmem_st16(to + 16u * c, o);
+                        }
                     }
-                    return max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ls;
-                };
-                // weights of 32 keys against the running maximum, in 16 bits, and their sum
-                auto weights = [&](int c, uint32_t* pk, float2& sum) {
-                    const float2 sc = make_float2(ls, ls), nm = make_float2(m_neg, m_neg);
-                    float2 acc[2] = {};
+                    if (raise) l_run *= f, m_run = top, m_neg = -top;
+                }
+                // weights against the running maximum, in 16 bits, and their sum
+                const float2 sc = make_float2(ls, ls), nm = make_float2(m_neg, m_neg);
+                float2 acc[2] = {};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int k = 32 * c + 2 * e;
@@ -513,60 +531,18 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         pk[e] = kInt4 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
                         acc[e & 1] = __fadd2_rn(acc[e & 1], z);
                     }
-                    sum = __fadd2_rn(acc[0], acc[1]);
-                };
-                // the scores of this tile being done, so is the product of the one before: O stands still
-                auto rescale = [&](float f) {
-#pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        float o[16];
-                        tmem_ld16(to + 16u * c, o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= f;
-                        tmem_st16(to + 16u * c, o);
-                    }
-                };
-                uint32_t pk[2][16];
-                float2 sum[4];
-                if constexpr (kInt4) {   // no registers to spare for weights that may be taken twice
-                    const float top = maximum();
-                    const bool raise = top > m_run + kLazy;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float f = raise ? ex2(m_run - top) : 1.f;
-                        if (s > 0) rescale(f);
-                        if (raise) l_run *= f, m_run = top, m_neg = -top;
-                    }
-                    weights(0, pk[0], sum[0]);
-                    tmem_st16_async(ts, pk[0]);
-                    weights(1, pk[1], sum[1]);
-                } else {
-                    if (s == 0) {
-                        const float top = maximum();
-                        if (top > -INFINITY) m_run = top, m_neg = -top;
-                    }
-                    weights(0, pk[0], sum[0]);
-                    weights(1, pk[1], sum[1]);
-                    if (s > 0) {
-                        const float top = maximum();
-                        const bool raise = top > m_run + kLazy;
-                        if (__any_sync(0xffffffffu, raise)) {
-                            const float f = raise ? ex2(m_run - top) : 1.f;
-                            rescale(f);
-                            if (raise) l_run *= f, m_run = top, m_neg = -top;
-                            weights(0, pk[0], sum[0]);
-                            weights(1, pk[1], sum[1]);
-                        }
-                    }
+                    tmem_st16_async(ts + 16u * c, pk);
                 }
+                const float2 all = __fadd2_rn(acc[0], acc[1]);
+                l_run += all.x + all.y;
                 // keys nobody sees: whatever their slots held is not used.  Both row
                 // tiles write the same zeros, each before its own product.
                 if (!kInt4 && (key0 < klo || key0 + 128 > khi)) {
-                    const int vx = 2 * g + 1;
+                    const int vx = 2 * g + 1, key = key0 + m;
                     if (!warp_wait(&full[vx % kRing], (uint32_t)(vx / kRing) & 1u)) {
                         ok = false;
                         break;
                     }
-                    const int key = key0 + m;
                     if (key < klo || key >= khi) {
                         const uint32_t d = sbase + kOffRing + (uint32_t)(vx % kRing) * kTile + (uint32_t)m * 128u;
 #pragma unroll
@@ -577,20 +553,10 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                // (P handed over in halves was slower: the issuing thread held the pipe
-                // for the second half while the other row tile had products to run)
-                if (!kInt4) tmem_st16_async(ts, pk[0]);
-                tmem_st16_async(ts + 16u, pk[1]);
-                weights(2, pk[0], sum[2]);
-                tmem_st16_async(ts + 32u, pk[0]);
-                weights(3, pk[1], sum[3]);
-                tmem_st16_async(ts + 48u, pk[1]);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[t]);
-                const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-                l_run += all.x + all.y;
             }
             if (!ok) break;
             // ---- the next run's Q, so that its first scores are on their way meanwhile
