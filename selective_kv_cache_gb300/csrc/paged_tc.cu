@@ -441,6 +441,16 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             float m_run = -INFINITY, m_neg = 0.f, l_run = 0.f;
             for (int s = 0; s < n; ++s, ++g, ++tile) {
                 const int key0 = key_base + 128 * s;
+                uint32_t lw[4] = {0u, 0u, 0u, 0u}, sw[4] = {0u, 0u, 0u, 0u};   // mask words, under the wait
+                if (kExtra && (a.loc || a.snk)) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int word = (key0 >> 5) + q;
+                        if (word >= a.words) continue;
+                        if (a.loc) lw[q] = a.loc[(int64_t)seq * a.words + word];
+                        if (a.snk) sw[q] = a.snk[(int64_t)seq * a.words + word];
+                    }
+                }
                 if (!warp_wait(&s_full[t], (uint32_t)tile & 1u)) {
                     ok = false;
                     break;
@@ -461,17 +471,20 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         for (int k = 0; k < 128; ++k) x[k] *= lsr;
                     }
                     if (a.loc || a.snk) {
-                        const int word = key0 >> 5;
-                        const int64_t at = (int64_t)seq * a.words + word;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const bool in = word + q < a.words;
-                            const uint32_t lw = a.loc && in ? a.loc[at + q] : 0u, sw = a.snk && in ? a.snk[at + q] : 0u;
-                            if ((lw | sw) == 0u) continue;   // warp-uniform
+                            // the words are the same for every row: words with no bit set cost
+                            // nothing, wholly local ones an addition a key
+                            if ((lw[q] | sw[q]) == 0u) continue;
+                            if (sw[q] == 0u && lw[q] == 0xffffffffu) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) x[32 * q + k] += a.alpha * kLog2e;
+                                continue;
+                            }
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
-                                float b = ((lw >> k) & 1u) ? a.alpha * kLog2e : 0.f;
-                                b += ((sw >> k) & 1u) ? a.beta * kLog2e : 0.f;
+                                float b = ((lw[q] >> k) & 1u) ? a.alpha * kLog2e : 0.f;
+                                b += ((sw[q] >> k) & 1u) ? a.beta * kLog2e : 0.f;
                                 x[32 * q + k] += b;
                             }
                         }
@@ -623,56 +636,62 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         reg_dec<88>();
         // -------------------------------------------------------------- 4-bit tiles to fp16
         // thread (key, q): keys ct / 4 + 32 i, the 16 bytes that hold dims 8 q..
-        // of each 32-dim block; the quad's first copies the key's scale pairs
+        // of each 32-dim block; the quad copies the key's scale pairs
         const int ct = threadIdx.x - 384, q = ct & 3, kr = ct >> 2;
-        const int in_page = (1 << a.p.page_shift) - 1, mb = 4 * n_groups;
+        const int mb = 4 * n_groups, lg = n_groups >> 1;   // log2(n_groups) for 1, 2, 4
         const uint32_t stage0 = sbase + kOffStage;
         int x = 0, y = 0;        // tiles converted, tiles asked for
         int s = 0;               // unit being asked for, of run w
-        int id[4];               // its pages; -1: the key is not seen
+        int id[4];               // pages of the next unit's keys; -1: the key is not seen
+        int64_t at[4];           // code bytes from slot 0 of page 0 of the unit being asked for
+        int64_t head = 0;        // and from there to the run's head
         auto locate = [&]() {
             if (!w.live()) return;
             const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
+            const int key0 = first_key(w, s) + kr, klo = w.it.klo, khi = w.it.khi;
+            head = (int64_t)w.h * a.p.head_stride * 64;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int key = first_key(w, s) + kr + 32 * i;
+                const int key = key0 + 32 * i;
                 id[i] = -1;
-                if (key >= w.it.klo && key < w.it.khi) id[i] = table[key >> a.p.page_shift] & 0x7fffffff;   // checked when used
+                if (key >= klo && key < khi) id[i] = table[key >> a.p.page_shift] & 0x7fffffff;   // checked when used
             }
         };
-        // ask for the next tile (K then V of a unit); a key nobody sees gets zeros:
-        // 0 * (c - 8) + 0
+        // ask for the next tile (K, then V at the same places); a key nobody sees
+        // gets zeros: 0 * (c - 8) + 0
         auto ask = [&]() {
-            if (w.live()) {
+            if ((y & 1) || w.live()) {
                 const bool is_v = y & 1;
-                const int key0 = first_key(w, s), head = w.h;
-                const uint32_t d = stage0 + (uint32_t)(y % kStaged) * kStage;
+                if (!is_v) {
+                    const int page_b = (int)a.p.page_stride * 64, slot_b = (int)a.p.slot_stride * 64;   // below 2^31 (checked)
+                    const int slot = (first_key(w, s) + kr) & ((1 << a.p.page_shift) - 1), in_page = (1 << a.p.page_shift) - 1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = kr + 32 * i;
-                    const uint32_t dc = d + 64u * k + 16u * q, dm = d + kStageCodes + (uint32_t)(mb * k);
-                    if (id[i] < 0) {
-                        sts16(dc, make_uint4(0u, 0u, 0u, 0u));
-                        if (q < n_groups) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dm + 4u * q), "r"(0u) : "memory");
-                        continue;
-                    }
-                    const int64_t row = paged_row(a.p, paged_id(a.p, id[i]), (key0 + k) & in_page, head);
-                    copy_async<16>(dc, (is_v ? a.p.v : a.p.k) + row * 64 + 16 * q);
-                    if (q == 0) {
-                        const uint8_t* mp = (is_v ? a.p.vs : a.p.ks) + row * mb;
-                        if (n_groups == 4) copy_async<16>(dm, mp);
-                        else if (n_groups == 2) copy_async<8>(dm, mp);
-                        else copy_async<4>(dm, mp);
-                    }
-                }
-                ++y;
-                if (is_v) {
+                    for (int i = 0; i < 4; ++i)
+                        at[i] = id[i] < 0 ? -1 : head + (int64_t)paged_id(a.p, id[i]) * page_b +
+                                                     (int64_t)((slot + 32 * i) & in_page) * slot_b;
                     if (++s == w.n) {
                         s = 0;
                         advance();
                     }
                     locate();
                 }
+                const uint8_t* codes = (is_v ? a.p.v : a.p.k) + 16 * q;
+                const uint8_t* pairs = is_v ? a.p.vs : a.p.ks;
+                const uint32_t d = stage0 + (uint32_t)(y % kStaged) * kStage;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = kr + 32 * i;
+                    const uint32_t dc = d + 64u * k + 16u * q, dm = d + kStageCodes + (uint32_t)(mb * k);
+                    if (at[i] < 0) {
+                        sts16(dc, make_uint4(0u, 0u, 0u, 0u));
+                        if (q < n_groups) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dm + 4u * q), "r"(0u) : "memory");
+                        continue;
+                    }
+                    copy_async<16>(dc, codes + at[i]);
+                    // the key's pairs, a word for each of the quad's first lanes
+                    if (q < n_groups) copy_async<4>(dm + 4u * q, pairs + (at[i] >> (4 - lg)) + 4 * q);
+                }
+                ++y;
             }
             copy_commit();
         };
