@@ -581,10 +581,10 @@ kvr_status kvr_profile_read(kvr_cache* c, double* ms, int64_t* launches, int32_t
  *             pairs (s, o) of a row are at k_scale + row * 4 * (128 / group)
  *             bytes, group by group.  The row is 32 two-byte units of four
  *             dims each, dim 4u + e in bits 4e..4e+3 of unit u; unit u is
- *             stored at place 4 * (u % 8) + u / 8.  Values are held to the
- *             range of fp16 (larger magnitudes saturate at 65504).
+ *             stored at place 4 * (u % 8) + u / 8.  Magnitudes saturate at
+ *             2^15 (fp16 holds the scales and, in attention, the values).
  * page_size is 16, 32, 64, 128 or 256; n_q_heads / n_kv_heads is at most 16;
- * page and slot strides are at most 2^21 rows.
+ * page and slot strides are at most 2^21 rows, head strides 2^31.
  * k, v and the scale arrays are 16-byte aligned.
  * ------------------------------------------------------------------------- */
 #define KVR_INT4 2   /* page format only (see kvr_dtype for the others) */
@@ -642,7 +642,7 @@ typedef struct {
  *               q_rows itself when that is packed too.
  * The rotation is in fp32, each product and sum rounded on its own, and
  * rounded once to the page format.  KVR_INT4, per group of fp32 values x (after the
- * rotation): o = fp16(min x), s = fp16((max x - min x) * fp32(1/15)), code =
+ * rotation, brought into +-2^15): o = fp16(min x), s = fp16((max x - min x) * fp32(1/15)), code =
  * clamp(rint((x - o) * (1/s)), 0, 15), 0 when s = 0.
  * Positions of a sequence ascend; a row that does not lie above the row
  * before it, or whose position is outside the table, the rope table or the
@@ -671,9 +671,9 @@ kvr_status kvr_paged_read(const kvr_pages* p, int32_t n_rows, const int32_t* cu_
  *          j in [max(0, begin_r), min(end_r, kv_len_b)).
  * A row that sees no key gets zeros.  Positions may come in any order and
  * repeat; g_r sets the default end and the distance |g_r - j|, nothing else.
- * Keys outside every row's interval, and past kv_len, are never used, whatever
- * their slots hold; a non-finite K or V row inside one row's interval may
- * reach the other rows of that sequence.
+ * Keys before the first and past the last key that any of a sequence's rows in
+ * the call sees, and past kv_len, are never used, whatever their slots hold; a
+ * non-finite K or V row between those may reach any of that sequence's rows.
  *   max_rows    upper bound of the rows of any sequence (1 for a decode
  *               step); rows past it are not computed and reported.
  *   q, out      device [n_rows][n_q_heads][head_dim], row strides in elements.

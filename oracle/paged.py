@@ -24,7 +24,7 @@ def rotate(x: np.ndarray, cs: np.ndarray) -> np.ndarray:
 
 def quantise(x: np.ndarray, group: int):
     """Codes uint8 [..., dh] and fp16 (scale, offset) [..., dh/group, 2] of fp32 x."""
-    g = np.clip(x, np.float32(-65504), np.float32(65504)).reshape(*x.shape[:-1], -1, group)
+    g = np.clip(x, np.float32(-32768), np.float32(32768)).reshape(*x.shape[:-1], -1, group)
     lo, hi = g.min(-1), g.max(-1)
     s = ((hi - lo) * np.float32(1.0 / 15.0)).astype(np.float16)
     o = lo.astype(np.float16)

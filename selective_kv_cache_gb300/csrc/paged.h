@@ -147,11 +147,12 @@ __device__ __forceinline__ int paged_seq_rows(const PagedView& p, const PagedRow
     return e - a;
 }
 
-// Keys a row of sequence b may see: [lo, hi).
+// Keys a row of sequence b may see: [lo, hi), both brought into [0, kv_len] so
+// that differences with key numbers stay in range whatever the arrays hold.
 __device__ __forceinline__ void paged_interval(const PagedAttn& a, int row, int kv_len, int* lo, int* hi) {
     const int g = a.r.pos[row];
-    *lo = a.key_begin ? max(a.key_begin[row], 0) : 0;
-    *hi = min(a.key_end ? a.key_end[row] : (g < 0x7fffffff ? g + 1 : g), kv_len);
+    *lo = a.key_begin ? min(max(a.key_begin[row], 0), kv_len) : 0;
+    *hi = max(min(a.key_end ? a.key_end[row] : (g < 0x7fffffff ? g + 1 : g), kv_len), 0);
 }
 __device__ __forceinline__ int paged_kv_len(const PagedView& p, int b) {
     return min(max(p.kv_len[b], 0), p.capacity);

@@ -42,8 +42,8 @@ kvr_status check_pages(const kvr_pages* p) {
         return fail(KVR_EUNSUPPORTED, "pages: more than 65535 heads, 2^20 sequences or 2^30 positions of a sequence");
     if (p->page_stride < 1 || p->head_stride < 1 || p->slot_stride < 1)
         return fail(KVR_EINVAL, "pages: strides must be positive");
-    if (p->page_stride > (int64_t(1) << 21) || p->slot_stride > (int64_t(1) << 21) || p->head_stride > (int64_t(1) << 40))
-        return fail(KVR_EUNSUPPORTED, "pages: page and slot strides above 2^21 rows");
+    if (p->page_stride > (int64_t(1) << 21) || p->slot_stride > (int64_t(1) << 21) || p->head_stride > (int64_t(1) << 31))
+        return fail(KVR_EUNSUPPORTED, "pages: page and slot strides above 2^21 rows or head strides above 2^31");
     if (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v))
         return fail(KVR_EINVAL, "pages: k and v must be non-NULL and 16-byte aligned");
     if (p->format == KVR_INT4 && (!p->k_scale || !p->v_scale || !aligned16(p->k_scale) || !aligned16(p->v_scale)))

@@ -6,39 +6,24 @@
 // pages).  Read is the inverse of the write.  Both move each byte once and do
 // a few flops on it: HBM-bound for prompts, launch-bound for decode steps.
 //
-// A CTA takes a few packed rows (up to 8, so that models of few heads fill its
-// threads too): a warp per row finds the row's sequence and slot, then all
-// threads walk the rows' (row, head) units.  Sixteen or eight threads share a
-// unit and own whole rotation pairs, so nothing is exchanged between threads
-// but the extrema of a 4-bit group.  Rotation: fp32, products and sum rounded separately, so
+// A CTA takes a few packed rows, about three (row, head) units per group of
+// eight or sixteen threads: one warp finds the rows' sequences and slots (three
+// dependent loads) while every thread already has its units' rows on their
+// way.  Threads of a unit own whole rotation pairs, so nothing is exchanged
+// between them but the extrema of a 4-bit group.
+// Rotation: fp32, products and sum rounded separately, so
 // that a plain elementwise evaluation gives the same bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "paged.h"
 
 namespace kvr {
 namespace {
 
-constexpr int kRowThreads = 256, kMaxRows = 8;
-
-// Sequence that owns row r: the number of ends cu[b+1] <= r.  Every lane of
-// the warp gets it; -1 when r lies past the last sequence or cu is malformed
-// around it.
-__device__ __forceinline__ int owner(const PagedView& p, const PagedRows& rr, int r) {
-    const int lane = threadIdx.x & 31;
-    int b = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const bool past = b0 + lane < p.batch && rr.cu[b0 + lane + 1] <= r;
-        b += __popc(__ballot_sync(0xffffffffu, past));
-    }
-    if (b >= p.batch) return -1;
-    if (r < rr.cu[b]) {
-        if (threadIdx.x == 0) paged_err(p.err, DEV_ERR_INDEX, r);
-        return -1;
-    }
-    return b;
-}
+constexpr int kRowThreads = 128, kMaxRows = 16, kBatch = 3;   // units a thread has in flight
 
 __device__ __forceinline__ void unpack8(uint4 u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -87,79 +72,110 @@ struct Pair<float> {
     }
 };
 
-// Slots of the CTA's rows in shared memory: the page row of head 0 and the
-// position, page row -1 for a row that is not to be touched.  kAppend checks
-// what a write needs besides.
+// Slots of the CTA's rows in shared memory, by warp 0, lane i for row i: the page
+// row of head 0 and the position, page row -1 for a row that is not to be
+// touched.  A row's sequence is the number of ends cu[b + 1] <= r; kAppend checks
+// what a write needs besides.  The caller synchronises.
 struct RowSlot {
     int64_t at;
     int g;
 };
 template <bool kAppend>
-__device__ __forceinline__ void find_slots(const PagedRowIo& a, RowSlot* slots, int rows) {
-    for (int i = threadIdx.x >> 5; i < rows; i += kRowThreads / 32) {   // a warp per row
-        const int r = blockIdx.x * a.rows_per_block + i, lane = threadIdx.x & 31;
-        const int b = r < a.r.n_rows ? owner(a.p, a.r, r) : -1;
-        int64_t at = -1;
-        int g = 0;
-        if (b >= 0) {
-            g = a.r.pos[r];
-            int bad = 0;
-            if (g < 0 || g >= a.p.capacity || (kAppend && a.rope && g >= a.rope_len)) bad = DEV_ERR_INDEX;
-            else if (kAppend && r > a.r.cu[b] && a.r.pos[r - 1] >= g) bad = DEV_ERR_ORDER;
-            int id = 0;
-            if (!bad) {
-                id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];
-                if ((unsigned)id >= (unsigned)a.p.n_pages) bad = DEV_ERR_INDEX;
-            }
-            if (!bad) at = paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
-            else if (lane == 0) paged_err(a.p.err, bad, g);
+__device__ __forceinline__ void find_slots(const PagedRowIo& a, RowSlot* slots) {
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x, r0 = blockIdx.x * a.rows_per_block, r = r0 + lane;
+    int b = 0;
+    for (int b0 = 0; b0 < a.p.batch; b0 += 32) {
+        const int end = b0 + lane < a.p.batch ? a.r.cu[b0 + lane + 1] : 0x7fffffff;
+        for (int i = 0; i < a.rows_per_block; ++i) {
+            const int n = __popc(__ballot_sync(0xffffffffu, end <= r0 + i));
+            if (lane == i) b += n;
         }
-        if (lane == 0) slots[i] = RowSlot{at, g};
     }
-    __syncthreads();
+    if (lane >= a.rows_per_block) return;
+    int64_t at = -1;
+    int g = 0;
+    if (r < a.r.n_rows && b < a.p.batch) {   // else behind the last sequence: left alone
+        const int first = a.r.cu[b];
+        g = a.r.pos[r];
+        int bad = 0;
+        if (first < 0 || r < first || g < 0 || g >= a.p.capacity || (kAppend && a.rope && g >= a.rope_len)) bad = DEV_ERR_INDEX;
+        else if (kAppend && r > first && a.r.pos[r - 1] >= g) bad = DEV_ERR_ORDER;
+        int id = 0;
+        if (!bad) {
+            id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];
+            if ((unsigned)id >= (unsigned)a.p.n_pages) bad = DEV_ERR_INDEX;
+        }
+        if (bad) paged_err(a.p.err, bad, g);
+        else at = paged_row(a.p, id, g & ((1 << a.p.page_shift) - 1), 0);
+    }
+    slots[lane] = RowSlot{at, g};
+}
+
+// Unit x of the CTA: row i of its rows, head u (K heads, V heads, query heads).
+struct RowUnit {
+    int i, u;
+    int64_t r;
+    bool live;
+};
+__device__ __forceinline__ RowUnit unit_of(const PagedRowIo& a, int x) {
+    const int total = a.rows_per_block * a.units, y = min(x, total - 1), i = y / a.units;
+    const int64_t r = (int64_t)blockIdx.x * a.rows_per_block + i;
+    return RowUnit{i, y - i * a.units, r, x < total && r < a.r.n_rows};
+}
+__device__ __forceinline__ const uint8_t* unit_src(const PagedRowIo& a, const RowUnit& x, int bytes) {
+    const int H = a.p.n_kv_heads;
+    return x.u < H ? a.k_in + x.r * a.k_stride + (int64_t)x.u * bytes
+         : x.u < 2 * H ? a.v_in + x.r * a.v_stride + (int64_t)(x.u - H) * bytes
+                       : a.q_in + x.r * a.q_stride + (int64_t)(x.u - 2 * H) * bytes;
 }
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(PagedRowIo a) {
     constexpr int E = Pair<T>::E, VT = DH / 2 / E;   // elements per vector, threads per unit
-    constexpr int kBytes = DH * (int)sizeof(T);
+    constexpr int kBytes = DH * (int)sizeof(T), kStep = kRowThreads / VT;
     __shared__ RowSlot slots[kMaxRows];
-    find_slots<true>(a, slots, a.rows_per_block);
-    const int v = threadIdx.x % VT, H = a.p.n_kv_heads;
+    const int v = threadIdx.x % VT, H = a.p.n_kv_heads, total = a.rows_per_block * a.units;
     float2 cs[E];   // of the row in hand
     int in_hand = -1;
-    for (int x = threadIdx.x / VT; x < a.rows_per_block * a.units; x += kRowThreads / VT) {
-        const int i = x / a.units, u = x - i * a.units;
-        const RowSlot slot = slots[i];
-        if (slot.at < 0) continue;
-        const int64_t r = (int64_t)blockIdx.x * a.rows_per_block + i;
-        const uint8_t* src;
-        uint8_t* dst;
-        if (u < H) {
-            src = a.k_in + r * a.k_stride + (int64_t)u * kBytes;
-            dst = a.p.k + (slot.at + u * a.p.head_stride) * kBytes;
-        } else if (u < 2 * H) {
-            src = a.v_in + r * a.v_stride + (int64_t)(u - H) * kBytes;
-            dst = a.p.v + (slot.at + (u - H) * a.p.head_stride) * kBytes;
-        } else {
-            src = a.q_in + r * a.q_stride + (int64_t)(u - 2 * H) * kBytes;
-            dst = a.q_out + (r * a.n_q_heads + u - 2 * H) * kBytes;
-        }
-        uint4 lo = reinterpret_cast<const uint4*>(src)[v], hi = reinterpret_cast<const uint4*>(src)[v + VT];
-        if (a.rope && (u < H || u >= 2 * H)) {
-            if (i != in_hand) {
-                in_hand = i;
+    for (int x0 = 0; x0 < total; x0 += kBatch * kStep) {
+        uint4 lo[kBatch], hi[kBatch];
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float4 w = *reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * (DH / 2) + v * E + e);
-                    cs[e] = make_float2(w.x, w.y);
-                    cs[e + 1] = make_float2(w.z, w.w);
-                }
-            }
-            Pair<T>::rotate(lo, hi, cs);
+        for (int j = 0; j < kBatch; ++j) {
+            const RowUnit x = unit_of(a, x0 + j * kStep + threadIdx.x / VT);
+            if (!x.live) continue;
+            const uint4* src = reinterpret_cast<const uint4*>(unit_src(a, x, kBytes));
+            lo[j] = src[v];
+            hi[j] = src[v + VT];
         }
-        reinterpret_cast<uint4*>(dst)[v] = lo;
-        reinterpret_cast<uint4*>(dst)[v + VT] = hi;
+        if (x0 == 0) {
+            find_slots<true>(a, slots);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const RowUnit x = unit_of(a, x0 + j * kStep + threadIdx.x / VT);
+            const RowSlot slot = slots[x.i];
+            if (!x.live || slot.at < 0) continue;
+            if (a.rope && (x.u < H || x.u >= 2 * H)) {
+                if (x.i != in_hand) {
+                    in_hand = x.i;
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float4 w = *reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * (DH / 2) + v * E + e);
+                        cs[e] = make_float2(w.x, w.y);
+                        cs[e + 1] = make_float2(w.z, w.w);
+                    }
+                }
+                Pair<T>::rotate(lo[j], hi[j], cs);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(
+                x.u < H ? a.p.k + (slot.at + x.u * a.p.head_stride) * kBytes
+                : x.u < 2 * H ? a.p.v + (slot.at + (x.u - H) * a.p.head_stride) * kBytes
+                              : a.q_out + (x.r * a.n_q_heads + x.u - 2 * H) * kBytes);
+            dst[v] = lo[j];
+            dst[v + VT] = hi[j];
+        }
     }
 }
 
@@ -177,27 +193,36 @@ __device__ __forceinline__ void extremum8(float& lo, float& hi) {
 
 template <int NG>
 __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) {
-    constexpr int kJoin = 4 / NG;
+    constexpr int kJoin = 4 / NG, kStep = kRowThreads / 8;
     __shared__ RowSlot slots[kMaxRows];
-    find_slots<true>(a, slots, a.rows_per_block);
-    const int v = threadIdx.x % 8, H = a.p.n_kv_heads;
-    const int total = a.rows_per_block * a.units;
+    const int v = threadIdx.x % 8, H = a.p.n_kv_heads, total = a.rows_per_block * a.units;
     // every thread of a warp runs the same rounds: the shuffles below need
     // the whole warp
-    for (int x0 = 0; x0 < total; x0 += kRowThreads / 8) {
-        const int n = x0 + threadIdx.x / 8, ri = min(n, total - 1) / a.units, u = n - ri * a.units;
-        const RowSlot slot = slots[ri];
-        const int64_t r = (int64_t)blockIdx.x * a.rows_per_block + ri, row = slot.at;
-        const bool live = n < total && row >= 0, is_q = u >= 2 * H, is_v = !is_q && u >= H;
-        const uint8_t* src = a.k_in;
-        if (live)
-            src = is_q ? a.q_in + r * a.q_stride + (int64_t)(u - 2 * H) * 256
-                       : (is_v ? a.v_in + r * a.v_stride + (int64_t)(u - H) * 256
-                               : a.k_in + r * a.k_stride + (int64_t)u * 256);
+    for (int x0 = 0; x0 < total; x0 += kBatch * kStep) {
+    uint2 raw[kBatch][4];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+        const RowUnit un = unit_of(a, x0 + j * kStep + threadIdx.x / 8);
+        const uint8_t* src = unit_src(a, un, 256) + 8 * v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            raw[j][i] = un.live ? *reinterpret_cast<const uint2*>(src + 64 * i) : make_uint2(0u, 0u);
+    }
+    if (x0 == 0) {
+        find_slots<true>(a, slots);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+        const RowUnit un = unit_of(a, x0 + j * kStep + threadIdx.x / 8);
+        const RowSlot slot = slots[un.i];
+        const int u = un.u;
+        const int64_t r = un.r, row = slot.at;
+        const bool live = un.live && row >= 0, is_q = u >= 2 * H, is_v = !is_q && u >= H;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint2 w = live ? *reinterpret_cast<const uint2*>(src + 64 * i + 8 * v) : make_uint2(0u, 0u);
+            const uint2 w = raw[j][i];
             x[4 * i] = __uint_as_float(w.x << 16);
             x[4 * i + 1] = __uint_as_float(w.x & 0xffff0000u);
             x[4 * i + 2] = __uint_as_float(w.y << 16);
@@ -224,7 +249,7 @@ __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) 
         if (__all_sync(0xffffffffu, !live || is_q)) continue;   // nothing to quantise in this warp
         float lo[NG], hi[NG];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -65504.f), 65504.f);   // fp16's range
+        for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -32768.f), 32768.f);   // 15 s + o stays in fp16's range
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             lo[n] = hi[n] = x[4 * kJoin * n];
@@ -263,51 +288,76 @@ __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) 
         *reinterpret_cast<uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v) =
             make_uint2(unit[0] | (unit[1] << 16), unit[2] | (unit[3] << 16));
     }
+    }
 }
 
 // NG = 0: rows copied as they are (VT 16-byte vectors); else 4-bit rows.  K heads first, then V heads;
 // when only one of the two is wanted, its heads alone.
 template <int VT, int NG>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(PagedRowIo a) {
-    constexpr int kPerUnit = NG ? 8 : VT;
+    constexpr int kPerUnit = NG ? 8 : VT, kStep = kRowThreads / kPerUnit, MB = NG ? 4 * NG : 4;
     __shared__ RowSlot slots[kMaxRows];
-    find_slots<false>(a, slots, a.rows_per_block);
-    const int v = threadIdx.x % kPerUnit, H = a.p.n_kv_heads;
-    for (int x = threadIdx.x / kPerUnit; x < a.rows_per_block * a.units; x += kRowThreads / kPerUnit) {
-        const int i = x / a.units, u = x - i * a.units;
-        const int64_t row = slots[i].at;
-        if (row < 0) continue;
-        const int64_t r = (int64_t)blockIdx.x * a.rows_per_block + i;
-        const bool is_v = u >= H || !a.k_out;
-        const int h = u >= H ? u - H : u;
-        uint8_t* dst = is_v ? a.v_out + r * a.v_stride : a.k_out + r * a.k_stride;
-        const int64_t at = row + h * a.p.head_stride;
-        if constexpr (NG == 0) {
-            reinterpret_cast<uint4*>(dst + (int64_t)h * VT * 16)[v] =
-                reinterpret_cast<const uint4*>((is_v ? a.p.v : a.p.k) + at * VT * 16)[v];
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v);
-            const __half2* meta = reinterpret_cast<const __half2*>((is_v ? a.p.vs : a.p.ks) + at * (4 * NG));
+    const int v = threadIdx.x % kPerUnit, H = a.p.n_kv_heads, total = a.rows_per_block * a.units;
+    find_slots<false>(a, slots);
+    __syncthreads();
+    for (int x0 = 0; x0 < total; x0 += kBatch * kStep) {
+        uint4 w[kBatch];
+        uint32_t meta[kBatch][NG ? NG : 1];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float2 so = __half22float2(meta[g * NG / 4]);
-                const uint32_t unit = (g < 2 ? w.x : w.y) >> (16 * (g & 1));
-                float y[4];
+        for (int j = 0; j < kBatch; ++j) {
+            const RowUnit x = unit_of(a, x0 + j * kStep + threadIdx.x / kPerUnit);
+            const int64_t row = slots[x.i].at;
+            if (!x.live || row < 0) continue;
+            const bool is_v = x.u >= H || !a.k_out;
+            const int64_t at = row + (x.u >= H ? x.u - H : x.u) * a.p.head_stride;
+            if constexpr (NG == 0) {
+                w[j] = reinterpret_cast<const uint4*>((is_v ? a.p.v : a.p.k) + at * VT * 16)[v];
+            } else {
+                const uint2 c = *reinterpret_cast<const uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v);
+                w[j].x = c.x;
+                w[j].y = c.y;
+                const uint8_t* m = (is_v ? a.p.vs : a.p.ks) + at * MB;
+                if constexpr (NG == 4) {
+                    const uint4 z = *reinterpret_cast<const uint4*>(m);
+                    meta[j][0] = z.x, meta[j][1] = z.y, meta[j][2] = z.z, meta[j][3] = z.w;
+                } else if constexpr (NG == 2) {
+                    const uint2 z = *reinterpret_cast<const uint2*>(m);
+                    meta[j][0] = z.x, meta[j][1] = z.y;
+                } else {
+                    meta[j][0] = *reinterpret_cast<const uint32_t*>(m);
+                }
+            }
+        }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = fmaf((float)((unit >> (4 * e)) & 15u), so.x, so.y);
-                *reinterpret_cast<uint2*>(dst + (int64_t)h * 256 + 64 * g + 8 * v) =
-                    make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+        for (int j = 0; j < kBatch; ++j) {
+            const RowUnit x = unit_of(a, x0 + j * kStep + threadIdx.x / kPerUnit);
+            if (!x.live || slots[x.i].at < 0) continue;
+            const bool is_v = x.u >= H || !a.k_out;
+            const int h = x.u >= H ? x.u - H : x.u;
+            uint8_t* dst = is_v ? a.v_out + x.r * a.v_stride : a.k_out + x.r * a.k_stride;
+            if constexpr (NG == 0) {
+                reinterpret_cast<uint4*>(dst + (int64_t)h * VT * 16)[v] = w[j];
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float2 so = __half22float2(*reinterpret_cast<const __half2*>(&meta[j][g * NG / 4]));
+                    const uint32_t unit = (g < 2 ? w[j].x : w[j].y) >> (16 * (g & 1));
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = fmaf((float)((unit >> (4 * e)) & 15u), so.x, so.y);
+                    *reinterpret_cast<uint2*>(dst + (int64_t)h * 256 + 64 * g + 8 * v) =
+                        make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+                }
             }
         }
     }
 }
 
-// Rows of a CTA: as many as keep its threads busy for about one round each,
-// while there are CTAs for every SM.
+// Rows of a CTA: about kBatch units for each group of threads, while there are
+// CTAs for every SM.
 int rows_per_block(int n_rows, int units, int threads_per_unit) {
-    int n = 1;
-    while (n < kMaxRows && 2 * n * units * threads_per_unit <= 2 * kRowThreads && n_rows / (2 * n) >= 2 * kNumSMs) n *= 2;
-    return n;
+    const int want = kBatch * (kRowThreads / threads_per_unit) / units;
+    return std::max(1, std::min(std::min(want, kMaxRows), n_rows / (2 * kNumSMs)));
 }
 
 }  // namespace

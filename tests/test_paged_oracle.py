@@ -39,12 +39,12 @@ def test_quantised_values_are_within_half_a_step(group):
 def test_flat_and_extreme_groups():
     x = np.zeros((3, 1, 128), np.float32)
     x[1] = 7.25
-    x[2, 0, 5] = 1e6    # saturates at fp16's largest
+    x[2, 0, 5] = 1e6    # saturates at 2^15
     code, meta = OP.quantise(x, 64)
     v = OP.values(OP.pack(code), meta, 64)
     np.testing.assert_array_equal(v[0], 0)
     np.testing.assert_array_equal(v[1], 7.25)
-    assert np.isfinite(v).all() and v[2, 0, 5] == v.max()
+    assert np.isfinite(v).all() and v[2, 0, 5] == v.max() and v.max() < 65504
 
 
 def test_rotation_composes_with_the_refresh_oracle():
@@ -109,7 +109,8 @@ BAD_PAGES = [
     (dict(group=32), "EINVAL"), (dict(page_stride=0), "EINVAL"), (dict(head_stride=-1), "EINVAL"),
     (dict(slot_stride=0), "EINVAL"), (dict(k=None), "EINVAL"), (dict(v=A + 8), "EINVAL"),
     (dict(page_table=None), "EINVAL"), (dict(kv_len=None), "EINVAL"), (dict(err=None), "EINVAL"),
-    (dict(page_table=A + 2), "EINVAL"), (dict(batch=1 << 21), "EUNSUPPORTED"), (dict(max_pages=1 << 27), "EUNSUPPORTED"),
+    (dict(page_table=A + 2), "EINVAL"), (dict(batch=1 << 21), "EUNSUPPORTED"), (dict(page_stride=(1 << 21) + 1), "EUNSUPPORTED"),
+    (dict(slot_stride=1 << 22), "EUNSUPPORTED"), (dict(head_stride=1 << 32), "EUNSUPPORTED"), (dict(max_pages=1 << 27), "EUNSUPPORTED"),
     (dict(format=2, group=0, k_scale=A, v_scale=A), "EINVAL"), (dict(format=2, group=16, k_scale=A, v_scale=A), "EINVAL"),
     (dict(format=2, group=32, k_scale=None, v_scale=A), "EINVAL"),
     (dict(format=2, group=32, k_scale=A, v_scale=A + 4), "EINVAL"),
