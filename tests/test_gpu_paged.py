@@ -90,13 +90,14 @@ def test_read_returns_what_the_pages_hold(fmt, dh, group):
 
 
 def test_quantiser_on_flat_extreme_and_non_finite_groups():
-    """A flat group keeps its value, magnitudes saturate at fp16's largest, and
+    """A flat group keeps its value, magnitudes saturate at 2^15, and
     a non-finite element stays within its own group."""
     c = Paged("int4", [8], 1, 128, 16, group=32, fill=False)
     x = torch.randn(8, 1, 128, device="cuda").bfloat16()
     x[0] = 0
     x[1] = 7.25
     x[2, 0, 5] = 3e38
+    x[6, 0] = torch.linspace(0, 4e4, 128).bfloat16()
     x[3, 0, 40] = float("nan")
     x[4, 0, 99] = float("-inf")
     x[5] *= 1e-30
@@ -149,9 +150,14 @@ def test_malformed_row_offsets_touch_nothing_else():
         kvr.kvr_paged_attend(c.p, None, 4, i32(cu), i32([1, 2, 3, 4]), out, out.clone(), ws)
         with pytest.raises(kvr.KvrError):
             kvr.kvr_paged_status(c.p)
-    kvr.kvr_paged_append(c.p, i32([4, 4, 4]), i32([1, 2, 3, 4]), x, x)
-    with pytest.raises(kvr.KvrError):
-        kvr.kvr_paged_status(c.p)
+    for cu in ([4, 4, 4], [-3, -1, -1], [3, 2, 1]):
+        kvr.kvr_paged_append(c.p, i32(cu), i32([1, 2, 3, 4]), x, x)
+        got = torch.full((4, 2, 128), 9.0, device="cuda", dtype=torch.bfloat16)
+        kvr.kvr_paged_read(c.p, i32(cu), i32([1, 2, 3, 4]), got)
+        if cu[0] > 0:
+            with pytest.raises(kvr.KvrError):
+                kvr.kvr_paged_status(c.p)
+        assert torch.all(got == 9.0)
     assert torch.equal(bits(c.k), before)
 
 
@@ -217,7 +223,10 @@ def intervals(kind, rng, pos, L):
         e[6::9] = -3
         return b, e
     a = rng.integers(-5, L + 5, n)
-    return a, a + rng.integers(-3, 200, n)    # any interval, reaching below 0 and past kv_len
+    e = a + rng.integers(-3, 200, n)          # any interval, reaching below 0 and past kv_len,
+    e[0::11], a[5::11] = -2 ** 31, 2 ** 31 - 1          # and the types' ends
+    a[7::11], e[7::11] = -2 ** 31, 2 ** 31 - 1
+    return a, e
 
 
 @pytest.mark.parametrize("fmt,dh,group", ATTEND)
@@ -404,20 +413,56 @@ def test_captured_calls_follow_their_device_arrays(fmt, dh, group):
         pos[:sum(counts)] += 1
 
 
-def test_other_stream_and_two_calls_at_once():
-    """Two attention calls on two streams, each with its own workspace."""
-    c = Paged("bf16", [3000, 800], 4, seed=4)
-    pos = np.array([2999, 799])
-    ref, q, _ = attend_case(c, 16, [1, 1], pos)
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("counts", [[1, 1], [200, 90]])
+def test_other_stream_and_two_calls_at_once(fmt, dh, group, counts):
+    """Attention calls on two streams at once, each with its own workspace."""
+    lens = [3000, 800]
+    c = Paged(fmt, lens, 4, dh, 64, "hnd", group, seed=4)
+    pos = tail(lens, counts)
+    ref, q, _ = attend_case(c, 16, counts, pos)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = []
-    for s in streams:
-        with torch.cuda.stream(s):
-            outs.append(attend_case(c, 16, [1, 1], pos)[0])
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(attend_case(c, 16, counts, pos)[0])
     torch.cuda.synchronize()
+    kvr.kvr_paged_status(c.p)
     for o in outs:
         assert torch.equal(bits(o), bits(ref))
+
+
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+def test_captured_prompt(fmt, dh, group):
+    """Many rows captured once, replayed with other lengths, positions, row
+    counts and an idle sequence; the workspace serves another call in between."""
+    lens = [500, 300, 60]
+    c = Paged(fmt, lens, 2, dh, 32, "nhd", group, seed=14)
+    n = 400
+    q = torch.randn(n, 8, dh, device="cuda").to(c.row_dtype)
+    out = torch.zeros_like(q)
+    cu, pos = i32([0, 200, 350, 400]), i32(tail(lens, [200, 150, 50]))
+    ws = torch.empty(kvr.kvr_paged_workspace_bytes(c.p, 8, n, 256), dtype=torch.uint8, device="cuda")
+    call = lambda: kvr.kvr_paged_attend(c.p, None, 256, cu, pos, q, out, ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for new_lens, counts in [(lens, [200, 150, 50]), ([256, 300, 60], [256, 0, 33]), ([17, 300, 1], [17, 100, 1])]:
+        c.lens = new_lens
+        c.kv_len.copy_(i32(new_lens))
+        cu.copy_(i32(np.concatenate([[0], np.cumsum(counts)])))
+        p = tail(new_lens, counts)
+        pos[:len(p)] = i32(p)
+        out.fill_(7.0)
+        g.replay()
+        kvr.kvr_paged_status(c.p)
+        assert torch.all(out[sum(counts):] == 7.0)
+        check_attend(c, 8, counts, p, out, q)
+        ws.random_(0, 256)
 
 
 def test_binding_refusals():
@@ -529,6 +574,18 @@ def test_answering_after_a_repair(dtype):
 
     check_attend(Twin, m.n_q_heads, [1], np.array([n]), out, qr, alpha=w.alpha, beta=w.beta, loc=mask(lw),
                  snk=mask(sw))
+    # the refreshed rows attend through the pages as kvr_attend does in the cache
+    U = np.sort(np.asarray(s.positions[0]))
+    rows = len(U)
+    qs = torch.randn(rows, m.n_q_heads, m.head_dim, device="cuda").to(m.torch_dtype)
+    po, ca = torch.zeros_like(qs), torch.zeros(rows, m.n_q_heads * m.head_dim, device="cuda", dtype=m.torch_dtype)
+    wide = torch.empty(kvr.kvr_paged_workspace_bytes(p, m.n_q_heads, rows, rows), dtype=torch.uint8, device="cuda")
+    kvr.kvr_paged_attend(p, kvr.score_opts(**opts), rows, i32([0, rows]), i32(U), qs, po, wide)
+    kvr.kvr_paged_status(p)
+    check_attend(Twin, m.n_q_heads, [rows], U, po, qs, alpha=w.alpha, beta=w.beta, loc=mask(lw), snk=mask(sw))
+    kvr.kvr_attend(s.handle, layer, qs, ca)
+    s.sync()
+    check_attend(Twin, m.n_q_heads, [rows], U, ca.view_as(qs), qs, alpha=w.alpha, beta=w.beta, loc=mask(lw), snk=mask(sw))
     if dtype == "bf16":
         c4 = Paged("int4", [n], m.n_kv_heads, 128, 64, group=32, fill=False)
         rows = lambda t: t[:, :n].transpose(0, 1).contiguous()  # noqa: E731
