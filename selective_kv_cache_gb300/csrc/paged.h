@@ -10,6 +10,7 @@ namespace kvr {
 enum : int { DEV_ERR_ORDER = 8 };   // appended positions of a sequence do not ascend
 
 constexpr int kPagedMaxGroup = 16;   // query heads per K/V head
+constexpr int kPagedInline = 256;    // calls of up to this many items need no plan launch, but in paged_tc.cu
 
 struct PagedView {
     uint8_t* k;
@@ -91,14 +92,14 @@ struct PagedAttn {
 };
 cudaError_t launch_paged_plan(const PagedAttn& a, cudaStream_t s);
 cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cudaStream_t s);
-cudaError_t launch_paged_simt(int format, int head_dim, int group, const PagedAttn& a, cudaStream_t s);
+// Up to 16 rows an item, fp32 pages, units of 32 keys.
+cudaError_t launch_paged_simt(int head_dim, const PagedAttn& a, cudaStream_t s);
 
 // Items of two tiles of 128 / G positions each, bf16 or 4-bit pages, units of 128 keys.
 cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStream_t s, std::string* why);
 // Up to 16 rows (positions * G) an item, bf16 or 4-bit pages.
 cudaError_t launch_paged_decode(int format, int group, const PagedAttn& a, cudaStream_t s);
 int paged_decode_unit(int format);
-int paged_decode_inline_items();   // calls of up to this many items need no plan launch
 // its CTAs resident per SM (registers: the blocks in flight and the output)
 constexpr int paged_decode_ctas(bool int4, int row_tiles) {
     return int4 && row_tiles == 1 ? 3 : 2;
@@ -210,6 +211,58 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttn& a, int u0, in
     const int H = a.p.n_kv_heads, len = it.units + a.run_cost, rem = u0 - H * it.before, head = rem / len;
     const int run = H * it.before + head * len;
     return PagedShare{i, head, max(u0 - run - a.run_cost, 0), u0, run, it};
+}
+
+// The call's items in shared memory and this CTA's share of their units, derived
+// by every CTA of 128 threads for itself from the lengths and positions: a few
+// dependent loads and a scan, instead of two launches before this one.  Thread i
+// takes items 2 i, 2 i + 1.
+__device__ __forceinline__ PagedShare paged_inline_share(const PagedAttn& a, PagedItem* items, int* u1) {
+    constexpr int kWarps = kPagedInline / 64;
+    __shared__ int sums[kWarps];
+    __shared__ PagedShare out;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    PagedItem it[2] = {};
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (2 * (int)threadIdx.x + e < a.n_items) it[e] = paged_item<1>(a, 2 * threadIdx.x + e, 0);
+    const int cost[2] = {it[0].units ? it[0].units + a.run_cost : 0, it[1].units ? it[1].units + a.run_cost : 0};
+    int incl = cost[0] + cost[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int total = 0, before = incl - cost[0] - cost[1];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    const int H = a.p.n_kv_heads;
+    const long long T = (long long)total * H;
+    const int n = paged_shares(a, T), c = blockIdx.x;
+    const int u0 = c < n ? (int)(T * c / n) : (int)T;
+    if (threadIdx.x == 0) out = PagedShare{-1, 0, 0, u0, u0, {}};
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        it[e].before = before + (e ? cost[0] : 0);
+        const int i = 2 * threadIdx.x + e;
+        if (i < a.n_items) items[i] = it[e];
+        const long long rem = (long long)u0 - (long long)H * it[e].before;
+        if (c < n && rem >= 0 && rem < (long long)H * cost[e]) out = paged_share(a, u0, i, it[e]);
+    }
+    __syncthreads();
+    const PagedShare sh = out;
+    *u1 = c + 1 < n ? (int)(T * (c + 1) / n) : (int)T;
+    if (threadIdx.x == 0) {   // for the merge
+        a.shares[c] = sh;
+        if (c == (int)gridDim.x - 1) a.shares[c + 1] = PagedShare{-1, 0, 0, (int)T, (int)T, {}};
+    }
+    return sh;
 }
 
 // The runs of a CTA's share in order: n units of head h of item i from unit off.

@@ -291,11 +291,11 @@ kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int3
     a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     std::string why;
-    a.planned = !g.decode || g.n_items > paged_decode_inline_items();
+    a.planned = g.tc || g.n_items > kPagedInline;
     if (a.planned) KVR_CHECK_LAUNCH(launch_paged_plan(a, s), "paged plan");
     if (g.decode) KVR_CHECK_LAUNCH(launch_paged_decode(p->format, p->group, a, s), "paged attention");
     else if (g.tc) KVR_CHECK_LAUNCH(launch_paged_tc(p->format, p->group, a, s, &why), ("paged attention " + why).c_str());
-    else KVR_CHECK_LAUNCH(launch_paged_simt(p->format, p->head_dim, p->group, a, s), "paged attention");
+    else KVR_CHECK_LAUNCH(launch_paged_simt(p->head_dim, a, s), "paged attention");
     KVR_CHECK_LAUNCH(launch_paged_merge(p->format == KVR_F32 ? KVR_F32 : KVR_BF16, p->head_dim, a, s), "paged merge");
     return KVR_OK;
 }

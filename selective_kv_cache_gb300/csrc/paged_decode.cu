@@ -41,7 +41,6 @@ namespace kvr {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kItemsInline = 2 * kThreads;   // up to here a CTA derives its share itself
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;   // log2 of the largest P before the maximum is raised
 
@@ -153,56 +152,6 @@ struct Decode {
     static constexpr int kSmem = kWarps * kRing > kJoin ? kWarps * kRing : kJoin;
 };
 
-// The call's items in shared memory and this CTA's share of their units, derived by every
-// CTA for itself from the lengths and positions: a few dependent loads and a
-// scan, instead of a launch before this one.  Thread i takes items 2 i, 2 i + 1.
-__device__ __forceinline__ PagedShare inline_share(const PagedAttn& a, PagedItem* items, int* u1) {
-    __shared__ int sums[kWarps];
-    __shared__ PagedShare out;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    PagedItem it[2] = {};
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        if (2 * (int)threadIdx.x + e < a.n_items) it[e] = paged_item<1>(a, 2 * threadIdx.x + e, 0);
-    const int cost[2] = {it[0].units ? it[0].units + a.run_cost : 0, it[1].units ? it[1].units + a.run_cost : 0};
-    int incl = cost[0] + cost[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    int total = 0, before = incl - cost[0] - cost[1];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    const int H = a.p.n_kv_heads;
-    const long long T = (long long)total * H;
-    const int n = paged_shares(a, T), c = blockIdx.x;
-    const int u0 = c < n ? (int)(T * c / n) : (int)T;
-    if (threadIdx.x == 0) out = PagedShare{-1, 0, 0, u0, u0, {}};
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        it[e].before = before + (e ? cost[0] : 0);
-        const int i = 2 * threadIdx.x + e;
-        if (i < a.n_items) items[i] = it[e];
-        const long long rem = (long long)u0 - (long long)H * it[e].before;
-        if (c < n && rem >= 0 && rem < (long long)H * cost[e]) out = paged_share(a, u0, i, it[e]);
-    }
-    __syncthreads();
-    const PagedShare sh = out;
-    *u1 = c + 1 < n ? (int)(T * (c + 1) / n) : (int)T;
-    if (threadIdx.x == 0) {   // for the merge
-        a.shares[c] = sh;
-        if (c == (int)gridDim.x - 1) a.shares[c + 1] = PagedShare{-1, 0, 0, (int)T, (int)T, {}};
-    }
-    return sh;
-}
-
 // kExtra: cap, biases or slopes
 template <int NG, int NT, bool kExtra>
 __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_kernel(PagedAttn a) {
@@ -211,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
     extern __shared__ __align__(128) uint8_t smem[];   // the warps' rings; the outputs to join over them
     float(*sO)[8][D::LDO] = reinterpret_cast<float(*)[8][D::LDO]>(smem);
     __shared__ float sM[kWarps][8 * NT], sL[kWarps][8 * NT];
-    __shared__ PagedItem items[kItemsInline];
+    __shared__ PagedItem items[kPagedInline];
     pdl_wait();
     pdl_trigger();
     PagedShare sh;
@@ -220,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
         sh = a.shares[blockIdx.x];
         u1 = a.shares[blockIdx.x + 1].u0;
     } else {
-        sh = inline_share(a, items, &u1);
+        sh = paged_inline_share(a, items, &u1);
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
     const int G = a.G, shift = a.p.page_shift, in_page = (1 << shift) - 1;
@@ -755,7 +704,6 @@ cudaError_t launch_ng(const PagedAttn& a, cudaStream_t s) {
 
 }  // namespace
 
-int paged_decode_inline_items() { return kItemsInline; }
 int paged_decode_unit(int format) { return format == KVR_INT4 ? Decode<1, 1>::kUnit : Decode<0, 1>::kUnit; }
 
 cudaError_t launch_paged_decode(int format, int group, const PagedAttn& a, cudaStream_t s) {
