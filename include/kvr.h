@@ -610,7 +610,8 @@ typedef struct {
 
 /* How kvr_paged_attend turns products into logits and which keys a row sees.
  * Zero-initialise and set what is wanted; a NULL kvr_score_opts is the plain
- * causal softmax. */
+ * causal softmax.  scale and softcap are 0 or in [2^-64, 2^64]; logits have to
+ * stay within fp32's range. */
 typedef struct {
     float scale;           /* x = scale * <q, k>; 0 = 1/sqrt(head_dim) */
     float softcap;         /* > 0: x <- softcap * tanh(x / softcap), before the biases */
@@ -641,13 +642,14 @@ typedef struct {
  *               q_out is packed (stride n_q_heads * head_dim) and may be
  *               q_rows itself when that is packed too.
  * The rotation is in fp32, each product and sum rounded on its own, and
- * rounded once to the page format.  KVR_INT4, per group of fp32 values x (after the
- * rotation, brought into +-2^15): o = fp16(min x), s = fp16((max x - min x) * fp32(1/15)), code =
- * clamp(rint((x - o) * (1/s)), 0, 15), 0 when s = 0.
+ * rounded once to the page format.  KVR_INT4, per group of fp32 values x
+ * (after the rotation, brought into +-2^15): o = fp16(min x), s = fp16((max x -
+ * min x) * fp32(1/15)), code = clamp(rint((x - o) * (1/s)), 0, 15), 0 when s = 0.
  * Positions of a sequence ascend; a row that does not lie above the row
  * before it, or whose position is outside the table, the rope table or the
  * pool, is not written (nor its query) and is reported by kvr_paged_status.
- * kv_len is neither read nor changed.
+ * kv_len is neither read nor changed.  Sequences may share pages; a slot that
+ * two of them write in one call holds one of the two values of each part of a row.
  * ------------------------------------------------------------------------- */
 kvr_status kvr_paged_append(const kvr_pages* p, int32_t n_rows, const int32_t* cu_rows, const int32_t* positions,
                             const void* k_rows, int64_t k_stride, const void* v_rows, int64_t v_stride,
@@ -676,7 +678,8 @@ kvr_status kvr_paged_read(const kvr_pages* p, int32_t n_rows, const int32_t* cu_
  * non-finite K or V row between those may reach any of that sequence's rows.
  *   max_rows    upper bound of the rows of any sequence (1 for a decode
  *               step); rows past it are not computed and reported.
- *   q, out      device [n_rows][n_q_heads][head_dim], row strides in elements.
+ *   q, out      device [n_rows][n_q_heads][head_dim], row strides in elements;
+ *               they do not overlap.
  *   workspace   device, >= kvr_paged_workspace_bytes(p, n_q_heads, n_rows,
  *               max_rows), 256-byte aligned; needs no initialisation.  Calls
  *               whose GPU work overlaps need a workspace each.

@@ -42,7 +42,8 @@ kvr_status check_pages(const kvr_pages* p) {
         return fail(KVR_EUNSUPPORTED, "pages: more than 65535 heads, 2^20 sequences or 2^30 positions of a sequence");
     if (p->page_stride < 1 || p->head_stride < 1 || p->slot_stride < 1)
         return fail(KVR_EINVAL, "pages: strides must be positive");
-    if (p->page_stride > (int64_t(1) << 21) || p->slot_stride > (int64_t(1) << 21) || p->head_stride > (int64_t(1) << 31))
+    if (p->page_stride > (int64_t(1) << 21) || p->slot_stride > (int64_t(1) << 21) ||
+        p->head_stride > (int64_t(1) << 31))
         return fail(KVR_EUNSUPPORTED, "pages: page and slot strides above 2^21 rows or head strides above 2^31");
     if (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v))
         return fail(KVR_EINVAL, "pages: k and v must be non-NULL and 16-byte aligned");
@@ -95,7 +96,8 @@ struct Geometry {
 constexpr int kSimtRows = 16, kSimtKeys = 32;
 
 kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32_t max_rows, Geometry* g) {
-    if (n_q_heads < 1 || n_q_heads % p->n_kv_heads) return fail(KVR_EINVAL, "n_q_heads must be a multiple of n_kv_heads");
+    if (n_q_heads < 1 || n_q_heads % p->n_kv_heads)
+        return fail(KVR_EINVAL, "n_q_heads must be a multiple of n_kv_heads");
     g->G = n_q_heads / p->n_kv_heads;
     if (g->G > kPagedMaxGroup) return fail(KVR_EUNSUPPORTED, "more than 16 query heads per K/V head");
     if (max_rows < 1) return fail(KVR_EINVAL, "max_rows must be positive");
@@ -242,9 +244,10 @@ kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int3
     if ((st = check_rows(n_rows, cu_rows, positions)) != KVR_OK) return st;
     kvr_score_opts o{};
     if (opts) o = *opts;
-    if (!std::isfinite(o.scale) || o.scale < 0.f || !std::isfinite(o.softcap) || o.softcap < 0.f ||
-        !std::isfinite(o.alpha) || !std::isfinite(o.beta))
-        return fail(KVR_EINVAL, "attend: scale and softcap must be finite and not negative, alpha and beta finite");
+    // within these a product with log2 e or 2 / softcap is neither infinite nor zero
+    auto usable = [](float x) { return x == 0.f || (x >= 0x1p-64f && x <= 0x1p64f); };
+    if (!usable(o.scale) || !usable(o.softcap) || !std::isfinite(o.alpha) || !std::isfinite(o.beta))
+        return fail(KVR_EINVAL, "attend: scale and softcap must be 0 or in [2^-64, 2^64], alpha and beta finite");
     if (!aligned4(o.local_bits) || !aligned4(o.sink_bits) || !aligned4(o.slopes) || !aligned4(o.key_begin) ||
         !aligned4(o.key_end))
         return fail(KVR_EINVAL, "attend: misaligned option array");
@@ -294,7 +297,8 @@ kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int3
     a.planned = g.tc || g.n_items > kPagedInline;
     if (a.planned) KVR_CHECK_LAUNCH(launch_paged_plan(a, s), "paged plan");
     if (g.decode) KVR_CHECK_LAUNCH(launch_paged_decode(p->format, p->group, a, s), "paged attention");
-    else if (g.tc) KVR_CHECK_LAUNCH(launch_paged_tc(p->format, p->group, a, s, &why), ("paged attention " + why).c_str());
+    else if (g.tc)
+        KVR_CHECK_LAUNCH(launch_paged_tc(p->format, p->group, a, s, &why), ("paged attention " + why).c_str());
     else KVR_CHECK_LAUNCH(launch_paged_simt(p->head_dim, a, s), "paged attention");
     KVR_CHECK_LAUNCH(launch_paged_merge(p->format == KVR_F32 ? KVR_F32 : KVR_BF16, p->head_dim, a, s), "paged merge");
     return KVR_OK;

@@ -132,6 +132,8 @@ __device__ __forceinline__ void lds_meta(uint32_t a, uint32_t* m) {
         m[0] = lds4(a);
     }
 }
+// A row's scale: finite and not zero, so that 0 and -inf stay what they are under it.
+__device__ __forceinline__ float logit_scale(float sl2, float back) { return fminf(fmaxf(sl2 * back, 2e-38f), 2e38f); }
 __device__ __forceinline__ float scale_of(uint32_t m) { return __low2float(*reinterpret_cast<const __half2*>(&m)); }
 
 // NG: 0 = bf16 pages, else the scale groups of a 4-bit row.  NT: 8-row tiles of an item.
@@ -228,7 +230,8 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
                     for (int c = 0; c < 16 / kRowsApart; ++c) {
                         const int64_t o = off_b + (int64_t)(c * kRowsApart) * slot_b;
                         copy_async<16>(d + k_put + c * kRowsApart * RB, k_src + o);
-                        copy_async<16>(d + D::kV + (NG ? v_put : v_put ^ (32 * (c & 3))) + c * kRowsApart * RB, v_src + o);
+                        copy_async<16>(d + D::kV + (NG ? v_put : v_put ^ (32 * (c & 3))) + c * kRowsApart * RB,
+                                       v_src + o);
                     }
                     if constexpr (NG != 0)
                         copy_async<MB>(d + D::kKm + lane * MB, m_src + (int64_t)page * page_m + (int64_t)at * slot_m);
@@ -263,8 +266,10 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
             }
             if constexpr (NG == 0) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    q[nt][4 * c] = w[c].x, q[nt][4 * c + 1] = w[c].y, q[nt][4 * c + 2] = w[c].z, q[nt][4 * c + 3] = w[c].w;
+                for (int c = 0; c < 4; ++c) {
+                    q[nt][4 * c] = w[c].x, q[nt][4 * c + 1] = w[c].y;
+                    q[nt][4 * c + 2] = w[c].z, q[nt][4 * c + 3] = w[c].w;
+                }
                 lsr[nt][0] = lsr[nt][1] = sl2;
             } else {
                 uint32_t top = 0u;   // largest exponent of the row
@@ -313,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
                 const float own_hi = __half2float(__float2half_rn(own));
                 q_off[nt][0] = pack2h(0.f, own_hi);
                 q_off[nt][1] = pack2h(0.f, own - own_hi);
-                lsr[nt][0] = sl2 * __shfl_sync(0xffffffffu, back, 8 * t);
-                lsr[nt][1] = sl2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+                lsr[nt][0] = logit_scale(sl2, __shfl_sync(0xffffffffu, back, 8 * t));
+                lsr[nt][1] = logit_scale(sl2, __shfl_sync(0xffffffffu, back, 8 * t + 4));
             }
         }
         // the intervals of rows 2t, 2t + 1 (rows that do not exist: the item's)
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
                         for (int e = 0; e < 4; ++e) {
                             float y = x[b][nt][e] * lsr[nt][e & 1];
                             // cap tanh(u) = cap (1 - 2 / (1 + exp(2u)))
-                            y = a.softcap > 0.f ? cap_out - 2.f * cap_out * __fdividef(1.f, 1.f + ex2(y * cap_in)) : y;
+                            if (a.softcap > 0.f) y = cap_out - 2.f * cap_out * __fdividef(1.f, 1.f + ex2(y * cap_in));
                             const int key = 16 * (kb + b) + r + 8 * (e >> 1);
                             y = fmaf(-slope[nt][e & 1], (float)abs(gpos[nt][e & 1] - key), y + bias[e >> 1]);
                             x[b][nt][e] = y;
@@ -593,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
                             const uint32_t w = __byte_perm(g < 2 ? vw[2 * j].x : vw[2 * j].y,
                                                            g < 2 ? vw[2 * j + 1].x : vw[2 * j + 1].y, sel);
                             const uint32_t s = __byte_perm(vm[2 * j][n], vm[2 * j + 1][n], 0x5410);
-                            const uint32_t o8 = hfma2(s, 0x48004800u, __byte_perm(vm[2 * j][n], vm[2 * j + 1][n], 0x7632));
+                            const uint32_t o8 =
+                                hfma2(s, 0x48004800u, __byte_perm(vm[2 * j][n], vm[2 * j + 1][n], 0x7632));
                             v[j][0] = hfma2(even8(w), s, o8);
                             v[j][1] = hfma2(odd8(w), s, o8);
                             v[j][2] = hfma2(even8(w >> 8), s, o8);
@@ -646,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
 #pragma unroll
                     for (int d = 0; d < 8; d += 2)
                         *reinterpret_cast<float4*>(dst + 16 * r + 2 * d) =
-                            make_float4(o[nt][d][e] * f, o[nt][d][e + 2] * f, o[nt][d + 1][e] * f, o[nt][d + 1][e + 2] * f);
+                            make_float4(o[nt][d][e] * f, o[nt][d][e + 2] * f, o[nt][d + 1][e] * f,
+                                        o[nt][d + 1][e + 2] * f);
                 } else {                   // dims 32 g + 4 r + 2 s (+ 1)
 #pragma unroll
                     for (int g = 0; g < 4; ++g)

@@ -109,12 +109,13 @@ __device__ __forceinline__ int count_parts(const PagedAttn& a, int c, int end) {
     }
 }
 
-// Block c - 1: the rows of the run that share c enters in its middle,
-// if share c is the first to do so.  Items of up to 16 rows: the warps are dealt to the rows (one each, or several to a row when there are
-// few), a row's warps take its partials in turn, eight loads in flight a lane,
-// four dims a lane (lanes past head_dim idle), and are joined through shared
-// memory, in order.  A long sequence has a partial per CTA, so it is the loads
-// in flight that count: 57 partials of 4 rows 12 -> 5 us against a warp per row.
+// Block c - 1: the rows of the run that share c enters in its middle, if share c
+// is the first to do so.  Items of up to 16 rows: the warps are dealt to the
+// rows (one each, or several to a row when there are few), a row's warps take
+// its partials in turn, eight loads in flight a lane, four dims a lane (lanes
+// past head_dim idle), and are joined through shared memory, in order.  A long
+// sequence has a partial per CTA, so it is the loads in flight that count: 57
+// partials of 4 rows 12 -> 5 us against a warp per row.
 template <typename T, int DH>
 __global__ void __launch_bounds__(32 * 16) merge_kernel(PagedAttn a) {
     constexpr int kWarps = 16;
@@ -235,7 +236,8 @@ __global__ void __launch_bounds__(128) merge_tiles_kernel(PagedAttn a) {
         float4 o[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            o[x] = *reinterpret_cast<const float4*>(a.part_o + slot * 128 + 4 * ((size_t)(8 * warp + x) * a.tile_rows + m));
+            o[x] = *reinterpret_cast<const float4*>(a.part_o + slot * 128 +
+                                                    4 * ((size_t)(8 * warp + x) * a.tile_rows + m));
         if (ml.x == -INFINITY) continue;   // saw no key of the row
         const float top = fmaxf(M, ml.x), f = M == -INFINITY ? 0.f : exp2f(M - top), g = exp2f(ml.x - top);
         M = top;

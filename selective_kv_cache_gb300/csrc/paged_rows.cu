@@ -99,7 +99,8 @@ __device__ __forceinline__ void find_slots(const PagedRowIo& a, RowSlot* slots) 
         const int first = a.r.cu[b];
         g = a.r.pos[r];
         int bad = 0;
-        if (first < 0 || r < first || g < 0 || g >= a.p.capacity || (kAppend && a.rope && g >= a.rope_len)) bad = DEV_ERR_INDEX;
+        if (first < 0 || r < first || g < 0 || g >= a.p.capacity || (kAppend && a.rope && g >= a.rope_len))
+            bad = DEV_ERR_INDEX;
         else if (kAppend && r > first && a.r.pos[r - 1] >= g) bad = DEV_ERR_ORDER;
         int id = 0;
         if (!bad) {
@@ -162,7 +163,8 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(PagedRowIo a) {
                     in_hand = x.i;
 #pragma unroll
                     for (int e = 0; e < E; e += 2) {
-                        const float4 w = *reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * (DH / 2) + v * E + e);
+                        const float4 w =
+                            *reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * (DH / 2) + v * E + e);
                         cs[e] = make_float2(w.x, w.y);
                         cs[e + 1] = make_float2(w.z, w.w);
                     }

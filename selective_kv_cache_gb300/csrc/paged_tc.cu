@@ -1,6 +1,6 @@
 // paged_tc.cu -- attention of many rows over the paged cache on the sm_103a
-// tensor cores (bf16 and 4-bit pages): prompts, refreshed rows, drafted tokens
-// beyond 16 rows per K/V head.
+// tensor cores (bf16 and 4-bit pages): prompts and refreshed rows, what
+// paged_decode.cu would have to read the keys too often for.
 //
 //   x_rj = cap(scale <q_r, k_j>) + alpha loc_j + beta snk_j - slope |g_r - j|
 //   o_r  = sum_j softmax_j(x_rj) v_j,   j in [lo_r, hi_r)
@@ -24,7 +24,8 @@
 //               2^8.  P goes to tensor memory in 16 bits (bf16; fp16 for 4-bit
 //               pages) as the A operand: 2^-8 (2^-11) of a weight at most.
 //   warps 12-15 4 bits only, in warp 0's place: packed rows come in
-//               asynchronously three tiles ahead; codes to their values in fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
+//               asynchronously three tiles ahead; codes to their values in
+//               fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
 //               ring in the operand's swizzle.  A word's nibbles come out in
 //               pairs (e, e + 4), so the 8 dims of a chunk lie in the order 0 4 1
 //               5 2 6 3 7; Q is stored in that order and O read back from it.
@@ -63,7 +64,8 @@ constexpr uint32_t kOffWalk = kOffBar + 256;    // a PagedWalk per warp
 constexpr uint32_t kWalkBytes = 72;
 constexpr uint32_t kSmem = kOffWalk + 16 * kWalkBytes;
 static_assert(sizeof(PagedWalk) <= kWalkBytes && kStaged * kStage <= kTile && kSmem <= 232448, "shared memory layout");
-constexpr uint32_t kColS = 0, kColO = 256;      // TMEM columns of tile t: S (P over its first 64) at 128 t, O at 256 + 128 t
+// TMEM columns of tile t: S (P over its first 64) at 128 t, O at 256 + 128 t
+constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
 
@@ -96,8 +98,12 @@ __device__ __forceinline__ uint32_t with_1024(uint32_t x, uint32_t mask) {
     return y;
 }
 // code - 8 of the even and of the odd nibble of each half, exact
-__device__ __forceinline__ uint32_t even8(uint32_t x) { return hfma2(with_1024(x, 0x000f000fu), 0x3c003c00u, 0xe408e408u); }
-__device__ __forceinline__ uint32_t odd8(uint32_t x) { return hfma2(with_1024(x, 0x00f000f0u), 0x2c002c00u, 0xd480d480u); }
+__device__ __forceinline__ uint32_t even8(uint32_t x) {
+    return hfma2(with_1024(x, 0x000f000fu), 0x3c003c00u, 0xe408e408u);
+}
+__device__ __forceinline__ uint32_t odd8(uint32_t x) {
+    return hfma2(with_1024(x, 0x00f000f0u), 0x2c002c00u, 0xd480d480u);
+}
 // 128 consecutive columns of this thread's lane: four loads, one wait
 __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -137,7 +143,10 @@ template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds4(uint32_t a) {
@@ -155,7 +164,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity) ? 1 : 0;
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn_major, int b_mn_major) {   // kind::f16 with fp16 A/B, fp32 D
+// kind::f16 with fp16 A/B, fp32 D
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn_major, int b_mn_major) {
     return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
@@ -244,125 +254,127 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     // 216 of 3 x 168 a thread (bf16), 72 + 2 x 176 + 88 of 4 x 128 (4 bits)
     if (warp < 4) {
         reg_dec<72>();
-    if (warp == 0) {
-        if constexpr (!kInt4) {
-            // ---------------------------------------------------------- K and V copies
-            // a lane per (operand half, page): tiles of 16-slot pages take 16 copies each
-            const int shift = min(a.p.page_shift, 7), pages = 128 >> shift;   // pages of a tile
-            const int half = lane & 1, pg = lane >> 1;
-            const uint32_t dst_off = (uint32_t)half * kHalf + ((uint32_t)pg << (shift + 7));
-            int x = 0;   // ring index of the next tile
-            for (; w.live() && ok; advance()) {
-                const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
-                const int n = w.n, klo = w.it.klo, khi = w.it.khi, head = w.h, key_base = first_key(w, 0) + (pg << shift);
-                for (int s = 0; s < n && ok; ++s) {
-                    const int k0 = key_base + 128 * s;
-                    // pages none of whose keys is visible are not touched
-                    const bool mine = pg < pages && k0 < khi && k0 + (1 << shift) > klo;
-                    const int id = mine ? paged_id(a.p, table[k0 >> a.p.page_shift]) : 0;
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) << (shift + 7);
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++x) {
-                        const int slot = x % kRing;
-                        // a full barrier is armed again only after every poller of its last phase has passed it:
-                        // the products that free the slot waited for it
-                        if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) {
+        if (warp == 0) {
+            if constexpr (!kInt4) {
+                // ---------------------------------------------------------- K and V copies
+                // a lane per (operand half, page): tiles of 16-slot pages take 16 copies each
+                const int shift = min(a.p.page_shift, 7), pages = 128 >> shift;   // pages of a tile
+                const int half = lane & 1, pg = lane >> 1;
+                const uint32_t dst_off = (uint32_t)half * kHalf + ((uint32_t)pg << (shift + 7));
+                int x = 0;   // ring index of the next tile
+                for (; w.live() && ok; advance()) {
+                    const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
+                    const int n = w.n, klo = w.it.klo, khi = w.it.khi, head = w.h;
+                    const int key_base = first_key(w, 0) + (pg << shift);
+                    for (int s = 0; s < n && ok; ++s) {
+                        const int k0 = key_base + 128 * s;
+                        // pages none of whose keys is visible are not touched
+                        const bool mine = pg < pages && k0 < khi && k0 + (1 << shift) > klo;
+                        const int id = mine ? paged_id(a.p, table[k0 >> a.p.page_shift]) : 0;
+                        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) << (shift + 7);
+    #pragma unroll
+                        for (int kv = 0; kv < 2; ++kv, ++x) {
+                            const int slot = x % kRing;
+                            // a full barrier is armed again only after every poller of its last phase has passed it:
+                            // the products that free the slot waited for it
+                            if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                            __syncwarp();
+                            if (mine)
+                                tma_load_4d(smem + kOffRing + slot * kTile + dst_off, kv ? &tmV : &tmK, &full[slot],
+                                            64 * half, k0 & ((1 << a.p.page_shift) - 1), head, id);
+                        }
+                    }
+                }
+                // let every copy still in flight land before the CTA exits
+                if (!ok)
+                    for (int y = max(x - kRing, 0); y < x; ++y) warp_wait(&full[y % kRing], (uint32_t)(y / kRing) & 1u);
+            }
+        } else if (warp == 1) {
+            // -------------------------------------------------------------- products
+            if (lane == 0) {
+                const uint32_t id_s = kInt4 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+                const uint32_t id_o = kInt4 ? idesc_f16(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);   // V is MN-major
+                int g = 0;                      // tiles so far
+                uint32_t runs = 0, ps = 0;      // bit t: parity of the runs and of the P tiles of row tile t
+                auto landed = [&](int x) { return mbar_wait(&full[x % kRing], (uint32_t)(x / kRing) & 1u); };
+                auto scores = [&](int t, int x) {
+                    // descriptors advance by addresses / 16 in their low bits
+                    const uint64_t qd = sdesc_sw128(sbase + kOffQ + (uint32_t)t * kTile, 16, 1024);
+                    const uint64_t kd = sdesc_sw128(sbase + kOffRing + (uint32_t)(x % kRing) * kTile, 16, 1024);
+    #pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t o = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
+                        mma_bf16(tmem + kColS + 128u * t, qd + o, kd + o, id_s, kk > 0);
+                    }
+                    mma_commit(&s_full[t]);
+                };
+                for (; w.live() && ok; w.next(a, a.items)) {
+                    const int nt = row_tiles(w, per_tile), n = w.n;
+                    for (int t = 0; t < nt && ok; ++t) {
+                        ok = mbar_wait(&q_full[t], (runs >> t) & 1u) && (t || landed(2 * g));
+                        if (!ok) break;
+                        runs ^= 1u << t;
+                        tc_fence_after();
+                        scores(t, 2 * g);
+                        if (n == 1) mma_commit(&q_empty[t]);
+                        if (t == nt - 1) mma_commit(&empty[(2 * g) % kRing]);
+                    }
+                    for (int s = 0; s < n && ok; ++s, ++g) {
+                        const int v = 2 * g + 1;
+                        const uint64_t vd = sdesc_sw128(sbase + kOffRing + (uint32_t)(v % kRing) * kTile, kHalf, 1024);
+                        for (int t = 0; t < nt; ++t) {
+                            const uint32_t pt = tmem + kColS + 128u * t;
+                            // everything the tile's two products need is waited for before the
+                            // first, so that nothing comes between them on the pipe
+                            ok = (t || (landed(v) && (s + 1 == n || landed(v + 1)))) &&
+                                 mbar_wait(&p_full[t], (ps >> t) & 1u);
+                            if (!ok) break;
+                            tc_fence_after();
+    #pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
+                                            vd + (uint32_t)kk * 128u, id_o, (s > 0 || kk > 0));
+                            ps ^= 1u << t;
+                            if (s + 1 < n) scores(t, v + 1);
+                            if (s + 2 == n) mma_commit(&q_empty[t]);
+                            if (s + 1 == n) mma_commit(&o_done[t]);
+                            if (t == nt - 1) {
+                                mma_commit(&empty[v % kRing]);
+                                if (s + 1 < n) mma_commit(&empty[(v + 1) % kRing]);
+                            }
+                        }
+                    }
+                }
+                mma_commit(drained);
+                if (!mbar_wait(drained, 0)) ok = false;
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------------------- Q by TMA
+            if (lane == 0) {
+                uint64_t* landed = kInt4 ? q_raw : q_full;
+                uint32_t begun = 0, runs = 0;   // bit t: row tile t has begun a run; parity of its runs
+                for (; w.live() && ok; w.next(a, a.items))
+                    for (int t = 0; t < row_tiles(w, per_tile); ++t) {
+                        // the run before this one; its own parity is the other
+                        if (((begun >> t) & 1u) && !mbar_wait(&q_empty[t], ((runs >> t) & 1u) ^ 1u)) {
                             ok = false;
                             break;
                         }
-                        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                        __syncwarp();
-                        if (mine)
-                            tma_load_4d(smem + kOffRing + slot * kTile + dst_off, kv ? &tmV : &tmK, &full[slot], 64 * half,
-                                        k0 & ((1 << a.p.page_shift) - 1), head, id);
+                        uint8_t* dst = smem + kOffQ + (uint32_t)t * kTile;
+                        mbar_arrive_expect_tx(&landed[t], 2u * 128u * (uint32_t)(per_tile * G));
+                        tma_load_3d(dst, &tmQ, &landed[t], 0, w.h * G, w.it.row0 + t * per_tile);
+                        tma_load_3d(dst + kHalf, &tmQ, &landed[t], 64, w.h * G, w.it.row0 + t * per_tile);
+                        begun |= 1u << t;
+                        runs ^= 1u << t;
                     }
-                }
+                for (int t = 0; t < 2; ++t)   // the last copies land before the CTA exits
+                    if (((begun >> t) & 1u) && !mbar_wait(&landed[t], ((runs >> t) & 1u) ^ 1u)) ok = false;
             }
-            // let every copy still in flight land before the CTA exits
-            if (!ok)
-                for (int y = max(x - kRing, 0); y < x; ++y) warp_wait(&full[y % kRing], (uint32_t)(y / kRing) & 1u);
         }
-    } else if (warp == 1) {
-        // -------------------------------------------------------------- products
-        if (lane == 0) {
-            const uint32_t id_s = kInt4 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
-            const uint32_t id_o = kInt4 ? idesc_f16(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);   // V is MN-major
-            int g = 0;                      // tiles so far
-            uint32_t runs = 0, ps = 0;      // bit t: parity of the runs and of the P tiles of row tile t
-            auto landed = [&](int x) { return mbar_wait(&full[x % kRing], (uint32_t)(x / kRing) & 1u); };
-            auto scores = [&](int t, int x) {
-                // descriptors advance by addresses / 16 in their low bits
-                const uint64_t qd = sdesc_sw128(sbase + kOffQ + (uint32_t)t * kTile, 16, 1024);
-                const uint64_t kd = sdesc_sw128(sbase + kOffRing + (uint32_t)(x % kRing) * kTile, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t o = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
-                    mma_bf16(tmem + kColS + 128u * t, qd + o, kd + o, id_s, kk > 0);
-                }
-                mma_commit(&s_full[t]);
-            };
-            for (; w.live() && ok; w.next(a, a.items)) {
-                const int nt = row_tiles(w, per_tile), n = w.n;
-                for (int t = 0; t < nt && ok; ++t) {
-                    ok = mbar_wait(&q_full[t], (runs >> t) & 1u) && (t || landed(2 * g));
-                    if (!ok) break;
-                    runs ^= 1u << t;
-                    tc_fence_after();
-                    scores(t, 2 * g);
-                    if (n == 1) mma_commit(&q_empty[t]);
-                    if (t == nt - 1) mma_commit(&empty[(2 * g) % kRing]);
-                }
-                for (int s = 0; s < n && ok; ++s, ++g) {
-                    const int v = 2 * g + 1;
-                    const uint64_t vd = sdesc_sw128(sbase + kOffRing + (uint32_t)(v % kRing) * kTile, kHalf, 1024);
-                    for (int t = 0; t < nt; ++t) {
-                        const uint32_t pt = tmem + kColS + 128u * t;
-                        // everything the tile's two products need is waited for before the
-                        // first, so that nothing comes between them on the pipe
-                        ok = (t || (landed(v) && (s + 1 == n || landed(v + 1)))) && mbar_wait(&p_full[t], (ps >> t) & 1u);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
-                                        vd + (uint32_t)kk * 128u, id_o, (s > 0 || kk > 0));
-                        ps ^= 1u << t;
-                        if (s + 1 < n) scores(t, v + 1);
-                        if (s + 2 == n) mma_commit(&q_empty[t]);
-                        if (s + 1 == n) mma_commit(&o_done[t]);
-                        if (t == nt - 1) {
-                            mma_commit(&empty[v % kRing]);
-                            if (s + 1 < n) mma_commit(&empty[(v + 1) % kRing]);
-                        }
-                    }
-                }
-            }
-            mma_commit(drained);
-            if (!mbar_wait(drained, 0)) ok = false;
-        }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------- Q by TMA
-        if (lane == 0) {
-            uint64_t* landed = kInt4 ? q_raw : q_full;
-            uint32_t begun = 0, runs = 0;   // bit t: row tile t has begun a run; parity of its runs
-            for (; w.live() && ok; w.next(a, a.items))
-                for (int t = 0; t < row_tiles(w, per_tile); ++t) {
-                    // the run before this one; its own parity is the other
-                    if (((begun >> t) & 1u) && !mbar_wait(&q_empty[t], ((runs >> t) & 1u) ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* dst = smem + kOffQ + (uint32_t)t * kTile;
-                    mbar_arrive_expect_tx(&landed[t], 2u * 128u * (uint32_t)(per_tile * G));
-                    tma_load_3d(dst, &tmQ, &landed[t], 0, w.h * G, w.it.row0 + t * per_tile);
-                    tma_load_3d(dst + kHalf, &tmQ, &landed[t], 64, w.h * G, w.it.row0 + t * per_tile);
-                    begun |= 1u << t;
-                    runs ^= 1u << t;
-                }
-            for (int t = 0; t < 2; ++t)   // the last copies land before the CTA exits
-                if (((begun >> t) & 1u) && !mbar_wait(&landed[t], ((runs >> t) & 1u) ^ 1u)) ok = false;
-        }
-    }
     } else if (warp < 12) {
         reg_inc<kInt4 ? 176 : 216>();
         // -------------------------------------------------------------- softmax
@@ -397,7 +409,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 }
                 const int ex = min(max((int)(top >> 7), 8), 253);
                 const float f = __uint_as_float((uint32_t)(261 - ex) << 23);      // 2^(134 - ex)
-                lsr_next = sl2 * __uint_as_float((uint32_t)(ex - 7) << 23);       // 2^(ex - 134)
+                // 2^(ex - 134); finite and not zero, so that 0 and -inf stay what they are under it
+                lsr_next = fminf(fmaxf(sl2 * __uint_as_float((uint32_t)(ex - 7) << 23), 2e-38f), 2e38f);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const uint32_t ws[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
@@ -513,7 +526,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
 #pragma unroll
                     for (int q = 1; q < 8; ++q) mx[i] = max3f(mx[i], x[i + 16 * q], x[i + 16 * q + 8]);
                 }
-                const float top = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ls;
+                const float top =
+                    max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ls;
                 const bool raise = top > m_run + kLazy;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m_run - top) : 1.f;
@@ -609,8 +623,9 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                         for (int e = 0; e < 8; ++e) k[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
                         // even lane: first 16 bytes of its own row and of its neighbour's; odd lane: the second
                         const bool odd = lane & 1;
-                        const uint4 own = odd ? make_uint4(k[4], k[5], k[6], k[7]) : make_uint4(k[0], k[1], k[2], k[3]);
-                        uint4 other = odd ? make_uint4(k[0], k[1], k[2], k[3]) : make_uint4(k[4], k[5], k[6], k[7]);
+                        const uint4 low = make_uint4(k[0], k[1], k[2], k[3]), high = make_uint4(k[4], k[5], k[6], k[7]);
+                        const uint4 own = odd ? high : low;
+                        uint4 other = odd ? low : high;
                         other.x = __shfl_xor_sync(0xffffffffu, other.x, 1);
                         other.y = __shfl_xor_sync(0xffffffffu, other.y, 1);
                         other.z = __shfl_xor_sync(0xffffffffu, other.z, 1);
@@ -663,8 +678,9 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             if ((y & 1) || w.live()) {
                 const bool is_v = y & 1;
                 if (!is_v) {
-                    const int page_b = (int)a.p.page_stride * 64, slot_b = (int)a.p.slot_stride * 64;   // below 2^31 (checked)
-                    const int slot = (first_key(w, s) + kr) & ((1 << a.p.page_shift) - 1), in_page = (1 << a.p.page_shift) - 1;
+                    // below 2^31 (checked)
+                    const int page_b = (int)a.p.page_stride * 64, slot_b = (int)a.p.slot_stride * 64;
+                    const int in_page = (1 << a.p.page_shift) - 1, slot = (first_key(w, s) + kr) & in_page;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         at[i] = id[i] < 0 ? -1 : head + (int64_t)paged_id(a.p, id[i]) * page_b +
@@ -684,7 +700,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     const uint32_t dc = d + 64u * k + 16u * q, dm = d + kStageCodes + (uint32_t)(mb * k);
                     if (at[i] < 0) {
                         sts16(dc, make_uint4(0u, 0u, 0u, 0u));
-                        if (q < n_groups) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dm + 4u * q), "r"(0u) : "memory");
+                        if (q < n_groups)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dm + 4u * q), "r"(0u) : "memory");
                         continue;
                     }
                     copy_async<16>(dc, codes + at[i]);
@@ -728,7 +745,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 uint4 v[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {   // 32-dim block: units of the chunk's two 8-byte halves
-                    const uint32_t z = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w, (b & 1) ? 0x7632 : 0x5410);
+                    const uint32_t z = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w,
+                                                   (b & 1) ? 0x7632 : 0x5410);
                     const uint32_t sc = __byte_perm(cm[i][b], 0u, 0x1010);
                     const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[i][b], 0u, 0x3232));
                     v[b] = make_uint4(hfma2(even8(z), sc, o8), hfma2(odd8(z), sc, o8), hfma2(even8(z >> 8), sc, o8),
@@ -759,7 +777,8 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(paged_tc_kernel<kInt4, kExtra>, (int)kSmem, &allowed);
     if (e != cudaSuccess) return e;
-    KVR_LAUNCH(paged_tc_kernel<kInt4, kExtra>, dim3((unsigned)a.n_cta), dim3(kInt4 ? 512 : 384), kSmem, s, k, v, q, a, n_groups);
+    KVR_LAUNCH(paged_tc_kernel<kInt4, kExtra>, dim3((unsigned)a.n_cta), dim3(kInt4 ? 512 : 384), kSmem, s, k, v, q, a,
+               n_groups);
     return cudaSuccess;
 }
 
@@ -779,7 +798,8 @@ cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStrea
     const uint64_t strides[3] = {(uint64_t)a.p.slot_stride * 256, (uint64_t)a.p.head_stride * 256,
                                  (uint64_t)a.p.page_stride * 256};
     const uint32_t box[4] = {64, 1u << (a.p.page_shift < 7 ? a.p.page_shift : 7), 1, 1};
-    if (!make_tmap_4d_bf16(&k, a.p.k, dims, strides, box, why) || !make_tmap_4d_bf16(&v, a.p.v, dims, strides, box, why))
+    if (!make_tmap_4d_bf16(&k, a.p.k, dims, strides, box, why) ||
+        !make_tmap_4d_bf16(&v, a.p.v, dims, strides, box, why))
         return cudaErrorInvalidValue;
     return extra ? launch<false, true>(k, v, q, a, 0, s) : launch<false, false>(k, v, q, a, 0, s);
 }

@@ -515,8 +515,7 @@ def _packed_rows(p: kvr_pages, t, what: str, n: int):
 
 
 def _rows(p: kvr_pages, cu_rows, positions):
-    """(n_rows, the two pointers).  A call on pages of another device than the
-    current one fails in the launch: its stream is of the pages' device."""
+    """(n_rows, the two pointers)"""
     if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.device != p.device:
         _int_array(positions, "positions", None, p.device)
     if cu_rows.dtype is not torch.int32 or not cu_rows.is_contiguous() or cu_rows.device != p.device or \
@@ -526,6 +525,9 @@ def _rows(p: kvr_pages, cu_rows, positions):
 
 
 def _paged_stream(p: kvr_pages, stream) -> int:
+    # a launch goes to the current device, whichever device the pointers are of
+    if torch._C._cuda_getDevice() != p.device.index:
+        raise ValueError(f"pages on {p.device}: make it the current device")
     return torch._C._cuda_getCurrentRawStream(p.device.index) if stream is None else _stream(stream)
 
 

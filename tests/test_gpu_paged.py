@@ -316,6 +316,35 @@ def test_magnitudes(fmt, dh, group, scale_v, q_scale, counts):
     check_attend(c, 8, counts, pos, out, q)
 
 
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("most", [1, 40])
+def test_many_sequences(fmt, dh, group, most):
+    """More sequences than a kernel derives its shares of by itself, some
+    without keys, some without rows."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 90, 300)
+    counts = np.minimum(rng.integers(0, most + 1, 300), lens)
+    c = Paged(fmt, lens, 2, dh, 16, "nhd", group, seed=21)
+    pos = tail(lens, counts)
+    out, q, _ = attend_case(c, 8, counts, pos, spare_rows=3)
+    kvr.kvr_paged_status(c.p)
+    assert torch.all(out[counts.sum():] == 7.0)
+    check_attend(c, 8, counts, pos, out, q)
+
+
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("counts", [[1, 1], [70, 33]])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 2.0 ** 64])
+def test_extreme_scales_of_flat_rows(fmt, dh, group, counts, scale):
+    """Queries of zeros: the mean of the visible values, whatever the scale."""
+    lens = [400, 77]
+    c = Paged(fmt, lens, 2, dh, 32, "hnd", group, seed=5)
+    pos = tail(lens, counts)
+    out, q, _ = attend_case(c, 8, counts, pos, q_scale=0.0, scale=scale)
+    kvr.kvr_paged_status(c.p)
+    check_attend(c, 8, counts, pos, out, q, scale=scale)
+
+
 def test_order_of_rows_does_not_matter():
     """Positions in any order and repeated; strided q and out rows."""
     c = Paged("bf16", [400], 2, seed=3)
@@ -465,7 +494,7 @@ def test_captured_prompt(fmt, dh, group):
         ws.random_(0, 256)
 
 
-def test_binding_refusals():
+def test_binding_refusals(monkeypatch):
     c = Paged("bf16", [40], 2)
     q = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")
     ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
@@ -480,6 +509,14 @@ def test_binding_refusals():
     with pytest.raises(kvr.KvrError) as e:
         kvr.kvr_paged_attend(c.p, None, 1, **{**ok, "workspace": ws[:256]})
     assert e.value.status == kvr.KVR_EINVAL
+    with monkeypatch.context() as m:   # another device is the current one
+        m.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+        with pytest.raises(ValueError, match="current device"):
+            kvr.kvr_paged_attend(c.p, None, 1, **ok)
+        with pytest.raises(ValueError, match="current device"):
+            kvr.kvr_paged_read(c.p, cu, pos, q[:, :2].clone())
+        with pytest.raises(ValueError, match="current device"):
+            kvr.kvr_paged_append(c.p, cu, pos, q[:, :2], q[:, :2])
     with pytest.raises(ValueError):
         kvr.kvr_paged_attend(c.p, kvr.score_opts(slopes=torch.ones(2, device="cuda")), 1, **ok)
     with pytest.raises(ValueError):
@@ -585,7 +622,8 @@ def test_answering_after_a_repair(dtype):
     check_attend(Twin, m.n_q_heads, [rows], U, po, qs, alpha=w.alpha, beta=w.beta, loc=mask(lw), snk=mask(sw))
     kvr.kvr_attend(s.handle, layer, qs, ca)
     s.sync()
-    check_attend(Twin, m.n_q_heads, [rows], U, ca.view_as(qs), qs, alpha=w.alpha, beta=w.beta, loc=mask(lw), snk=mask(sw))
+    check_attend(Twin, m.n_q_heads, [rows], U, ca.view_as(qs), qs, alpha=w.alpha, beta=w.beta, loc=mask(lw),
+                 snk=mask(sw))
     if dtype == "bf16":
         c4 = Paged("int4", [n], m.n_kv_heads, 128, 64, group=32, fill=False)
         rows = lambda t: t[:, :n].transpose(0, 1).contiguous()  # noqa: E731

@@ -109,8 +109,9 @@ BAD_PAGES = [
     (dict(group=32), "EINVAL"), (dict(page_stride=0), "EINVAL"), (dict(head_stride=-1), "EINVAL"),
     (dict(slot_stride=0), "EINVAL"), (dict(k=None), "EINVAL"), (dict(v=A + 8), "EINVAL"),
     (dict(page_table=None), "EINVAL"), (dict(kv_len=None), "EINVAL"), (dict(err=None), "EINVAL"),
-    (dict(page_table=A + 2), "EINVAL"), (dict(batch=1 << 21), "EUNSUPPORTED"), (dict(page_stride=(1 << 21) + 1), "EUNSUPPORTED"),
-    (dict(slot_stride=1 << 22), "EUNSUPPORTED"), (dict(head_stride=1 << 32), "EUNSUPPORTED"), (dict(max_pages=1 << 27), "EUNSUPPORTED"),
+    (dict(page_table=A + 2), "EINVAL"), (dict(batch=1 << 21), "EUNSUPPORTED"),
+    (dict(page_stride=(1 << 21) + 1), "EUNSUPPORTED"), (dict(slot_stride=1 << 22), "EUNSUPPORTED"),
+    (dict(head_stride=1 << 32), "EUNSUPPORTED"), (dict(max_pages=1 << 27), "EUNSUPPORTED"),
     (dict(format=2, group=0, k_scale=A, v_scale=A), "EINVAL"), (dict(format=2, group=16, k_scale=A, v_scale=A), "EINVAL"),
     (dict(format=2, group=32, k_scale=None, v_scale=A), "EINVAL"),
     (dict(format=2, group=32, k_scale=A, v_scale=A + 4), "EINVAL"),
@@ -157,7 +158,8 @@ def test_attend_refusals(kvr, kw, status):
 
 
 @pytest.mark.parametrize("kw", [dict(scale=-1.0), dict(scale=float("nan")), dict(softcap=-2.0),
-                                dict(softcap=float("inf")), dict(alpha=float("nan")), dict(beta=float("-inf")),
+                                dict(softcap=float("inf")), dict(scale=1e-20), dict(scale=1e20),
+                                dict(softcap=1e-20), dict(softcap=2e19), dict(alpha=float("nan")), dict(beta=float("-inf")),
                                 dict(slopes=A + 2), dict(key_begin=A + 1), dict(local_bits=A + 3)])
 def test_score_option_refusals(kvr, kw):
     o = kvr.kvr_score_opts()
