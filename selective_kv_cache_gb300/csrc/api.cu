@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "kvr_internal.h"
+#include "paged.h"
 
 namespace kvr {
 
@@ -508,8 +509,10 @@ bool encode_cached(CUtensorMap* out, CUtensorMapDataType dtype, int rank, const 
         if (i + 1 < rank) st[i] = strides[i];
     }
     CUresult r = g_encode(out, dtype, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          dtype == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                                                 : CU_TENSOR_MAP_SWIZZLE_128B,
+                          l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         if (why) *why = std::string("cuTensorMapEncodeTiled") + what + " failed with " + std::to_string((int)r);
         return false;
@@ -542,6 +545,12 @@ bool make_tmap_4d_bf16(CUtensorMap* out, const void* base, const uint64_t dims_i
                        const uint32_t box_in[4], std::string* why) {
     return encode_cached(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims_in, strides_bytes, box_in,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, " (4-d)", why);
+}
+
+bool make_tmap_4d_bytes(CUtensorMap* out, const void* base, const uint64_t dims_in[4], const uint64_t strides_bytes[3],
+                        const uint32_t box_in[4], std::string* why) {
+    return encode_cached(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims_in, strides_bytes, box_in,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, " (4-d bytes)", why);
 }
 
 bool make_tmap_2d_f32_sw128(CUtensorMap* out, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,

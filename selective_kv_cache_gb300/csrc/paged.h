@@ -95,6 +95,9 @@ cudaError_t launch_paged_merge(int dtype, int head_dim, const PagedAttn& a, cuda
 // Up to 16 rows an item, fp32 pages, units of 32 keys.
 cudaError_t launch_paged_simt(int head_dim, const PagedAttn& a, cudaStream_t s);
 
+// Tensor map of bytes, dims[0] innermost, strides of dims 1-3, boxes not swizzled (api.cu).
+bool make_tmap_4d_bytes(CUtensorMap* out, const void* base, const uint64_t dims[4], const uint64_t strides_bytes[3],
+                        const uint32_t box[4], std::string* why);
 // Items of two tiles of 128 / G positions each, bf16 or 4-bit pages, units of 128 keys.
 cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStream_t s, std::string* why);
 // Up to 16 rows (positions * G) an item, bf16 or 4-bit pages.

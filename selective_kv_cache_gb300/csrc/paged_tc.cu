@@ -13,9 +13,11 @@
 // score buffers and two outputs fill tensor memory exactly.
 //   warp 0      bf16: K and V pages by TMA into a ring of five 32 KB tiles, a
 //               copy per page and 64-column half (one lane each), K_0 V_0 K_1 V_1 ...
-//   warp 1      tcgen05.mma: S_t = Q_t K^T, O_t += P_t V.  One thread issues all
+//   warp 1      tcgen05.mma: S_t = Q_t K^T, O_t += P_t V.  One lane issues all
 //               products; they complete in order, so "S_t of tile j is done" also
-//               says that tile j - 1's product with V is.
+//               says that tile j - 1's product with V is.  The warp runs the loop
+//               together: in one thread's code the descriptors passed through its
+//               registers, 100-130 cycles a product (4096 rows 378 us, now 304).
 //   warp 2      Q of the next run by TMA, as soon as the last scores are done
 //               with its tile (4 bits: the softmax warps then scale it to fp16 in place).
 //   warps 4-11  softmax, four warps a row tile, one thread a row: no exchange
@@ -23,18 +25,20 @@
 //               rescaled in tensor memory, only when it grows by more than
 //               2^8.  P goes to tensor memory in 16 bits (bf16; fp16 for 4-bit
 //               pages) as the A operand: 2^-8 (2^-11) of a weight at most.
-//   warps 12-15 4 bits only, in warp 0's place: packed rows come in
-//               asynchronously three tiles ahead; codes to their values in
-//               fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
+//   warp 3      4 bits: the scale pairs of the packed tiles that warp 0's copies bring
+//   warps 12-15 4 bits only: packed tiles, which come in three ahead, to their values
+//               in fp16, s (c - 8) + (o + 8 s) in two packed FMAs, written into the
 //               ring in the operand's swizzle.  A word's nibbles come out in
 //               pairs (e, e + 4), so the 8 dims of a chunk lie in the order 0 4 1
 //               5 2 6 3 7; Q is stored in that order and O read back from it.
+// Biases of keys (the same for every row) are written to shared memory once a
+// tile and read as broadcasts: 8192 keys, 4096 rows 329 us with, 304 us without.
 // A unit is four 128^3 products (2048 cycles of the pipe) and 2 x 128 x 128
-// exponentials (1024).  Measured: about 3900 cycles, 1.09 PFLOP/s at 4096 rows
-// over 8192 keys of a 32/8-head model.  What bounds it is the chain of a row tile
-// (scores, softmax 1750, product with V) together with the issuing thread, which
-// shares its scheduler with the softmax: the waits and commits around a
-// tile's 16 products take as long as the products.
+// exponentials (1024).  Measured: 1.36 PFLOP/s at 4096 rows over 8192 keys of a
+// 32/8-head model (0.30 ms), about 3000 cycles a unit, close to the chain of a row
+// tile that bounds it: softmax 1450, its two products 1024, three hand-overs of
+// 100-150.  4 bits: 0.93 PFLOP/s at 8192 causal rows, bound by the conversion
+// (1400 cycles for each of a unit's two tiles, against the softmax's issue slots).
 // The runs' bookkeeping lives in shared memory, a copy per warp: a spilled register
 // costs an L2 round trip here, where shared memory takes all but a few KB of L1.
 // Every wait is bounded; on a timeout the CTA records it, drains its copies and
@@ -62,10 +66,11 @@ constexpr uint32_t kOffStage = kOffRing + 4 * kTile;
 constexpr uint32_t kOffBar = kOffRing + 5 * kTile;
 constexpr uint32_t kOffWalk = kOffBar + 256;    // a PagedWalk per warp
 constexpr uint32_t kWalkBytes = 72;
-constexpr uint32_t kSmem = kOffWalk + 16 * kWalkBytes;
+constexpr uint32_t kOffBias = kOffWalk + 16 * kWalkBytes;   // of each row tile's 128 keys, fp32
+constexpr uint32_t kSmem = kOffBias + 2 * 512;
 static_assert(sizeof(PagedWalk) <= kWalkBytes && kStaged * kStage <= kTile && kSmem <= 232448, "shared memory layout");
 // TMEM columns of tile t: S (P over its first 64) at 128 t, O at 256 + 128 t
-constexpr uint32_t kColS = 0, kColO = 256;
+constexpr uint32_t kColS = 0, kColO = 256, kTmem = 0;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
 
@@ -131,16 +136,16 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
                      "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
                      "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])::"memory");
 }
+// N bytes, or zeros
 template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, bool take) {
     if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0)
+                     : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(take ? N : 0)
+                     : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -158,11 +163,11 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
-// one lane polls, the whole warp follows (keeps tcgen05 .sync.aligned ops converged)
+// The warp waits and stays together.  All lanes poll (one instruction) and vote: a
+// shuffle of one lane's answer takes longer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 // kind::f16 with fp16 A/B, fp32 D
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn_major, int b_mn_major) {
@@ -198,8 +203,11 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     uint64_t* o_done = p_full + 2;                                  // [2] a run's last product with V is done
     uint64_t* q_raw = o_done + 2;                                   // [2] 4 bits: Q_t has landed in bf16
     uint64_t* drained = q_raw + 2;                                  // every product issued is done
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t* c_full = drained + 1;                                 // [kStaged] 4 bits: a tile's codes have landed
+    uint64_t* c_empty = c_full + kStaged;                           // [kStaged] and have been read
+    uint64_t* b_full = c_empty + kStaged;                           // [2] a tile's biases are written
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 2);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int G = a.G, per_tile = 128 / G;
     PagedWalk& w = *reinterpret_cast<PagedWalk*>(smem + kOffWalk + warp * kWalkBytes);
     auto advance = [&]() {
@@ -212,21 +220,24 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         for (int i = 0; i < kRing; ++i) mbar_init(&full[i], kInt4 ? 4 : 1);
         for (int i = 0; i < kRing; ++i) mbar_init(&empty[i], 1);
         mbar_init(drained, 1);
+        for (int i = 0; i < kStaged; ++i) {
+            mbar_init(&c_full[i], 33);
+            mbar_init(&c_empty[i], 4);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], kInt4 ? 4 : 1);
             mbar_init(&q_raw[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
+            mbar_init(&b_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        if (!kInt4) {
-            prefetch_tmap(&tmK);
-            prefetch_tmap(&tmV);
-        }
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
         prefetch_tmap(&tmQ);
     }
     if (warp == 2)   // rows of a tile that no position fills (128 % G): zeros for good
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+
     pdl_trigger();
     bool ok = true;
 
@@ -255,103 +266,134 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     if (warp < 4) {
         reg_dec<72>();
         if (warp == 0) {
-            if constexpr (!kInt4) {
-                // ---------------------------------------------------------- K and V copies
-                // a lane per (operand half, page): tiles of 16-slot pages take 16 copies each
-                const int shift = min(a.p.page_shift, 7), pages = 128 >> shift;   // pages of a tile
-                const int half = lane & 1, pg = lane >> 1;
-                const uint32_t dst_off = (uint32_t)half * kHalf + ((uint32_t)pg << (shift + 7));
-                int x = 0;   // ring index of the next tile
-                for (; w.live() && ok; advance()) {
-                    const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
-                    const int n = w.n, klo = w.it.klo, khi = w.it.khi, head = w.h;
-                    const int key_base = first_key(w, 0) + (pg << shift);
-                    for (int s = 0; s < n && ok; ++s) {
-                        const int k0 = key_base + 128 * s;
-                        // pages none of whose keys is visible are not touched
-                        const bool mine = pg < pages && k0 < khi && k0 + (1 << shift) > klo;
-                        const int id = mine ? paged_id(a.p, table[k0 >> a.p.page_shift]) : 0;
-                        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) << (shift + 7);
-    #pragma unroll
-                        for (int kv = 0; kv < 2; ++kv, ++x) {
-                            const int slot = x % kRing;
-                            // a full barrier is armed again only after every poller of its last phase has passed it:
-                            // the products that free the slot waited for it
-                            if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) {
-                                ok = false;
-                                break;
-                            }
-                            if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                            __syncwarp();
-                            if (mine)
-                                tma_load_4d(smem + kOffRing + slot * kTile + dst_off, kv ? &tmV : &tmK, &full[slot],
-                                            64 * half, k0 & ((1 << a.p.page_shift) - 1), head, id);
+            // ------------------------------------------------------------ K and V copies
+            // into the ring, or 4-bit codes into the staged tiles: a lane per page (bf16:
+            // and operand half), so tiles of 16-slot pages take 8 copies (16)
+            constexpr int kSlots = kInt4 ? kStaged : kRing;
+            constexpr uint32_t kPitch = kInt4 ? kStage : kTile;
+            constexpr int kRowLog = kInt4 ? 6 : 7;   // bytes of a row in a copy
+            uint64_t* landed = kInt4 ? c_full : full;
+            uint64_t* freed = kInt4 ? c_empty : empty;
+            uint8_t* ring = smem + (kInt4 ? kOffStage : kOffRing);
+            const int shift = min(a.p.page_shift, 7), pages = 128 >> shift;   // pages of a tile
+            const int half = kInt4 ? 0 : lane & 1, pg = kInt4 ? lane : lane >> 1;
+            const uint32_t dst_off = (uint32_t)half * kHalf + ((uint32_t)pg << (shift + kRowLog));
+            int x = 0;   // tiles so far
+            for (; w.live() && ok; advance()) {
+                const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
+                const int n = w.n, klo = w.it.klo, khi = w.it.khi, head = w.h;
+                const int key_base = first_key(w, 0) + (pg << shift);
+                for (int s = 0; s < n && ok; ++s) {
+                    const int k0 = key_base + 128 * s;
+                    // pages none of whose keys is visible are not touched
+                    const bool mine = pg < pages && k0 < khi && k0 + (1 << shift) > klo;
+                    const int id = mine ? paged_id(a.p, table[k0 >> a.p.page_shift]) : 0;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) << (shift + kRowLog);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++x) {
+                        const int slot = x % kSlots;
+                        // a full barrier is armed again only after every poller of its last phase has passed it:
+                        // what frees the slot waited for it
+                        if (x >= kSlots && !warp_wait(&freed[slot], (uint32_t)(x / kSlots - 1) & 1u)) {
+                            ok = false;
+                            break;
                         }
+                        if (lane == 0) mbar_arrive_expect_tx(&landed[slot], bytes);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_4d(ring + slot * kPitch + dst_off, kv ? &tmV : &tmK, &landed[slot], 64 * half,
+                                        k0 & ((1 << a.p.page_shift) - 1), head, id);
                     }
                 }
-                // let every copy still in flight land before the CTA exits
-                if (!ok)
-                    for (int y = max(x - kRing, 0); y < x; ++y) warp_wait(&full[y % kRing], (uint32_t)(y / kRing) & 1u);
             }
+            // let every copy still in flight land before the CTA exits
+            if (!ok)
+                for (int y = max(x - kSlots, 0); y < x; ++y)
+                    warp_wait(&landed[y % kSlots], (uint32_t)(y / kSlots) & 1u);
         } else if (warp == 1) {
             // -------------------------------------------------------------- products
-            if (lane == 0) {
-                const uint32_t id_s = kInt4 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
-                const uint32_t id_o = kInt4 ? idesc_f16(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);   // V is MN-major
-                int g = 0;                      // tiles so far
-                uint32_t runs = 0, ps = 0;      // bit t: parity of the runs and of the P tiles of row tile t
-                auto landed = [&](int x) { return mbar_wait(&full[x % kRing], (uint32_t)(x / kRing) & 1u); };
-                auto scores = [&](int t, int x) {
-                    // descriptors advance by addresses / 16 in their low bits
-                    const uint64_t qd = sdesc_sw128(sbase + kOffQ + (uint32_t)t * kTile, 16, 1024);
-                    const uint64_t kd = sdesc_sw128(sbase + kOffRing + (uint32_t)(x % kRing) * kTile, 16, 1024);
-    #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t o = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
-                        mma_bf16(tmem + kColS + 128u * t, qd + o, kd + o, id_s, kk > 0);
-                    }
-                    mma_commit(&s_full[t]);
-                };
-                for (; w.live() && ok; w.next(a, a.items)) {
-                    const int nt = row_tiles(w, per_tile), n = w.n;
-                    for (int t = 0; t < nt && ok; ++t) {
-                        ok = mbar_wait(&q_full[t], (runs >> t) & 1u) && (t || landed(2 * g));
-                        if (!ok) break;
-                        runs ^= 1u << t;
-                        tc_fence_after();
-                        scores(t, 2 * g);
+            // the warp stays together and one lane issues, so that addresses and
+            // descriptors are uniform values, made once a warp and not moved from a
+            // thread's registers for every product
+            const bool leader = elect_one();
+            const uint32_t id_s = kInt4 ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+            const uint32_t id_o = kInt4 ? idesc_f16(128, 128, 0, 1) : idesc_bf16(128, 128, 0, 1);   // V is MN-major
+            uint32_t runs = 0, ps = 0;   // bit t: parity of the runs and of the P tiles of row tile t
+            int slot = 0;                // the ring's next tile and its parity
+            uint32_t par = 0;
+            auto step = [&]() {
+                if (++slot == kRing) slot = 0, par ^= 1u;
+            };
+            // descriptors advance by addresses / 16 in their low bits
+            const uint64_t q_desc = sdesc_sw128(sbase + kOffQ, 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(sbase + kOffRing, 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(sbase + kOffRing, kHalf, 1024);
+            auto scores = [&](int t, int k_slot) {
+                const uint64_t qd = q_desc + (uint64_t)(t * (kTile >> 4));
+                const uint64_t kd = k_desc + (uint64_t)(k_slot * (kTile >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t o = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
+                    mma_bf16(kTmem + kColS + 128u * t, qd + o, kd + o, id_s, kk > 0);
+                }
+                mma_commit(&s_full[t]);
+            };
+            int n = __shfl_sync(0xffffffffu, w.n, 0);
+            while (n > 0 && ok) {
+                const int nt = __shfl_sync(0xffffffffu, row_tiles(w, per_tile), 0);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= nt || !ok) continue;
+                    ok = warp_wait(&q_full[t], (runs >> t) & 1u) && (t || warp_wait(&full[slot], par));
+                    if (!ok) continue;
+                    runs ^= 1u << t;
+                    tc_fence_after();
+                    if (leader) {
+                        scores(t, slot);
                         if (n == 1) mma_commit(&q_empty[t]);
-                        if (t == nt - 1) mma_commit(&empty[(2 * g) % kRing]);
+                        if (t == nt - 1) mma_commit(&empty[slot]);
                     }
-                    for (int s = 0; s < n && ok; ++s, ++g) {
-                        const int v = 2 * g + 1;
-                        const uint64_t vd = sdesc_sw128(sbase + kOffRing + (uint32_t)(v % kRing) * kTile, kHalf, 1024);
-                        for (int t = 0; t < nt; ++t) {
-                            const uint32_t pt = tmem + kColS + 128u * t;
-                            // everything the tile's two products need is waited for before the
-                            // first, so that nothing comes between them on the pipe
-                            ok = (t || (landed(v) && (s + 1 == n || landed(v + 1)))) &&
-                                 mbar_wait(&p_full[t], (ps >> t) & 1u);
-                            if (!ok) break;
-                            tc_fence_after();
-    #pragma unroll
+                }
+                step();
+                for (int s = 0; s < n && ok; ++s) {
+                    const int v_slot = slot;
+                    const uint32_t v_par = par;
+                    step();
+                    const bool more = s + 1 < n;   // its K tile is the next
+                    const uint64_t vd = v_desc + (uint64_t)(v_slot * (kTile >> 4));
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= nt || !ok) continue;
+                        ok = (t || warp_wait(&full[v_slot], v_par)) && warp_wait(&p_full[t], (ps >> t) & 1u);
+                        if (!ok) continue;
+                        ps ^= 1u << t;
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                mma_bf16_ta(tmem + kColO + 128u * t, pt + (uint32_t)kk * 8u,
-                                            vd + (uint32_t)kk * 128u, id_o, (s > 0 || kk > 0));
-                            ps ^= 1u << t;
-                            if (s + 1 < n) scores(t, v + 1);
+                                mma_bf16_ta(kTmem + kColO + 128u * t, kTmem + kColS + 128u * t + (uint32_t)kk * 8u,
+                                            vd + (uint64_t)(kk * 128), id_o, (s > 0 || kk > 0));
+                        }
+                        // waited for while the pipe works on the product with V
+                        if (!t && more && !(ok = warp_wait(&full[slot], par))) continue;
+                        if (leader) {
+                            if (more) scores(t, slot);
                             if (s + 2 == n) mma_commit(&q_empty[t]);
                             if (s + 1 == n) mma_commit(&o_done[t]);
                             if (t == nt - 1) {
-                                mma_commit(&empty[v % kRing]);
-                                if (s + 1 < n) mma_commit(&empty[(v + 1) % kRing]);
+                                mma_commit(&empty[v_slot]);
+                                if (more) mma_commit(&empty[slot]);
                             }
                         }
+                        __syncwarp();
                     }
+                    if (more) step();
                 }
-                mma_commit(drained);
-                if (!mbar_wait(drained, 0)) ok = false;
+                advance();
+                n = __shfl_sync(0xffffffffu, w.n, 0);
             }
+            if (leader) mma_commit(drained);
+            if (!warp_wait(drained, 0)) ok = false;
         } else if (warp == 2) {
             // ------------------------------------------------------------- Q by TMA
             if (lane == 0) {
@@ -374,15 +416,62 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 for (int t = 0; t < 2; ++t)   // the last copies land before the CTA exits
                     if (((begun >> t) & 1u) && !mbar_wait(&landed[t], ((runs >> t) & 1u) ^ 1u)) ok = false;
             }
+        } else if constexpr (kInt4) {
+            // ------------------------------------------------------------ scale pairs
+            // lane: keys lane + 32 i of a tile; a key nobody sees gets zeros: 0 * (c - 8) + 0
+            const int mb = 4 * n_groups, in_page = (1 << a.p.page_shift) - 1;
+            const int page_m = (int)a.p.page_stride * mb, slot_m = (int)a.p.slot_stride * mb;   // below 2^31 (checked)
+            int x = 0;   // tiles so far
+            for (; w.live() && ok; advance()) {
+                const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
+                const int n = w.n, klo = w.it.klo, khi = w.it.khi, key_base = first_key(w, 0) + lane;
+                const int64_t head = w.h * a.p.head_stride * mb;
+                for (int s = 0; s < n && ok; ++s) {
+                    int id[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = key_base + 128 * s + 32 * i;
+                        id[i] = -1;
+                        if (key >= klo && key < khi) id[i] = table[key >> a.p.page_shift] & 0x7fffffff;
+                    }
+                    int64_t at[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        at[i] = id[i] < 0 ? 0 : head + (int64_t)paged_id(a.p, id[i]) * page_m +
+                                                    (int64_t)((key_base + 128 * s + 32 * i) & in_page) * slot_m;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++x) {
+                        const int stage = x % kStaged;
+                        if (x >= kStaged && !warp_wait(&c_empty[stage], (uint32_t)(x / kStaged - 1) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint8_t* pairs = kv ? a.p.vs : a.p.ks;
+                        const uint32_t d = sbase + kOffStage + (uint32_t)stage * kStage + kStageCodes +
+                                           (uint32_t)(mb * lane);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t dst = d + (uint32_t)(32 * mb * i);
+                            if (n_groups == 4) copy_async<16>(dst, pairs + at[i], id[i] >= 0);
+                            else if (n_groups == 2) copy_async<8>(dst, pairs + at[i], id[i] >= 0);
+                            else copy_async<4>(dst, pairs + at[i], id[i] >= 0);
+                        }
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                                         smem_u32(&c_full[stage]))
+                                     : "memory");
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp < 12) {
         reg_inc<kInt4 ? 176 : 216>();
         // -------------------------------------------------------------- softmax
         const int t = warp >= 8 ? 1 : 0, m = 32 * (warp & 3) + lane;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + kColS + 128u * t + lane_base, to = tmem + kColO + 128u * t + lane_base;
+        const uint32_t ts = kTmem + kColS + 128u * t + lane_base, to = kTmem + kColO + 128u * t + lane_base;
         const float sl2 = a.scale * kLog2e;
-        int g = 0, tile = 0, runs = 0;   // tiles of the CTA, tiles and runs of this row tile
+        int g = 0, tile = 0, runs = 0, biases = 0;   // tiles of the CTA; tiles, runs and biased tiles of this row tile
         auto skip = [&]() {   // to the next run this row tile has rows in; the units passed are counted
             while (w.live() && t >= row_tiles(w, per_tile)) {
                 g += w.n;
@@ -454,57 +543,62 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
             float m_run = -INFINITY, m_neg = 0.f, l_run = 0.f;
             for (int s = 0; s < n; ++s, ++g, ++tile) {
                 const int key0 = key_base + 128 * s;
-                uint32_t lw[4] = {0u, 0u, 0u, 0u}, sw[4] = {0u, 0u, 0u, 0u};   // mask words, under the wait
+                uint32_t lw = 0u, sw = 0u;   // lane: mask word lane % 4, on its way during the wait
                 if (kExtra && (a.loc || a.snk)) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int word = (key0 >> 5) + q;
-                        if (word >= a.words) continue;
-                        if (a.loc) lw[q] = a.loc[(int64_t)seq * a.words + word];
-                        if (a.snk) sw[q] = a.snk[(int64_t)seq * a.words + word];
-                    }
+                    const int64_t word = (int64_t)seq * a.words + min((key0 >> 5) + (lane & 3), a.words - 1);
+                    if (a.loc) lw = a.loc[word];
+                    if (a.snk) sw = a.snk[word];
                 }
                 if (!warp_wait(&s_full[t], (uint32_t)tile & 1u)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                // the keys' biases are the same for every row: each warp writes those of 32
+                // keys, to be read as broadcasts.  The last tile's have been read: its P
+                // was waited for before these scores.
+                const bool biased = kExtra && __any_sync(0xffffffffu, (lw | sw) != 0u);
+                if (biased) {
+                    lw = __shfl_sync(0xffffffffu, lw, warp & 3);
+                    sw = __shfl_sync(0xffffffffu, sw, warp & 3);
+                    const float bias = ((lw >> lane) & 1u ? a.alpha * kLog2e : 0.f) +
+                                       ((sw >> lane) & 1u ? a.beta * kLog2e : 0.f);
+                    reinterpret_cast<float*>(smem + kOffBias + 512 * t)[m] = bias;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b_full[t]);
+                }
                 float x[128], ls = lsr;
                 tmem_ld128(ts, x);
                 if constexpr (kExtra) {
-                    ls = 1.f;
-                    const float cap_in = a.softcap > 0.f ? 2.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
                     if (a.softcap > 0.f) {
-                        const float c_in = lsr * cap_in;
+                        const float cap_out = a.softcap * kLog2e, c_in = lsr * (2.f / a.softcap);
 #pragma unroll
                         for (int k = 0; k < 128; ++k)   // cap tanh(u) = cap (1 - 2 / (1 + exp(2u)))
                             x[k] = fmaf(-2.f * cap_out, __fdividef(1.f, 1.f + ex2(x[k] * c_in)), cap_out);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 128; ++k) x[k] *= lsr;
+                        ls = 1.f;
                     }
-                    if (a.loc || a.snk) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            // the words are the same for every row: words with no bit set cost
-                            // nothing, wholly local ones an addition a key
-                            if ((lw[q] | sw[q]) == 0u) continue;
-                            if (sw[q] == 0u && lw[q] == 0xffffffffu) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) x[32 * q + k] += a.alpha * kLog2e;
-                                continue;
-                            }
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                float b = ((lw[q] >> k) & 1u) ? a.alpha * kLog2e : 0.f;
-                                b += ((sw[q] >> k) & 1u) ? a.beta * kLog2e : 0.f;
-                                x[32 * q + k] += b;
-                            }
+                    if (biased) {
+                        if (!warp_wait(&b_full[t], (uint32_t)biases & 1u)) {
+                            ok = false;
+                            break;
                         }
-                    }
-                    if (a.slopes) {
+                        ++biases;
+                        const float4* bias = reinterpret_cast<const float4*>(smem + kOffBias + 512 * t);
+                        const float2 l2 = make_float2(ls, ls);
 #pragma unroll
-                        for (int k = 0; k < 128; ++k) x[k] = fmaf(-slope, (float)abs(gpos - key0 - k), x[k]);
+                        for (int k = 0; k < 128; k += 4) {
+                            const float4 b = bias[k / 4];
+                            const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), l2, make_float2(b.x, b.y));
+                            const float2 z = __ffma2_rn(make_float2(x[k + 2], x[k + 3]), l2, make_float2(b.z, b.w));
+                            x[k] = y.x, x[k + 1] = y.y, x[k + 2] = z.x, x[k + 3] = z.y;
+                        }
+                        ls = 1.f;
+                    }
+                    if (a.slopes) {   // the distance's roundings, 2^-24 of it, are the product's own size
+                        const float ahead = (float)(gpos - key0);
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) x[k] = fmaf(-slope, fabsf(ahead - (float)k), x[k] * ls);
+                        ls = 1.f;
                     }
                 }
                 if (key0 + 128 > all_hi) {   // warp-uniform, as the next
@@ -650,125 +744,68 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     } else if constexpr (kInt4) {
         reg_dec<88>();
         // -------------------------------------------------------------- 4-bit tiles to fp16
-        // thread (key, q): keys ct / 4 + 32 i, the 16 bytes that hold dims 8 q..
-        // of each 32-dim block; the quad copies the key's scale pairs
-        const int ct = threadIdx.x - 384, q = ct & 3, kr = ct >> 2;
-        const int mb = 4 * n_groups, lg = n_groups >> 1;   // log2(n_groups) for 1, 2, 4
+        // a warp's keys are 32 of the tile: lane (kr, q) takes keys kr + 8 i, the 16 bytes
+        // that hold dims 8 q.. of each 32-dim block.  Eight lanes that read or write
+        // together hold keys p and p ^ 5, whose codes and whose swizzled chunks lie in
+        // different banks.
+        const int q = lane & 3, kr = 32 * (warp & 3) + ((lane >> 3) ^ ((lane & 4) ? 5 : 0));
+        const int mb = 4 * n_groups;
         const uint32_t stage0 = sbase + kOffStage;
-        int x = 0, y = 0;        // tiles converted, tiles asked for
-        int s = 0;               // unit being asked for, of run w
-        int id[4];               // pages of the next unit's keys; -1: the key is not seen
-        int64_t at[4];           // code bytes from slot 0 of page 0 of the unit being asked for
-        int64_t head = 0;        // and from there to the run's head
-        auto locate = [&]() {
-            if (!w.live()) return;
-            const int* table = a.p.table + (int64_t)w.it.seq * a.p.max_pages;
-            const int key0 = first_key(w, s) + kr, klo = w.it.klo, khi = w.it.khi;
-            head = (int64_t)w.h * a.p.head_stride * 64;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = key0 + 32 * i;
-                id[i] = -1;
-                if (key >= klo && key < khi) id[i] = table[key >> a.p.page_shift] & 0x7fffffff;   // checked when used
-            }
-        };
-        // ask for the next tile (K, then V at the same places); a key nobody sees
-        // gets zeros: 0 * (c - 8) + 0
-        auto ask = [&]() {
-            if ((y & 1) || w.live()) {
-                const bool is_v = y & 1;
-                if (!is_v) {
-                    // below 2^31 (checked)
-                    const int page_b = (int)a.p.page_stride * 64, slot_b = (int)a.p.slot_stride * 64;
-                    const int in_page = (1 << a.p.page_shift) - 1, slot = (first_key(w, s) + kr) & in_page;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        at[i] = id[i] < 0 ? -1 : head + (int64_t)paged_id(a.p, id[i]) * page_b +
-                                                     (int64_t)((slot + 32 * i) & in_page) * slot_b;
-                    if (++s == w.n) {
-                        s = 0;
-                        advance();
-                    }
-                    locate();
+        int x = 0;   // tiles so far
+        for (; w.live() && ok; advance())
+            for (int left = 2 * w.n; left > 0; --left, ++x) {
+                const int slot = x % kRing, stage = x % kStaged;
+                if (!warp_wait(&c_full[stage], (uint32_t)(x / kStaged) & 1u) ||
+                    (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u))) {
+                    ok = false;
+                    break;
                 }
-                const uint8_t* codes = (is_v ? a.p.v : a.p.k) + 16 * q;
-                const uint8_t* pairs = is_v ? a.p.vs : a.p.ks;
-                const uint32_t d = stage0 + (uint32_t)(y % kStaged) * kStage;
+                const uint32_t d = stage0 + (uint32_t)stage * kStage;
+                uint4 cw[4];
+                uint32_t cm[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int k = kr + 32 * i;
-                    const uint32_t dc = d + 64u * k + 16u * q, dm = d + kStageCodes + (uint32_t)(mb * k);
-                    if (at[i] < 0) {
-                        sts16(dc, make_uint4(0u, 0u, 0u, 0u));
-                        if (q < n_groups)
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dm + 4u * q), "r"(0u) : "memory");
-                        continue;
+                    const int k = kr + 8 * i;
+                    cw[i] = lds16(d + 64u * k + 16u * q);
+                    const uint32_t dm = d + kStageCodes + (uint32_t)(mb * k);
+                    if (n_groups == 4) {
+                        const uint4 v = lds16(dm);
+                        cm[i][0] = v.x, cm[i][1] = v.y, cm[i][2] = v.z, cm[i][3] = v.w;
+                    } else {
+                        cm[i][0] = cm[i][1] = lds4(dm);
+                        cm[i][2] = cm[i][3] = n_groups == 2 ? lds4(dm + 4u) : cm[i][0];
                     }
-                    copy_async<16>(dc, codes + at[i]);
-                    // the key's pairs, a word for each of the quad's first lanes
-                    if (q < n_groups) copy_async<4>(dm + 4u * q, pairs + (at[i] >> (4 - lg)) + 4 * q);
                 }
-                ++y;
-            }
-            copy_commit();
-        };
-        locate();
-        for (int i = 0; i < kStaged; ++i) ask();
-        while (x < y) {
-            const int slot = x % kRing;
-            copy_wait<kStaged - 1>();
-            __syncwarp();
-            if (x >= kRing && !warp_wait(&empty[slot], (uint32_t)(x / kRing - 1) & 1u)) {
-                ok = false;
-                break;
-            }
-            const uint32_t d = stage0 + (uint32_t)(x % kStaged) * kStage;
-            uint4 cw[4];
-            uint32_t cm[4][4];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c_empty[stage]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = kr + 32 * i;
-                cw[i] = lds16(d + 64u * k + 16u * q);
-                const uint32_t dm = d + kStageCodes + (uint32_t)(mb * k);
-                if (n_groups == 4) {
-                    const uint4 v = lds16(dm);
-                    cm[i][0] = v.x, cm[i][1] = v.y, cm[i][2] = v.z, cm[i][3] = v.w;
-                } else {
-                    cm[i][0] = cm[i][1] = lds4(dm);
-                    cm[i][2] = cm[i][3] = n_groups == 2 ? lds4(dm + 4u) : cm[i][0];
+                for (int i = 0; i < 4; ++i) {
+                    const int k = kr + 8 * i;
+                    const uint32_t dst = sbase + kOffRing + (uint32_t)slot * kTile + (uint32_t)k * 128u;
+                    uint4 v[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {   // 32-dim block: units of the chunk's two 8-byte halves
+                        const uint32_t z = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w,
+                                                       (b & 1) ? 0x7632 : 0x5410);
+                        const uint32_t sc = __byte_perm(cm[i][b], 0u, 0x1010);
+                        const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[i][b], 0u, 0x3232));
+                        v[b] = make_uint4(hfma2(even8(z), sc, o8), hfma2(odd8(z), sc, o8),
+                                          hfma2(even8(z >> 8), sc, o8), hfma2(odd8(z >> 8), sc, o8));
+                    }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        sts16(dst + (uint32_t)(b >> 1) * kHalf + (uint32_t)(((4 * (b & 1) + q) ^ (k & 7)) << 4), v[b]);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[slot]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = kr + 32 * i;
-                const uint32_t dst = sbase + kOffRing + (uint32_t)slot * kTile + (uint32_t)k * 128u;
-                uint4 v[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {   // 32-dim block: units of the chunk's two 8-byte halves
-                    const uint32_t z = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w,
-                                                   (b & 1) ? 0x7632 : 0x5410);
-                    const uint32_t sc = __byte_perm(cm[i][b], 0u, 0x1010);
-                    const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[i][b], 0u, 0x3232));
-                    v[b] = make_uint4(hfma2(even8(z), sc, o8), hfma2(odd8(z), sc, o8), hfma2(even8(z >> 8), sc, o8),
-                                      hfma2(odd8(z >> 8), sc, o8));
-                }
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    sts16(dst + (uint32_t)(b >> 1) * kHalf + (uint32_t)(((4 * (b & 1) + q) ^ (k & 7)) << 4), v[b]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();   // the packed tile has been read, too
-            if (lane == 0) mbar_arrive(&full[slot]);
-            ++x;
-            ask();
-        }
-        copy_wait<0>();
     }
     if (!ok && lane == 0) paged_err(a.p.err, DEV_ERR_TIMEOUT, warp);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(kTmem, 512);
 }
 
 template <bool kInt4, bool kExtra>
@@ -791,16 +828,20 @@ cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStrea
     if (!make_tmap_3d_bf16(&q, a.q, 128, (uint64_t)a.n_q_heads, (uint64_t)a.r.n_rows, 256, (uint64_t)a.q_stride * 2, 64,
                            (uint32_t)a.G, (uint32_t)(128 / a.G), why))
         return cudaErrorInvalidValue;
-    if (format == KVR_INT4)
-        return extra ? launch<true, true>(k, v, q, a, 128 / group, s) : launch<true, false>(k, v, q, a, 128 / group, s);
-    // pages as (dim, slot, head, page); a box is one page's share of a 128-key tile, half a row wide
-    const uint64_t dims[4] = {128, 1ull << a.p.page_shift, (uint64_t)a.p.n_kv_heads, (uint64_t)a.p.n_pages};
-    const uint64_t strides[3] = {(uint64_t)a.p.slot_stride * 256, (uint64_t)a.p.head_stride * 256,
-                                 (uint64_t)a.p.page_stride * 256};
+    // pages as (dim, slot, head, page); a box is one page's share of a 128-key tile:
+    // half a row wide, or a row of codes
+    const bool int4 = format == KVR_INT4;
+    const uint64_t row = int4 ? 64 : 256;
+    const uint64_t dims[4] = {int4 ? row : 128, 1ull << a.p.page_shift, (uint64_t)a.p.n_kv_heads,
+                              (uint64_t)a.p.n_pages};
+    const uint64_t strides[3] = {(uint64_t)a.p.slot_stride * row, (uint64_t)a.p.head_stride * row,
+                                 (uint64_t)a.p.page_stride * row};
     const uint32_t box[4] = {64, 1u << (a.p.page_shift < 7 ? a.p.page_shift : 7), 1, 1};
-    if (!make_tmap_4d_bf16(&k, a.p.k, dims, strides, box, why) ||
-        !make_tmap_4d_bf16(&v, a.p.v, dims, strides, box, why))
+    auto pages = int4 ? make_tmap_4d_bytes : make_tmap_4d_bf16;
+    if (!pages(&k, a.p.k, dims, strides, box, why) || !pages(&v, a.p.v, dims, strides, box, why))
         return cudaErrorInvalidValue;
+    if (int4)
+        return extra ? launch<true, true>(k, v, q, a, 128 / group, s) : launch<true, false>(k, v, q, a, 128 / group, s);
     return extra ? launch<false, true>(k, v, q, a, 0, s) : launch<false, false>(k, v, q, a, 0, s);
 }
 
