@@ -37,8 +37,10 @@
 // exponentials (1024).  Measured: 1.36 PFLOP/s at 4096 rows over 8192 keys of a
 // 32/8-head model (0.30 ms), about 3000 cycles a unit, close to the chain of a row
 // tile that bounds it: softmax 1450, its two products 1024, three hand-overs of
-// 100-150.  4 bits: 0.93 PFLOP/s at 8192 causal rows, bound by the conversion
-// (1400 cycles for each of a unit's two tiles, against the softmax's issue slots).
+// 100-150; 1.22 PFLOP/s at 8192 causal rows (0.45 ms).  4 bits: 1.01 PFLOP/s there
+// (0.54 ms); softmax and conversion share the issue slots, 3000 of a unit's 4000
+// cycles.  The group count is a template argument: a pair per 32 dims whatever the
+// group took 0.59 ms.
 // The runs' bookkeeping lives in shared memory, a copy per warp: a spilled register
 // costs an L2 round trip here, where shared memory takes all but a few KB of L1.
 // Every wait is bounded; on a timeout the CTA records it, drains its copies and
@@ -183,10 +185,12 @@ __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.al
 __device__ __forceinline__ int first_key(const PagedWalk& w, int s) { return ((w.it.klo >> 7) + w.off + s) << 7; }
 __device__ __forceinline__ int row_tiles(const PagedWalk& w, int per_tile) { return w.it.rows > per_tile ? 2 : 1; }
 
-template <bool kInt4, bool kExtra>
-__global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
+// NG: scale groups of a 4-bit row, 0 for bf16 pages; kExtra: cap, biases or slopes
+template <int NG, bool kExtra>
+__global__ void __launch_bounds__(NG ? 512 : 384, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ CUtensorMap tmQ, PagedAttn a, int n_groups) {
+                    const __grid_constant__ CUtensorMap tmQ, PagedAttn a) {
+    constexpr bool kInt4 = NG != 0;
     constexpr int kRing = kInt4 ? 4 : 5;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -419,7 +423,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         } else if constexpr (kInt4) {
             // ------------------------------------------------------------ scale pairs
             // lane: keys lane + 32 i of a tile; a key nobody sees gets zeros: 0 * (c - 8) + 0
-            const int mb = 4 * n_groups, in_page = (1 << a.p.page_shift) - 1;
+            constexpr int mb = 4 * NG;   // bytes of a row's pairs
+            const int in_page = (1 << a.p.page_shift) - 1;
             const int page_m = (int)a.p.page_stride * mb, slot_m = (int)a.p.slot_stride * mb;   // below 2^31 (checked)
             int x = 0;   // tiles so far
             for (; w.live() && ok; advance()) {
@@ -452,9 +457,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t dst = d + (uint32_t)(32 * mb * i);
-                            if (n_groups == 4) copy_async<16>(dst, pairs + at[i], id[i] >= 0);
-                            else if (n_groups == 2) copy_async<8>(dst, pairs + at[i], id[i] >= 0);
-                            else copy_async<4>(dst, pairs + at[i], id[i] >= 0);
+                            copy_async<mb>(dst, pairs + at[i], id[i] >= 0);
                         }
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                                          smem_u32(&c_full[stage]))
@@ -749,7 +752,7 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
         // together hold keys p and p ^ 5, whose codes and whose swizzled chunks lie in
         // different banks.
         const int q = lane & 3, kr = 32 * (warp & 3) + ((lane >> 3) ^ ((lane & 4) ? 5 : 0));
-        const int mb = 4 * n_groups;
+        constexpr int mb = 4 * NG;
         const uint32_t stage0 = sbase + kOffStage;
         int x = 0;   // tiles so far
         for (; w.live() && ok; advance())
@@ -762,18 +765,18 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                 }
                 const uint32_t d = stage0 + (uint32_t)stage * kStage;
                 uint4 cw[4];
-                uint32_t cm[4][4];
+                uint32_t cm[4][NG];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int k = kr + 8 * i;
                     cw[i] = lds16(d + 64u * k + 16u * q);
                     const uint32_t dm = d + kStageCodes + (uint32_t)(mb * k);
-                    if (n_groups == 4) {
+                    if constexpr (NG == 4) {
                         const uint4 v = lds16(dm);
                         cm[i][0] = v.x, cm[i][1] = v.y, cm[i][2] = v.z, cm[i][3] = v.w;
                     } else {
-                        cm[i][0] = cm[i][1] = lds4(dm);
-                        cm[i][2] = cm[i][3] = n_groups == 2 ? lds4(dm + 4u) : cm[i][0];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) cm[i][g] = lds4(dm + 4u * g);
                     }
                 }
                 __syncwarp();
@@ -787,8 +790,8 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
                     for (int b = 0; b < 4; ++b) {   // 32-dim block: units of the chunk's two 8-byte halves
                         const uint32_t z = __byte_perm(b < 2 ? cw[i].x : cw[i].y, b < 2 ? cw[i].z : cw[i].w,
                                                        (b & 1) ? 0x7632 : 0x5410);
-                        const uint32_t sc = __byte_perm(cm[i][b], 0u, 0x1010);
-                        const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(cm[i][b], 0u, 0x3232));
+                        const uint32_t pair = cm[i][b * NG / 4], sc = __byte_perm(pair, 0u, 0x1010);
+                        const uint32_t o8 = hfma2(sc, 0x48004800u, __byte_perm(pair, 0u, 0x3232));
                         v[b] = make_uint4(hfma2(even8(z), sc, o8), hfma2(odd8(z), sc, o8),
                                           hfma2(even8(z >> 8), sc, o8), hfma2(odd8(z >> 8), sc, o8));
                     }
@@ -808,21 +811,25 @@ __global__ void __launch_bounds__(kInt4 ? 512 : 384, 1)
     if (warp == 1) tmem_dealloc(kTmem, 512);
 }
 
-template <bool kInt4, bool kExtra>
-cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const PagedAttn& a, int n_groups,
+template <int NG, bool kExtra>
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const PagedAttn& a,
                    cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(paged_tc_kernel<kInt4, kExtra>, (int)kSmem, &allowed);
+    const cudaError_t e = allow_smem(paged_tc_kernel<NG, kExtra>, (int)kSmem, &allowed);
     if (e != cudaSuccess) return e;
-    KVR_LAUNCH(paged_tc_kernel<kInt4, kExtra>, dim3((unsigned)a.n_cta), dim3(kInt4 ? 512 : 384), kSmem, s, k, v, q, a,
-               n_groups);
+    KVR_LAUNCH(paged_tc_kernel<NG, kExtra>, dim3((unsigned)a.n_cta), dim3(NG ? 512 : 384), kSmem, s, k, v, q, a);
     return cudaSuccess;
+}
+template <int NG>
+cudaError_t launch_ng(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const PagedAttn& a,
+                      cudaStream_t s) {
+    const bool extra = a.softcap > 0.f || a.loc || a.snk || a.slopes;
+    return extra ? launch<NG, true>(k, v, q, a, s) : launch<NG, false>(k, v, q, a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStream_t s, std::string* why) {
-    const bool extra = a.softcap > 0.f || a.loc || a.snk || a.slopes;
     CUtensorMap k{}, v{}, q{};
     // Q as (dim, head, row): a box is a row tile of one K/V head, positions x query heads
     if (!make_tmap_3d_bf16(&q, a.q, 128, (uint64_t)a.n_q_heads, (uint64_t)a.r.n_rows, 256, (uint64_t)a.q_stride * 2, 64,
@@ -840,9 +847,10 @@ cudaError_t launch_paged_tc(int format, int group, const PagedAttn& a, cudaStrea
     auto pages = int4 ? make_tmap_4d_bytes : make_tmap_4d_bf16;
     if (!pages(&k, a.p.k, dims, strides, box, why) || !pages(&v, a.p.v, dims, strides, box, why))
         return cudaErrorInvalidValue;
-    if (int4)
-        return extra ? launch<true, true>(k, v, q, a, 128 / group, s) : launch<true, false>(k, v, q, a, 128 / group, s);
-    return extra ? launch<false, true>(k, v, q, a, 0, s) : launch<false, false>(k, v, q, a, 0, s);
+    if (!int4) return launch_ng<0>(k, v, q, a, s);
+    if (group == 32) return launch_ng<4>(k, v, q, a, s);
+    if (group == 64) return launch_ng<2>(k, v, q, a, s);
+    return launch_ng<1>(k, v, q, a, s);
 }
 
 }  // namespace kvr
