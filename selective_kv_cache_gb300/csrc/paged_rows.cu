@@ -201,95 +201,98 @@ __global__ void __launch_bounds__(kRowThreads) append_int4_kernel(PagedRowIo a) 
     // every thread of a warp runs the same rounds: the shuffles below need
     // the whole warp
     for (int x0 = 0; x0 < total; x0 += kBatch * kStep) {
-    uint2 raw[kBatch][4];
+        uint2 raw[kBatch][4];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-        const RowUnit un = unit_of(a, x0 + j * kStep + threadIdx.x / 8);
-        const uint8_t* src = unit_src(a, un, 256) + 8 * v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            raw[j][i] = un.live ? *reinterpret_cast<const uint2*>(src + 64 * i) : make_uint2(0u, 0u);
-    }
-    if (x0 == 0) {
-        find_slots<true>(a, slots);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-        const RowUnit un = unit_of(a, x0 + j * kStep + threadIdx.x / 8);
-        const RowSlot slot = slots[un.i];
-        const int u = un.u;
-        const int64_t r = un.r, row = slot.at;
-        const bool live = un.live && row >= 0, is_q = u >= 2 * H, is_v = !is_q && u >= H;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint2 w = raw[j][i];
-            x[4 * i] = __uint_as_float(w.x << 16);
-            x[4 * i + 1] = __uint_as_float(w.x & 0xffff0000u);
-            x[4 * i + 2] = __uint_as_float(w.y << 16);
-            x[4 * i + 3] = __uint_as_float(w.y & 0xffff0000u);
-        }
-        if (a.rope && live && !is_v) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {   // dims 4v.. and 32 + 4v.. with their pairs 64 further
-                const float4* cs = reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * 64 + 32 * i + 4 * v);
-                const float4 c0 = cs[0], c1 = cs[1];
-                turn(x[4 * i], x[4 * i + 8], make_float2(c0.x, c0.y));
-                turn(x[4 * i + 1], x[4 * i + 9], make_float2(c0.z, c0.w));
-                turn(x[4 * i + 2], x[4 * i + 10], make_float2(c1.x, c1.y));
-                turn(x[4 * i + 3], x[4 * i + 11], make_float2(c1.z, c1.w));
-            }
-        }
-        if (live && is_q) {
-            uint8_t* dst = a.q_out + (r * a.n_q_heads + u - 2 * H) * 256;
+        for (int j = 0; j < kBatch; ++j) {
+            const RowUnit un = unit_of(a, x0 + j * kStep + threadIdx.x / 8);
+            const uint8_t* src = unit_src(a, un, 256) + 8 * v;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint2*>(dst + 64 * i + 8 * v) =
-                    make_uint2(pack2(x[4 * i], x[4 * i + 1]), pack2(x[4 * i + 2], x[4 * i + 3]));
+                raw[j][i] = un.live ? *reinterpret_cast<const uint2*>(src + 64 * i) : make_uint2(0u, 0u);
         }
-        if (__all_sync(0xffffffffu, !live || is_q)) continue;   // nothing to quantise in this warp
-        float lo[NG], hi[NG];
+        if (x0 == 0) {
+            find_slots<true>(a, slots);
+            __syncthreads();
+        }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -32768.f), 32768.f);   // 15 s + o stays in fp16's range
+        for (int j = 0; j < kBatch; ++j) {
+            const RowUnit un = unit_of(a, x0 + j * kStep + threadIdx.x / 8);
+            const RowSlot slot = slots[un.i];
+            const int u = un.u;
+            const int64_t r = un.r, row = slot.at;
+            const bool live = un.live && row >= 0, is_q = u >= 2 * H, is_v = !is_q && u >= H;
+            float x[16];
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            lo[n] = hi[n] = x[4 * kJoin * n];
-#pragma unroll
-            for (int e = 1; e < 4 * kJoin; ++e) {
-                lo[n] = fminf(lo[n], x[4 * kJoin * n + e]);
-                hi[n] = fmaxf(hi[n], x[4 * kJoin * n + e]);
+            for (int i = 0; i < 4; ++i) {
+                const uint2 w = raw[j][i];
+                x[4 * i] = __uint_as_float(w.x << 16);
+                x[4 * i + 1] = __uint_as_float(w.x & 0xffff0000u);
+                x[4 * i + 2] = __uint_as_float(w.y << 16);
+                x[4 * i + 3] = __uint_as_float(w.y & 0xffff0000u);
             }
-            extremum8(lo[n], hi[n]);
-        }
-        if (!live || is_q) continue;
-        const int64_t at = row + (u - (is_v ? H : 0)) * a.p.head_stride;
-        __half2* meta = reinterpret_cast<__half2*>((is_v ? a.p.vs : a.p.ks) + at * (4 * NG));
-        uint32_t unit[4];
+            if (a.rope && live && !is_v) {
+                const float4* cs = reinterpret_cast<const float4*>(a.rope + (int64_t)slot.g * 64 + 4 * v);
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            // scale and offset are rounded to fp16 first and the codes chosen
-            // against the rounded ones, so their rounding costs range, not
-            // bias: a value is off by half a step plus at most the offset's
-            // rounding (2^-11 of it)
-            const __half sh = __float2half_rn(__fmul_rn(__fsub_rn(hi[n], lo[n]), 1.0f / 15.0f));
-            const __half oh = __float2half_rn(lo[n]);
-            const float s = __half2float(sh), o = __half2float(oh);
-            const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
-            if (v == n) meta[n] = __halves2half2(sh, oh);   // NG <= 4 of the eight threads
-#pragma unroll
-            for (int i = n * kJoin; i < (n + 1) * kJoin; ++i) {
-                unit[i] = 0u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[4 * i + e], o), inv)), 0.f), 15.f);
-                    unit[i] |= (uint32_t)c << (4 * e);
+                for (int i = 0; i < 2; ++i) {   // dims 4v.. and 32 + 4v.. with their pairs 64 further
+                    const float4 c0 = cs[16 * i], c1 = cs[16 * i + 1];
+                    turn(x[4 * i], x[4 * i + 8], make_float2(c0.x, c0.y));
+                    turn(x[4 * i + 1], x[4 * i + 9], make_float2(c0.z, c0.w));
+                    turn(x[4 * i + 2], x[4 * i + 10], make_float2(c1.x, c1.y));
+                    turn(x[4 * i + 3], x[4 * i + 11], make_float2(c1.z, c1.w));
                 }
             }
+            if (live && is_q) {
+                uint8_t* dst = a.q_out + (r * a.n_q_heads + u - 2 * H) * 256;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint2*>(dst + 64 * i + 8 * v) =
+                        make_uint2(pack2(x[4 * i], x[4 * i + 1]), pack2(x[4 * i + 2], x[4 * i + 3]));
+            }
+            if (__all_sync(0xffffffffu, !live || is_q)) continue;   // nothing to quantise in this warp
+            float lo[NG], hi[NG];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)   // 15 s + o stays in fp16's range
+                x[e] = fminf(fmaxf(x[e], -32768.f), 32768.f);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                lo[n] = hi[n] = x[4 * kJoin * n];
+#pragma unroll
+                for (int e = 1; e < 4 * kJoin; ++e) {
+                    lo[n] = fminf(lo[n], x[4 * kJoin * n + e]);
+                    hi[n] = fmaxf(hi[n], x[4 * kJoin * n + e]);
+                }
+                extremum8(lo[n], hi[n]);
+            }
+            if (!live || is_q) continue;
+            const int64_t at = row + (u - (is_v ? H : 0)) * a.p.head_stride;
+            __half2* meta = reinterpret_cast<__half2*>((is_v ? a.p.vs : a.p.ks) + at * (4 * NG));
+            uint32_t unit[4];
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                // scale and offset are rounded to fp16 first and the codes chosen
+                // against the rounded ones, so their rounding costs range, not
+                // bias: a value is off by half a step plus at most the offset's
+                // rounding (2^-11 of it)
+                const __half sh = __float2half_rn(__fmul_rn(__fsub_rn(hi[n], lo[n]), 1.0f / 15.0f));
+                const __half oh = __float2half_rn(lo[n]);
+                const float s = __half2float(sh), o = __half2float(oh);
+                const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+                if (v == n) meta[n] = __halves2half2(sh, oh);   // NG <= 4 of the eight threads
+#pragma unroll
+                for (int i = n * kJoin; i < (n + 1) * kJoin; ++i) {
+                    // 2^23 + 2^22 leaves the rounded code in the low bits; bits 16 and up of the
+                    // sum are not used
+                    uint32_t c[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c[e] = __float_as_uint(
+                            __fadd_rn(fminf(fmaxf(__fmul_rn(__fsub_rn(x[4 * i + e], o), inv), 0.f), 15.f), 12582912.f));
+                    unit[i] = c[0] + (c[1] << 4) + (c[2] << 8) + (c[3] << 12);
+                }
+            }
+            *reinterpret_cast<uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v) =
+                make_uint2(__byte_perm(unit[0], unit[1], 0x5410), __byte_perm(unit[2], unit[3], 0x5410));
         }
-        *reinterpret_cast<uint2*>((is_v ? a.p.v : a.p.k) + at * 64 + 8 * v) =
-            make_uint2(unit[0] | (unit[1] << 16), unit[2] | (unit[3] << 16));
-    }
     }
 }
 
