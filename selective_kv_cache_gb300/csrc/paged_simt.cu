@@ -11,7 +11,10 @@
 // output stays in registers.  The next K tile is copied while the output's
 // products run and the next V tile while the scores' do, so one buffer of each
 // is enough and four CTAs fit an SM.  Shared memory's reads bound it: 8
-// wavefronts of K and q for 16 products a lane.
+// wavefronts of K and q for 16 products a lane.  Measured: 4.49 ms, 21 TFLOP/s, at
+// 8 x 300 rows over 4096 keys of a 32/8-head model; 25 us at 2 x 64 rows over 1024
+// keys of 4 heads of 64.  Tiles twice as tall and wide (255 registers, two CTAs an
+// SM) took 4.10 ms and 31 us.
 #include <type_traits>
 
 #include "paged.h"
