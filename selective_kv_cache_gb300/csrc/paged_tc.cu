@@ -37,10 +37,11 @@
 // exponentials (1024).  Measured: 1.36 PFLOP/s at 4096 rows over 8192 keys of a
 // 32/8-head model (0.30 ms), about 3000 cycles a unit, close to the chain of a row
 // tile that bounds it: softmax 1450, its two products 1024, three hand-overs of
-// 100-150; 1.22 PFLOP/s at 8192 causal rows (0.45 ms).  4 bits: 1.01 PFLOP/s there
-// (0.54 ms); softmax and conversion share the issue slots, 3000 of a unit's 4000
+// 100-150; 1.42 PFLOP/s at 8192 causal rows (0.39 ms).  4 bits: 1.10 PFLOP/s there
+// (0.49 ms); softmax and conversion share the issue slots, 3000 of a unit's 3700
 // cycles.  The group count is a template argument: a pair per 32 dims whatever the
-// group took 0.59 ms.
+// group took 8 % longer.  Rows leave as one 32-byte store a thread: with 16-byte
+// halves exchanged between neighbours a run's end took 4500 cycles in place of 3000.
 // The runs' bookkeeping lives in shared memory, a copy per warp: a spilled register
 // costs an L2 round trip here, where shared memory takes all but a few KB of L1.
 // Every wait is bounded; on a timeout the CTA records it, drains its copies and
@@ -137,6 +138,12 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
         asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                      "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
                      "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])::"memory");
+}
+// a sector of a row; 32-byte aligned
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 // N bytes, or zeros
 template <int N>
@@ -521,26 +528,39 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                 if (lane == 0) mbar_arrive(&q_full[t]);
             }
         };
-        skip();
-        if (w.live()) load_q();
-        while (w.live() && ok) {
-            const bool whole = w.whole();
-            const size_t slot = ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.tile_rows;
-            const int p = t * per_tile + m / G, gi = m % G;
-            const bool valid = m < per_tile * G && p < w.it.rows;
-            const int64_t row = w.it.row0 + p;
-            const int head = w.h * G + gi;
-            // ---- what the row sees
-            int lo = w.it.klo, hi = w.it.khi, gpos = 0;
-            float slope = 0.f;
-            if (valid) {
-                paged_interval(a, (int)row, w.it.kv, &lo, &hi);
+        // this thread's row of a run, and what it sees
+        struct Row {
+            bool whole, valid;
+            int row, head, lo, hi, pos;
+            float slope;
+            size_t slot;
+        };
+        Row next{};
+        auto load_row = [&]() {
+            const int p = t * per_tile + m / G;
+            next.whole = w.whole();
+            next.slot = ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.tile_rows;
+            next.valid = m < per_tile * G && p < w.it.rows;
+            next.row = w.it.row0 + p;
+            next.head = w.h * G + m % G;
+            next.lo = w.it.klo, next.hi = w.it.khi;
+            if (next.valid) {
+                paged_interval(a, next.row, w.it.kv, &next.lo, &next.hi);
                 if (kExtra && a.slopes) {
-                    gpos = a.r.pos[row];
-                    slope = a.slopes[head] * kLog2e;
+                    next.pos = a.r.pos[next.row];
+                    next.slope = a.slopes[next.head] * kLog2e;
                 }
             }
-            const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+        };
+        const bool sectors = !(reinterpret_cast<uintptr_t>(a.out) & 31u) && a.out_stride % 16 == 0;
+        skip();
+        if (w.live()) {
+            load_row();
+            load_q();
+        }
+        while (w.live() && ok) {
+            const Row me = next;
+            const int all_lo = __reduce_max_sync(0xffffffffu, me.lo), all_hi = __reduce_min_sync(0xffffffffu, me.hi);
             const int n = w.n, klo = w.it.klo, khi = w.it.khi, key_base = first_key(w, 0), seq = w.it.seq;
             const float lsr = lsr_next;
             float m_run = -INFINITY, m_neg = 0.f, l_run = 0.f;
@@ -581,37 +601,42 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                         ls = 1.f;
                     }
                     if (biased) {
-                        if (!warp_wait(&b_full[t], (uint32_t)biases & 1u)) {
+                        if (!warp_wait(&b_full[t], (uint32_t)biases++ & 1u)) {
                             ok = false;
                             break;
                         }
-                        ++biases;
                         const float4* bias = reinterpret_cast<const float4*>(smem + kOffBias + 512 * t);
                         const float2 l2 = make_float2(ls, ls);
 #pragma unroll
-                        for (int k = 0; k < 128; k += 4) {
-                            const float4 b = bias[k / 4];
-                            const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), l2, make_float2(b.x, b.y));
-                            const float2 z = __ffma2_rn(make_float2(x[k + 2], x[k + 3]), l2, make_float2(b.z, b.w));
-                            x[k] = y.x, x[k + 1] = y.y, x[k + 2] = z.x, x[k + 3] = z.y;
+                        for (int k = 0; k < 128; k += 16) {
+                            float4 b[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) b[i] = bias[k / 4 + i];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float* y = x + k + 4 * i;
+                                const float2 u = __ffma2_rn(make_float2(y[0], y[1]), l2, make_float2(b[i].x, b[i].y));
+                                const float2 v = __ffma2_rn(make_float2(y[2], y[3]), l2, make_float2(b[i].z, b[i].w));
+                                y[0] = u.x, y[1] = u.y, y[2] = v.x, y[3] = v.y;
+                            }
                         }
                         ls = 1.f;
                     }
                     if (a.slopes) {   // the distance's roundings, 2^-24 of it, are the product's own size
-                        const float ahead = (float)(gpos - key0);
+                        const float ahead = (float)(me.pos - key0);
 #pragma unroll
-                        for (int k = 0; k < 128; ++k) x[k] = fmaf(-slope, fabsf(ahead - (float)k), x[k] * ls);
+                        for (int k = 0; k < 128; ++k) x[k] = fmaf(-me.slope, fabsf(ahead - (float)k), x[k] * ls);
                         ls = 1.f;
                     }
                 }
                 if (key0 + 128 > all_hi) {   // warp-uniform, as the next
-                    const int h = hi - key0;
+                    const int h = me.hi - key0;
 #pragma unroll
                     for (int k = 0; k < 128; ++k)
                         if (k >= h) x[k] = -INFINITY;
                 }
                 if (key0 < all_lo) {
-                    const int l = lo - key0;
+                    const int l = me.lo - key0;
 #pragma unroll
                     for (int k = 0; k < 128; ++k)
                         if (k < l) x[k] = -INFINITY;
@@ -683,11 +708,14 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                 if (lane == 0) mbar_arrive(&p_full[t]);
             }
             if (!ok) break;
-            // ---- the next run's Q, so that its first scores are on their way meanwhile
+            // ---- the next run's rows and Q, so that its first scores are on their way meanwhile
             advance();
             skip();
             ++runs;
-            if (w.live()) load_q();
+            if (w.live()) {
+                load_row();
+                load_q();
+            }
             // ---- the run's rows
             if (!ok || !warp_wait(&o_done[t], (uint32_t)(runs - 1) & 1u)) {
                 ok = false;
@@ -695,14 +723,11 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
             }
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
-            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.out_stride + (int64_t)head * 128;
-            __nv_bfloat16* out_pair = reinterpret_cast<__nv_bfloat16*>(
-                __shfl_xor_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), 1));
-            const bool valid_pair = __shfl_xor_sync(0xffffffffu, (int)valid, 1) != 0;
+            __nv_bfloat16* out =
+                static_cast<__nv_bfloat16*>(a.out) + me.row * a.out_stride + (int64_t)me.head * 128;
             // partials lie chunk by chunk of four dims, [32][tile_rows], so that the
-            // lanes' rows are neighbours; whole rows leave as 32-byte sectors, two lanes
-            // exchanging 16 bytes each
-            float* po = a.part_o + slot * 128 + 4 * (size_t)(t * 128 + m);
+            // lanes' rows are neighbours; whole rows leave as 32-byte sectors
+            float* po = a.part_o + me.slot * 128 + 4 * (size_t)(t * 128 + m);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float y[64];
@@ -714,25 +739,17 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                     for (int e = 0; e < 16; ++e)   // 4 bits: column 2 k + b of a chunk of 8 is dim k + 4 b
                         o[e] = kInt4 ? y[16 * c + (e & 8) + 2 * (e & 3) + ((e >> 2) & 1)] : y[16 * c + e];
                     const int d = 64 * hf + 16 * c;
-                    if (whole) {
+                    if (me.whole) {
                         uint32_t k[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) k[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-                        // even lane: first 16 bytes of its own row and of its neighbour's; odd lane: the second
-                        const bool odd = lane & 1;
-                        const uint4 low = make_uint4(k[0], k[1], k[2], k[3]), high = make_uint4(k[4], k[5], k[6], k[7]);
-                        const uint4 own = odd ? high : low;
-                        uint4 other = odd ? low : high;
-                        other.x = __shfl_xor_sync(0xffffffffu, other.x, 1);
-                        other.y = __shfl_xor_sync(0xffffffffu, other.y, 1);
-                        other.z = __shfl_xor_sync(0xffffffffu, other.z, 1);
-                        other.w = __shfl_xor_sync(0xffffffffu, other.w, 1);
-                        // first the even lane's row, then the odd lane's
-                        if (odd ? valid_pair : valid)
-                            *reinterpret_cast<uint4*>((odd ? out_pair : out) + d + 8 * odd) = odd ? other : own;
-                        if (odd ? valid : valid_pair)
-                            *reinterpret_cast<uint4*>((odd ? out : out_pair) + d + 8 * odd) = odd ? own : other;
-                    } else if (valid) {
+                        if (me.valid && sectors) {
+                            store32(out + d, k);
+                        } else if (me.valid) {
+                            *reinterpret_cast<uint4*>(out + d) = make_uint4(k[0], k[1], k[2], k[3]);
+                            *reinterpret_cast<uint4*>(out + d + 8) = make_uint4(k[4], k[5], k[6], k[7]);
+                        }
+                    } else if (me.valid) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             *reinterpret_cast<float4*>(po + (size_t)(d / 4 + e) * 4 * a.tile_rows) =
@@ -740,8 +757,8 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                     }
                 }
             }
-            if (valid && !whole)
-                *reinterpret_cast<float2*>(a.part_ml + 2 * (slot + t * 128 + m)) = make_float2(m_run, l_run);
+            if (me.valid && !me.whole)
+                *reinterpret_cast<float2*>(a.part_ml + 2 * (me.slot + t * 128 + m)) = make_float2(m_run, l_run);
             tc_fence_before();
         }
     } else if constexpr (kInt4) {

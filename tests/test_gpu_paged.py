@@ -345,6 +345,28 @@ def test_extreme_scales_of_flat_rows(fmt, dh, group, counts, scale):
     check_attend(c, 8, counts, pos, out, q, scale=scale)
 
 
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("counts", [[1, 1], [70, 90]])
+@pytest.mark.parametrize("shift,pad", [(8, 0), (0, 8), (16, 16)])
+def test_rows_at_any_16_bytes(fmt, dh, group, counts, shift, pad):
+    """q and out rows that begin between two 32-byte sectors; what lies between
+    the rows stays as it was."""
+    lens = [300, 200]
+    c = Paged(fmt, lens, 2, dh, 64, "hnd", group, seed=6)
+    pos = tail(lens, counts)
+    n, hq = sum(counts), 8
+    view = lambda x: torch.as_strided(x, (n, hq, dh), (hq * dh + pad, dh, 1), shift)  # noqa: E731
+    flat = [torch.full((n * (hq * dh + pad) + shift,), 7.0, dtype=c.row_dtype, device="cuda") for _ in range(2)]
+    q, out = view(flat[0]), view(flat[1])
+    q.copy_(torch.randn(n, hq, dh, device="cuda"))
+    ws = torch.empty(kvr.kvr_paged_workspace_bytes(c.p, hq, n, max(counts)), dtype=torch.uint8, device="cuda")
+    kvr.kvr_paged_attend(c.p, None, max(counts), i32(np.concatenate([[0], np.cumsum(counts)])), i32(pos), q, out, ws)
+    kvr.kvr_paged_status(c.p)
+    check_attend(c, hq, counts, pos, out, q)
+    out.fill_(7.0)
+    assert torch.all(flat[1] == 7.0)
+
+
 def test_order_of_rows_does_not_matter():
     """Positions in any order and repeated; strided q and out rows."""
     c = Paged("bf16", [400], 2, seed=3)
