@@ -125,7 +125,10 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     } else if (g->tc) {
         g->tile_rows = 256;
         g->unit_keys = 128;
-        g->run_cost = 2;
+        // a run's start and end (rows and Q looked up, first scores and last product with
+        // nothing beside them, O out), in units; 2, 4 and 6: 8192 causal rows 390, 366,
+        // 376 us (4 bits 498, 441, 450), packed documents 114, 103, 105
+        g->run_cost = 4;
         g->n_cta = kNumSMs;
     } else {
         g->tile_rows = kSimtRows;

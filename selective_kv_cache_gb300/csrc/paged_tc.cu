@@ -37,8 +37,8 @@
 // exponentials (1024).  Measured: 1.36 PFLOP/s at 4096 rows over 8192 keys of a
 // 32/8-head model (0.30 ms), about 3000 cycles a unit, close to the chain of a row
 // tile that bounds it: softmax 1450, its two products 1024, three hand-overs of
-// 100-150; 1.42 PFLOP/s at 8192 causal rows (0.39 ms).  4 bits: 1.10 PFLOP/s there
-// (0.49 ms); softmax and conversion share the issue slots, 3000 of a unit's 3700
+// 100-150; 1.50 PFLOP/s at 8192 causal rows (0.37 ms).  4 bits: 1.24 PFLOP/s there
+// (0.44 ms); softmax and conversion share the issue slots, 3000 of a unit's 3700
 // cycles.  The group count is a template argument: a pair per 32 dims whatever the
 // group took 8 % longer.  Rows leave as one 32-byte store a thread: with 16-byte
 // halves exchanged between neighbours a run's end took 4500 cycles in place of 3000.
