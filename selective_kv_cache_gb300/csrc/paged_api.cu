@@ -116,7 +116,6 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     const int64_t bound = passes * p->batch * p->n_kv_heads * (((int64_t)p->max_pages * p->page_size + 127) / 128);
     g->decode = p->format == KVR_BF16 ? passes == 1 || (passes <= 8 && bound <= 3600)
                                       : p->format == KVR_INT4 && (passes <= 2 || (passes <= 8 && bound <= 5500));
-    g->run_cost = 0;
     g->tc = p->format != KVR_F32 && !g->decode;
     if (g->decode) {
         g->tile_rows = max_rows * g->G <= 8 ? 8 : 16;
@@ -137,8 +136,13 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     }
     g->positions = g->tc ? 2 * (128 / g->G) : g->tile_rows / g->G;
     g->tiles = (max_rows + g->positions - 1) / g->positions;
-    // shares and items are counted in 32 bits
     const int64_t items = (int64_t)g->tiles * p->batch;
+    // A run's start is worth more when there are runs for every CTA anyway; with few,
+    // splitting them finely is.  0, 1 and 3 (us): decode 64 x 300 keys 39, 37, 33 (4
+    // bits 29, 27, 26), 4 drafted rows x 3 x 5001 keys 29, 25, 25, 1 x 1000 keys 17,
+    // 17, 19.  In fp32 the units themselves outweigh it (4 x 500 keys 19 with 0, 23 with 1).
+    if (!g->tc) g->run_cost = !g->decode ? 0 : items * p->n_kv_heads >= g->n_cta ? 3 : 1;
+    // shares and items are counted in 32 bits
     const int64_t units = ((int64_t)p->max_pages * p->page_size + g->unit_keys - 1) / g->unit_keys + g->run_cost;
     if (items > (int64_t(1) << 28) || items * units * p->n_kv_heads >= (int64_t(1) << 31))
         return fail(KVR_EUNSUPPORTED, "batch * rows * keys is too large for one call");
