@@ -32,10 +32,13 @@
 //               pairs (e, e + 4), so the 8 dims of a chunk lie in the order 0 4 1
 //               5 2 6 3 7; Q is stored in that order and O read back from it.
 // Biases of keys (the same for every row) are written to shared memory once a
-// tile and read as broadcasts: 8192 keys, 4096 rows 329 us with, 304 us without.
+// tile and read as broadcasts; a cap well above the logits is its series on the
+// FMA pipe, where two special functions a key (12 cycles of a warp) would bound the
+// tile.  4096 rows over 8192 keys: 276 us plain, 340 with biases, 426 with slopes,
+// 455 capped (610 with logits near the cap).
 // A unit is four 128^3 products (2048 cycles of the pipe) and 2 x 128 x 128
-// exponentials (1024).  Measured: 1.36 PFLOP/s at 4096 rows over 8192 keys of a
-// 32/8-head model (0.30 ms), about 3000 cycles a unit, close to the chain of a row
+// exponentials (1024).  Measured: 1.49 PFLOP/s at 4096 rows over 8192 keys of a
+// 32/8-head model (0.28 ms), under 3000 cycles a unit, close to the chain of a row
 // tile that bounds it: softmax 1450, its two products 1024, three hand-overs of
 // 100-150; 1.50 PFLOP/s at 8192 causal rows (0.37 ms).  4 bits: 1.24 PFLOP/s there
 // (0.44 ms); softmax and conversion share the issue slots, 3000 of a unit's 3700
@@ -192,12 +195,14 @@ __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.al
 __device__ __forceinline__ int first_key(const PagedWalk& w, int s) { return ((w.it.klo >> 7) + w.off + s) << 7; }
 __device__ __forceinline__ int row_tiles(const PagedWalk& w, int per_tile) { return w.it.rows > per_tile ? 2 : 1; }
 
-// NG: scale groups of a 4-bit row, 0 for bf16 pages; kExtra: cap, biases or slopes
-template <int NG, bool kExtra>
+// NG: scale groups of a 4-bit row, 0 for bf16 pages.  kScore: 0 products alone, 1 with
+// biases or slopes, 2 capped (a kernel of its own: the cap's code made the others
+// spill, 327 -> 349 us with biases)
+template <int NG, int kScore>
 __global__ void __launch_bounds__(NG ? 512 : 384, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ CUtensorMap tmQ, PagedAttn a) {
-    constexpr bool kInt4 = NG != 0;
+    constexpr bool kInt4 = NG != 0, kExtra = kScore != 0, kCap = kScore == 2;
     constexpr int kRing = kInt4 ? 4 : 5;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -528,27 +533,20 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                 if (lane == 0) mbar_arrive(&q_full[t]);
             }
         };
-        // this thread's row of a run, and what it sees
-        struct Row {
-            bool whole, valid;
-            int row, head, lo, hi, pos;
+        // what this thread's row of a run sees
+        struct Sees {
+            int lo, hi, pos;
             float slope;
-            size_t slot;
         };
-        Row next{};
+        Sees next{};
         auto load_row = [&]() {
             const int p = t * per_tile + m / G;
-            next.whole = w.whole();
-            next.slot = ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.tile_rows;
-            next.valid = m < per_tile * G && p < w.it.rows;
-            next.row = w.it.row0 + p;
-            next.head = w.h * G + m % G;
             next.lo = w.it.klo, next.hi = w.it.khi;
-            if (next.valid) {
-                paged_interval(a, next.row, w.it.kv, &next.lo, &next.hi);
+            if (m < per_tile * G && p < w.it.rows) {
+                paged_interval(a, w.it.row0 + p, w.it.kv, &next.lo, &next.hi);
                 if (kExtra && a.slopes) {
-                    next.pos = a.r.pos[next.row];
-                    next.slope = a.slopes[next.head] * kLog2e;
+                    next.pos = a.r.pos[w.it.row0 + p];
+                    next.slope = a.slopes[w.h * G + m % G] * kLog2e;
                 }
             }
         };
@@ -559,7 +557,7 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
             load_q();
         }
         while (w.live() && ok) {
-            const Row me = next;
+            const Sees me = next;
             const int all_lo = __reduce_max_sync(0xffffffffu, me.lo), all_hi = __reduce_min_sync(0xffffffffu, me.hi);
             const int n = w.n, klo = w.it.klo, khi = w.it.khi, key_base = first_key(w, 0), seq = w.it.seq;
             const float lsr = lsr_next;
@@ -593,12 +591,32 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                 float x[128], ls = lsr;
                 tmem_ld128(ts, x);
                 if constexpr (kExtra) {
-                    if (a.softcap > 0.f) {
-                        const float cap_out = a.softcap * kLog2e, c_in = lsr * (2.f / a.softcap);
+                    if constexpr (kCap) {
+                        const float cap_out = a.softcap * kLog2e, in = lsr / cap_out;   // u = in x
+                        float top_abs = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 128; ++k)   // cap tanh(u) = cap (1 - 2 / (1 + exp(2u)))
-                            x[k] = fmaf(-2.f * cap_out, __fdividef(1.f, 1.f + ex2(x[k] * c_in)), cap_out);
-                        ls = 1.f;
+                        for (int k = 0; k < 128; k += 2) top_abs = max3f(top_abs, fabsf(x[k]), fabsf(x[k + 1]));
+                        if (__all_sync(0xffffffffu, top_abs * in <= 0.4f)) {
+                            // below 2/5 of the cap, tanh's series up to u^9: off by 2^-20 of u at most
+                            const float2 in2 = make_float2(in, in);
+#pragma unroll
+                            for (int k = 0; k < 128; k += 2) {
+                                const float2 u = __fmul2_rn(make_float2(x[k], x[k + 1]), in2), v = __fmul2_rn(u, u);
+                                float2 y = __ffma2_rn(v, make_float2(62.f / 2835.f, 62.f / 2835.f),
+                                                      make_float2(-17.f / 315.f, -17.f / 315.f));
+                                y = __ffma2_rn(v, y, make_float2(2.f / 15.f, 2.f / 15.f));
+                                y = __ffma2_rn(v, y, make_float2(-1.f / 3.f, -1.f / 3.f));
+                                y = __ffma2_rn(__fmul2_rn(u, v), y, u);
+                                x[k] = y.x, x[k + 1] = y.y;
+                            }
+                            ls = cap_out;
+                        } else {
+                            const float c_in = lsr * (2.f / a.softcap);
+#pragma unroll
+                            for (int k = 0; k < 128; ++k)   // cap tanh(u) = cap (1 - 2 / (1 + exp(2u)))
+                                x[k] = fmaf(-2.f * cap_out, __fdividef(1.f, 1.f + ex2(x[k] * c_in)), cap_out);
+                            ls = 1.f;
+                        }
                     }
                     if (biased) {
                         if (!warp_wait(&b_full[t], (uint32_t)biases++ & 1u)) {
@@ -708,6 +726,12 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                 if (lane == 0) mbar_arrive(&p_full[t]);
             }
             if (!ok) break;
+            // ---- where the run's rows go
+            const int p = t * per_tile + m / G;
+            const int64_t row = w.it.row0 + p;
+            const int head = w.h * G + m % G;
+            const bool whole = w.whole(), valid = m < per_tile * G && p < w.it.rows;
+            const size_t slot = ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.tile_rows;
             // ---- the next run's rows and Q, so that its first scores are on their way meanwhile
             advance();
             skip();
@@ -723,11 +747,10 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
             }
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
-            __nv_bfloat16* out =
-                static_cast<__nv_bfloat16*>(a.out) + me.row * a.out_stride + (int64_t)me.head * 128;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.out_stride + (int64_t)head * 128;
             // partials lie chunk by chunk of four dims, [32][tile_rows], so that the
             // lanes' rows are neighbours; whole rows leave as 32-byte sectors
-            float* po = a.part_o + me.slot * 128 + 4 * (size_t)(t * 128 + m);
+            float* po = a.part_o + slot * 128 + 4 * (size_t)(t * 128 + m);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float y[64];
@@ -739,17 +762,17 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                     for (int e = 0; e < 16; ++e)   // 4 bits: column 2 k + b of a chunk of 8 is dim k + 4 b
                         o[e] = kInt4 ? y[16 * c + (e & 8) + 2 * (e & 3) + ((e >> 2) & 1)] : y[16 * c + e];
                     const int d = 64 * hf + 16 * c;
-                    if (me.whole) {
+                    if (whole) {
                         uint32_t k[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) k[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-                        if (me.valid && sectors) {
+                        if (valid && sectors) {
                             store32(out + d, k);
-                        } else if (me.valid) {
+                        } else if (valid) {
                             *reinterpret_cast<uint4*>(out + d) = make_uint4(k[0], k[1], k[2], k[3]);
                             *reinterpret_cast<uint4*>(out + d + 8) = make_uint4(k[4], k[5], k[6], k[7]);
                         }
-                    } else if (me.valid) {
+                    } else if (valid) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             *reinterpret_cast<float4*>(po + (size_t)(d / 4 + e) * 4 * a.tile_rows) =
@@ -757,8 +780,8 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                     }
                 }
             }
-            if (me.valid && !me.whole)
-                *reinterpret_cast<float2*>(a.part_ml + 2 * (me.slot + t * 128 + m)) = make_float2(m_run, l_run);
+            if (valid && !whole)
+                *reinterpret_cast<float2*>(a.part_ml + 2 * (slot + t * 128 + m)) = make_float2(m_run, l_run);
             tc_fence_before();
         }
     } else if constexpr (kInt4) {
@@ -828,20 +851,20 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
     if (warp == 1) tmem_dealloc(kTmem, 512);
 }
 
-template <int NG, bool kExtra>
+template <int NG, int kScore>
 cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const PagedAttn& a,
                    cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(paged_tc_kernel<NG, kExtra>, (int)kSmem, &allowed);
+    const cudaError_t e = allow_smem(paged_tc_kernel<NG, kScore>, (int)kSmem, &allowed);
     if (e != cudaSuccess) return e;
-    KVR_LAUNCH(paged_tc_kernel<NG, kExtra>, dim3((unsigned)a.n_cta), dim3(NG ? 512 : 384), kSmem, s, k, v, q, a);
+    KVR_LAUNCH((paged_tc_kernel<NG, kScore>), dim3((unsigned)a.n_cta), dim3(NG ? 512 : 384), kSmem, s, k, v, q, a);
     return cudaSuccess;
 }
 template <int NG>
 cudaError_t launch_ng(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const PagedAttn& a,
                       cudaStream_t s) {
-    const bool extra = a.softcap > 0.f || a.loc || a.snk || a.slopes;
-    return extra ? launch<NG, true>(k, v, q, a, s) : launch<NG, false>(k, v, q, a, s);
+    if (a.softcap > 0.f) return launch<NG, 2>(k, v, q, a, s);
+    return a.loc || a.snk || a.slopes ? launch<NG, 1>(k, v, q, a, s) : launch<NG, 0>(k, v, q, a, s);
 }
 
 }  // namespace
