@@ -107,11 +107,11 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     // The mma.sync kernel reads the keys once per pass, needs no plan and splits
     // finely; the tcgen05 one reads them once, at 1.6 us (bf16) and 2 us (4 bits) a
     // unit of up to 256 rows, and starts later.  Measured (us, mma.sync / tcgen05,
-    // 8 K/V heads, rows per head): bf16, one sequence of 8192 keys 64 rows 31 / 44,
-    // 128 rows 40 / 45; 3 x 5001 keys 48 rows 30 / 32, 64 rows 36 / 31; 8 x 8192 24
-    // rows 58 / 53, 64 rows 97 / 52.  4 bits: 32 x 8192 32 rows 128 / 149, 48 rows
-    // 168 / 144; 8 x 8192 48 rows 52 / 54, 64 rows 69 / 54; 3 x 5001 64 rows 34 / 35,
-    // 128 rows 39 / 36; 1 x 8192 128 rows 37 / 48.
+    // 8 K/V heads, rows per head): bf16, one sequence of 8192 keys 64 rows 30 / 39,
+    // 128 rows 39 / 40; 3 x 5001 keys 48 rows 29 / 32, 64 rows 35 / 33; 8 x 8192 24
+    // rows 57 / 54, 64 rows 95 / 56.  4 bits: 32 x 8192 32 rows 124 / 149, 48 rows
+    // 162 / 141; 8 x 8192 48 rows 52 / 53, 64 rows 67 / 55; 3 x 5001 64 rows 31 / 36,
+    // 128 rows 38 / 35; 1 x 8192 128 rows 36 / 43.
     const int64_t passes = ((int64_t)max_rows * g->G + 15) / 16;
     const int64_t bound = passes * p->batch * p->n_kv_heads * (((int64_t)p->max_pages * p->page_size + 127) / 128);
     g->decode = p->format == KVR_BF16 ? passes == 1 || (passes <= 8 && bound <= 3600)

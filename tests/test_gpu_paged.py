@@ -196,6 +196,19 @@ def test_rows_and_pages(fmt, dh, group, page, layout):
 
 
 @pytest.mark.parametrize("fmt,dh,group", FORMATS)
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (14, 2), (12, 1)])
+@pytest.mark.parametrize("opts", [dict(), dict(softcap=15.0)])
+def test_several_passes(fmt, dh, group, hq, hkv, opts):
+    """Rows for several passes over the keys, ragged and one alone."""
+    lens, counts = [333, 40, 1100], [17, 9, 1]
+    c = Paged(fmt, lens, hkv, dh, 32, "nhd", group, seed=13)
+    pos = tail(lens, counts)
+    out, q, _ = attend_case(c, hq, counts, pos, **opts)
+    kvr.kvr_paged_status(c.p)
+    check_attend(c, hq, counts, pos, out, q, **opts)
+
+
+@pytest.mark.parametrize("fmt,dh,group", FORMATS)
 @pytest.mark.parametrize("hq,hkv,n", [(4, 4, 260), (14, 2, 75), (6, 1, 300), (16, 1, 33)])
 def test_prompt(fmt, dh, group, hq, hkv, n):
     """A prompt against its own cache: many row tiles of every group size."""
