@@ -34,7 +34,7 @@
 // Biases of keys (the same for every row) are written to shared memory once a
 // tile and read as broadcasts; a cap well above the logits is its series on the
 // FMA pipe, where two special functions a key (12 cycles of a warp) would bound the
-// tile.  4096 rows over 8192 keys: 276 us plain, 340 with biases, 426 with slopes,
+// tile.  4096 rows over 8192 keys: 276 us plain, 333 with biases, 426 with slopes,
 // 455 capped (610 with logits near the cap).
 // A unit is four 128^3 products (2048 cycles of the pipe) and 2 x 128 x 128
 // exponentials (1024).  Measured: 1.49 PFLOP/s at 4096 rows over 8192 keys of a
@@ -196,13 +196,13 @@ __device__ __forceinline__ int first_key(const PagedWalk& w, int s) { return ((w
 __device__ __forceinline__ int row_tiles(const PagedWalk& w, int per_tile) { return w.it.rows > per_tile ? 2 : 1; }
 
 // NG: scale groups of a 4-bit row, 0 for bf16 pages.  kScore: 0 products alone, 1 with
-// biases or slopes, 2 capped (a kernel of its own: the cap's code made the others
-// spill, 327 -> 349 us with biases)
+// biases, 2 also slopes, 3 also capped (kernels of their own: the others' code made
+// a biased call's registers spill)
 template <int NG, int kScore>
 __global__ void __launch_bounds__(NG ? 512 : 384, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ CUtensorMap tmQ, PagedAttn a) {
-    constexpr bool kInt4 = NG != 0, kExtra = kScore != 0, kCap = kScore == 2;
+    constexpr bool kInt4 = NG != 0, kExtra = kScore != 0, kSlopes = kScore >= 2, kCap = kScore == 3;
     constexpr int kRing = kInt4 ? 4 : 5;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
             next.lo = w.it.klo, next.hi = w.it.khi;
             if (m < per_tile * G && p < w.it.rows) {
                 paged_interval(a, w.it.row0 + p, w.it.kv, &next.lo, &next.hi);
-                if (kExtra && a.slopes) {
+                if (kSlopes && a.slopes) {
                     next.pos = a.r.pos[w.it.row0 + p];
                     next.slope = a.slopes[w.h * G + m % G] * kLog2e;
                 }
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                         }
                         ls = 1.f;
                     }
-                    if (a.slopes) {   // the distance's roundings, 2^-24 of it, are the product's own size
+                    if (kSlopes && a.slopes) {   // the distance's roundings, 2^-24 of it, are the product's own size
                         const float ahead = (float)(me.pos - key0);
 #pragma unroll
                         for (int k = 0; k < 128; ++k) x[k] = fmaf(-me.slope, fabsf(ahead - (float)k), x[k] * ls);
@@ -863,8 +863,9 @@ cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap
 template <int NG>
 cudaError_t launch_ng(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const PagedAttn& a,
                       cudaStream_t s) {
-    if (a.softcap > 0.f) return launch<NG, 2>(k, v, q, a, s);
-    return a.loc || a.snk || a.slopes ? launch<NG, 1>(k, v, q, a, s) : launch<NG, 0>(k, v, q, a, s);
+    if (a.softcap > 0.f) return launch<NG, 3>(k, v, q, a, s);
+    if (a.slopes) return launch<NG, 2>(k, v, q, a, s);
+    return a.loc || a.snk ? launch<NG, 1>(k, v, q, a, s) : launch<NG, 0>(k, v, q, a, s);
 }
 
 }  // namespace
