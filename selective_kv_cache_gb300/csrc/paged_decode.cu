@@ -44,11 +44,6 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;   // log2 of the largest P before the maximum is raised
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -447,8 +442,7 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
             }
             // ---- logits in base 2
             if (kExtra) {
-                const float cap_in = a.softcap > 0.f ? 2.f / a.softcap : 0.f;
-                const float cap_out = a.softcap * kLog2e;
+                const float cap_out = a.softcap * kLog2e, cap_in = a.softcap > 0.f ? 1.f / cap_out : 0.f;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     float bias[2] = {0.f, 0.f};
@@ -467,13 +461,16 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float y = x[b][nt][e] * lsr[nt][e & 1];
-                            // cap tanh(u) = cap (1 - 2 / (1 + exp(2u)))
-                            if (a.softcap > 0.f) y = cap_out - 2.f * cap_out * __fdividef(1.f, 1.f + ex2(y * cap_in));
-                            const int key = 16 * (kb + b) + r + 8 * (e >> 1);
-                            y = fmaf(-slope[nt][e & 1], (float)abs(gpos[nt][e & 1] - key), y + bias[e >> 1]);
-                            x[b][nt][e] = y;
+                        for (int e = 0; e < 4; e += 2) {   // rows 2t, 2t + 1 of one key
+                            float2 y = make_float2(x[b][nt][e] * lsr[nt][0], x[b][nt][e + 1] * lsr[nt][1]);
+                            if (a.softcap > 0.f) {
+                                y = tanh_unit(make_float2(y.x * cap_in, y.y * cap_in));
+                                y.x *= cap_out, y.y *= cap_out;
+                            }
+                            const int key = 16 * (kb + b) + r + 4 * e;
+                            const float bk = bias[e >> 1];
+                            x[b][nt][e] = fmaf(-slope[nt][0], (float)abs(gpos[nt][0] - key), y.x + bk);
+                            x[b][nt][e + 1] = fmaf(-slope[nt][1], (float)abs(gpos[nt][1] - key), y.y + bk);
                         }
                 }
             }

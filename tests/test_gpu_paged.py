@@ -672,3 +672,18 @@ def test_answering_after_a_repair(dtype):
         kvr.kvr_sync_status(s.handle)
         assert torch.equal(s.K[0, layer, :, :n], block[0][layer]) and torch.equal(s.V[0, 0, :, :n], block[1][0])
     s.close()
+
+
+@pytest.mark.parametrize("fmt,dh,group", FORMATS)
+@pytest.mark.parametrize("counts", [[1, 1], [4, 3], [70, 33]])
+@pytest.mark.parametrize("cap", [1e3, 1e4, 1e7, 2.0 ** 64])
+def test_caps_far_above_the_logits(fmt, dh, group, counts, cap):
+    """cap tanh(x / cap) is nearly x there: a logit keeps its own precision,
+    not the cap's (a few roundings of logits of about 10, 2^-24 each, well
+    inside the bound's term for the cap)."""
+    lens = [517, 64]
+    c = Paged(fmt, lens, 2, dh, 16, "hnd", group, seed=2)
+    pos = tail(lens, counts)
+    out, q, _ = attend_case(c, 8, counts, pos, softcap=cap)
+    kvr.kvr_paged_status(c.p)
+    check_attend(c, 8, counts, pos, out, q, softcap=cap)
