@@ -114,11 +114,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Capped logits, cap tanh(u) with u = x / cap.  tanh(u) = 1 - 2 / (1 + exp(2u)) is
-// off by about 2^-22 whatever u is, which a cap far above the logits would turn
-// into an error of the cap's size; so up to 2/5 it is the series to u^9, off by
-// 2^-20 of u at most.  Which of the two is a matter of the logit alone.
-constexpr float kTanhSeries = 0.4f;
+// Capped logits, cap tanh(u) with u = x / cap.  The quotient 1 - 2 / (1 + exp(2u)) is
+// off by about 2^-22 whatever u is, so a logit by cap 2^-22: up to a cap of 64,
+// 2^-16, far below what weights in 16 bits show.  A larger cap would drown logits far
+// below it, so there u up to 2/5 goes by the series to u^9, off by 2^-20 of u at most.
+constexpr float kTanhSeries = 0.4f, kCapQuotient = 64.f;
 __device__ __forceinline__ float2 tanh_series(float2 u) {
     const float2 v = __fmul2_rn(u, u);
     float2 y = __ffma2_rn(v, make_float2(62.f / 2835.f, 62.f / 2835.f), make_float2(-17.f / 315.f, -17.f / 315.f));
@@ -126,13 +126,15 @@ __device__ __forceinline__ float2 tanh_series(float2 u) {
     y = __ffma2_rn(v, y, make_float2(-1.f / 3.f, -1.f / 3.f));
     return __ffma2_rn(__fmul2_rn(u, v), y, u);
 }
-__device__ __forceinline__ float tanh_beyond(float u) {
-    return fmaf(-2.f, __fdividef(1.f, 1.f + ex2(u * (2.f * 1.4426950408889634f))), 1.f);
+constexpr float kTwoLog2e = 2.f * 1.4426950408889634f;
+__device__ __forceinline__ float tanh_quotient(float e2u) {   // of 2u in base 2
+    return fmaf(-2.f, __fdividef(1.f, 1.f + ex2(e2u)), 1.f);
 }
-__device__ __forceinline__ float2 tanh_unit(float2 u) {
+// Which of the two is a matter of the logit alone.
+__device__ __forceinline__ float2 tanh_either(float2 u) {
     const float2 y = tanh_series(u);
-    return make_float2(fabsf(u.x) <= kTanhSeries ? y.x : tanh_beyond(u.x),
-                       fabsf(u.y) <= kTanhSeries ? y.y : tanh_beyond(u.y));
+    return make_float2(fabsf(u.x) <= kTanhSeries ? y.x : tanh_quotient(u.x * kTwoLog2e),
+                       fabsf(u.y) <= kTanhSeries ? y.y : tanh_quotient(u.y * kTwoLog2e));
 }
 
 // Dynamic shared memory above 48 KB for a kernel: set once per device.

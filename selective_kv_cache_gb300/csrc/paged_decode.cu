@@ -442,7 +442,32 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
             }
             // ---- logits in base 2
             if (kExtra) {
-                const float cap_out = a.softcap * kLog2e, cap_in = a.softcap > 0.f ? 1.f / cap_out : 0.f;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[b][nt][e] *= lsr[nt][e & 1];
+                if (a.softcap > 0.f) {
+                    const float cap_out = a.softcap * kLog2e, cap_in = 1.f / cap_out;
+                    auto capped = [&](auto f) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; e += 2) {
+                                    const float2 y = f(make_float2(x[b][nt][e], x[b][nt][e + 1]));
+                                    x[b][nt][e] = y.x * cap_out, x[b][nt][e + 1] = y.y * cap_out;
+                                }
+                    };
+                    if (a.softcap <= kCapQuotient) {
+                        const float in_q = cap_in * kTwoLog2e;
+                        capped([=](float2 y) { return make_float2(tanh_quotient(y.x * in_q), tanh_quotient(y.y * in_q)); });
+                    } else {
+                        capped([=](float2 y) { return tanh_either(make_float2(y.x * cap_in, y.y * cap_in)); });
+                    }
+                }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     float bias[2] = {0.f, 0.f};
@@ -461,16 +486,10 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; e += 2) {   // rows 2t, 2t + 1 of one key
-                            float2 y = make_float2(x[b][nt][e] * lsr[nt][0], x[b][nt][e + 1] * lsr[nt][1]);
-                            if (a.softcap > 0.f) {
-                                y = tanh_unit(make_float2(y.x * cap_in, y.y * cap_in));
-                                y.x *= cap_out, y.y *= cap_out;
-                            }
-                            const int key = 16 * (kb + b) + r + 4 * e;
-                            const float bk = bias[e >> 1];
-                            x[b][nt][e] = fmaf(-slope[nt][0], (float)abs(gpos[nt][0] - key), y.x + bk);
-                            x[b][nt][e + 1] = fmaf(-slope[nt][1], (float)abs(gpos[nt][1] - key), y.y + bk);
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = 16 * (kb + b) + r + 8 * (e >> 1);
+                            x[b][nt][e] = fmaf(-slope[nt][e & 1], (float)abs(gpos[nt][e & 1] - key),
+                                               x[b][nt][e] + bias[e >> 1]);
                         }
                 }
             }
