@@ -532,12 +532,14 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
         struct Sees {
             int lo, hi, pos;
             float slope;
+            bool live;   // a row of the item
         };
         Sees next{};
         auto load_row = [&]() {
             const int p = t * per_tile + m / G;
             next.lo = w.it.klo, next.hi = w.it.khi;
-            if (m < per_tile * G && p < w.it.rows) {
+            next.live = m < per_tile * G && p < w.it.rows;
+            if (next.live) {
                 paged_interval(a, w.it.row0 + p, w.it.kv, &next.lo, &next.hi);
                 if (kSlopes && a.slopes) {
                     next.pos = a.r.pos[w.it.row0 + p];
@@ -588,30 +590,31 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                 if constexpr (kExtra) {
                     if constexpr (kCap) {
                         const float cap_out = a.softcap * kLog2e, in = lsr / cap_out;   // u = in x
+                        // The warp's choice comes from its rows' logits of a tile that they all see
+                        // whole: what other columns and rows hold decides nothing.
                         float top_abs = 0.f;
 #pragma unroll
                         for (int k = 0; k < 128; k += 2) top_abs = max3f(top_abs, fabsf(x[k]), fabsf(x[k + 1]));
-                        if (__all_sync(0xffffffffu, top_abs * in <= 0.4f)) {
-                            // below 2/5 of the cap, tanh's series up to u^9: off by 2^-20 of u at most
-                            const float2 in2 = make_float2(in, in);
+                        const bool whole = key0 >= all_lo && key0 + 128 <= all_hi;
+                        const float2 in2 = make_float2(in, in);
+                        if (whole && __all_sync(0xffffffffu, !me.live || top_abs * in <= kTanhSeries)) {
 #pragma unroll
                             for (int k = 0; k < 128; k += 2) {
-                                const float2 u = __fmul2_rn(make_float2(x[k], x[k + 1]), in2), v = __fmul2_rn(u, u);
-                                float2 y = __ffma2_rn(v, make_float2(62.f / 2835.f, 62.f / 2835.f),
-                                                      make_float2(-17.f / 315.f, -17.f / 315.f));
-                                y = __ffma2_rn(v, y, make_float2(2.f / 15.f, 2.f / 15.f));
-                                y = __ffma2_rn(v, y, make_float2(-1.f / 3.f, -1.f / 3.f));
-                                y = __ffma2_rn(__fmul2_rn(u, v), y, u);
+                                const float2 y = tanh_series(__fmul2_rn(make_float2(x[k], x[k + 1]), in2));
                                 x[k] = y.x, x[k + 1] = y.y;
                             }
-                            ls = cap_out;
-                        } else {
-                            const float c_in = lsr * (2.f / a.softcap);
+                        } else if (a.softcap <= kCapQuotient) {
+                            const float in_q = in * kTwoLog2e;
 #pragma unroll
-                            for (int k = 0; k < 128; ++k)   // cap tanh(u) = cap (1 - 2 / (1 + exp(2u)))
-                                x[k] = fmaf(-2.f * cap_out, __fdividef(1.f, 1.f + ex2(x[k] * c_in)), cap_out);
-                            ls = 1.f;
+                            for (int k = 0; k < 128; ++k) x[k] = tanh_quotient(x[k] * in_q);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 128; k += 2) {
+                                const float2 y = tanh_either(__fmul2_rn(make_float2(x[k], x[k + 1]), in2));
+                                x[k] = y.x, x[k + 1] = y.y;
+                            }
                         }
+                        ls = cap_out;
                     }
                     if (biased) {
                         if (!warp_wait(&b_full[t], (uint32_t)biases++ & 1u)) {

@@ -687,3 +687,60 @@ def test_caps_far_above_the_logits(fmt, dh, group, counts, cap):
     out, q, _ = attend_case(c, 8, counts, pos, softcap=cap)
     kvr.kvr_paged_status(c.p)
     check_attend(c, 8, counts, pos, out, q, softcap=cap)
+
+
+def attend_rows(c, q, counts, pos, **opts):
+    """kvr_paged_attend on the given query rows; returns out."""
+    out = torch.full_like(q, 7.0)
+    ws = torch.empty(kvr.kvr_paged_workspace_bytes(c.p, q.shape[1], len(q), max(counts)), dtype=torch.uint8,
+                     device="cuda")
+    kvr.kvr_paged_attend(c.p, kvr.score_opts(**opts), max(counts), i32(np.concatenate([[0], np.cumsum(counts)])),
+                         i32(pos), q, out, ws)
+    kvr.kvr_paged_status(c.p)
+    return out
+
+
+@pytest.mark.parametrize("fmt,dh,group", FORMATS)
+@pytest.mark.parametrize("counts", [[2, 2], [70, 33]])
+def test_capped_rows_keep_their_own_precision(fmt, dh, group, counts):
+    """Rows whose logits reach the cap beside rows far below it: a row's bound
+    knows its own logits only."""
+    lens, cap = [517, 64], 2.0 ** 20
+    c = Paged(fmt, lens, 2, dh, 16, "hnd", group, seed=2)
+    pos = tail(lens, counts)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(sum(counts), 8, dh, generator=g, device="cuda") * 1.5
+    q[::2] *= cap
+    q = q.to(c.row_dtype)
+    out = attend_rows(c, q, counts, pos, softcap=cap)
+    check_attend(c, 8, counts, pos, out, q, softcap=cap)
+
+
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("counts", [[1, 1], [4, 2], [70, 33]])
+@pytest.mark.parametrize("opts", [dict(), dict(softcap=30.0), dict(softcap=1e4), dict(softcap=1e4, slopes=True)])
+def test_unseen_slots_decide_nothing(fmt, dh, group, counts, opts):
+    """The same bits whatever the slots behind a sequence's end, the unused
+    pages and the keys no row sees hold: NaN, infinities, the type's largest
+    values, small ones."""
+    lens = [517, 77]
+    c = Paged(fmt, lens, 2, dh, 32, "hnd", group, seed=12)
+    pos = tail(lens, counts)
+    pools = [c.ks, c.vs] if fmt == "int4" else [c.k, c.v]
+    unseen = [torch.isnan(t) for t in pools]
+    kw = dict(opts)
+    if kw.pop("slopes", False):
+        kw["slopes"] = torch.full((8,), 2.0 ** -6, device="cuda")
+    kw["key_begin"] = i32(np.full(sum(counts), 3))
+    for t, m in zip(pools, unseen):      # the first three keys of sequence 0 are seen by no row
+        m[c.table_np[0, 0], :, :3] = True
+        m[c.table_np[1, 0], :, :3] = True
+    ref = None
+    top = torch.finfo(pools[0].dtype).max
+    for value in (0.5, float("nan"), top, -top, float("inf"), -float("inf"), 1e3):
+        for t, m in zip(pools, unseen):
+            t[m] = value
+        out, _, _ = attend_case(c, 8, counts, pos, **kw)
+        kvr.kvr_paged_status(c.p)
+        ref = out if ref is None else ref
+        assert torch.isfinite(out).all() and torch.equal(bits(out), bits(ref)), value
