@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(NG ? 512 : 384, 1)
                 tmem_ld128(ts, x);
                 if constexpr (kExtra) {
                     if constexpr (kCap) {
-                        const float cap_out = a.softcap * kLog2e, in = lsr / cap_out;   // u = in x
+                        // u = in x; finite, so that a product of zero stays zero under the ranges' ends
+                        const float cap_out = a.softcap * kLog2e, in = fminf(lsr / cap_out, 1e38f);
                         // The warp's choice comes from its rows' logits of a tile that they all see
                         // whole: what other columns and rows hold decides nothing.
                         float top_abs = 0.f;

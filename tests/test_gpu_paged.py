@@ -744,3 +744,16 @@ def test_unseen_slots_decide_nothing(fmt, dh, group, counts, opts):
         kvr.kvr_paged_status(c.p)
         ref = out if ref is None else ref
         assert torch.isfinite(out).all() and torch.equal(bits(out), bits(ref)), value
+
+
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("counts", [[1, 1], [70, 33]])
+@pytest.mark.parametrize("scale,cap", [(2.0 ** 64, 2.0 ** -64), (2.0 ** -64, 2.0 ** 64), (2.0 ** -64, 2.0 ** -64)])
+def test_extreme_caps_and_scales_of_flat_rows(fmt, dh, group, counts, scale, cap):
+    """Queries of zeros under the ends of both ranges: the mean of the visible values."""
+    lens = [400, 77]
+    c = Paged(fmt, lens, 2, dh, 32, "hnd", group, seed=5)
+    pos = tail(lens, counts)
+    out, q, _ = attend_case(c, 8, counts, pos, q_scale=0.0, scale=scale, softcap=cap)
+    kvr.kvr_paged_status(c.p)
+    check_attend(c, 8, counts, pos, out, q, scale=scale, softcap=cap)
