@@ -113,7 +113,8 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     // 162 / 141; 8 x 8192 48 rows 52 / 53, 64 rows 67 / 55; 3 x 5001 64 rows 31 / 36,
     // 128 rows 38 / 35; 1 x 8192 128 rows 36 / 43.
     const int64_t passes = ((int64_t)max_rows * g->G + 15) / 16;
-    const int64_t bound = passes * p->batch * p->n_kv_heads * (((int64_t)p->max_pages * p->page_size + 127) / 128);
+    const int64_t bound = std::min<int64_t>(passes, 9) * p->batch * p->n_kv_heads *   // below 2^63; past 8 passes not asked
+                          (((int64_t)p->max_pages * p->page_size + 127) / 128);
     g->decode = p->format == KVR_BF16 ? passes == 1 || (passes <= 8 && bound <= 3600)
                                       : p->format == KVR_INT4 && (passes <= 2 || (passes <= 8 && bound <= 5500));
     g->tc = p->format != KVR_F32 && !g->decode;
@@ -144,7 +145,8 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     if (!g->tc) g->run_cost = !g->decode ? 0 : items * p->n_kv_heads >= g->n_cta ? 3 : 1;
     // shares and items are counted in 32 bits
     const int64_t units = ((int64_t)p->max_pages * p->page_size + g->unit_keys - 1) / g->unit_keys + g->run_cost;
-    if (items > (int64_t(1) << 28) || items * units * p->n_kv_heads >= (int64_t(1) << 31))
+    if (items > (int64_t(1) << 28) || units * p->n_kv_heads >= (int64_t(1) << 31) ||
+        items * (units * p->n_kv_heads) >= (int64_t(1) << 31))   // each factor first: the product of all can pass 2^63
         return fail(KVR_EUNSUPPORTED, "batch * rows * keys is too large for one call");
     g->n_items = (int)items;
     return KVR_OK;

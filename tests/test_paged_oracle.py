@@ -180,6 +180,16 @@ def test_call_too_large_is_refused(kvr):
     assert _attend(kvr, p) == kvr.KVR_EUNSUPPORTED
 
 
+@pytest.mark.parametrize("kw,n,m", [
+    (dict(batch=1 << 20, max_pages=1 << 22, page_size=256, n_kv_heads=65535), 1 << 16, 1 << 16),
+    (dict(batch=1 << 18, max_pages=1 << 22, page_size=256, n_kv_heads=65535), 1 << 18, 1 << 18)])
+def test_call_too_large_for_64_bits_is_refused(kvr, kw, n, m):
+    """Items times units times heads past 2^63 is too large as well."""
+    p = _pages(kvr, **kw)
+    assert kvr.kvr_paged_workspace_bytes(p, kw["n_kv_heads"], n, m) == 0
+    assert _attend(kvr, p, hq=kw["n_kv_heads"], n=n, m=m) == kvr.KVR_EUNSUPPORTED
+
+
 def test_binding_refuses_host_tensors(kvr):
     import torch
     k = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
