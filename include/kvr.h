@@ -629,7 +629,9 @@ typedef struct {
  * non-decreasing, at most n_rows); positions[r] (device int32 [n_rows]) is the
  * row's global position g_r.  Rows at or past cu_rows[batch] belong to no
  * sequence and are left alone, so a captured call can be replayed with fewer
- * rows.  Row strides are in elements, heads of a row contiguous
+ * rows.  Offsets that do not begin at 0, fall or pass n_rows are reported by
+ * kvr_paged_status; append and read then touch nothing, and attend leaves alone
+ * the rows of the sequences whose offsets they are.  Row strides are in elements, heads of a row contiguous
  * ([heads][head_dim]); row pointers and strides are 16-byte aligned.
  *
  * kvr_paged_append -- write the K/V of new rows into their pages, rotated on

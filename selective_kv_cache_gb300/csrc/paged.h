@@ -167,12 +167,12 @@ __device__ __forceinline__ int64_t paged_row(const PagedView& p, int page, int s
     return page * p.page_stride + slot * p.slot_stride + head * p.head_stride;
 }
 
-// Rows of sequence b that lie in [0, n_rows); a malformed cu_rows gives none
-// and is reported.
+// Rows of sequence b; offsets that begin before or past 0 (the first sequence's),
+// fall or pass n_rows give none and are reported.
 __device__ __forceinline__ int paged_seq_rows(const PagedView& p, const PagedRows& r, int b, int* row0) {
     const int a = r.cu[b], e = r.cu[b + 1];
     *row0 = a;
-    if (a < 0 || e < a || e > r.n_rows) {
+    if (a < 0 || (b == 0 && a != 0) || e < a || e > r.n_rows) {
         paged_err(p.err, DEV_ERR_INDEX, b);
         return 0;
     }

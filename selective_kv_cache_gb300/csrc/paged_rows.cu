@@ -74,8 +74,9 @@ struct Pair<float> {
 
 // Slots of the CTA's rows in shared memory, by warp 0, lane i for row i: the page
 // row of head 0 and the position, page row -1 for a row that is not to be
-// touched.  A row's sequence is the number of ends cu[b + 1] <= r; kAppend checks
-// what a write needs besides.  The caller synchronises.
+// touched.  A row's sequence is the number of ends cu[b + 1] <= r.  Offsets that do
+// not begin at 0, fall or pass n_rows are reported, and no row is touched; kAppend
+// checks what a write needs besides.  The caller synchronises.
 struct RowSlot {
     int64_t at;
     int g;
@@ -84,24 +85,30 @@ template <bool kAppend>
 __device__ __forceinline__ void find_slots(const PagedRowIo& a, RowSlot* slots) {
     if (threadIdx.x >= 32) return;
     const int lane = threadIdx.x, r0 = blockIdx.x * a.rows_per_block, r = r0 + lane;
-    int b = 0;
+    int b = 0, malformed = -1, last = a.r.cu[0];
+    if (last != 0) malformed = 0;
     for (int b0 = 0; b0 < a.p.batch; b0 += 32) {
-        const int end = b0 + lane < a.p.batch ? a.r.cu[b0 + lane + 1] : 0x7fffffff;
+        const bool in = b0 + lane < a.p.batch;
+        const int end = in ? a.r.cu[b0 + lane + 1] : 0x7fffffff;
+        int begin = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) begin = last;
+        last = __shfl_sync(0xffffffffu, end, 31);
+        if (in && (end < begin || end > a.r.n_rows)) malformed = b0 + lane;
         for (int i = 0; i < a.rows_per_block; ++i) {
             const int n = __popc(__ballot_sync(0xffffffffu, end <= r0 + i));
             if (lane == i) b += n;
         }
     }
+    const bool usable = !__any_sync(0xffffffffu, malformed >= 0);
+    if (malformed >= 0) paged_err(a.p.err, DEV_ERR_INDEX, malformed);
     if (lane >= a.rows_per_block) return;
     int64_t at = -1;
     int g = 0;
-    if (r < a.r.n_rows && b < a.p.batch) {   // else behind the last sequence: left alone
-        const int first = a.r.cu[b];
+    if (usable && r < a.r.n_rows && b < a.p.batch) {   // else behind the last sequence: left alone
         g = a.r.pos[r];
         int bad = 0;
-        if (first < 0 || r < first || g < 0 || g >= a.p.capacity || (kAppend && a.rope && g >= a.rope_len))
-            bad = DEV_ERR_INDEX;
-        else if (kAppend && r > first && a.r.pos[r - 1] >= g) bad = DEV_ERR_ORDER;
+        if (g < 0 || g >= a.p.capacity || (kAppend && a.rope && g >= a.rope_len)) bad = DEV_ERR_INDEX;
+        else if (kAppend && r > a.r.cu[b] && a.r.pos[r - 1] >= g) bad = DEV_ERR_ORDER;
         int id = 0;
         if (!bad) {
             id = a.p.table[(int64_t)b * a.p.max_pages + (g >> a.p.page_shift)];

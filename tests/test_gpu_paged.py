@@ -757,3 +757,51 @@ def test_extreme_caps_and_scales_of_flat_rows(fmt, dh, group, counts, scale, cap
     out, q, _ = attend_case(c, 8, counts, pos, q_scale=0.0, scale=scale, softcap=cap)
     kvr.kvr_paged_status(c.p)
     check_attend(c, 8, counts, pos, out, q, scale=scale, softcap=cap)
+
+
+MALFORMED = [([0, 9, 4], [0, 1]), ([-3, 2, 4], [0]), ([2, 1, 0], [0, 1]), ([3, 2, 1], [0, 1]), ([1, 2, 4], [0]),
+             ([0, 3, 9], [1]), ([0, 4, 9], [1]), ([0, 3, 2], [1]), ([4, 4, 4], [0]), ([-3, -1, -1], [0, 1]),
+             ([0, -2 ** 31, 2 ** 31 - 1], [0, 1])]
+
+
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("cu,bad", MALFORMED)
+def test_malformed_row_offsets_are_alike_in_every_call(fmt, dh, group, cu, bad):
+    """Offsets that do not begin at 0, fall or pass n_rows are reported by each
+    of the three calls.  Append and read then touch nothing, attention leaves
+    alone the rows of the sequences whose offsets they are (bad)."""
+    c = Paged(fmt, [20, 20], 2, dh, 16, "hnd", group, seed=1, spare=4)
+    pos = np.array([1, 2, 3, 4])
+    good = np.full(4, -1)
+    for b in {0, 1} - set(bad):
+        good[cu[b]:cu[b + 1]] = b
+    x = torch.ones(4, 2, dh, device="cuda", dtype=c.row_dtype)
+    q = torch.randn(4, 8, dh, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(c.row_dtype)
+
+    def reported():
+        with pytest.raises(kvr.KvrError, match="index") as e:
+            kvr.kvr_paged_status(c.p)
+        assert e.value.status == kvr.KVR_EDEVICE
+        kvr.kvr_paged_status(c.p)
+
+    out = torch.full_like(q, 7.0)
+    for max_rows in (4, 1):
+        ws = torch.empty(kvr.kvr_paged_workspace_bytes(c.p, 8, 4, max_rows), dtype=torch.uint8, device="cuda")
+        kvr.kvr_paged_attend(c.p, None, max_rows, i32(cu), i32(pos), q, out, ws)
+        reported()
+        if max_rows == 4:
+            for r in range(4):
+                if good[r] >= 0:
+                    one = [1 if b == good[r] else 0 for b in range(2)]
+                    check_attend(c, 8, one, pos[r:r + 1], out[r:r + 1], q[r:r + 1])
+        assert torch.all(out[torch.as_tensor(good < 0)] == 7.0)
+    back = torch.full((4, 2, dh), 9.0, device="cuda", dtype=c.row_dtype)
+    kvr.kvr_paged_read(c.p, i32(cu), i32(pos), back, back.clone())
+    reported()
+    assert torch.all(back == 9.0)
+    pools = [t for t in (c.k, c.v, c.ks, c.vs) if t is not None]
+    before = [bits(t).clone() for t in pools]
+    turned = torch.full_like(q, 5.0)
+    kvr.kvr_paged_append(c.p, i32(cu), i32(pos), x, x, None, q, turned)
+    reported()
+    assert all(torch.equal(bits(t), b) for t, b in zip(pools, before)) and torch.all(turned == 5.0)
