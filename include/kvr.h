@@ -642,7 +642,7 @@ typedef struct {
  *               angles of each position, or NULL: nothing is rotated.
  *   q_rows, q_out   device [n_rows][n_q_heads][head_dim] or both NULL;
  *               q_out is packed (stride n_q_heads * head_dim) and may be
- *               q_rows itself when that is packed too.
+ *               q_rows itself when that is packed too (a single row always is).
  * The rotation is in fp32, each product and sum rounded on its own, and
  * rounded once to the page format.  KVR_INT4, per group of fp32 values x
  * (after the rotation, brought into +-2^15): o = fp16(min x), s = fp16((max x -

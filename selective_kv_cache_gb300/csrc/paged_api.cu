@@ -192,7 +192,7 @@ kvr_status kvr_paged_append(const kvr_pages* p, int32_t n_rows, const int32_t* c
         if (n_q_heads < 1 || n_q_heads > 65535) return fail(KVR_EINVAL, "append: n_q_heads out of range");
         if (!row_operand(p, q_rows, q_stride, n_q_heads) || !aligned16(q_out))
             return fail(KVR_EINVAL, "append: query rows must be 16-byte aligned and at least a row apart");
-        if (q_rows == q_out && q_stride != (int64_t)n_q_heads * p->head_dim)
+        if (q_rows == q_out && n_rows > 1 && q_stride != (int64_t)n_q_heads * p->head_dim)
             return fail(KVR_EINVAL, "append: queries are rotated in place only when they are packed");
     }
     PagedRowIo a{};

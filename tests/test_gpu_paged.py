@@ -805,3 +805,17 @@ def test_malformed_row_offsets_are_alike_in_every_call(fmt, dh, group, cu, bad):
     kvr.kvr_paged_append(c.p, i32(cu), i32(pos), x, x, None, q, turned)
     reported()
     assert all(torch.equal(bits(t), b) for t, b in zip(pools, before)) and torch.all(turned == 5.0)
+
+
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+def test_one_row_of_a_wide_tensor_turns_in_place(fmt, dh, group):
+    """A single row is packed whatever its stride: a decode step's fused q, k, v."""
+    c = Paged(fmt, [40], 2, dh, 16, "hnd", group, seed=1)
+    x = torch.randn(1, 12, dh, device="cuda").to(c.row_dtype)
+    q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+    rope = OP.rope_table(64, dh, THETA)
+    want = torch.from_numpy(OP.rotate(q.float().cpu().numpy(), rope[[39]])).to(c.row_dtype)
+    rest = x[:, 8:].clone()
+    kvr.kvr_paged_append(c.p, i32([0, 1]), i32([39]), k, v, torch.from_numpy(rope).cuda(), q, q)
+    kvr.kvr_paged_status(c.p)
+    assert torch.equal(bits(q.cpu()), bits(want)) and torch.equal(bits(x[:, 8:]), bits(rest))
