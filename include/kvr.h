@@ -604,14 +604,18 @@ typedef struct {
     void* k_scale;         /* KVR_INT4: fp16 pairs; NULL otherwise */
     void* v_scale;
     const int32_t* page_table;   /* device [batch][max_pages]; entries past a sequence's end are not read */
-    const int32_t* kv_len;       /* device [batch]: keys at or past it are never read by kvr_paged_attend */
+    const int32_t* kv_len;       /* device [batch]: kvr_paged_attend uses no key at or past it, whatever its slot
+                                    holds; slots behind it, up to the end of its page, may be read */
     int32_t* err;                /* device [4], zeroed once by the caller: device-side checks land here */
 } kvr_pages;
 
 /* How kvr_paged_attend turns products into logits and which keys a row sees.
  * Zero-initialise and set what is wanted; a NULL kvr_score_opts is the plain
  * causal softmax.  scale and softcap are 0 or in [2^-64, 2^64]; logits have to
- * stay within fp32's range. */
+ * stay within fp32's range.  They are formed in fp32, so a bias costs them
+ * 2^-23 of itself: a key with alpha = -1e9 has no weight beside one without, but
+ * where every key that a row sees has it, their weights come out equal.  Keys
+ * that are not to be seen at all belong outside [key_begin, key_end). */
 typedef struct {
     float scale;           /* x = scale * <q, k>; 0 = 1/sqrt(head_dim) */
     float softcap;         /* > 0: x <- softcap * tanh(x / softcap), before the biases */
@@ -663,7 +667,8 @@ kvr_status kvr_paged_append(const kvr_pages* p, int32_t n_rows, const int32_t* c
  * values they stand for (KVR_INT4: s * code + o in fp32, rounded once to
  * bf16); the inverse of the append's write.  k_out, v_out: device
  * [n_rows][n_kv_heads][head_dim], row strides in elements; either may be NULL.
- * Positions may come in any order and repeat.  kv_len is not read.
+ * Positions may come in any order and repeat; rows whose position or page is out
+ * of range are left alone and reported.  kv_len is not read.
  * ------------------------------------------------------------------------- */
 kvr_status kvr_paged_read(const kvr_pages* p, int32_t n_rows, const int32_t* cu_rows, const int32_t* positions,
                           void* k_out, int64_t k_stride, void* v_out, int64_t v_stride, void* stream);

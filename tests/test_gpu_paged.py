@@ -819,3 +819,25 @@ def test_one_row_of_a_wide_tensor_turns_in_place(fmt, dh, group):
     kvr.kvr_paged_append(c.p, i32([0, 1]), i32([39]), k, v, torch.from_numpy(rope).cuda(), q, q)
     kvr.kvr_paged_status(c.p)
     assert torch.equal(bits(q.cpu()), bits(want)) and torch.equal(bits(x[:, 8:]), bits(rest))
+
+
+@pytest.mark.parametrize("fmt,dh,group", ATTEND)
+@pytest.mark.parametrize("counts", [[1], [70]])
+@pytest.mark.parametrize("alpha", [-64.0, -1000.0, -2.0 ** 17, 5000.0])
+def test_a_bias_that_all_keys_share_costs_its_own_rounding(fmt, dh, group, counts, alpha):
+    """The plain softmax, with logits off by 2^-24 of the bias twice: in its
+    sum with the logit and in base 2's factor (check_attend's bound without
+    the bias, and that)."""
+    c = Paged(fmt, [517], 2, dh, 16, "hnd", group, seed=2)
+    pos = tail([517], counts)
+    bit = torch.full((c.max_pages * 16 // 32 + 1,), -1, dtype=torch.int32, device="cuda")
+    out, q, _ = attend_case(c, 8, counts, pos, alpha=alpha, local_bits=bit)
+    kvr.kvr_paged_status(c.p)
+    K, V, step = c.rows64(0)
+    got, q64 = out.double().cpu().numpy(), q.double().cpu().numpy()
+    o, spread, noise = OP.attend(q64, K, V, np.zeros(len(pos)), pos + 1, v_step=step)
+    f32 = fmt == "f32"
+    r = 2.0 ** -24 if f32 else 2.0 ** -8
+    d = 128 * 2.0 ** -24 * noise[..., None] * (16 if fmt == "int4" else 1) + (2.0 ** -19 if f32 else 2.0 ** -14)
+    d = d + 2 * abs(alpha) * 2.0 ** -24
+    assert np.all(np.abs(got - o) <= r * np.abs(o) + ((0 if f32 else r) + 2 * d) * spread + 1e-30)
