@@ -690,6 +690,10 @@ kvr_status kvr_paged_read(const kvr_pages* p, int32_t n_rows, const int32_t* cu_
  *   workspace   device, >= kvr_paged_workspace_bytes(p, n_q_heads, n_rows,
  *               max_rows), 256-byte aligned; needs no initialisation.  Calls
  *               whose GPU work overlaps need a workspace each.
+ * Logits, maxima, sums and outputs are fp32 until the one rounding to the row
+ * type.  The weights enter the product with V in bf16 over bf16 pages (as in
+ * kvr_attend), in fp16 over 4-bit ones, whose values enter it in fp16 too (their
+ * keys as well where there are many rows); over fp32 pages nothing is rounded.
  * Long sequences are split over the GPU and merged in a fixed order: the same
  * inputs give the same bits.  A sequence whose table holds an entry outside
  * the pool is computed with page 0 in its place and reported.

@@ -112,8 +112,13 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     // rows 57 / 54, 64 rows 95 / 56.  4 bits: 32 x 8192 32 rows 124 / 149, 48 rows
     // 162 / 141; 8 x 8192 48 rows 52 / 53, 64 rows 67 / 55; 3 x 5001 64 rows 31 / 36,
     // 128 rows 38 / 35; 1 x 8192 128 rows 36 / 43.
+    // The rule knows the table's width, not the lengths, so sequences of 2048 keys in
+    // a table of 131072 go to tcgen05 sooner than in one of their own width: bf16, one
+    // sequence 32 rows 28 us in place of 26, 64 rows 30 in place of 27, 8 sequences 32
+    // rows 39 in place of 44; 4 bits, one sequence 64 rows 32 in place of 24, 8
+    // sequences 64 rows 40 in place of 48.
     const int64_t passes = ((int64_t)max_rows * g->G + 15) / 16;
-    const int64_t bound = std::min<int64_t>(passes, 9) * p->batch * p->n_kv_heads *   // below 2^63; past 8 passes not asked
+    const int64_t bound = std::min<int64_t>(passes, 9) * p->batch * p->n_kv_heads *   // below 2^63; not asked past 8
                           (((int64_t)p->max_pages * p->page_size + 127) / 128);
     g->decode = p->format == KVR_BF16 ? passes == 1 || (passes <= 8 && bound <= 3600)
                                       : p->format == KVR_INT4 && (passes <= 2 || (passes <= 8 && bound <= 5500));
@@ -142,6 +147,8 @@ kvr_status geometry(const kvr_pages* p, int32_t n_q_heads, int32_t n_rows, int32
     // splitting them finely is.  0, 1 and 3 (us): decode 64 x 300 keys 39, 37, 33 (4
     // bits 29, 27, 26), 4 drafted rows x 3 x 5001 keys 29, 25, 25, 1 x 1000 keys 17,
     // 17, 19.  In fp32 the units themselves outweigh it (4 x 500 keys 19 with 0, 23 with 1).
+    // These are captured calls alone on the GPU with inputs out of L2; one call after
+    // another takes less (1 x 1000 keys 12).
     if (!g->tc) g->run_cost = !g->decode ? 0 : items * p->n_kv_heads >= g->n_cta ? 3 : 1;
     // shares and items are counted in 32 bits
     const int64_t units = ((int64_t)p->max_pages * p->page_size + g->unit_keys - 1) / g->unit_keys + g->run_cost;

@@ -463,7 +463,9 @@ __global__ void __launch_bounds__(kThreads, Decode<NG, NT>::kCtas) paged_decode_
                     };
                     if (a.softcap <= kCapQuotient) {
                         const float in_q = cap_in * kTwoLog2e;
-                        capped([=](float2 y) { return make_float2(tanh_quotient(y.x * in_q), tanh_quotient(y.y * in_q)); });
+                        capped([=](float2 y) {
+                            return make_float2(tanh_quotient(y.x * in_q), tanh_quotient(y.y * in_q));
+                        });
                     } else {
                         capped([=](float2 y) { return tanh_either(make_float2(y.x * cap_in, y.y * cap_in)); });
                     }

@@ -17,7 +17,7 @@
 //               products; they complete in order, so "S_t of tile j is done" also
 //               says that tile j - 1's product with V is.  The warp runs the loop
 //               together: in one thread's code the descriptors passed through its
-//               registers, 100-130 cycles a product (4096 rows 378 us, now 304).
+//               registers, 100-130 cycles a product (4096 rows 378 us in place of 304 then).
 //   warp 2      Q of the next run by TMA, as soon as the last scores are done
 //               with its tile (4 bits: the softmax warps then scale it to fp16 in place).
 //   warps 4-11  softmax, four warps a row tile, one thread a row: no exchange
@@ -32,21 +32,24 @@
 //               pairs (e, e + 4), so the 8 dims of a chunk lie in the order 0 4 1
 //               5 2 6 3 7; Q is stored in that order and O read back from it.
 // Biases of keys (the same for every row) are written to shared memory once a
-// tile and read as broadcasts; a cap well above the logits is its series on the
-// FMA pipe, where two special functions a key (12 cycles of a warp) would bound the
-// tile.  4096 rows over 8192 keys: 276 us plain, 333 with biases, 426 with slopes,
-// 455 capped (610 with logits near the cap).
+// tile and read as broadcasts; a cap well above a whole tile's logits is its series
+// on the FMA pipe, where two special functions a key (12 cycles of a warp) would bound
+// the tile.  4096 rows over 8192 keys: 280 us plain, 332 with biases, 428 with slopes,
+// 475 capped (620 with logits near the cap, 833 there for caps above 64, whose small
+// logits go by the series one by one).
 // A unit is four 128^3 products (2048 cycles of the pipe) and 2 x 128 x 128
-// exponentials (1024).  Measured: 1.49 PFLOP/s at 4096 rows over 8192 keys of a
+// exponentials (1024).  Measured: 1.47 PFLOP/s at 4096 rows over 8192 keys of a
 // 32/8-head model (0.28 ms), under 3000 cycles a unit, close to the chain of a row
 // tile that bounds it: softmax 1450, its two products 1024, three hand-overs of
-// 100-150; 1.50 PFLOP/s at 8192 causal rows (0.37 ms).  4 bits: 1.24 PFLOP/s there
+// 100-150; 1.48 PFLOP/s at 8192 causal rows (0.37 ms).  4 bits: 1.26 PFLOP/s there
 // (0.44 ms); softmax and conversion share the issue slots, 3000 of a unit's 3700
 // cycles.  The group count is a template argument: a pair per 32 dims whatever the
 // group took 8 % longer.  Rows leave as one 32-byte store a thread: with 16-byte
 // halves exchanged between neighbours a run's end took 4500 cycles in place of 3000.
 // The runs' bookkeeping lives in shared memory, a copy per warp: a spilled register
-// costs an L2 round trip here, where shared memory takes all but a few KB of L1.
+// costs an L2 round trip here, where shared memory takes all but a few KB of L1.  The
+// kernels with biases or slopes still spill, 60 bytes a thread in bf16 and 122 or 142
+// in 4 bits (-Xptxas -v); plain and capped ones none.
 // Every wait is bounded; on a timeout the CTA records it, drains its copies and
 // products, frees tensor memory and returns.
 #include <cuda_bf16.h>
@@ -191,8 +194,8 @@ __device__ __forceinline__ int first_key(const PagedWalk& w, int s) { return ((w
 __device__ __forceinline__ int row_tiles(const PagedWalk& w, int per_tile) { return w.it.rows > per_tile ? 2 : 1; }
 
 // NG: scale groups of a 4-bit row, 0 for bf16 pages.  kScore: 0 products alone, 1 with
-// biases, 2 also slopes, 3 also capped (kernels of their own: the others' code made
-// a biased call's registers spill)
+// biases, 2 also slopes, 3 also capped (kernels of their own: with the others' code in
+// it a biased call spilled more, 343 us in place of 333)
 template <int NG, int kScore>
 __global__ void __launch_bounds__(NG ? 512 : 384, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
