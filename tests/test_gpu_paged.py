@@ -841,3 +841,19 @@ def test_a_bias_that_all_keys_share_costs_its_own_rounding(fmt, dh, group, count
     d = 128 * 2.0 ** -24 * noise[..., None] * (16 if fmt == "int4" else 1) + (2.0 ** -19 if f32 else 2.0 ** -14)
     d = d + 2 * abs(alpha) * 2.0 ** -24
     assert np.all(np.abs(got - o) <= r * np.abs(o) + ((0 if f32 else r) + 2 * d) * spread + 1e-30)
+
+
+@pytest.mark.parametrize("fmt,dh,group", FORMATS)
+@pytest.mark.parametrize("counts", [[1, 1, 1], [12, 9, 12], [70, 0, 33]])
+def test_tables_far_wider_than_their_sequences(fmt, dh, group, counts):
+    """A serving table of 131072 positions; two of its sequences share their
+    first pages.  The masks' words follow the table's width."""
+    lens, wide = [300, 400, 77], 131072 // 16
+    c = Paged(fmt, lens, 2, dh, 16, "hnd", group, seed=17, max_pages=wide)
+    c.table_np[1, :5] = c.table_np[0, :5]
+    c.table.copy_(i32(c.table_np))
+    pos = tail(lens, counts)
+    loc = np.random.default_rng(1).random((3, wide * 16)) < 0.3
+    out, q, _ = attend_case(c, 8, counts, pos, alpha=-2.0, local_bits=bit_words(loc))
+    kvr.kvr_paged_status(c.p)
+    check_attend(c, 8, counts, pos, out, q, alpha=-2.0, loc=loc)
