@@ -712,6 +712,119 @@ kvr_status kvr_paged_attend(const kvr_pages* p, const kvr_score_opts* opts, int3
  * enqueues nothing. */
 kvr_status kvr_paged_status(const kvr_pages* p, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Packed rows: the steps of a decoder block around the paged attention, one
+ * operator a call, with rows and weights in eight bits.  A decode step is
+ *     kvr_rows_norm -> kvr_linear (q, k, v) -> kvr_rows_rotate ->
+ *     kvr_paged_append -> kvr_paged_attend -> kvr_rows_quantise -> kvr_linear
+ *     (output) -> kvr_rows_norm (with the residual) -> kvr_linear (gate, up)
+ *     -> kvr_rows_swiglu -> kvr_linear (down),
+ * and kvr_rows_quantise / kvr_rows_dequantise also store rows such as the
+ * boundary states of kvr_refresh_range in a quarter to a half of their bytes.
+ *
+ * Rows in eight bits: signed codes and one fp32 scale a row, value = scale *
+ * code.  For the fp32 values y of a row,
+ *     top = max |y|, scale = top * fp32(1/127), code = rint(y * (1 / scale)),
+ * so codes lie in [-127, 127].  A row whose scale would be below 2^-126 gets
+ * scale 0 and codes 0; a row with an infinity or a NaN gets scale NaN and
+ * codes 0, so all it stands for is NaN and no other row is touched.
+ *
+ * dtype is KVR_F32 or KVR_BF16.  Strides are in elements of their array, at
+ * least a row's width.  Rows of any width and alignment of their elements are
+ * taken; 16-byte aligned pointers and strides (codes: 8) are moved in vectors.
+ * Widths go up to 2^20, rows to 2^31 - 1, strides to 2^29.  Sums, maxima and products are fp32
+ * (|h| stays below 2^60, so that its squares do not overflow).  Where an
+ * output may be an input, it is that array from its first element on, with
+ * the same stride; arrays do not overlap otherwise.
+ * Nothing is kept between calls, so all of them can be captured.
+ * EINVAL on NULL or misaligned arguments, sizes or strides out of range;
+ * n_rows = 0 enqueues nothing.
+ * ------------------------------------------------------------------------- */
+
+/* kvr_rows_norm -- h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight.
+ *   residual    device [n_rows][d] or NULL (h = x).
+ *   sum_out     device [n_rows][d] or NULL: h, rounded to dtype (the norm uses
+ *               it unrounded); may be x or residual.
+ *   weight      device [d], dtype.
+ *   out         device [n_rows][d] or NULL: y, rounded to dtype; may be x or
+ *               residual.
+ *   codes, scales  device int8 [n_rows][d] and float [n_rows], or both NULL: y
+ *               in eight bits.  out or codes has to be given. */
+kvr_status kvr_rows_norm(int32_t dtype, int32_t n_rows, int32_t d, const void* x, int64_t x_stride,
+                         const void* residual, int64_t residual_stride, void* sum_out, int64_t sum_stride,
+                         const void* weight, float eps, void* out, int64_t out_stride, int8_t* codes,
+                         int64_t code_stride, float* scales, void* stream);
+
+/* kvr_rows_swiglu -- y = g / (1 + exp(-g)) * u.  gate_up: device [n_rows][2 d],
+ * g the first d elements of a row, u the others; outputs as kvr_rows_norm (out
+ * may not be gate_up). */
+kvr_status kvr_rows_swiglu(int32_t dtype, int32_t n_rows, int32_t d, const void* gate_up, int64_t stride, void* out,
+                           int64_t out_stride, int8_t* codes, int64_t code_stride, float* scales, void* stream);
+
+/* kvr_rows_quantise -- rows into eight bits (weights too: a row is then an
+ * output channel); kvr_rows_dequantise -- their values scale * code, rounded
+ * once to dtype. */
+kvr_status kvr_rows_quantise(int32_t dtype, int32_t n_rows, int32_t d, const void* x, int64_t x_stride, int8_t* codes,
+                             int64_t code_stride, float* scales, void* stream);
+kvr_status kvr_rows_dequantise(int32_t dtype, int32_t n_rows, int32_t d, const int8_t* codes, int64_t code_stride,
+                               const float* scales, void* out, int64_t out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary map of any layout, part of the head, and scaled for long contexts.
+ * A kvr_rope is a plain host struct, filled by kvr_rope_init or by the caller
+ * and copied by every call.  The angle of pair i at position g is g * turns[i]
+ * modulo one turn, in integers, so it is as exact at position 2^31 - 1 as at 1.
+ *   KVR_ROPE_HALF         pair i is dims (i, i + rotary_dim / 2)
+ *   KVR_ROPE_INTERLEAVED  pair i is dims (2 i, 2 i + 1)
+ * Dims at and past rotary_dim are not turned.  cos and sin are multiplied by
+ * attn.  head_dim and rotary_dim are even, rotary_dim <= head_dim <= 256.
+ *
+ * kvr_rope_init: f_i = theta^(-2 i / rotary_dim) radians a position, then
+ *   KVR_ROPE_PLAIN   f_i
+ *   KVR_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   KVR_ROPE_NTK     theta replaced by theta * factor^(rotary_dim / (rotary_dim - 2))
+ *   KVR_ROPE_BANDS   by the turns t_i = original_len f_i / 2 pi that the trained
+ *                    length holds: f_i where t_i >= high, f_i / factor where
+ *                    t_i <= low, between them f_i (w + (1 - w) / factor) with
+ *                    w = (t_i - low) / (high - low)
+ *   KVR_ROPE_YARN    ("YaRN: Efficient Context Window Extension") f_i (1 - r) +
+ *                    f_i / factor r, r the ramp from 0 to 1 over the pairs
+ *                    [floor(d(high)), ceil(d(low))] with d(t) = rotary_dim *
+ *                    ln(original_len / (2 pi t)) / (2 ln theta); attn = 0.1 ln(factor) + 1
+ * attn_factor replaces attn when it is not 0.  theta > 1, factor >= 1; low,
+ * high (0 < low < high) and original_len >= 1 for the last two only.
+ * ------------------------------------------------------------------------- */
+enum { KVR_ROPE_HALF = 0, KVR_ROPE_INTERLEAVED = 1 };
+enum { KVR_ROPE_PLAIN = 0, KVR_ROPE_LINEAR, KVR_ROPE_NTK, KVR_ROPE_BANDS, KVR_ROPE_YARN };
+#define KVR_ROPE_INVERSE 0x1u   /* turn by minus the angle and divide by attn: takes a rotation out again */
+
+typedef struct {
+    int32_t head_dim, rotary_dim, layout;
+    float attn;
+    uint64_t turns[128];   /* fraction of a turn a position, times 2^64 */
+} kvr_rope;
+
+kvr_status kvr_rope_init(kvr_rope* rope, int32_t head_dim, int32_t rotary_dim, int32_t layout, int32_t scaling,
+                         double theta, double factor, double low, double high, int32_t original_len,
+                         float attn_factor);
+
+/* kvr_rope_table -- (cos, sin) of positions [0, rope_len): device float
+ * [rope_len][rotary_dim / 2][2], 8-byte aligned.  With rotary_dim = head_dim and
+ * KVR_ROPE_HALF it is the table that kvr_paged_append takes. */
+kvr_status kvr_rope_table(const kvr_rope* rope, int32_t rope_len, float* table, void* stream);
+
+/* kvr_rows_rotate -- query and key heads of packed rows, turned at the rows'
+ * positions (device int32 [n_rows], any value, negative ones too: a splice or a
+ * shift turns keys by the difference).  q, k: device [n_rows][heads][head_dim],
+ * a row's heads contiguous; either may be NULL with its output and heads 0.
+ * An output may be its input (dims that are not turned then stay untouched).
+ * fp32, each product and sum rounded on its own, rounded once to dtype.
+ * flags: KVR_ROPE_INVERSE. */
+kvr_status kvr_rows_rotate(const kvr_rope* rope, int32_t dtype, int32_t n_rows, const int32_t* positions, const void* q,
+                           int64_t q_stride, int32_t n_q_heads, void* q_out, int64_t q_out_stride, const void* k,
+                           int64_t k_stride, int32_t n_kv_heads, void* k_out, int64_t k_out_stride, uint32_t flags,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,40 @@
+// rows.h -- packed-row operators: norms and gates into eight bits, the rotary
+// map, and projections by 8-bit weights (rows_api.cu, rows_quant.cu,
+// rows_rotate.cu, linear.cu).
+#pragma once
+#include "kvr_internal.h"
+
+namespace kvr {
+
+enum class RowOp { Norm, Swiglu, Quantise };
+
+struct RowsQuant {
+    const uint8_t* x;       // Norm: rows; Swiglu: gate, up halves; Quantise: rows
+    const uint8_t* res;     // Norm, nullable
+    const uint8_t* weight;  // Norm
+    uint8_t* sum;           // Norm, nullable
+    uint8_t* out;           // nullable
+    int8_t* codes;          // nullable, with scales
+    float* scales;
+    int64_t x_stride, res_stride, sum_stride, out_stride, code_stride;   // elements
+    int n_rows, d;
+    float eps;
+};
+cudaError_t launch_rows_quant(RowOp op, int dtype, const RowsQuant& a, cudaStream_t s);
+cudaError_t launch_rows_dequantise(int dtype, int n_rows, int d, const int8_t* codes, int64_t code_stride,
+                                   const float* scales, void* out, int64_t out_stride, cudaStream_t s);
+
+struct RowsRotate {
+    kvr_rope rope;
+    const uint8_t* in[2];   // queries, keys
+    uint8_t* out[2];
+    int64_t in_stride[2], out_stride[2];   // elements
+    int heads[2];
+    const int* pos;
+    int n_rows;
+    bool inverse;
+};
+cudaError_t launch_rows_rotate(int dtype, const RowsRotate& a, cudaStream_t s);
+cudaError_t launch_rope_table(const kvr_rope& rope, int rope_len, float2* table, cudaStream_t s);
+
+}  // namespace kvr

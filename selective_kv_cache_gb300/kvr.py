@@ -40,7 +40,8 @@ EXPORTS = ["kvr_create_cache", "kvr_destroy_cache", "kvr_select", "kvr_workspace
            "kvr_policy_create", "kvr_policy_destroy", "kvr_policy_plan", "kvr_policy_commit", "kvr_policy_versions",
            "kvr_sur_workspace_bytes", "kvr_sur_select", "kvr_sur_status", "kvr_refresh_range",
            "kvr_wait_check", "kvr_paged_append", "kvr_paged_read", "kvr_paged_workspace_bytes", "kvr_paged_attend",
-           "kvr_paged_status"]
+           "kvr_paged_status", "kvr_rows_norm", "kvr_rows_swiglu", "kvr_rows_quantise", "kvr_rows_dequantise",
+           "kvr_rope_init", "kvr_rope_table", "kvr_rows_rotate"]
 
 
 class kvr_model_desc(C.Structure):
@@ -65,6 +66,11 @@ class kvr_pages(C.Structure):
 class kvr_score_opts(C.Structure):
     _fields_ = [(n, C.c_float) for n in ("scale", "softcap", "alpha", "beta")] + \
                [(n, C.c_void_p) for n in ("local_bits", "sink_bits", "slopes", "key_begin", "key_end")]
+
+
+class kvr_rope(C.Structure):
+    _fields_ = [("head_dim", C.c_int32), ("rotary_dim", C.c_int32), ("layout", C.c_int32), ("attn", C.c_float),
+                ("turns", C.c_uint64 * 128)]
 
 
 class KvrError(RuntimeError):
@@ -121,6 +127,13 @@ lib.kvr_paged_workspace_bytes.argtypes = [P, I32, I32, I32]
 lib.kvr_paged_workspace_bytes.restype = C.c_size_t
 lib.kvr_paged_attend.argtypes = [P, P, I32, I32, I32, P, P, P, I64, P, I64, P, C.c_size_t, P]
 lib.kvr_paged_status.argtypes = [P, P]
+lib.kvr_rows_norm.argtypes = [I32, I32, I32, P, I64, P, I64, P, I64, P, C.c_float, P, I64, P, I64, P, P]
+lib.kvr_rows_swiglu.argtypes = [I32, I32, I32, P, I64, P, I64, P, I64, P, P]
+lib.kvr_rows_quantise.argtypes = [I32, I32, I32, P, I64, P, I64, P, P]
+lib.kvr_rows_dequantise.argtypes = [I32, I32, I32, P, I64, P, P, I64, P]
+lib.kvr_rope_init.argtypes = [P, I32, I32, I32, I32, C.c_double, C.c_double, C.c_double, C.c_double, I32, C.c_float]
+lib.kvr_rope_table.argtypes = [P, I32, P, P]
+lib.kvr_rows_rotate.argtypes = [P, I32, I32, P, P, I64, I32, P, I64, P, I64, I32, P, I64, C.c_uint32, P]
 for _f in EXPORTS:
     if _f not in ("kvr_workspace_bytes", "kvr_last_error", "kvr_restart_layer", "kvr_sur_workspace_bytes",
                   "kvr_paged_workspace_bytes"):
@@ -598,3 +611,158 @@ def kvr_paged_attend(p: kvr_pages, opts: Optional[kvr_score_opts], max_rows: int
 
 def kvr_paged_status(p: kvr_pages, stream=None):
     _check(lib.kvr_paged_status(C.byref(p), _paged_stream(p, stream)), "kvr_paged_status")
+
+
+# ---------------------------------------------------------------- packed rows
+_DTYPES = {torch.float32: KVR_F32, torch.bfloat16: KVR_BF16}
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+KVR_ROPE_INVERSE = 0x1
+
+
+def _row_stream(dev, stream) -> int:
+    # a launch goes to the current device, whichever device the pointers are of
+    if torch._C._cuda_getDevice() != dev.index:
+        raise ValueError(f"tensors on {dev}: make it the current device")
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+
+
+def _row_args(t, what: str, like, width: int, dtype=None, n: Optional[int] = None):
+    """(pointer, stride) of [rows, width] rows beside the tensor `like`."""
+    try:
+        rows, w = t.shape
+        s0, s1 = t.stride()
+    except (AttributeError, ValueError):
+        raise ValueError(f"{what}: need a tensor of rows") from None
+    n = like.shape[0] if n is None else n
+    if rows != n or w != width or (s1 != 1 and w > 1) or t.dtype is not (dtype or like.dtype) or t.device != like.device \
+            or not t.is_cuda or (s0 < w and rows > 1):
+        raise ValueError(f"{what}: need [{n}, {width}] of {dtype or like.dtype} on {like.device}, elements of a row "
+                         f"contiguous; got {tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
+    # the stride of a single row is whatever torch says; the library wants a full one
+    return t.data_ptr(), s0 if s0 > w else w
+
+
+def _scales(t, what: str, like, n: int):
+    if t.dtype is not torch.float32 or t.device != like.device or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what}: need {n} contiguous fp32 values on {like.device}")
+    return t.data_ptr()
+
+
+def _outputs(x, d: int, out, codes, scales):
+    """The arguments of the two forms of a row operator's result."""
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+    o = (None, 0) if out is None else _row_args(out, "out", x, d)
+    c = (None, 0, None) if codes is None else (*_row_args(codes, "codes", x, d, torch.int8),
+                                               _scales(scales, "scales", x, x.shape[0]))
+    return (*o, *c)
+
+
+def _dtype(x, what: str = "x") -> int:
+    if x.dtype not in _DTYPES or x.dim() != 2:
+        raise ValueError(f"{what}: need a 2-d bf16 or fp32 tensor, got a {x.dim()}-d {x.dtype} tensor")
+    return _DTYPES[x.dtype]
+
+
+def kvr_rows_norm(x, weight, eps: float, residual=None, sum_out=None, out=None, codes=None, scales=None, stream=None):
+    """x: [n, d]; residual, sum_out, out: as x or None; weight: [d] of x's
+    type; codes: int8 [n, d] with scales fp32 [n], or None."""
+    dt, (n, d) = _dtype(x), x.shape
+    xp = _row_args(x, "x", x, d)
+    rp = (None, 0) if residual is None else _row_args(residual, "residual", x, d)
+    sp = (None, 0) if sum_out is None else _row_args(sum_out, "sum_out", x, d)
+    if weight.dtype is not x.dtype or weight.device != x.device or not weight.is_contiguous() or weight.numel() != d:
+        raise ValueError(f"weight: need {d} contiguous values of {x.dtype} on {x.device}")
+    _check(lib.kvr_rows_norm(dt, n, d, *xp, *rp, *sp, weight.data_ptr(), eps, *_outputs(x, d, out, codes, scales),
+                             _row_stream(x.device, stream)), "kvr_rows_norm")
+
+
+def kvr_rows_swiglu(gate_up, out=None, codes=None, scales=None, stream=None):
+    """gate_up: [n, 2 d]; outputs as kvr_rows_norm, d wide."""
+    dt, (n, wide) = _dtype(gate_up, "gate_up"), gate_up.shape
+    if wide % 2:
+        raise ValueError("gate_up: need an even width")
+    gp = _row_args(gate_up, "gate_up", gate_up, wide)
+    _check(lib.kvr_rows_swiglu(dt, n, wide // 2, *gp, *_outputs(gate_up, wide // 2, out, codes, scales),
+                               _row_stream(gate_up.device, stream)), "kvr_rows_swiglu")
+
+
+def kvr_rows_quantise(x, codes, scales, stream=None):
+    """x: [n, d] into codes int8 [n, d] and scales fp32 [n]."""
+    dt, (n, d) = _dtype(x), x.shape
+    _check(lib.kvr_rows_quantise(dt, n, d, *_row_args(x, "x", x, d), *_outputs(x, d, None, codes, scales)[2:],
+                                 _row_stream(x.device, stream)), "kvr_rows_quantise")
+
+
+def kvr_rows_dequantise(codes, scales, out, stream=None):
+    """codes int8 [n, d] and scales fp32 [n] into out [n, d], bf16 or fp32."""
+    dt, (n, d) = _dtype(out, "out"), out.shape
+    _check(lib.kvr_rows_dequantise(dt, n, d, *_row_args(codes, "codes", out, d, torch.int8),
+                                   _scales(scales, "scales", out, n), *_row_args(out, "out", out, d),
+                                   _row_stream(out.device, stream)), "kvr_rows_dequantise")
+
+
+def kvr_rope_init(head_dim: int, rotary_dim: int, layout: int, scaling: int, theta: float, factor: float, low: float,
+                  high: float, original_len: int, attn_factor: float) -> kvr_rope:
+    r = kvr_rope()
+    _check(lib.kvr_rope_init(C.byref(r), head_dim, rotary_dim, layout, scaling, theta, factor, low, high, original_len,
+                             attn_factor), "kvr_rope_init")
+    r.addr = C.addressof(r)
+    return r
+
+
+def rope(head_dim: int, rotary_dim: Optional[int] = None, layout: str = "half", theta: float = 10000.0,
+         scaling: str = "plain", factor: float = 1.0, low: float = 0.0, high: float = 0.0, original_len: int = 0,
+         attn_factor: float = 0.0) -> kvr_rope:
+    """kvr_rope by names: layout "half" or "interleaved"; scaling "plain",
+    "linear", "ntk", "bands" or "yarn" (low, high: turns of the trained length,
+    see kvr_rope_init; a yarn's beta_slow and beta_fast)."""
+    if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"layout one of {sorted(_ROPE_LAYOUTS)}, scaling one of {sorted(_ROPE_SCALINGS)}")
+    return kvr_rope_init(head_dim, head_dim if rotary_dim is None else rotary_dim, _ROPE_LAYOUTS[layout],
+                         _ROPE_SCALINGS[scaling], theta, factor, low, high, original_len, attn_factor)
+
+
+def kvr_rope_table(r: kvr_rope, rope_len: int, table, stream=None):
+    """table: contiguous fp32 [rope_len, rotary_dim / 2, 2]."""
+    if _want(table, "table", torch.float32).shape != (rope_len, r.rotary_dim // 2, 2) or not table.is_contiguous():
+        raise ValueError(f"table: need a contiguous [{rope_len}, {r.rotary_dim // 2}, 2]")
+    _check(lib.kvr_rope_table(r.addr, rope_len, table.data_ptr(), _row_stream(table.device, stream)), "kvr_rope_table")
+
+
+def _heads(r: kvr_rope, t, what: str, n: int, like):
+    """(pointer, row stride, heads) of a [rows, heads, head_dim] operand."""
+    dh = r.head_dim
+    try:
+        rows, heads, d = t.shape
+        s0, s1, s2 = t.stride()
+    except ValueError:
+        rows = -1
+    if rows != n or d != dh or s2 != 1 or (s1 != dh and heads > 1) or (s0 < heads * dh and rows > 1) or \
+            t.dtype is not like.dtype or t.dtype not in _DTYPES or t.device != like.device:
+        raise ValueError(f"{what}: need [{n}, heads, {dh}] in bf16 or fp32, a row's heads contiguous, like the others; "
+                         f"got {tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
+    return t.data_ptr(), s0 if s0 > heads * dh else heads * dh, heads
+
+
+def kvr_rows_rotate(r: kvr_rope, positions, q=None, q_out=None, k=None, k_out=None, inverse: bool = False, stream=None):
+    """q, k: [n, heads, head_dim]; q_out, k_out: the same shapes, or the
+    inputs themselves; a pair may be None.  positions: int32 [n]."""
+    like = q if q is not None else k
+    if like is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out, k and k_out go together, and one of the pairs is needed")
+    _int_array(positions, "positions", None, like.device)
+    n = positions.numel()
+    args = []
+    for i, o, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if i is None:
+            args += (None, 0, 0, None, 0)
+            continue
+        ip, istride, heads = _heads(r, i, what, n, like)
+        op, ostride, ho = _heads(r, o, what + "_out", n, like)
+        if ho != heads:
+            raise ValueError(f"{what}_out: need {what}'s heads")
+        args += (ip, istride, heads, op, ostride)
+    _check(lib.kvr_rows_rotate(r.addr, _DTYPES[like.dtype], n, positions.data_ptr(), *args,
+                               KVR_ROPE_INVERSE if inverse else 0, _row_stream(like.device, stream)), "kvr_rows_rotate")
