@@ -825,6 +825,43 @@ kvr_status kvr_rows_rotate(const kvr_rope* rope, int32_t dtype, int32_t n_rows, 
                            int64_t k_stride, int32_t n_kv_heads, void* k_out, int64_t k_out_stride, uint32_t flags,
                            void* stream);
 
+/* ---------------------------------------------------------------------------
+ * kvr_linear -- projection of 8-bit rows by 8-bit weights:
+ *     out[r][n] = (sum_k a[r][k] w[n][k]) * scales[r] * w.scales[n] + bias[n],
+ * rounded once to dtype.  A kvr_linear_weights is a plain host struct of
+ * device pointers, one weight matrix in nn.Linear layout (a row an output
+ * channel, as kvr_rows_quantise leaves it); nothing is owned or kept.
+ *   codes       device int8 [n_rows][k], stride bytes apart; 16-byte aligned,
+ *               stride a multiple of 16, for the weights too.  Codes may be
+ *               -128 to 127.  k up to 65536 and n_out up to 2^20, any size.
+ *   out         device [n_rows][n_out], out_stride elements apart; it does not
+ *               overlap an input.
+ *   workspace   device, >= kvr_linear_workspace_bytes(w, n_rows), 256-byte
+ *               aligned; needs no initialisation.  Calls whose GPU work
+ *               overlaps need a workspace each.
+ * Up to 16 rows the sums are 32-bit integers; for more rows they are formed by
+ * the tensor cores in fp32, which holds them exactly up to 2^24 and rounds
+ * each step above that to 2^-24 of itself.  The same inputs give the same
+ * bits.  A row or channel whose scale is NaN is NaN.
+ * EINVAL as the row operators; device-side failures (a wait that gave up) go
+ * to w->err and are reported, and cleared, by kvr_linear_status, which
+ * synchronises `stream`.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t n_out, k;
+    int64_t stride;          /* bytes between rows */
+    const int8_t* codes;     /* device [n_out][k] */
+    const float* scales;     /* device [n_out] */
+    const float* bias;       /* device [n_out] or NULL */
+    int32_t* err;            /* device [4], zeroed once by the caller */
+} kvr_linear_weights;
+
+size_t kvr_linear_workspace_bytes(const kvr_linear_weights* w, int32_t n_rows);
+kvr_status kvr_linear(const kvr_linear_weights* w, int32_t n_rows, const int8_t* codes, int64_t stride,
+                      const float* scales, int32_t dtype, void* out, int64_t out_stride, void* workspace,
+                      size_t ws_bytes, void* stream);
+kvr_status kvr_linear_status(const kvr_linear_weights* w, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,157 @@
+// linear_mma.cu -- projection of a few 8-bit rows: y[r][f] = s_r t_f sum_k
+// a[r][k] w[f][k] + bias[f], the sums as 32-bit integers (m16n8k32 on signed
+// bytes: products and sums exact).
+//
+// A decode step's handful of rows reads every weight byte once and does 2 n_rows
+// operations on it: HBM-bound.  Weights are the M operand, loaded straight into
+// registers: K may be taken in any order as long as both operands take the
+// same, so a thread's fragments are 16 consecutive bytes of one weight row, and
+// four threads read 64 of it.  A warp holds 32 features; the block's eight warps
+// and the cluster's blocks take every 64-byte step in turn, so that they read
+// neighbouring bytes at a time, and the partial sums meet in shared memory, the
+// cluster's over distributed shared memory: one launch, no workspace, any order
+// of addition the same integer.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "rows.h"
+
+namespace kvr {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMT = 2, kFeatures = 16 * kMT;   // weight tiles of a warp, features of a block
+
+__device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 load_stream(const int8_t* p) {   // weights: read once
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+// the bytes of [p, p + 16) that lie before the end of the row, zeros behind
+__device__ __forceinline__ uint4 load_tail(const int8_t* p, int left) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < left) w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ int load_peer(const int* p, uint32_t rank) {
+    int v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.s32 %0, [a];\n\t}"
+        : "=r"(v)
+        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// kNT: groups of eight rows a block takes; kUnroll: steps in flight a warp.
+template <int kNT, int kUnroll>
+__global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ Linear a, int split) {
+    constexpr int kRows = 8 * kNT, kTile = kFeatures * kRows;
+    __shared__ int part[kWarps][kTile];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int rank = (int)blockIdx.x % split, f0 = (int)blockIdx.x / split * kFeatures, r0 = blockIdx.y * kRows;
+    // rows past the end are read as the last one and not written
+    const int8_t* wp[kMT][2];
+    const int8_t* xp[kNT];
+#pragma unroll
+    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) wp[m][h] = a.w + (int64_t)min(f0 + 16 * m + 8 * h + g, a.n_out - 1) * a.w_stride + 16 * t;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) xp[n] = a.x + (int64_t)min(r0 + 8 * n + g, a.n_rows - 1) * a.x_stride + 16 * t;
+    int acc[kMT][kNT][4] = {};
+    auto products = [&](const uint4 (&w)[kMT][2], const uint4 (&x)[kNT]) {
+#pragma unroll
+        for (int m = 0; m < kMT; ++m)
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+                mma_s8(acc[m][n], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[n].x, x[n].y);
+                mma_s8(acc[m][n], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[n].z, x[n].w);
+            }
+    };
+    const int steps = a.k / 64, stride = kWarps * split;
+    for (int s = rank * kWarps + warp; s < steps; s += stride * kUnroll) {
+        uint4 w[kUnroll][kMT][2], x[kUnroll][kNT];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int at = 64 * min(s + u * stride, steps - 1);   // a step past the end is loaded, not used
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) w[u][m][h] = load_stream(wp[m][h] + at);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) x[u][n] = *reinterpret_cast<const uint4*>(xp[n] + at);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (s + u * stride < steps) products(w[u], x[u]);
+    }
+    if (rank == split - 1 && warp == kWarps - 1 && a.k % 64) {
+        const int at = 64 * steps, left = a.k - at - 16 * t;
+        uint4 w[kMT][2], x[kNT];
+#pragma unroll
+        for (int m = 0; m < kMT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[m][h] = load_tail(wp[m][h] + at, left);
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) x[n] = load_tail(xp[n] + at, left);
+        products(w, x);
+    }
+#pragma unroll
+    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)   // row 2 t + i % 2 of the group, feature g + 8 (i / 2) of the tile
+                part[warp][(8 * n + 2 * t + (i & 1)) * kFeatures + 16 * m + g + 8 * (i >> 1)] = acc[m][n][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile; i += kThreads) {
+        int v = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += part[w][i];
+        part[0][i] = v;   // entry i is this thread's alone
+    }
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    // each block of the cluster finishes its share of the tile
+    for (int i = rank * kThreads + threadIdx.x; i < kTile; i += split * kThreads) {
+        const int r = r0 + i / kFeatures, f = f0 + i % kFeatures;
+        int v = part[0][i];
+        for (int p = 1; p < split; ++p) v += load_peer(&part[0][i], (rank + p) % split);
+        if (r >= a.n_rows || f >= a.n_out) continue;
+        float y = (float)v * a.x_scale[r] * a.w_scale[f];
+        if (a.bias) y += a.bias[f];
+        const int64_t o = (int64_t)r * a.out_stride + f;
+        if (a.dtype == KVR_F32) static_cast<float*>(a.out)[o] = y;
+        else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
+    }
+    if (split > 1) cluster_sync();   // no block leaves while another reads its sums
+}
+
+}  // namespace
+
+cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s) {
+    const int groups = (a.n_out + kFeatures - 1) / kFeatures, steps = a.k / 64;
+    // blocks for every SM twice over, as long as a warp has a batch of steps
+    int split = 1;
+    while (split < 8 && groups * split < 2 * kNumSMs && steps >= 2 * split * kWarps * 2) split *= 2;
+    auto go = [&](auto kernel, int rows) {
+        return launch_clusters(split, kernel, dim3(groups * split, (a.n_rows + rows - 1) / rows), dim3(kThreads), 0, s, a,
+                               split);
+    };
+    return a.n_rows <= 8 ? go(linear_mma_kernel<1, 4>, 8) : go(linear_mma_kernel<2, 4>, 16);
+}
+
+}  // namespace kvr

@@ -35,6 +35,21 @@ struct RowsRotate {
     bool inverse;
 };
 cudaError_t launch_rows_rotate(int dtype, const RowsRotate& a, cudaStream_t s);
+struct Linear {
+    const int8_t* w;
+    const float* w_scale;
+    const float* bias;      // nullable
+    const int8_t* x;
+    const float* x_scale;
+    void* out;
+    int64_t w_stride, x_stride, out_stride;   // bytes, bytes, elements
+    int n_out, k, n_rows, dtype;
+    int* err;
+    void* workspace;
+};
+constexpr int kLinearMmaRows = 16;   // up to these rows the integer kernel takes the call
+cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s);
+
 cudaError_t launch_rope_table(const kvr_rope& rope, int rope_len, float2* table, cudaStream_t s);
 
 }  // namespace kvr

@@ -49,6 +49,18 @@ kvr_status check_outputs(int32_t dtype, int32_t d, const void* out, int64_t out_
     return KVR_OK;
 }
 
+kvr_status check_weights(const kvr_linear_weights* w) {
+    if (!w) return fail(KVR_EINVAL, "weights is NULL");
+    if (w->n_out < 1 || w->n_out > kMaxWidth || w->k < 1 || w->k > 65536)
+        return fail(KVR_EINVAL, "weights: n_out or k out of range");
+    if (!rows_ok(w->codes, w->k, w->stride, 16) || w->stride % 16)
+        return fail(KVR_EINVAL, "weights: codes must be 16-byte aligned, their stride a multiple of 16 and at least a row");
+    if (!rows_ok(w->scales, 1, 1, 4) || (w->bias && !rows_ok(w->bias, 1, 1, 4)) || !rows_ok(w->err, 1, 1, 4))
+        return fail(KVR_EINVAL, "weights: scales, bias and err must be aligned, scales and err not NULL");
+    return KVR_OK;
+}
+size_t linear_workspace(const kvr_linear_weights&, int32_t) { return 256; }
+
 kvr_status check_rope(const kvr_rope* r) {
     if (!r) return fail(KVR_EINVAL, "rope is NULL");
     if (r->head_dim < 2 || r->head_dim > 256 || r->head_dim % 2 || r->rotary_dim < 2 || r->rotary_dim > r->head_dim ||
@@ -259,6 +271,62 @@ kvr_status kvr_rows_rotate(const kvr_rope* rope, int32_t dtype, int32_t n_rows, 
     a.inverse = (flags & KVR_ROPE_INVERSE) != 0;
     KVR_CHECK_LAUNCH(launch_rows_rotate(dtype, a, reinterpret_cast<cudaStream_t>(stream)), "rows rotate");
     return KVR_OK;
+}
+
+size_t kvr_linear_workspace_bytes(const kvr_linear_weights* w, int32_t n_rows) {
+    if (check_weights(w) != KVR_OK || n_rows < 1) return 0;
+    return linear_workspace(*w, n_rows);
+}
+
+kvr_status kvr_linear(const kvr_linear_weights* w, int32_t n_rows, const int8_t* codes, int64_t stride,
+                      const float* scales, int32_t dtype, void* out, int64_t out_stride, void* workspace,
+                      size_t ws_bytes, void* stream) {
+    pdl_begin_call();
+    kvr_status st = check_weights(w);
+    if (st != KVR_OK) return st;
+    if (!dtype_ok(dtype)) return fail(KVR_EINVAL, "linear: dtype must be KVR_F32 or KVR_BF16");
+    if (n_rows < 0 || n_rows > kMaxWidth * 4) return fail(KVR_EINVAL, "linear: n_rows out of range");
+    if (!rows_ok(codes, w->k, stride, 16) || stride % 16 || !rows_ok(scales, 1, 1, 4))
+        return fail(KVR_EINVAL, "linear: row codes must be 16-byte aligned, their stride a multiple of 16 and at least a "
+                                "row, scales aligned");
+    if (!rows_ok(out, w->n_out, out_stride, size_of(dtype)))
+        return fail(KVR_EINVAL, "linear: out must be non-NULL, aligned to its elements and at least a row apart");
+    if (n_rows == 0) return KVR_OK;
+    const size_t need = linear_workspace(*w, n_rows);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || ws_bytes < need)
+        return fail(KVR_EINVAL, "linear: workspace is NULL, not 256-byte aligned or below kvr_linear_workspace_bytes");
+    Linear a{};
+    a.w = w->codes;
+    a.w_scale = w->scales;
+    a.bias = w->bias;
+    a.x = codes;
+    a.x_scale = scales;
+    a.out = out;
+    a.w_stride = w->stride;
+    a.x_stride = stride;
+    a.out_stride = out_stride;
+    a.n_out = w->n_out;
+    a.k = w->k;
+    a.n_rows = n_rows;
+    a.dtype = dtype;
+    a.err = w->err;
+    a.workspace = workspace;
+    KVR_CHECK_LAUNCH(launch_linear_mma(a, reinterpret_cast<cudaStream_t>(stream)), "linear");
+    return KVR_OK;
+}
+
+kvr_status kvr_linear_status(const kvr_linear_weights* w, void* stream) {
+    if (!w || !w->err) return fail(KVR_EINVAL, "linear: weights or their err are NULL");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int32_t e4[4] = {0, 0, 0, 0};
+    cudaError_t e = cudaMemcpyAsync(e4, w->err, sizeof(e4), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "linear status");
+    if (e4[0] == 0) return KVR_OK;
+    e = cudaMemsetAsync(w->err, 0, sizeof(e4), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "linear status");
+    return fail((e4[0] & DEV_ERR_TIMEOUT) ? KVR_ETIMEOUT : KVR_EDEVICE, "linear: a device-side wait timed out");
 }
 
 }  // extern "C"

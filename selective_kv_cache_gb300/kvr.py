@@ -41,7 +41,8 @@ EXPORTS = ["kvr_create_cache", "kvr_destroy_cache", "kvr_select", "kvr_workspace
            "kvr_sur_workspace_bytes", "kvr_sur_select", "kvr_sur_status", "kvr_refresh_range",
            "kvr_wait_check", "kvr_paged_append", "kvr_paged_read", "kvr_paged_workspace_bytes", "kvr_paged_attend",
            "kvr_paged_status", "kvr_rows_norm", "kvr_rows_swiglu", "kvr_rows_quantise", "kvr_rows_dequantise",
-           "kvr_rope_init", "kvr_rope_table", "kvr_rows_rotate"]
+           "kvr_rope_init", "kvr_rope_table", "kvr_rows_rotate", "kvr_linear_workspace_bytes", "kvr_linear",
+           "kvr_linear_status"]
 
 
 class kvr_model_desc(C.Structure):
@@ -71,6 +72,11 @@ class kvr_score_opts(C.Structure):
 class kvr_rope(C.Structure):
     _fields_ = [("head_dim", C.c_int32), ("rotary_dim", C.c_int32), ("layout", C.c_int32), ("attn", C.c_float),
                 ("turns", C.c_uint64 * 128)]
+
+
+class kvr_linear_weights(C.Structure):
+    _fields_ = [("n_out", C.c_int32), ("k", C.c_int32), ("stride", C.c_int64)] + \
+               [(n, C.c_void_p) for n in ("codes", "scales", "bias", "err")]
 
 
 class KvrError(RuntimeError):
@@ -131,12 +137,16 @@ lib.kvr_rows_norm.argtypes = [I32, I32, I32, P, I64, P, I64, P, I64, P, C.c_floa
 lib.kvr_rows_swiglu.argtypes = [I32, I32, I32, P, I64, P, I64, P, I64, P, P]
 lib.kvr_rows_quantise.argtypes = [I32, I32, I32, P, I64, P, I64, P, P]
 lib.kvr_rows_dequantise.argtypes = [I32, I32, I32, P, I64, P, P, I64, P]
+lib.kvr_linear_workspace_bytes.argtypes = [P, I32]
+lib.kvr_linear_workspace_bytes.restype = C.c_size_t
+lib.kvr_linear.argtypes = [P, I32, P, I64, P, I32, P, I64, P, C.c_size_t, P]
+lib.kvr_linear_status.argtypes = [P, P]
 lib.kvr_rope_init.argtypes = [P, I32, I32, I32, I32, C.c_double, C.c_double, C.c_double, C.c_double, I32, C.c_float]
 lib.kvr_rope_table.argtypes = [P, I32, P, P]
 lib.kvr_rows_rotate.argtypes = [P, I32, I32, P, P, I64, I32, P, I64, P, I64, I32, P, I64, C.c_uint32, P]
 for _f in EXPORTS:
     if _f not in ("kvr_workspace_bytes", "kvr_last_error", "kvr_restart_layer", "kvr_sur_workspace_bytes",
-                  "kvr_paged_workspace_bytes"):
+                  "kvr_paged_workspace_bytes", "kvr_linear_workspace_bytes"):
         getattr(lib, _f).restype = C.c_int
 
 
@@ -766,3 +776,45 @@ def kvr_rows_rotate(r: kvr_rope, positions, q=None, q_out=None, k=None, k_out=No
         args += (ip, istride, heads, op, ostride)
     _check(lib.kvr_rows_rotate(r.addr, _DTYPES[like.dtype], n, positions.data_ptr(), *args,
                                KVR_ROPE_INVERSE if inverse else 0, _row_stream(like.device, stream)), "kvr_rows_rotate")
+
+
+def linear_weights(codes, scales, err, bias=None) -> kvr_linear_weights:
+    """kvr_linear_weights of device tensors (kept alive by the struct): codes
+    int8 [n_out, k], rows a multiple of 16 bytes apart; scales, bias: fp32
+    [n_out]; err: int32 [4], zeroed."""
+    if codes.dim() != 2:
+        raise ValueError("codes: need [n_out, k]")
+    ptr, stride = _row_args(codes, "codes", codes, codes.shape[1], torch.int8)
+    _int_array(err, "err", 4, codes.device)
+    n = codes.shape[0]
+    w = kvr_linear_weights(n, codes.shape[1], stride if n > 1 else -(-stride // 16) * 16, ptr,
+                           _scales(scales, "scales", codes, n), None if bias is None else _scales(bias, "bias", codes, n),
+                           _ptr(err))
+    w.tensors = (codes, scales, bias, err)
+    w.device = codes.device
+    w.addr = C.addressof(w)
+    return w
+
+
+def kvr_linear_workspace_bytes(w: kvr_linear_weights, n_rows: int) -> int:
+    return int(lib.kvr_linear_workspace_bytes(w.addr, n_rows))
+
+
+def kvr_linear(w: kvr_linear_weights, codes, scales, out, workspace, stream=None):
+    """codes: int8 [n, k], rows a multiple of 16 bytes apart; scales: fp32 [n];
+    out: [n, n_out] in bf16 or fp32; workspace: uint8 of
+    kvr_linear_workspace_bytes."""
+    dt, n = _dtype(out, "out"), out.shape[0]
+    op, os_ = _row_args(out, "out", out, w.n_out)
+    cp, cs = _row_args(codes, "codes", out, w.k, torch.int8)
+    if out.device != w.device:
+        raise ValueError(f"out: need a tensor on {w.device}")
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != w.device:
+        _want(workspace, "workspace", torch.uint8, 1, w.device)
+    # a single row's stride is whatever torch says
+    _check(lib.kvr_linear(w.addr, n, cp, cs if n > 1 else -(-cs // 16) * 16, _scales(scales, "scales", out, n), dt, op, os_,
+                          workspace.data_ptr(), workspace.numel(), _row_stream(w.device, stream)), "kvr_linear")
+
+
+def kvr_linear_status(w: kvr_linear_weights, stream=None):
+    _check(lib.kvr_linear_status(w.addr, _row_stream(w.device, stream)), "kvr_linear_status")

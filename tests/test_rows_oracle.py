@@ -158,3 +158,28 @@ def test_divisions_by_multiplication():
         for x in [0, 1, d - 1, d, d + 1, (1 << 31) - 1, (1 << 31) // d * d - 1, ((1 << 31) - 1) // d * d] + \
                 [int(v) for v in rng.integers(0, 1 << 31, 20)]:
             assert (mul * x >> 32) >> (bits - 1) == x // d
+
+
+def test_linear_refuses():
+    good = dict(n_out=64, k=128, stride=128, codes=P1, scales=P1, bias=None, err=P1)
+    args = dict(n=0, codes=P1, stride=128, scales=P1, dtype=1, out=P1, os=64, ws=P1, bytes=1 << 40, stream=None)
+
+    def call(w=None, **change):
+        s = kvr.kvr_linear_weights(*{**good, **(w or {})}.values())
+        return lib.kvr_linear(ctypes.addressof(s), *{**args, **change}.values())
+
+    assert call() == kvr.KVR_OK and call(dict(bias=P1)) == kvr.KVR_OK
+    for w in (dict(n_out=0), dict(n_out=(1 << 20) + 1), dict(k=0), dict(k=65537), dict(stride=127), dict(stride=136),
+              dict(codes=None), dict(codes=P1 + 8), dict(scales=None), dict(scales=P1 + 2), dict(bias=P3), dict(err=None)):
+        assert call(w) == kvr.KVR_EINVAL, w
+        s = kvr.kvr_linear_weights(*{**good, **w}.values())
+        assert lib.kvr_linear_workspace_bytes(ctypes.addressof(s), 4) == 0
+    for change in (dict(n=-1), dict(n=(1 << 22) + 1), dict(codes=None), dict(codes=P1 + 8), dict(stride=112),
+                   dict(stride=136), dict(scales=None), dict(dtype=2), dict(out=None), dict(out=P3), dict(os=63),
+                   dict(n=4, ws=None), dict(n=4, ws=P1 + 128), dict(n=4, bytes=255)):
+        assert call(**change) == kvr.KVR_EINVAL, change
+    assert lib.kvr_linear(None, *args.values()) == kvr.KVR_EINVAL
+    assert lib.kvr_linear_workspace_bytes(None, 4) == 0
+    s = kvr.kvr_linear_weights(*good.values())
+    assert lib.kvr_linear_workspace_bytes(ctypes.addressof(s), 0) == 0
+    assert lib.kvr_linear_status(None, None) == kvr.KVR_EINVAL
