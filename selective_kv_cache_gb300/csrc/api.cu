@@ -553,6 +553,19 @@ bool make_tmap_4d_bytes(CUtensorMap* out, const void* base, const uint64_t dims_
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, " (4-d bytes)", why);
 }
 
+bool make_tmap_2d_sw128(CUtensorMap* out, int element_bytes, const void* base, uint64_t inner, uint64_t rows,
+                        uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, std::string* why) {
+    if (!get_encode(why)) return false;
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {row_stride_bytes};
+    const cuuint32_t box[2] = {box_inner, box_rows}, step[2] = {1, 1};
+    const CUresult r = g_encode(out, element_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                                const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS && why) *why = "cuTensorMapEncodeTiled failed with " + std::to_string((int)r);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_2d_f32_sw128(CUtensorMap* out, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
                             std::string* why) {
     const uint64_t dims[2] = {inner, rows}, strides[1] = {inner * 4};

@@ -100,6 +100,10 @@ bool make_tmap_3d_bf16(CUtensorMap* out, const void* base, uint64_t d0, uint64_t
 // 4-d: dims[0] innermost (elements), strides of dims 1-3 in bytes
 bool make_tmap_4d_bf16(CUtensorMap* out, const void* base, const uint64_t dims[4], const uint64_t strides_bytes[3],
                        const uint32_t box[4], std::string* why);
+// boxes of integer elements of 1 or 2 bytes with the 128-byte swizzle, zeros
+// outside the tensor; encoded anew on every call
+bool make_tmap_2d_sw128(CUtensorMap* out, int element_bytes, const void* base, uint64_t inner, uint64_t rows,
+                        uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, std::string* why);
 // fp32 rows x 128-byte boxes with the 128-byte swizzle (rows of `inner` floats)
 bool make_tmap_2d_f32_sw128(CUtensorMap* out, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
                             std::string* why);

@@ -1,0 +1,586 @@
+// linear_tc.cu -- projection of many 8-bit rows on the sm_103a tensor cores:
+//   y[r][f] = s_r t_f sum_k a[r][k] w[f][k] + bias[f]
+//
+// This GPU's integer tensor rate is a small part of its fp16 one, and 8-bit
+// integers are exact in fp16, as are their products in the fp32 accumulator:
+// so the products run as fp16 (kind::f16) on operands that are widened on the
+// way.  The weights, which are read once, stay in eight bits up to the SM and
+// are widened there; the rows, which every feature tile reads again, are
+// widened once into the workspace by a small kernel before this one.
+//
+// Two CTAs (a cluster) work on one tile of 256 features by up to 256 rows with
+// paired products (cta_group::2): each holds 128 features of the weights and
+// half of the rows, so the rows' tile crosses shared memory half as often.
+// The widened weights are the A operand in tensor memory: written once with
+// tcgen05.st, they never return through shared memory, whose port the rows'
+// tile needs.
+//   warp 0       TMA: per stage 128 features x 128 codes and N/2 rows x 128
+//                fp16 (two swizzle atoms)
+//   warp 1       products, in the leader CTA: four of K = 16 a 64-code chunk
+//   warps 4-11   widening: set 0 (4-7) takes the first 64 codes of every stage,
+//                set 1 the second; a thread a feature.  b ^ 0x80 under the exponent of
+//                1024 is 1152 + b, less 1152 is b: exact.
+//   warps 12-15  accumulators out, a TMEM lane quarter each
+// Barriers: full (copies landed, own CTA) -> widening warps of both CTAs ->
+// a_ready (leader) -> products -> a_free, empty (both CTAs).  That the peer's
+// rows have landed the issuing thread knows from the peer's widening warps,
+// which wait for the same stage.
+//
+// Tensor memory: accumulators of two tiles at columns 0 and 384 - N (side by
+// side up to N = 192; above, they share columns, which the epilogue reads first), four
+// chunks of widened weights at 384.
+//
+// Tiles are taken in turn by the 76 pairs, whole.  The tiles that are left
+// after the last whole turn, or all of them where there are fewer than pairs,
+// are one line of (tile, 128 codes) units of which every pair takes an equal
+// share; its pieces of tiles go to the workspace as fp32 and a last kernel adds
+// them as integers.  Every wait is bounded.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+#include "rows.h"
+
+namespace kvr {
+namespace {
+
+constexpr int kPairs = kNumSMs / 2;
+constexpr int kThreads = 512;
+constexpr int kStageK = 128;                      // codes of a stage: two chunks
+constexpr uint32_t kStageA = 128 * 128;           // 128 features x 128 bytes
+constexpr uint32_t kColA = 384;                   // four chunks of 32 columns
+constexpr int kSmemMost = 227 * 1024;
+constexpr int kSuper = 8;                         // row tiles that are walked beside one another
+
+struct LinearTc {
+    Linear a;
+    float* part;            // [pairs][2][N][256]
+    int N, m_tiles, n_tiles, KB, stages;
+    int whole, rest, pairs; // tiles taken whole, tiles of the line, pairs in the grid
+    uint32_t base1;         // columns of the second accumulator
+    int shared_cols;        // whether the two share columns
+    int vec;                // out rows can be written four features at a time
+};
+
+// ---------------------------------------------------------------- paired instructions
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// one arrival on the leader CTA's barrier at this offset
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// A barrier that the other CTA's threads or products arrive on; the whole warp gets the answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    bool ok = try_wait_cluster(bar, parity);
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = try_wait_cluster(bar, parity)) && clock64() - t0 <= kWaitLimitCycles) {
+        }
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ void pair_alloc(uint32_t* slot) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+}
+// D (+)= A[tmem of both CTAs] B[smem of both]^T, fp16, K = 16
+__device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrive on both CTAs' barriers at this offset when the products issued so far are done
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// ---------------------------------------------------------------- work
+// Piece j of a pair's work: the line's pieces first (at most two), then whole tiles.
+struct Piece {
+    int tile, kb0, kb1, slot;   // slot < 0: whole
+};
+__device__ __forceinline__ int share_begin(const LinearTc& g, int pair) {
+    return (int)((long long)g.rest * g.KB * pair / g.pairs);
+}
+struct Walk {
+    int u, u1, next, slot;
+    __device__ __forceinline__ Walk(const LinearTc& g, int pair)
+        : u(share_begin(g, pair)), u1(share_begin(g, pair + 1)), next(pair), slot(2 * pair) {}
+    __device__ __forceinline__ bool take(const LinearTc& g, Piece* p) {
+        if (u < u1) {
+            const int t = u / g.KB;
+            p->tile = g.whole + t;
+            p->kb0 = u - t * g.KB;
+            p->kb1 = min(g.KB, u1 - t * g.KB);
+            const bool all = p->kb1 - p->kb0 == g.KB;
+            p->slot = all ? -1 : slot;
+            ++slot;
+            u += p->kb1 - p->kb0;
+            return true;
+        }
+        if (next >= g.whole) return false;
+        *p = Piece{next, 0, g.KB, -1};
+        next += g.pairs;
+        return true;
+    }
+};
+// Tiles in order: groups of kSuper row tiles, in a group feature tile by feature tile.
+__device__ __forceinline__ void tile_coords(const LinearTc& g, int tile, int* m, int* n) {
+    const int sg = tile / (g.m_tiles * kSuper), n0 = sg * kSuper, w = min(kSuper, g.n_tiles - n0);
+    const int i = tile - n0 * g.m_tiles;
+    *m = i / w;
+    *n = n0 + i - *m * w;
+}
+
+// ---------------------------------------------------------------- widening
+// 16 codes to fp16, in order
+__device__ __forceinline__ void widen16(uint4 u, uint32_t* h) {
+    const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+    const __half2 off = __half2half2(__ushort_as_half((unsigned short)0xe480));   // -1152
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t x = __byte_perm(w[i], 0x64646464u, e ? 0x4342 : 0x4140);
+            const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&x), off);
+            h[2 * i + e] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+    }
+}
+
+// rows of codes to rows of fp16, `pitch` elements apart
+__global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, int64_t stride, __half* out, int pitch, int k, int n_rows) {
+    pdl_trigger();
+    const int per = (k + 15) / 16;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < (int64_t)n_rows * per; t += (int64_t)gridDim.x * 256) {
+        const int64_t r = t / per;
+        const int i = (int)(t - r * per) * 16;
+        const int8_t* p = x + r * stride + i;
+        __half* o = out + r * pitch + i;
+        if (i + 16 <= k) {
+            uint32_t h[8];
+            widen16(*reinterpret_cast<const uint4*>(p), h);
+            reinterpret_cast<uint4*>(o)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            reinterpret_cast<uint4*>(o)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        } else {
+            for (int e = 0; i + e < k; ++e) o[e] = __int2half_rn(p[e]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- output
+template <bool kVec>
+__device__ __forceinline__ void write4(const LinearTc& g, int row, int f, const float* v, const float* sw, const float* bias) {
+    const float s = g.a.x_scale[row];
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = v[e] * s * sw[e] + bias[e];
+    const int64_t o = (int64_t)row * g.a.out_stride + f;
+    if (kVec && f + 4 <= g.a.n_out) {
+        if (g.a.dtype == KVR_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + o) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(y[0], y[1]), q = __floats2bfloat162_rn(y[2], y[3]);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.a.out) + o) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (f + e >= g.a.n_out) break;
+        if (g.a.dtype == KVR_F32) static_cast<float*>(g.a.out)[o + e] = y[e];
+        else static_cast<__nv_bfloat16*>(g.a.out)[o + e] = __float2bfloat16_rn(y[e]);
+    }
+}
+__device__ __forceinline__ void channel4(const LinearTc& g, int f, float* sw, float* bias) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool in = f + e < g.a.n_out;
+        sw[e] = in ? g.a.w_scale[f + e] : 0.f;
+        bias[e] = in && g.a.bias ? g.a.bias[f + e] : 0.f;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_constant__ CUtensorMap tmA,
+                                                            const __grid_constant__ CUtensorMap tmB,
+                                                            const __grid_constant__ LinearTc g) {
+    extern __shared__ uint8_t smem_raw[];
+    // the same offset in both CTAs: dynamic shared memory begins at one address in all of a grid's blocks
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int stages = g.stages;
+    const uint32_t half_rows = g.N / 2, atomB = half_rows * 128, stage_bytes = kStageA + 2 * atomB;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)stages * stage_bytes);
+    uint64_t* empty = full + stages;
+    uint64_t* a_ready = empty + stages;   // [4], the leader's
+    uint64_t* a_free = a_ready + 4;       // [4]
+    uint64_t* acc_full = a_free + 4;      // [2]
+    uint64_t* acc_empty = acc_full + 2;   // [2], the leader's
+    uint64_t* cols_free = acc_empty + 2;  // the leader's: the columns that both accumulators use are read
+    uint64_t* all_done = cols_free + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const int pair = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int t = 0; t < 4; ++t) {
+            mbar_init(&a_ready[t], 8);
+            mbar_init(&a_free[t], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8);
+        }
+        mbar_init(cols_free, 8);
+        mbar_init(all_done, 1);
+        fence_mbar_init();
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+    }
+    if (warp == 1) pair_alloc(tmem_slot);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the other CTA's barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+    pdl_trigger();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0) {
+            auto load_a = [&](int s, int m, int kb) {
+                tma_load_2d(smem + (size_t)s * stage_bytes, &tmA, &full[s], kb * kStageK, m * 256 + (int)rank * 128);
+            };
+            // no kernel of the call writes the weights: the ring's first ones go out before the wait for the rows
+            int pre = 0;
+            Piece p;
+            int m, n;
+            for (Walk w(g, pair); pre < stages && w.take(g, &p);) {
+                tile_coords(g, p.tile, &m, &n);
+                for (int kb = p.kb0; kb < p.kb1 && pre < stages; ++kb, ++pre) {
+                    mbar_arrive_expect_tx(&full[pre], stage_bytes);
+                    load_a(pre, m, kb);
+                }
+            }
+            pdl_wait();
+            int it = 0, s = 0;
+            uint32_t phase = 1;
+            for (Walk w(g, pair); ok && w.take(g, &p);) {
+                tile_coords(g, p.tile, &m, &n);
+                for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
+                    if (it >= pre) {
+                        if (!mbar_wait(&empty[s], phase)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&full[s], stage_bytes);
+                        load_a(s, m, kb);
+                    }
+                    uint8_t* b = smem + (size_t)s * stage_bytes + kStageA;
+                    tma_load_2d(b, &tmB, &full[s], kb * kStageK, n * g.N + (int)(rank * half_rows));
+                    tma_load_2d(b + atomB, &tmB, &full[s], kb * kStageK + 64, n * g.N + (int)(rank * half_rows));
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {   // let every copy still in flight land before the CTA exits
+                for (int i = (it > stages ? it - stages : 0); i < it; ++i)
+                    mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        const bool issuer = elect_one();
+        if (rank == 0) {
+            const uint32_t idesc = (1u << 4) | ((uint32_t)(g.N >> 3) << 17) | ((256u >> 4) << 24);   // fp16, fp32 sums
+            const uint64_t descB = sdesc_sw128(smem_u32(smem) + kStageA, 16, 1024);
+            int s = 0, local = 0;
+            uint32_t q = 0;
+            Piece p;
+            for (Walk w(g, pair); ok && w.take(g, &p); ++local) {
+                const int ab = local & 1;
+                if (!warp_wait(&acc_empty[ab], ((uint32_t)(local >> 1) & 1u) ^ 1u) ||
+                    (g.shared_cols && local > 0 && !warp_wait(cols_free, (uint32_t)(local - 1) & 1u))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (ab ? g.base1 : 0u);
+                for (int kb = p.kb0; kb < p.kb1; ++kb) {
+                    const uint64_t db = descB + (uint64_t)(((uint32_t)s * stage_bytes) >> 4);
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h, ++q) {
+                        const uint32_t t = q & 3u;
+                        if (!warp_wait(&a_ready[t], (q >> 2) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (issuer) {
+#pragma unroll
+                            for (uint32_t kk = 0; kk < 4; ++kk)
+                                pair_mma(d, tmem + kColA + 32 * t + 8 * kk, db + (uint64_t)((h * atomB >> 4) + 2 * kk), idesc,
+                                         (h > 0 || kk > 0) ? 1u : (kb > p.kb0 ? 1u : 0u));
+                            pair_commit(&a_free[t]);
+                            if (h == 1) pair_commit(&empty[s]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (++s == stages) s = 0;
+                }
+                if (!ok) break;
+                if (issuer) pair_commit(&acc_full[ab]);
+                __syncwarp();
+            }
+            if (issuer) pair_commit(all_done);
+            __syncwarp();
+        }
+        if (!warp_wait(all_done, 0)) ok = false;
+    } else if (warp >= 4 && warp < 12) {
+        // ------------------------------------------------------------ widening
+        const int set = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+        const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16) + kColA;
+        int s = 0;
+        uint32_t phase = 0, q = set;
+        Piece p;
+        for (Walk w(g, pair); ok && w.take(g, &p);) {
+            for (int kb = p.kb0; kb < p.kb1; ++kb, q += 2) {
+                const uint32_t t = q & 3u;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase)) || !warp_wait(&a_free[t], ((q >> 2) & 1u) ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint8_t* a = smem + (size_t)s * stage_bytes + row * 128;
+                uint32_t h[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    widen16(*reinterpret_cast<const uint4*>(a + (((4 * set + c) ^ (row & 7)) << 4)), h + 8 * c);
+                tmem_st16_async(dst + 32 * t, h);
+                tmem_st16_async(dst + 32 * t + 16, h + 16);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(&a_ready[t]);
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------ accumulators out
+        const int quarter = warp & 3, b = lane & 3;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const int fo = (int)rank * 128 + quarter * 32 + (lane & ~3);   // this lane's four features in the tile
+        int local = 0;
+        Piece p;
+        for (Walk w(g, pair); w.take(g, &p); ++local) {
+            const int ab = local & 1;
+            if (!warp_wait(&acc_full[ab], (uint32_t)(local >> 1) & 1u)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            int m, n;
+            tile_coords(g, p.tile, &m, &n);
+            const int row0 = n * g.N, f = m * 256 + fo;
+            const uint32_t src = tmem + lane_base + (ab ? g.base1 : 0u);
+            float sw[4], bias[4];
+            channel4(g, f, sw, bias);
+            // Lane l holds feature l for 16 rows; a 4 x 4 transpose within each quad of lanes leaves it features
+            // 4 (l / 4) .. + 3 of rows 4 i + l % 4.
+            auto drain = [&](int lo, int hi) {
+                for (int c = lo; c < hi; c += 16) {
+                    float v[16];
+                    tmem_ld16(src + (uint32_t)c, v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x0 = v[4 * i], x1 = v[4 * i + 1], x2 = v[4 * i + 2], x3 = v[4 * i + 3];
+                        float a0 = (b & 2) ? x0 : x2, a1 = (b & 2) ? x1 : x3;
+                        a0 = __shfl_xor_sync(0xffffffffu, a0, 2);
+                        a1 = __shfl_xor_sync(0xffffffffu, a1, 2);
+                        if (b & 2) { x0 = a0; x1 = a1; } else { x2 = a0; x3 = a1; }
+                        float c0 = (b & 1) ? x0 : x1, c1 = (b & 1) ? x2 : x3;
+                        c0 = __shfl_xor_sync(0xffffffffu, c0, 1);
+                        c1 = __shfl_xor_sync(0xffffffffu, c1, 1);
+                        if (b & 1) { x0 = c0; x2 = c1; } else { x1 = c0; x3 = c1; }
+                        const int col = c + 4 * i + b, row = row0 + col;
+                        if (row < g.a.n_rows && f < g.a.n_out) {
+                            const float y[4] = {x0, x1, x2, x3};
+                            if (p.slot >= 0)
+                                *reinterpret_cast<float4*>(g.part + ((size_t)p.slot * g.N + col) * 256 + fo) =
+                                    make_float4(x0, x1, x2, x3);
+                            else if (g.vec)
+                                write4<true>(g, row, f, y, sw, bias);
+                            else
+                                write4<false>(g, row, f, y, sw, bias);
+                        }
+                    }
+                }
+            };
+            if (g.shared_cols) {   // the columns that the next tile's accumulator shares first
+                const int lo = ab ? 0 : (int)g.base1, hi = ab ? g.N - (int)g.base1 : g.N;
+                drain(lo, hi);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(cols_free);
+                drain(0, lo);
+                drain(hi, g.N);
+            } else {
+                drain(0, g.N);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_leader(&acc_empty[ab]);
+        }
+    }
+    if (!ok) atomicOr(g.a.err, DEV_ERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no product or arrival of the pair is on its way any more
+    if (warp == 1) {
+        tc_fence_after();
+        pair_dealloc(tmem);
+    }
+}
+
+// The line's tiles: pieces added as integers, in any order the same.
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearTc g) {
+    pdl_wait();
+    const int per = 64 * g.N;   // four features a thread
+    const int tile = (int)(blockIdx.x / ((per + 255) / 256)), i = (int)(blockIdx.x % ((per + 255) / 256)) * 256 + threadIdx.x;
+    int m, n;
+    tile_coords(g, g.whole + tile, &m, &n);
+    const int col = i / 64, fo = 4 * (i % 64), row = n * g.N + col, f = m * 256 + fo;
+    if (i >= per || row >= g.a.n_rows || f >= g.a.n_out) return;
+    // the pairs whose shares meet [u0, u0 + KB)
+    const long long T = (long long)g.rest * g.KB, u0 = (long long)tile * g.KB, u1 = u0 + g.KB;
+    int pair = (int)(u0 * g.pairs / T);
+    while (pair > 0 && share_begin(g, pair) > u0) --pair;
+    while (share_begin(g, pair + 1) <= u0) ++pair;
+    int sum[4] = {0, 0, 0, 0};
+    for (; pair < g.pairs; ++pair) {
+        const int b = share_begin(g, pair), e = share_begin(g, pair + 1);
+        if (b >= u1) break;
+        if (b == e) continue;
+        if (b <= u0 && e >= u1) return;   // one pair had all of it and wrote it
+        const int slot = 2 * pair + (tile - b / g.KB);
+        const float4 v = *reinterpret_cast<const float4*>(g.part + ((size_t)slot * g.N + col) * 256 + fo);
+        sum[0] += __float2int_rn(v.x);
+        sum[1] += __float2int_rn(v.y);
+        sum[2] += __float2int_rn(v.z);
+        sum[3] += __float2int_rn(v.w);
+    }
+    float sw[4], bias[4];
+    channel4(g, f, sw, bias);
+    const float y[4] = {(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]};
+    if (g.vec) write4<true>(g, row, f, y, sw, bias);
+    else write4<false>(g, row, f, y, sw, bias);
+}
+
+struct Plan {
+    int N, m_tiles, n_tiles, KB, stages, whole, rest, pairs, pitch;
+    size_t rows_bytes, part_bytes;
+};
+Plan make_plan(int n_out, int k, int n_rows) {
+    Plan p{};
+    p.m_tiles = (n_out + 255) / 256;
+    p.n_tiles = (n_rows + 255) / 256;
+    p.N = std::max(32, ((n_rows + p.n_tiles - 1) / p.n_tiles + 31) / 32 * 32);
+    p.KB = (k + kStageK - 1) / kStageK;
+    const int stage = kStageA + p.N * 128;
+    p.stages = std::min(12, (kSmemMost - 2048) / stage);
+    const int tiles = p.m_tiles * p.n_tiles;
+    p.rest = tiles % kPairs;
+    p.whole = tiles - p.rest;
+    p.pairs = (int)std::min<long long>(kPairs, p.whole ? kPairs : (long long)p.rest * p.KB);
+    p.pitch = (k + 7) / 8 * 8;
+    p.rows_bytes = ((size_t)n_rows * p.pitch * 2 + 255) / 256 * 256;
+    p.part_bytes = p.rest ? (size_t)p.pairs * 2 * p.N * 256 * 4 : 0;
+    return p;
+}
+
+}  // namespace
+
+size_t linear_tc_workspace(int n_out, int k, int n_rows) {
+    const Plan p = make_plan(n_out, k, n_rows);
+    return p.rows_bytes + p.part_bytes;
+}
+
+cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) {
+    const Plan p = make_plan(a.n_out, a.k, a.n_rows);
+    LinearTc g{};
+    g.a = a;
+    __half* rows = static_cast<__half*>(a.workspace);
+    g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + p.rows_bytes);
+    g.N = p.N;
+    g.m_tiles = p.m_tiles;
+    g.n_tiles = p.n_tiles;
+    g.KB = p.KB;
+    g.stages = p.stages;
+    g.whole = p.whole;
+    g.rest = p.rest;
+    g.pairs = p.pairs;
+    g.shared_cols = 2 * p.N > (int)kColA;
+    g.base1 = g.shared_cols ? kColA - p.N : p.N;
+    const int es = a.dtype == KVR_F32 ? 4 : 2;
+    g.vec = reinterpret_cast<uintptr_t>(a.out) % (4 * es) == 0 && a.out_stride % 4 == 0;
+    CUtensorMap ta, tb;
+    if (!make_tmap_2d_sw128(&ta, 1, a.w, a.k, a.n_out, a.w_stride, kStageK, 128, why) ||
+        !make_tmap_2d_sw128(&tb, 2, rows, a.k, a.n_rows, (uint64_t)p.pitch * 2, 64, p.N / 2, why))
+        return cudaErrorInvalidValue;
+    const int64_t units = (int64_t)a.n_rows * ((a.k + 15) / 16);
+    KVR_LAUNCH(widen_kernel, dim3((unsigned)std::min<int64_t>((units + 255) / 256, 16 * kNumSMs)), dim3(256), 0, s, a.x,
+               a.x_stride, rows, p.pitch, a.k, a.n_rows);
+    const size_t smem = 1024 + (size_t)p.stages * (kStageA + p.N * 128) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    if (e != cudaSuccess) return e;
+    e = launch_clusters(2, linear_tc_kernel, dim3(2 * p.pairs), dim3(kThreads), smem, s, ta, tb, g);
+    if (e != cudaSuccess || p.rest == 0) return e;
+    KVR_LAUNCH(linear_join_kernel, dim3((unsigned)p.rest * ((64 * p.N + 255) / 256)), dim3(256), 0, s, g);
+    return cudaSuccess;
+}
+
+}  // namespace kvr

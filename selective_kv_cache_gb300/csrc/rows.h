@@ -50,6 +50,10 @@ struct Linear {
 constexpr int kLinearMmaRows = 16;   // up to these rows the integer kernel takes the call
 cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s);
 
+// Many rows; needs linear_tc_workspace bytes of workspace.
+size_t linear_tc_workspace(int n_out, int k, int n_rows);
+cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why);
+
 cudaError_t launch_rope_table(const kvr_rope& rope, int rope_len, float2* table, cudaStream_t s);
 
 }  // namespace kvr

@@ -59,7 +59,9 @@ kvr_status check_weights(const kvr_linear_weights* w) {
         return fail(KVR_EINVAL, "weights: scales, bias and err must be aligned, scales and err not NULL");
     return KVR_OK;
 }
-size_t linear_workspace(const kvr_linear_weights&, int32_t) { return 256; }
+size_t linear_workspace(const kvr_linear_weights& w, int32_t n_rows) {
+    return n_rows <= kLinearMmaRows ? 256 : linear_tc_workspace(w.n_out, w.k, n_rows);
+}
 
 kvr_status check_rope(const kvr_rope* r) {
     if (!r) return fail(KVR_EINVAL, "rope is NULL");
@@ -274,7 +276,7 @@ kvr_status kvr_rows_rotate(const kvr_rope* rope, int32_t dtype, int32_t n_rows, 
 }
 
 size_t kvr_linear_workspace_bytes(const kvr_linear_weights* w, int32_t n_rows) {
-    if (check_weights(w) != KVR_OK || n_rows < 1) return 0;
+    if (check_weights(w) != KVR_OK || n_rows < 1 || n_rows > kMaxWidth * 4) return 0;
     return linear_workspace(*w, n_rows);
 }
 
@@ -311,7 +313,13 @@ kvr_status kvr_linear(const kvr_linear_weights* w, int32_t n_rows, const int8_t*
     a.dtype = dtype;
     a.err = w->err;
     a.workspace = workspace;
-    KVR_CHECK_LAUNCH(launch_linear_mma(a, reinterpret_cast<cudaStream_t>(stream)), "linear");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (n_rows <= kLinearMmaRows) {
+        KVR_CHECK_LAUNCH(launch_linear_mma(a, s), "linear");
+        return KVR_OK;
+    }
+    std::string why;
+    KVR_CHECK_LAUNCH(launch_linear_tc(a, s, &why), ("linear " + why).c_str());
     return KVR_OK;
 }
 
