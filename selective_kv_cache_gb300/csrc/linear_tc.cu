@@ -26,9 +26,9 @@
 // rows have landed the issuing thread knows from the peer's widening warps,
 // which wait for the same stage.
 //
-// Tensor memory: accumulators of two tiles at columns 0 and 384 - N (side by
-// side up to N = 192; above, they share columns, which the epilogue reads first), four
-// chunks of widened weights at 384.
+// Tensor memory: accumulators of two tiles (side by side up to N = 192; above,
+// they share columns, which the epilogue reads first), and four chunks of widened
+// weights behind them, eight up to N = 128.
 //
 // Tiles are taken in turn by the 76 pairs, whole.  The tiles that are left
 // after the last whole turn, or all of them where there are fewer than pairs,
@@ -50,7 +50,6 @@ constexpr int kPairs = kNumSMs / 2;
 constexpr int kThreads = 512;
 constexpr int kStageK = 128;                      // codes of a stage: two chunks
 constexpr uint32_t kStageA = 128 * 128;           // 128 features x 128 bytes
-constexpr uint32_t kColA = 384;                   // four chunks of 32 columns
 constexpr int kSmemMost = 227 * 1024;
 constexpr int kSuper = 8;                         // row tiles that are walked beside one another
 
@@ -61,7 +60,7 @@ struct LinearTc {
     int whole, rest, pairs; // tiles taken whole, tiles of the line, pairs in the grid
     uint32_t base1;         // columns of the second accumulator
     int shared_cols;        // whether the two share columns
-    int vec;                // out rows can be written four features at a time
+    uint32_t col_a, slots;  // widened chunks: their first column and their number, 4 or 8
 };
 
 // ---------------------------------------------------------------- paired instructions
@@ -136,7 +135,7 @@ struct Piece {
     int tile, kb0, kb1, slot;   // slot < 0: whole
 };
 __device__ __forceinline__ int share_begin(const LinearTc& g, int pair) {
-    return (int)((long long)g.rest * g.KB * pair / g.pairs);
+    return (int)((uint32_t)(g.rest * g.KB) * (uint32_t)pair / (uint32_t)g.pairs);   // below 76 * 512 * 76
 }
 struct Walk {
     int u, u1, next, slot;
@@ -205,37 +204,9 @@ __global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, int64_t str
 }
 
 // ---------------------------------------------------------------- output
-template <bool kVec>
-__device__ __forceinline__ void write4(const LinearTc& g, int row, int f, const float* v, const float* sw, const float* bias) {
-    const float s = g.a.x_scale[row];
-    float y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = v[e] * s * sw[e] + bias[e];
-    const int64_t o = (int64_t)row * g.a.out_stride + f;
-    if (kVec && f + 4 <= g.a.n_out) {
-        if (g.a.dtype == KVR_F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + o) = make_float4(y[0], y[1], y[2], y[3]);
-        } else {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(y[0], y[1]), q = __floats2bfloat162_rn(y[2], y[3]);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.a.out) + o) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (f + e >= g.a.n_out) break;
-        if (g.a.dtype == KVR_F32) static_cast<float*>(g.a.out)[o + e] = y[e];
-        else static_cast<__nv_bfloat16*>(g.a.out)[o + e] = __float2bfloat16_rn(y[e]);
-    }
-}
-__device__ __forceinline__ void channel4(const LinearTc& g, int f, float* sw, float* bias) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const bool in = f + e < g.a.n_out;
-        sw[e] = in ? g.a.w_scale[f + e] : 0.f;
-        bias[e] = in && g.a.bias ? g.a.bias[f + e] : 0.f;
-    }
+__device__ __forceinline__ void write_out(const Linear& a, int64_t at, float y) {
+    if (a.dtype == KVR_F32) static_cast<float*>(a.out)[at] = y;
+    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
 }
 
 __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -248,9 +219,9 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     const uint32_t half_rows = g.N / 2, atomB = half_rows * 128, stage_bytes = kStageA + 2 * atomB;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)stages * stage_bytes);
     uint64_t* empty = full + stages;
-    uint64_t* a_ready = empty + stages;   // [4], the leader's
-    uint64_t* a_free = a_ready + 4;       // [4]
-    uint64_t* acc_full = a_free + 4;      // [2]
+    uint64_t* a_ready = empty + stages;   // [slots], the leader's
+    uint64_t* a_free = a_ready + 8;       // [slots]
+    uint64_t* acc_full = a_free + 8;      // [2]
     uint64_t* acc_empty = acc_full + 2;   // [2], the leader's
     uint64_t* cols_free = acc_empty + 2;  // the leader's: the columns that both accumulators use are read
     uint64_t* all_done = cols_free + 1;
@@ -264,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 8; ++t) {
             mbar_init(&a_ready[t], 8);
             mbar_init(&a_free[t], 1);
         }
@@ -284,6 +255,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     cluster_sync();   // the other CTA's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const uint32_t slots = g.slots, lap = slots == 8 ? 3 : 2;   // chunk q: slot q % slots, its use number q >> lap
     bool ok = true;
     pdl_trigger();
 
@@ -354,8 +326,8 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                     const uint64_t db = descB + (uint64_t)(((uint32_t)s * stage_bytes) >> 4);
 #pragma unroll
                     for (uint32_t h = 0; h < 2; ++h, ++q) {
-                        const uint32_t t = q & 3u;
-                        if (!warp_wait(&a_ready[t], (q >> 2) & 1u)) {
+                        const uint32_t t = q & (slots - 1);
+                        if (!warp_wait(&a_ready[t], (q >> lap) & 1u)) {
                             ok = false;
                             break;
                         }
@@ -363,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                         if (issuer) {
 #pragma unroll
                             for (uint32_t kk = 0; kk < 4; ++kk)
-                                pair_mma(d, tmem + kColA + 32 * t + 8 * kk, db + (uint64_t)((h * atomB >> 4) + 2 * kk), idesc,
+                                pair_mma(d, tmem + g.col_a + 32 * t + 8 * kk, db + (uint64_t)((h * atomB >> 4) + 2 * kk), idesc,
                                          (h > 0 || kk > 0) ? 1u : (kb > p.kb0 ? 1u : 0u));
                             pair_commit(&a_free[t]);
                             if (h == 1) pair_commit(&empty[s]);
@@ -384,82 +356,89 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------ widening
         const int set = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
-        const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16) + kColA;
-        int s = 0;
+        const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16) + g.col_a;
+        int s = 0, pending = -1;
         uint32_t phase = 0, q = set;
+        // A chunk is handed over when the next one's codes are in registers, so that its stores complete meanwhile,
+        // or at once where those have not come yet.
+        auto hand_over = [&]() {
+            if (pending < 0) return;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_leader(&a_ready[pending]);
+            pending = -1;
+        };
         Piece p;
         for (Walk w(g, pair); ok && w.take(g, &p);) {
             for (int kb = p.kb0; kb < p.kb1; ++kb, q += 2) {
-                const uint32_t t = q & 3u;
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase)) || !warp_wait(&a_free[t], ((q >> 2) & 1u) ^ 1u)) {
-                    ok = false;
-                    break;
+                const uint32_t t = q & (slots - 1);
+                if (!__all_sync(0xffffffffu, mbar_test(&full[s], phase))) {
+                    hand_over();
+                    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
+                        ok = false;
+                        break;
+                    }
                 }
-                tc_fence_after();
                 const uint8_t* a = smem + (size_t)s * stage_bytes + row * 128;
                 uint32_t h[32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     widen16(*reinterpret_cast<const uint4*>(a + (((4 * set + c) ^ (row & 7)) << 4)), h + 8 * c);
+                hand_over();
+                if (!warp_wait(&a_free[t], ((q >> lap) & 1u) ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
                 tmem_st16_async(dst + 32 * t, h);
                 tmem_st16_async(dst + 32 * t + 16, h + 16);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_leader(&a_ready[t]);
+                pending = (int)t;
                 if (++s == stages) {
                     s = 0;
                     phase ^= 1u;
                 }
             }
         }
+        hand_over();
     } else if (warp >= 12) {
         // ------------------------------------------------------------ accumulators out
-        const int quarter = warp & 3, b = lane & 3;
+        const int quarter = warp & 3, fo = (int)rank * 128 + quarter * 32 + lane;   // this lane's feature in the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const int fo = (int)rank * 128 + quarter * 32 + (lane & ~3);   // this lane's four features in the tile
         int local = 0;
         Piece p;
         for (Walk w(g, pair); w.take(g, &p); ++local) {
             const int ab = local & 1;
+            int m, n;
+            tile_coords(g, p.tile, &m, &n);
+            const int row0 = n * g.N, f = m * 256 + fo, rows = min(g.N, g.a.n_rows - row0);
+            const bool in = f < g.a.n_out;
+            const float sw = in ? g.a.w_scale[f] : 0.f, bias = in && g.a.bias ? g.a.bias[f] : 0.f;
             if (!warp_wait(&acc_full[ab], (uint32_t)(local >> 1) & 1u)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            int m, n;
-            tile_coords(g, p.tile, &m, &n);
-            const int row0 = n * g.N, f = m * 256 + fo;
             const uint32_t src = tmem + lane_base + (ab ? g.base1 : 0u);
-            float sw[4], bias[4];
-            channel4(g, f, sw, bias);
-            // Lane l holds feature l for 16 rows; a 4 x 4 transpose within each quad of lanes leaves it features
-            // 4 (l / 4) .. + 3 of rows 4 i + l % 4.
+            // A lane holds a feature, a column is a row of the output: each store is 32 features of one row, 64 or
+            // 128 bytes in a piece, whatever the alignment.
             auto drain = [&](int lo, int hi) {
-                for (int c = lo; c < hi; c += 16) {
-                    float v[16];
-                    tmem_ld16(src + (uint32_t)c, v);
+                for (int c = lo; c < hi; c += 32) {
+                    const float sx = c + lane < rows ? g.a.x_scale[row0 + c + lane] : 0.f;
+                    float v[32];
+                    tmem_ld32(src + (uint32_t)c, v);
+                    const int left = rows - c;
+                    if (p.slot >= 0) {
+                        float* o = g.part + ((size_t)p.slot * g.N + c) * 256 + fo;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x0 = v[4 * i], x1 = v[4 * i + 1], x2 = v[4 * i + 2], x3 = v[4 * i + 3];
-                        float a0 = (b & 2) ? x0 : x2, a1 = (b & 2) ? x1 : x3;
-                        a0 = __shfl_xor_sync(0xffffffffu, a0, 2);
-                        a1 = __shfl_xor_sync(0xffffffffu, a1, 2);
-                        if (b & 2) { x0 = a0; x1 = a1; } else { x2 = a0; x3 = a1; }
-                        float c0 = (b & 1) ? x0 : x1, c1 = (b & 1) ? x2 : x3;
-                        c0 = __shfl_xor_sync(0xffffffffu, c0, 1);
-                        c1 = __shfl_xor_sync(0xffffffffu, c1, 1);
-                        if (b & 1) { x0 = c0; x2 = c1; } else { x1 = c0; x3 = c1; }
-                        const int col = c + 4 * i + b, row = row0 + col;
-                        if (row < g.a.n_rows && f < g.a.n_out) {
-                            const float y[4] = {x0, x1, x2, x3};
-                            if (p.slot >= 0)
-                                *reinterpret_cast<float4*>(g.part + ((size_t)p.slot * g.N + col) * 256 + fo) =
-                                    make_float4(x0, x1, x2, x3);
-                            else if (g.vec)
-                                write4<true>(g, row, f, y, sw, bias);
-                            else
-                                write4<false>(g, row, f, y, sw, bias);
+                        for (int i = 0; i < 32; ++i)
+                            if (i < left) o[i * 256] = v[i];
+                    } else {
+                        const int64_t at = (int64_t)(row0 + c) * g.a.out_stride + f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float y = v[i] * __shfl_sync(0xffffffffu, sx, i) * sw + bias;
+                            if (i < left && in) write_out(g.a, at + i * g.a.out_stride, y);
                         }
                     }
                 }
@@ -493,22 +472,19 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
 // The line's tiles: pieces added as integers, in any order the same.
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearTc g) {
     pdl_wait();
-    const int per = 64 * g.N;   // four features a thread
-    const int tile = (int)(blockIdx.x / ((per + 255) / 256)), i = (int)(blockIdx.x % ((per + 255) / 256)) * 256 + threadIdx.x;
+    // a block: four rows of a tile, four features a thread
+    const int blocks = g.N / 4, tile = blockIdx.x / blocks, col = (blockIdx.x - tile * blocks) * 4 + threadIdx.x / 64;
     int m, n;
     tile_coords(g, g.whole + tile, &m, &n);
-    const int col = i / 64, fo = 4 * (i % 64), row = n * g.N + col, f = m * 256 + fo;
-    if (i >= per || row >= g.a.n_rows || f >= g.a.n_out) return;
-    // the pairs whose shares meet [u0, u0 + KB)
-    const long long T = (long long)g.rest * g.KB, u0 = (long long)tile * g.KB, u1 = u0 + g.KB;
-    int pair = (int)(u0 * g.pairs / T);
-    while (pair > 0 && share_begin(g, pair) > u0) --pair;
+    const int fo = 4 * (threadIdx.x % 64), row = n * g.N + col, f = m * 256 + fo;
+    if (row >= g.a.n_rows || f >= g.a.n_out) return;
+    // the pairs whose shares meet [u0, u1)
+    const int u0 = tile * g.KB, u1 = u0 + g.KB;
+    int pair = (int)((uint32_t)u0 * (uint32_t)g.pairs / (uint32_t)(g.rest * g.KB));
     while (share_begin(g, pair + 1) <= u0) ++pair;
     int sum[4] = {0, 0, 0, 0};
-    for (; pair < g.pairs; ++pair) {
-        const int b = share_begin(g, pair), e = share_begin(g, pair + 1);
-        if (b >= u1) break;
-        if (b == e) continue;
+    for (int b = share_begin(g, pair), e; b < u1; ++pair, b = e) {
+        e = share_begin(g, pair + 1);
         if (b <= u0 && e >= u1) return;   // one pair had all of it and wrote it
         const int slot = 2 * pair + (tile - b / g.KB);
         const float4 v = *reinterpret_cast<const float4*>(g.part + ((size_t)slot * g.N + col) * 256 + fo);
@@ -517,11 +493,12 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         sum[2] += __float2int_rn(v.z);
         sum[3] += __float2int_rn(v.w);
     }
-    float sw[4], bias[4];
-    channel4(g, f, sw, bias);
-    const float y[4] = {(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]};
-    if (g.vec) write4<true>(g, row, f, y, sw, bias);
-    else write4<false>(g, row, f, y, sw, bias);
+    const float sx = g.a.x_scale[row];
+    const int64_t at = (int64_t)row * g.a.out_stride + f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (f + i < g.a.n_out)
+            write_out(g.a, at + i, (float)sum[i] * sx * g.a.w_scale[f + i] + (g.a.bias ? g.a.bias[f + i] : 0.f));
 }
 
 struct Plan {
@@ -567,10 +544,10 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     g.whole = p.whole;
     g.rest = p.rest;
     g.pairs = p.pairs;
-    g.shared_cols = 2 * p.N > (int)kColA;
-    g.base1 = g.shared_cols ? kColA - p.N : p.N;
-    const int es = a.dtype == KVR_F32 ? 4 : 2;
-    g.vec = reinterpret_cast<uintptr_t>(a.out) % (4 * es) == 0 && a.out_stride % 4 == 0;
+    g.slots = p.N <= 128 ? 8 : 4;
+    g.col_a = 512 - 32 * g.slots;
+    g.shared_cols = 2 * p.N > (int)g.col_a;
+    g.base1 = g.shared_cols ? g.col_a - p.N : p.N;
     CUtensorMap ta, tb;
     if (!make_tmap_2d_sw128(&ta, 1, a.w, a.k, a.n_out, a.w_stride, kStageK, 128, why) ||
         !make_tmap_2d_sw128(&tb, 2, rows, a.k, a.n_rows, (uint64_t)p.pitch * 2, 64, p.N / 2, why))
@@ -583,7 +560,7 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     if (e != cudaSuccess) return e;
     e = launch_clusters(2, linear_tc_kernel, dim3(2 * p.pairs), dim3(kThreads), smem, s, ta, tb, g);
     if (e != cudaSuccess || p.rest == 0) return e;
-    KVR_LAUNCH(linear_join_kernel, dim3((unsigned)p.rest * ((64 * p.N + 255) / 256)), dim3(256), 0, s, g);
+    KVR_LAUNCH(linear_join_kernel, dim3((unsigned)p.rest * (p.N / 4)), dim3(256), 0, s, g);
     return cudaSuccess;
 }
 
