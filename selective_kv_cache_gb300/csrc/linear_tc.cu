@@ -17,10 +17,11 @@
 //   warp 0       TMA: per stage 128 features x 128 codes and N/2 rows x 128
 //                fp16 (two swizzle atoms)
 //   warp 1       products, in the leader CTA: four of K = 16 a 64-code chunk
-//   warps 4-11   widening: set 0 (4-7) takes the first 64 codes of every stage,
-//                set 1 the second; a thread a feature.  b ^ 0x80 under the exponent of
-//                1024 is 1152 + b, less 1152 is b: exact.
-//   warps 12-15  accumulators out, a TMEM lane quarter each
+//   warps 4-7    accumulators out, a TMEM lane quarter each
+//   warps 8-23   widening: four sets of four warps take the 64-code chunks in turn,
+//                a thread a feature.  b ^ 0x80 under the exponent of 1024 is 1152 + b, less 1152
+//                is b: exact.  A chunk takes a set about 800 cycles, most of them
+//                latency, so four of them keep up with the copies.
 // Barriers: full (copies landed, own CTA) -> widening warps of both CTAs ->
 // a_ready (leader) -> products -> a_free, empty (both CTAs).  That the peer's
 // rows have landed the issuing thread knows from the peer's widening warps,
@@ -47,14 +48,17 @@ namespace kvr {
 namespace {
 
 constexpr int kPairs = kNumSMs / 2;
-constexpr int kThreads = 512;
+constexpr int kSets = 4, kThreads = 32 * (8 + 4 * kSets);   // sets of widening warps
 constexpr int kStageK = 128;                      // codes of a stage: two chunks
 constexpr uint32_t kStageA = 128 * 128;           // 128 features x 128 bytes
 constexpr int kSmemMost = 227 * 1024;
 constexpr int kSuper = 8;                         // row tiles that are walked beside one another
 
+enum : int { kOutF32, kOutBf16, kOutPairs };
+
 struct LinearTc {
     Linear a;
+    int out_as;
     float* part;            // [pairs][2][N][256]
     int N, m_tiles, n_tiles, KB, stages;
     int whole, rest, pairs; // tiles taken whole, tiles of the line, pairs in the grid
@@ -204,6 +208,54 @@ __global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, int64_t str
 }
 
 // ---------------------------------------------------------------- output
+// Of 32 columns in registers a lane holds its feature, a column is a row of the
+// output.  Rows and features past the ends are not written.
+__device__ __forceinline__ void write_part(float* o, const float* v, int left) {
+    if (left >= 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i * 256] = v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) o[i * 256] = v[i];
+    }
+}
+// any alignment: a store is 32 features of one row
+template <typename T>
+__device__ __forceinline__ void write_lanes(const Linear& a, int row, int f, const float* v, float sx, float sw, float bias,
+                                            int left) {
+    T* o = static_cast<T*>(a.out) + (int64_t)row * a.out_stride + f;
+    const bool in = f < a.n_out;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float y = v[i] * __shfl_sync(0xffffffffu, sx, i) * sw + bias;
+        if (in && i < left) {
+            if constexpr (sizeof(T) == 4) *o = y;
+            else *o = __float2bfloat16_rn(y);
+        }
+        o += a.out_stride;
+    }
+}
+// bf16, even sizes: neighbouring lanes exchange, the even one takes both
+// features of the first of two rows, the odd one of the second; a store is 64
+// bytes of each.
+__device__ __forceinline__ void write_pairs(const Linear& a, int row, int f, const float* v, float sx, float sw, float bias,
+                                            int left) {
+    const int odd = f & 1;
+    const float sw2 = __shfl_xor_sync(0xffffffffu, sw, 1), bias2 = __shfl_xor_sync(0xffffffffu, bias, 1);
+    const float s0 = odd ? sw2 : sw, s1 = odd ? sw : sw2, b0 = odd ? bias2 : bias, b1 = odd ? bias : bias2;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (int64_t)(row + odd) * a.out_stride + (f - odd);
+    const int64_t step = 2 * a.out_stride;
+    left = f < a.n_out ? left - odd : 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+        const float s = __shfl_sync(0xffffffffu, sx, i + odd);
+        const __nv_bfloat162 y = __floats2bfloat162_rn((odd ? got : v[i]) * s * s0 + b0, (odd ? v[i + 1] : got) * s * s1 + b1);
+        if (i < left) *reinterpret_cast<__nv_bfloat162*>(o) = y;
+        o += step;
+    }
+}
 __device__ __forceinline__ void write_out(const Linear& a, int64_t at, float y) {
     if (a.dtype == KVR_F32) static_cast<float*>(a.out)[at] = y;
     else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
@@ -353,11 +405,11 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             __syncwarp();
         }
         if (!warp_wait(all_done, 0)) ok = false;
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp >= 8) {
         // ------------------------------------------------------------ widening
-        const int set = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+        const int set = (warp - 8) >> 2, half = set & 1, quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16) + g.col_a;
-        int s = 0, pending = -1;
+        int s = 0, turn = set >> 1, pending = -1;   // this set's stages: every kSets / 2-th
         uint32_t phase = 0, q = set;
         // A chunk is handed over when the next one's codes are in registers, so that its stores complete meanwhile,
         // or at once where those have not come yet.
@@ -371,20 +423,28 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         };
         Piece p;
         for (Walk w(g, pair); ok && w.take(g, &p);) {
-            for (int kb = p.kb0; kb < p.kb1; ++kb, q += 2) {
+            for (int kb = p.kb0; kb < p.kb1; ++kb) {
+                const int stage = s;
+                const uint32_t parity = phase;
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+                if (turn-- != 0) continue;
+                turn = kSets / 2 - 1;
                 const uint32_t t = q & (slots - 1);
-                if (!__all_sync(0xffffffffu, mbar_test(&full[s], phase))) {
+                if (!__all_sync(0xffffffffu, mbar_test(&full[stage], parity))) {
                     hand_over();
-                    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], parity))) {
                         ok = false;
                         break;
                     }
                 }
-                const uint8_t* a = smem + (size_t)s * stage_bytes + row * 128;
+                const uint8_t* a = smem + (size_t)stage * stage_bytes + row * 128;
                 uint32_t h[32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    widen16(*reinterpret_cast<const uint4*>(a + (((4 * set + c) ^ (row & 7)) << 4)), h + 8 * c);
+                    widen16(*reinterpret_cast<const uint4*>(a + (((4 * half + c) ^ (row & 7)) << 4)), h + 8 * c);
                 hand_over();
                 if (!warp_wait(&a_free[t], ((q >> lap) & 1u) ^ 1u)) {
                     ok = false;
@@ -394,14 +454,11 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                 tmem_st16_async(dst + 32 * t, h);
                 tmem_st16_async(dst + 32 * t + 16, h + 16);
                 pending = (int)t;
-                if (++s == stages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
+                q += kSets;
             }
         }
         hand_over();
-    } else if (warp >= 12) {
+    } else if (warp >= 4) {
         // ------------------------------------------------------------ accumulators out
         const int quarter = warp & 3, fo = (int)rank * 128 + quarter * 32 + lane;   // this lane's feature in the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -412,35 +469,23 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             int m, n;
             tile_coords(g, p.tile, &m, &n);
             const int row0 = n * g.N, f = m * 256 + fo, rows = min(g.N, g.a.n_rows - row0);
-            const bool in = f < g.a.n_out;
-            const float sw = in ? g.a.w_scale[f] : 0.f, bias = in && g.a.bias ? g.a.bias[f] : 0.f;
+            const float sw = f < g.a.n_out ? g.a.w_scale[f] : 0.f, bias = f < g.a.n_out && g.a.bias ? g.a.bias[f] : 0.f;
             if (!warp_wait(&acc_full[ab], (uint32_t)(local >> 1) & 1u)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const uint32_t src = tmem + lane_base + (ab ? g.base1 : 0u);
-            // A lane holds a feature, a column is a row of the output: each store is 32 features of one row, 64 or
-            // 128 bytes in a piece, whatever the alignment.
             auto drain = [&](int lo, int hi) {
                 for (int c = lo; c < hi; c += 32) {
                     const float sx = c + lane < rows ? g.a.x_scale[row0 + c + lane] : 0.f;
                     float v[32];
                     tmem_ld32(src + (uint32_t)c, v);
                     const int left = rows - c;
-                    if (p.slot >= 0) {
-                        float* o = g.part + ((size_t)p.slot * g.N + c) * 256 + fo;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < left) o[i * 256] = v[i];
-                    } else {
-                        const int64_t at = (int64_t)(row0 + c) * g.a.out_stride + f;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float y = v[i] * __shfl_sync(0xffffffffu, sx, i) * sw + bias;
-                            if (i < left && in) write_out(g.a, at + i * g.a.out_stride, y);
-                        }
-                    }
+                    if (p.slot >= 0) write_part(g.part + ((size_t)p.slot * g.N + c) * 256 + fo, v, left);
+                    else if (g.out_as == kOutPairs) write_pairs(g.a, row0 + c, f, v, sx, sw, bias, left);
+                    else if (g.out_as == kOutF32) write_lanes<float>(g.a, row0 + c, f, v, sx, sw, bias, left);
+                    else write_lanes<__nv_bfloat16>(g.a, row0 + c, f, v, sx, sw, bias, left);
                 }
             };
             if (g.shared_cols) {   // the columns that the next tile's accumulator shares first
@@ -544,6 +589,8 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     g.whole = p.whole;
     g.rest = p.rest;
     g.pairs = p.pairs;
+    const bool even = a.n_out % 2 == 0 && a.out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
+    g.out_as = a.dtype == KVR_F32 ? kOutF32 : even ? kOutPairs : kOutBf16;
     g.slots = p.N <= 128 ? 8 : 4;
     g.col_a = 512 - 32 * g.slots;
     g.shared_cols = 2 * p.N > (int)g.col_a;
