@@ -17,8 +17,8 @@
 //   warp 0       TMA: per stage 128 features x 128 codes and N/2 rows x 128
 //                fp16 (two swizzle atoms)
 //   warp 1       products, in the leader CTA: four of K = 16 a 64-code chunk
-//   warps 4-7    accumulators out, a TMEM lane quarter each
-//   warps 8-23   widening: four sets of four warps take the 64-code chunks in turn,
+//   warps 4-11   accumulators out, two warps a TMEM lane quarter
+//   warps 12-27  widening: four sets of four warps take the 64-code chunks in turn,
 //                a thread a feature.  b ^ 0x80 under the exponent of 1024 is 1152 + b, less 1152
 //                is b: exact.  A chunk takes a set about 800 cycles, most of them
 //                latency, so four of them keep up with the copies.
@@ -48,7 +48,8 @@ namespace kvr {
 namespace {
 
 constexpr int kPairs = kNumSMs / 2;
-constexpr int kSets = 4, kThreads = 32 * (8 + 4 * kSets);   // sets of widening warps
+constexpr int kSets = 4, kOuts = 2;                // sets of widening warps; warps a lane quarter that write out
+constexpr int kThreads = 32 * (4 + 4 * kOuts + 4 * kSets);
 constexpr int kStageK = 128;                      // codes of a stage: two chunks
 constexpr uint32_t kStageA = 128 * 128;           // 128 features x 128 bytes
 constexpr int kSmemMost = 227 * 1024;
@@ -293,9 +294,9 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], 8 * kOuts);
         }
-        mbar_init(cols_free, 8);
+        mbar_init(cols_free, 8 * kOuts);
         mbar_init(all_done, 1);
         fence_mbar_init();
         prefetch_tmap(&tmA);
@@ -405,9 +406,9 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             __syncwarp();
         }
         if (!warp_wait(all_done, 0)) ok = false;
-    } else if (warp >= 8) {
+    } else if (warp >= 4 + 4 * kOuts) {
         // ------------------------------------------------------------ widening
-        const int set = (warp - 8) >> 2, half = set & 1, quarter = warp & 3, row = 32 * quarter + lane;
+        const int set = (warp - 4 - 4 * kOuts) >> 2, half = set & 1, quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16) + g.col_a;
         int s = 0, turn = set >> 1, pending = -1;   // this set's stages: every kSets / 2-th
         uint32_t phase = 0, q = set;
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         hand_over();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ accumulators out
-        const int quarter = warp & 3, fo = (int)rank * 128 + quarter * 32 + lane;   // this lane's feature in the tile
+        const int part = (warp - 4) >> 2, quarter = warp & 3, fo = (int)rank * 128 + quarter * 32 + lane;   // this lane's feature in the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         int local = 0;
         Piece p;
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             tc_fence_after();
             const uint32_t src = tmem + lane_base + (ab ? g.base1 : 0u);
             auto drain = [&](int lo, int hi) {
-                for (int c = lo; c < hi; c += 32) {
+                for (int c = lo + 32 * part; c < hi; c += 32 * kOuts) {
                     const float sx = c + lane < rows ? g.a.x_scale[row0 + c + lane] : 0.f;
                     float v[32];
                     tmem_ld32(src + (uint32_t)c, v);
