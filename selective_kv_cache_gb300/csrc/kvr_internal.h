@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <string>
@@ -318,6 +319,19 @@ cudaError_t launch_clusters(unsigned cluster, void (*kernel)(KArgs...), dim3 gri
     cfg.numAttrs = pdl_take() ? 2 : 1;
     if (fault_at("launch")) return cudaErrorLaunchFailure;   // injected: nothing is issued
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Dynamic shared memory above 48 KB for a kernel: set once per device.
+template <typename... A>
+cudaError_t allow_smem(void (*kernel)(A...), int bytes, std::atomic<uint64_t>* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 #define KVR_LAUNCH(...)                                     \

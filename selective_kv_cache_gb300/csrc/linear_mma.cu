@@ -11,11 +11,9 @@
 // neighbouring bytes at a time, and the partial sums meet in shared memory, the
 // cluster's over distributed shared memory: one launch, no workspace, any order
 // of addition the same integer.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 
-#include "rows.h"
+#include "linear.cuh"
 
 namespace kvr {
 namespace {
@@ -42,19 +40,6 @@ __device__ __forceinline__ uint4 load_tail(const int8_t* p, int left) {
         if (i < left) w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ int load_peer(const int* p, uint32_t rank) {
-    int v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.s32 %0, [a];\n\t}"
-        : "=r"(v)
-        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank)
-        : "memory");
-    return v;
-}
-
 // kNT: groups of eight rows a block takes; kUnroll: steps in flight a warp.
 template <int kNT, int kUnroll>
 __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ Linear a, int split) {
@@ -129,13 +114,9 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
     for (int i = rank * kThreads + threadIdx.x; i < kTile; i += split * kThreads) {
         const int r = r0 + i / kFeatures, f = f0 + i % kFeatures;
         int v = part[0][i];
-        for (int p = 1; p < split; ++p) v += load_peer(&part[0][i], (rank + p) % split);
+        for (int p = 1; p < split; ++p) v += load_peer(peer_address(&part[0][i], (rank + p) % split));
         if (r >= a.n_rows || f >= a.n_out) continue;
-        float y = (float)v * a.x_scale[r] * a.w_scale[f];
-        if (a.bias) y += a.bias[f];
-        const int64_t o = (int64_t)r * a.out_stride + f;
-        if (a.dtype == KVR_F32) static_cast<float*>(a.out)[o] = y;
-        else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
+        write_out(a, (int64_t)r * a.out_stride + f, (float)v * a.x_scale[r] * a.w_scale[f] + (a.bias ? a.bias[f] : 0.f));
     }
     if (split > 1) cluster_sync();   // no block leaves while another reads its sums
 }

@@ -19,8 +19,7 @@
 //   warp 1       products, in the leader CTA: four of K = 16 a 64-code chunk
 //   warps 4-11   accumulators out, two warps a TMEM lane quarter
 //   warps 12-27  widening: four sets of four warps take the 64-code chunks in turn,
-//                a thread a feature.  b ^ 0x80 under the exponent of 1024 is 1152 + b, less 1152
-//                is b: exact.  A chunk takes a set about 800 cycles, most of them
+//                a thread a feature.  A chunk takes a set about 800 cycles, most of them
 //                latency, so four of them keep up with the copies.
 // Barriers: full (copies landed, own CTA) -> widening warps of both CTAs ->
 // a_ready (leader) -> products -> a_free, empty (both CTAs).  That the peer's
@@ -36,13 +35,10 @@
 // are one line of (tile, 128 codes) units of which every pair takes an equal
 // share; its pieces of tiles go to the workspace as fp32 and a last kernel adds
 // them as integers.  Every wait is bounded.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
+#include "linear.cuh"
 #include "ptx.cuh"
-#include "rows.h"
 
 namespace kvr {
 namespace {
@@ -54,8 +50,6 @@ constexpr int kStageK = 128;                      // codes of a stage: two chunk
 constexpr uint32_t kStageA = 128 * 128;           // 128 features x 128 bytes
 constexpr int kSmemMost = 227 * 1024;
 constexpr int kSuper = 8;                         // row tiles that are walked beside one another
-
-enum : int { kOutF32, kOutBf16, kOutPairs };
 
 struct LinearTc {
     Linear a;
@@ -69,14 +63,6 @@ struct LinearTc {
 };
 
 // ---------------------------------------------------------------- paired instructions
-__device__ __forceinline__ uint32_t cta_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 // One arrival on the leader CTA's barrier at this offset.  What it tells of are
 // tensor memory's contents, ordered by the tcgen05 fences, and copies that have
 // landed; nothing in ordinary memory is handed over, so neither side names the
@@ -173,21 +159,6 @@ __device__ __forceinline__ void tile_coords(const LinearTc& g, int tile, int* m,
 }
 
 // ---------------------------------------------------------------- widening
-// 16 codes to fp16, in order
-__device__ __forceinline__ void widen16(uint4 u, uint32_t* h) {
-    const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
-    const __half2 off = __half2half2(__ushort_as_half((unsigned short)0xe480));   // -1152
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t x = __byte_perm(w[i], 0x64646464u, e ? 0x4342 : 0x4140);
-            const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&x), off);
-            h[2 * i + e] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-    }
-}
-
 // rows of codes to rows of fp16, `pitch` elements apart
 __global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, int64_t stride, __half* out, int pitch, int k, int n_rows) {
     pdl_trigger();
@@ -209,8 +180,7 @@ __global__ void __launch_bounds__(256) widen_kernel(const int8_t* x, int64_t str
 }
 
 // ---------------------------------------------------------------- output
-// Of 32 columns in registers a lane holds its feature, a column is a row of the
-// output.  Rows and features past the ends are not written.
+// A lane holds its feature, a column is a row of the output.
 __device__ __forceinline__ void write_part(float* o, const float* v, int left) {
     if (left >= 32) {
 #pragma unroll
@@ -221,47 +191,6 @@ __device__ __forceinline__ void write_part(float* o, const float* v, int left) {
             if (i < left) o[i * 256] = v[i];
     }
 }
-// any alignment: a store is 32 features of one row
-template <typename T>
-__device__ __forceinline__ void write_lanes(const Linear& a, int row, int f, const float* v, float sx, float sw, float bias,
-                                            int left) {
-    T* o = static_cast<T*>(a.out) + (int64_t)row * a.out_stride + f;
-    const bool in = f < a.n_out;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float y = v[i] * __shfl_sync(0xffffffffu, sx, i) * sw + bias;
-        if (in && i < left) {
-            if constexpr (sizeof(T) == 4) *o = y;
-            else *o = __float2bfloat16_rn(y);
-        }
-        o += a.out_stride;
-    }
-}
-// bf16, even sizes: neighbouring lanes exchange, the even one takes both
-// features of the first of two rows, the odd one of the second; a store is 64
-// bytes of each.
-__device__ __forceinline__ void write_pairs(const Linear& a, int row, int f, const float* v, float sx, float sw, float bias,
-                                            int left) {
-    const int odd = f & 1;
-    const float sw2 = __shfl_xor_sync(0xffffffffu, sw, 1), bias2 = __shfl_xor_sync(0xffffffffu, bias, 1);
-    const float s0 = odd ? sw2 : sw, s1 = odd ? sw : sw2, b0 = odd ? bias2 : bias, b1 = odd ? bias : bias2;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (int64_t)(row + odd) * a.out_stride + (f - odd);
-    const int64_t step = 2 * a.out_stride;
-    left = f < a.n_out ? left - odd : 0;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-        const float s = __shfl_sync(0xffffffffu, sx, i + odd);
-        const __nv_bfloat162 y = __floats2bfloat162_rn((odd ? got : v[i]) * s * s0 + b0, (odd ? v[i + 1] : got) * s * s1 + b1);
-        if (i < left) *reinterpret_cast<__nv_bfloat162*>(o) = y;
-        o += step;
-    }
-}
-__device__ __forceinline__ void write_out(const Linear& a, int64_t at, float y) {
-    if (a.dtype == KVR_F32) static_cast<float*>(a.out)[at] = y;
-    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-}
-
 __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                                                             const __grid_constant__ CUtensorMap tmB,
                                                             const __grid_constant__ LinearTc g) {
@@ -484,9 +413,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                     tmem_ld32(src + (uint32_t)c, v);
                     const int left = rows - c;
                     if (p.slot >= 0) write_part(g.part + ((size_t)p.slot * g.N + c) * 256 + fo, v, left);
-                    else if (g.out_as == kOutPairs) write_pairs(g.a, row0 + c, f, v, sx, sw, bias, left);
-                    else if (g.out_as == kOutF32) write_lanes<float>(g.a, row0 + c, f, v, sx, sw, bias, left);
-                    else write_lanes<__nv_bfloat16>(g.a, row0 + c, f, v, sx, sw, bias, left);
+                    else write32(g.a, g.out_as, row0 + c, f, v, sx, sw, bias, left);
                 }
             };
             if (g.shared_cols) {   // the columns that the next tile's accumulator shares first
@@ -539,12 +466,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         sum[2] += __float2int_rn(v.z);
         sum[3] += __float2int_rn(v.w);
     }
-    const float sx = g.a.x_scale[row];
-    const int64_t at = (int64_t)row * g.a.out_stride + f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (f + i < g.a.n_out)
-            write_out(g.a, at + i, (float)sum[i] * sx * g.a.w_scale[f + i] + (g.a.bias ? g.a.bias[f + i] : 0.f));
+    write4(g.a, row, f, sum);
 }
 
 struct Plan {
@@ -590,8 +512,7 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     g.whole = p.whole;
     g.rest = p.rest;
     g.pairs = p.pairs;
-    const bool even = a.n_out % 2 == 0 && a.out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
-    g.out_as = a.dtype == KVR_F32 ? kOutF32 : even ? kOutPairs : kOutBf16;
+    g.out_as = out_kind(a);
     g.slots = p.N <= 128 ? 8 : 4;
     g.col_a = 512 - 32 * g.slots;
     g.shared_cols = 2 * p.N > (int)g.col_a;
@@ -604,7 +525,8 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     KVR_LAUNCH(widen_kernel, dim3((unsigned)std::min<int64_t>((units + 255) / 256, 16 * kNumSMs)), dim3(256), 0, s, a.x,
                a.x_stride, rows, p.pitch, a.k, a.n_rows);
     const size_t smem = 1024 + (size_t)p.stages * (kStageA + p.N * 128) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(linear_tc_kernel, kSmemMost, &done);
     if (e != cudaSuccess) return e;
     e = launch_clusters(2, linear_tc_kernel, dim3(2 * p.pairs), dim3(kThreads), smem, s, ta, tb, g);
     if (e != cudaSuccess || p.rest == 0) return e;

@@ -1,8 +1,6 @@
 // paged.h -- the paged cache's device view, and how its attention shares work
 // over the GPU (paged_api.cu, paged_rows.cu, paged_plan.cu, paged_simt.cu).
 #pragma once
-#include <atomic>
-
 #include "kvr_internal.h"
 
 namespace kvr {
@@ -135,19 +133,6 @@ __device__ __forceinline__ float2 tanh_either(float2 u) {
     const float2 y = tanh_series(u);
     return make_float2(fabsf(u.x) <= kTanhSeries ? y.x : tanh_quotient(u.x * kTwoLog2e),
                        fabsf(u.y) <= kTanhSeries ? y.y : tanh_quotient(u.y * kTwoLog2e));
-}
-
-// Dynamic shared memory above 48 KB for a kernel: set once per device.
-template <typename... A>
-cudaError_t allow_smem(void (*kernel)(A...), int bytes, std::atomic<uint64_t>* done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
-    return e;
 }
 
 __device__ __forceinline__ void paged_err(int* err, int bit, int detail) {

@@ -47,9 +47,11 @@ struct Linear {
     int* err;
     void* workspace;
 };
-constexpr int kLinearMmaRows = 16;   // up to these rows the integer kernel takes the call
+// up to these rows the integer kernel takes a call, then the one for a batch's rows
+constexpr int kLinearMmaRows = 16, kLinearFewRows = 64;
 cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s);
 
+cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why);
 // Many rows; needs linear_tc_workspace bytes of workspace.
 size_t linear_tc_workspace(int n_out, int k, int n_rows);
 cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why);

@@ -60,7 +60,7 @@ kvr_status check_weights(const kvr_linear_weights* w) {
     return KVR_OK;
 }
 size_t linear_workspace(const kvr_linear_weights& w, int32_t n_rows) {
-    return n_rows <= kLinearMmaRows ? 256 : linear_tc_workspace(w.n_out, w.k, n_rows);
+    return n_rows <= kLinearFewRows ? 256 : linear_tc_workspace(w.n_out, w.k, n_rows);
 }
 
 kvr_status check_rope(const kvr_rope* r) {
@@ -319,7 +319,8 @@ kvr_status kvr_linear(const kvr_linear_weights* w, int32_t n_rows, const int8_t*
         return KVR_OK;
     }
     std::string why;
-    KVR_CHECK_LAUNCH(launch_linear_tc(a, s, &why), ("linear " + why).c_str());
+    KVR_CHECK_LAUNCH(n_rows <= kLinearFewRows ? launch_linear_few(a, s, &why) : launch_linear_tc(a, s, &why),
+                     ("linear " + why).c_str());
     return KVR_OK;
 }
 
