@@ -55,14 +55,25 @@ __device__ __forceinline__ void write_out(const Linear& a, int64_t at, float y) 
     if (a.dtype == KVR_F32) static_cast<float*>(a.out)[at] = y;
     else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
 }
-// four sums of one row, features f..f+3
-__device__ __forceinline__ void write4(const Linear& a, int row, int f, const int* sum) {
-    const float s = a.x_scale[row];
+// Features f .. f + 3 of one row; vec: out_vec4.
+__device__ __forceinline__ void write4(const Linear& a, int vec, int row, int f, const float* y) {
     const int64_t at = (int64_t)row * a.out_stride + f;
+    if (vec && f + 4 <= a.n_out) {
+        if (a.dtype == KVR_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(y[0], y[1]), q = __floats2bfloat162_rn(y[2], y[3]);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (f + i < a.n_out)
-            write_out(a, at + i, (float)sum[i] * s * a.w_scale[f + i] + (a.bias ? a.bias[f + i] : 0.f));
+        if (f + i < a.n_out) write_out(a, at + i, y[i]);
+}
+inline int out_vec4(const Linear& a) {
+    return a.out_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.dtype == KVR_F32 ? 16 : 8) == 0;
 }
 
 // Of 32 accumulator columns in registers a lane holds its feature, a column is

@@ -10,9 +10,9 @@
 // the workspace.  Two blocks an SM, so that one streams while the other starts
 // or ends.
 //   warp 0     TMA: per stage 128 features x 128 codes and N rows x 128 codes
-//   warp 1     products, four of K = 16 a 64-code chunk
-//   warps 2-9  widening, in two sets of four: set 0 takes the first 64 codes of every
-//              stage, set 1 the second, a thread a feature and two pieces of
+//   warp 1     products, eight of K = 16 a stage
+//   warps 2-9  widening, in two sets of four that take the stages in turn, each
+//              into a slot of its own: a thread a feature and up to four pieces of
 //              the rows; then they write the sums out
 // Every wait is bounded.
 #include <algorithm>
@@ -23,14 +23,23 @@
 namespace kvr {
 namespace {
 
-constexpr int kThreads = 320, kSlots = 4;
+constexpr int kSets = 2, kThreads = 64 + 128 * kSets;
 constexpr uint32_t kStageA = 128 * 128;
-constexpr uint32_t kCols = 256, kColA = 128;   // accumulator (up to 64 columns), then four chunks of 32
-constexpr int kSmemMost = 113 * 1024;          // two blocks an SM
+constexpr uint32_t kCols = 256, kColA = 64;   // accumulator (up to 64 columns), then a slot of 64 columns for each set
+constexpr int kSmemMost = 113 * 1024;         // two blocks an SM
+
+__device__ __forceinline__ uint4 lds128(uint32_t address) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(address) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t address, const uint32_t* v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(address), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 
 struct LinearFew {
     Linear a;
-    int N, split, KB, stages, out_as;
+    int N, split, KB, stages, out_as, vec;   // vec: four features of an output row are one aligned store
 };
 
 __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -40,36 +49,39 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stages = g.stages;
     const uint32_t tile = (uint32_t)g.N * 128, stage_bytes = kStageA + tile;   // N rows of 128 codes, or of 64 widened ones
-    uint8_t* wide = smem + (size_t)stages * stage_bytes;                       // [kSlots]
-    uint64_t* full = reinterpret_cast<uint64_t*>(wide + kSlots * tile);
+    uint8_t* wide = smem + (size_t)stages * stage_bytes;                       // [kSets][2 chunks]
+    uint64_t* full = reinterpret_cast<uint64_t*>(wide + 2 * kSets * tile);
     uint64_t* empty = full + stages;
-    uint64_t* ready = empty + stages;   // [kSlots]
-    uint64_t* freed = ready + kSlots;   // [kSlots]
-    uint64_t* done = freed + kSlots;
+    uint64_t* ready = empty + stages;   // [kSets]
+    uint64_t* freed = ready + kSets;    // [kSets]
+    uint64_t* done = freed + kSets;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = g.split, rank = (int)blockIdx.x % split, f0 = (int)blockIdx.x / split * 128;
     const int kb0 = g.KB * rank / split, n_kb = g.KB * (rank + 1) / split - kb0;
+    auto copies = [&](int s, int it) {
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        uint8_t* d = smem + (size_t)s * stage_bytes;
+        tma_load_2d(d, &tmA, &full[s], (kb0 + it) * 128, f0);
+        tma_load_2d(d + kStageA, &tmB, &full[s], (kb0 + it) * 128, 0);
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 8);
+            mbar_init(&empty[s], 4);
         }
-        for (int t = 0; t < kSlots; ++t) {
+        for (int t = 0; t < kSets; ++t) {
             mbar_init(&ready[t], 4);
             mbar_init(&freed[t], 1);
         }
         mbar_init(done, 1);
         fence_mbar_init();
+        for (int it = 0; it < min(stages, n_kb); ++it) copies(it, it);   // the ring fills while the block sets up
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kCols);
         tmem_relinquish();
-    }
-    if (warp == 0 && lane == 0) {
-        prefetch_tmap(&tmA);
-        prefetch_tmap(&tmB);
     }
     tc_fence_before();
     __syncthreads();
@@ -79,43 +91,40 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
 
     if (warp == 0) {
         if (lane == 0) {
-            int s = 0, it = 0;
-            uint32_t phase = 1;
+            int s = 0, it = stages;
+            uint32_t phase = 0;
             for (; it < n_kb; ++it) {
                 if (!mbar_wait(&empty[s], phase)) {
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(&full[s], stage_bytes);
-                uint8_t* d = smem + (size_t)s * stage_bytes;
-                tma_load_2d(d, &tmA, &full[s], (kb0 + it) * 128, f0);
-                tma_load_2d(d + kStageA, &tmB, &full[s], (kb0 + it) * 128, 0);
+                copies(s, it);
                 if (++s == stages) {
                     s = 0;
                     phase ^= 1u;
                 }
             }
             if (!ok) {   // let every copy still in flight land before the block exits
-                for (int i = (it > stages ? it - stages : 0); i < it; ++i)
-                    mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
+                for (int i = it - stages; i < it; ++i) mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
         const uint32_t idesc = (1u << 4) | ((uint32_t)(g.N >> 3) << 17) | ((128u >> 4) << 24);   // fp16, fp32 sums
         const uint64_t descB = sdesc_sw128(smem_u32(wide), 16, 1024);
         const bool issuer = elect_one();
-        for (int q = 0; q < 2 * n_kb; ++q) {
-            const uint32_t t = q & (kSlots - 1);
-            if (!__all_sync(0xffffffffu, mbar_wait(&ready[t], (uint32_t)(q / kSlots) & 1u))) {
+        for (int it = 0; it < n_kb; ++it) {
+            const uint32_t t = it % kSets;
+            if (!__all_sync(0xffffffffu, mbar_wait(&ready[t], (uint32_t)(it / kSets) & 1u))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             if (issuer) {
 #pragma unroll
-                for (uint32_t kk = 0; kk < 4; ++kk)
-                    mma_bf16_ta(tmem, tmem + kColA + 32 * t + 8 * kk, descB + (uint64_t)((t * tile >> 4) + 2 * kk), idesc,
-                                q > 0 || kk > 0);
+                for (uint32_t kk = 0; kk < 8; ++kk)
+                    mma_bf16_ta(tmem, tmem + kColA + 64 * t + 8 * kk,
+                                descB + (uint64_t)(((2 * t + kk / 4) * tile >> 4) + 2 * (kk % 4)), idesc, it > 0 || kk > 0);
                 mma_commit(&freed[t]);
             }
             __syncwarp();
@@ -124,80 +133,70 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
         __syncwarp();
         if (!__all_sync(0xffffffffu, mbar_wait(done, 0))) ok = false;
     } else {
-        const int half = (warp - 2) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
-        const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16);
-        int s = 0, pending = -1;
-        uint32_t phase = 0;
-        // A chunk is handed over when the next one's codes are in registers, or at once where those have not come.
-        auto hand_over = [&]() {
-            if (pending < 0) return;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ready[pending]);
-            pending = -1;
-        };
-        for (int it = 0; it < n_kb; ++it) {
-            const int q = 2 * it + half;
-            const uint32_t t = q & (kSlots - 1);
-            if (!__all_sync(0xffffffffu, mbar_test(&full[s], phase))) {
-                hand_over();
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
-                    ok = false;
-                    break;
-                }
+        const int set = (warp - 2) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+        const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16), slot = dst + kColA + 64 * set;
+        // Piece p of the rows' tile: row p / 8, its 16 codes p % 8, which become two 16-byte pieces of a chunk's row.
+        // A thread's pieces lie 16 rows apart: the same swizzle.
+        const uint32_t r = row >> 3, piece = row & 7;
+        const uint32_t from = smem_u32(smem) + row * 128, from_b = smem_u32(smem) + kStageA + r * 128 + ((piece ^ (r & 7)) << 4);
+        const uint32_t to_b = smem_u32(wide) + (2 * set + (piece >> 2)) * tile + r * 128;
+        const uint32_t lo = ((2 * (piece & 3)) ^ (r & 7)) << 4, hi = ((2 * (piece & 3) + 1) ^ (r & 7)) << 4;
+        int s = set % stages;
+        uint32_t phase = (uint32_t)(set / stages) & 1u, use = 1;
+        for (int it = set; it < n_kb; it += kSets, use ^= 1u) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
+                ok = false;
+                break;
             }
-            const uint8_t* a = smem + (size_t)s * stage_bytes;
-            uint4 c[4], b[2];
+            const uint32_t at = (uint32_t)s * stage_bytes;
+            uint4 c[8], b[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = lds128(from + at + ((i ^ (row & 7)) << 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                c[i] = *reinterpret_cast<const uint4*>(a + row * 128 + (((4 * half + i) ^ (row & 7)) << 4));
-            // piece p of the rows: row p / 4, 16 codes p % 4 of the chunk
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int p = row + 128 * i, r = p >> 2;
-                if (r < g.N)
-                    b[i] = *reinterpret_cast<const uint4*>(a + kStageA + r * 128 + (((4 * half + (p & 3)) ^ (r & 7)) << 4));
-            }
+                if (16 * i < g.N) b[i] = lds128(from_b + at + 2048 * i);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
             uint32_t h[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) widen16(c[i], h + 8 * i);
-            hand_over();
-            if (!__all_sync(0xffffffffu, mbar_wait(&freed[t], ((uint32_t)(q / kSlots) & 1u) ^ 1u))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&freed[set], use))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            tmem_st16_async(dst + kColA + 32 * t, h);
-            tmem_st16_async(dst + kColA + 32 * t + 16, h + 16);
+            tmem_st16_async(slot, h);
+            tmem_st16_async(slot + 16, h + 16);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int p = row + 128 * i, r = p >> 2;
-                if (r < g.N) {
-                    uint32_t y[8];
-                    widen16(b[i], y);
-                    uint8_t* o = wide + t * tile + r * 128;
-                    *reinterpret_cast<uint4*>(o + (((2 * (p & 3)) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4*>(o + (((2 * (p & 3) + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                if (16 * i >= g.N) break;
+                uint32_t y[8];
+                widen16(b[i], y);
+                sts128(to_b + 2048 * i + lo, y);
+                sts128(to_b + 2048 * i + hi, y + 4);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) widen16(c[4 + i], h + 8 * i);
+            tmem_st16_async(slot + 32, h);
+            tmem_st16_async(slot + 48, h + 16);
             fence_proxy_async_smem();
-            pending = (int)t;
-            if (++s == stages) {
-                s = 0;
-                phase ^= 1u;
-            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[set]);
+            for (int i = 0; i < kSets; ++i)
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
         }
-        hand_over();
         // ---------------------------------------------------------------- sums out
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(done, 0)) != 0;
         if (ok) {
             tc_fence_after();
             const int f = f0 + row, left = min(g.a.n_rows, g.N);
             const float sw = f < g.a.n_out ? g.a.w_scale[f] : 0.f, bias = f < g.a.n_out && g.a.bias ? g.a.bias[f] : 0.f;
-            for (int c = 32 * half; c < g.N; c += 64) {
+            for (int c = 32 * set; c < g.N; c += 64) {
                 float v[32];
                 tmem_ld32(dst + (uint32_t)c, v);
                 if (split == 1) {
@@ -215,20 +214,34 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
     if (!ok) atomicOr(g.a.err, DEV_ERR_TIMEOUT);
     tc_fence_before();
     if (split > 1) {
+        // a row of the tile a warp, four features a lane; this block's rows are [r0, r1)
+        const int f = f0 + 4 * lane, r0 = g.N * rank / split, r1 = min(g.N * (rank + 1) / split, g.a.n_rows);
+        float sw[4], bias[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sw[i] = f + i < g.a.n_out ? g.a.w_scale[f + i] : 0.f;
+            bias[i] = f + i < g.a.n_out && g.a.bias ? g.a.bias[f + i] : 0.f;
+        }
         cluster_sync();
-        // this block's rows of the tile, four features a thread
-        const int r0 = g.N * rank / split, n = min(g.N * (rank + 1) / split, g.a.n_rows) - r0;
-        for (int i = threadIdx.x; i < n * 32; i += kThreads) {
-            const int r = r0 + i / 32, f = 4 * (i % 32);
+        for (int r = r0 + warp; r < r1; r += kThreads / 32) {
+            const float sx = g.a.x_scale[r];
+            float4 v[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                if (p < split) v[p] = load_peer4(peer_address(smem + (size_t)(r * 128 + 4 * lane) * 4, (uint32_t)p));
             int sum[4] = {0, 0, 0, 0};
-            for (int p = 0; p < split; ++p) {
-                const float4 v = load_peer4(peer_address(smem + (size_t)(r * 128 + f) * 4, (uint32_t)((rank + p) % split)));
-                sum[0] += __float2int_rn(v.x);
-                sum[1] += __float2int_rn(v.y);
-                sum[2] += __float2int_rn(v.z);
-                sum[3] += __float2int_rn(v.w);
-            }
-            if (f0 + f < g.a.n_out) write4(g.a, r, f0 + f, sum);
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                if (p < split) {
+                    sum[0] += __float2int_rn(v[p].x);
+                    sum[1] += __float2int_rn(v[p].y);
+                    sum[2] += __float2int_rn(v[p].z);
+                    sum[3] += __float2int_rn(v[p].w);
+                }
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = (float)sum[i] * sx * sw[i] + bias[i];
+            write4(g.a, g.vec, r, f, y);
         }
         cluster_sync();   // no block leaves while another reads its sums
     } else {
@@ -248,21 +261,16 @@ cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why)
     g.N = std::max(16, (a.n_rows + 15) / 16 * 16);
     g.KB = (a.k + 127) / 128;
     const int tiles = (a.n_out + 127) / 128;
-    // Blocks a cluster: those on the busiest SM times their share of k, and a
-    // little for joining.
-    double best = 1e30;
-    for (int c = 1; c <= std::min(8, std::max(1, g.KB / 2)); ++c) {
-        const double t = (double)((tiles * c + kNumSMs - 1) / kNumSMs) * ((g.KB + c - 1) / c) + 0.25 * c;
-        if (t < best) {
-            best = t;
-            g.split = c;
-        }
-    }
+    // Blocks a cluster: as many as leave every block resident at once (two an SM).
+    g.split = 1;
+    while (g.split < 8 && 2 * g.split * tiles <= 2 * kNumSMs && g.KB >= 8 * g.split) g.split *= 2;
     const uint32_t tile = g.N * 128, stage = kStageA + tile;
-    const uint32_t fixed = 1024 + kSlots * tile + 512;   // the ring's size also holds the [N][128] sums
-    g.stages = (kSmemMost - 1024 - (int)fixed) / (int)stage;
-    g.stages = std::min(g.stages, 8);
+    const uint32_t fixed = 1024 + 2 * kSets * tile + 512;   // the ring's size also holds the [N][128] sums
+    // A multiple of the sets, so that a stage always belongs to the same one: a set that skipped a stage's earlier
+    // use could not tell its phases apart.
+    g.stages = std::min(8, (kSmemMost - 1024 - (int)fixed) / (int)stage / kSets * kSets);
     g.out_as = out_kind(a);
+    g.vec = out_vec4(a);
     CUtensorMap ta, tb;
     if (!make_tmap_2d_sw128(&ta, 1, a.w, a.k, a.n_out, a.w_stride, 128, 128, why) ||
         !make_tmap_2d_sw128(&tb, 1, a.x, a.k, a.n_rows, a.x_stride, 128, g.N, why))

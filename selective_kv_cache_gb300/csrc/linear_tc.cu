@@ -46,6 +46,7 @@ namespace {
 constexpr int kPairs = kNumSMs / 2;
 constexpr int kSets = 4, kOuts = 2;                // sets of widening warps; warps a lane quarter that write out
 constexpr int kThreads = 32 * (4 + 4 * kOuts + 4 * kSets);
+static_assert(kSets == 4, "two sets take the halves of every other stage");
 constexpr int kStageK = 128;                      // codes of a stage: two chunks
 constexpr uint32_t kStageA = 128 * 128;           // 128 features x 128 bytes
 constexpr int kSmemMost = 227 * 1024;
@@ -53,7 +54,7 @@ constexpr int kSuper = 8;                         // row tiles that are walked b
 
 struct LinearTc {
     Linear a;
-    int out_as;
+    int out_as, vec;
     float* part;            // [pairs][2][N][256]
     int N, m_tiles, n_tiles, KB, stages;
     int whole, rest, pairs; // tiles taken whole, tiles of the line, pairs in the grid
@@ -466,7 +467,12 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         sum[2] += __float2int_rn(v.z);
         sum[3] += __float2int_rn(v.w);
     }
-    write4(g.a, row, f, sum);
+    const float sx = g.a.x_scale[row];
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = f + i < g.a.n_out ? (float)sum[i] * sx * g.a.w_scale[f + i] + (g.a.bias ? g.a.bias[f + i] : 0.f) : 0.f;
+    write4(g.a, g.vec, row, f, y);
 }
 
 struct Plan {
@@ -480,7 +486,9 @@ Plan make_plan(int n_out, int k, int n_rows) {
     p.N = std::max(32, ((n_rows + p.n_tiles - 1) / p.n_tiles + 31) / 32 * 32);
     p.KB = (k + kStageK - 1) / kStageK;
     const int stage = kStageA + p.N * 128;
-    p.stages = std::min(12, (kSmemMost - 2048) / stage);
+    // even, so that a stage always belongs to the same two of the four sets: a set that skipped a stage's earlier use
+    // could not tell its phases apart
+    p.stages = std::min(12, (kSmemMost - 2048) / stage / 2 * 2);
     const int tiles = p.m_tiles * p.n_tiles;
     p.rest = tiles % kPairs;
     p.whole = tiles - p.rest;
@@ -513,6 +521,7 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     g.rest = p.rest;
     g.pairs = p.pairs;
     g.out_as = out_kind(a);
+    g.vec = out_vec4(a);
     g.slots = p.N <= 128 ? 8 : 4;
     g.col_a = 512 - 32 * g.slots;
     g.shared_cols = 2 * p.N > (int)g.col_a;
