@@ -30,11 +30,13 @@
 // they share columns, which the epilogue reads first), and four chunks of widened
 // weights behind them, eight up to N = 128.
 //
-// Tiles are taken in turn by the 76 pairs, whole.  The tiles that are left
-// after the last whole turn, or all of them where there are fewer than pairs,
-// are one line of (tile, 128 codes) units of which every pair takes an equal
-// share; its pieces of tiles go to the workspace as fp32 and a last kernel adds
-// them as integers.  Every wait is bounded.
+// Work: pairs take whole tiles in turn.  The tiles that are left after the last
+// whole turn, or all of them where there are few, may be split: a cluster then
+// holds several pairs, each takes its part of k, writes it to the workspace as
+// fp32, and the cluster's CTAs add the parts as integers, a share of the rows
+// each, as soon as all have arrived on their barriers.  How many pairs a
+// cluster has, and how wide a tile is, go by a model of the time (make_plan).
+// Every wait is bounded.
 #include <algorithm>
 
 #include "linear.cuh"
@@ -43,7 +45,6 @@
 namespace kvr {
 namespace {
 
-constexpr int kPairs = kNumSMs / 2;
 constexpr int kSets = 4, kOuts = 2;                // sets of widening warps; warps a lane quarter that write out
 constexpr int kThreads = 32 * (4 + 4 * kOuts + 4 * kSets);
 static_assert(kSets == 4, "two sets take the halves of every other stage");
@@ -55,9 +56,10 @@ constexpr int kSuper = 8;                         // row tiles that are walked b
 struct LinearTc {
     Linear a;
     int out_as, vec;
-    float* part;            // [pairs][2][N][256]
+    float* part;            // [split tile][split][N][256]
     int N, m_tiles, n_tiles, KB, stages;
-    int whole, rest, pairs; // tiles taken whole, tiles of the line, pairs in the grid
+    int whole, rest;        // tiles taken whole, tiles split
+    int split, clusters;    // pairs of a cluster, clusters of the grid
     uint32_t base1;         // columns of the second accumulator
     int shared_cols;        // whether the two share columns
     uint32_t col_a, slots;  // widened chunks: their first column and their number, 4 or 8
@@ -69,11 +71,27 @@ struct LinearTc {
 // landed; nothing in ordinary memory is handed over, so neither side names the
 // cluster's scope: with .release.cluster and .acquire.cluster a stage took 2500 cycles, the
 // fences' round trips, in place of 1400.
-__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
+__device__ __forceinline__ void arrive_leader(uint64_t* bar, uint32_t leader) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_address(bar, leader)) : "memory");
+}
+// One arrival on another CTA's barrier that hands over what this warp wrote to
+// the workspace, and the wait for it.
+__device__ __forceinline__ void arrive_release(uint64_t* bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_address(bar, rank)) : "memory");
+}
+__device__ __forceinline__ bool warp_wait_acquire(uint64_t* bar, uint32_t parity) {
+    uint32_t ok = 0;
+    const long long t0 = clock64();
+    do {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    } while (!ok && clock64() - t0 <= kWaitLimitCycles);
+    return __all_sync(0xffffffffu, ok != 0) != 0;
 }
 __device__ __forceinline__ bool try_wait_pair(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -113,41 +131,32 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint64_t bdesc,
         : "memory");
 }
 // arrive on both CTAs' barriers at this offset when the products issued so far are done
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint32_t leader) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << leader))
         : "memory");
 }
 
 // ---------------------------------------------------------------- work
-// Piece j of a pair's work: the line's pieces first (at most two), then whole tiles.
+// A pair's work in order: whole tiles, then its parts of split ones.
 struct Piece {
-    int tile, kb0, kb1, slot;   // slot < 0: whole
+    int tile, kb0, kb1, rest;   // rest: number of the split tile, or below 0
 };
-__device__ __forceinline__ int share_begin(const LinearTc& g, int pair) {
-    return (int)((uint32_t)(g.rest * g.KB) * (uint32_t)pair / (uint32_t)g.pairs);   // below 76 * 512 * 76
-}
 struct Walk {
-    int u, u1, next, slot;
-    __device__ __forceinline__ Walk(const LinearTc& g, int pair)
-        : u(share_begin(g, pair)), u1(share_begin(g, pair + 1)), next(pair), slot(2 * pair) {}
+    int next, pair, cluster, part;
+    __device__ __forceinline__ Walk(const LinearTc& g, int id)
+        : next(id), pair(id), cluster(id / g.split), part(id - id / g.split * g.split) {}
     __device__ __forceinline__ bool take(const LinearTc& g, Piece* p) {
-        if (u < u1) {
-            const int t = u / g.KB;
-            p->tile = g.whole + t;
-            p->kb0 = u - t * g.KB;
-            p->kb1 = min(g.KB, u1 - t * g.KB);
-            const bool all = p->kb1 - p->kb0 == g.KB;
-            p->slot = all ? -1 : slot;
-            ++slot;
-            u += p->kb1 - p->kb0;
+        if (next < g.whole) {
+            *p = Piece{next, 0, g.KB, -1};
+            next += g.split * g.clusters;
             return true;
         }
-        if (next >= g.whole) return false;
-        *p = Piece{next, 0, g.KB, -1};
-        next += g.pairs;
+        if (cluster >= g.rest) return false;
+        *p = Piece{g.whole + cluster, g.KB * part / g.split, g.KB * (part + 1) / g.split, cluster};
+        cluster += g.clusters;
         return true;
     }
 };
@@ -208,9 +217,10 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     uint64_t* acc_empty = acc_full + 2;   // [2], the leader's
     uint64_t* cols_free = acc_empty + 2;  // the leader's: the columns that both accumulators use are read
     uint64_t* all_done = cols_free + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
+    uint64_t* joined = all_done + 1;      // the cluster's parts of a split tile, of this CTA's features, are written
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cta_rank();
+    const uint32_t rank = cta_rank(), leader = rank & ~1u, half = rank & 1u;   // half: of the tile's features and rows
     const int pair = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -228,6 +238,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         }
         mbar_init(cols_free, 8 * kOuts);
         mbar_init(all_done, 1);
+        mbar_init(joined, 4 * kOuts * g.split);
         fence_mbar_init();
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         // ------------------------------------------------------------ copies
         if (lane == 0) {
             auto load_a = [&](int s, int m, int kb) {
-                tma_load_2d(smem + (size_t)s * stage_bytes, &tmA, &full[s], kb * kStageK, m * 256 + (int)rank * 128);
+                tma_load_2d(smem + (size_t)s * stage_bytes, &tmA, &full[s], kb * kStageK, m * 256 + (int)half * 128);
             };
             // no kernel of the call writes the weights: the ring's first ones go out before the wait for the rows
             int pre = 0;
@@ -274,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                         load_a(s, m, kb);
                     }
                     uint8_t* b = smem + (size_t)s * stage_bytes + kStageA;
-                    tma_load_2d(b, &tmB, &full[s], kb * kStageK, n * g.N + (int)(rank * half_rows));
-                    tma_load_2d(b + atomB, &tmB, &full[s], kb * kStageK + 64, n * g.N + (int)(rank * half_rows));
+                    tma_load_2d(b, &tmB, &full[s], kb * kStageK, n * g.N + (int)(half * half_rows));
+                    tma_load_2d(b + atomB, &tmB, &full[s], kb * kStageK + 64, n * g.N + (int)(half * half_rows));
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1u;
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         const bool issuer = elect_one();
-        if (rank == 0) {
+        if (half == 0) {
             const uint32_t idesc = (1u << 4) | ((uint32_t)(g.N >> 3) << 17) | ((256u >> 4) << 24);   // fp16, fp32 sums
             const uint64_t descB = sdesc_sw128(smem_u32(smem) + kStageA, 16, 1024);
             int s = 0, local = 0;
@@ -320,8 +331,8 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                             for (uint32_t kk = 0; kk < 4; ++kk)
                                 pair_mma(d, tmem + g.col_a + 32 * t + 8 * kk, db + (uint64_t)((h * atomB >> 4) + 2 * kk), idesc,
                                          (h > 0 || kk > 0) ? 1u : (kb > p.kb0 ? 1u : 0u));
-                            pair_commit(&a_free[t]);
-                            if (h == 1) pair_commit(&empty[s]);
+                            pair_commit(&a_free[t], leader);
+                            if (h == 1) pair_commit(&empty[s], leader);
                         }
                         __syncwarp();
                     }
@@ -329,16 +340,16 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                     if (++s == stages) s = 0;
                 }
                 if (!ok) break;
-                if (issuer) pair_commit(&acc_full[ab]);
+                if (issuer) pair_commit(&acc_full[ab], leader);
                 __syncwarp();
             }
-            if (issuer) pair_commit(all_done);
+            if (issuer) pair_commit(all_done, leader);
             __syncwarp();
         }
         if (!warp_wait(all_done, 0)) ok = false;
     } else if (warp >= 4 + 4 * kOuts) {
         // ------------------------------------------------------------ widening
-        const int set = (warp - 4 - 4 * kOuts) >> 2, half = set & 1, quarter = warp & 3, row = 32 * quarter + lane;
+        const int set = (warp - 4 - 4 * kOuts) >> 2, chunk = set & 1, quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t dst = tmem + ((uint32_t)(32 * quarter) << 16) + g.col_a;
         int s = 0, turn = set >> 1, pending = -1;   // this set's stages: every kSets / 2-th
         uint32_t phase = 0, q = set;
@@ -349,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_leader(&a_ready[pending]);
+            if (lane == 0) arrive_leader(&a_ready[pending], leader);
             pending = -1;
         };
         Piece p;
@@ -375,7 +386,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                 uint32_t h[32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    widen16(*reinterpret_cast<const uint4*>(a + (((4 * half + c) ^ (row & 7)) << 4)), h + 8 * c);
+                    widen16(*reinterpret_cast<const uint4*>(a + (((4 * chunk + c) ^ (row & 7)) << 4)), h + 8 * c);
                 hand_over();
                 if (!warp_wait(&a_free[t], ((q >> lap) & 1u) ^ 1u)) {
                     ok = false;
@@ -391,9 +402,9 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         hand_over();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ accumulators out
-        const int part = (warp - 4) >> 2, quarter = warp & 3, fo = (int)rank * 128 + quarter * 32 + lane;   // this lane's feature in the tile
+        const int part = (warp - 4) >> 2, quarter = warp & 3, fo = (int)half * 128 + quarter * 32 + lane;   // this lane's feature in the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        int local = 0;
+        int local = 0, splits = 0;
         Piece p;
         for (Walk w(g, pair); w.take(g, &p); ++local) {
             const int ab = local & 1;
@@ -407,13 +418,15 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             }
             tc_fence_after();
             const uint32_t src = tmem + lane_base + (ab ? g.base1 : 0u);
+            float* tile_parts = g.part + (size_t)max(p.rest, 0) * g.split * g.N * 256;   // [split][N][256]
+            float* mine = tile_parts + (size_t)w.part * g.N * 256;
             auto drain = [&](int lo, int hi) {
                 for (int c = lo + 32 * part; c < hi; c += 32 * kOuts) {
                     const float sx = c + lane < rows ? g.a.x_scale[row0 + c + lane] : 0.f;
                     float v[32];
                     tmem_ld32(src + (uint32_t)c, v);
                     const int left = rows - c;
-                    if (p.slot >= 0) write_part(g.part + ((size_t)p.slot * g.N + c) * 256 + fo, v, left);
+                    if (p.rest >= 0) write_part(mine + c * 256 + fo, v, left);
                     else write32(g.a, g.out_as, row0 + c, f, v, sx, sw, bias, left);
                 }
             };
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                 drain(lo, hi);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_leader(cols_free);
+                if (lane == 0) arrive_leader(cols_free, leader);
                 drain(0, lo);
                 drain(hi, g.N);
             } else {
@@ -430,7 +443,43 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_leader(&acc_empty[ab]);
+            if (lane == 0) arrive_leader(&acc_empty[ab], leader);
+            if (p.rest < 0) continue;
+            // the parts of this CTA's features, a share of the rows: a row a warp, four features a lane
+            if (lane < g.split) arrive_release(joined, 2 * lane + half);
+            const int f4 = m * 256 + (int)half * 128 + 4 * lane;
+            const int c1 = min(rows, g.N * (w.part + 1) / g.split);
+            float sw4[4], bias4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sw4[i] = f4 + i < g.a.n_out ? g.a.w_scale[f4 + i] : 0.f;
+                bias4[i] = f4 + i < g.a.n_out && g.a.bias ? g.a.bias[f4 + i] : 0.f;
+            }
+            if (!warp_wait_acquire(joined, (uint32_t)(splits++) & 1u)) {
+                ok = false;
+                break;
+            }
+            for (int c = g.N * w.part / g.split + (warp - 4); c < c1; c += 4 * kOuts) {
+                const float* from = tile_parts + c * 256 + half * 128 + 4 * lane;
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < g.split) v[i] = __ldcg(reinterpret_cast<const float4*>(from + (size_t)i * g.N * 256));
+                const float sx = g.a.x_scale[row0 + c];
+                int sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < g.split) {
+                        sum[0] += __float2int_rn(v[i].x);
+                        sum[1] += __float2int_rn(v[i].y);
+                        sum[2] += __float2int_rn(v[i].z);
+                        sum[3] += __float2int_rn(v[i].w);
+                    }
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = (float)sum[i] * sx * sw4[i] + bias4[i];
+                write4(g.a, g.vec, row0 + c, f4, y);
+            }
         }
     }
     if (!ok) atomicOr(g.a.err, DEV_ERR_TIMEOUT);
@@ -443,59 +492,52 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     }
 }
 
-// The line's tiles: pieces added as integers, in any order the same.
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearTc g) {
-    pdl_wait();
-    // a block: four rows of a tile, four features a thread
-    const int blocks = g.N / 4, tile = blockIdx.x / blocks, col = (blockIdx.x - tile * blocks) * 4 + threadIdx.x / 64;
-    int m, n;
-    tile_coords(g, g.whole + tile, &m, &n);
-    const int fo = 4 * (threadIdx.x % 64), row = n * g.N + col, f = m * 256 + fo;
-    if (row >= g.a.n_rows || f >= g.a.n_out) return;
-    // the pairs whose shares meet [u0, u1)
-    const int u0 = tile * g.KB, u1 = u0 + g.KB;
-    int pair = (int)((uint32_t)u0 * (uint32_t)g.pairs / (uint32_t)(g.rest * g.KB));
-    while (share_begin(g, pair + 1) <= u0) ++pair;
-    int sum[4] = {0, 0, 0, 0};
-    for (int b = share_begin(g, pair), e; b < u1; ++pair, b = e) {
-        e = share_begin(g, pair + 1);
-        if (b <= u0 && e >= u1) return;   // one pair had all of it and wrote it
-        const int slot = 2 * pair + (tile - b / g.KB);
-        const float4 v = *reinterpret_cast<const float4*>(g.part + ((size_t)slot * g.N + col) * 256 + fo);
-        sum[0] += __float2int_rn(v.x);
-        sum[1] += __float2int_rn(v.y);
-        sum[2] += __float2int_rn(v.z);
-        sum[3] += __float2int_rn(v.w);
-    }
-    const float sx = g.a.x_scale[row];
-    float y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        y[i] = f + i < g.a.n_out ? (float)sum[i] * sx * g.a.w_scale[f + i] + (g.a.bias ? g.a.bias[f + i] : 0.f) : 0.f;
-    write4(g.a, g.vec, row, f, y);
-}
+// Clusters of 1, 2, 3 and 4 pairs that a GB300 holds at once, one CTA an SM
+// (cudaOccupancyMaxActiveClusters): its GPCs are not multiples of a cluster.
+constexpr int kClusters[5] = {0, 76, 36, 23, 15};
 
 struct Plan {
-    int N, m_tiles, n_tiles, KB, stages, whole, rest, pairs, pitch;
+    int N, m_tiles, n_tiles, KB, stages, whole, rest, split, clusters, pitch;
     size_t rows_bytes, part_bytes;
 };
+// The width of a tile and the pairs of a cluster that take the shortest time in
+// cycles: a stage of 128 codes takes its products' 4 N, or what copying and
+// widening the weights take; a tile's end stops the products of a
+// wide one while shared columns are read; a split tile's parts are joined.
 Plan make_plan(int n_out, int k, int n_rows) {
-    Plan p{};
-    p.m_tiles = (n_out + 255) / 256;
-    p.n_tiles = (n_rows + 255) / 256;
-    p.N = std::max(32, ((n_rows + p.n_tiles - 1) / p.n_tiles + 31) / 32 * 32);
-    p.KB = (k + kStageK - 1) / kStageK;
+    Plan best{};
+    double least = 1e300;
+    for (int N = 32; N <= 256; N += 32) {
+        for (int split = 1; split <= 4; ++split) {
+            Plan p{};
+            p.N = N;
+            p.split = split;
+            p.m_tiles = (n_out + 255) / 256;
+            p.n_tiles = (n_rows + N - 1) / N;
+            p.KB = (k + kStageK - 1) / kStageK;
+            if (split > p.KB || (N > 32 && N - 32 >= n_rows)) continue;
+            const long long tiles = (long long)p.m_tiles * p.n_tiles;
+            const int pairs = split * kClusters[split];
+            p.whole = split == 1 ? (int)tiles : (int)(tiles / pairs * pairs);
+            p.rest = (int)(tiles - p.whole);
+            const int turns = (p.whole + pairs - 1) / pairs, rest_turns = (p.rest + kClusters[split] - 1) / kClusters[split];
+            const double stage = std::max(850.0, 4.0 * N), end = N > 192 ? 4000 : 500;
+            const double t = turns * (p.KB * stage + end) +
+                             rest_turns * ((p.KB + split - 1) / split * stage + 3000 + 16.0 * N);
+            if (t >= least) continue;
+            least = t;
+            p.clusters = (int)std::min<long long>(kClusters[split], p.whole ? (p.whole + split - 1) / split + p.rest : p.rest);
+            best = p;
+        }
+    }
+    Plan p = best;
     const int stage = kStageA + p.N * 128;
     // even, so that a stage always belongs to the same two of the four sets: a set that skipped a stage's earlier use
     // could not tell its phases apart
     p.stages = std::min(12, (kSmemMost - 2048) / stage / 2 * 2);
-    const int tiles = p.m_tiles * p.n_tiles;
-    p.rest = tiles % kPairs;
-    p.whole = tiles - p.rest;
-    p.pairs = (int)std::min<long long>(kPairs, p.whole ? kPairs : (long long)p.rest * p.KB);
     p.pitch = (k + 7) / 8 * 8;
     p.rows_bytes = ((size_t)n_rows * p.pitch * 2 + 255) / 256 * 256;
-    p.part_bytes = p.rest ? (size_t)p.pairs * 2 * p.N * 256 * 4 : 0;
+    p.part_bytes = (size_t)p.rest * p.split * p.N * 256 * 4;
     return p;
 }
 
@@ -519,7 +561,8 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     g.stages = p.stages;
     g.whole = p.whole;
     g.rest = p.rest;
-    g.pairs = p.pairs;
+    g.split = p.split;
+    g.clusters = p.clusters;
     g.out_as = out_kind(a);
     g.vec = out_vec4(a);
     g.slots = p.N <= 128 ? 8 : 4;
@@ -535,12 +578,9 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
                a.x_stride, rows, p.pitch, a.k, a.n_rows);
     const size_t smem = 1024 + (size_t)p.stages * (kStageA + p.N * 128) + 1024;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(linear_tc_kernel, kSmemMost, &done);
+    const cudaError_t e = allow_smem(linear_tc_kernel, kSmemMost, &done);
     if (e != cudaSuccess) return e;
-    e = launch_clusters(2, linear_tc_kernel, dim3(2 * p.pairs), dim3(kThreads), smem, s, ta, tb, g);
-    if (e != cudaSuccess || p.rest == 0) return e;
-    KVR_LAUNCH(linear_join_kernel, dim3((unsigned)p.rest * (p.N / 4)), dim3(256), 0, s, g);
-    return cudaSuccess;
+    return launch_clusters(2 * p.split, linear_tc_kernel, dim3(2 * p.split * p.clusters), dim3(kThreads), smem, s, ta, tb, g);
 }
 
 }  // namespace kvr
