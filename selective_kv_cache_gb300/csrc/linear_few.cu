@@ -28,15 +28,6 @@ constexpr uint32_t kStageA = 128 * 128;
 constexpr uint32_t kCols = 256, kColA = 64;   // accumulator (up to 64 columns), then a slot of 64 columns for each set
 constexpr int kSmemMost = 113 * 1024;         // two blocks an SM
 
-__device__ __forceinline__ uint4 lds128(uint32_t address) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(address) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts128(uint32_t address, const uint32_t* v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(address), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-}
-
 struct LinearFew {
     Linear a;
     int N, split, KB, stages, out_as, vec;   // vec: four features of an output row are one aligned store
@@ -59,11 +50,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = g.split, rank = (int)blockIdx.x % split, f0 = (int)blockIdx.x / split * 128;
     const int kb0 = g.KB * rank / split, n_kb = g.KB * (rank + 1) / split - kb0;
+    const int row0 = blockIdx.y * g.N, rows = min(g.N, g.a.n_rows - row0);   // of this block's tile
     auto copies = [&](int s, int it) {
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         uint8_t* d = smem + (size_t)s * stage_bytes;
         tma_load_2d(d, &tmA, &full[s], (kb0 + it) * 128, f0);
-        tma_load_2d(d + kStageA, &tmB, &full[s], (kb0 + it) * 128, 0);
+        tma_load_2d(d + kStageA, &tmB, &full[s], (kb0 + it) * 128, row0);
     };
 
     if (threadIdx.x == 0) {
@@ -143,13 +135,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
         const uint32_t lo = ((2 * (piece & 3)) ^ (r & 7)) << 4, hi = ((2 * (piece & 3) + 1) ^ (r & 7)) << 4;
         int s = set % stages;
         uint32_t phase = (uint32_t)(set / stages) & 1u, use = 1;
-        for (int it = set; it < n_kb; it += kSets, use ^= 1u) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
-                ok = false;
-                break;
-            }
+        uint4 c[8], b[4];
+        auto fetch = [&]() {   // and give the stage back
             const uint32_t at = (uint32_t)s * stage_bytes;
-            uint4 c[8], b[4];
 #pragma unroll
             for (int i = 0; i < 8; ++i) c[i] = lds128(from + at + ((i ^ (row & 7)) << 4));
 #pragma unroll
@@ -157,14 +145,24 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
                 if (16 * i < g.N) b[i] = lds128(from_b + at + 2048 * i);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
-            uint32_t h[32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) widen16(c[i], h + 8 * i);
+        };
+        bool have = false;
+        for (int it = set; it < n_kb; it += kSets, use ^= 1u) {
+            if (!have) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
+                    ok = false;
+                    break;
+                }
+                fetch();
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(&freed[set], use))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
+            uint32_t h[32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) widen16(c[i], h + 8 * i);
             tmem_st16_async(slot, h);
             tmem_st16_async(slot + 16, h + 16);
 #pragma unroll
@@ -179,29 +177,32 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
             for (int i = 0; i < 4; ++i) widen16(c[4 + i], h + 8 * i);
             tmem_st16_async(slot + 32, h);
             tmem_st16_async(slot + 48, h + 16);
-            fence_proxy_async_smem();
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ready[set]);
+            // the next stage's codes on their way while these stores complete
             for (int i = 0; i < kSets; ++i)
                 if (++s == stages) {
                     s = 0;
                     phase ^= 1u;
                 }
+            have = it + kSets < n_kb && __all_sync(0xffffffffu, mbar_test(&full[s], phase));
+            if (have) fetch();
+            fence_proxy_async_smem();
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[set]);
         }
         // ---------------------------------------------------------------- sums out
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(done, 0)) != 0;
         if (ok) {
             tc_fence_after();
-            const int f = f0 + row, left = min(g.a.n_rows, g.N);
+            const int f = f0 + row;
             const float sw = f < g.a.n_out ? g.a.w_scale[f] : 0.f, bias = f < g.a.n_out && g.a.bias ? g.a.bias[f] : 0.f;
             for (int c = 32 * set; c < g.N; c += 64) {
                 float v[32];
                 tmem_ld32(dst + (uint32_t)c, v);
                 if (split == 1) {
-                    const float sx = c + lane < left ? g.a.x_scale[c + lane] : 0.f;
-                    write32(g.a, g.out_as, c, f, v, sx, sw, bias, left - c);
+                    const float sx = c + lane < rows ? g.a.x_scale[row0 + c + lane] : 0.f;
+                    write32(g.a, g.out_as, row0 + c, f, v, sx, sw, bias, rows - c);
                 } else {   // into the ring, which nothing uses any more: [N][128]
                     float* o = reinterpret_cast<float*>(smem) + c * 128 + row;
 #pragma unroll
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
     tc_fence_before();
     if (split > 1) {
         // a row of the tile a warp, four features a lane; this block's rows are [r0, r1)
-        const int f = f0 + 4 * lane, r0 = g.N * rank / split, r1 = min(g.N * (rank + 1) / split, g.a.n_rows);
+        const int f = f0 + 4 * lane, r0 = g.N * rank / split, r1 = min(g.N * (rank + 1) / split, rows);
         float sw[4], bias[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
         }
         cluster_sync();
         for (int r = r0 + warp; r < r1; r += kThreads / 32) {
-            const float sx = g.a.x_scale[r];
+            const float sx = g.a.x_scale[row0 + r];
             float4 v[8];
 #pragma unroll
             for (int p = 0; p < 8; ++p)
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
             float y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = (float)sum[i] * sx * sw[i] + bias[i];
-            write4(g.a, g.vec, r, f, y);
+            write4(g.a, g.vec, row0 + r, f, y);
         }
         cluster_sync();   // no block leaves while another reads its sums
     } else {
@@ -258,12 +259,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
 cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why) {
     LinearFew g{};
     g.a = a;
-    g.N = std::max(16, (a.n_rows + 15) / 16 * 16);
+    const int row_tiles = (a.n_rows + 63) / 64;
+    g.N = ((a.n_rows + row_tiles - 1) / row_tiles + 15) / 16 * 16;
     g.KB = (a.k + 127) / 128;
     const int tiles = (a.n_out + 127) / 128;
     // Blocks a cluster: as many as leave every block resident at once (two an SM).
     g.split = 1;
-    while (g.split < 8 && 2 * g.split * tiles <= 2 * kNumSMs && g.KB >= 8 * g.split) g.split *= 2;
+    while (g.split < 8 && 2 * g.split * tiles * row_tiles <= 2 * kNumSMs && g.KB >= 8 * g.split) g.split *= 2;
     const uint32_t tile = g.N * 128, stage = kStageA + tile;
     const uint32_t fixed = 1024 + 2 * kSets * tile + 512;   // the ring's size also holds the [N][128] sums
     // A multiple of the sets, so that a stage always belongs to the same one: a set that skipped a stage's earlier
@@ -278,7 +280,7 @@ cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why)
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(linear_few_kernel, kSmemMost, &done);
     if (e != cudaSuccess) return e;
-    return launch_clusters((unsigned)g.split, linear_few_kernel, dim3(tiles * g.split), dim3(kThreads),
+    return launch_clusters((unsigned)g.split, linear_few_kernel, dim3(tiles * g.split, row_tiles), dim3(kThreads),
                            fixed + (size_t)g.stages * stage, s, ta, tb, g);
 }
 

@@ -182,18 +182,26 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         mbar_init(cols_free, 8 * kOuts);
         mbar_init(all_done, 1);
         fence_mbar_init();
-        // no kernel of the call writes the weights: the ring's first ones go out while the block sets up
-        for (int it = 0; it < pre; ++it) {
-            int m, n;
-            tile_coords(g, pair + it / g.KB * g.pairs, &m, &n);
-            mbar_arrive_expect_tx(&full[it], stage_bytes);
-            load_a(it, m, it % g.KB);
-        }
     }
     if (warp == 1) pair_alloc(tmem_slot);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // the other CTA's barriers are initialised
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    if (threadIdx.x == 0) {
+        // no kernel of the call writes the weights: the ring's first ones go out while the other CTA sets up
+        prefetch_tmap(&tmB);
+        int tile = pair, kb = 0, m, n;
+        tile_coords(g, tile, &m, &n);
+        for (int it = 0; it < pre; ++it) {
+            mbar_arrive_expect_tx(&full[it], stage_bytes);
+            load_a(it, m, kb);
+            if (++kb == g.KB && it + 1 < pre) {
+                kb = 0;
+                tile_coords(g, tile += g.pairs, &m, &n);
+            }
+        }
+    }
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");   // the other CTA's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t slots = g.slots, lap = slots == 8 ? 3 : 2;   // chunk q: slot q % slots, its use number q >> lap
@@ -287,8 +295,8 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         // Every stage's and every slot's uses are one set's, in order, so that it can tell their phases apart.
         int s = 0, pending = -1;
         uint32_t phase = 0;
-        // A chunk is handed over when the next one's codes are in registers, so that its stores complete meanwhile,
-        // or at once where those have not come yet.
+        // A chunk is handed over when the next one is half widened, so that its stores complete meanwhile, or at once
+        // where that one's codes have not come.
         auto hand_over = [&]() {
             if (pending < 0) return;
             tmem_wait_st();
@@ -297,33 +305,43 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             if (lane == 0) arrive_leader(&a_ready[pending]);
             pending = -1;
         };
+        const uint32_t from = smem_u32(smem) + row * 128;
+        uint4 c[4];
+        auto fetch = [&](int stage) {
+            const uint32_t a = from + (uint32_t)stage * stage_bytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = lds128(a + (((4 * chunk + i) ^ (row & 7)) << 4));
+        };
         const int total = (g.tiles - pair + g.pairs - 1) / g.pairs * g.KB;
+        bool have = false;
         for (int it = 0; it < total; ++it) {
-            const int stage = s;
-            const uint32_t parity = phase, q = 2 * it + chunk, t = q & (slots - 1);
-            if (++s == stages) {
-                s = 0;
-                phase ^= 1u;
-            }
-            if (!__all_sync(0xffffffffu, mbar_test(&full[stage], parity))) {
+            const uint32_t q = 2 * it + chunk, t = q & (slots - 1);
+            if (!have) {
                 hand_over();
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], parity))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
                     ok = false;
                     break;
                 }
+                fetch(s);
             }
-            const uint8_t* a = smem + (size_t)stage * stage_bytes + row * 128;
-            uint32_t h[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                widen16(*reinterpret_cast<const uint4*>(a + (((4 * chunk + c) ^ (row & 7)) << 4)), h + 8 * c);
-            hand_over();
             if (!warp_wait(&a_free[t], ((q >> lap) & 1u) ^ 1u)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
+            uint32_t h[32];
+            widen16(c[0], h);
+            widen16(c[1], h + 8);
+            hand_over();
             tmem_st16_async(dst + 32 * t, h);
+            widen16(c[2], h + 16);
+            widen16(c[3], h + 24);
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1u;
+            }
+            have = it + 1 < total && __all_sync(0xffffffffu, mbar_test(&full[s], phase));
+            if (have) fetch(s);
             tmem_st16_async(dst + 32 * t + 16, h + 16);
             pending = (int)t;
         }
