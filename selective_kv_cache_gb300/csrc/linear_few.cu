@@ -2,7 +2,8 @@
 // on the sm_103a tensor cores, in one launch:
 //   y[r][f] = s_r t_f sum_k a[r][k] w[f][k] + bias[f]
 //
-// HBM-bound: the weights come in once, 128 features by up to 64 rows a block.
+// HBM-bound: the weights come in once, 128 features by up to 64 rows a block
+// (more rows: as many blocks side by side, the weights then from L2).
 // Both operands are widened to fp16 on the way (8-bit integers, their products
 // and the fp32 sums up to 2^24 are exact): the weights into tensor memory, the A
 // operand, the rows into shared memory.  A cluster's blocks split k, and join
@@ -136,13 +137,23 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
         int s = set % stages;
         uint32_t phase = (uint32_t)(set / stages) & 1u, use = 1;
         uint4 c[8], b[4];
-        auto fetch = [&]() {   // and give the stage back
+        auto fetch = [&]() {
             const uint32_t at = (uint32_t)s * stage_bytes;
 #pragma unroll
             for (int i = 0; i < 8; ++i) c[i] = lds128(from + at + ((i ^ (row & 7)) << 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (16 * i < g.N) b[i] = lds128(from_b + at + 2048 * i);
+                b[i] = 16 * i < g.N ? lds128(from_b + at + 2048 * i) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        // A word of every vector is looked at before the stage goes back: an arrival does not wait for loads whose
+        // values nothing has used, and the copy that it allows would overtake them.
+        auto give_back = [&]() {
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) seen ^= c[i].w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) seen ^= b[i].w;
+            asm volatile("" ::"r"(seen) : "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
         };
@@ -154,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
                     break;
                 }
                 fetch();
+                give_back();
             }
             if (!__all_sync(0xffffffffu, mbar_wait(&freed[set], use))) {
                 ok = false;
@@ -190,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ready[set]);
+            if (have) give_back();
         }
         // ---------------------------------------------------------------- sums out
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(done, 0)) != 0;
@@ -256,16 +269,39 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
 
 }  // namespace
 
+namespace {
+struct Plan {
+    int row_tiles, N, tiles, KB, split, waves;
+};
+Plan make_plan(int n_out, int k, int n_rows) {
+    Plan p{};
+    p.row_tiles = (n_rows + 63) / 64;
+    p.N = ((n_rows + p.row_tiles - 1) / p.row_tiles + 15) / 16 * 16;
+    p.tiles = (n_out + 127) / 128;
+    p.KB = (k + 127) / 128;
+    const long long blocks = (long long)p.tiles * p.row_tiles;
+    // Blocks a cluster: as many as leave every block resident at once (two an SM).  28672 features, 17 rows: 25 us
+    // alone, 30 in twos, which a second wave follows; 6144 features: 15 alone, 11.4 in fours.  Threes and sixes
+    // fit the GPCs badly.
+    p.split = 1;
+    while (p.split < 8 && 2 * p.split * blocks <= 2 * kNumSMs && p.KB >= 8 * p.split) p.split *= 2;
+    p.waves = (int)std::min<long long>(1 << 20, (blocks * p.split + 2 * kNumSMs - 1) / (2 * kNumSMs));
+    return p;
+}
+}  // namespace
+
+double linear_few_us(int n_out, int k, int n_rows) {
+    const Plan p = make_plan(n_out, k, n_rows);
+    return 9.5 + 0.72 * p.waves * ((p.KB + p.split - 1) / p.split);
+}
+
 cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why) {
+    const Plan p = make_plan(a.n_out, a.k, a.n_rows);
     LinearFew g{};
     g.a = a;
-    const int row_tiles = (a.n_rows + 63) / 64;
-    g.N = ((a.n_rows + row_tiles - 1) / row_tiles + 15) / 16 * 16;
-    g.KB = (a.k + 127) / 128;
-    const int tiles = (a.n_out + 127) / 128;
-    // Blocks a cluster: as many as leave every block resident at once (two an SM).
-    g.split = 1;
-    while (g.split < 8 && 2 * g.split * tiles * row_tiles <= 2 * kNumSMs && g.KB >= 8 * g.split) g.split *= 2;
+    g.N = p.N;
+    g.KB = p.KB;
+    g.split = p.split;
     const uint32_t tile = g.N * 128, stage = kStageA + tile;
     const uint32_t fixed = 1024 + 2 * kSets * tile + 512;   // the ring's size also holds the [N][128] sums
     // A multiple of the sets, so that a stage always belongs to the same one: a set that skipped a stage's earlier
@@ -280,7 +316,7 @@ cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why)
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(linear_few_kernel, kSmemMost, &done);
     if (e != cudaSuccess) return e;
-    return launch_clusters((unsigned)g.split, linear_few_kernel, dim3(tiles * g.split, row_tiles), dim3(kThreads),
+    return launch_clusters((unsigned)g.split, linear_few_kernel, dim3(p.tiles * p.split, p.row_tiles), dim3(kThreads),
                            fixed + (size_t)g.stages * stage, s, ta, tb, g);
 }
 

@@ -19,6 +19,7 @@ namespace kvr {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kRows = kLinearMmaRows, kUnroll = 4;   // rows of a block; 64-byte steps a warp has in flight
 constexpr int kMT = 2, kFeatures = 16 * kMT;   // weight tiles of a warp, features of a block
 
 __device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -40,35 +41,29 @@ __device__ __forceinline__ uint4 load_tail(const int8_t* p, int left) {
         if (i < left) w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// kNT: groups of eight rows a block takes; kUnroll: steps in flight a warp.
-template <int kNT, int kUnroll>
 __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ Linear a, int split) {
-    constexpr int kRows = 8 * kNT, kTile = kFeatures * kRows;
+    constexpr int kTile = kFeatures * kRows;
     __shared__ int part[kWarps][kTile];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int rank = (int)blockIdx.x % split, f0 = (int)blockIdx.x / split * kFeatures, r0 = blockIdx.y * kRows;
+    const int rank = (int)blockIdx.x % split, f0 = (int)blockIdx.x / split * kFeatures;
     // rows past the end are read as the last one and not written
     const int8_t* wp[kMT][2];
-    const int8_t* xp[kNT];
 #pragma unroll
     for (int m = 0; m < kMT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) wp[m][h] = a.w + (int64_t)min(f0 + 16 * m + 8 * h + g, a.n_out - 1) * a.w_stride + 16 * t;
+    const int8_t* xp = a.x + (int64_t)min(g, a.n_rows - 1) * a.x_stride + 16 * t;
+    int acc[kMT][4] = {};
+    auto products = [&](const uint4 (&w)[kMT][2], uint4 x) {
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) xp[n] = a.x + (int64_t)min(r0 + 8 * n + g, a.n_rows - 1) * a.x_stride + 16 * t;
-    int acc[kMT][kNT][4] = {};
-    auto products = [&](const uint4 (&w)[kMT][2], const uint4 (&x)[kNT]) {
-#pragma unroll
-        for (int m = 0; m < kMT; ++m)
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-                mma_s8(acc[m][n], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[n].x, x[n].y);
-                mma_s8(acc[m][n], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[n].z, x[n].w);
-            }
+        for (int m = 0; m < kMT; ++m) {
+            mma_s8(acc[m], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x.x, x.y);
+            mma_s8(acc[m], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x.z, x.w);
+        }
     };
     const int steps = a.k / 64, stride = kWarps * split;
     for (int s = rank * kWarps + warp; s < steps; s += stride * kUnroll) {
-        uint4 w[kUnroll][kMT][2], x[kUnroll][kNT];
+        uint4 w[kUnroll][kMT][2], x[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int at = 64 * min(s + u * stride, steps - 1);   // a step past the end is loaded, not used
@@ -76,8 +71,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
             for (int m = 0; m < kMT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) w[u][m][h] = load_stream(wp[m][h] + at);
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) x[u][n] = *reinterpret_cast<const uint4*>(xp[n] + at);
+            x[u] = *reinterpret_cast<const uint4*>(xp + at);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
@@ -85,22 +79,18 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
     }
     if (rank == split - 1 && warp == kWarps - 1 && a.k % 64) {
         const int at = 64 * steps, left = a.k - at - 16 * t;
-        uint4 w[kMT][2], x[kNT];
+        uint4 w[kMT][2];
 #pragma unroll
         for (int m = 0; m < kMT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) w[m][h] = load_tail(wp[m][h] + at, left);
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) x[n] = load_tail(xp[n] + at, left);
-        products(w, x);
+        products(w, load_tail(xp + at, left));
     }
 #pragma unroll
     for (int m = 0; m < kMT; ++m)
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)   // row 2 t + i % 2 of the group, feature g + 8 (i / 2) of the tile
-                part[warp][(8 * n + 2 * t + (i & 1)) * kFeatures + 16 * m + g + 8 * (i >> 1)] = acc[m][n][i];
+        for (int i = 0; i < 4; ++i)   // row 2 t + i % 2, feature g + 8 (i / 2) of the tile
+            part[warp][(2 * t + (i & 1)) * kFeatures + 16 * m + g + 8 * (i >> 1)] = acc[m][i];
     __syncthreads();
     for (int i = threadIdx.x; i < kTile; i += kThreads) {
         int v = 0;
@@ -112,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
     else __syncthreads();
     // each block of the cluster finishes its share of the tile
     for (int i = rank * kThreads + threadIdx.x; i < kTile; i += split * kThreads) {
-        const int r = r0 + i / kFeatures, f = f0 + i % kFeatures;
+        const int r = i / kFeatures, f = f0 + i % kFeatures;
         int v = part[0][i];
         for (int p = 1; p < split; ++p) v += load_peer(peer_address(&part[0][i], (rank + p) % split));
         if (r >= a.n_rows || f >= a.n_out) continue;
@@ -128,11 +118,7 @@ cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s) {
     // blocks for every SM twice over, as long as a warp has a batch of steps
     int split = 1;
     while (split < 8 && groups * split < 2 * kNumSMs && steps >= 2 * split * kWarps * 2) split *= 2;
-    auto go = [&](auto kernel, int rows) {
-        return launch_clusters(split, kernel, dim3(groups * split, (a.n_rows + rows - 1) / rows), dim3(kThreads), 0, s, a,
-                               split);
-    };
-    return a.n_rows <= 8 ? go(linear_mma_kernel<1, 4>, 8) : go(linear_mma_kernel<2, 4>, 16);
+    return launch_clusters(split, linear_mma_kernel, dim3(groups * split), dim3(kThreads), 0, s, a, split);
 }
 
 }  // namespace kvr

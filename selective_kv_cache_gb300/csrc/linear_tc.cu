@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
 
 struct Plan {
     int N, m_tiles, n_tiles, KB, stages, pitch, tiles, pairs;
+    double cycles;
 };
 // The width of a tile that takes the shortest time in cycles: a stage of 128
 // codes takes its products' 4 N, or what the widening takes; a tile's end stops
@@ -412,12 +413,13 @@ Plan make_plan(int n_out, int k, int n_rows) {
     for (int N = 32; N <= 256; N += 32) {
         const int n_tiles = (n_rows + N - 1) / N;
         const long long turns = ((long long)p.m_tiles * n_tiles + kPairs - 1) / kPairs;
-        const double t = (double)turns * (p.KB * std::max(800.0, 4.05 * N) + (N > 192 ? 4000 : 0)) + 20.0 * N;
+        const double t = (double)turns * (p.KB * std::max(650.0, 4.05 * N) + (N > 192 ? 4000 : 0)) + 20.0 * N;
         if (t >= least) continue;
         least = t;
         p.N = N;
         p.n_tiles = n_tiles;
     }
+    p.cycles = least;
     p.tiles = p.m_tiles * p.n_tiles;
     p.pairs = std::min(kPairs, p.tiles);
     p.stages = std::min(12, (kSmemMost - 2048) / ((int)kStageA + p.N * 128));
@@ -425,6 +427,8 @@ Plan make_plan(int n_out, int k, int n_rows) {
 }
 
 }  // namespace
+
+double linear_tc_us(int n_out, int k, int n_rows) { return 7.0 + make_plan(n_out, k, n_rows).cycles / 1900; }
 
 size_t linear_tc_workspace(int n_out, int k, int n_rows) {
     return (size_t)n_rows * make_plan(n_out, k, n_rows).pitch * 2;

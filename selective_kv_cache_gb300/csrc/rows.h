@@ -47,12 +47,13 @@ struct Linear {
     int* err;
     void* workspace;
 };
-// up to these rows the integer kernel takes a call, then the one for a batch's rows
-constexpr int kLinearMmaRows = 16, kLinearFewRows = 64;
+constexpr int kLinearMmaRows = 8;   // up to these rows the integer kernel takes a call
 cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s);
 
+double linear_few_us(int n_out, int k, int n_rows);   // estimated time
 cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why);
 // Many rows; needs linear_tc_workspace bytes of workspace.
+double linear_tc_us(int n_out, int k, int n_rows);
 size_t linear_tc_workspace(int n_out, int k, int n_rows);
 cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why);
 

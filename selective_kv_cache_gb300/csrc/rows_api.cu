@@ -59,8 +59,29 @@ kvr_status check_weights(const kvr_linear_weights* w) {
         return fail(KVR_EINVAL, "weights: scales, bias and err must be aligned, scales and err not NULL");
     return KVR_OK;
 }
+// Which kernel a call takes, measured on GB300 with weights from HBM (us):
+//   rows x k -> n_out        integer    batch    tiles
+//    8 x  4096 ->  6144          8.6     11.0     17.4
+//    8 x  4096 -> 28672         23.8     25.6     31.4
+//    9 x  4096 ->  6144         12.0     11.0     17.4
+//   16 x 14336 ->  4096         25.1     15.8     42.1
+//   64 x  4096 ->  6144                  13.9     17.7
+//   64 x  4096 -> 28672                  32.8     32.3
+//   64 x 14336 ->  4096                  20.8     42.5
+//  128 x  4096 ->  6144                  20.3     17.7
+//  128 x 14336 ->  4096                  30.2     43.2
+//  256 x  8960 ->  1536                  21.3     29.9
+//  512 x  8960 ->  1536                  33.9     31.0
+// Above 64 rows the batch kernel reads the weights once for every 64 of them,
+// and splits k where the tiles are few: the two estimates decide.
+enum class LinearWay { Mma, Few, Tc };
+LinearWay linear_way(int n_out, int k, int n_rows) {
+    if (n_rows <= kLinearMmaRows) return LinearWay::Mma;
+    if (n_rows <= 64) return LinearWay::Few;
+    return linear_few_us(n_out, k, n_rows) < linear_tc_us(n_out, k, n_rows) ? LinearWay::Few : LinearWay::Tc;
+}
 size_t linear_workspace(const kvr_linear_weights& w, int32_t n_rows) {
-    return n_rows <= kLinearFewRows ? 256 : linear_tc_workspace(w.n_out, w.k, n_rows);
+    return linear_way(w.n_out, w.k, n_rows) == LinearWay::Tc ? linear_tc_workspace(w.n_out, w.k, n_rows) : 256;
 }
 
 kvr_status check_rope(const kvr_rope* r) {
@@ -314,13 +335,14 @@ kvr_status kvr_linear(const kvr_linear_weights* w, int32_t n_rows, const int8_t*
     a.err = w->err;
     a.workspace = workspace;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (n_rows <= kLinearMmaRows) {
-        KVR_CHECK_LAUNCH(launch_linear_mma(a, s), "linear");
-        return KVR_OK;
-    }
     std::string why;
-    KVR_CHECK_LAUNCH(n_rows <= kLinearFewRows ? launch_linear_few(a, s, &why) : launch_linear_tc(a, s, &why),
-                     ("linear " + why).c_str());
+    cudaError_t e = cudaSuccess;
+    switch (linear_way(w->n_out, w->k, n_rows)) {
+        case LinearWay::Mma: e = launch_linear_mma(a, s); break;
+        case LinearWay::Few: e = launch_linear_few(a, s, &why); break;
+        case LinearWay::Tc: e = launch_linear_tc(a, s, &why); break;
+    }
+    if (e != cudaSuccess) return cuda_fail(e, ("linear " + why).c_str());
     return KVR_OK;
 }
 
