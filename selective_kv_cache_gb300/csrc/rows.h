@@ -6,6 +6,22 @@
 
 namespace kvr {
 
+// Quotients by a divisor of a launch, for numerators below 2^31: umulhi with
+// ceil(2^(31 + l) / d), l = ceil(log2 d), and a shift by l - 1.
+struct Div {
+    uint32_t d, mul, shift;
+    explicit Div(uint32_t n) : d(n), mul(0), shift(0) {
+        if (n == 1) return;
+        uint32_t l = 0;
+        while ((1u << l) < n) ++l;
+        mul = (uint32_t)(((uint64_t(1) << (31 + l)) + n - 1) / n);
+        shift = l - 1;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return d == 1 ? x : __umulhi(x, mul) >> shift; }
+#endif
+};
+
 enum class RowOp { Norm, Swiglu, Quantise };
 
 struct RowsQuant {
@@ -19,6 +35,7 @@ struct RowsQuant {
     int64_t x_stride, res_stride, sum_stride, out_stride, code_stride;   // elements
     int n_rows, d;
     float eps;
+    int codes_aligned;      // set by the launcher
 };
 cudaError_t launch_rows_quant(RowOp op, int dtype, const RowsQuant& a, cudaStream_t s);
 cudaError_t launch_rows_dequantise(int dtype, int n_rows, int d, const int8_t* codes, int64_t code_stride,

@@ -7,11 +7,18 @@
 // so the sum of squares and the maximum are found in one pass and one
 // exchange, and nothing waits for r but the scale.
 //
-// HBM-bound: every byte moves once.  A group of threads holds a row in
-// registers (up to 32 values a thread, unrounded) between its loads and its
-// stores; rows wider than 1024 threads hold are read twice.  Maxima are taken
-// on the bits of |y| as unsigned numbers, where NaN lies above infinity: a row
-// that is not finite shows in its maximum.
+// HBM-bound: every byte moves once.  A warp or a block holds a row in registers
+// between its loads and its stores, and has the next row's on their way
+// meanwhile; rows wider than a block's registers are read twice.  A thread's
+// unit is eight elements.  Rows that do not begin on 16 bytes, and widths that
+// are not a multiple of eight, move in aligned 16-byte pieces all the same: a
+// unit is shifted out of the pieces that hold it, and on the way out lanes
+// hand the bytes of a piece to the lane that writes it.
+// Instructions count as much as bytes (a row of 1536 in bf16 has 28 of them an
+// element to spare at HBM's rate), so a thread has many elements, and a norm's
+// sum leaves as soon as it is formed, which leaves h w alone to be kept.
+// Maxima hand NaN on, and meet as unsigned numbers, where NaN lies above
+// infinity: a row that is not finite shows in its maximum.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -23,53 +30,133 @@ namespace {
 
 constexpr float kTiny = 1.17549435e-38f;   // 2^-126
 
+// words of a unit of eight elements
 template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+constexpr int kWords = 2 * (int)sizeof(T);
 
-// V consecutive elements at p as fp32: vectors of 16 bytes where V = 8
-template <typename T, int V>
-__device__ __forceinline__ void load(const T* p, float* x) {
-    if constexpr (V == 1) {
-        x[0] = to_f<T>(*p);
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 16 bytes of lo | hi from byte `at` on, 0 < at < 16 a multiple of the element's size
+__device__ __forceinline__ void shifted(const uint32_t* lo, const uint32_t* hi, uint32_t at, uint32_t* out) {
+    uint32_t w[7];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) w[i] = lo[i];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) w[4 + i] = hi[i];
+    uint32_t last = hi[3];
+    if (at & 8) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
+        w[5] = last;
+    }
+    if (at & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = 8 * (at & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], bits);
+}
+
+// n of a unit's eight elements (0 to 8) at p.
+template <typename T, bool kAligned>
+__device__ __forceinline__ void load_unit(const T* p, int n, uint32_t* w) {
+    constexpr int kPieces = kWords<T> / 4;
+    if constexpr (kAligned) {
+        if (n > 0) {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) reinterpret_cast<uint4*>(w)[k] = reinterpret_cast<const uint4*>(p)[k];
+        }
+    } else {
+        // aligned pieces, those that hold an element of the unit: they share its 16 bytes, so nothing else is touched
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+        uint32_t c[4 * (kPieces + 1)];
+#pragma unroll
+        for (int k = 0; k <= kPieces; ++k)
+            reinterpret_cast<uint4*>(c)[k] = 16 * k < (int)(n * sizeof(T) + off) && n > 0 ? from[k] : make_uint4(0u, 0u, 0u, 0u);
+        if (off == 0) {
+#pragma unroll
+            for (int k = 0; k < 4 * kPieces; ++k) w[k] = c[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) shifted(c + 4 * k, c + 4 * k + 4, off, w + 4 * k);
         }
     }
 }
-template <typename T, int V>
-__device__ __forceinline__ void store(T* p, const float* x) {
-    if constexpr (V == 1) {
-        *p = from_f<T>(x[0]);
-    } else if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+
+template <typename T>
+__device__ __forceinline__ void store_one(T* p, const uint32_t* w, int e) {   // element e of a unit's words
+    if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<uint32_t*>(p)[e] = w[e];
     } else {
-        uint32_t w[4];
+        reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+// The same way out; consecutive lanes hold consecutive units, all lanes of the warp call.
+template <typename T, bool kAligned>
+__device__ __forceinline__ void store_unit(T* p, int n, const uint32_t* w) {
+    constexpr int kPieces = kWords<T> / 4, E = 16 / (int)sizeof(T);   // elements of a piece
+    if constexpr (kAligned) {
+        if (n > 0) {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) reinterpret_cast<uint4*>(p)[k] = reinterpret_cast<const uint4*>(w)[k];
+        }
+    } else {
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;   // one for all units of a row
+        const int lane = threadIdx.x & 31, head = off ? (int)(16 - off) / (int)sizeof(T) : 0;   // elements before a border
+        uint32_t next[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+        int n_next = __shfl_down_sync(0xffffffffu, n, 1);
+        if (lane == 31) n_next = 0;
+        // piece k begins `head` elements into the unit's k-th 16 bytes; the last takes the next lane's first elements
+        const bool last = n == 8 && n_next >= head;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            uint32_t c[4];
+            const uint32_t* hi = k + 1 < kPieces ? w + 4 * k + 4 : next;
+            if (off) {
+                shifted(w + 4 * k, hi, 16 - off, c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] = w[4 * k + i];
+            }
+            const int first = k * E + head;
+            if (k + 1 < kPieces ? n >= first + E : last) {
+                *reinterpret_cast<uint4*>(p + first) = make_uint4(c[0], c[1], c[2], c[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e >= first && e < n && e < first + E) store_one(p, w, e);
+            }
+        }
+        const bool taken = __shfl_up_sync(0xffffffffu, (int)last, 1) != 0 && lane > 0;
+        if (!taken) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < head && e < n) store_one(p, w, e);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint32_t* w, float* x) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(w[i]);
+        else x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void pack(const float* x, uint32_t* w) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -78,19 +165,20 @@ __device__ __forceinline__ void store(T* p, const float* x) {
 __device__ __forceinline__ uint32_t code_bits(float y, float inv) {
     return __float_as_uint(fmaf(y, inv, 12582912.f));
 }
-template <int V>
-__device__ __forceinline__ void store_codes(int8_t* p, const float* y, float inv, bool bad) {
-    if constexpr (V == 1) {
-        *p = bad ? (int8_t)0 : (int8_t)(code_bits(y[0], inv) & 0xffu);
-    } else {
-        uint32_t w[2];
+__device__ __forceinline__ void store_codes(int8_t* p, int n, const float* y, float inv, bool bad, bool whole) {
+    uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = __byte_perm(code_bits(y[4 * i], inv), code_bits(y[4 * i + 1], inv), 0x0040);
-            const uint32_t hi = __byte_perm(code_bits(y[4 * i + 2], inv), code_bits(y[4 * i + 3], inv), 0x0040);
-            w[i] = bad ? 0u : __byte_perm(lo, hi, 0x5410);
-        }
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __byte_perm(code_bits(y[4 * i], inv), code_bits(y[4 * i + 1], inv), 0x0040);
+        const uint32_t hi = __byte_perm(code_bits(y[4 * i + 2], inv), code_bits(y[4 * i + 3], inv), 0x0040);
+        w[i] = bad ? 0u : __byte_perm(lo, hi, 0x5410);
+    }
+    if (whole && n == 8) {   // whole: the codes' units are 8-byte aligned
         *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) p[e] = (int8_t)(w[e / 4] >> (8 * (e % 4)));
     }
 }
 
@@ -102,195 +190,291 @@ __device__ __forceinline__ float gated(float g, float u) {
     return __fdividef(g, 1.f + __expf(-g)) * u;
 }
 
-// The V values at element i of a row, as the row's operator has them before
-// the quantiser: h (norm, the sum of x and residual), the gated value, or x.
-template <RowOp kOp, typename T, int V>
-__device__ __forceinline__ void row_values(const RowsQuant& a, const T* x, const T* res, int i, float* v) {
-    load<T, V>(x + i, v);
-    if constexpr (kOp == RowOp::Norm) {
-        if (res) {
-            float r[V];
-            load<T, V>(res + i, r);
+// What a thread reads of one unit: the row's, and the residual's or the up half's.
+template <RowOp kOp, typename T, bool kAligned>
+struct Unit {
+    uint32_t a[kWords<T>], b[kOp == RowOp::Quantise ? 1 : kWords<T>];
+    __device__ __forceinline__ void load(const RowsQuant& q, int64_t row, int i, int n) {
+        const T* x = reinterpret_cast<const T*>(q.x) + row * q.x_stride + i;
+        load_unit<T, kAligned>(x, n, a);
+        if constexpr (kOp == RowOp::Norm) {
+            if (q.res) load_unit<T, kAligned>(reinterpret_cast<const T*>(q.res) + row * q.res_stride + i, n, b);
+        }
+        if constexpr (kOp == RowOp::Swiglu) load_unit<T, kAligned>(x + q.d, n, b);
+    }
+    // the values before the quantiser: h (norm), the gated value, or x
+    __device__ __forceinline__ void values(const RowsQuant& q, float* v) const {
+        unpack<T>(a, v);
+        if constexpr (kOp != RowOp::Quantise) {
+            if (kOp == RowOp::Swiglu || q.res) {
+                float o[8];
+                unpack<T>(b, o);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] += r[e];
+                for (int e = 0; e < 8; ++e) v[e] = kOp == RowOp::Swiglu ? gated<T>(v[e], o[e]) : v[e] + o[e];
+            }
         }
     }
-    if constexpr (kOp == RowOp::Swiglu) {
-        float u[V];
-        load<T, V>(x + a.d + i, u);
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = gated<T>(v[e], u[e]);
-    }
+};
+
+// max(|a|, |b|, c), NaN if one of them is
+__device__ __forceinline__ float top3(float a, float b, float c) {
+    float d;
+    asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %1;\n\tabs.f32 y, %2;\n\tmax.NaN.f32 %0, x, y, %3;\n\t}" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
-// Sum and maximum over the threads of a row's group: a warp by itself, or the
-// whole block.
+// Sum and maximum over the threads of a row: a warp by itself, or the whole
+// block, through slot `turn` of two.
 template <bool kWarp, bool kSum>
-__device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
+__device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int turn) {
     top = __reduce_max_sync(0xffffffffu, top);
     if constexpr (kSum) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     if constexpr (!kWarp) {
-        __shared__ float sums[32];
-        __shared__ uint32_t tops[32];
+        __shared__ float sums[2][32];
+        __shared__ uint32_t tops[2][32];
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
         if (lane == 0) {
-            sums[warp] = sum;
-            tops[warp] = top;
+            sums[turn][warp] = sum;
+            tops[turn][warp] = top;
         }
         __syncthreads();
-        top = __reduce_max_sync(0xffffffffu, lane < n ? tops[lane] : 0u);
+        top = __reduce_max_sync(0xffffffffu, lane < n ? tops[turn][lane] : 0u);
         if constexpr (kSum) {
-            sum = lane < n ? sums[lane] : 0.f;
+            sum = lane < n ? sums[turn][lane] : 0.f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
     }
 }
 
-// kV: 8 (vectors) or 1; kSlots: groups of kV values a thread holds, 0: the row
-// is read twice.  kWarp: a warp a row, several rows a block; else a block a row.
-constexpr int block_most(int values, bool warp) {
-    return warp ? 128 : values == 8 ? 256 : values == 16 ? 512 : 1024;
+// Threads of a block at most, and blocks an SM at least.  Rows of bf16 leave
+// registers for the next row's units beside this one's.
+constexpr int block_most(int slots, bool warp, int size) {
+    return warp ? 128 : slots == 1 ? 256 : slots == 2 ? 512 : slots == 4 && size == 2 ? 640 : 1024;
 }
-template <RowOp kOp, typename T, int kV, int kSlots, bool kWarp>
-__global__ void __launch_bounds__(block_most(kV * kSlots, kWarp)) rows_quant_kernel(const __grid_constant__ RowsQuant a) {
+constexpr int blocks_least(int slots, bool warp, int size, bool aligned) {
+    return warp ? (slots == 1 ? 8 : 5) : slots == 1 ? 4 : slots == 2 && size == 2 && aligned ? 2 : 1;
+}
+
+// kSlots: units a thread holds of a row, 0: the row is read twice.  kWarp: a
+// warp a row, several rows a block; else a block a row.
+template <RowOp kOp, typename T, bool kAligned, int kSlots, bool kWarp>
+__global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T)), blocks_least(kSlots, kWarp, sizeof(T), kAligned))
+    rows_quant_kernel(const __grid_constant__ RowsQuant a) {
     constexpr bool kNorm = kOp == RowOp::Norm;
-    // 32 values a thread leave no registers for their weights, which are read again (from L1)
-    constexpr bool kKeepW = kNorm && kSlots > 0 && kSlots * kV <= 16;
-    const int lane = kWarp ? threadIdx.x & 31 : threadIdx.x, step = (kWarp ? 32 : blockDim.x) * kV;
-    const int64_t row = kWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-    if (row >= a.n_rows) return;
-    const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
-    const T* res = kNorm && a.res ? reinterpret_cast<const T*>(a.res) + row * a.res_stride : nullptr;
-    const T* weight = reinterpret_cast<const T*>(a.weight);
+    // the next row's loads go out before this one's exchange
+    constexpr bool kAhead = kSlots > 0 && sizeof(T) == 2;
+    constexpr bool kKeepW = kNorm && (kSlots == 1 || kSlots == 2);   // else the weights are read for every row, from L1
     constexpr int kHold = kSlots > 0 ? kSlots : 1;
-    float v[kHold][kV], w[kKeepW ? kHold : 1][kV];
-    float sum = 0.f;
-    uint32_t top = 0u;
-    auto take = [&](const float* h, const float* wt) {
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            if constexpr (kNorm) sum = fmaf(h[e], h[e], sum);
-            top = max(top, __float_as_uint(kNorm ? h[e] * wt[e] : h[e]) & 0x7fffffffu);
-        }
+    const int lane = kWarp ? threadIdx.x & 31 : threadIdx.x, step = kWarp ? 32 : blockDim.x;
+    const int64_t per_block = kWarp ? blockDim.x >> 5 : 1, stride = gridDim.x * per_block;
+    int64_t row = blockIdx.x * per_block + (kWarp ? threadIdx.x >> 5 : 0);
+    const T* weight = reinterpret_cast<const T*>(a.weight);
+    auto count = [&](int k) { return min(8, max(0, a.d - 8 * (lane + k * step))); };
+    float wt[kKeepW ? kHold : 1][8];
+    auto load_weight = [&](int k, float* w) {
+        uint32_t raw[kWords<T>];
+        load_unit<T, kAligned>(weight + 8 * (lane + k * step), count(k), raw);
+        unpack<T>(raw, w);
     };
-    if constexpr (kSlots > 0) {
+    if constexpr (kKeepW) {
 #pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-            const int i = lane * kV + k * step;
-            if (i < a.d) {
-                row_values<kOp, T, kV>(a, x, res, i, v[k]);
-                if constexpr (kKeepW) load<T, kV>(weight + i, w[k]);
-            }
-        }
+        for (int k = 0; k < kHold; ++k) load_weight(k, wt[k]);
+    }
+    Unit<kOp, T, kAligned> u[kAhead ? kHold : 1];
+    if constexpr (kAhead) {
+        if (row < a.n_rows) {
 #pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-            const int i = lane * kV + k * step;
-            if (i < a.d) {
-                if constexpr (kNorm && !kKeepW) load<T, kV>(weight + i, w[0]);
-                take(v[k], w[kKeepW ? k : 0]);
-            }
-        }
-    } else {
-        for (int i = lane * kV; i < a.d; i += step) {
-            row_values<kOp, T, kV>(a, x, res, i, v[0]);
-            if constexpr (kNorm) load<T, kV>(weight + i, w[0]);
-            take(v[0], w[0]);
+            for (int k = 0; k < kHold; ++k) u[k].load(a, row, 8 * (lane + k * step), count(k));
         }
     }
-    row_reduce<kWarp, kNorm>(sum, top);
-    const float r = kNorm ? rsqrtf(sum / (float)a.d + a.eps) : 1.f;
-    const bool bad = top >= 0x7f800000u || (kNorm && !(r <= 3.4028234e38f));
-    // of the values before r: r lies in the scale alone
-    const float s0 = __uint_as_float(top) * (1.f / 127.f);
-    const float scale = kNorm ? s0 * r : s0;
-    const bool none = !bad && (s0 < kTiny || scale < kTiny);
-    const float inv = bad || none ? 0.f : 1.f / s0;
-    if (a.codes && lane == 0) a.scales[row] = bad ? __int_as_float(0x7fffffff) : none ? 0.f : scale;
-    auto put = [&](int i, const float* h, const float* wt) {
-        float y[kV];
-#pragma unroll
-        for (int e = 0; e < kV; ++e) y[e] = kNorm ? h[e] * wt[e] : h[e];
-        if (a.codes) store_codes<kV>(a.codes + row * a.code_stride + i, y, inv, bad);
-        if constexpr (kNorm) {
-            if (a.sum) store<T, kV>(reinterpret_cast<T*>(a.sum) + row * a.sum_stride + i, h);
-        }
-        if (a.out) {
+    for (int turn = 0; row < a.n_rows; row += stride, turn ^= 1) {
+        float v[kHold][8];   // h w, or the value
+        float sum = 0.f, top = 0.f;
+        // Unit k of the row into v; `first`: for the statistics, with the sum on its way out.  Outputs may be inputs:
+        // a unit is written by its own warp, from what its lanes have read by then.
+        auto take = [&](int k, const Unit<kOp, T, kAligned>& from, float* v, bool first) {
+            const int n = count(k);
+            from.values(a, v);
             if constexpr (kNorm) {
-#pragma unroll
-                for (int e = 0; e < kV; ++e) y[e] = h[e] * r * wt[e];
+                if (a.sum && (kSlots > 0 || !first)) {   // a row that is read twice: in the second reading
+                    uint32_t o[kWords<T>];
+                    pack<T>(v, o);
+                    if constexpr (!kAligned) __syncwarp();
+                    store_unit<T, kAligned>(reinterpret_cast<T*>(a.sum) + row * a.sum_stride + 8 * (lane + k * step), n, o);
+                }
             }
-            store<T, kV>(reinterpret_cast<T*>(a.out) + row * a.out_stride + i, y);
-        }
-    };
-    if constexpr (kSlots > 0) {
+            if (n > 0) {
+                if constexpr (!kAligned) {
 #pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-            const int i = lane * kV + k * step;
-            if (i < a.d) {
-                if constexpr (kNorm && !kKeepW) load<T, kV>(weight + i, w[0]);
-                put(i, v[k], w[kKeepW ? k : 0]);
+                    for (int e = 0; e < 8; ++e)
+                        if (e >= n) v[e] = 0.f;
+                }
+                if constexpr (kNorm) {
+                    float* w = wt[kKeepW ? k : 0];
+                    if constexpr (!kKeepW) load_weight(k, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        sum = fmaf(v[e], v[e], sum);
+                        v[e] = kAligned || e < n ? v[e] * w[e] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) top = top3(v[e], v[e + 1], top);
+            }
+        };
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) take(k, u[k], v[k], true);
+            if (row + stride < a.n_rows) {
+#pragma unroll
+                for (int k = 0; k < kHold; ++k) u[k].load(a, row + stride, 8 * (lane + k * step), count(k));
+            }
+        } else if constexpr (kSlots > 0) {
+            // two units' loads together, as many as registers hold
+            constexpr int kTogether = kSlots < 2 ? 1 : 2;
+#pragma unroll
+            for (int k0 = 0; k0 < kHold; k0 += kTogether) {
+                Unit<kOp, T, kAligned> now[kTogether];
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) now[k].load(a, row, 8 * (lane + (k0 + k) * step), count(k0 + k));
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) take(k0 + k, now[k], v[k0 + k], true);
+            }
+        } else {
+            for (int k = 0; 8 * (k * step) < a.d; ++k) {
+                u[0].load(a, row, 8 * (lane + k * step), count(k));
+                take(k, u[0], v[0], true);
             }
         }
-    } else {
-        // a thread writes only the elements that it has just read, so outputs may be inputs
-        for (int i = lane * kV; i < a.d; i += step) {
-            row_values<kOp, T, kV>(a, x, res, i, v[0]);
-            if constexpr (kNorm) load<T, kV>(weight + i, w[0]);
-            put(i, v[0], w[0]);
+        uint32_t top_bits = __float_as_uint(top);
+        row_reduce<kWarp, kNorm>(sum, top_bits, turn);
+        const float r = kNorm ? rsqrtf(sum / (float)a.d + a.eps) : 1.f;
+        const bool bad = top_bits >= 0x7f800000u || (kNorm && !(r <= 3.4028234e38f));
+        // of the values before r: r lies in the scale alone
+        const float s0 = __uint_as_float(top_bits) * (1.f / 127.f);
+        const float scale = kNorm ? s0 * r : s0;
+        const bool none = !bad && (s0 < kTiny || scale < kTiny);
+        const float inv = bad || none ? 0.f : 1.f / s0;
+        if (a.codes && lane == 0) a.scales[row] = bad ? __int_as_float(0x7fffffff) : none ? 0.f : scale;
+        auto put = [&](int k, const float* v) {
+            const int i = 8 * (lane + k * step), n = count(k);
+            if (a.codes && n > 0) store_codes(a.codes + row * a.code_stride + i, n, v, inv, bad, a.codes_aligned);
+            if (a.out) {
+                float y[8];
+                uint32_t o[kWords<T>];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = kNorm ? v[e] * r : v[e];
+                pack<T>(y, o);
+                store_unit<T, kAligned>(reinterpret_cast<T*>(a.out) + row * a.out_stride + i, n, o);
+            }
+        };
+        if constexpr (kSlots > 0) {
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) put(k, v[k]);
+        } else {
+            for (int k = 0; 8 * (k * step) < a.d; ++k) {
+                u[0].load(a, row, 8 * (lane + k * step), count(k));
+                take(k, u[0], v[0], false);
+                put(k, v[0]);
+            }
         }
     }
 }
 
-// codes to values; kV = 16 codes a thread in vectors, or one
-template <typename T, int kV>
-__global__ void __launch_bounds__(256) rows_dequantise_kernel(const int8_t* codes, int64_t code_stride,
-                                                              const float* scales, T* out, int64_t out_stride, int n_rows,
-                                                              int d) {
-    const int per = (d + kV - 1) / kV;
-    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < (int64_t)n_rows * per; t += (int64_t)gridDim.x * 256) {
-        const int64_t row = t / per;
-        const int i = (int)(t - row * per) * kV;
-        const int8_t* c = codes + row * code_stride + i;
+// codes to values: 16 a thread in vectors, or a unit of eight whatever the
+// alignment, 32 units of a row a warp
+template <typename T>
+__global__ void __launch_bounds__(256) rows_dequantise_kernel(const int8_t* codes, int64_t code_stride, const float* scales,
+                                                              T* out, int64_t out_stride, int64_t total, Div per) {
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
+        const int64_t row = total < (int64_t(1) << 31) ? per((uint32_t)t) : t / per.d;
+        const int i = (int)(t - row * per.d) * 16;
         T* o = out + row * out_stride + i;
         const float s = scales[row];
-        if constexpr (kV == 1) {
-            *o = from_f<T>(s * (float)*c);
-        } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(c);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            float y[16];
+        const uint4 u = *reinterpret_cast<const uint4*>(codes + row * code_stride + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        float y[16];
+        uint32_t packed[2 * kWords<T>];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = s * (float)(int8_t)(w[e / 4] >> (8 * (e % 4)));
-            store<T, 8>(o, y);
-            store<T, 8>(o + 8, y + 8);
+        for (int e = 0; e < 16; ++e) y[e] = s * (float)(int8_t)(w[e / 4] >> (8 * (e % 4)));
+        pack<T>(y, packed);
+        pack<T>(y + 8, packed + kWords<T>);
+        store_unit<T, true>(o, 8, packed);
+        store_unit<T, true>(o + 8, 8, packed + kWords<T>);
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) rows_dequantise_any_kernel(const int8_t* codes, int64_t code_stride, const float* scales,
+                                                                  T* out, int64_t out_stride, int64_t total, Div per,
+                                                                  int d, int codes_aligned) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < total; t += (int64_t)gridDim.x * 8) {   // a warp's
+        const int64_t row = total < (int64_t(1) << 31) ? per((uint32_t)t) : t / per.d;
+        const int i = (int)(t - row * per.d) * 256 + 8 * lane, n = min(8, max(0, d - i));
+        const int8_t* c = codes + row * code_stride + i;
+        const float s = scales[row];
+        uint32_t w[2] = {0u, 0u}, packed[kWords<T>];
+        if (codes_aligned && n == 8) {
+            const uint2 u = *reinterpret_cast<const uint2*>(c);
+            w[0] = u.x;
+            w[1] = u.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) w[e / 4] |= (uint32_t)(uint8_t)c[e] << (8 * (e % 4));
         }
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = s * (float)(int8_t)(w[e / 4] >> (8 * (e % 4)));
+        pack<T>(y, packed);
+        store_unit<T, false>(out + row * out_stride + i, n, packed);
     }
 }
 
-template <RowOp kOp, typename T, int kV>
-cudaError_t launch_as(const RowsQuant& a, cudaStream_t s) {
-    constexpr int kPer = kV == 8 ? 1 : 8;   // slots of a step of eight values a thread
-    const int n = (a.d + kV - 1) / kV;      // groups of a row
-    if (n <= 32 * kPer) {
-        const int per_block = 4;
-        KVR_LAUNCH((rows_quant_kernel<kOp, T, kV, kPer, true>), dim3((a.n_rows + per_block - 1) / per_block),
-                   dim3(32 * per_block), 0, s, a);
-        return cudaSuccess;
-    }
-    auto block = [&](int slots) { return dim3(std::min(1024, ((n + slots - 1) / slots + 31) / 32 * 32)); };
-    if (n <= 256 * kPer)
-        KVR_LAUNCH((rows_quant_kernel<kOp, T, kV, kPer, false>), dim3(a.n_rows), block(kPer), 0, s, a);
-    else if (n <= 1024 * kPer)
-        KVR_LAUNCH((rows_quant_kernel<kOp, T, kV, 2 * kPer, false>), dim3(a.n_rows), block(2 * kPer), 0, s, a);
-    else if (n <= 4096 * kPer)
-        KVR_LAUNCH((rows_quant_kernel<kOp, T, kV, 4 * kPer, false>), dim3(a.n_rows), block(4 * kPer), 0, s, a);
-    else
-        KVR_LAUNCH((rows_quant_kernel<kOp, T, kV, 0, false>), dim3(a.n_rows), dim3(1024), 0, s, a);
+// Blocks of a kernel that the GPU holds at once, asked for once per block size.
+template <typename K>
+int resident(K kernel, int threads) {
+    static std::atomic<uint32_t> seen{0};   // threads, blocks an SM
+    const uint32_t v = seen.load(std::memory_order_relaxed);
+    if ((int)(v >> 16) == threads) return (int)(v & 0xffffu) * kNumSMs;
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+    seen.store((uint32_t)threads << 16 | (uint32_t)n, std::memory_order_relaxed);
+    return n * kNumSMs;
+}
+
+template <RowOp kOp, typename T, bool kAligned, int kSlots, bool kWarp>
+cudaError_t launch_with(const RowsQuant& a, int units, cudaStream_t s) {
+    const auto kernel = rows_quant_kernel<kOp, T, kAligned, kSlots, kWarp>;
+    const int slots = std::max(kSlots, 1);
+    const int threads = kWarp ? 128 : kSlots == 0 ? 1024 : ((units + slots - 1) / slots + 31) / 32 * 32;
+    const int blocks = kWarp ? (int)((a.n_rows + int64_t(3)) / 4) : a.n_rows;
+    KVR_LAUNCH(kernel, dim3(std::min(blocks, resident(kernel, threads))), dim3(threads), 0, s, a);
     return cudaSuccess;
+}
+
+// A warp a row up to 512 elements, a block above.  Units a thread, measured:
+// fp32 of 1024, 8000 rows gated: one 14.6 us, two 17.3, four 26; bf16 of 1536,
+// 98304 rows stored: two 103 us, four 78; of 4096, 5632 rows stored: 18.5 and
+// 14.5; 4000 rows of 5001, added and normed: two 55 us, four 73.
+template <RowOp kOp, typename T, bool kAligned>
+cudaError_t launch_as(const RowsQuant& a, cudaStream_t s) {
+    const int units = (a.d + 7) / 8;
+    if (units <= 32) return launch_with<kOp, T, kAligned, 1, true>(a, units, s);
+    if (units <= 64) return launch_with<kOp, T, kAligned, 2, true>(a, units, s);
+    constexpr bool kMost = sizeof(T) == 2 && kAligned && kOp != RowOp::Norm;
+    if constexpr (sizeof(T) == 4) {
+        if (units <= 256) return launch_with<kOp, T, kAligned, 1, false>(a, units, s);
+    }
+    if constexpr (!kMost) {
+        if (units <= 1024) return launch_with<kOp, T, kAligned, 2, false>(a, units, s);
+    }
+    if (units <= 2560) return launch_with<kOp, T, kAligned, 4, false>(a, units, s);
+    return launch_with<kOp, T, kAligned, 0, false>(a, units, s);
 }
 
 bool in_vectors(const void* p, int64_t stride, int size, int bytes) {
@@ -302,8 +486,10 @@ cudaError_t launch_op(const RowsQuant& a, cudaStream_t s) {
     const int es = sizeof(T);
     const bool vec = a.d % 8 == 0 && in_vectors(a.x, a.x_stride, es, 16) && in_vectors(a.res, a.res_stride, es, 16) &&
                      in_vectors(a.sum, a.sum_stride, es, 16) && in_vectors(a.out, a.out_stride, es, 16) &&
-                     in_vectors(a.weight, 0, es, 16) && in_vectors(a.codes, a.code_stride, 1, 8);
-    return vec ? launch_as<kOp, T, 8>(a, s) : launch_as<kOp, T, 1>(a, s);
+                     in_vectors(a.weight, 0, es, 16);
+    RowsQuant b = a;
+    b.codes_aligned = in_vectors(a.codes, a.code_stride, 1, 8);
+    return vec ? launch_as<kOp, T, true>(b, s) : launch_as<kOp, T, false>(b, s);
 }
 
 }  // namespace
@@ -324,16 +510,18 @@ cudaError_t launch_rows_dequantise(int dtype, int n_rows, int d, const int8_t* c
                                    const float* scales, void* out, int64_t out_stride, cudaStream_t s) {
     const int es = dtype == KVR_F32 ? 4 : 2;
     const bool vec = d % 16 == 0 && in_vectors(codes, code_stride, 1, 16) && in_vectors(out, out_stride, es, 16);
-    const int64_t units = (int64_t)n_rows * (vec ? d / 16 : d);
-    const dim3 grid((unsigned)std::min<int64_t>((units + 255) / 256, 1 << 20));
+    const int codes_aligned = in_vectors(codes, code_stride, 1, 8);
     auto go = [&](auto* o) -> cudaError_t {
         using T = std::remove_pointer_t<decltype(o)>;
+        const Div per(vec ? d / 16 : (d + 255) / 256);   // 16 codes a thread, 256 a warp
+        const int64_t total = (int64_t)n_rows * per.d;
+        const dim3 grid((unsigned)std::min<int64_t>((total + (vec ? 255 : 7)) / (vec ? 256 : 8), 1 << 20));
         if (vec)
-            KVR_LAUNCH((rows_dequantise_kernel<T, 16>), grid, dim3(256), 0, s, codes, code_stride, scales, o, out_stride,
-                       n_rows, d);
+            KVR_LAUNCH((rows_dequantise_kernel<T>), grid, dim3(256), 0, s, codes, code_stride, scales, o, out_stride, total,
+                       per);
         else
-            KVR_LAUNCH((rows_dequantise_kernel<T, 1>), grid, dim3(256), 0, s, codes, code_stride, scales, o, out_stride,
-                       n_rows, d);
+            KVR_LAUNCH((rows_dequantise_any_kernel<T>), grid, dim3(256), 0, s, codes, code_stride, scales, o, out_stride,
+                       total, per, d, codes_aligned);
         return cudaSuccess;
     };
     return dtype == KVR_F32 ? go(static_cast<float*>(out)) : go(static_cast<__nv_bfloat16*>(out));

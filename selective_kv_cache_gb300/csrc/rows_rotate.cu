@@ -22,7 +22,11 @@
 namespace kvr {
 namespace {
 
-constexpr int kThreads = 256, kBatch = 4, kMaxRows = 16;   // units a thread has in flight; rows a block
+constexpr int kThreads = 128, kMaxRows = 16;   // rows a block
+// Units a thread has in flight.  7680 rows of 32/8 heads x 128 in bf16: 32 us with two of 128 threads, 36 with four,
+// 34 to 40 with 256 threads.
+template <int kBytes>
+constexpr int kBatchOf = kBytes == 16 ? 2 : 4;
 
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int g, float m, bool inverse) {
     const uint32_t t = (uint32_t)((turns * (uint64_t)(int64_t)g) >> 32);
@@ -44,52 +48,40 @@ __device__ __forceinline__ void turn(float& x, float& y, float2 cs) {
     x = a;
 }
 
-template <typename T>
-struct Vec;   // 16 bytes of T as fp32
-template <>
-struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void get(uint4 u, float* x) {
-        x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+// A vector of kBytes (16, 8 or 4) as fp32.
+template <typename T, int kBytes>
+struct Vec {
+    static constexpr int N = kBytes / (int)sizeof(T), W = kBytes / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (W == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+        else if constexpr (W == 2) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+        else w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
-    static __device__ __forceinline__ uint4 put(const float* x) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (W == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (W == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(p) = w[0];
     }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void get(uint4 u, float* x) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    __device__ __forceinline__ void get(float* x) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(w[i]);
+            else x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
         }
     }
-    static __device__ __forceinline__ uint4 put(const float* x) {
-        uint32_t w[4];
+    __device__ __forceinline__ void put(const float* x) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int i = 0; i < N; ++i) w[i] = __float_as_uint(x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-};
-
-// Quotients by a divisor of a launch, for numerators below 2^31: umulhi with
-// ceil(2^(31 + l) / d), l = ceil(log2 d), and a shift by l - 1.
-struct Div {
-    uint32_t d, mul, shift;
-    explicit Div(uint32_t n) : d(n), mul(0), shift(0) {
-        if (n == 1) return;
-        uint32_t l = 0;
-        while ((1u << l) < n) ++l;
-        mul = (uint32_t)(((uint64_t(1) << (31 + l)) + n - 1) / n);
-        shift = l - 1;
-    }
-    __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return d == 1 ? x : __umulhi(x, mul) >> shift; }
 };
 
 struct RotateDev {
@@ -101,9 +93,8 @@ struct RotateDev {
 
 // A head's units: `turned` of them hold two vectors of whole pairs, the others
 // two vectors that are copied (or left alone in place).
-template <typename T, int kLayout>
+template <int N, int kLayout>
 __device__ __forceinline__ void unit_offsets(const RotateDev& d, int u, int* first, int* second) {
-    constexpr int N = Vec<T>::N;
     if (u < d.turned && kLayout == KVR_ROPE_HALF) {
         *first = u * N;
         *second = u * N + d.a.rope.rotary_dim / 2;
@@ -113,9 +104,10 @@ __device__ __forceinline__ void unit_offsets(const RotateDev& d, int u, int* fir
     }
 }
 
-template <typename T, int kLayout>
-__global__ void __launch_bounds__(kThreads) rows_rotate_kernel(const __grid_constant__ RotateDev d) {
-    constexpr int N = Vec<T>::N;
+template <typename T, int kLayout, int kBytes>
+__global__ void __launch_bounds__(kThreads, 8) rows_rotate_kernel(const __grid_constant__ RotateDev d) {
+    using V = Vec<T, kBytes>;
+    constexpr int N = V::N, kBatch = kBatchOf<kBytes>;
     extern __shared__ float2 cs[];   // [rows_per_block][rotary_dim / 2]
     const RowsRotate& a = d.a;
     const int dh = a.rope.head_dim, half = a.rope.rotary_dim / 2;
@@ -124,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) rows_rotate_kernel(const __grid_cons
     const int total = rows * d.heads * d.units;
     bool ready = false;
     for (int base = 0; base < total; base += kThreads * kBatch) {
-        uint4 x[kBatch][2];
+        V x[kBatch][2];
         T* to[kBatch];
         int row[kBatch], unit[kBatch];
 #pragma unroll
@@ -142,9 +134,9 @@ __global__ void __launch_bounds__(kThreads) rows_rotate_kernel(const __grid_cons
             T* out = reinterpret_cast<T*>(a.out[which]) + (row0 + row[k]) * a.out_stride[which] + h * dh;
             if (unit[k] >= d.turned && in == out) continue;   // copied dims in place
             int f, s;
-            unit_offsets<T, kLayout>(d, unit[k], &f, &s);
-            x[k][0] = *reinterpret_cast<const uint4*>(in + f);
-            x[k][1] = *reinterpret_cast<const uint4*>(in + s);
+            unit_offsets<N, kLayout>(d, unit[k], &f, &s);
+            x[k][0].load(in + f);
+            x[k][1].load(in + s);
             to[k] = out;
         }
         if (!ready) {
@@ -159,11 +151,11 @@ __global__ void __launch_bounds__(kThreads) rows_rotate_kernel(const __grid_cons
         for (int k = 0; k < kBatch; ++k) {
             if (!to[k]) continue;
             int f, s;
-            unit_offsets<T, kLayout>(d, unit[k], &f, &s);
+            unit_offsets<N, kLayout>(d, unit[k], &f, &s);
             if (unit[k] < d.turned) {
                 float p[N], q[N];
-                Vec<T>::get(x[k][0], p);
-                Vec<T>::get(x[k][1], q);
+                x[k][0].get(p);
+                x[k][1].get(q);
                 const float2* c = cs + row[k] * half;
                 if constexpr (kLayout == KVR_ROPE_HALF) {
 #pragma unroll
@@ -175,11 +167,11 @@ __global__ void __launch_bounds__(kThreads) rows_rotate_kernel(const __grid_cons
                         turn(q[2 * e], q[2 * e + 1], c[unit[k] * N + N / 2 + e]);
                     }
                 }
-                x[k][0] = Vec<T>::put(p);
-                x[k][1] = Vec<T>::put(q);
+                x[k][0].put(p);
+                x[k][1].put(q);
             }
-            *reinterpret_cast<uint4*>(to[k] + f) = x[k][0];
-            *reinterpret_cast<uint4*>(to[k] + s) = x[k][1];
+            x[k][0].store(to[k] + f);
+            x[k][1].store(to[k] + s);
         }
     }
 }
@@ -229,28 +221,39 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__
 
 template <typename T>
 cudaError_t launch_as(const RowsRotate& a, cudaStream_t s) {
-    constexpr int N = Vec<T>::N, es = sizeof(T);
-    const int dh = a.rope.head_dim, rot = a.rope.rotary_dim;
-    bool vec = rot % (2 * N) == 0 && dh % (2 * N) == 0;
-    for (int w = 0; w < 2; ++w)
-        if (a.heads[w])
-            vec = vec && reinterpret_cast<uintptr_t>(a.in[w]) % 16 == 0 && reinterpret_cast<uintptr_t>(a.out[w]) % 16 == 0 &&
-                  a.in_stride[w] * es % 16 == 0 && a.out_stride[w] * es % 16 == 0;
-    const int units = vec ? dh / (2 * N) : dh / 2, heads = a.heads[0] + a.heads[1];
+    constexpr int es = sizeof(T);
+    const int dh = a.rope.head_dim, rot = a.rope.rotary_dim, layout = a.rope.layout;
+    // the widest vector that whole units are made of, each of two
+    auto fits = [&](int bytes) {
+        const int n = bytes / es;
+        bool ok = rot % (2 * n) == 0 && dh % (2 * n) == 0 && (n > 1 || layout == KVR_ROPE_HALF);
+        for (int w = 0; w < 2; ++w)
+            if (a.heads[w])
+                ok = ok && reinterpret_cast<uintptr_t>(a.in[w]) % bytes == 0 && reinterpret_cast<uintptr_t>(a.out[w]) % bytes == 0 &&
+                     a.in_stride[w] * es % bytes == 0 && a.out_stride[w] * es % bytes == 0;
+        return ok;
+    };
+    const int bytes = fits(16) ? 16 : fits(8) ? 8 : fits(4) ? 4 : 0, n = bytes / es;
+    const int units = n ? dh / (2 * n) : dh / 2, heads = a.heads[0] + a.heads[1];
     // rows that fill a block's batch, fewer where there are not enough rows for the GPU
-    int rows = std::max(1, std::min(kMaxRows, kThreads * kBatch / (units * heads)));
+    int rows = std::max(1, std::min(kMaxRows, kThreads * (bytes == 16 ? kBatchOf<16> : kBatchOf<8>) / (units * heads)));
     rows = std::min(rows, std::max(1, a.n_rows / (2 * kNumSMs)));
-    const RotateDev d{a, a.inverse ? 1.f / a.rope.attn : a.rope.attn, rows, units, vec ? rot / (2 * N) : rot / 2, heads,
+    const RotateDev d{a, a.inverse ? 1.f / a.rope.attn : a.rope.attn, rows, units, n ? rot / (2 * n) : rot / 2, heads,
                       Div(units), Div(heads)};
     const dim3 grid((unsigned)((a.n_rows + (int64_t)rows - 1) / rows));
     const size_t smem = sizeof(float2) * rows * (rot / 2);
-    if (!vec)
-        KVR_LAUNCH((rows_rotate_pairs_kernel<T>), grid, dim3(kThreads), smem, s, d, a.rope.layout);
-    else if (a.rope.layout == KVR_ROPE_HALF)
-        KVR_LAUNCH((rows_rotate_kernel<T, KVR_ROPE_HALF>), grid, dim3(kThreads), smem, s, d);
-    else
-        KVR_LAUNCH((rows_rotate_kernel<T, KVR_ROPE_INTERLEAVED>), grid, dim3(kThreads), smem, s, d);
-    return cudaSuccess;
+    if (n == 0) {
+        KVR_LAUNCH((rows_rotate_pairs_kernel<T>), grid, dim3(kThreads), smem, s, d, layout);
+        return cudaSuccess;
+    }
+    auto go = [&](auto half, auto interleaved) -> cudaError_t {
+        KVR_LAUNCH(layout == KVR_ROPE_HALF ? half : interleaved, grid, dim3(kThreads), smem, s, d);
+        return cudaSuccess;
+    };
+    constexpr int H = KVR_ROPE_HALF, I = KVR_ROPE_INTERLEAVED;
+    if (bytes == 16) return go(rows_rotate_kernel<T, H, 16>, rows_rotate_kernel<T, I, 16>);
+    if (bytes == 8) return go(rows_rotate_kernel<T, H, 8>, rows_rotate_kernel<T, I, 8>);
+    return go(rows_rotate_kernel<T, H, 4>, rows_rotate_kernel<T, es == 4 ? H : I, 4>);
 }
 
 }  // namespace
