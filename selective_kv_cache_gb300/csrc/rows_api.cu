@@ -78,7 +78,7 @@ enum class LinearWay { Mma, Few, Tc };
 LinearWay linear_way(int n_out, int k, int n_rows) {
     if (n_rows <= kLinearMmaRows) return LinearWay::Mma;
     if (n_rows <= 64) return LinearWay::Few;
-    return linear_few_us(n_out, k, n_rows) < linear_tc_us(n_out, k, n_rows) ? LinearWay::Few : LinearWay::Tc;
+    return n_rows <= 4096 && linear_few_us(n_out, k, n_rows) < linear_tc_us(n_out, k, n_rows) ? LinearWay::Few : LinearWay::Tc;
 }
 size_t linear_workspace(const kvr_linear_weights& w, int32_t n_rows) {
     return linear_way(w.n_out, w.k, n_rows) == LinearWay::Tc ? linear_tc_workspace(w.n_out, w.k, n_rows) : 256;

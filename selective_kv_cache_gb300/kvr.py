@@ -630,43 +630,40 @@ _ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 KVR_ROPE_INVERSE = 0x1
 
 
-def _row_stream(dev, stream) -> int:
+def _row_stream(dev: int, stream) -> int:
     # a launch goes to the current device, whichever device the pointers are of
-    if torch._C._cuda_getDevice() != dev.index:
-        raise ValueError(f"tensors on {dev}: make it the current device")
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+    if dev < 0 or torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"tensors on {'the CPU' if dev < 0 else f'cuda:{dev}'}: need the current device's")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _row_args(t, what: str, like, width: int, dtype=None, n: Optional[int] = None):
-    """(pointer, stride) of [rows, width] rows beside the tensor `like`."""
-    try:
-        rows, w = t.shape
-        s0, s1 = t.stride()
-    except (AttributeError, ValueError):
-        raise ValueError(f"{what}: need a tensor of rows") from None
-    n = like.shape[0] if n is None else n
-    if rows != n or w != width or (s1 != 1 and w > 1) or t.dtype is not (dtype or like.dtype) or t.device != like.device \
-            or not t.is_cuda or (s0 < w and rows > 1):
-        raise ValueError(f"{what}: need [{n}, {width}] of {dtype or like.dtype} on {like.device}, elements of a row "
-                         f"contiguous; got {tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
-    # the stride of a single row is whatever torch says; the library wants a full one
-    return t.data_ptr(), s0 if s0 > w else w
+def _row_args(t, what: str, shape, dtype, dev: int):
+    """(pointer, stride) of [rows, width] rows; the first test is the usual case."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        s = t.stride()
+        if s[1] == 1 and s[0] >= shape[1]:
+            return t.data_ptr(), s[0]
+        if (s[1] == 1 or shape[1] == 1) and (s[0] >= shape[1] or shape[0] <= 1):
+            # the stride of a single row is whatever torch says; the library wants a full one
+            return t.data_ptr(), max(s[0], shape[1])
+    raise ValueError(f"{what}: need {tuple(shape)} of {dtype} on cuda:{dev}, elements of a row contiguous; got "
+                     f"{tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
 
 
-def _scales(t, what: str, like, n: int):
-    if t.dtype is not torch.float32 or t.device != like.device or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{what}: need {n} contiguous fp32 values on {like.device}")
+def _values(t, what: str, n: int, dtype, dev: int):
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: need {n} contiguous values of {dtype} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _outputs(x, d: int, out, codes, scales):
-    """The arguments of the two forms of a row operator's result."""
-    if (codes is None) != (scales is None):
-        raise ValueError("codes and scales go together")
-    o = (None, 0) if out is None else _row_args(out, "out", x, d)
-    c = (None, 0, None) if codes is None else (*_row_args(codes, "codes", x, d, torch.int8),
-                                               _scales(scales, "scales", x, x.shape[0]))
-    return (*o, *c)
+def _codes(codes, scales, shape, dev: int):
+    """The arguments of rows in eight bits, which may be left out."""
+    if codes is None or scales is None:
+        if codes is not scales:
+            raise ValueError("codes and scales go together")
+        return None, 0, None
+    ptr, stride = _row_args(codes, "codes", shape, torch.int8, dev)
+    return ptr, stride, _values(scales, "scales", shape[0], torch.float32, dev)
 
 
 def _dtype(x, what: str = "x") -> int:
@@ -678,39 +675,47 @@ def _dtype(x, what: str = "x") -> int:
 def kvr_rows_norm(x, weight, eps: float, residual=None, sum_out=None, out=None, codes=None, scales=None, stream=None):
     """x: [n, d]; residual, sum_out, out: as x or None; weight: [d] of x's
     type; codes: int8 [n, d] with scales fp32 [n], or None."""
-    dt, (n, d) = _dtype(x), x.shape
-    xp = _row_args(x, "x", x, d)
-    rp = (None, 0) if residual is None else _row_args(residual, "residual", x, d)
-    sp = (None, 0) if sum_out is None else _row_args(sum_out, "sum_out", x, d)
-    if weight.dtype is not x.dtype or weight.device != x.device or not weight.is_contiguous() or weight.numel() != d:
-        raise ValueError(f"weight: need {d} contiguous values of {x.dtype} on {x.device}")
-    _check(lib.kvr_rows_norm(dt, n, d, *xp, *rp, *sp, weight.data_ptr(), eps, *_outputs(x, d, out, codes, scales),
-                             _row_stream(x.device, stream)), "kvr_rows_norm")
+    dt, shape, t, dev = _dtype(x), x.shape, x.dtype, x.get_device()
+    s = _row_stream(dev, stream)
+    xp, xs = _row_args(x, "x", shape, t, dev)
+    rp, rs = (None, 0) if residual is None else _row_args(residual, "residual", shape, t, dev)
+    sp, ss = (None, 0) if sum_out is None else _row_args(sum_out, "sum_out", shape, t, dev)
+    op, os_ = (None, 0) if out is None else _row_args(out, "out", shape, t, dev)
+    cp, cs, scp = _codes(codes, scales, shape, dev)
+    wp = _values(weight, "weight", shape[1], t, dev)
+    _check(lib.kvr_rows_norm(dt, shape[0], shape[1], xp, xs, rp, rs, sp, ss, wp, eps, op, os_, cp, cs, scp, s),
+           "kvr_rows_norm")
 
 
 def kvr_rows_swiglu(gate_up, out=None, codes=None, scales=None, stream=None):
     """gate_up: [n, 2 d]; outputs as kvr_rows_norm, d wide."""
-    dt, (n, wide) = _dtype(gate_up, "gate_up"), gate_up.shape
+    dt, t, dev = _dtype(gate_up, "gate_up"), gate_up.dtype, gate_up.get_device()
+    n, wide = gate_up.shape
     if wide % 2:
         raise ValueError("gate_up: need an even width")
-    gp = _row_args(gate_up, "gate_up", gate_up, wide)
-    _check(lib.kvr_rows_swiglu(dt, n, wide // 2, *gp, *_outputs(gate_up, wide // 2, out, codes, scales),
-                               _row_stream(gate_up.device, stream)), "kvr_rows_swiglu")
+    s = _row_stream(dev, stream)
+    gp, gs = _row_args(gate_up, "gate_up", (n, wide), t, dev)
+    op, os_ = (None, 0) if out is None else _row_args(out, "out", (n, wide // 2), t, dev)
+    cp, cs, scp = _codes(codes, scales, (n, wide // 2), dev)
+    _check(lib.kvr_rows_swiglu(dt, n, wide // 2, gp, gs, op, os_, cp, cs, scp, s), "kvr_rows_swiglu")
 
 
 def kvr_rows_quantise(x, codes, scales, stream=None):
     """x: [n, d] into codes int8 [n, d] and scales fp32 [n]."""
-    dt, (n, d) = _dtype(x), x.shape
-    _check(lib.kvr_rows_quantise(dt, n, d, *_row_args(x, "x", x, d), *_outputs(x, d, None, codes, scales)[2:],
-                                 _row_stream(x.device, stream)), "kvr_rows_quantise")
+    dt, shape, dev = _dtype(x), x.shape, x.get_device()
+    s = _row_stream(dev, stream)
+    xp, xs = _row_args(x, "x", shape, x.dtype, dev)
+    cp, cs, scp = _codes(codes, scales, shape, dev)
+    _check(lib.kvr_rows_quantise(dt, shape[0], shape[1], xp, xs, cp, cs, scp, s), "kvr_rows_quantise")
 
 
 def kvr_rows_dequantise(codes, scales, out, stream=None):
     """codes int8 [n, d] and scales fp32 [n] into out [n, d], bf16 or fp32."""
-    dt, (n, d) = _dtype(out, "out"), out.shape
-    _check(lib.kvr_rows_dequantise(dt, n, d, *_row_args(codes, "codes", out, d, torch.int8),
-                                   _scales(scales, "scales", out, n), *_row_args(out, "out", out, d),
-                                   _row_stream(out.device, stream)), "kvr_rows_dequantise")
+    dt, shape, dev = _dtype(out, "out"), out.shape, out.get_device()
+    s = _row_stream(dev, stream)
+    op, os_ = _row_args(out, "out", shape, out.dtype, dev)
+    cp, cs, scp = _codes(codes, scales, shape, dev)
+    _check(lib.kvr_rows_dequantise(dt, shape[0], shape[1], cp, cs, scp, op, os_, s), "kvr_rows_dequantise")
 
 
 def kvr_rope_init(head_dim: int, rotary_dim: int, layout: int, scaling: int, theta: float, factor: float, low: float,
@@ -738,21 +743,20 @@ def kvr_rope_table(r: kvr_rope, rope_len: int, table, stream=None):
     """table: contiguous fp32 [rope_len, rotary_dim / 2, 2]."""
     if _want(table, "table", torch.float32).shape != (rope_len, r.rotary_dim // 2, 2) or not table.is_contiguous():
         raise ValueError(f"table: need a contiguous [{rope_len}, {r.rotary_dim // 2}, 2]")
-    _check(lib.kvr_rope_table(r.addr, rope_len, table.data_ptr(), _row_stream(table.device, stream)), "kvr_rope_table")
+    _check(lib.kvr_rope_table(r.addr, rope_len, table.data_ptr(), _row_stream(table.get_device(), stream)), "kvr_rope_table")
 
 
-def _heads(r: kvr_rope, t, what: str, n: int, like):
+def _heads(t, what: str, n: int, dh: int, dtype, dev: int):
     """(pointer, row stride, heads) of a [rows, heads, head_dim] operand."""
-    dh = r.head_dim
     try:
         rows, heads, d = t.shape
         s0, s1, s2 = t.stride()
     except ValueError:
         rows = -1
     if rows != n or d != dh or s2 != 1 or (s1 != dh and heads > 1) or (s0 < heads * dh and rows > 1) or \
-            t.dtype is not like.dtype or t.dtype not in _DTYPES or t.device != like.device:
-        raise ValueError(f"{what}: need [{n}, heads, {dh}] in bf16 or fp32, a row's heads contiguous, like the others; "
-                         f"got {tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
+            t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{what}: need [{n}, heads, {dh}] of {dtype} on cuda:{dev}, a row's heads contiguous; got "
+                         f"{tuple(t.shape)} strides {t.stride()} of {t.dtype} on {t.device}")
     return t.data_ptr(), s0 if s0 > heads * dh else heads * dh, heads
 
 
@@ -762,20 +766,23 @@ def kvr_rows_rotate(r: kvr_rope, positions, q=None, q_out=None, k=None, k_out=No
     like = q if q is not None else k
     if like is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q and q_out, k and k_out go together, and one of the pairs is needed")
-    _int_array(positions, "positions", None, like.device)
-    n = positions.numel()
-    args = []
-    for i, o, what in ((q, q_out, "q"), (k, k_out, "k")):
-        if i is None:
-            args += (None, 0, 0, None, 0)
-            continue
-        ip, istride, heads = _heads(r, i, what, n, like)
-        op, ostride, ho = _heads(r, o, what + "_out", n, like)
-        if ho != heads:
-            raise ValueError(f"{what}_out: need {what}'s heads")
-        args += (ip, istride, heads, op, ostride)
-    _check(lib.kvr_rows_rotate(r.addr, _DTYPES[like.dtype], n, positions.data_ptr(), *args,
-                               KVR_ROPE_INVERSE if inverse else 0, _row_stream(like.device, stream)), "kvr_rows_rotate")
+    t, dev, n, dh = like.dtype, like.get_device(), positions.numel(), r.head_dim
+    if t not in _DTYPES:
+        raise ValueError(f"need heads in bf16 or fp32, got {t}")
+    s = _row_stream(dev, stream)
+    pp = _values(positions, "positions", n, torch.int32, dev)
+    qa = ka = (None, 0, 0)
+    qo = ko = (None, 0, 0)
+    if q is not None:
+        qa = _heads(q, "q", n, dh, t, dev)
+        qo = qa if q_out is q else _heads(q_out, "q_out", n, dh, t, dev)
+    if k is not None:
+        ka = _heads(k, "k", n, dh, t, dev)
+        ko = ka if k_out is k else _heads(k_out, "k_out", n, dh, t, dev)
+    if qo[2] != qa[2] or ko[2] != ka[2]:
+        raise ValueError("q_out, k_out: need the heads of q and k")
+    _check(lib.kvr_rows_rotate(r.addr, _DTYPES[t], n, pp, *qa, qo[0], qo[1], *ka, ko[0], ko[1],
+                               KVR_ROPE_INVERSE if inverse else 0, s), "kvr_rows_rotate")
 
 
 def linear_weights(codes, scales, err, bias=None) -> kvr_linear_weights:
@@ -784,14 +791,14 @@ def linear_weights(codes, scales, err, bias=None) -> kvr_linear_weights:
     [n_out]; err: int32 [4], zeroed."""
     if codes.dim() != 2:
         raise ValueError("codes: need [n_out, k]")
-    ptr, stride = _row_args(codes, "codes", codes, codes.shape[1], torch.int8)
+    dev, n = codes.get_device(), codes.shape[0]
+    ptr, stride = _row_args(codes, "codes", codes.shape, torch.int8, dev)
     _int_array(err, "err", 4, codes.device)
-    n = codes.shape[0]
     w = kvr_linear_weights(n, codes.shape[1], stride if n > 1 else -(-stride // 16) * 16, ptr,
-                           _scales(scales, "scales", codes, n), None if bias is None else _scales(bias, "bias", codes, n),
-                           _ptr(err))
+                           _values(scales, "scales", n, torch.float32, dev),
+                           None if bias is None else _values(bias, "bias", n, torch.float32, dev), _ptr(err))
     w.tensors = (codes, scales, bias, err)
-    w.device = codes.device
+    w.device = dev
     w.addr = C.addressof(w)
     return w
 
@@ -804,16 +811,16 @@ def kvr_linear(w: kvr_linear_weights, codes, scales, out, workspace, stream=None
     """codes: int8 [n, k], rows a multiple of 16 bytes apart; scales: fp32 [n];
     out: [n, n_out] in bf16 or fp32; workspace: uint8 of
     kvr_linear_workspace_bytes."""
-    dt, n = _dtype(out, "out"), out.shape[0]
-    op, os_ = _row_args(out, "out", out, w.n_out)
-    cp, cs = _row_args(codes, "codes", out, w.k, torch.int8)
-    if out.device != w.device:
-        raise ValueError(f"out: need a tensor on {w.device}")
-    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != w.device:
-        _want(workspace, "workspace", torch.uint8, 1, w.device)
+    dt, dev, n = _dtype(out, "out"), w.device, out.shape[0]
+    s = _row_stream(dev, stream)
+    op, os_ = _row_args(out, "out", (n, w.n_out), out.dtype, dev)
+    cp, cs = _row_args(codes, "codes", (n, w.k), torch.int8, dev)
+    sp = _values(scales, "scales", n, torch.float32, dev)
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        _want(workspace, "workspace", torch.uint8, 1, codes.device)
     # a single row's stride is whatever torch says
-    _check(lib.kvr_linear(w.addr, n, cp, cs if n > 1 else -(-cs // 16) * 16, _scales(scales, "scales", out, n), dt, op, os_,
-                          workspace.data_ptr(), workspace.numel(), _row_stream(w.device, stream)), "kvr_linear")
+    _check(lib.kvr_linear(w.addr, n, cp, cs if n > 1 else -(-cs // 16) * 16, sp, dt, op, os_, workspace.data_ptr(),
+                          workspace.numel(), s), "kvr_linear")
 
 
 def kvr_linear_status(w: kvr_linear_weights, stream=None):
