@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
                     phase ^= 1u;
                 }
             }
-            if (!ok) {   // let every copy still in flight land before the block exits
-                for (int i = it - stages; i < it; ++i) mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
-            }
+            // whatever the others met, every copy lands before the block exits
+            const int sent = min(it, n_kb);
+            for (int i = max(0, sent - stages); i < sent; ++i) mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -235,10 +235,8 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
                     }
                 }
             }
-            if (!ok) {   // let every copy still in flight land before the CTA exits
-                for (int i = (it > stages ? it - stages : 0); i < it; ++i)
-                    mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
-            }
+            // whatever the others met, every copy lands before the CTA exits
+            for (int i = max(0, it - stages); i < it; ++i) mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ products

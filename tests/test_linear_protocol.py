@@ -1,0 +1,153 @@
+"""Model check of the barrier protocols of the 8-bit projections on tensor
+cores (csrc/linear_few.cu, csrc/linear_tc.cu), run on the CPU.
+
+The roles are played out as coroutines under random interleavings; copies land
+in any order, products complete in the order of their issue.
+
+  copies     a ring of `stages`: iteration it arms full[it % stages] after
+             empty[it % stages] has completed for its previous use
+  few        two widening sets take the iterations in turn, each into a slot of
+             its own: wait full, read, arrive on empty; wait freed[set], write
+             the slot, arrive on ready[set].  Products of iteration it wait for
+             ready[it % 2], read the slot and complete freed[it % 2].
+  tc         both sets take a half of every iteration: chunk q = 2 it + half goes
+             to slot q % slots; the products of a chunk complete freed[slot],
+             those of the second half empty as well (they read the stage's
+             rows); a pair's two CTAs both widen, and ready counts both.
+
+A wait names a completion by its parity alone, so it is only sound while the
+barrier is at most one completion away; the model fails where it is further,
+where a stage is refilled before it was read, or a slot rewritten before its
+products read it."""
+import random
+
+import pytest
+
+
+class Unsound(AssertionError):
+    pass
+
+
+class Barriers:
+    def __init__(self):
+        self.done, self.arrived = {}, {}
+
+    def arrive(self, b, count):
+        n = self.arrived.get(b, 0) + 1
+        self.arrived[b] = n % count
+        if n == count:
+            self.done[b] = self.done.get(b, 0) + 1
+
+    def passes(self, b, k):
+        """The wait for completion number k (-1: the phase before the first)."""
+        c = self.done.get(b, 0)
+        if not k <= c <= k + 1 and not (k == -1 and c == 0):
+            raise Unsound(f"{b}: waits for completion {k} with {c} done")
+        return c == k + 1
+
+
+def play(kind, total, stages, slots, ctas, seed):
+    R, B = random.Random(seed), Barriers()
+    landed, read, widened, used = {}, set(), {}, set()   # stage's iteration, (cta, it, set) read, slot's chunk, chunks multiplied
+    flying, queue = [], []
+    halves = 1 if kind == "few" else 2
+
+    def copies(c):
+        for it in range(total):
+            s = it % stages
+            while not B.passes(("empty", c, s), it // stages - 1):
+                yield
+            readers = [it % 2] if kind == "few" else [0, 1]
+            if it >= stages and not all((c, it - stages, x) in read for x in readers):
+                raise Unsound("a stage is refilled before its codes were read")
+            if kind == "tc" and it >= stages and not all(2 * (it - stages) + h in used for h in (0, 1)):
+                raise Unsound("a stage is refilled before its rows were multiplied")
+            flying.append((c, s, it))
+            yield
+
+    def widen(c, x):
+        uses = {}
+        for it in range(x if kind == "few" else 0, total, 2 if kind == "few" else 1):
+            s = it % stages
+            while not B.passes(("full", c, s), it // stages):
+                yield
+            if landed.get((c, s)) != it:
+                raise Unsound("codes of another iteration")
+            read.add((c, it, x))
+            if kind == "few":
+                B.arrive(("empty", c, s), 1)
+            yield
+            q = it if kind == "few" else 2 * it + x
+            t = x if kind == "few" else q % slots
+            k = uses.get(t, 0)
+            uses[t] = k + 1
+            while not B.passes(("freed", c, t), k - 1):
+                yield
+            if (c, t) in widened and widened[c, t] not in used:
+                raise Unsound("a slot is rewritten before its products")
+            widened[c, t] = q
+            yield
+            B.arrive(("ready", t), ctas)
+
+    def products():
+        for q in range(total * halves):
+            t = q % 2 if kind == "few" else q % slots
+            per = 2 if kind == "few" else slots
+            while not B.passes(("ready", t), q // per):
+                yield
+            if any(widened.get((c, t)) != q for c in range(ctas)):
+                raise Unsound("products of another chunk")
+            queue.append((q, t))
+            yield
+
+    def world():
+        while True:
+            if flying and R.random() < 0.5:
+                c, s, it = flying.pop(R.randrange(len(flying)))
+                landed[c, s] = it
+                B.arrive(("full", c, s), 1)
+            if queue and R.random() < 0.5:
+                q, t = queue.pop(0)
+                used.add(q)
+                for c in range(ctas):
+                    B.arrive(("freed", c, t), 1)
+                    if kind == "tc" and q % 2:
+                        B.arrive(("empty", c, q // 2 % stages), 1)
+            yield
+
+    roles = [products()] + [copies(c) for c in range(ctas)] + [widen(c, x) for c in range(ctas) for x in (0, 1)]
+    w = world()
+    for _ in range(200000):
+        if not roles and not queue:
+            assert len(used) == total * halves
+            return
+        next(w)
+        if roles:
+            i = R.randrange(len(roles))
+            try:
+                next(roles[i])
+            except StopIteration:
+                roles.pop(i)
+    raise Unsound("no progress")
+
+
+@pytest.mark.parametrize("stages", [2, 4, 6])
+@pytest.mark.parametrize("total", [1, 2, 3, 7, 20])
+def test_batch_kernel(stages, total):
+    for seed in range(60):
+        play("few", total, stages, 2, 1, seed)
+
+
+@pytest.mark.parametrize("stages,slots", [(4, 4), (5, 4), (7, 8), (12, 8), (1, 4)])
+@pytest.mark.parametrize("total", [1, 2, 5, 20])
+def test_tile_kernel(stages, slots, total):
+    for seed in range(25):
+        play("tc", total, stages, slots, 2, seed)
+
+
+def test_an_odd_ring_is_unsound_for_sets_that_take_turns():
+    """With three stages a set meets a stage whose earlier use was the other
+    set's, and takes an early look at it for a completion of its own."""
+    with pytest.raises(Unsound):
+        for seed in range(2000):
+            play("few", 12, 3, 2, 1, seed)
