@@ -280,11 +280,14 @@ Plan make_plan(int n_out, int k, int n_rows) {
     p.tiles = (n_out + 127) / 128;
     p.KB = (k + 127) / 128;
     const long long blocks = (long long)p.tiles * p.row_tiles;
-    // Blocks a cluster: as many as leave every block resident at once (two an SM).  28672 features, 17 rows: 25 us
-    // alone, 30 in twos, which a second wave follows; 6144 features: 15 alone, 11.4 in fours.  Threes and sixes
-    // fit the GPCs badly.
+    // Blocks a cluster.  A block an SM as long as each has two stages, two an SM where each keeps six; all of them
+    // resident at once.  64 rows (us): 4096 -> 6144 in ones 23, twos 16, fours 14, eights, which a second wave follows, 19;
+    // 4096 -> 4096 in fours 11.8, eights 12.4; 14336 -> 4096 in fours 25, eights 21; 1536 -> 2048 in twos 8.8, fours 7.2,
+    // eights 8.7.  Threes and sixes fit the GPCs badly.
     p.split = 1;
-    while (p.split < 8 && 2 * p.split * blocks <= 2 * kNumSMs && p.KB >= 8 * p.split) p.split *= 2;
+    while (p.split < 8 && ((2 * p.split * blocks <= kNumSMs && p.KB >= 4 * p.split) ||
+                           (2 * p.split * blocks <= 2 * kNumSMs && p.KB >= 12 * p.split)))
+        p.split *= 2;
     p.waves = (int)std::min<long long>(1 << 20, (blocks * p.split + 2 * kNumSMs - 1) / (2 * kNumSMs));
     return p;
 }
