@@ -295,7 +295,10 @@ Plan make_plan(int n_out, int k, int n_rows) {
 
 double linear_few_us(int n_out, int k, int n_rows) {
     const Plan p = make_plan(n_out, k, n_rows);
-    return 9.5 + 0.72 * p.waves * ((p.KB + p.split - 1) / p.split);
+    // starting and joining, and a stage: with one block on the busiest SM, with two
+    const int stages = (p.KB + p.split - 1) / p.split;
+    const bool two = (long long)p.tiles * p.row_tiles * p.split > kNumSMs;
+    return (two ? 8.5 : 5.5) + (two ? 0.74 : 0.64) * p.waves * stages;
 }
 
 cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why) {

@@ -426,7 +426,7 @@ Plan make_plan(int n_out, int k, int n_rows) {
 
 }  // namespace
 
-double linear_tc_us(int n_out, int k, int n_rows) { return 7.0 + make_plan(n_out, k, n_rows).cycles / 1900; }
+double linear_tc_us(int n_out, int k, int n_rows) { return 5.5 + make_plan(n_out, k, n_rows).cycles / 1900; }
 
 size_t linear_tc_workspace(int n_out, int k, int n_rows) {
     return (size_t)n_rows * make_plan(n_out, k, n_rows).pitch * 2;

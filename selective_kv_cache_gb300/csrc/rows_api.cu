@@ -68,10 +68,13 @@ kvr_status check_weights(const kvr_linear_weights* w) {
 //   64 x  4096 ->  6144                  13.9     17.7
 //   64 x  4096 -> 28672                  32.8     32.3
 //   64 x 14336 ->  4096                  20.8     42.5
-//  128 x  4096 ->  6144                  20.3     17.7
-//  128 x 14336 ->  4096                  30.2     43.2
-//  256 x  8960 ->  1536                  21.3     29.9
-//  512 x  8960 ->  1536                  33.9     31.0
+//   96 x  4096 ->  6144                  18.5     18.2
+//  128 x  1536 ->  2048                   7.2     10.5
+//  128 x  4096 ->  4096                  14.3     17.9
+//  256 x  4096 ->  4096                  20.5     18.0
+//  128 x 18944 ->  3584                  37.1     56.5
+//  192 x 18944 ->  3584                  63.8     56.9
+//  512 x  1536 ->  2048                  12.6     10.8
 // Above 64 rows the batch kernel reads the weights once for every 64 of them,
 // and splits k where the tiles are few: the two estimates decide.
 enum class LinearWay { Mma, Few, Tc };
