@@ -730,8 +730,9 @@ kvr_status kvr_paged_status(const kvr_pages* p, void* stream);
  * codes 0, so all it stands for is NaN and no other row is touched.
  *
  * dtype is KVR_F32 or KVR_BF16.  Strides are in elements of their array, at
- * least a row's width.  Rows of any width and alignment of their elements are
- * taken; 16-byte aligned pointers and strides (codes: 8) are moved in vectors.
+ * least a row's width.  Rows of any width and of any alignment of their elements
+ * are taken; 16-byte aligned pointers and strides (codes: 8) are the faster.  A
+ * row's last or first aligned 16 bytes may be read past it, never written.
  * Widths go up to 2^20, rows to 2^31 - 1, strides to 2^29.  Sums, maxima and products are fp32
  * (|h| stays below 2^60, so that its squares do not overflow).  Where an
  * output may be an input, it is that array from its first element on, with

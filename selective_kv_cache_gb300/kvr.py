@@ -676,6 +676,8 @@ def kvr_rows_norm(x, weight, eps: float, residual=None, sum_out=None, out=None, 
     """x: [n, d]; residual, sum_out, out: as x or None; weight: [d] of x's
     type; codes: int8 [n, d] with scales fp32 [n], or None."""
     dt, shape, t, dev = _dtype(x), x.shape, x.dtype, x.get_device()
+    if shape[0] == 0:
+        return   # an empty tensor has no address
     s = _row_stream(dev, stream)
     xp, xs = _row_args(x, "x", shape, t, dev)
     rp, rs = (None, 0) if residual is None else _row_args(residual, "residual", shape, t, dev)
@@ -693,6 +695,8 @@ def kvr_rows_swiglu(gate_up, out=None, codes=None, scales=None, stream=None):
     n, wide = gate_up.shape
     if wide % 2:
         raise ValueError("gate_up: need an even width")
+    if n == 0:
+        return
     s = _row_stream(dev, stream)
     gp, gs = _row_args(gate_up, "gate_up", (n, wide), t, dev)
     op, os_ = (None, 0) if out is None else _row_args(out, "out", (n, wide // 2), t, dev)
@@ -703,6 +707,8 @@ def kvr_rows_swiglu(gate_up, out=None, codes=None, scales=None, stream=None):
 def kvr_rows_quantise(x, codes, scales, stream=None):
     """x: [n, d] into codes int8 [n, d] and scales fp32 [n]."""
     dt, shape, dev = _dtype(x), x.shape, x.get_device()
+    if shape[0] == 0:
+        return
     s = _row_stream(dev, stream)
     xp, xs = _row_args(x, "x", shape, x.dtype, dev)
     cp, cs, scp = _codes(codes, scales, shape, dev)
@@ -712,6 +718,8 @@ def kvr_rows_quantise(x, codes, scales, stream=None):
 def kvr_rows_dequantise(codes, scales, out, stream=None):
     """codes int8 [n, d] and scales fp32 [n] into out [n, d], bf16 or fp32."""
     dt, shape, dev = _dtype(out, "out"), out.shape, out.get_device()
+    if shape[0] == 0:
+        return
     s = _row_stream(dev, stream)
     op, os_ = _row_args(out, "out", shape, out.dtype, dev)
     cp, cs, scp = _codes(codes, scales, shape, dev)
@@ -769,6 +777,8 @@ def kvr_rows_rotate(r: kvr_rope, positions, q=None, q_out=None, k=None, k_out=No
     t, dev, n, dh = like.dtype, like.get_device(), positions.numel(), r.head_dim
     if t not in _DTYPES:
         raise ValueError(f"need heads in bf16 or fp32, got {t}")
+    if n == 0:
+        return
     s = _row_stream(dev, stream)
     pp = _values(positions, "positions", n, torch.int32, dev)
     qa = ka = (None, 0, 0)
@@ -812,6 +822,8 @@ def kvr_linear(w: kvr_linear_weights, codes, scales, out, workspace, stream=None
     out: [n, n_out] in bf16 or fp32; workspace: uint8 of
     kvr_linear_workspace_bytes."""
     dt, dev, n = _dtype(out, "out"), w.device, out.shape[0]
+    if n == 0:
+        return
     s = _row_stream(dev, stream)
     op, os_ = _row_args(out, "out", (n, w.n_out), out.dtype, dev)
     cp, cs = _row_args(codes, "codes", (n, w.k), torch.int8, dev)

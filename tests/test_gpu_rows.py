@@ -26,7 +26,7 @@ HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 REL = 2.0 ** -18
 # widths at every kernel's borders: a warp a row (256, 257), one, two and four
 # groups of eight a thread, rows that are read twice, odd ones
-WIDTHS = [1, 2, 7, 8, 31, 64, 255, 256, 257, 264, 1536, 2047, 2048, 2056, 4096, 5001, 8192, 8200, 14336, 18944, 32768,
+WIDTHS = [1, 2, 7, 8, 31, 64, 255, 256, 257, 264, 1792, 2047, 2048, 2056, 4096, 5001, 8192, 8200, 14336, 18944, 32768,
           32776, 40001]
 
 
@@ -344,3 +344,78 @@ def test_many_rows():
     out = torch.empty_like(x)
     kvr.kvr_rows_dequantise(codes, scale, out)
     assert torch.equal(out, (codes.float() * scale[:, None]).bfloat16())
+
+
+def test_no_rows():
+    """Empty tensors, which have no address: nothing happens."""
+    x, c, s = torch.empty(0, 64, device="cuda"), torch.empty(0, 64, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    w, h, p = torch.ones(64, device="cuda"), torch.empty(0, 2, 64, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    kvr.kvr_rows_norm(x, w, 1e-5, codes=c, scales=s)
+    kvr.kvr_rows_swiglu(x, codes=c[:, :32], scales=s)
+    kvr.kvr_rows_quantise(x, c, s)
+    kvr.kvr_rows_dequantise(c, s, x)
+    kvr.kvr_rows_rotate(kvr.rope(64), p, h, h)
+    codes, scale = empty_codes(32, 64)
+    W = kvr.linear_weights(codes, scale, torch.zeros(4, dtype=torch.int32, device="cuda"))
+    kvr.kvr_linear(W, c, s, torch.empty(0, 32, device="cuda"), torch.empty(256, dtype=torch.uint8, device="cuda"))
+    kvr.kvr_linear_status(W)
+
+
+def test_failed_launches_are_reported(monkeypatch):
+    """Every launch made to fail on the host: an error from each call, the next ones work."""
+    x, (codes, scale) = rows(70, 64, "bf16", 15), empty_codes(70, 64)
+    kvr.kvr_rows_quantise(x, codes, scale)
+    W = kvr.linear_weights(codes, scale, torch.zeros(4, dtype=torch.int32, device="cuda"))
+    out = torch.empty(70, 70, device="cuda")
+    ws = torch.empty(max(kvr.kvr_linear_workspace_bytes(W, n) for n in (4, 40, 70)), dtype=torch.uint8, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    h, p, table = x.view(70, 1, 64), torch.zeros(70, dtype=torch.int32, device="cuda"), torch.empty(8, 32, 2, device="cuda")
+    calls = [lambda: kvr.kvr_rows_quantise(x, codes, scale), lambda: kvr.kvr_rows_dequantise(codes, scale, x),
+             lambda: kvr.kvr_rows_norm(x, w, 1e-5, out=x), lambda: kvr.kvr_rows_swiglu(x, out=torch.empty_like(x[:, :32])),
+             lambda: kvr.kvr_rows_rotate(kvr.rope(64), p, h, h), lambda: kvr.kvr_rope_table(kvr.rope(64), 8, table)] + \
+        [lambda n=n: kvr.kvr_linear(W, codes[:n], scale[:n], out[:n], ws) for n in (4, 40, 70)]
+    monkeypatch.setenv("KVR_FAULT", "launch")
+    for call in calls:
+        with pytest.raises(kvr.KvrError) as e:
+            call()
+        assert e.value.status == kvr.KVR_ECUDA
+    monkeypatch.delenv("KVR_FAULT")
+    for call in calls:
+        call()
+    kvr.kvr_linear_status(W)
+    want = OR.linear(codes.cpu().numpy(), f64(scale), codes.cpu().numpy(), f64(scale))
+    assert np.allclose(f64(out), want, rtol=2.0 ** -20, atol=0)
+
+
+def test_rows_of_every_alignment():
+    """All operands off by every number of elements, apart from one another:
+    the values of aligned rows, and nothing outside."""
+    n, d = 3, 520
+    for dtype in DTYPES:
+        x, res, w = rows(n, d, dtype, 16), rows(n, d, dtype, 17), rows(1, d, dtype, 18)[0]
+        want, wsum = torch.empty_like(x), torch.empty_like(x)
+        codes, scale = empty_codes(n, d)
+        kvr.kvr_rows_norm(x, w, 1e-5, residual=res, sum_out=wsum, out=want, codes=codes, scales=scale)
+        for off in range(8):
+            def at(t, k):
+                flat = torch.full((t.numel() + n * 9 + 32,), 3.0, dtype=t.dtype, device="cuda")
+                v = flat.as_strided((n, t.shape[1]), (t.shape[1] + 9, 1), k)
+                v.copy_(t)
+                return flat, v
+            (_, x2), (_, r2) = at(x, off), at(res, (3 * off + 1) % 8)
+            (fo, o2), (fs, s2) = at(want, (5 * off + 2) % 8), at(wsum, (7 * off + 3) % 8)
+            (fc, c2) = at(codes, off)
+            wo = torch.zeros(d + 8, dtype=w.dtype, device="cuda")
+            wo[off:off + d] = w
+            before = [t.clone() for t in (fo, fs, fc)]
+            for v in (o2, s2, c2):
+                v.zero_()
+            sc = torch.empty(n, device="cuda")
+            kvr.kvr_rows_norm(x2, wo[off:off + d], 1e-5, residual=r2, sum_out=s2, out=o2, codes=c2, scales=sc)
+            assert torch.equal(s2, wsum)
+            check_values(o2, OR.norm(f64(x), f64(w), 1e-5, f64(res))[1], dtype, REL)
+            assert (c2.int() - codes.int()).abs().max() <= 1
+            for flat, old, v in zip((fo, fs, fc), before, (o2, s2, c2)):
+                keep = torch.ones_like(flat, dtype=torch.bool)
+                keep.as_strided(v.shape, v.stride(), v.storage_offset()).fill_(False)
+                assert torch.equal(flat[keep], old[keep])

@@ -14,7 +14,7 @@ kvr = pytest.importorskip("selective_kv_cache_gb300.kvr")
 from paged_case import Paged, check_attend, i32  # noqa: E402
 from test_gpu_rows import check_codes, check_rotated, check_values, f64  # noqa: E402
 
-D, HQ, HK, DH, F = 512, 4, 2, 128, 1536
+D, HQ, HK, DH, F = 512, 4, 2, 128, 1408
 EPS = 1e-5
 
 
