@@ -393,9 +393,9 @@ __global__ void __launch_bounds__(256) rows_dequantise_kernel(const int8_t* code
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
         const int64_t row = total < (int64_t(1) << 31) ? per((uint32_t)t) : t / per.d;
         const int i = (int)(t - row * per.d) * 16;
-        T* o = out + row * out_stride + i;
-        const float s = scales[row];
         const uint4 u = *reinterpret_cast<const uint4*>(codes + row * code_stride + i);
+        const float s = scales[row];
+        T* o = out + row * out_stride + i;
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         float y[16];
         uint32_t packed[2 * kWords<T>];
