@@ -108,9 +108,9 @@ template <typename T, int kLayout, int kBytes>
 __global__ void __launch_bounds__(kThreads, 8) rows_rotate_kernel(const __grid_constant__ RotateDev d) {
     using V = Vec<T, kBytes>;
     constexpr int N = V::N, kBatch = kBatchOf<kBytes>;
-    extern __shared__ float2 cs[];   // [rows_per_block][rotary_dim / 2]
+    extern __shared__ float2 cs[];   // [rows_per_block][N][turned units]: pair e of every unit side by side, for the banks' sake
     const RowsRotate& a = d.a;
-    const int dh = a.rope.head_dim, half = a.rope.rotary_dim / 2;
+    const int dh = a.rope.head_dim, half = a.rope.rotary_dim / 2, turned = d.turned;
     const int64_t row0 = (int64_t)blockIdx.x * d.rows_per_block;
     const int rows = (int)min((int64_t)d.rows_per_block, a.n_rows - row0);
     const int total = rows * d.heads * d.units;
@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, 8) rows_rotate_kernel(const __grid_c
         }
         if (!ready) {
             for (int i = threadIdx.x; i < rows * half; i += kThreads) {
-                const int r = i / half;
-                cs[i] = cos_sin(a.rope.turns[i - r * half], a.pos[row0 + r], d.m, a.inverse);
+                const int r = i / half, p = i - r * half;
+                cs[r * half + p % N * turned + p / N] = cos_sin(a.rope.turns[p], a.pos[row0 + r], d.m, a.inverse);
             }
             __syncthreads();
             ready = true;
@@ -156,15 +156,15 @@ __global__ void __launch_bounds__(kThreads, 8) rows_rotate_kernel(const __grid_c
                 float p[N], q[N];
                 x[k][0].get(p);
                 x[k][1].get(q);
-                const float2* c = cs + row[k] * half;
+                const float2* c = cs + row[k] * half + unit[k];
                 if constexpr (kLayout == KVR_ROPE_HALF) {
 #pragma unroll
-                    for (int e = 0; e < N; ++e) turn(p[e], q[e], c[unit[k] * N + e]);
+                    for (int e = 0; e < N; ++e) turn(p[e], q[e], c[e * turned]);
                 } else {
 #pragma unroll
                     for (int e = 0; e < N / 2; ++e) {
-                        turn(p[2 * e], p[2 * e + 1], c[unit[k] * N + e]);
-                        turn(q[2 * e], q[2 * e + 1], c[unit[k] * N + N / 2 + e]);
+                        turn(p[2 * e], p[2 * e + 1], c[e * turned]);
+                        turn(q[2 * e], q[2 * e + 1], c[(N / 2 + e) * turned]);
                     }
                 }
                 x[k][0].put(p);
