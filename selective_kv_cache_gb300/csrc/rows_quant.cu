@@ -436,24 +436,24 @@ __global__ void __launch_bounds__(256) rows_dequantise_any_kernel(const int8_t* 
 }
 
 // Blocks of a kernel that the GPU holds at once, asked for once per block size.
-template <typename K>
-int resident(K kernel, int threads) {
+template <auto kKernel>
+int resident(int threads) {
     static std::atomic<uint32_t> seen{0};   // threads, blocks an SM
     const uint32_t v = seen.load(std::memory_order_relaxed);
     if ((int)(v >> 16) == threads) return (int)(v & 0xffffu) * kNumSMs;
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, threads, 0) != cudaSuccess || n < 1) n = 1;
     seen.store((uint32_t)threads << 16 | (uint32_t)n, std::memory_order_relaxed);
     return n * kNumSMs;
 }
 
 template <RowOp kOp, typename T, bool kAligned, int kSlots, bool kWarp>
 cudaError_t launch_with(const RowsQuant& a, int units, cudaStream_t s) {
-    const auto kernel = rows_quant_kernel<kOp, T, kAligned, kSlots, kWarp>;
+    constexpr auto kernel = rows_quant_kernel<kOp, T, kAligned, kSlots, kWarp>;
     const int slots = std::max(kSlots, 1);
     const int threads = kWarp ? 128 : kSlots == 0 ? 1024 : ((units + slots - 1) / slots + 31) / 32 * 32;
     const int blocks = kWarp ? (int)((a.n_rows + int64_t(3)) / 4) : a.n_rows;
-    KVR_LAUNCH(kernel, dim3(std::min(blocks, resident(kernel, threads))), dim3(threads), 0, s, a);
+    KVR_LAUNCH(kernel, dim3(std::min(blocks, resident<kernel>(threads))), dim3(threads), 0, s, a);
     return cudaSuccess;
 }
 
