@@ -833,8 +833,8 @@ kvr_status kvr_rows_rotate(const kvr_rope* rope, int32_t dtype, int32_t n_rows, 
  * device pointers, one weight matrix in nn.Linear layout (a row an output
  * channel, as kvr_rows_quantise leaves it); nothing is owned or kept.
  *   codes       device int8 [n_rows][k], stride bytes apart; 16-byte aligned,
- *               stride a multiple of 16, for the weights too.  Codes may be
- *               -128 to 127.  k up to 65536 and n_out up to 2^20, any size.
+ *               stride a multiple of 16, for the weights too (a row's last 16
+ *               bytes are read whole).  Codes may be -128 to 127.  k up to 65536 and n_out up to 2^20, any size.
  *   out         device [n_rows][n_out], out_stride elements apart; it does not
  *               overlap an input.
  *   workspace   device, >= kvr_linear_workspace_bytes(w, n_rows), 256-byte

@@ -33,14 +33,21 @@ __device__ __forceinline__ uint4 load_stream(const int8_t* p) {   // weights: re
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
-// the bytes of [p, p + 16) that lie before the end of the row, zeros behind
-__device__ __forceinline__ uint4 load_tail(const int8_t* p, int left) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+// The row's last pieces: one that holds a code lies in the row up to 16-byte
+// alignment.  The rows' codes behind k are made zeros, the weights' then do not count.
+__device__ __forceinline__ uint4 load_tail(const int8_t* p, int left, bool zeros) {
+    uint4 v = left > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+    if (zeros) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < left) w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; ++i) {
+            const int n = left - 4 * i;
+            w[i] = n >= 4 ? w[i] : n <= 0 ? 0u : w[i] & (0xffffffffu >> (32 - 8 * n));
+        }
+    }
+    return v;
 }
+
 __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ Linear a, int split) {
     constexpr int kTile = kFeatures * kRows;
     __shared__ int part[kWarps][kTile];
@@ -83,8 +90,8 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
 #pragma unroll
         for (int m = 0; m < kMT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) w[m][h] = load_tail(wp[m][h] + at, left);
-        products(w, load_tail(xp + at, left));
+            for (int h = 0; h < 2; ++h) w[m][h] = load_tail(wp[m][h] + at, left, false);
+        products(w, load_tail(xp + at, left, true));
     }
 #pragma unroll
     for (int m = 0; m < kMT; ++m)

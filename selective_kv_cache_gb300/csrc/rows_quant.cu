@@ -252,8 +252,8 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, int turn) 
 
 // Threads of a block at most, and blocks an SM at least.  Rows of bf16 leave
 // registers for the next row's units beside this one's.
-constexpr int block_most(int slots, bool warp, int size) {
-    return warp ? 128 : slots == 1 ? 256 : slots == 2 ? 512 : slots == 4 && size == 2 ? 640 : 1024;
+constexpr int block_most(int slots, bool warp, int size, bool aligned) {
+    return warp ? 128 : slots == 1 ? 256 : slots == 2 ? (aligned ? 512 : 1024) : slots == 4 && size == 2 ? 640 : 1024;
 }
 constexpr int blocks_least(int slots, bool warp, int size, bool aligned) {
     return warp ? (slots == 1 ? 8 : 5) : slots == 1 ? 4 : slots == 2 && size == 2 && aligned ? 2 : 1;
@@ -262,11 +262,11 @@ constexpr int blocks_least(int slots, bool warp, int size, bool aligned) {
 // kSlots: units a thread holds of a row, 0: the row is read twice.  kWarp: a
 // warp a row, several rows a block; else a block a row.
 template <RowOp kOp, typename T, bool kAligned, int kSlots, bool kWarp>
-__global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T)), blocks_least(kSlots, kWarp, sizeof(T), kAligned))
+__global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T), kAligned), blocks_least(kSlots, kWarp, sizeof(T), kAligned))
     rows_quant_kernel(const __grid_constant__ RowsQuant a) {
     constexpr bool kNorm = kOp == RowOp::Norm;
-    // the next row's loads go out before this one's exchange
-    constexpr bool kAhead = kSlots > 0 && sizeof(T) == 2;
+    // the next row's loads go out before this one's exchange; units that are shifted would wait for them there
+    constexpr bool kAhead = kSlots > 0 && sizeof(T) == 2 && kAligned;
     constexpr bool kKeepW = kNorm && (kSlots == 1 || kSlots == 2);   // else the weights are read for every row, from L1
     constexpr int kHold = kSlots > 0 ? kSlots : 1;
     const int lane = kWarp ? threadIdx.x & 31 : threadIdx.x, step = kWarp ? 32 : blockDim.x;
@@ -471,7 +471,7 @@ cudaError_t launch_as(const RowsQuant& a, cudaStream_t s) {
         if (units <= 256) return launch_with<kOp, T, kAligned, 1, false>(a, units, s);
     }
     if constexpr (!kMost) {
-        if (units <= 1024) return launch_with<kOp, T, kAligned, 2, false>(a, units, s);
+        if (units <= (kAligned || sizeof(T) == 4 ? 1024 : 2048)) return launch_with<kOp, T, kAligned, 2, false>(a, units, s);
     }
     if (units <= 2560) return launch_with<kOp, T, kAligned, 4, false>(a, units, s);
     return launch_with<kOp, T, kAligned, 0, false>(a, units, s);
