@@ -10,16 +10,15 @@
 // and the cluster's blocks take every 64-byte step in turn, so that they read
 // neighbouring bytes at a time, and the partial sums meet in shared memory, the
 // cluster's over distributed shared memory: one launch, no workspace, any order
-// of addition the same integer.
-#include <algorithm>
-
+// of addition the same integer.  A warp holds two steps in registers and loads
+// each again right after its products, three blocks on an SM.
 #include "linear.cuh"
 
 namespace kvr {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRows = kLinearMmaRows, kUnroll = 4;   // rows of a block; 64-byte steps a warp has in flight
+constexpr int kRows = kLinearMmaRows, kUnroll = 2;   // rows of a block; 64-byte steps a warp has in flight
 constexpr int kMT = 2, kFeatures = 16 * kMT;   // weight tiles of a warp, features of a block
 
 __device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -48,7 +47,7 @@ __device__ __forceinline__ uint4 load_tail(const int8_t* p, int left, bool zeros
     return v;
 }
 
-__global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_constant__ Linear a, int split) {
+__global__ void __launch_bounds__(kThreads, 3) linear_mma_kernel(const __grid_constant__ Linear a, int split) {
     constexpr int kTile = kFeatures * kRows;
     __shared__ int part[kWarps][kTile];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -69,20 +68,25 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
         }
     };
     const int steps = a.k / 64, stride = kWarps * split;
-    for (int s = rank * kWarps + warp; s < steps; s += stride * kUnroll) {
-        uint4 w[kUnroll][kMT][2], x[kUnroll];
+    // a ring of kUnroll steps in registers: each is loaded again as soon as its products are out
+    uint4 w[kUnroll][kMT][2], x[kUnroll];
+    auto fetch = [&](int u, int step) {
+#pragma unroll
+        for (int m = 0; m < kMT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[u][m][h] = load_stream(wp[m][h] + 64 * step);
+        x[u] = *reinterpret_cast<const uint4*>(xp + 64 * step);
+    };
+    const int first = rank * kWarps + warp;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        if (first + u * stride < steps) fetch(u, first + u * stride);
+    for (int s = first; s < steps; s += stride * kUnroll) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int at = 64 * min(s + u * stride, steps - 1);   // a step past the end is loaded, not used
-#pragma unroll
-            for (int m = 0; m < kMT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) w[u][m][h] = load_stream(wp[m][h] + at);
-            x[u] = *reinterpret_cast<const uint4*>(xp + at);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
             if (s + u * stride < steps) products(w[u], x[u]);
+            if (s + (u + kUnroll) * stride < steps) fetch(u, s + (u + kUnroll) * stride);
+        }
     }
     if (rank == split - 1 && warp == kWarps - 1 && a.k % 64) {
         const int at = 64 * steps, left = a.k - at - 16 * t;
@@ -122,9 +126,11 @@ __global__ void __launch_bounds__(kThreads) linear_mma_kernel(const __grid_const
 
 cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s) {
     const int groups = (a.n_out + kFeatures - 1) / kFeatures, steps = a.k / 64;
-    // blocks for every SM twice over, as long as a warp has a batch of steps
+    // The fewest shares of K that give the SMs one and a half blocks each, as long as a warp keeps
+    // two steps: 14336 -> 4096 one share 20.2 us, two 15.0, three 14.8, four 17.8, eight 20.8;
+    // 18944 -> 3584 25.2, 18.5, 18.0, 20.9, 22.7; 8960 -> 1536 one 12.3, three 7.7, five 6.9, eight 8.3.
     int split = 1;
-    while (split < 8 && groups * split < 2 * kNumSMs && steps >= 2 * split * kWarps * 2) split *= 2;
+    while (split < 8 && 2 * groups * split < 3 * kNumSMs && steps >= 2 * (split + 1) * kWarps) ++split;
     return launch_clusters(split, linear_mma_kernel, dim3(groups * split), dim3(kThreads), 0, s, a, split);
 }
 

@@ -61,8 +61,8 @@ kvr_status check_weights(const kvr_linear_weights* w) {
 }
 // Which kernel a call takes, measured on GB300 with weights from HBM (us):
 //   rows x k -> n_out        integer    batch    tiles
-//    8 x  4096 ->  6144          8.6     11.0     17.4
-//    8 x  4096 -> 28672         23.8     25.6     31.4
+//    8 x  4096 ->  6144          8.2     11.0     17.4
+//    8 x  4096 -> 28672         22.7     25.6     31.4
 //    9 x  4096 ->  6144         12.0     11.0     17.4
 //   16 x 14336 ->  4096         25.1     15.8     42.1
 //   64 x  4096 ->  6144                  13.9     17.7
