@@ -733,8 +733,8 @@ kvr_status kvr_paged_status(const kvr_pages* p, void* stream);
  * least a row's width.  Rows of any width and of any alignment of their elements
  * are taken; 16-byte aligned pointers and strides (codes: 8) are the faster.  A
  * row's last or first aligned 16 bytes may be read past it, never written.
- * Widths go up to 2^20, rows to 2^31 - 1, strides to 2^29.  Sums, maxima and products are fp32
- * (|h| stays below 2^60, so that its squares do not overflow).  Where an
+ * Widths go up to 2^20, rows to 2^31 - 1, strides to 2^29.  Sums, maxima and
+ * products are fp32 (|h| stays below 2^60, so that its squares do not overflow).  Where an
  * output may be an input, it is that array from its first element on, with
  * the same stride; arrays do not overlap otherwise.
  * Nothing is kept between calls, so all of them can be captured.
@@ -834,13 +834,15 @@ kvr_status kvr_rows_rotate(const kvr_rope* rope, int32_t dtype, int32_t n_rows, 
  * channel, as kvr_rows_quantise leaves it); nothing is owned or kept.
  *   codes       device int8 [n_rows][k], stride bytes apart; 16-byte aligned,
  *               stride a multiple of 16, for the weights too (a row's last 16
- *               bytes are read whole).  Codes may be -128 to 127.  k up to 65536 and n_out up to 2^20, any size.
+ *               bytes are read whole).  Codes may be -128 to 127.  k up to
+ *               65536 and n_out up to 2^20, any size.
  *   out         device [n_rows][n_out], out_stride elements apart; it does not
  *               overlap an input.
  *   workspace   device, >= kvr_linear_workspace_bytes(w, n_rows), 256-byte
- *               aligned; needs no initialisation.  Calls whose GPU work
- *               overlaps need a workspace each.
- * Up to 16 rows the sums are 32-bit integers; for more rows they are formed by
+ *               aligned; needs no initialisation.  One for the most rows
+ *               serves fewer too.  Calls whose GPU work overlaps need a
+ *               workspace each.
+ * Up to 8 rows the sums are 32-bit integers; for more rows they are formed by
  * the tensor cores in fp32, which holds them exactly up to 2^24 and rounds
  * each step above that to 2^-24 of itself.  The same inputs give the same
  * bits.  A row or channel whose scale is NaN is NaN.

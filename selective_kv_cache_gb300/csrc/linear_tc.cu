@@ -395,8 +395,10 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     }
 }
 
+int pitch_of(int k) { return (k + 7) / 8 * 8; }   // elements of a widened row
+
 struct Plan {
-    int N, m_tiles, n_tiles, KB, stages, pitch, tiles, pairs;
+    int N, m_tiles, n_tiles, KB, stages, tiles, pairs;
     double cycles;
 };
 // The width of a tile that takes the shortest time in cycles: a stage of 128
@@ -406,7 +408,6 @@ Plan make_plan(int n_out, int k, int n_rows) {
     Plan p{};
     p.m_tiles = (n_out + 255) / 256;
     p.KB = (k + kStageK - 1) / kStageK;
-    p.pitch = (k + 7) / 8 * 8;
     double least = 1e300;
     for (int N = 32; N <= 256; N += 32) {
         const int n_tiles = (n_rows + N - 1) / N;
@@ -428,12 +429,11 @@ Plan make_plan(int n_out, int k, int n_rows) {
 
 double linear_tc_us(int n_out, int k, int n_rows) { return 5.5 + make_plan(n_out, k, n_rows).cycles / 1900; }
 
-size_t linear_tc_workspace(int n_out, int k, int n_rows) {
-    return (size_t)n_rows * make_plan(n_out, k, n_rows).pitch * 2;
-}
+size_t linear_tc_workspace(int k, int n_rows) { return (size_t)n_rows * pitch_of(k) * 2; }
 
 cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) {
     const Plan p = make_plan(a.n_out, a.k, a.n_rows);
+    const int pitch = pitch_of(a.k);
     LinearTc g{};
     g.a = a;
     __half* rows = static_cast<__half*>(a.workspace);
@@ -451,11 +451,11 @@ cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why) 
     g.base1 = g.shared_cols ? g.col_a - p.N : p.N;
     CUtensorMap ta, tb;
     if (!make_tmap_2d_sw128(&ta, 1, a.w, a.k, a.n_out, a.w_stride, kStageK, 128, why) ||
-        !make_tmap_2d_sw128(&tb, 2, rows, a.k, a.n_rows, (uint64_t)p.pitch * 2, 64, p.N / 2, why))
+        !make_tmap_2d_sw128(&tb, 2, rows, a.k, a.n_rows, (uint64_t)pitch * 2, 64, p.N / 2, why))
         return cudaErrorInvalidValue;
     const int64_t units = (int64_t)a.n_rows * ((a.k + 15) / 16);
     KVR_LAUNCH(widen_kernel, dim3((unsigned)std::min<int64_t>((units + 255) / 256, 16 * kNumSMs)), dim3(256), 0, s, a.x,
-               a.x_stride, rows, p.pitch, a.k, a.n_rows);
+               a.x_stride, rows, pitch, a.k, a.n_rows);
     const size_t smem = 1024 + (size_t)p.stages * (kStageA + p.N * 128) + 1024;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(linear_tc_kernel, kSmemMost, &done);

@@ -1,6 +1,6 @@
 // rows.h -- packed-row operators: norms and gates into eight bits, the rotary
 // map, and projections by 8-bit weights (rows_api.cu, rows_quant.cu,
-// rows_rotate.cu, linear.cu).
+// rows_rotate.cu, linear_*.cu).
 #pragma once
 #include "kvr_internal.h"
 
@@ -71,7 +71,7 @@ double linear_few_us(int n_out, int k, int n_rows);   // estimated time
 cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why);
 // Many rows; needs linear_tc_workspace bytes of workspace.
 double linear_tc_us(int n_out, int k, int n_rows);
-size_t linear_tc_workspace(int n_out, int k, int n_rows);
+size_t linear_tc_workspace(int k, int n_rows);
 cudaError_t launch_linear_tc(const Linear& a, cudaStream_t s, std::string* why);
 
 cudaError_t launch_rope_table(const kvr_rope& rope, int rope_len, float2* table, cudaStream_t s);

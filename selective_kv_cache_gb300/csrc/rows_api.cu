@@ -83,8 +83,9 @@ LinearWay linear_way(int n_out, int k, int n_rows) {
     if (n_rows <= 64) return LinearWay::Few;
     return n_rows <= 4096 && linear_few_us(n_out, k, n_rows) < linear_tc_us(n_out, k, n_rows) ? LinearWay::Few : LinearWay::Tc;
 }
+// grows with n_rows, whichever kernel takes them
 size_t linear_workspace(const kvr_linear_weights& w, int32_t n_rows) {
-    return linear_way(w.n_out, w.k, n_rows) == LinearWay::Tc ? linear_tc_workspace(w.n_out, w.k, n_rows) : 256;
+    return std::max<size_t>(256, n_rows > 64 ? linear_tc_workspace(w.k, n_rows) : 0);
 }
 
 kvr_status check_rope(const kvr_rope* r) {

@@ -731,7 +731,6 @@ def kvr_rope_init(head_dim: int, rotary_dim: int, layout: int, scaling: int, the
     r = kvr_rope()
     _check(lib.kvr_rope_init(C.byref(r), head_dim, rotary_dim, layout, scaling, theta, factor, low, high, original_len,
                              attn_factor), "kvr_rope_init")
-    r.addr = C.addressof(r)
     return r
 
 
@@ -751,7 +750,7 @@ def kvr_rope_table(r: kvr_rope, rope_len: int, table, stream=None):
     """table: contiguous fp32 [rope_len, rotary_dim / 2, 2]."""
     if _want(table, "table", torch.float32).shape != (rope_len, r.rotary_dim // 2, 2) or not table.is_contiguous():
         raise ValueError(f"table: need a contiguous [{rope_len}, {r.rotary_dim // 2}, 2]")
-    _check(lib.kvr_rope_table(r.addr, rope_len, table.data_ptr(), _row_stream(table.get_device(), stream)), "kvr_rope_table")
+    _check(lib.kvr_rope_table(C.addressof(r), rope_len, table.data_ptr(), _row_stream(table.get_device(), stream)), "kvr_rope_table")
 
 
 def _heads(t, what: str, n: int, dh: int, dtype, dev: int):
@@ -791,7 +790,7 @@ def kvr_rows_rotate(r: kvr_rope, positions, q=None, q_out=None, k=None, k_out=No
         ko = ka if k_out is k else _heads(k_out, "k_out", n, dh, t, dev)
     if qo[2] != qa[2] or ko[2] != ka[2]:
         raise ValueError("q_out, k_out: need the heads of q and k")
-    _check(lib.kvr_rows_rotate(r.addr, _DTYPES[t], n, pp, *qa, qo[0], qo[1], *ka, ko[0], ko[1],
+    _check(lib.kvr_rows_rotate(C.addressof(r), _DTYPES[t], n, pp, *qa, qo[0], qo[1], *ka, ko[0], ko[1],
                                KVR_ROPE_INVERSE if inverse else 0, s), "kvr_rows_rotate")
 
 

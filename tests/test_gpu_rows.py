@@ -11,6 +11,9 @@ before the quantiser is off by rel |y|:
           division by 2^-22; |g| <= 40 here: below 2^-17.  fp32: 2^-20.
 A code is off its value's place by at most half a step and 127 times three
 roundings (1/127, 1 / scale, the product): 0.5 + 2^-14 steps; a scale by rel."""
+import copy
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -330,6 +333,25 @@ def test_rows_follow_their_stream_and_replay():
     step(None)
     torch.cuda.synchronize()
     check_codes(c2, s2, f64(x), 0.0)
+
+
+def test_rotate_by_copied_and_by_filled_maps():
+    """A kvr_rope is plain data: a copy outlives its original, and a caller may fill one."""
+    n, dh = 5, 64
+    x = rows(n, 3 * dh, "f32", 15).view(n, 3, dh)
+    pos = torch.arange(7, 7 + n, dtype=torch.int32, device="cuda")
+    want = torch.empty_like(x)
+    kvr.kvr_rows_rotate(kvr.rope(dh), pos, x, want)
+    first = kvr.rope(dh)
+    copied = copy.copy(first)
+    ctypes.memset(ctypes.addressof(first), 0, ctypes.sizeof(first))
+    filled = kvr.kvr_rope(dh, dh, 0, 1.0)
+    for i in range(dh // 2):
+        filled.turns[i] = copied.turns[i]
+    for r in (copied, filled):
+        out = torch.empty_like(x)
+        kvr.kvr_rows_rotate(r, pos, x, out)
+        assert torch.equal(out, want)
 
 
 def test_many_rows():

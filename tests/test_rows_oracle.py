@@ -114,7 +114,7 @@ def test_swiglu_quantise_and_dequantise_refuse():
 
 def test_rotate_and_table_refuse():
     r = kvr.rope(128)
-    good = dict(rope=r.addr, dtype=1, n=0, pos=P1, q=P1, qs=512, hq=4, qo=P1, qos=512, k=P1, ks=256, hk=2, ko=P1, kos=256,
+    good = dict(rope=ctypes.addressof(r), dtype=1, n=0, pos=P1, q=P1, qs=512, hq=4, qo=P1, qos=512, k=P1, ks=256, hk=2, ko=P1, kos=256,
                 flags=0, stream=None)
     assert lib.kvr_rows_rotate(*good.values()) == kvr.KVR_OK
     none = dict(q=None, hq=0, qo=None)
@@ -128,8 +128,8 @@ def test_rotate_and_table_refuse():
                    dict(hq=-1), dict(hq=65536), dict(hk=0), dict(k=None, ko=None), dict(ko=P3), dict(kos=255),
                    dict(flags=2), dict(n=2, qos=520), {**none, "k": None, "hk": 0, "ko": None}):
         assert refused(lib.kvr_rows_rotate, good, **change), change
-    assert lib.kvr_rope_table(r.addr, 0, P1, None) == kvr.KVR_OK
-    for a in ((None, 4, P1, None), (r.addr, -1, P1, None), (r.addr, 4, None, None), (r.addr, 4, P1 + 4, None)):
+    assert lib.kvr_rope_table(ctypes.addressof(r), 0, P1, None) == kvr.KVR_OK
+    for a in ((None, 4, P1, None), (ctypes.addressof(r), -1, P1, None), (ctypes.addressof(r), 4, None, None), (ctypes.addressof(r), 4, P1 + 4, None)):
         assert lib.kvr_rope_table(*a) == kvr.KVR_EINVAL
 
 
@@ -183,3 +183,11 @@ def test_linear_refuses():
     s = kvr.kvr_linear_weights(*good.values())
     assert lib.kvr_linear_workspace_bytes(ctypes.addressof(s), 0) == 0
     assert lib.kvr_linear_status(None, None) == kvr.KVR_EINVAL
+
+
+@pytest.mark.parametrize("n_out,k", [(1, 1), (2048, 1536), (4096, 14336), (28672, 4096)])
+def test_linear_workspace_grows_with_the_rows(n_out, k):
+    """A program that sizes it for its largest batch calls with fewer rows too."""
+    s = kvr.kvr_linear_weights(n_out, k, -(-k // 16) * 16, P1, P1, None, P1)
+    sizes = [lib.kvr_linear_workspace_bytes(ctypes.addressof(s), n) for n in range(1, 6000)]
+    assert sizes[0] >= 1 and all(a <= b for a, b in zip(sizes, sizes[1:]))
