@@ -8,14 +8,23 @@
 // and the fp32 sums up to 2^24 are exact): the weights into tensor memory, the A
 // operand, the rows into shared memory.  A cluster's blocks split k, and join
 // their sums as integers over distributed shared memory: nothing goes through
-// the workspace.  Two blocks an SM, so that one streams while the other starts
-// or ends.
+// the workspace.
 //   warp 0     TMA: per stage 128 features x 128 codes and N rows x 128 codes
 //   warp 1     products, eight of K = 16 a stage
-//   warps 2-9  widening, in two sets of four that take the stages in turn, each
-//              into a slot of its own: a thread a feature and up to four pieces of
-//              the rows; then they write the sums out
-// Every wait is bounded.
+//   warps 2..  widening, in sets of four that take the stages in turn, each into
+//              a slot of its own: a thread a feature and up to four pieces of the
+//              rows; then they write the sums out
+// A stage is bound by its widened weights' way into tensor memory (770 cycles),
+// which takes four sets to keep busy.  They are one block of four sets an SM, or
+// two blocks of two, so that one streams while the other starts or ends
+// (make_plan).  A block's shared memory leaves no room on its SM for more
+// tensor memory than there is, so blocks of other clusters do not wait for one
+// another's.  Every wait is bounded.
+//
+// Where 18.8 us of 64 rows, 14336 -> 4096 go (clock64, cycles): setting up 1800,
+// the first stage's copies 5200 from the start, 28 stages to 25500, products and
+// sums out 28700, the cluster 29800, the join over distributed shared memory
+// 31900, the end 32600.
 #include <algorithm>
 
 #include "linear.cuh"
@@ -24,19 +33,27 @@
 namespace kvr {
 namespace {
 
-constexpr int kSets = 2, kThreads = 64 + 128 * kSets;
 constexpr uint32_t kStageA = 128 * 128;
-constexpr uint32_t kCols = 256, kColA = 64;   // accumulator (up to 64 columns), then a slot of 64 columns for each set
-constexpr int kSmemMost = 113 * 1024;         // two blocks an SM
+constexpr uint32_t kColA = 64;   // columns: the accumulator (up to 64), then a slot of 64 for each set
+// by the number of sets: a block's threads, blocks an SM, columns, shared memory
+template <int kSets>
+constexpr int kThreadsOf = 64 + 128 * kSets;
+template <int kSets>
+constexpr int kBlocksOf = kSets == 2 ? 2 : 1;
+template <int kSets>
+constexpr int kSmemOf = (kSets == 2 ? 113 : 227) * 1024;
 
 struct LinearFew {
     Linear a;
     int N, split, KB, stages, out_as, vec;   // vec: four features of an output row are one aligned store
 };
 
-__global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_constant__ CUtensorMap tmA,
-                                                                const __grid_constant__ CUtensorMap tmB,
-                                                                const __grid_constant__ LinearFew g) {
+template <int kSets>
+__global__ void __launch_bounds__(kThreadsOf<kSets>, kBlocksOf<kSets>)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ LinearFew g) {
+    constexpr int kThreads = kThreadsOf<kSets>;
+    constexpr uint32_t kCols = kSets == 2 ? 256 : 512;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stages = g.stages;
@@ -59,17 +76,21 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
         tma_load_2d(d + kStageA, &tmB, &full[s], (kb0 + it) * 128, row0);
     };
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 4);
+    if (warp == 0) {
+        // a barrier a lane: one thread takes 50 cycles for each
+        if (lane < stages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 4);
+        } else if (lane >= 16 && lane < 16 + kSets) {
+            mbar_init(&ready[lane - 16], 4);
+            mbar_init(&freed[lane - 16], 1);
+        } else if (lane == 31) {
+            mbar_init(done, 1);
         }
-        for (int t = 0; t < kSets; ++t) {
-            mbar_init(&ready[t], 4);
-            mbar_init(&freed[t], 1);
-        }
-        mbar_init(done, 1);
         fence_mbar_init();
+        __syncwarp();
+    }
+    if (threadIdx.x == 0) {
         for (int it = 0; it < min(stages, n_kb); ++it) copies(it, it);   // the ring fills while the block sets up
     }
     if (warp == 1) {
@@ -210,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
             tc_fence_after();
             const int f = f0 + row;
             const float sw = f < g.a.n_out ? g.a.w_scale[f] : 0.f, bias = f < g.a.n_out && g.a.bias ? g.a.bias[f] : 0.f;
-            for (int c = 32 * set; c < g.N; c += 64) {
+            for (int c = 32 * set; c < g.N; c += 32 * kSets) {
                 float v[32];
                 tmem_ld32(dst + (uint32_t)c, v);
                 if (split == 1) {
@@ -236,9 +257,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
             sw[i] = f + i < g.a.n_out ? g.a.w_scale[f + i] : 0.f;
             bias[i] = f + i < g.a.n_out && g.a.bias ? g.a.bias[f + i] : 0.f;
         }
+        constexpr int kWarps = kThreads / 32;   // at most 64 rows: a lane holds the scale of one of its warp's
+        const int mine = r0 + warp + kWarps * lane;
+        const float scales = mine < r1 ? g.a.x_scale[row0 + mine] : 0.f;
         cluster_sync();
-        for (int r = r0 + warp; r < r1; r += kThreads / 32) {
-            const float sx = g.a.x_scale[row0 + r];
+        for (int r = r0 + warp, i = 0; r < r1; r += kWarps, ++i) {
+            const float sx = __shfl_sync(0xffffffffu, scales, i);
             float4 v[8];
 #pragma unroll
             for (int p = 0; p < 8; ++p)
@@ -257,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
             for (int i = 0; i < 4; ++i) y[i] = (float)sum[i] * sx * sw[i] + bias[i];
             write4(g.a, g.vec, row0 + r, f, y);
         }
-        cluster_sync();   // no block leaves while another reads its sums
+        cluster_leave();   // no block leaves while another reads its sums
     } else {
         __syncthreads();
     }
@@ -271,8 +295,32 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
 
 namespace {
 struct Plan {
-    int row_tiles, N, tiles, KB, split, waves;
+    int row_tiles, N, tiles, KB, sets, split, waves;
 };
+
+// Clusters of `split` blocks of four sets that the GPU holds at once: a cluster's blocks share a GPC.
+int clusters_at_once(int split) {
+    static std::atomic<int> known[9];
+    int n = known[split].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    static std::atomic<uint64_t> done{0};
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(kThreadsOf<4>);
+    cfg.dynamicSmemBytes = kSmemOf<4>;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (allow_smem(linear_few_kernel<4>, kSmemOf<4>, &done) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, linear_few_kernel<4>, &cfg) != cudaSuccess || n < 1)
+        return 0;
+    known[split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 Plan make_plan(int n_out, int k, int n_rows) {
     Plan p{};
     p.row_tiles = (n_rows + 63) / 64;
@@ -280,10 +328,20 @@ Plan make_plan(int n_out, int k, int n_rows) {
     p.tiles = (n_out + 127) / 128;
     p.KB = (k + 127) / 128;
     const long long blocks = (long long)p.tiles * p.row_tiles;
-    // Blocks a cluster.  A block an SM as long as each has two stages, two an SM where each keeps six; all of them
-    // resident at once.  64 rows (us): 4096 -> 6144 in ones 23, twos 16, fours 14, eights, which a second wave follows, 19;
-    // 4096 -> 4096 in fours 11.8, eights 12.4; 14336 -> 4096 in fours 25, eights 21; 1536 -> 2048 in twos 8.8, fours 7.2,
-    // eights 8.7.  Threes and sixes fit the GPCs badly.
+    // Four sets, where all clusters fit at once and a block keeps six stages, eight up to 32 rows: 64 rows, 14336 -> 4096
+    // in fours 18.5 us (two sets in eights 20.3); 18944 -> 3584 in fives 20.3 (23.5); 4096 -> 4096 in fours 10.2 (11.2);
+    // 3584 -> 4608 in fours 10.3 (11.1); 48 rows, 4096 -> 12288 unsplit 16.4 (19.4).  Up to 16 rows, and with fewer
+    // stages, two sets are as fast or faster.
+    if (p.N > 16 && blocks <= kNumSMs) {
+        p.sets = 4;
+        p.waves = 1;
+        for (p.split = std::min(8, std::max(1, p.KB / 4)); p.split > 1; --p.split)
+            if (blocks * p.split <= kNumSMs && blocks <= clusters_at_once(p.split)) break;
+        if (p.KB >= (p.N > 32 ? 6 : 8) * p.split) return p;
+    }
+    p.sets = 2;
+    // Two sets: a block an SM as long as each has two stages, two an SM where each keeps six; all of them resident at
+    // once.  1536 -> 2048 in twos 8.5 us, fours 6.7, eights 8.4.  Threes and sixes fit the GPCs badly.
     p.split = 1;
     while (p.split < 8 && ((2 * p.split * blocks <= kNumSMs && p.KB >= 4 * p.split) ||
                            (2 * p.split * blocks <= 2 * kNumSMs && p.KB >= 12 * p.split)))
@@ -291,14 +349,36 @@ Plan make_plan(int n_out, int k, int n_rows) {
     p.waves = (int)std::min<long long>(1 << 20, (blocks * p.split + 2 * kNumSMs - 1) / (2 * kNumSMs));
     return p;
 }
+
+template <int kSets>
+cudaError_t launch(LinearFew& g, const Plan& p, cudaStream_t s, std::string* why) {
+    const Linear& a = g.a;
+    const uint32_t tile = g.N * 128, stage = kStageA + tile;
+    const uint32_t fixed = 1024 + 2 * kSets * tile + 512;   // the ring's size also holds the [N][128] sums
+    // A multiple of the sets, so that a stage always belongs to the same one: a set that skipped a stage's earlier
+    // use could not tell its phases apart.
+    g.stages = std::min(8, (kSmemOf<kSets> - 1024 - (int)fixed) / (int)stage / kSets * kSets);
+    g.out_as = out_kind(a);
+    g.vec = out_vec4(a);
+    CUtensorMap ta, tb;
+    if (!make_tmap_2d_sw128(&ta, 1, a.w, a.k, a.n_out, a.w_stride, 128, 128, why) ||
+        !make_tmap_2d_sw128(&tb, 1, a.x, a.k, a.n_rows, a.x_stride, 128, g.N, why))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(linear_few_kernel<kSets>, kSmemOf<kSets>, &done);
+    if (e != cudaSuccess) return e;
+    return launch_clusters((unsigned)g.split, linear_few_kernel<kSets>, dim3(p.tiles * p.split, p.row_tiles),
+                           dim3(kThreadsOf<kSets>), fixed + (size_t)g.stages * stage, s, ta, tb, g);
+}
 }  // namespace
 
 double linear_few_us(int n_out, int k, int n_rows) {
     const Plan p = make_plan(n_out, k, n_rows);
-    // starting and joining, and a stage: with one block on the busiest SM, with two
+    // starting and joining, and a stage: of four sets, of two with one block on the busiest SM, with two
     const int stages = (p.KB + p.split - 1) / p.split;
+    if (p.sets == 4) return (p.split > 1 ? 7.0 : 6.0) + (0.27 + 0.1 / 32 * std::max(0, p.N - 32)) * stages;
     const bool two = (long long)p.tiles * p.row_tiles * p.split > kNumSMs;
-    return (two ? 8.5 : 5.5) + (two ? 0.74 : 0.64) * p.waves * stages;
+    return (two ? 8.0 : 5.5) + (two ? 0.74 : 0.64) * p.waves * stages;
 }
 
 cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why) {
@@ -308,22 +388,7 @@ cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why)
     g.N = p.N;
     g.KB = p.KB;
     g.split = p.split;
-    const uint32_t tile = g.N * 128, stage = kStageA + tile;
-    const uint32_t fixed = 1024 + 2 * kSets * tile + 512;   // the ring's size also holds the [N][128] sums
-    // A multiple of the sets, so that a stage always belongs to the same one: a set that skipped a stage's earlier
-    // use could not tell its phases apart.
-    g.stages = std::min(8, (kSmemMost - 1024 - (int)fixed) / (int)stage / kSets * kSets);
-    g.out_as = out_kind(a);
-    g.vec = out_vec4(a);
-    CUtensorMap ta, tb;
-    if (!make_tmap_2d_sw128(&ta, 1, a.w, a.k, a.n_out, a.w_stride, 128, 128, why) ||
-        !make_tmap_2d_sw128(&tb, 1, a.x, a.k, a.n_rows, a.x_stride, 128, g.N, why))
-        return cudaErrorInvalidValue;
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(linear_few_kernel, kSmemMost, &done);
-    if (e != cudaSuccess) return e;
-    return launch_clusters((unsigned)g.split, linear_few_kernel, dim3(p.tiles * p.split, p.row_tiles), dim3(kThreads),
-                           fixed + (size_t)g.stages * stage, s, ta, tb, g);
+    return p.sets == 2 ? launch<2>(g, p, s, why) : launch<4>(g, p, s, why);
 }
 
 }  // namespace kvr

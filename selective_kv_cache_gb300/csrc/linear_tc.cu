@@ -166,22 +166,24 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
         tma_load_2d(smem + (size_t)s * stage_bytes, &tmA, &full[s], kb * kStageK, m * 256 + (int)half * 128);
     };
     const int pre = min(stages, (g.tiles - pair + g.pairs - 1) / g.pairs * g.KB);   // first stages of this pair's tiles
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+    if (warp == 0) {
+        // a barrier or two a lane: one thread takes 50 cycles for each
+        if (lane < stages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
         }
-        for (int t = 0; t < 8; ++t) {
-            mbar_init(&a_ready[t], 8);
-            mbar_init(&a_free[t], 1);
+        if (lane < 8) {
+            mbar_init(&a_ready[lane], 8);
+            mbar_init(&a_free[lane], 1);
+        } else if (lane < 10) {
+            mbar_init(&acc_full[lane - 8], 1);
+            mbar_init(&acc_empty[lane - 8], 8 * kOuts);
+        } else if (lane == 10) {
+            mbar_init(cols_free, 8 * kOuts);
+            mbar_init(all_done, 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8 * kOuts);
-        }
-        mbar_init(cols_free, 8 * kOuts);
-        mbar_init(all_done, 1);
         fence_mbar_init();
+        __syncwarp();
     }
     if (warp == 1) pair_alloc(tmem_slot);
     tc_fence_before();
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     if (!ok) atomicOr(g.a.err, DEV_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // no product or arrival of the pair is on its way any more
+    cluster_leave();   // no product or arrival of the pair is on its way any more
     if (warp == 1) {
         tc_fence_after();
         pair_dealloc(tmem);

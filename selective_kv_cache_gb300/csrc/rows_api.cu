@@ -65,16 +65,17 @@ kvr_status check_weights(const kvr_linear_weights* w) {
 //    8 x  4096 -> 28672         22.7     25.6     31.4
 //    9 x  4096 ->  6144         12.0     11.0     17.4
 //   16 x 14336 ->  4096         25.1     15.8     42.1
-//   64 x  4096 ->  6144                  13.9     17.7
-//   64 x  4096 -> 28672                  32.8     32.3
-//   64 x 14336 ->  4096                  20.8     42.5
-//   96 x  4096 ->  6144                  18.5     18.2
-//  128 x  1536 ->  2048                   7.2     10.5
-//  128 x  4096 ->  4096                  14.3     17.9
-//  256 x  4096 ->  4096                  20.5     18.0
-//  128 x 18944 ->  3584                  37.1     56.5
-//  192 x 18944 ->  3584                  63.8     56.9
-//  512 x  1536 ->  2048                  12.6     10.8
+//   64 x  4096 ->  6144                  13.3     17.0
+//   64 x  4096 -> 28672                  32.8     32.2
+//   64 x 14336 ->  4096                  18.5     43.9
+//  128 x  1536 ->  2048                   7.0     10.2
+//  128 x  4096 ->  4096                  12.8     17.2
+//  160 x  4096 ->  4096                  17.9     17.0
+//  128 x 18944 ->  3584                  35.9     56.6
+//  160 x 18944 ->  3584                  61.9     57.0
+//  256 x  8960 ->  1536                  19.8     30.0
+//  512 x  1536 ->  2048                   9.5     10.5
+// 1024 x  1536 ->  2048                  14.6     11.8
 // Above 64 rows the batch kernel reads the weights once for every 64 of them,
 // and splits k where the tiles are few: the two estimates decide.
 enum class LinearWay { Mma, Few, Tc };

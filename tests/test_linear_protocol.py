@@ -6,10 +6,10 @@ in any order, products complete in the order of their issue.
 
   copies     a ring of `stages`: iteration it arms full[it % stages] after
              empty[it % stages] has completed for its previous use
-  few        two widening sets take the iterations in turn, each into a slot of
-             its own: wait full, read, arrive on empty; wait freed[set], write
-             the slot, arrive on ready[set].  Products of iteration it wait for
-             ready[it % 2], read the slot and complete freed[it % 2].
+  few        two or four widening sets take the iterations in turn, each into a
+             slot of its own: wait full, read, arrive on empty; wait freed[set],
+             write the slot, arrive on ready[set].  Products of iteration it wait
+             for ready[it % sets], read the slot and complete freed[it % sets].
   tc         both sets take a half of every iteration: chunk q = 2 it + half goes
              to slot q % slots; the products of a chunk complete freed[slot],
              those of the second half empty as well (they read the stage's
@@ -50,14 +50,14 @@ def play(kind, total, stages, slots, ctas, seed):
     R, B = random.Random(seed), Barriers()
     landed, read, widened, used = {}, set(), {}, set()   # stage's iteration, (cta, it, set) read, slot's chunk, chunks multiplied
     flying, queue = [], []
-    halves = 1 if kind == "few" else 2
+    halves, sets = (1, slots) if kind == "few" else (2, 2)
 
     def copies(c):
         for it in range(total):
             s = it % stages
             while not B.passes(("empty", c, s), it // stages - 1):
                 yield
-            readers = [it % 2] if kind == "few" else [0, 1]
+            readers = [it % slots] if kind == "few" else [0, 1]
             if it >= stages and not all((c, it - stages, x) in read for x in readers):
                 raise Unsound("a stage is refilled before its codes were read")
             if kind == "tc" and it >= stages and not all(2 * (it - stages) + h in used for h in (0, 1)):
@@ -67,7 +67,7 @@ def play(kind, total, stages, slots, ctas, seed):
 
     def widen(c, x):
         uses = {}
-        for it in range(x if kind == "few" else 0, total, 2 if kind == "few" else 1):
+        for it in range(x if kind == "few" else 0, total, slots if kind == "few" else 1):
             s = it % stages
             while not B.passes(("full", c, s), it // stages):
                 yield
@@ -91,9 +91,8 @@ def play(kind, total, stages, slots, ctas, seed):
 
     def products():
         for q in range(total * halves):
-            t = q % 2 if kind == "few" else q % slots
-            per = 2 if kind == "few" else slots
-            while not B.passes(("ready", t), q // per):
+            t = q % slots
+            while not B.passes(("ready", t), q // slots):
                 yield
             if any(widened.get((c, t)) != q for c in range(ctas)):
                 raise Unsound("products of another chunk")
@@ -115,7 +114,7 @@ def play(kind, total, stages, slots, ctas, seed):
                         B.arrive(("empty", c, q // 2 % stages), 1)
             yield
 
-    roles = [products()] + [copies(c) for c in range(ctas)] + [widen(c, x) for c in range(ctas) for x in (0, 1)]
+    roles = [products()] + [copies(c) for c in range(ctas)] + [widen(c, x) for c in range(ctas) for x in range(sets)]
     w = world()
     for _ in range(200000):
         if not roles and not queue:
@@ -131,11 +130,11 @@ def play(kind, total, stages, slots, ctas, seed):
     raise Unsound("no progress")
 
 
-@pytest.mark.parametrize("stages", [2, 4, 6])
+@pytest.mark.parametrize("stages,sets", [(2, 2), (4, 2), (6, 2), (4, 4), (8, 4)])
 @pytest.mark.parametrize("total", [1, 2, 3, 7, 20])
-def test_batch_kernel(stages, total):
+def test_batch_kernel(stages, sets, total):
     for seed in range(60):
-        play("few", total, stages, 2, 1, seed)
+        play("few", total, stages, sets, 1, seed)
 
 
 @pytest.mark.parametrize("stages,slots", [(4, 4), (5, 4), (7, 8), (12, 8), (1, 4)])
