@@ -376,7 +376,7 @@ double linear_few_us(int n_out, int k, int n_rows) {
     const Plan p = make_plan(n_out, k, n_rows);
     // starting and joining, and a stage: of four sets, of two with one block on the busiest SM, with two
     const int stages = (p.KB + p.split - 1) / p.split;
-    if (p.sets == 4) return (p.split > 1 ? 7.0 : 6.0) + (0.27 + 0.1 / 32 * std::max(0, p.N - 32)) * stages;
+    if (p.sets == 4) return (p.split > 1 ? 6.8 : 5.0) + (0.30 + 0.12 / 32 * std::max(0, p.N - 32)) * stages;
     const bool two = (long long)p.tiles * p.row_tiles * p.split > kNumSMs;
     return (two ? 8.0 : 5.5) + (two ? 0.74 : 0.64) * p.waves * stages;
 }
