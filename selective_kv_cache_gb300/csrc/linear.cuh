@@ -40,11 +40,6 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// The same where nothing but reads of the others' shared memory has to be over: the values that were read are in use
-// by then, and what went out to global memory is not waited for.
-__device__ __forceinline__ void cluster_leave() {
-    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
-}
 // the shared-memory address of another block of the cluster
 __device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
     uint32_t a;

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kThreadsOf<kSets>, kBlocksOf<kSets>)
     uint64_t* freed = ready + kSets;    // [kSets]
     uint64_t* done = freed + kSets;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint32_t* unread = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = g.split, rank = (int)blockIdx.x % split, f0 = (int)blockIdx.x / split * 128;
     const int kb0 = g.KB * rank / split, n_kb = g.KB * (rank + 1) / split - kb0;
@@ -166,15 +167,21 @@ __global__ void __launch_bounds__(kThreadsOf<kSets>, kBlocksOf<kSets>)
             for (int i = 0; i < 4; ++i)
                 b[i] = 16 * i < g.N ? lds128(from_b + at + 2048 * i) : make_uint4(0u, 0u, 0u, 0u);
         };
-        // A word of every vector is looked at before the stage goes back: an arrival does not wait for loads whose
-        // values nothing has used, and the copy that it allows would overtake them.
+        // The stage goes back once its codes are in registers.  An arrival does not wait for loads whose values nothing
+        // has used, and the copy that it allows would overtake them: so a word of every vector decides on a store that
+        // precedes the arrival, and that the assembler cannot drop.  Where it happens, nobody reads what it writes.
         auto give_back = [&]() {
             uint32_t seen = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) seen ^= c[i].w;
 #pragma unroll
             for (int i = 0; i < 4; ++i) seen ^= b[i].w;
-            asm volatile("" ::"r"(seen) : "memory");
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.eq.u32 p, %0, 0x5bd1e995;\n\t"
+                "@p st.volatile.shared.u32 [%1], %0;\n\t}\n" ::"r"(seen),
+                "r"(smem_u32(unread))
+                : "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
         };
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(kThreadsOf<kSets>, kBlocksOf<kSets>)
             for (int i = 0; i < 4; ++i) y[i] = (float)sum[i] * sx * sw[i] + bias[i];
             write4(g.a, g.vec, row0 + r, f, y);
         }
-        cluster_leave();   // no block leaves while another reads its sums
+        cluster_sync();   // no block leaves while another reads its sums
     } else {
         __syncthreads();
     }

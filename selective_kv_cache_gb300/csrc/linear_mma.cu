@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 3) linear_mma_kernel(const __grid_co
         if (r >= a.n_rows || f >= a.n_out) continue;
         write_out(a, (int64_t)r * a.out_stride + f, (float)v * a.x_scale[r] * a.w_scale[f] + (a.bias ? a.bias[f] : 0.f));
     }
-    if (split > 1) cluster_leave();   // no block leaves while another reads its sums
+    if (split > 1) cluster_sync();   // no block leaves while another reads its sums
 }
 
 }  // namespace

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
     if (!ok) atomicOr(g.a.err, DEV_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    cluster_leave();   // no product or arrival of the pair is on its way any more
+    cluster_sync();   // no product or arrival of the pair is on its way any more
     if (warp == 1) {
         tc_fence_after();
         pair_dealloc(tmem);

@@ -87,6 +87,29 @@ def test_linear_of_model_shapes(rows, n_out, k):
     c.check()
 
 
+@pytest.mark.parametrize("rows,n_out,k", [(64, 28672, 4096), (64, 6144, 4096), (128, 3584, 18944), (16, 4096, 14336),
+                                          (282, 4608, 3584), (8, 4096, 14336)])
+def test_linear_holds_over_many_launches(rows, n_out, k):
+    """Every bit of a hundred launches, weights from HBM or from L2: no stage of
+    codes is overwritten before it was read.  Sums below 2^24 are exact."""
+    a, w = codes(rows, k, 3, lo=-100, hi=101), codes(n_out, k, 4, lo=-100, hi=101)
+    want = a.double() @ w.double().T
+    assert want.abs().max() < 2 ** 23
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    W = kvr.linear_weights(w, torch.ones(n_out, device="cuda"), err)
+    ws = torch.empty(kvr.kvr_linear_workspace_bytes(W, rows), dtype=torch.uint8, device="cuda")
+    out, one, wrong = torch.empty(rows, n_out, device="cuda"), torch.ones(rows, device="cuda"), torch.zeros((), device="cuda")
+    other = torch.empty(200 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(100):
+        out.fill_(float("nan"))
+        if i % 3 == 0:
+            other.fill_(i)
+        kvr.kvr_linear(W, a, one, out, ws)
+        wrong += (out != want).any()
+    kvr.kvr_linear_status(W)
+    assert wrong.item() == 0
+
+
 @pytest.mark.parametrize("rows", [1, 8, 16, 40, 300])
 def test_sums_are_integers(rows):
     """Scales of one: the output is the integer itself, bit for bit, wherever every running sum stays below 2^24."""
