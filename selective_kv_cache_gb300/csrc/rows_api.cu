@@ -62,20 +62,21 @@ kvr_status check_weights(const kvr_linear_weights* w) {
 // Which kernel a call takes, measured on GB300 with weights from HBM (us):
 //   rows x k -> n_out        integer    batch    tiles
 //    8 x  4096 ->  6144          8.2     11.0     17.4
-//    8 x  4096 -> 28672         22.7     25.6     31.4
-//    9 x  4096 ->  6144         12.0     11.0     17.4
-//   16 x 14336 ->  4096         25.1     15.8     42.1
-//   64 x  4096 ->  6144                  13.3     17.0
-//   64 x  4096 -> 28672                  32.8     32.2
-//   64 x 14336 ->  4096                  18.5     43.9
-//  128 x  1536 ->  2048                   7.0     10.2
-//  128 x  4096 ->  4096                  12.8     17.2
-//  160 x  4096 ->  4096                  17.9     17.0
-//  128 x 18944 ->  3584                  35.9     56.6
-//  160 x 18944 ->  3584                  61.9     57.0
-//  256 x  8960 ->  1536                  19.8     30.0
-//  512 x  1536 ->  2048                   9.5     10.5
-// 1024 x  1536 ->  2048                  14.6     11.8
+//    8 x  4096 -> 28672         22.7     25.8     31.4
+//    9 x  4096 ->  6144         12.0     11.3     17.4
+//   16 x 14336 ->  4096         25.1     15.7     42.1
+//   64 x  4096 -> 28672                  30.3     32.2
+//   64 x 14336 ->  4096                  19.2     43.9
+//   96 x  4096 -> 28672                  40.0     32.9
+//  128 x  1536 ->  2048                   7.5     10.5
+//  128 x  4096 ->  4096                  13.1     17.7
+//  128 x 18944 ->  3584                  32.3     57.1
+//  192 x 14336 ->  4096                  41.8     45.1
+//  256 x  4096 ->  4096                  17.2     17.9
+//  320 x  4096 ->  4096                  25.0     18.2
+//  256 x  8960 ->  1536                  19.5     30.5
+//  320 x  1536 ->  2048                   9.0     10.5
+// 1024 x  1536 ->  2048                  14.6     12.2
 // Above 64 rows the batch kernel reads the weights once for every 64 of them,
 // and splits k where the tiles are few: the two estimates decide.
 enum class LinearWay { Mma, Few, Tc };

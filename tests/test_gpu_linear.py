@@ -80,7 +80,9 @@ def test_linear(rows, n_out, k):
                                           (282, 4608, 3584), (96, 37888, 3584), (1024, 1536, 8960), (2000, 5000, 777),
                                           (7, 300, 65536), (40, 300, 65536), (8, 1530, 8960), (5, 1300, 8200),
                                           (8, 1100, 8192), (1, 3584, 18944), (64, 3584, 18944), (48, 12288, 4096),
-                                          (33, 4600, 3600), (100, 4100, 4100), (20, 1000, 9000), (57, 1024, 12288)])
+                                          (33, 4600, 3600), (100, 4100, 4100), (20, 1000, 9000), (57, 1024, 12288),
+                                          (64, 28672, 4096), (50, 28500, 4000), (9, 37888, 3584), (30, 20000, 1111),
+                                          (64, 55000, 900), (128, 13000, 2000)])
 def test_linear_of_model_shapes(rows, n_out, k):
     c = Case(rows, n_out, k, "f32", True, seed=3, lo=-100, hi=101)
     c.run()

@@ -150,3 +150,28 @@ def test_an_odd_ring_is_unsound_for_sets_that_take_turns():
     with pytest.raises(Unsound):
         for seed in range(2000):
             play("few", 12, 3, 2, 1, seed)
+
+
+@pytest.mark.parametrize("split", range(1, 9))
+def test_shares_of_a_clusters_tiles(split):
+    """linear_few.cu: blocks of a cluster share the stages of T tiles.  Each stage
+    is one block's; a block has at most four tiles (as many accumulators), and at
+    most one that it shares in each of its two buffers."""
+    R = random.Random(split)
+    for _ in range(400):
+        tiles, clusters, kb = R.randint(1, 700), R.randint(1, 152 // split), R.randint(1, 512)
+        clusters = min(clusters, tiles)
+        T = -(-tiles // clusters)
+        touched = 1 if T == 1 else T if split == 1 else -(-T // split) + 1
+        if touched > 4 or -(-T * kb // split) < 6:
+            continue
+        for c in {0, clusters // 2, clusters - 1}:
+            t = tiles * (c + 1) // clusters - tiles * c // clusters
+            lo = [t * kb * p // split for p in range(split + 1)]
+            assert t >= 1 and lo[0] == 0 and lo[-1] == t * kb
+            for a, b in zip(lo, lo[1:]):
+                assert a < b
+                mine = range(a // kb, (b - 1) // kb + 1)
+                assert len(mine) <= 4
+                shared = [i for i in mine if not (a <= i * kb and (i + 1) * kb <= b)]
+                assert sum(a < i * kb for i in shared) <= 1 and sum(a >= i * kb for i in shared) <= 1
