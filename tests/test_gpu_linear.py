@@ -192,6 +192,22 @@ def test_captured_and_on_two_streams(rows):
         e.check()
 
 
+def test_kernels_of_two_streams_side_by_side():
+    """Batches that split k over clusters, shared tiles, many rows and few, in
+    turn on two streams: whichever blocks meet on an SM, both finish."""
+    shapes = [(64, 4096, 2048), (40, 640, 9000), (64, 24000, 800), (300, 2048, 1536), (4, 4096, 2048), (12, 2048, 1536)]
+    cases = [[Case(*shape, "f32", seed=21 + i, lo=-100, hi=101) for i, shape in enumerate(shapes)] for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for turn in range(20):
+        for i in range(len(shapes)):
+            cases[0][i].run(streams[0])
+            cases[1][(i + turn) % len(shapes)].run(streams[1])
+    torch.cuda.synchronize()
+    for c in cases[0] + cases[1]:
+        c.check()
+
+
 def test_binding_refuses():
     c = Case(20, 64, 128)
     ok = (c.weights, c.a, c.sa, c.out, c.ws)
