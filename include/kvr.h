@@ -725,7 +725,9 @@ kvr_status kvr_paged_status(const kvr_pages* p, void* stream);
  * Rows in eight bits: signed codes and one fp32 scale a row, value = scale *
  * code.  For the fp32 values y of a row,
  *     top = max |y|, scale = top * fp32(1/127), code = rint(y * (1 / scale)),
- * so codes lie in [-127, 127].  A row whose scale would be below 2^-126 gets
+ * each product and quotient rounded to fp32, so codes lie in [-127, 127].  (A
+ * norm's y is h * weight times one number a row, which goes into the scale
+ * alone: its codes are those of h * weight.)  A row whose scale would be below 2^-126 gets
  * scale 0 and codes 0; a row with an infinity or a NaN gets scale NaN and
  * codes 0, so all it stands for is NaN and no other row is touched.
  *

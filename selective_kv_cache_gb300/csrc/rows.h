@@ -36,6 +36,7 @@ struct RowsQuant {
     int n_rows, d;
     float eps;
     int codes_aligned;      // set by the launcher
+    float zero = 0.f;       // one that the compiler does not know
 };
 cudaError_t launch_rows_quant(RowOp op, int dtype, const RowsQuant& a, cudaStream_t s);
 cudaError_t launch_rows_dequantise(int dtype, int n_rows, int d, const int8_t* codes, int64_t code_stride,
