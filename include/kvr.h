@@ -727,24 +727,26 @@ kvr_status kvr_paged_status(const kvr_pages* p, void* stream);
  *     top = max |y|, scale = top * fp32(1/127), code = rint(y * (1 / scale)),
  * each product and quotient rounded to fp32, so codes lie in [-127, 127].  (A
  * norm's y is h * weight times one number a row, which goes into the scale
- * alone: its codes are those of h * weight.)  A row whose scale would be below 2^-126 gets
- * scale 0 and codes 0; a row with an infinity or a NaN gets scale NaN and
- * codes 0, so all it stands for is NaN and no other row is touched.
+ * alone: its codes are those of h * weight.)  A row whose scale would be below
+ * 2^-126 gets scale 0 and codes 0; a row with an infinity or a NaN gets scale
+ * NaN and codes 0, so all it stands for is NaN and no other row is touched.
  *
  * dtype is KVR_F32 or KVR_BF16.  Strides are in elements of their array, at
  * least a row's width.  Rows of any width and of any alignment of their elements
  * are taken; 16-byte aligned pointers and strides (codes: 8) are the faster.  A
  * row's last or first aligned 16 bytes may be read past it, never written.
  * Widths go up to 2^20, rows to 2^31 - 1, strides to 2^29.  Sums, maxima and
- * products are fp32 (|h| stays below 2^60, so that its squares do not overflow).  Where an
- * output may be an input, it is that array from its first element on, with
- * the same stride; arrays do not overlap otherwise.
+ * products are fp32.  Where an output may be an input, it is that array from
+ * its first element on, with the same stride; arrays do not overlap otherwise.
  * Nothing is kept between calls, so all of them can be captured.
  * EINVAL on NULL or misaligned arguments, sizes or strides out of range;
  * n_rows = 0 enqueues nothing.
  * ------------------------------------------------------------------------- */
 
 /* kvr_rows_norm -- h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight.
+ * A row whose sum of h^2 reaches 2^128 (|h| below 2^54 never does, below
+ * 2^64 / sqrt(d) neither) or whose mean(h^2) + eps lies below 2^-126 (eps = 0
+ * and |h| of some 2^-63) is NaN, in out and in eight bits.
  *   residual    device [n_rows][d] or NULL (h = x).
  *   sum_out     device [n_rows][d] or NULL: h, rounded to dtype (the norm uses
  *               it unrounded); may be x or residual.

@@ -367,8 +367,17 @@ __global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T), kAligned)
         }
         uint32_t top_bits = __float_as_uint(top);
         row_reduce<kWarp, kNorm>(sum, top_bits, turn);
-        const float r = kNorm ? rsqrtf(sum / (float)a.d + a.eps) : 1.f;
-        const bool bad = top_bits >= 0x7f800000u || (kNorm && !(r <= 3.4028234e38f));
+        float r = 1.f;
+        bool bad = top_bits >= 0x7f800000u;
+        if constexpr (kNorm) {
+            const float q = sum / (float)a.d + a.eps;
+            r = rsqrtf(q);
+            // A sum past fp32's range would make zeros of the row, one that has lost its squares below it a wrong root: NaN.
+            if (!bad && !(q >= kTiny && q <= 3.4028234e38f)) {
+                bad = true;
+                r = __int_as_float(0x7fffffff);
+            }
+        }
         // of the values before r: r lies in the scale alone
         const float s0 = __uint_as_float(top_bits) * (1.f / 127.f);
         const float scale = kNorm ? s0 * r : s0;
