@@ -369,6 +369,9 @@ __global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T), kAligned)
         row_reduce<kWarp, kNorm>(sum, top_bits, turn);
         float r = 1.f;
         bool bad = top_bits >= 0x7f800000u;
+        // A row's own scale decides whether it is zeros.  Where h w are tiny and r is large, h w go up by 2^32 and r down,
+        // so that the scale before r is no subnormal number: 2^-149 / 127 * 2^32 is 2^-124.
+        const bool tiny = kNorm && top_bits < 0x12800000u;   // 2^-90
         if constexpr (kNorm) {
             const float q = sum / (float)a.d + a.eps;
             r = rsqrtf(q);
@@ -377,11 +380,21 @@ __global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T), kAligned)
                 bad = true;
                 r = __int_as_float(0x7fffffff);
             }
+            if (tiny) {
+                top_bits = __float_as_uint(__uint_as_float(top_bits) * 0x1p32f);
+                r *= 0x1p-32f;
+                if constexpr (kSlots > 0) {
+#pragma unroll
+                    for (int k = 0; k < kHold; ++k)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[k][e] *= 0x1p32f;
+                }
+            }
         }
         // of the values before r: r lies in the scale alone
         const float s0 = __uint_as_float(top_bits) * (1.f / 127.f);
         const float scale = kNorm ? s0 * r : s0;
-        const bool none = !bad && (s0 < kTiny || scale < kTiny);
+        const bool none = !bad && scale < kTiny;
         const float inv = bad || none ? 0.f : 1.f / s0;
         if (a.codes && lane == 0) a.scales[row] = bad ? __int_as_float(0x7fffffff) : none ? 0.f : scale;
         auto put = [&](int k, const float* v) {
@@ -403,6 +416,10 @@ __global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T), kAligned)
             for (int k = 0; 8 * (k * step) < a.d; ++k) {
                 u[0].load(a, row, 8 * (lane + k * step), count(k));
                 take(k, u[0], v[0], false);
+                if (tiny) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[0][e] *= 0x1p32f;
+                }
                 put(k, v[0]);
             }
         }

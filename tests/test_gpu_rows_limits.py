@@ -86,3 +86,17 @@ def test_norm_of_large_and_of_tiny_squares(dtype, d, eps):
     x = rows_of_size([-100, -80, -70, -66, -62, -50, -20, 0, 20, 50, 54, 57, 59, 62, 63, 66, 100, 120], d, dtype, d)
     lost, _ = check_norm(x, torch.ones(d, dtype=x.dtype, device="cuda"), eps)
     assert lost[-2:].all() and not lost[4:11].any() and (lost[:4] == (eps == 0)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", NORM_WIDTHS)
+@pytest.mark.parametrize("eps,size", [(0.0, 0), (1e-12, -40), (2.0 ** -126, 0), (1e-30, -70), (1e-12, 0), (1e-5, 0), (1e-5, 20)])
+def test_norm_of_tiny_products_keeps_its_codes(dtype, d, eps, size):
+    """A row's own scale decides whether it stands for zeros, not the one
+    before the root: h = 1e-37 with eps = 1e-12 is y = 1e-31.  Weights of 2^size."""
+    x = rows_of_size([-145, -135, -128, -123, -117, -110, -101, -92, -90, -88, -70, -62, -40, 0], d, dtype, d + 1)
+    w = rows_of_size([size], d, dtype, 1)[0].abs()
+    lost, none = check_norm(x, w, eps)
+    assert not lost[-3:].any()
+    if (eps, size) == (1e-12, 0):
+        assert not none[2:].any()
