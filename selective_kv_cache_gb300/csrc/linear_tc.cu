@@ -287,7 +287,6 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             if (issuer) pair_commit(all_done);
             __syncwarp();
         }
-        if (!warp_wait(all_done, 0)) ok = false;
     } else if (warp >= 4 + 4 * kOuts) {
         // ------------------------------------------------------------ widening
         const int chunk = (warp - 4 - 4 * kOuts) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
@@ -387,9 +386,12 @@ __global__ void __launch_bounds__(kThreads) linear_tc_kernel(const __grid_consta
             if (lane == 0) arrive_leader(&acc_empty[ab]);
         }
     }
-    if (!ok) atomicOr(g.a.err, DEV_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
+    // The last products' end on both CTAs.  Waited for here, when the accumulators are out, so that this wait spans no more
+    // than another's: the other CTA's warp 1 has nothing to do before, and a call may take longer than a wait's limit.
+    if (warp == 1 && !warp_wait(all_done, 0)) ok = false;
+    if (!ok) atomicOr(g.a.err, DEV_ERR_TIMEOUT);
     cluster_sync();   // no product or arrival of the pair is on its way any more
     if (warp == 1) {
         tc_fence_after();

@@ -1,0 +1,29 @@
+"""kvr_linear at the ends of its range: a call of more than a second."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+kvr = pytest.importorskip("selective_kv_cache_gb300.kvr")
+
+
+def test_a_call_of_more_than_a_second():
+    """Waits are bounded by a second each, calls are not: 3.4e15 operations take
+    the GPU 1.7 s and more.  The status is good and the sums are right."""
+    torch.cuda.empty_cache()
+    rows, n, k = 400000, 65536, 65536
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = torch.empty(rows, k, dtype=torch.int8, device="cuda").random_(-8, 9, generator=g)
+    w = torch.empty(n, k, dtype=torch.int8, device="cuda").random_(-8, 9, generator=g)
+    ones = torch.ones(rows, device="cuda")
+    W = kvr.linear_weights(w, ones[:n], torch.zeros(4, dtype=torch.int32, device="cuda"))
+    out = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kvr.kvr_linear_workspace_bytes(W, rows), dtype=torch.uint8, device="cuda")
+    kvr.kvr_linear(W, a, ones, out, ws)
+    kvr.kvr_linear_status(W)
+    at = torch.tensor([0, 1, 255, 256, 131071, 200000, rows - 257, rows - 1], device="cuda")
+    ch = torch.tensor([0, 127, 128, 255, 256, 40000, n - 1], device="cuda")
+    want = (a[at].cpu().double() @ w[ch].cpu().double().T).bfloat16()   # sums of 65536 products up to 64: below 2^23, exact
+    assert torch.equal(out[at][:, ch].cpu(), want)
+    del a, w, out, ws, W
+    torch.cuda.empty_cache()
