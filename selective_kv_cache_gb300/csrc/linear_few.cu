@@ -19,8 +19,10 @@
 // which takes four sets to keep busy.  They are one block of four sets an SM, or
 // two blocks of two, so that one streams while the other starts or ends
 // (make_plan).  A block's shared memory leaves no room on its SM for more
-// tensor memory than there is, so blocks of other clusters do not wait for one
-// another's.  Every wait is bounded.
+// tensor memory than there is (linear_few_smem), so blocks of other clusters do
+// not wait for one another's: an allocation is no bounded wait, and two clusters
+// that each hold what the other's second block waits for would never end.  Every
+// other wait is bounded.
 //
 // Where 19.2 us of 64 rows, 14336 -> 4096 go (clock64, cycles): set up at 1700,
 // the first stage there at 5000, all 28 widened at 26000, products and sums out
@@ -419,11 +421,7 @@ Plan make_plan(int n_out, int k, int n_rows) {
 template <int kSets, bool kSpread>
 cudaError_t launch(LinearFew& g, const Plan& p, cudaStream_t s, std::string* why) {
     const Linear& a = g.a;
-    const uint32_t tile = g.N * 128, stage = kStageA + tile;
-    const uint32_t fixed = 1024 + 2 * kSets * tile + 512;   // the ring's size also holds the [N][128] sums
-    // A multiple of the sets, so that a stage always belongs to the same one: a set that skipped a stage's earlier
-    // use could not tell its phases apart.
-    g.stages = std::min(8, (kSmemOf<kSets> - 1024 - (int)fixed) / (int)stage / kSets * kSets);
+    const int smem = linear_few_smem(kSets, g.N, &g.stages);
     CUtensorMap ta, tb;
     if (!make_tmap_2d_sw128(&ta, 1, a.w, a.k, a.n_out, a.w_stride, 128, 128, why) ||
         !make_tmap_2d_sw128(&tb, 1, a.x, a.k, a.n_rows, a.x_stride, 128, g.N, why))
@@ -432,9 +430,20 @@ cudaError_t launch(LinearFew& g, const Plan& p, cudaStream_t s, std::string* why
     const cudaError_t e = allow_smem(linear_few_kernel<kSets, kSpread>, kSmemOf<kSets>, &done);
     if (e != cudaSuccess) return e;
     return launch_clusters((unsigned)g.split, linear_few_kernel<kSets, kSpread>, dim3(p.clusters * p.split, p.row_tiles),
-                           dim3(kThreadsOf<kSets>), fixed + (size_t)g.stages * stage, s, ta, tb, g);
+                           dim3(kThreadsOf<kSets>), (size_t)smem, s, ta, tb, g);
 }
 }  // namespace
+
+int linear_few_smem(int sets, int N, int* stages) {
+    const int tile = N * 128, stage = (int)kStageA + tile, most = sets == 2 ? kSmemOf<2> : kSmemOf<4>;
+    const int fixed = 1024 + 2 * sets * tile + 512;   // the ring's size also holds the [N][128] sums
+    // A multiple of the sets, so that a stage always belongs to the same one: a set that skipped a stage's earlier
+    // use could not tell its phases apart.
+    *stages = std::min(8, (most - 1024 - fixed) / stage / sets * sets);
+    // Two sets take 256 of an SM's 512 columns: more than a third of its 228 KB (a block costs 1 KB more than it asks
+    // for), which 48 rows a tile with their 69.5 KB would leave.
+    return std::max(fixed + *stages * stage, sets == 2 ? 76 * 1024 : 0);
+}
 
 double linear_few_us(int n_out, int k, int n_rows) { return make_plan(n_out, k, n_rows).us; }
 

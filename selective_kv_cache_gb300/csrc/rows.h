@@ -69,6 +69,8 @@ constexpr int kLinearMmaRows = 8;   // up to these rows the integer kernel takes
 cudaError_t launch_linear_mma(const Linear& a, cudaStream_t s);
 
 double linear_few_us(int n_out, int k, int n_rows);   // estimated time
+// A block's dynamic shared memory and ring, with two or four widening sets and N rows a tile.
+int linear_few_smem(int sets, int N, int* stages);
 cudaError_t launch_linear_few(const Linear& a, cudaStream_t s, std::string* why);
 // Many rows; needs linear_tc_workspace bytes of workspace.
 double linear_tc_us(int n_out, int k, int n_rows);
