@@ -808,19 +808,19 @@ def linear_weights(codes, scales, err, bias=None) -> kvr_linear_weights:
                            None if bias is None else _values(bias, "bias", n, torch.float32, dev), _ptr(err))
     w.tensors = (codes, scales, bias, err)
     w.device = dev
-    w.addr = C.addressof(w)
     return w
 
 
 def kvr_linear_workspace_bytes(w: kvr_linear_weights, n_rows: int) -> int:
-    return int(lib.kvr_linear_workspace_bytes(w.addr, n_rows))
+    return int(lib.kvr_linear_workspace_bytes(C.addressof(w), n_rows))
 
 
 def kvr_linear(w: kvr_linear_weights, codes, scales, out, workspace, stream=None):
     """codes: int8 [n, k], rows a multiple of 16 bytes apart; scales: fp32 [n];
     out: [n, n_out] in bf16 or fp32; workspace: uint8 of
-    kvr_linear_workspace_bytes."""
-    dt, dev, n = _dtype(out, "out"), w.device, out.shape[0]
+    kvr_linear_workspace_bytes.  w is linear_weights' or filled by the caller,
+    with weights on out's device."""
+    dt, dev, n = _dtype(out, "out"), getattr(w, "device", out.get_device()), out.shape[0]
     if n == 0:
         return
     s = _row_stream(dev, stream)
@@ -830,9 +830,10 @@ def kvr_linear(w: kvr_linear_weights, codes, scales, out, workspace, stream=None
     if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
         _want(workspace, "workspace", torch.uint8, 1, codes.device)
     # a single row's stride is whatever torch says
-    _check(lib.kvr_linear(w.addr, n, cp, cs if n > 1 else -(-cs // 16) * 16, sp, dt, op, os_, workspace.data_ptr(),
+    _check(lib.kvr_linear(C.addressof(w), n, cp, cs if n > 1 else -(-cs // 16) * 16, sp, dt, op, os_, workspace.data_ptr(),
                           workspace.numel(), s), "kvr_linear")
 
 
 def kvr_linear_status(w: kvr_linear_weights, stream=None):
-    _check(lib.kvr_linear_status(w.addr, _row_stream(w.device, stream)), "kvr_linear_status")
+    dev = w.device if hasattr(w, "device") else torch.cuda.current_device()   # a filled one's is the current device
+    _check(lib.kvr_linear_status(C.addressof(w), _row_stream(dev, stream)), "kvr_linear_status")

@@ -1,10 +1,14 @@
-"""kvr_linear at the ends of its range: a call of more than a second."""
+"""kvr_linear at the ends of its range: a call of more than a second; weights
+that the caller fills or copies."""
+import ctypes
+
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 
 kvr = pytest.importorskip("selective_kv_cache_gb300.kvr")
+from test_gpu_linear import Case  # noqa: E402
 
 
 def test_a_call_of_more_than_a_second():
@@ -27,3 +31,22 @@ def test_a_call_of_more_than_a_second():
     assert torch.equal(out[at][:, ch].cpu(), want)
     del a, w, out, ws, W
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows", [3, 40, 300])
+def test_weights_filled_by_the_caller_and_copied(rows):
+    c = Case(rows, 200, 320, "f32", True, seed=30)
+    c.run()
+    c.check()
+    want, made = c.out.clone(), c.weights
+    p = lambda t: t.data_ptr()  # noqa: E731
+    filled = kvr.kvr_linear_weights(200, 320, c.w.stride(0), p(c.w), p(c.sw), p(c.bias), p(c.err))
+    copied = kvr.kvr_linear_weights.from_buffer_copy(made)
+    ctypes.memset(ctypes.addressof(made), 0, ctypes.sizeof(made))
+    for w in (filled, copied):
+        c.weights = w
+        c.out.fill_(0)
+        assert kvr.kvr_linear_workspace_bytes(w, rows) == c.ws.numel()
+        c.run()
+        kvr.kvr_linear_status(w)
+        assert torch.equal(c.out, want)
