@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(kThreads, 3) linear_mma_kernel(const __grid_co
     }
     if (split > 1) cluster_sync();
     else __syncthreads();
-    // each block of the cluster finishes its share of the tile
+    // The cluster's blocks would take the tile's entries in turn; there are as many as threads, so the first one adds up and
+    // writes them all.
     for (int i = rank * kThreads + threadIdx.x; i < kTile; i += split * kThreads) {
         const int r = i / kFeatures, f = f0 + i % kFeatures;
         int v = part[0][i];
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 3) linear_mma_kernel(const __grid_co
         if (r >= a.n_rows || f >= a.n_out) continue;
         write_out(a, (int64_t)r * a.out_stride + f, (float)v * a.x_scale[r] * a.w_scale[f] + (a.bias ? a.bias[f] : 0.f));
     }
-    if (split > 1) cluster_sync();   // no block leaves while another reads its sums
+    if (split > 1) cluster_sync();   // no block leaves while the first reads its sums
 }
 
 }  // namespace
