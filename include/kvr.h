@@ -764,7 +764,10 @@ kvr_status kvr_rows_norm(int32_t dtype, int32_t n_rows, int32_t d, const void* x
 
 /* kvr_rows_swiglu -- y = g / (1 + exp(-g)) * u.  gate_up: device [n_rows][2 d],
  * g the first d elements of a row, u the others; outputs as kvr_rows_norm (out
- * may not be gate_up). */
+ * may not be gate_up).  bf16 rows use an approximate exponential and division:
+ * y is off by (6 + 1.2 |g|) 2^-23 of itself before it is rounded.  Below g =
+ * -88.7 (bf16: -87.3) exp(-g) is beyond the range, and y is 0 (|y / u| is below
+ * 2^-119 there). */
 kvr_status kvr_rows_swiglu(int32_t dtype, int32_t n_rows, int32_t d, const void* gate_up, int64_t stride, void* out,
                            int64_t out_stride, int8_t* codes, int64_t code_stride, float* scales, void* stream);
 
