@@ -5,7 +5,8 @@
 // HBM-bound: the weights come in once, 128 features by up to 64 rows a block
 // (more rows: as many blocks side by side, the weights then from L2).
 // Both operands are widened to fp16 on the way (8-bit integers, their products
-// and the fp32 sums up to 2^24 are exact): the weights into tensor memory, the A
+// and the fp32 sums up to 2^24 are exact; above, the accumulator cuts each step
+// of 16 products off, by up to 2^-23): the weights into tensor memory, the A
 // operand, the rows into shared memory.  A cluster's blocks split k, and join
 // their sums as integers over distributed shared memory: nothing goes through
 // the workspace.  Where there are more tiles than clusters, a cluster has several
@@ -191,7 +192,9 @@ __global__ void __launch_bounds__(kThreadsOf<kSets>, kBlocksOf<kSets>)
         };
         // The stage goes back once its codes are in registers.  An arrival does not wait for loads whose values nothing
         // has used, and the copy that it allows would overtake them: so a word of every vector decides on a store that
-        // precedes the arrival, and that the assembler cannot drop.  Where it happens, nobody reads what it writes.
+        // precedes the arrival, and that the assembler cannot drop.  Where it happens, nobody reads what it writes.  What
+        // this relies on: a vector's words arrive together, the predicate needs one of each, and a warp issues its
+        // instructions in order, so the arrival is not issued before the predicate is known.
         auto give_back = [&]() {
             uint32_t seen = 0;
 #pragma unroll

@@ -1,5 +1,5 @@
 """kvr_linear at the ends of its range: a call of more than a second; weights
-that the caller fills or copies."""
+that the caller fills or copies; sums up to the last that fp32 holds exactly."""
 import ctypes
 
 import pytest
@@ -50,3 +50,26 @@ def test_weights_filled_by_the_caller_and_copied(rows):
         c.run()
         kvr.kvr_linear_status(w)
         assert torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("rows,n_out", [(1, 200), (8, 200), (9, 200), (40, 6000), (64, 200), (64, 25000), (300, 4608), (5000, 200)])
+@pytest.mark.parametrize("k,most", [(1040, 127), (1023, -128), (4096, 127), (18944, -127)])
+def test_sums_up_to_two_to_the_24(rows, n_out, k, most):
+    """Running sums that climb to 2^24 - 3056 (or 2^24 - 16384 of -128 by -128) and
+    stay there are exact, of either sign: a step is a multiple of one, and no sum
+    on the way is above the last.  Ones in the last places climb to it by one."""
+    a, w = torch.zeros(rows, k, dtype=torch.int8), torch.zeros(n_out, k, dtype=torch.int8)
+    top = 1040 if abs(most) == 127 else 1023
+    a[:, :top], w[:, :top] = most, abs(most) if most != -128 else most
+    a[1::2] = -a[1::2].clamp(min=-127)              # odd rows downwards
+    w[1::3, top - 2:top] = torch.tensor([1, -1], dtype=torch.int8)   # some channels end on other units
+    c = Case(rows, n_out, k, "f32")
+    c.a.copy_(a)
+    c.w.copy_(w)
+    c.sa.fill_(1)
+    c.sw.fill_(1)
+    c.run()
+    kvr.kvr_linear_status(c.weights)
+    want = a.double() @ w.double().T
+    assert 2 ** 24 - 20000 < want.abs().max() < 2 ** 24
+    assert torch.equal(c.out.cpu().double(), want)
