@@ -100,3 +100,70 @@ def test_norm_of_tiny_products_keeps_its_codes(dtype, d, eps, size):
     assert not lost[-3:].any()
     if (eps, size) == (1e-12, 0):
         assert not none[2:].any()
+
+
+# ---------------------------------------------------------------- more rows than blocks
+def off_by(codes, scale, y, rel):
+    """The furthest of every row from check_codes' bounds, on the GPU: at most 0 where all hold."""
+    top = y.abs().amax(1) / 127
+    s = scale.double()
+    a = (s - top).abs() - (rel + 2.0 ** -22) * top
+    b = ((codes.double() * s[:, None] - y).abs() - rel * y.abs()).amax(1) - (0.5 + 2.0 ** -14) * s
+    return float(torch.maximum(a, b).amax())
+
+
+def many(n, d, dtype, seed, pad):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(n, d + pad, generator=g, device="cuda") * torch.exp(torch.randn(n, 1, generator=g, device="cuda"))
+    return x.to(DTYPES[dtype])[:, :d]
+
+
+# (rows, width): more rows than the GPU holds blocks, or warps, of every kernel
+MANY = [(20000, 40), (20000, 264), (20000, 500), (6000, 520), (6000, 1792), (6000, 2056), (2500, 4096), (2500, 8200), (2500, 14336), (1200, 20488)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,d", MANY)
+@pytest.mark.parametrize("off", [0, 1])
+def test_every_row_of_thousands(dtype, n, d, off):
+    """Norm, gate and quantiser where a block or a warp takes many rows in turn,
+    aligned rows and rows (off = 1) of odd widths that begin anywhere."""
+    d, pad = d - off, 7 * off if off else 8
+    code = torch.zeros(n, d + pad, dtype=torch.int8, device="cuda")
+    codes, scale = code[:, :d], torch.empty(n, device="cuda")
+    x = many(n, d, dtype, d, pad)
+    kvr.kvr_rows_quantise(x, codes, scale)
+    assert off_by(codes, scale, x.double(), 0.0) <= 0
+    # the gate: |g| below 40
+    gu = many(n, 2 * d, dtype, d + 1, pad).clamp(-40, 40)
+    out = torch.empty(n, d + pad, dtype=x.dtype, device="cuda")[:, :d]
+    codes.fill_(99)
+    kvr.kvr_rows_swiglu(gu, out=out, codes=codes, scales=scale)
+    y, rel = gu[:, :d].double() * torch.sigmoid(gu[:, :d].double()) * gu[:, d:].double(), 2.0 ** (-17 if dtype == "bf16" else -20)
+    assert off_by(codes, scale, y, rel) <= 0
+    assert bool(((out.double() - y).abs() <= (HALF[dtype] + rel) * y.abs() + 1e-37).all())
+    del gu, y
+    # the norm, both outputs in place
+    res, w = many(n, d, dtype, d + 2, pad), (1 + 0.3 * many(1, d, "f32", 3, 0)[0].tanh()).to(x.dtype)
+    h = x.double() + res.double()
+    y = h / torch.sqrt(h.square().mean(1, keepdim=True) + 1e-5) * w.double()
+    codes.fill_(99)
+    kvr.kvr_rows_norm(x, w, 1e-5, residual=res, sum_out=res, out=x, codes=codes, scales=scale)
+    # n/t + 12 additions of the sum are at most 52 (see test_gpu_rows): a thread has up to 32 elements
+    assert off_by(codes, scale, y, REL) <= 0
+    assert bool(((x.double() - y).abs() <= (HALF[dtype] + REL) * y.abs() + 1e-37).all())
+    assert bool(((res.double() - h).abs() <= HALF[dtype] * h.abs() + 2.0 ** -24 * h.abs()).all())
+    assert int(torch.count_nonzero(code[:, d:])) == 0
+
+
+@pytest.mark.parametrize("n,d", [((1 << 23) + 1000, 1), ((1 << 28) + 1000, 16)])
+def test_read_back_of_more_rows_than_a_grid(n, d):
+    """Rows behind the grid's last block are its first ones' again."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    codes = torch.empty(n, d, dtype=torch.int8, device="cuda").random_(-127, 128, generator=g)
+    scale = torch.rand(n, generator=g, device="cuda")
+    out = torch.full((n, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    kvr.kvr_rows_dequantise(codes, scale, out)
+    for a in range(0, n, 1 << 26):
+        b = min(n, a + (1 << 26))
+        assert torch.equal(out[a:b], (codes[a:b].float() * scale[a:b, None]).bfloat16())
