@@ -854,8 +854,9 @@ kvr_status kvr_rows_rotate(const kvr_rope* rope, int32_t dtype, int32_t n_rows, 
  * Up to 8 rows the sums are 32-bit integers; for more rows they are formed by
  * the tensor cores in fp32, 16 products a step, which holds them exactly up to
  * 2^24; each step above that cuts off what is below the last place, up to
- * 2^-23 of the sum and always towards zero (k = 16384, all codes near 127: 2^-14
- * too small).  The same inputs give the same bits.  A row or channel whose scale is NaN is NaN.
+ * 2^-23 of the sum and always towards zero (k = 16384, all codes near 127: 7e-5
+ * of the sum is lost).  The same inputs give the same bits.  A row or channel
+ * whose scale is NaN is NaN.
  * EINVAL as the row operators; device-side failures (a wait that gave up) go
  * to w->err and are reported, and cleared, by kvr_linear_status, which
  * synchronises `stream`.
