@@ -746,9 +746,10 @@ kvr_status kvr_paged_status(const kvr_pages* p, void* stream);
 /* kvr_rows_norm -- h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight.
  * A row whose sum of h^2 reaches 2^128 (|h| below 2^54 never does, below
  * 2^64 / sqrt(d) neither) or whose mean(h^2) + eps lies below 2^-126 (eps = 0
- * and |h| of some 2^-63) is NaN, in out and in eight bits.  h * weight is
- * rounded to fp32 before the division: it and y stay below 2^128, and below
- * 2^-126 it is off by up to 2^-150.
+ * and |h| of some 2^-63) is NaN, in out and in eight bits; where h * weight is
+ * all zeros, eps above 0 is enough for zeros.  h * weight is rounded to fp32
+ * before the division: it and y stay below 2^128, and below 2^-126 it is off by
+ * up to 2^-150.
  *   residual    device [n_rows][d] or NULL (h = x).
  *   sum_out     device [n_rows][d] or NULL: h, rounded to dtype (the norm uses
  *               it unrounded); may be x or residual.

@@ -379,7 +379,8 @@ __global__ void __launch_bounds__(block_most(kSlots, kWarp, sizeof(T), kAligned)
             const float q = sum / (float)a.d + a.eps;
             r = rsqrtf(q);
             // A sum past fp32's range would make zeros of the row, one that has lost its squares below it a wrong root: NaN.
-            if (!bad && !(q >= kTiny && q <= 3.4028234e38f)) {
+            // (Zeros need no root but a finite one.)
+            if (!bad && !((q >= kTiny || (top_bits == 0u && q > 0.f)) && q <= 3.4028234e38f)) {
                 bad = true;
                 r = __int_as_float(0x7fffffff);
             }

@@ -102,6 +102,18 @@ def test_norm_of_tiny_products_keeps_its_codes(dtype, d, eps, size):
         assert not none[2:].any()
 
 
+@pytest.mark.parametrize("d", NORM_WIDTHS)
+@pytest.mark.parametrize("eps,zeros", [(0.0, False), (1e-44, True), (1e-40, True), (1e-12, True)])
+def test_norm_of_zero_rows(d, eps, zeros):
+    """0 / sqrt(eps) is 0 for any eps above 0, and no number for eps = 0."""
+    for dtype in DTYPES.values():
+        x, w = torch.zeros(3, d, dtype=dtype, device="cuda"), torch.ones(d, dtype=dtype, device="cuda")
+        out, (codes, scale) = torch.full_like(x, 3), empty_codes(3, d)
+        kvr.kvr_rows_norm(x, w, eps, out=out, codes=codes, scales=scale)
+        assert (codes == 0).all()
+        assert ((scale == 0).all() and (out == 0).all()) if zeros else (scale.isnan().all() and out.isnan().all())
+
+
 # ---------------------------------------------------------------- more rows than blocks
 def off_by(codes, scale, y, rel):
     """The furthest of every row from check_codes' bounds, on the GPU: at most 0 where all hold."""
